@@ -247,6 +247,119 @@ int lidx_indexer_bwd_ranges(const void* q, const void* k, const float* w,
                             int grad_dtype, void* dq, void* dk, float* dw,
                             void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators around the indexer: rotary positions of its (and the attention's)
+ * queries and keys, a paged cache of 8-bit keys and values, and attention over
+ * that cache at every key or at the keys the indexer selected.
+ *
+ * Rules that differ from the ones above: heads need not be a power of two, and
+ * strides (host arrays, in elements) may be passed where stated; the last
+ * dimension is always contiguous.  Integer tensors need 4-byte alignment.
+ * ---------------------------------------------------------------------- */
+
+/* Long-context scaling of the rotary frequencies. */
+typedef enum {
+    LIDX_ROPE_PLAIN = 0,
+    LIDX_ROPE_LINEAR = 1,  /* every frequency divided by `factor` */
+    LIDX_ROPE_NTK = 2,     /* base theta * factor^(R/(R-2)): the lowest frequency is divided by `factor` */
+    LIDX_ROPE_YARN = 3     /* w (1-g)/factor + w g, g = clamp((r - beta_slow)/(beta_fast - beta_slow), 0, 1),
+                              r = original_len * w / (2 pi) turns within the original length */
+} lidx_rope_scaling;
+
+/*
+ * Rotary frequencies of rot_dim/2 pairs, w_i = theta^(-2i/rot_dim) radians per
+ * position before scaling, as turns per position in 0.64 fixed point:
+ * freqs[i] = rint(w_i / (2 pi) * 2^64).  HOST call: `freqs` is a host array of
+ * rot_dim/2 entries that the caller copies to the device once.  With it the angle
+ * of position p is p * freqs[i] mod 2^64, exact for every int32 position.
+ * Rules: rot_dim even, 2 .. 1024; theta > 1; factor >= 1 and, for YARN,
+ * original_len > 0 and beta_fast > beta_slow (finite).
+ */
+int lidx_rope_freqs(int rot_dim, double theta, int scaling, double factor, double original_len,
+                    double beta_fast, double beta_slow, uint64_t* freqs);
+
+/* One tensor of a rotary call: x and y [T0,T1,H,D] with strides (T0, T1, H) in elements. */
+typedef struct {
+    const void* x;
+    void* y;        /* y == x with equal strides rotates in place; other overlaps are not supported */
+    int64_t xs[3];
+    int64_t ys[3];
+    int H;
+} lidx_rope_tensor;
+
+typedef enum { LIDX_ROPE_INTERLEAVED = 0, LIDX_ROPE_HALF = 1 } lidx_rope_layout;
+
+/*
+ * Rotary positions.  With t = pos * freqs[i] mod 1 turns, c = mscale * cos(2 pi t) and
+ * s = mscale * sin(2 pi t), pair i = (a, b) of each head becomes (a c - b s, b c + a s); the other
+ * dimensions are copied.  Pair i is dims (o + 2i, o + 2i + 1) (INTERLEAVED) or
+ * (o + i, o + i + rot_dim/2) (HALF), o = rot_off.  inverse = 1 turns the other way (s negated):
+ * the gradient of x is the inverse call on the gradient of y.
+ *   t       host array of nt = 1 or 2 tensors that share positions (queries and keys)
+ *   pos     int32 [T0,T1], strides ps (host int64[2]; 0 repeats a position)
+ *   freqs   device copy of lidx_rope_freqs's array
+ *   dtype   of every x and y: 0 fp32, 1 bf16 (computed in fp32, rounded once)
+ * Rules: T0, T1, H >= 1; D even, 2 .. 1024; rot_dim even >= 2, 0 <= rot_off,
+ * rot_off + rot_dim <= D.  Pointers need only be aligned to their element; 16-byte aligned
+ * tensors, strides and rotated parts take the faster path.
+ */
+int lidx_rope(const lidx_rope_tensor* t, int nt, const int32_t* pos, const int64_t* ps,
+              const uint64_t* freqs, int64_t T0, int64_t T1, int D, int rot_dim, int rot_off,
+              int layout, int inverse, float mscale, int dtype, void* stream);
+
+/*
+ * Writing new keys and values into a paged 8-bit cache.
+ *   k, v         bf16 [B,S,Hkv,D], strides (B, S, Hkv) in ks, vs (host int64[3]; multiples of 8)
+ *   k/v_cache    e4m3 [num_pages,Hkv,page,D] (1 + 4 + 3 bits, +-448, contiguous)
+ *   k/v_scale    fp32 [num_pages,Hkv]: a slot holds the number code * scale
+ *   block_table  int32 [B,max_pages]: the pages of a sequence in order
+ *   start        int32 [B]: tokens the sequence holds already
+ *   count        int32 [B], nullable: new tokens of the sequence (at most S; NULL: S)
+ * Token i < count[b] goes to position p = start[b] + i: page block_table[b][p / page], slot p % page.
+ * Tokens whose position or page id is out of range are dropped.  The scale of a page and head is a
+ * power of two: the smallest 2^e, e >= -40, with |x| <= 448 * 2^e for all its new tokens; a
+ * page that holds earlier tokens of the sequence keeps the larger of that and its old scale, and if it
+ * grows the earlier tokens are rounded to it.  Other slots and pages are left as they were.
+ * A page must belong to one sequence of the call.
+ * Rules: B, S, Hkv, num_pages, max_pages >= 1; D a multiple of 16 <= 128; page 16, 32, 64 or 128;
+ * num_pages * Hkv * page < 2^31 and max_pages * page <= 2^30; k, v and the caches 16-byte aligned.
+ */
+int lidx_cache_append(const void* k, const void* v, const int64_t* ks, const int64_t* vs,
+                      const int32_t* block_table, const int32_t* start, const int32_t* count,
+                      int64_t B, int64_t S, int Hkv, int D, int page, int64_t max_pages,
+                      int64_t num_pages, void* k_cache, void* v_cache, float* k_scale,
+                      float* v_scale, void* stream);
+
+/*
+ * Attention over a paged 8-bit cache.
+ *   q            bf16 [B,S,Hq,D], strides (B, S, Hq) in qs (host int64[3]; multiples of 8)
+ *   caches, scales, block_table: as lidx_cache_append; scales positive and finite
+ *   kv_len       int32 [B]: keys of the sequence
+ *   q_pos        int32 [B], nullable: position of the sequence's first query.  Row (b,s) sees keys
+ *                [0, min(kv_len[b], (q_pos[b]+s+1)/compress_ratio)) (the causal rule of
+ *                lidx_indexer_fwd); NULL: [0, kv_len[b]).
+ *   topk_indices int32 [B,S,topk], nullable: the row sees exactly the listed keys that lie in its range
+ *                (as returned by lidx_indexer_fwd; -1 and other keys out of range are skipped, a key
+ *                listed twice counts twice)
+ *   softmax_scale  the scores are softmax_scale * q . k
+ *   out          bf16 [B,S,Hq,D]; a row that sees no key is 0
+ *   lse          fp32 [B,S,Hq], nullable: log of the sum of exp(score); -inf where no key is seen
+ * Query head h reads key/value head h / (Hq/Hkv).  Keys on pages whose id is out of range are not seen;
+ * what unseen slots hold (NaN codes included) does not reach the output.
+ *   workspace    lidx_cache_attn_workspace_bytes(...) bytes, 256-byte aligned (NULL when 0)
+ * Rules as lidx_cache_append, and: Hq a multiple of Hkv, Hq/Hkv <= 128; topk 1 .. 2^20 with
+ * topk_indices; B * S * Hq < 2^31; softmax_scale finite.
+ */
+int lidx_cache_attn(const void* q, const int64_t* qs, const void* k_cache, const void* v_cache,
+                    const float* k_scale, const float* v_scale, const int32_t* block_table,
+                    const int32_t* kv_len, const int32_t* q_pos, const int32_t* topk_indices,
+                    int64_t B, int64_t S, int Hq, int Hkv, int D, int page, int64_t max_pages,
+                    int64_t num_pages, int compress_ratio, int topk, float softmax_scale, void* out,
+                    float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Device scratch of lidx_cache_attn on the current device, in bytes. */
+size_t lidx_cache_attn_workspace_bytes(int64_t B, int64_t S, int Hq, int Hkv, int D, int topk);
+
 /* Device scratch the call needs for these sizes, in bytes (0 = none).
  * logits_materialised: 1 if logits_out will be non-NULL (LIDX_OP_INDEXER_FWD). */
 size_t lidx_workspace_bytes(int op, int64_t B, int64_t S, int64_t Skv, int H, int D,

@@ -17,8 +17,12 @@ Functions carry the C names:
   lidx_indexer_bwd          backward through the selected entries
   lidx_indexer_bwd_ranges   the same over explicit per-row ranges
   lidx_indexer_fwd_noalloc  fused forward with the library's own scratch
-  lidx_workspace_bytes, lidx_device_status, lidx_status_string,
-  lidx_set_wait_limit_ns, lidx_debug_stall_producer
+  lidx_rope_freqs           rotary frequencies in fixed point, scaled for long contexts
+  lidx_rope, lidx_rope_bwd  rotary positions of queries and keys, and their gradient
+  lidx_cache_append         new keys and values into a paged 8-bit cache
+  lidx_cache_attn           attention over that cache, at every key or at selected ones
+  lidx_workspace_bytes, lidx_cache_attn_workspace_bytes, lidx_device_status,
+  lidx_status_string, lidx_set_wait_limit_ns, lidx_debug_stall_producer
 """
 
 from __future__ import annotations
@@ -38,6 +42,8 @@ STATUS = {0: "LIDX_OK", 1: "LIDX_ERR_NULL", 2: "LIDX_ERR_SHAPE", 3: "LIDX_ERR_AL
           7: "LIDX_ERR_DEVICE_TIMEOUT", 8: "LIDX_ERR_NO_DEVICE"}
 OP_INDEXER_FWD, OP_INDEXER_BWD, OP_SCORES_V41, OP_TOPK_V41 = 0, 1, 2, 3
 ACT = {"relu": 0, "identity": 1}
+ROPE_SCALING = {None: 0, "linear": 1, "ntk": 2, "yarn": 3}
+ROPE_LAYOUT = {"interleaved": 0, "half": 1}
 
 # every symbol include/lidx.h declares
 EXPORTS = ("lidx_indexer_fwd", "lidx_indexer_fwd_ranges", "lidx_indexer_logits",
@@ -45,7 +51,13 @@ EXPORTS = ("lidx_indexer_fwd", "lidx_indexer_fwd_ranges", "lidx_indexer_logits",
            "lidx_indexer_topk_v41", "lidx_indexer_bwd", "lidx_indexer_bwd_ranges",
            "lidx_workspace_bytes", "lidx_device_status", "lidx_status_string", "lidx_version",
            "lidx_indexer_fwd_noalloc", "lidx_noalloc_scratch_bytes", "lidx_set_wait_limit_ns",
-           "lidx_debug_stall_producer")
+           "lidx_debug_stall_producer", "lidx_rope_freqs", "lidx_rope", "lidx_cache_append",
+           "lidx_cache_attn", "lidx_cache_attn_workspace_bytes")
+
+
+class _RopeTensor(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("y", C.c_void_p), ("xs", C.c_int64 * 3), ("ys", C.c_int64 * 3),
+                ("H", C.c_int)]
 
 
 class LidxError(RuntimeError):
@@ -100,7 +112,17 @@ def lib() -> C.CDLL:
             L.lidx_status_string.argtypes = [i32]
             L.lidx_status_string.restype = C.c_char_p
             L.lidx_version.restype = i32
-            for name in ("lidx_indexer_fwd", "lidx_indexer_fwd_ranges", "lidx_indexer_logits",
+            f32, f64 = C.c_float, C.c_double
+            L.lidx_rope_freqs.argtypes = [i32, f64, i32, f64, f64, f64, f64, P]
+            L.lidx_rope.argtypes = [P, i32, P, P, P, i64, i64, i32, i32, i32, i32, i32, f32, i32, P]
+            L.lidx_cache_append.argtypes = [P, P, P, P, P, P, P, i64, i64, i32, i32, i32, i64, i64,
+                                            P, P, P, P, P]
+            L.lidx_cache_attn.argtypes = [P, P, P, P, P, P, P, P, P, P, i64, i64, i32, i32, i32, i32,
+                                          i64, i64, i32, i32, f32, P, P, P, sz, P]
+            L.lidx_cache_attn_workspace_bytes.argtypes = [i64, i64, i32, i32, i32, i32]
+            L.lidx_cache_attn_workspace_bytes.restype = sz
+            for name in ("lidx_rope_freqs", "lidx_rope", "lidx_cache_append", "lidx_cache_attn",
+                         "lidx_indexer_fwd", "lidx_indexer_fwd_ranges", "lidx_indexer_logits",
                          "lidx_extract_topk_scores", "lidx_topk_rows", "lidx_indexer_scores_v41",
                          "lidx_indexer_topk_v41", "lidx_indexer_bwd", "lidx_indexer_bwd_ranges",
                          "lidx_device_status"):
@@ -396,3 +418,192 @@ def lidx_indexer_bwd(q, k, w, idx, grad, compress_ratio, act="relu", grad_dtype=
                                 _stream(stream))
     _check(rc, "lidx_indexer_bwd")
     return dq, dk, dw
+
+
+def _need_strided(t, name, dtype, dim):
+    """As _need, with any strides as long as the last dimension is contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dims, got {tuple(t.shape)}")
+    if t.shape[-1] != 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+
+
+def _same_device(first, **others):
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, not on {first.device}")
+
+
+def _strides(t):
+    """Element strides of the leading dimensions (0 where the size is 1: never stepped over)."""
+    return [st if n > 1 else 0 for st, n in zip(t.stride()[:-1], t.shape[:-1])]
+
+
+def lidx_rope_freqs(rot_dim, theta=10000.0, scaling=None, factor=1.0, original_len=4096, beta_fast=32.0,
+                    beta_slow=1.0, device="cuda") -> torch.Tensor:
+    """Rotary frequencies int64 [rot_dim/2]: turns per position in 0.64 fixed point (the bits of
+    unsigned integers).  scaling: None, "linear", "ntk" or "yarn"."""
+    if scaling not in ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {list(ROPE_SCALING)}")
+    out = torch.empty(max(int(rot_dim) // 2, 1), dtype=torch.int64)
+    rc = lib().lidx_rope_freqs(int(rot_dim), theta, ROPE_SCALING[scaling], factor, original_len, beta_fast,
+                               beta_slow, _ptr(out))
+    _check(rc, "lidx_rope_freqs")
+    return out.to(device)
+
+
+def _rope(x, pos, freqs, x2, layout, rot_off, mscale, inverse, stream, out, call):
+    if x.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"x must be float32 or bfloat16, got {x.dtype}")
+    _need_strided(x, "x", x.dtype, 4)
+    if x2 is not None:
+        _need_strided(x2, "x2", x.dtype, 4)
+        if x2.shape[:2] != x.shape[:2] or x2.shape[3] != x.shape[3]:
+            raise ValueError("x and x2 shapes disagree")
+    if not isinstance(pos, torch.Tensor) or pos.dtype != torch.int32 or not pos.is_cuda:
+        raise TypeError("pos must be an int32 CUDA tensor")
+    pos = pos.expand(x.shape[:2])  # repeated positions have stride 0
+    _need(freqs, "freqs", torch.int64, 1)
+    _same_device(x, x2=x2, pos=pos, freqs=freqs)
+    if layout not in ROPE_LAYOUT:
+        raise ValueError(f"layout must be one of {list(ROPE_LAYOUT)}")
+    xs = [x] if x2 is None else [x, x2]
+    if out is None:
+        ys = [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in xs]
+    else:
+        ys = [out] if x2 is None else list(out)
+        for t, y in zip(xs, ys):
+            _need_strided(y, "out", t.dtype, 4)
+            if y.shape != t.shape:
+                raise ValueError("out has another shape than x")
+            _same_device(x, out=y)
+    T0, T1, _, D = x.shape
+    arr = (_RopeTensor * len(xs))()
+    for a, t, y in zip(arr, xs, ys):
+        a.x, a.y, a.H = t.data_ptr(), y.data_ptr(), t.shape[2]
+        a.xs[:] = _strides(t)
+        a.ys[:] = _strides(y)
+    ps = (C.c_int64 * 2)(*[st if n > 1 else 0 for st, n in zip(pos.stride(), pos.shape)])
+    rc = lib().lidx_rope(arr, len(xs), _ptr(pos), ps, _ptr(freqs), T0, T1, D, 2 * freqs.shape[0], rot_off,
+                         ROPE_LAYOUT[layout], int(inverse), mscale, int(x.dtype == torch.bfloat16),
+                         _stream(stream))
+    _check(rc, call)
+    return ys[0] if x2 is None else tuple(ys)
+
+
+def lidx_rope(x, pos, freqs, x2=None, layout="interleaved", rot_off=0, mscale=1.0, stream=None, out=None):
+    """Rotary positions of x [T0,T1,H,D] (fp32 or bf16, any strides of the leading dimensions) and, in
+    the same launch, of x2 [T0,T1,H2,D].  pos: int32, broadcast to [T0,T1]; freqs: lidx_rope_freqs's,
+    the rotated dims are [rot_off, rot_off + 2*len(freqs)).  Returns y, or (y, y2).  ``out`` may be the
+    inputs themselves (in place)."""
+    return _rope(x, pos, freqs, x2, layout, rot_off, mscale, False, stream, out, "lidx_rope")
+
+
+def lidx_rope_bwd(g, pos, freqs, x2=None, layout="interleaved", rot_off=0, mscale=1.0, stream=None, out=None):
+    """Gradient of lidx_rope's x (and x2) from the gradients g (and x2) of its outputs: the inverse turn."""
+    return _rope(g, pos, freqs, x2, layout, rot_off, mscale, True, stream, out, "lidx_rope_bwd")
+
+
+def _cache_dims(k_cache, v_cache, k_scale, v_scale, block_table, B):
+    _need(k_cache, "k_cache", torch.float8_e4m3fn, 4)
+    _need(v_cache, "v_cache", torch.float8_e4m3fn, 4)
+    _need(k_scale, "k_scale", torch.float32, 2)
+    _need(v_scale, "v_scale", torch.float32, 2)
+    _need(block_table, "block_table", torch.int32, 2)
+    pages, Hkv, page, D = k_cache.shape
+    if v_cache.shape != k_cache.shape or tuple(k_scale.shape) != (pages, Hkv) or k_scale.shape != v_scale.shape:
+        raise ValueError("cache and scale shapes disagree")
+    if block_table.shape[0] != B:
+        raise ValueError("block_table must have B rows")
+    _same_device(k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, block_table=block_table)
+    return pages, Hkv, page, D, block_table.shape[1]
+
+
+def _per_sequence(t, name, B):
+    _need(t, name, torch.int32, 1)
+    if t.shape[0] != B:
+        raise ValueError(f"{name} must have B entries")
+
+
+def lidx_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, start, count=None, stream=None):
+    """Writes k, v [B,S,Hkv,D] bf16 behind the start[b] tokens that each sequence's pages hold, in
+    8 bits with a power-of-two scale for each page and head.  k_cache, v_cache [P,Hkv,page,D]
+    float8_e4m3fn and k_scale, v_scale [P,Hkv] fp32 are updated in place; block_table int32
+    [B,max_pages]; count int32 [B] or None: new tokens of each sequence."""
+    _need_strided(k, "k", torch.bfloat16, 4)
+    _need_strided(v, "v", torch.bfloat16, 4)
+    B, S, Hkv, D = k.shape
+    pages, Hc, page, Dc, MP = _cache_dims(k_cache, v_cache, k_scale, v_scale, block_table, B)
+    if v.shape != k.shape or (Hc, Dc) != (Hkv, D):
+        raise ValueError("k/v/cache shapes disagree")
+    _per_sequence(start, "start", B)
+    if count is not None:
+        _per_sequence(count, "count", B)
+    _same_device(k, v=v, k_cache=k_cache, start=start, count=count)
+    i3 = C.c_int64 * 3
+    rc = lib().lidx_cache_append(_ptr(k), _ptr(v), i3(*_strides(k)), i3(*_strides(v)), _ptr(block_table),
+                                 _ptr(start), _ptr(count), B, S, Hkv, D, page, MP, pages, _ptr(k_cache),
+                                 _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _stream(stream))
+    _check(rc, "lidx_cache_append")
+
+
+def lidx_cache_attn_workspace_bytes(B, S, Hq, Hkv, D, topk=0) -> int:
+    return int(lib().lidx_cache_attn_workspace_bytes(B, S, Hq, Hkv, D, topk))
+
+
+def lidx_cache_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, q_pos=None, compress_ratio=1,
+                    topk_indices=None, softmax_scale=None, want_lse=False, stream=None, out=None,
+                    workspace=None):
+    """Attention of q [B,S,Hq,D] bf16 over a cache written by lidx_cache_append.
+
+    kv_len int32 [B]: keys of each sequence.  q_pos int32 [B] or None: with it, row (b,s) sees keys
+    below (q_pos[b]+s+1)//compress_ratio only.  topk_indices int32 [B,S,topk] or None: the row sees
+    only the listed keys (lidx_indexer_fwd's indices).  softmax_scale defaults to D**-0.5.
+    Returns (out [B,S,Hq,D] bf16, lse [B,S,Hq] fp32 or None); ``out`` may hold preallocated ones."""
+    _need_strided(q, "q", torch.bfloat16, 4)
+    B, S, Hq, D = q.shape
+    pages, Hkv, page, Dc, MP = _cache_dims(k_cache, v_cache, k_scale, v_scale, block_table, B)
+    if Dc != D:
+        raise ValueError("q/cache shapes disagree")
+    _per_sequence(kv_len, "kv_len", B)
+    if q_pos is not None:
+        _per_sequence(q_pos, "q_pos", B)
+    topk = 0
+    if topk_indices is not None:
+        _need(topk_indices, "topk_indices", torch.int32, 3)
+        if tuple(topk_indices.shape[:2]) != (B, S):
+            raise ValueError("topk_indices must be [B,S,topk]")
+        topk = topk_indices.shape[2]
+    if out is None:
+        o = torch.empty(B, S, Hq, D, dtype=torch.bfloat16, device=q.device)
+        lse = torch.empty(B, S, Hq, dtype=torch.float32, device=q.device) if want_lse else None
+    else:
+        o, lse = out
+        _need(o, "out", torch.bfloat16, 4)
+        if tuple(o.shape) != (B, S, Hq, D):
+            raise ValueError("out must be [B,S,Hq,D]")
+        if lse is not None:
+            _need(lse, "lse", torch.float32, 3)
+            if tuple(lse.shape) != (B, S, Hq):
+                raise ValueError("lse must be [B,S,Hq]")
+    _same_device(q, k_cache=k_cache, kv_len=kv_len, q_pos=q_pos, topk_indices=topk_indices, out=o, lse=lse,
+                 workspace=workspace)
+    ws_bytes = lidx_cache_attn_workspace_bytes(B, S, Hq, Hkv, D, topk)
+    if workspace is None and ws_bytes:
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+    elif workspace is not None:
+        _need(workspace, "workspace", torch.uint8, 1)
+        ws_bytes = workspace.numel()
+    rc = lib().lidx_cache_attn(_ptr(q), (C.c_int64 * 3)(*_strides(q)), _ptr(k_cache), _ptr(v_cache),
+                               _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(kv_len), _ptr(q_pos),
+                               _ptr(topk_indices), B, S, Hq, Hkv, D, page, MP, pages, compress_ratio, topk,
+                               D ** -0.5 if softmax_scale is None else softmax_scale, _ptr(o), _ptr(lse),
+                               _ptr(workspace), ws_bytes, _stream(stream))
+    _check(rc, "lidx_cache_attn")
+    return o, lse

@@ -166,6 +166,8 @@ static int device_sms(bool require_sm103) {
     return d->sms;
 }
 
+int sm103_sms() { return device_sms(true); }
+
 static std::atomic<uint64_t> g_wait_limit_ns{kWaitLimitNs};
 static std::atomic<int> g_debug_stall{0};
 
