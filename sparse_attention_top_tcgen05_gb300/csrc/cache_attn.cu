@@ -2,28 +2,45 @@
 //
 //     o = sum_t p_t v_t,  p = softmax over the row's keys of softmax_scale * q . k_t
 // with k_t = code * scale of its page and head, v_t likewise.  One pass over the keys with the running
-// maximum m and sum l of the softmax:
-//     m' = max(m, max_t s_t);  l = l e^(m - m') + sum_t e^(s_t - m');  o = o e^(m - m') + sum_t e^(s_t - m') v_t
+// maximum m and sum l of the softmax.
 //
-// One block per (row, query head): a thread takes one key of a tile of 128, then one output dim.
+// Mathematics on the tensor cores.  A bf16 number has 8 significant bits and e4m3 has 4, so a query row,
+// scaled by a power of two to at most 256, is exactly hi + lo with hi = e4m3(q), lo = e4m3(q - hi)
+// (elements below 2^-10 of the row's largest keep an error of 2^-17 of it).  The cache's codes then
+// go to tcgen05 kind::f8f6f4 as they are stored, without conversion, two passes for q.  The weights are held
+// as hi + lo the same way (relative error 2^-8).  e4m3 spans few powers of two, so the weights of each tile
+// of 128 keys are scaled to the tile's own largest, every tile's product is taken by itself, and the
+// products are joined in fp32 registers with the running maximum: a key that takes nearly all the weight
+// costs the tiles behind it nothing.  With x_t = log2(e) softmax_scale q.k_t + log2(v scale):
+//     M = max_t x_t of the tile;  w_t = 2^(x_t - M + 8) -> hi + lo;  O = sum_t w_t code_t
+//     m' = max(m, M);  acc = acc 2^(m - m') + O 2^(M - m');  l likewise with w_t / v scale;  o = acc / l.
+//
+// Keys are the rows of both products (S^T = K Q^T, O^T = V^T P^T): 128 keys fill the tensor core's rows however
+// few queries there are.  The N columns are (query token, head of the group), N = 16, 32, 64 or 128.
+//
+// Work.  The units (sequence, tile of query tokens, kv head) have as many tiles of 128 keys as their last row
+// sees.  All tiles form one line that is cut into equal shares, one a CTA, found on the device from the
+// lengths.  A CTA that holds only part of a unit writes (m, l, acc) to the workspace, and cache_attn_join_kernel
+// joins the parts in order.  No atomics: two calls give the same bits.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+#include <string.h>
 
 #include <climits>
+#include <type_traits>
 
 #include "cache.cuh"
 #include "kernels.h"
 #include "lidx.h"
+#include "ptx.cuh"
 
 namespace lidx {
 
 struct AttnParams {
     const uint16_t* q;
     int64_t qs[3];
-    const uint8_t* kc;
-    const uint8_t* vc;
     const float* ks;
     const float* vs;
     const int32_t* table;
@@ -31,10 +48,55 @@ struct AttnParams {
     const int32_t* q_pos;  // nullable
     const int32_t* idx;    // nullable
     int64_t num_pages;
-    int B, S, Hq, Hkv, D, page, max_pages, ratio, topk;
-    float scale;
+    int B, S, Hq, Hkv, G, D, page, max_pages, ratio, topk;
+    int TS, ST;            // query tokens of a unit; units of a sequence
+    float scale_log2;      // softmax_scale * log2(e)
     uint16_t* out;
-    float* lse;  // nullable
+    float* lse;            // nullable
+    uint8_t* ws;
+    uint64_t wait_ns;
+    int debug_stall;       // 1: the producer issues nothing (failure-detection tests)
+};
+
+constexpr int kATile = 128;                     // keys of a tile
+constexpr int kASlotBytes = kATile * 128;       // one K or V tile: 128 bytes a key (zero past D)
+constexpr int kAThreads = 512;
+constexpr int kAMeta = 5;                       // stages of per-key scales
+constexpr float kATop = 8.f;                    // weights are scaled to 2^8
+constexpr float kALn2 = 0.693147180559945309f;
+
+// Shared memory of the configuration with N columns.
+template <int N>
+struct AttnCfg {
+    static constexpr bool SPLIT = N == 128;            // both softmax groups share each tile's columns
+    static constexpr int NC = SPLIT ? 64 : N;          // columns of a softmax group
+    static constexpr int QB = SPLIT ? 1 : 2;           // query buffers
+    static constexpr int SLOTS = N == 16 ? 9 : (N == 32 ? 8 : 7);
+    static constexpr int Q_BYTES = 2 * N * 128;        // hi and lo
+    static constexpr int P_BYTES = 2 * kASlotBytes;    // hi and lo
+    static constexpr int OFF_P = SLOTS * kASlotBytes;
+    static constexpr int OFF_Q = OFF_P + 2 * P_BYTES;
+    static constexpr int OFF_META = OFF_Q + QB * Q_BYTES;              // [kAMeta][128] float2
+    static constexpr int OFF_FLAG = OFF_META + kAMeta * kATile * 8;    // [kAMeta] int
+    static constexpr int OFF_QS = OFF_FLAG + 64;                       // [2][N] query scales
+    static constexpr int OFF_W = OFF_QS + 2 * N * 4;                   // [2][4][NC] warp maxima
+    static constexpr int OFF_MB = OFF_W + 2 * 4 * NC * 4;              // [2][NC] float2 (8 - M, fade of the tile)
+    static constexpr int OFF_AL = OFF_MB + 2 * NC * 8;                 // [2][NC] fade of the sum
+    static constexpr int OFF_END = OFF_AL + 2 * NC * 4;                // [2][NC] keys a column sees
+    static constexpr int OFF_MT = OFF_END + 2 * NC * 4;                // [2][N] tile maxima
+    static constexpr int OFF_AB = OFF_MT + 2 * N * 4;                  // [2][N] float2 fades of acc and tile
+    static constexpr int OFF_L = OFF_AB + 2 * N * 8;                   // [2][4][NC] sums of the warps
+    static constexpr int OFF_MW = OFF_L + 2 * 4 * NC * 4;              // [2][NC] their reference
+    static constexpr int OFF_INV = OFF_MW + 2 * NC * 4;                // [N] 1 / l
+    static constexpr int OFF_ROW = OFF_INV + N * 4;                    // [N] output rows
+    static constexpr int OFF_BAR = (OFF_ROW + N * 4 + 15) / 16 * 16;
+    static constexpr int NBAR = 2 * SLOTS + 2 * kAMeta + 2 * 2 + 5 * 2 + 2 + 1;
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;                // start of the share, TMEM address
+    static constexpr int TOTAL = OFF_MISC + 256 + 1024;                // + alignment of the base
+    static_assert(TOTAL <= 232448 && kAMeta * 4 <= 64, "shared memory");
+    static_assert(OFF_QS % 16 == 0 && OFF_MB % 16 == 0 && OFF_AL % 16 == 0 && OFF_END % 16 == 0 && OFF_AB % 16 == 0,
+                  "16-byte reads");
+    static constexpr int TMEM = 4 * N;                                 // columns: two tiles of S and of O
 };
 
 // Row (b, s) sees keys [0, end).
@@ -50,68 +112,874 @@ __device__ __forceinline__ int attn_end(const AttnParams& p, int b, int s) {
     return n;
 }
 
-constexpr int kAttnThreads = 128;
+// ---- the line of tiles.  Group g = (sequence, tile of query tokens); its Hkv units follow each other.
+struct AttnGroup {
+    int b, st, limit;  // limit: keys its last row sees
+    int n;             // tiles of a unit (0: nothing to see)
+    int w;             // places of a unit on the line: at least one
+};
+__device__ __forceinline__ AttnGroup attn_group(const AttnParams& p, int g) {
+    AttnGroup r;
+    r.b = g / p.ST;
+    r.st = g - r.b * p.ST;
+    const int s1 = min(r.st * p.TS + p.TS, p.S) - 1;
+    r.limit = attn_end(p, r.b, s1);
+    r.n = ((p.idx ? p.topk : r.limit) + kATile - 1) / kATile;
+    r.w = max(r.n, 1);
+    return r;
+}
+__device__ __forceinline__ int64_t attn_share(int64_t W, int c, int n) { return W * c / n; }
 
-__global__ void __launch_bounds__(kAttnThreads) cache_attn_kernel(const AttnParams p) {
-    __shared__ float sq[kCacheMaxD], sw[kAttnThreads], sred[8];
-    __shared__ int64_t srow[kAttnThreads];
-    const int hq = blockIdx.x % p.Hq, h = hq / (p.Hq / p.Hkv);
-    const int64_t row = blockIdx.x / p.Hq;
-    const int b = (int)(row / p.S), s = (int)(row % p.S), tid = threadIdx.x;
-    const uint16_t* q = p.q + b * p.qs[0] + s * p.qs[1] + hq * p.qs[2];
-    if (tid < p.D) sq[tid] = __uint_as_float((uint32_t)q[tid] << 16) * p.scale;
-    const int end = attn_end(p, b, s), n = p.idx ? p.topk : end;
-    float m = -INFINITY, l = 0.f, o = 0.f;
-    for (int t0 = 0; t0 < n; t0 += kAttnThreads) {
-        __syncthreads();
-        int t = t0 + tid < n ? t0 + tid : -1;
-        if (p.idx && t >= 0) {
-            t = p.idx[row * p.topk + t];
-            if (t >= end) t = -1;
+// The segments [t0, t1) of units that make up a CTA's share; every role walks them alike.
+struct AttnWalk {
+    int64_t pos, end, base;  // base: place of the group's first unit
+    int g, h, t0, t1;
+    int64_t unit_end;
+    AttnGroup gr;
+    bool first, fresh;
+
+    __device__ void begin(const AttnParams& p, int64_t pos_, int64_t end_, int g_, int64_t base_) {
+        pos = pos_;
+        end = end_;
+        g = g_;
+        base = base_;
+        fresh = true;
+        t1 = 0;
+    }
+    __device__ bool next(const AttnParams& p) {
+        if (pos >= end) return false;
+        first = fresh;
+        if (fresh) {
+            gr = attn_group(p, g);
+            fresh = false;
+        } else if (pos >= base + (int64_t)gr.w * p.Hkv) {
+            base += (int64_t)gr.w * p.Hkv;
+            gr = attn_group(p, ++g);
         }
-        float x = -INFINITY, vscale = 0.f;
-        srow[tid] = -1;
-        if (t >= 0) {
-            const int64_t pid = p.table[(int64_t)b * p.max_pages + t / p.page];
-            if (pid >= 0 && pid < p.num_pages) {
-                const int64_t cell = pid * p.Hkv + h, at = (cell * p.page + t % p.page) * p.D;
-                const uint16_t* k = reinterpret_cast<const uint16_t*>(p.kc + at);
-                float dot = 0.f;
-                for (int d = 0; d < p.D; d += 2) {
-                    const float2 kk = e4m3x2_to(k[d / 2]);
-                    dot += sq[d] * kk.x + sq[d + 1] * kk.y;
-                }
-                x = dot * p.ks[cell];
-                vscale = p.vs[cell];
-                srow[tid] = at;
-            }
-        }
-        float mt = x;
-        for (int i = 16; i; i >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, i));
-        if ((tid & 31) == 0) sred[tid >> 5] = mt;
-        __syncthreads();
-        mt = fmaxf(fmaxf(sred[0], sred[1]), fmaxf(sred[2], sred[3]));
-        const float mn = fmaxf(m, mt);
-        if (mn == -INFINITY) continue;  // nothing seen yet (uniform over the block)
-        const float w = x == -INFINITY ? 0.f : expf(x - mn), fade = m == -INFINITY ? 0.f : expf(m - mn);
-        float ws = w;
-        for (int i = 16; i; i >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, i);
-        if ((tid & 31) == 0) sred[4 + (tid >> 5)] = ws;
-        sw[tid] = w * vscale;
-        __syncthreads();
-        l = l * fade + (sred[4] + sred[5] + sred[6] + sred[7]);
-        m = mn;
-        if (tid < p.D) {
-            o *= fade;
-            for (int i = 0; i < kAttnThreads; ++i)
-                if (srow[i] >= 0) o += sw[i] * e4m3x2_to(p.vc[srow[i] + tid]).x;
+        const int64_t at = pos - base;
+        h = (int)(at / gr.w);
+        t0 = (int)(at - (int64_t)h * gr.w);
+        unit_end = base + (int64_t)(h + 1) * gr.w;
+        const int64_t e = unit_end < end ? unit_end : end;
+        t1 = t0 + (int)(e - pos);
+        pos = e;
+        return true;
+    }
+};
+
+// Workspace: a header for each CTA, then two parts for each (its first segment, its last).
+struct AttnHeader {
+    int32_t owner, g, h, slot;  // owner: the CTA holds the first tiles of a unit that goes on behind it
+    int64_t unit_end, W;
+};
+__host__ __device__ inline size_t attn_part_floats(int N) { return (size_t)N * 128 + 2 * N; }
+__host__ __device__ inline size_t attn_ws_bytes(int N, int grid) {
+    return (size_t)grid * sizeof(AttnHeader) + (size_t)grid * 2 * attn_part_floats(N) * 4;
+}
+
+// Two floats (at most 256 in size) -> e4m3 hi and lo pairs in the low halves.
+__device__ __forceinline__ void split_e4m3(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+    uint32_t f, b, r;
+    uint16_t h, l;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(f) : "f"(x1), "f"(x0));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(f));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"(h));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(f), "r"(b));  // exact
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(r));
+    hi = h;
+    lo = l;
+}
+
+// Sums over the warp's lanes of 32 columns: lane i returns column i's.
+__device__ __forceinline__ float warp_sum_columns(float (&v)[32], int lane) {
+#pragma unroll
+    for (int step = 16; step > 0; step >>= 1) {
+        const bool up = lane & step;
+#pragma unroll
+        for (int i = 0; i < step; ++i) {
+            const float send = up ? v[i] : v[i + step], keep = up ? v[i + step] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, step);
         }
     }
-    if (tid < p.D)
-        reinterpret_cast<__nv_bfloat16*>(p.out)[(row * p.Hq + hq) * p.D + tid] =
-            __float2bfloat16_rn(l > 0.f ? o / l : 0.f);
-    if (p.lse && tid == 0) p.lse[row * p.Hq + hq] = l > 0.f ? m + logf(l) : -INFINITY;
+    return v[0];
 }
+
+// x of CH columns of this thread's key: (S^T * key's factor) * column's factor + log2(v scale); unseen -inf.
+template <bool MASK, int CH>
+__device__ __forceinline__ void attn_scores(uint32_t s_addr, const float* qs, const int* ends, uint64_t a2,
+                                            uint64_t lv2, int key, bool seen, float (&x)[CH]) {
+    uint32_t r[CH];
+    if constexpr (CH == 32)
+        tmem_ld32(s_addr, r);
+    else
+        tmem_ld16(s_addr, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < CH; i += 4) {
+        const float4 q4 = *reinterpret_cast<const float4*>(qs + i);
+        const uint64_t x0 = fma2(mul2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), a2),
+                                 pack2(q4.x, q4.y), lv2);
+        const uint64_t x1 = fma2(mul2(pack2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), a2),
+                                 pack2(q4.z, q4.w), lv2);
+        unpack2(x0, x[i], x[i + 1]);
+        unpack2(x1, x[i + 2], x[i + 3]);
+        if constexpr (MASK) {
+            const int4 e4 = *reinterpret_cast<const int4*>(ends + i);
+            x[i] = seen && key < e4.x ? x[i] : -INFINITY;
+            x[i + 1] = seen && key < e4.y ? x[i + 1] : -INFINITY;
+            x[i + 2] = seen && key < e4.z ? x[i + 2] : -INFINITY;
+            x[i + 3] = seen && key < e4.w ? x[i + 3] : -INFINITY;
+        }
+    }
+}
+
+template <int N>
+__global__ void __launch_bounds__(kAThreads, 1)
+    cache_attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                      const __grid_constant__ AttnParams p) {
+    using C = AttnCfg<N>;
+    constexpr int NC = C::NC, SLOTS = C::SLOTS, QB = C::QB;
+    constexpr int CH = NC < 32 ? NC : 32;  // columns of a chunk in registers
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t* const sP = smem + C::OFF_P;
+    uint8_t* const sQ = smem + C::OFF_Q;
+    float2* const sMeta = (float2*)(smem + C::OFF_META);
+    int* const sFlag = (int*)(smem + C::OFF_FLAG);
+    float* const sQs = (float*)(smem + C::OFF_QS);
+    float* const sMt = (float*)(smem + C::OFF_MT);
+    float* const sL = (float*)(smem + C::OFF_L);
+    float* const sMw = (float*)(smem + C::OFF_MW);
+    uint64_t* bars = (uint64_t*)(smem + C::OFF_BAR);
+    uint64_t* kv_full = bars;               // [SLOTS] K or V tile landed
+    uint64_t* kv_empty = kv_full + SLOTS;   // [SLOTS] its product is done
+    uint64_t* meta_full = kv_empty + SLOTS;     // [kAMeta] scales of a tile's keys written
+    uint64_t* meta_empty = meta_full + kAMeta;  // [kAMeta] read by the softmax warps
+    uint64_t* q_full = meta_empty + kAMeta;     // [2]
+    uint64_t* q_empty = q_full + 2;             // [2]
+    uint64_t* s_full = q_empty + 2;         // [2] S^T of a tile in TMEM
+    uint64_t* p_full = s_full + 2;          // [2] weights and tile maxima written (and S^T read)
+    uint64_t* o_full = p_full + 2;          // [2] O^T of a tile in TMEM (and the weights read)
+    uint64_t* o_empty = o_full + 2;         // [2] O^T read
+    uint64_t* m_read = o_empty + 2;         // [2] tile maxima read
+    uint64_t* l_full = m_read + 2;          // sums of a segment written
+    uint64_t* l_empty = l_full + 1;
+    uint64_t* drain = l_empty + 1;
+    int64_t* sScan = (int64_t*)(smem + C::OFF_MISC);  // [16]
+    int64_t* sBase = sScan + 16;
+    int* sGroup = (int*)(sBase + 1);
+    uint32_t* tmem_slot = (uint32_t*)(sGroup + 1);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < SLOTS; ++i) {
+            mbar_init(kv_full + i, 1);
+            mbar_init(kv_empty + i, 1);
+        }
+        for (int i = 0; i < kAMeta; ++i) {
+            mbar_init(meta_full + i, 1);
+            mbar_init(meta_empty + i, C::SPLIT ? 8 : 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full + i, 2);
+            mbar_init(q_empty + i, 1 + 8);
+            mbar_init(s_full + i, 1);
+            mbar_init(p_full + i, C::SPLIT ? 8 : 4);
+            mbar_init(o_full + i, 1);
+            mbar_init(o_empty + i, 4);
+            mbar_init(m_read + i, 4);
+        }
+        mbar_init(l_full, 8);
+        mbar_init(l_empty, 4);
+        mbar_init(drain, 1);
+        fence_mbar_init();
+        tma_prefetch_desc(&tmk);
+        tma_prefetch_desc(&tmv);
+    }
+    if (warp == 0) {
+        tmem_alloc(tmem_slot, C::TMEM);
+        tmem_relinquish();
+    }
+
+    // ---- this CTA's share of the line
+    const int nc = gridDim.x, c = blockIdx.x;
+    int64_t W, pos0, pos1, base0 = 0;
+    int g0 = 0;
+    if (p.idx) {
+        // every unit has the same places
+        const int64_t w = (int64_t)((p.topk + kATile - 1) / kATile) * p.Hkv;
+        W = w * p.B * p.ST;
+        pos0 = attn_share(W, c, nc);
+        pos1 = attn_share(W, c + 1, nc);
+        g0 = (int)(pos0 / w);
+        base0 = g0 * w;
+    } else {
+        const int NG = p.B * p.ST, per = (NG + kAThreads - 1) / kAThreads;
+        const int ga = min(tid * per, NG), gz = min(ga + per, NG);
+        int64_t sum = 0;
+        for (int g = ga; g < gz; ++g) sum += (int64_t)attn_group(p, g).w * p.Hkv;
+        int64_t incl = sum;
+#pragma unroll
+        for (int i = 1; i < 32; i <<= 1) {
+            const int64_t o = __shfl_up_sync(0xffffffffu, incl, i);
+            if (lane >= i) incl += o;
+        }
+        if (lane == 31) sScan[warp] = incl;
+        __syncthreads();
+        W = 0;
+        int64_t before = 0;
+#pragma unroll
+        for (int i = 0; i < kAThreads / 32; ++i) {
+            if (i == warp) before = W;
+            W += sScan[i];
+        }
+        pos0 = attn_share(W, c, nc);
+        pos1 = attn_share(W, c + 1, nc);
+        int64_t at = before + incl - sum;
+        if (pos0 >= at && pos0 < at + sum) {
+            int g = ga;
+            for (; g < gz; ++g) {
+                const int64_t w = (int64_t)attn_group(p, g).w * p.Hkv;
+                if (pos0 < at + w) break;
+                at += w;
+            }
+            *sGroup = g;
+            *sBase = at;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (!p.idx && pos0 < pos1) {
+        g0 = *sGroup;
+        base0 = *sBase;
+    }
+    const uint32_t tmem = *tmem_slot;
+    AttnWalk wk;
+    wk.begin(p, pos0, pos1, g0, base0);
+
+    if (warp < 4) {
+        regs_dec<80>();
+        if (warp == 0) {
+            // ------------------------------------------------------- MMA issuer
+            // The whole warp walks and waits; lane 0 issues.
+            const uint32_t id_s = idesc_e4m3_f32(128, N);
+            const uint32_t id_o = idesc_e4m3_f32(128, N) | kIdescAMn | kIdescBMn;
+            const int nk = (p.D + 31) / 32;
+            const uint64_t dk0 = smem_desc_kmajor(smem_u32(smem), 128);
+            const uint64_t dv0 = smem_desc_mn_sw128(smem_u32(smem), kASlotBytes);
+            const uint64_t dq0 = smem_desc_kmajor(smem_u32(sQ), 128);
+            const uint64_t dp0 = smem_desc_mn_sw128(smem_u32(sP), kASlotBytes);
+            bool ok = true;
+            int tc = 0, sc = 0;
+            // O^T of tile t: V^T (hi + lo)
+            auto second = [&](int t) {
+                const int bf = t & 1, ph = (t >> 1) & 1, seq = 2 * t + 1, sl = seq % SLOTS;
+                ok = ok && mbar_wait(kv_full + sl, (seq / SLOTS) & 1, p.wait_ns);
+                ok = ok && mbar_wait(o_empty + bf, ph ^ 1, p.wait_ns);
+                ok = ok && mbar_wait(p_full + bf, ph, p.wait_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) return;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint64_t a = dv0 + (uint64_t)(sl * (kASlotBytes >> 4));
+                    const uint64_t b = dp0 + (uint64_t)(bf * (C::P_BYTES >> 4));
+                    const uint32_t d = tmem + 2 * N + bf * N;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {  // 32 keys a step
+                        umma_f8(d, a + k * (32 * 128 >> 4), b + k * (32 * 128 >> 4), id_o, k > 0);
+                        umma_f8(d, a + k * (32 * 128 >> 4), b + (kASlotBytes >> 4) + k * (32 * 128 >> 4), id_o, 1);
+                    }
+                    umma_commit(o_full + bf);
+                    umma_commit(kv_empty + sl);
+                }
+                __syncwarp();
+            };
+            while (ok && wk.next(p)) {
+                if (wk.gr.n == 0) continue;
+                const int qb = sc % QB;
+                ok = ok && mbar_wait(q_full + qb, (sc / QB) & 1, p.wait_ns);
+                for (int t = wk.t0; ok && t < wk.t1; ++t, ++tc) {
+                    const int seq = 2 * tc, sl = seq % SLOTS;
+                    ok = mbar_wait(kv_full + sl, (seq / SLOTS) & 1, p.wait_ns);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint64_t a = dk0 + (uint64_t)(sl * (kASlotBytes >> 4));
+                        const uint64_t b = dq0 + (uint64_t)(qb * (C::Q_BYTES >> 4));
+                        const uint32_t d = tmem + (tc & 1) * N;
+                        // 32 dims a step, hi then lo.  Loops, not unrolled conditions: with `if (k < nk)` around
+                        // each of eight unrolled products the N = 128 build multiplied by wrong operands.
+#pragma unroll 1
+                        for (int k = 0; k < nk; ++k) umma_f8(d, a + 2 * k, b + 2 * k, id_s, k > 0);
+#pragma unroll 1
+                        for (int k = 0; k < nk; ++k) umma_f8(d, a + 2 * k, b + (N * 128 >> 4) + 2 * k, id_s, 1);
+                        umma_commit(s_full + (tc & 1));
+                        umma_commit(kv_empty + sl);
+                        if (t == wk.t1 - 1) umma_commit(q_empty + qb);
+                    }
+                    __syncwarp();
+                    if (tc > 0) second(tc - 1);
+                }
+                ++sc;
+            }
+            if (ok && tc > 0) second(tc - 1);
+            if (!__all_sync(0xffffffffu, ok)) {  // products in flight end before the memory is given up
+                if (lane == 0) umma_commit(drain);
+                mbar_wait(drain, 0, p.wait_ns);
+            }
+        } else if (warp == 1) {
+            // --------------------------------------------------------- producer
+            // Three steps ahead: indices of tile i + 2, page ids of tile i + 1, scales of tile i, so that a
+            // step waits for one memory latency at most.  A lane has four keys.
+            bool ok = !p.debug_stall;
+            struct Ref {
+                bool live;
+                int b, h, tile, limit;
+                int64_t row;  // of topk_indices
+            };
+            int tile = 0;
+            bool more = true;
+            auto next_ref = [&]() {
+                Ref r{false, 0, 0, 0, 0, 0};
+                while (more && (tile >= wk.t1 || wk.gr.n == 0)) {
+                    more = wk.next(p);
+                    tile = wk.t0;
+                }
+                if (more) r = Ref{true, wk.gr.b, wk.h, tile++, wk.gr.limit, (int64_t)wk.gr.b * p.S + wk.gr.st};
+                return r;
+            };
+            auto keys = [&](const Ref& r, int (&t)[4]) {
+                const int k0 = r.tile * kATile + 4 * lane;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) t[i] = -1;
+                if (!r.live) return;
+                if (p.idx) {
+                    const int32_t* src = p.idx + r.row * p.topk;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (k0 + i < p.topk) t[i] = src[k0 + i];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (t[i] >= r.limit) t[i] = -1;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (k0 + i < r.limit) t[i] = k0 + i;
+                }
+            };
+            auto pages = [&](const Ref& r, const int (&t)[4], int (&pid)[4]) {
+                const int32_t* tab = p.table + (int64_t)r.b * p.max_pages;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (i > 0 && !p.idx)
+                        pid[i] = t[i] >= 0 ? pid[0] : -1;  // four keys in a row share a page
+                    else
+                        pid[i] = t[i] >= 0 ? tab[t[i] / p.page] : -1;
+                }
+            };
+            Ref r0 = next_ref();
+            int t0[4], t1[4], t2[4], pid0[4], pid1[4];
+            keys(r0, t0);
+            Ref r1 = next_ref();
+            keys(r1, t1);
+            pages(r0, t0, pid0);
+            int tc = 0;
+            while (ok && r0.live) {
+                float a[4], v[4];
+                bool good[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    good[i] = pid0[i] >= 0 && pid0[i] < p.num_pages;
+                    const int64_t cell = (int64_t)(good[i] ? pid0[i] : 0) * p.Hkv + r0.h;
+                    if (i > 0 && !p.idx) {
+                        a[i] = a[0];
+                        v[i] = v[0];
+                    } else {
+                        a[i] = good[i] ? p.ks[cell] : 0.f;
+                        v[i] = good[i] ? p.vs[cell] : 0.f;
+                    }
+                }
+                pages(r1, t1, pid1);
+                const Ref r2 = next_ref();
+                keys(r2, t2);
+                const int sk = 2 * tc, ms = tc % kAMeta;
+                uint64_t* fullb[2];
+                uint8_t* dst[2];
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const int sl = (sk + w) % SLOTS;
+                    ok = ok && mbar_wait(kv_empty + sl, (((sk + w) / SLOTS) & 1) ^ 1, p.wait_ns);
+                    fullb[w] = kv_full + sl;
+                    dst[w] = smem + sl * kASlotBytes;
+                }
+                ok = ok && mbar_wait(meta_empty + ms, ((tc / kAMeta) & 1) ^ 1, p.wait_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (p.idx) {
+                    const bool any = good[0] || good[1] || good[2] || good[3];
+                    const uint32_t bytes = 512u * __popc(__ballot_sync(0xffffffffu, any));
+                    int row[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        row[i] = good[i] ? (int)(((int64_t)pid0[i] * p.Hkv + r0.h) * p.page + t0[i] % p.page) : 0;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(fullb[0], bytes);
+                        mbar_arrive_expect_tx(fullb[1], bytes);
+                    }
+                    __syncwarp();
+                    if (any) {
+                        tma_gather4(dst[0] + lane * 512, &tmk, fullb[0], 0, row[0], row[1], row[2], row[3]);
+                        tma_gather4(dst[1] + lane * 512, &tmv, fullb[1], 0, row[0], row[1], row[2], row[3]);
+                    }
+                } else {
+                    // the lane with a page's first key loads the page
+                    const bool lead = good[0] && (4 * lane) % p.page == 0;
+                    const uint32_t bytes = (uint32_t)p.page * 128u * __popc(__ballot_sync(0xffffffffu, lead));
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(fullb[0], bytes);
+                        mbar_arrive_expect_tx(fullb[1], bytes);
+                    }
+                    __syncwarp();
+                    if (lead) {
+                        const int row = (int)(((int64_t)pid0[0] * p.Hkv + r0.h) * p.page);
+                        tma_load_2d(dst[0] + lane * 512, &tmk, fullb[0], 0, row);
+                        tma_load_2d(dst[1] + lane * 512, &tmv, fullb[1], 0, row);
+                    }
+                }
+                bool all = true;
+                float2 mv[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    mv[i].x = good[i] ? a[i] * p.scale_log2 : 0.f;
+                    mv[i].y = good[i] ? log2f(fmaxf(v[i], 0x1p-60f)) : -INFINITY;
+                    all = all && good[i];
+                }
+                float4* m4 = reinterpret_cast<float4*>(sMeta + ms * kATile + 4 * lane);
+                m4[0] = make_float4(mv[0].x, mv[0].y, mv[1].x, mv[1].y);
+                m4[1] = make_float4(mv[2].x, mv[2].y, mv[3].x, mv[3].y);
+                all = __all_sync(0xffffffffu, all);
+                if (lane == 0) {
+                    sFlag[ms] = all ? 0 : 1;
+                    mbar_arrive(meta_full + ms);
+                }
+                r0 = r1;
+                r1 = r2;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    t0[i] = t1[i];
+                    t1[i] = t2[i];
+                    pid0[i] = pid1[i];
+                }
+                ++tc;
+            }
+            if (!ok && !p.debug_stall)  // loads in flight end before the memory is given up
+                for (int seq = max(0, 2 * tc - SLOTS); seq < 2 * tc; ++seq)
+                    mbar_wait(kv_full + seq % SLOTS, (seq / SLOTS) & 1, p.wait_ns);
+        } else {
+            // ------------------------------------- queries: bf16 rows -> e4m3 hi and lo
+            // Eight lanes a row, 16 dims each; the two warps take rows 8i .. 8i+3 and 8i+4 .. 8i+7.
+            bool ok = true;
+            int sc = 0;
+            const int sub = lane & 7;
+            while (wk.next(p)) {
+                if (wk.gr.n == 0) continue;
+                const int qb = sc % QB;
+                ok = ok && mbar_wait(q_empty + qb, ((sc / QB) & 1) ^ 1, p.wait_ns);
+                uint8_t* dst = sQ + qb * C::Q_BYTES;
+#pragma unroll 2
+                for (int n = (warp - 2) * 4 + (lane >> 3); n < N; n += 8) {
+                    const int st = n / p.G, s = wk.gr.st * p.TS + st;
+                    const bool in = st < p.TS && s < p.S && sub * 16 < p.D;
+                    uint32_t w[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) w[i] = 0;
+                    if (in) {
+                        const uint4* src = reinterpret_cast<const uint4*>(
+                            p.q + wk.gr.b * p.qs[0] + s * p.qs[1] + (wk.h * p.G + n - st * p.G) * p.qs[2] + sub * 16);
+                        const uint4 u0 = src[0], u1 = src[1];
+                        w[0] = u0.x, w[1] = u0.y, w[2] = u0.z, w[3] = u0.w;
+                        w[4] = u1.x, w[5] = u1.y, w[6] = u1.z, w[7] = u1.w;
+                    }
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+                    top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+                    for (int i = 1; i < 8; i <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, i));
+                    // 2^(7 - exponent) brings the largest to [128, 256); exponents are kept where both the
+                    // factor and its inverse are normal numbers
+                    int ex = (int)(top >> 7);
+                    ex = top == 0 ? 127 + 7 : (ex < 16 ? 16 : ex);
+                    const float up = __int_as_float((254 + 7 - ex) << 23);
+                    if (sub == 0) sQs[qb * N + n] = __int_as_float((ex - 7) << 23);
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t h0, l0, h1, l1;
+                        split_e4m3(__uint_as_float(w[2 * i] << 16) * up, __uint_as_float(w[2 * i] & 0xffff0000u) * up, h0,
+                                   l0);
+                        split_e4m3(__uint_as_float(w[2 * i + 1] << 16) * up,
+                                   __uint_as_float(w[2 * i + 1] & 0xffff0000u) * up, h1, l1);
+                        hi[i] = h0 | (h1 << 16);
+                        lo[i] = l0 | (l1 << 16);
+                    }
+                    uint8_t* at = dst + n * 128 + ((sub ^ (n & 7)) << 4);  // 128-byte swizzle
+                    *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(at + N * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full + qb);
+                ++sc;
+            }
+        }
+    } else if (warp < 12) {
+        // -------------------------------------------------------------- softmax
+        // A thread has one key of a tile and the columns [c0, c0 + NC).  Up to N = 64 the two groups take
+        // the tiles in turn; at N = 128 each takes half of every tile's columns.
+        regs_inc<136>();
+        const int grp = (warp - 4) >> 2, wtid = tid - 128 - grp * 128, wg_warp = warp & 3;
+        const int c0 = C::SPLIT ? grp * NC : 0;
+        const uint32_t bar_id = 1 + grp;
+        float* const sW = (float*)(smem + C::OFF_W) + grp * 4 * NC;
+        float2* const sMB = (float2*)(smem + C::OFF_MB) + grp * NC;
+        float* const sAl = (float*)(smem + C::OFF_AL) + grp * NC;
+        int* const sEnd = (int*)(smem + C::OFF_END) + grp * NC;
+        const uint32_t lane_addr = tmem + ((uint32_t)(wg_warp * 32) << 16) + c0;
+        bool ok = true;
+        int tc = 0, sc = 0;
+        while (wk.next(p)) {
+            if (wk.gr.n == 0) continue;
+            const int qb = sc % QB;
+            // keys each column sees
+            const int st0 = wk.gr.st * p.TS;
+            named_bar_sync(bar_id, 128);  // the last segment's are read
+            if (wtid < NC) {
+                const int st = (c0 + wtid) / p.G;
+                sEnd[wtid] = p.idx ? INT_MAX : (st < p.TS && st0 + st < p.S ? attn_end(p, wk.gr.b, st0 + st) : 0);
+            }
+            const int least = p.idx ? INT_MAX : attn_end(p, wk.gr.b, st0);
+            named_bar_sync(bar_id, 128);
+            ok = ok && mbar_wait(q_full + qb, (sc / QB) & 1, p.wait_ns);
+            const float* const qs = sQs + qb * N + c0;
+            float l[NC];
+#pragma unroll
+            for (int i = 0; i < NC; ++i) l[i] = 0.f;
+            float mw = -INFINITY;  // of column wtid
+            for (int t = wk.t0; t < wk.t1; ++t, ++tc) {
+                if (!C::SPLIT && (tc & 1) != grp) continue;
+                const int bf = tc & 1, ph = (tc >> 1) & 1, ms = tc % kAMeta;
+                ok = ok && mbar_wait(meta_full + ms, (tc / kAMeta) & 1, p.wait_ns);
+                const float2 mv = sMeta[ms * kATile + wtid];
+                const bool flag = sFlag[ms] != 0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(meta_empty + ms);
+                const int key = t * kATile + wtid;
+                const bool seen = mv.y != -INFINITY;
+                const bool masked = flag || t * kATile + kATile > least;
+                const uint64_t a2 = pack2(mv.x, mv.x), lv2 = pack2(mv.y, mv.y);
+                ok = ok && mbar_wait(s_full + bf, ph, p.wait_ns);
+                tc_fence_after();
+                const uint32_t s_addr = lane_addr + bf * N;
+                uint8_t* const prow = sP + bf * C::P_BYTES + wtid * 128;
+
+                auto one_tile = [&](auto mask_c) {
+                    constexpr bool MASK = decltype(mask_c)::value;
+                    float x[CH];
+#pragma unroll
+                    for (int cc = 0; cc < NC; cc += CH) {
+                        attn_scores<MASK, CH>(s_addr + cc, qs + cc, sEnd + cc, a2, lv2, key, seen, x);
+                        float mine = 0.f;
+#pragma unroll
+                        for (int i = 0; i < CH; ++i) {
+                            const float r = warp_max(x[i]);
+                            mine = lane == i ? r : mine;
+                        }
+                        if (lane < CH) sW[wg_warp * NC + cc + lane] = mine;
+                    }
+                    named_bar_sync(bar_id, 128);
+                    bool fade = false;
+                    ok = ok && mbar_wait(m_read + bf, ph ^ 1, p.wait_ns);
+                    if (wtid < NC) {
+                        const float M = fmaxf(fmaxf(sW[wtid], sW[NC + wtid]), fmaxf(sW[2 * NC + wtid], sW[3 * NC + wtid]));
+                        const float mn = fmaxf(mw, M);
+                        fade = mn > mw && mw != -INFINITY;
+                        sAl[wtid] = fade ? exp2_approx(mw - mn) : 1.f;
+                        sMB[wtid] = M == -INFINITY ? make_float2(kATop, 0.f) : make_float2(kATop - M, exp2_approx(M - mn));
+                        sMt[bf * N + c0 + wtid] = M;
+                        mw = mn;
+                    }
+                    if (named_bar_or(bar_id, 128, fade)) {
+#pragma unroll
+                        for (int i = 0; i < NC; i += 4) {
+                            const float4 f = *reinterpret_cast<const float4*>(sAl + i);
+                            l[i] *= f.x, l[i + 1] *= f.y, l[i + 2] *= f.z, l[i + 3] *= f.w;
+                        }
+                    }
+                    ok = ok && mbar_wait(o_full + bf, ph ^ 1, p.wait_ns);  // the weights before last are read
+                    const float ivs = exp2_approx(-mv.y);
+                    const uint64_t iv2 = seen ? pack2(ivs, ivs) : pack2(0.f, 0.f);
+#pragma unroll
+                    for (int cc = 0; cc < NC; cc += CH) {
+                        if constexpr (NC > CH)
+                            attn_scores<MASK, CH>(s_addr + cc, qs + cc, sEnd + cc, a2, lv2, key, seen, x);
+                        uint32_t hi[CH / 4], lo[CH / 4];
+#pragma unroll
+                        for (int i = 0; i < CH; i += 2) {
+                            const float4 mb = *reinterpret_cast<const float4*>(sMB + cc + i);
+                            float e0, e1;
+                            unpack2(add2(pack2(x[i], x[i + 1]), pack2(mb.x, mb.z)), e0, e1);
+                            const float w0 = exp2_approx(e0), w1 = exp2_approx(e1);
+                            unpack2(fma2(mul2(pack2(w0, w1), iv2), pack2(mb.y, mb.w), pack2(l[cc + i], l[cc + i + 1])),
+                                    l[cc + i], l[cc + i + 1]);
+                            uint32_t h2, l2;
+                            split_e4m3(w0, w1, h2, l2);
+                            if (i & 2) {
+                                hi[i / 4] |= h2 << 16;
+                                lo[i / 4] |= l2 << 16;
+                            } else {
+                                hi[i / 4] = h2;
+                                lo[i / 4] = l2;
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < CH / 16; ++k) {
+                            const int j = (((c0 + cc) >> 4) + k) ^ (wtid & 7);  // 128-byte swizzle
+                            *reinterpret_cast<uint4*>(prow + (j << 4)) =
+                                make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
+                            *reinterpret_cast<uint4*>(prow + kASlotBytes + (j << 4)) =
+                                make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
+                        }
+                    }
+                };
+                if (masked)
+                    one_tile(std::true_type{});
+                else
+                    one_tile(std::false_type{});
+                if (flag && c0 == 0) {
+                    // unseen slots may hold anything (NaN codes): a zero weight alone would not keep them out
+                    const int seq = 2 * tc + 1, sl = seq % SLOTS;
+                    ok = ok && mbar_wait(kv_full + sl, (seq / SLOTS) & 1, p.wait_ns);
+                    if (!seen && ok) {
+                        uint4* vrow = reinterpret_cast<uint4*>(smem + sl * kASlotBytes + wtid * 128);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) vrow[i] = make_uint4(0, 0, 0, 0);
+                    }
+                }
+                fence_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + bf);
+            }
+            // the segment's sums: lanes, then (by the joining warps) warps and groups
+            ok = ok && mbar_wait(l_empty, (sc & 1) ^ 1, p.wait_ns);
+#pragma unroll
+            for (int cc = 0; cc < NC; cc += CH) {
+                float v[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = i < CH ? l[cc + (i < CH ? i : 0)] : 0.f;
+                const float sum = warp_sum_columns(v, lane);
+                if (lane < CH) sL[(grp * 4 + wg_warp) * NC + cc + lane] = sum;
+            }
+            if (wtid < NC) sMw[grp * NC + wtid] = mw;
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(l_full);
+                mbar_arrive(q_empty + qb);
+            }
+            ++sc;
+        }
+    } else {
+        // ---------------------------------------------------------------- joining
+        // A thread has one output dim (TMEM lane) of every column; thread i < N also keeps column i's maximum.
+        regs_inc<160>();
+        const int d = tid - 384, wg_warp = warp & 3;
+        const uint32_t lane_addr = tmem + ((uint32_t)(wg_warp * 32) << 16) + 2 * N;
+        float2* const sAB = (float2*)(smem + C::OFF_AB);
+        float* const sInv = (float*)(smem + C::OFF_INV);
+        int* const sRow = (int*)(smem + C::OFF_ROW);
+        bool ok = true;
+        int tc = 0, sc = 0;
+        AttnHeader hd{0, 0, 0, 0, 0, W};
+        float* const parts = (float*)(p.ws + (size_t)nc * sizeof(AttnHeader));
+        while (wk.next(p)) {
+            float acc[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) acc[i] = 0.f;
+            float m = -INFINITY, l = 0.f;
+            if (wk.gr.n > 0) {
+                for (int t = wk.t0; t < wk.t1; ++t, ++tc) {
+                    const int bf = tc & 1, ph = (tc >> 1) & 1;
+                    ok = ok && mbar_wait(p_full + bf, ph, p.wait_ns);
+                    if (d < N) {
+                        const float M = sMt[bf * N + d], mn = fmaxf(m, M);
+                        sAB[bf * N + d] = make_float2(m == -INFINITY ? 0.f : exp2_approx(m - mn),
+                                                      M == -INFINITY ? 0.f : exp2_approx(M - mn));
+                        m = mn;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(m_read + bf);
+                    named_bar_sync(3, 128);
+                    ok = ok && mbar_wait(o_full + bf, ph, p.wait_ns);
+                    tc_fence_after();
+#pragma unroll
+                    for (int cc = 0; cc < N; cc += 16) {
+                        uint32_t r[16];
+                        tmem_ld16(lane_addr + bf * N + cc, r);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            const float4 ab = *reinterpret_cast<const float4*>(sAB + bf * N + cc + i);
+                            const uint64_t o = mul2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])),
+                                                    pack2(ab.y, ab.w));
+                            unpack2(fma2(pack2(acc[cc + i], acc[cc + i + 1]), pack2(ab.x, ab.z), o), acc[cc + i],
+                                    acc[cc + i + 1]);
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(o_empty + bf);
+                }
+                ok = ok && mbar_wait(l_full, sc & 1, p.wait_ns);
+                if (d < N) {
+#pragma unroll
+                    for (int gi = 0; gi < 2; ++gi) {
+                        if (C::SPLIT && gi != d / NC) continue;
+                        const int col = C::SPLIT ? d % NC : d;
+                        const float* s = sL + gi * 4 * NC + col;
+                        const float mg = sMw[gi * NC + col];
+                        if (mg != -INFINITY) l += ((s[0] + s[NC]) + (s[2 * NC] + s[3 * NC])) * exp2_approx(mg - m);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(l_empty);
+                ++sc;
+            }
+            const bool whole = wk.t0 == 0 && wk.t1 == wk.gr.w;
+            if (whole) {
+                if (d < N) {
+                    const int st = d / p.G, s = wk.gr.st * p.TS + st;
+                    const int row = st < p.TS && s < p.S
+                                        ? (wk.gr.b * p.S + s) * p.Hq + wk.h * p.G + d - st * p.G
+                                        : -1;
+                    sRow[d] = row;
+                    sInv[d] = l > 0.f ? 1.f / l : 0.f;
+                    if (p.lse && row >= 0) p.lse[row] = l > 0.f ? (m + log2f(l) - kATop) * kALn2 : -INFINITY;
+                }
+                named_bar_sync(3, 128);
+                if (d < p.D) {
+                    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) + d;
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        const int row = sRow[i];
+                        if (row >= 0) out[(int64_t)row * p.D] = __float2bfloat16_rn(acc[i] * sInv[i]);
+                    }
+                }
+                named_bar_sync(3, 128);
+            } else {
+                const int slot = 2 * c + (wk.first ? 0 : 1);
+                float* part = parts + slot * attn_part_floats(N);
+#pragma unroll
+                for (int i = 0; i < N; ++i) part[i * 128 + d] = acc[i];
+                if (d < N) {
+                    part[N * 128 + d] = m;
+                    part[N * 128 + N + d] = l;
+                }
+                if (wk.t0 == 0) hd = AttnHeader{1, wk.g, wk.h, slot, wk.unit_end, W};
+            }
+        }
+        if (d == 0) reinterpret_cast<AttnHeader*>(p.ws)[c] = hd;
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM);
+    }
+}
+
+// Joins the parts of the units that were cut: block (c, y) takes kJoinRows rows of the unit whose first tiles CTA c had.
+// Parts are added in the line's order.
+constexpr int kJoinRows = 4;
+template <int N>
+__global__ void __launch_bounds__(128) cache_attn_join_kernel(const AttnParams p, int nc) {
+    grid_dependency_wait();
+    const AttnHeader hd = reinterpret_cast<const AttnHeader*>(p.ws)[blockIdx.x];
+    if (!hd.owner) return;
+    const float* parts = (const float*)(p.ws + (size_t)nc * sizeof(AttnHeader));
+    const int d = threadIdx.x, b = hd.g / p.ST, st0 = hd.g % p.ST * p.TS;
+#pragma unroll 1
+    for (int r = 0; r < kJoinRows; ++r) {
+        const int n = blockIdx.y * kJoinRows + r, st = n / p.G, s = st0 + st;
+        if (st >= p.TS || s >= p.S) break;
+        float m = -INFINITY;
+        for (int c = blockIdx.x; c < nc && attn_share(hd.W, c, nc) < hd.unit_end; ++c) {
+            if (attn_share(hd.W, c, nc) == attn_share(hd.W, c + 1, nc)) continue;
+            const int slot = c == blockIdx.x ? hd.slot : 2 * c;
+            m = fmaxf(m, parts[slot * attn_part_floats(N) + N * 128 + n]);
+        }
+        float l = 0.f, o = 0.f;
+        for (int c = blockIdx.x; m != -INFINITY && c < nc && attn_share(hd.W, c, nc) < hd.unit_end; ++c) {
+            if (attn_share(hd.W, c, nc) == attn_share(hd.W, c + 1, nc)) continue;
+            const float* part = parts + (c == blockIdx.x ? hd.slot : 2 * c) * attn_part_floats(N);
+            const float f = exp2_approx(part[N * 128 + n] - m);
+            l += part[N * 128 + N + n] * f;
+            o += part[n * 128 + d] * f;
+        }
+        const int64_t row = ((int64_t)b * p.S + s) * p.Hq + hd.h * p.G + n - st * p.G;
+        if (d < p.D)
+            reinterpret_cast<__nv_bfloat16*>(p.out)[row * p.D + d] = __float2bfloat16_rn(l > 0.f ? o / l : 0.f);
+        if (p.lse && d == 0) p.lse[row] = l > 0.f ? (m + log2f(l) - kATop) * kALn2 : -INFINITY;
+    }
+}
+
+// ------------------------------------------------------------------- host
+
+// Columns of the configuration for a call: the fewest that hold a row's group of heads and, without
+// indices, as many of the sequence's query tokens as fit.
+static int attn_columns(int64_t S, int G, bool selected) {
+    const int64_t want = selected ? G : (S * G < 128 ? S * G : 128);
+    return want <= 16 ? 16 : (want <= 32 ? 32 : (want <= 64 ? 64 : 128));
+}
+
+static int attn_cache_map(CUtensorMap* m, const void* cache, int64_t rows, int D, int box_rows) {
+    const cuuint64_t dim[2] = {(cuuint64_t)D, (cuuint64_t)rows};
+    const cuuint64_t str[1] = {(cuuint64_t)D};
+    const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+    const cuuint32_t es[2] = {1, 1};
+    return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, (void*)cache, dim, str, box, es,
+                        CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int N>
+static cudaError_t attn_launch(const CUtensorMap& mk, const CUtensorMap& mv, const AttnParams& p, int grid,
+                               cudaStream_t st) {
+    cudaError_t e = set_smem_attr((const void*)cache_attn_kernel<N>, AttnCfg<N>::TOTAL);
+    if (e != cudaSuccess) return e;
+    cache_attn_kernel<N><<<grid, kAThreads, AttnCfg<N>::TOTAL, st>>>(mk, mv, p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || grid == 1) return e;
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof cfg);
+    const int rows = p.TS * p.G;
+    cfg.gridDim = dim3(grid, (rows + kJoinRows - 1) / kJoinRows);
+    cfg.blockDim = dim3(128);
+    cfg.stream = st;
+    // the join is set up while the main kernel runs; it waits for its end itself
+    cudaLaunchAttribute at;
+    memset(&at, 0, sizeof at);
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<N>, p, grid);
+}
+
+LIDX_STATUS_READER(status_cache_attn)
 
 }  // namespace lidx
 
@@ -120,8 +988,11 @@ using namespace lidx;
 extern "C" {
 
 size_t lidx_cache_attn_workspace_bytes(int64_t B, int64_t S, int Hq, int Hkv, int D, int topk) {
-    (void)B, (void)S, (void)Hq, (void)Hkv, (void)D, (void)topk;
-    return 0;
+    (void)B, (void)D;
+    if (S < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv || Hq / Hkv > 128) return 0;
+    int sms = sm103_sms();
+    if (sms <= 0) sms = 256;  // no device: an upper bound
+    return attn_ws_bytes(attn_columns(S, Hq / Hkv, topk > 0), sms);
 }
 
 int lidx_cache_attn(const void* q, const int64_t* qs, const void* k_cache, const void* v_cache,
@@ -142,13 +1013,12 @@ int lidx_cache_attn(const void* q, const int64_t* qs, const void* k_cache, const
          (uintptr_t)q_pos | (uintptr_t)topk_indices | (uintptr_t)lse) & 3u)
         return LIDX_ERR_ALIGN;
     if ((qs[0] | qs[1] | qs[2]) & 7) return LIDX_ERR_ALIGN;
-    if (sm103_sms() <= 0) return LIDX_ERR_NO_DEVICE;
-    (void)workspace, (void)workspace_bytes;
+    const int sms = sm103_sms();
+    if (sms <= 0) return LIDX_ERR_NO_DEVICE;
     AttnParams p;
+    memset(&p, 0, sizeof p);
     p.q = (const uint16_t*)q;
     for (int i = 0; i < 3; ++i) p.qs[i] = qs[i];
-    p.kc = (const uint8_t*)k_cache;
-    p.vc = (const uint8_t*)v_cache;
     p.ks = k_scale;
     p.vs = v_scale;
     p.table = block_table;
@@ -160,16 +1030,41 @@ int lidx_cache_attn(const void* q, const int64_t* qs, const void* k_cache, const
     p.S = (int)S;
     p.Hq = Hq;
     p.Hkv = Hkv;
+    p.G = Hq / Hkv;
     p.D = D;
     p.page = page;
     p.max_pages = (int)max_pages;
     p.ratio = compress_ratio;
     p.topk = topk;
-    p.scale = softmax_scale;
+    const int N = attn_columns(S, p.G, topk_indices != nullptr);
+    p.TS = topk_indices ? 1 : (int)(N / p.G < S ? N / p.G : S);
+    p.ST = (int)((S + p.TS - 1) / p.TS);
+    p.scale_log2 = softmax_scale * 1.44269504088896341f;
     p.out = (uint16_t*)out;
     p.lse = lse;
-    cache_attn_kernel<<<(unsigned)(B * S * Hq), kAttnThreads, 0, (cudaStream_t)stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? LIDX_OK : LIDX_ERR_CUDA;
+    p.wait_ns = wait_limit_ns();
+    p.debug_stall = debug_stall();
+    // no more CTAs than the line can have places
+    const int64_t tiles = topk_indices ? (topk + kATile - 1) / kATile : (max_pages * page + kATile - 1) / kATile;
+    const int64_t most = tiles * B * p.ST * Hkv;
+    const int grid = most < sms ? (int)most : sms;
+    const size_t need = attn_ws_bytes(N, grid);
+    if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u)) return LIDX_ERR_WORKSPACE;
+    p.ws = (uint8_t*)workspace;
+    CUtensorMap mk, mv;
+    const int box = topk_indices ? 1 : page;
+    if (attn_cache_map(&mk, k_cache, num_pages * Hkv * page, D, box) ||
+        attn_cache_map(&mv, v_cache, num_pages * Hkv * page, D, box))
+        return LIDX_ERR_CUDA;
+    cudaStream_t st = (cudaStream_t)stream;
+    cudaError_t e;
+    switch (N) {
+        case 16: e = attn_launch<16>(mk, mv, p, grid, st); break;
+        case 32: e = attn_launch<32>(mk, mv, p, grid, st); break;
+        case 64: e = attn_launch<64>(mk, mv, p, grid, st); break;
+        default: e = attn_launch<128>(mk, mv, p, grid, st); break;
+    }
+    return e == cudaSuccess ? LIDX_OK : LIDX_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -121,5 +121,6 @@ int status_score_v4_fused(int clear);
 int status_score_v41(int clear);
 int status_misc(int clear);
 int status_bwd(int clear);
+int status_cache_attn(int clear);
 
 }  // namespace lidx

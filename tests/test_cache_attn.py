@@ -300,6 +300,34 @@ def test_offsets_past_32_bits():
 
 
 @pytest.mark.gpu
+def test_workspace_refusals():
+    c = Case(16, 1, 1, 8, 1, 64, 16, [40])
+    need = lidx.lidx_cache_attn_workspace_bytes(1, 1, 8, 1, 64)
+    assert need > 0
+    for ws in (torch.empty(need + 512, dtype=torch.uint8, device=DEV)[16:], torch.empty(64, dtype=torch.uint8, device=DEV)):
+        with pytest.raises(lidx.LidxError) as e:
+            lidx.lidx_cache_attn(*c.args(), workspace=ws)
+        assert e.value.status == 5
+    _status_ok()
+
+
+@pytest.mark.gpu
+def test_stall_times_out_and_the_next_call_is_correct():
+    """The producer loads nothing, every wait runs out, the launch ends by itself and says so."""
+    c = Case(17, 3, 1, 16, 2, 64, 32, [500, 0, 90])
+    assert lidx.lidx_device_status() == 0
+    old = lidx.lidx_set_wait_limit_ns(2_000_000)
+    lidx.lidx_debug_stall_producer(True)
+    try:
+        lidx.lidx_cache_attn(*c.args())
+        assert lidx.lidx_device_status() == 7
+    finally:
+        lidx.lidx_debug_stall_producer(False)
+        lidx.lidx_set_wait_limit_ns(old)
+    c.check()
+
+
+@pytest.mark.gpu
 def test_binding_refusals():
     c = Case(15, 2, 1, 4, 2, 32, 16, [20, 30])
     ok = c.args()
