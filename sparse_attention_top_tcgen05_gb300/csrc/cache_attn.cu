@@ -50,6 +50,10 @@ struct AttnParams {
     int64_t num_pages;
     int B, S, Hq, Hkv, G, D, page, max_pages, ratio, topk;
     int TS, ST;            // query tokens of a unit; units of a sequence
+    int page_shift;        // page = 1 << page_shift
+    uint32_t inv_g;        // ceil(2^16 / G): n / G = n * inv_g >> 16 for n < 128
+    const uint8_t* kc;     // the caches, for gathered keys
+    const uint8_t* vc;
     float scale_log2;      // softmax_scale * log2(e)
     uint16_t* out;
     float* lse;            // nullable
@@ -80,21 +84,23 @@ struct AttnCfg {
     static constexpr int OFF_FLAG = OFF_META + kAMeta * kATile * 8;    // [kAMeta] int
     static constexpr int OFF_QS = OFF_FLAG + 64;                       // [2][N] query scales
     static constexpr int OFF_W = OFF_QS + 2 * N * 4;                   // [2][4][NC] warp maxima
-    static constexpr int OFF_MB = OFF_W + 2 * 4 * NC * 4;              // [2][NC] float2 (8 - M, fade of the tile)
+    static constexpr int OFF_MB = OFF_W + 2 * 4 * NC * 4;              // [2][2][NC] 8 - M; fade of the tile
     static constexpr int OFF_AL = OFF_MB + 2 * NC * 8;                 // [2][NC] fade of the sum
     static constexpr int OFF_END = OFF_AL + 2 * NC * 4;                // [2][NC] keys a column sees
     static constexpr int OFF_MT = OFF_END + 2 * NC * 4;                // [2][N] tile maxima
-    static constexpr int OFF_AB = OFF_MT + 2 * N * 4;                  // [2][N] float2 fades of acc and tile
+    static constexpr int OFF_AB = OFF_MT + 2 * N * 4;                  // [2][2][N] fades of acc and tile
     static constexpr int OFF_L = OFF_AB + 2 * N * 8;                   // [2][4][NC] sums of the warps
     static constexpr int OFF_MW = OFF_L + 2 * 4 * NC * 4;              // [2][NC] their reference
     static constexpr int OFF_INV = OFF_MW + 2 * NC * 4;                // [N] 1 / l
     static constexpr int OFF_ROW = OFF_INV + N * 4;                    // [N] output rows
-    static constexpr int OFF_BAR = (OFF_ROW + N * 4 + 15) / 16 * 16;
+    static constexpr int OFF_GATHER = OFF_ROW + N * 4;                 // [128] cache rows of a tile's keys
+    static constexpr int OFF_BAR = OFF_GATHER + kATile * 4;
     static constexpr int NBAR = 2 * SLOTS + 2 * kAMeta + 2 * 2 + 5 * 2 + 2 + 1;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;                // start of the share, TMEM address
     static constexpr int TOTAL = OFF_MISC + 256 + 1024;                // + alignment of the base
     static_assert(TOTAL <= 232448 && kAMeta * 4 <= 64, "shared memory");
-    static_assert(OFF_QS % 16 == 0 && OFF_MB % 16 == 0 && OFF_AL % 16 == 0 && OFF_END % 16 == 0 && OFF_AB % 16 == 0,
+    static_assert(OFF_QS % 16 == 0 && OFF_MB % 16 == 0 && OFF_AL % 16 == 0 && OFF_END % 16 == 0 && OFF_AB % 16 == 0 && OFF_W % 16 == 0 &&
+                      OFF_GATHER % 16 == 0,
                   "16-byte reads");
     static constexpr int TMEM = 4 * N;                                 // columns: two tiles of S and of O
 };
@@ -128,6 +134,8 @@ __device__ __forceinline__ AttnGroup attn_group(const AttnParams& p, int g) {
     r.w = max(r.n, 1);
     return r;
 }
+// Query token of column n within a unit.
+__device__ __forceinline__ int attn_token(const AttnParams& p, int n) { return (int)(n * p.inv_g >> 16); }
 __device__ __forceinline__ int64_t attn_share(int64_t W, int c, int n) { return W * c / n; }
 
 // The segments [t0, t1) of units that make up a CTA's share; every role walks them alike.
@@ -169,8 +177,8 @@ struct AttnWalk {
 
 // Workspace: a header for each CTA, then two parts for each (its first segment, its last).
 struct AttnHeader {
-    int32_t owner, g, h, slot;  // owner: the CTA holds the first tiles of a unit that goes on behind it
-    int64_t unit_end, W;
+    // last > 0: the CTA holds the first tiles (in part `slot`) of a unit that ends with CTA `last`'s first segment
+    int32_t last, g, h, slot;
 };
 __host__ __device__ inline size_t attn_part_floats(int N) { return (size_t)N * 128 + 2 * N; }
 __host__ __device__ inline size_t attn_ws_bytes(int N, int grid) {
@@ -302,15 +310,17 @@ __global__ void __launch_bounds__(kAThreads, 1)
     }
 
     // ---- this CTA's share of the line
-    const int nc = gridDim.x, c = blockIdx.x;
+    const int c = blockIdx.x;
+    int nc = gridDim.x;  // CTAs with a share
     int64_t W, pos0, pos1, base0 = 0;
     int g0 = 0;
     if (p.idx) {
         // every unit has the same places
         const int64_t w = (int64_t)((p.topk + kATile - 1) / kATile) * p.Hkv;
         W = w * p.B * p.ST;
-        pos0 = attn_share(W, c, nc);
-        pos1 = attn_share(W, c + 1, nc);
+        nc = W < nc ? (int)W : nc;
+        pos0 = attn_share(W, min(c, nc), nc);
+        pos1 = attn_share(W, min(c + 1, nc), nc);
         g0 = (int)(pos0 / w);
         base0 = g0 * w;
     } else {
@@ -333,8 +343,9 @@ __global__ void __launch_bounds__(kAThreads, 1)
             if (i == warp) before = W;
             W += sScan[i];
         }
-        pos0 = attn_share(W, c, nc);
-        pos1 = attn_share(W, c + 1, nc);
+        nc = W < nc ? (int)W : nc;
+        pos0 = attn_share(W, min(c, nc), nc);
+        pos1 = attn_share(W, min(c + 1, nc), nc);
         int64_t at = before + incl - sum;
         if (pos0 >= at && pos0 < at + sum) {
             int g = ga;
@@ -362,7 +373,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
         regs_dec<80>();
         if (warp == 0) {
             // ------------------------------------------------------- MMA issuer
-            // The whole warp walks and waits; lane 0 issues.
+            // The whole warp walks and waits; one lane issues.
+            const bool issuer = elect_one();
             const uint32_t id_s = idesc_e4m3_f32(128, N);
             const uint32_t id_o = idesc_e4m3_f32(128, N) | kIdescAMn | kIdescBMn;
             const int nk = (p.D + 31) / 32;
@@ -381,7 +393,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) return;
                 tc_fence_after();
-                if (lane == 0) {
+                if (issuer) {
                     const uint64_t a = dv0 + (uint64_t)(sl * (kASlotBytes >> 4));
                     const uint64_t b = dp0 + (uint64_t)(bf * (C::P_BYTES >> 4));
                     const uint32_t d = tmem + 2 * N + bf * N;
@@ -405,16 +417,23 @@ __global__ void __launch_bounds__(kAThreads, 1)
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc_fence_after();
-                    if (lane == 0) {
+                    if (issuer) {
                         const uint64_t a = dk0 + (uint64_t)(sl * (kASlotBytes >> 4));
                         const uint64_t b = dq0 + (uint64_t)(qb * (C::Q_BYTES >> 4));
                         const uint32_t d = tmem + (tc & 1) * N;
-                        // 32 dims a step, hi then lo.  Loops, not unrolled conditions: with `if (k < nk)` around
-                        // each of eight unrolled products the N = 128 build multiplied by wrong operands.
+                        // 32 dims a step, hi then lo
+                        if (nk == 4) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) umma_f8(d, a + 2 * k, b + 2 * k, id_s, k > 0);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) umma_f8(d, a + 2 * k, b + (N * 128 >> 4) + 2 * k, id_s, 1);
+                        } else {
+                            // (with `if (k < nk)` around unrolled products the N = 128 build took wrong operands)
 #pragma unroll 1
-                        for (int k = 0; k < nk; ++k) umma_f8(d, a + 2 * k, b + 2 * k, id_s, k > 0);
+                            for (int k = 0; k < nk; ++k) umma_f8(d, a + 2 * k, b + 2 * k, id_s, k > 0);
 #pragma unroll 1
-                        for (int k = 0; k < nk; ++k) umma_f8(d, a + 2 * k, b + (N * 128 >> 4) + 2 * k, id_s, 1);
+                            for (int k = 0; k < nk; ++k) umma_f8(d, a + 2 * k, b + (N * 128 >> 4) + 2 * k, id_s, 1);
+                        }
                         umma_commit(s_full + (tc & 1));
                         umma_commit(kv_empty + sl);
                         if (t == wk.t1 - 1) umma_commit(q_empty + qb);
@@ -426,7 +445,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
             }
             if (ok && tc > 0) second(tc - 1);
             if (!__all_sync(0xffffffffu, ok)) {  // products in flight end before the memory is given up
-                if (lane == 0) umma_commit(drain);
+                if (issuer) umma_commit(drain);
                 mbar_wait(drain, 0, p.wait_ns);
             }
         } else if (warp == 1) {
@@ -450,133 +469,168 @@ __global__ void __launch_bounds__(kAThreads, 1)
                 if (more) r = Ref{true, wk.gr.b, wk.h, tile++, wk.gr.limit, (int64_t)wk.gr.b * p.S + wk.gr.st};
                 return r;
             };
-            auto keys = [&](const Ref& r, int (&t)[4]) {
-                const int k0 = r.tile * kATile + 4 * lane;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) t[i] = -1;
-                if (!r.live) return;
-                if (p.idx) {
-                    const int32_t* src = p.idx + r.row * p.topk;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (k0 + i < p.topk) t[i] = src[k0 + i];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (t[i] >= r.limit) t[i] = -1;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (k0 + i < r.limit) t[i] = k0 + i;
-                }
-            };
-            auto pages = [&](const Ref& r, const int (&t)[4], int (&pid)[4]) {
-                const int32_t* tab = p.table + (int64_t)r.b * p.max_pages;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (i > 0 && !p.idx)
-                        pid[i] = t[i] >= 0 ? pid[0] : -1;  // four keys in a row share a page
-                    else
-                        pid[i] = t[i] >= 0 ? tab[t[i] / p.page] : -1;
-                }
-            };
-            Ref r0 = next_ref();
-            int t0[4], t1[4], t2[4], pid0[4], pid1[4];
-            keys(r0, t0);
-            Ref r1 = next_ref();
-            keys(r1, t1);
-            pages(r0, t0, pid0);
             int tc = 0;
-            while (ok && r0.live) {
-                float a[4], v[4];
-                bool good[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    good[i] = pid0[i] >= 0 && pid0[i] < p.num_pages;
-                    const int64_t cell = (int64_t)(good[i] ? pid0[i] : 0) * p.Hkv + r0.h;
-                    if (i > 0 && !p.idx) {
-                        a[i] = a[0];
-                        v[i] = v[0];
-                    } else {
-                        a[i] = good[i] ? p.ks[cell] : 0.f;
-                        v[i] = good[i] ? p.vs[cell] : 0.f;
-                    }
-                }
-                pages(r1, t1, pid1);
-                const Ref r2 = next_ref();
-                keys(r2, t2);
+            const int page_mask = p.page - 1;
+            // waits for the slots of tile tc's K and V and its stage of scales
+            auto claim = [&]() {
                 const int sk = 2 * tc, ms = tc % kAMeta;
-                uint64_t* fullb[2];
-                uint8_t* dst[2];
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const int sl = (sk + w) % SLOTS;
-                    ok = ok && mbar_wait(kv_empty + sl, (((sk + w) / SLOTS) & 1) ^ 1, p.wait_ns);
-                    fullb[w] = kv_full + sl;
-                    dst[w] = smem + sl * kASlotBytes;
-                }
+                for (int w = 0; w < 2; ++w)
+                    ok = ok && mbar_wait(kv_empty + (sk + w) % SLOTS, (((sk + w) / SLOTS) & 1) ^ 1, p.wait_ns);
                 ok = ok && mbar_wait(meta_empty + ms, ((tc / kAMeta) & 1) ^ 1, p.wait_ns);
                 ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                if (p.idx) {
-                    const bool any = good[0] || good[1] || good[2] || good[3];
-                    const uint32_t bytes = 512u * __popc(__ballot_sync(0xffffffffu, any));
-                    int row[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        row[i] = good[i] ? (int)(((int64_t)pid0[i] * p.Hkv + r0.h) * p.page + t0[i] % p.page) : 0;
+            };
+            if (!p.idx) {
+                // Pages: the four keys of a lane share one; the lane with a page's first key loads it.
+                auto page_id = [&](const Ref& r) {
+                    const int k0 = r.tile * kATile + 4 * lane;
+                    return r.live && k0 < r.limit ? p.table[(int64_t)r.b * p.max_pages + (k0 >> p.page_shift)] : -1;
+                };
+                Ref r0 = next_ref();
+                int pid0 = page_id(r0);
+                Ref r1 = next_ref();
+                while (ok && r0.live) {
+                    const bool good = pid0 >= 0 && pid0 < p.num_pages;
+                    const int64_t cell = (int64_t)(good ? pid0 : 0) * p.Hkv + r0.h;
+                    const float a = p.ks[cell], v = p.vs[cell];
+                    const int pid1 = page_id(r1);
+                    const Ref r2 = next_ref();
+                    claim();
+                    if (!ok) break;
+                    const int sk = 2 * tc, ms = tc % kAMeta, s0 = sk % SLOTS, s1 = (sk + 1) % SLOTS;
+                    const bool lead = good && ((4 * lane) & page_mask) == 0;
+                    const uint32_t bytes = (128u << p.page_shift) * __popc(__ballot_sync(0xffffffffu, lead));
                     if (lane == 0) {
-                        mbar_arrive_expect_tx(fullb[0], bytes);
-                        mbar_arrive_expect_tx(fullb[1], bytes);
-                    }
-                    __syncwarp();
-                    if (any) {
-                        tma_gather4(dst[0] + lane * 512, &tmk, fullb[0], 0, row[0], row[1], row[2], row[3]);
-                        tma_gather4(dst[1] + lane * 512, &tmv, fullb[1], 0, row[0], row[1], row[2], row[3]);
-                    }
-                } else {
-                    // the lane with a page's first key loads the page
-                    const bool lead = good[0] && (4 * lane) % p.page == 0;
-                    const uint32_t bytes = (uint32_t)p.page * 128u * __popc(__ballot_sync(0xffffffffu, lead));
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(fullb[0], bytes);
-                        mbar_arrive_expect_tx(fullb[1], bytes);
+                        mbar_arrive_expect_tx(kv_full + s0, bytes);
+                        mbar_arrive_expect_tx(kv_full + s1, bytes);
                     }
                     __syncwarp();
                     if (lead) {
-                        const int row = (int)(((int64_t)pid0[0] * p.Hkv + r0.h) * p.page);
-                        tma_load_2d(dst[0] + lane * 512, &tmk, fullb[0], 0, row);
-                        tma_load_2d(dst[1] + lane * 512, &tmv, fullb[1], 0, row);
+                        const int row = (int)(cell << p.page_shift);
+                        tma_load_2d(smem + s0 * kASlotBytes + lane * 512, &tmk, kv_full + s0, 0, row);
+                        tma_load_2d(smem + s1 * kASlotBytes + lane * 512, &tmv, kv_full + s1, 0, row);
                     }
+                    const int left = good ? r0.limit - (r0.tile * kATile + 4 * lane) : 0;  // keys of the lane that count
+                    const float x = a * p.scale_log2, y = __log2f(fmaxf(v, 0x1p-60f));
+                    float4* m4 = reinterpret_cast<float4*>(sMeta + ms * kATile + 4 * lane);
+                    m4[0] = make_float4(x, left > 0 ? y : -INFINITY, x, left > 1 ? y : -INFINITY);
+                    m4[1] = make_float4(x, left > 2 ? y : -INFINITY, x, left > 3 ? y : -INFINITY);
+                    const bool all = __all_sync(0xffffffffu, left > 3);
+                    if (lane == 0) {
+                        sFlag[ms] = all ? 0 : 1;
+                        mbar_arrive(meta_full + ms);
+                    }
+                    r0 = r1;
+                    r1 = r2;
+                    pid0 = pid1;
+                    ++tc;
                 }
-                bool all = true;
-                float2 mv[4];
+                if (!ok && !p.debug_stall)  // loads in flight end before the memory is given up
+                    for (int seq = max(0, 2 * tc - SLOTS); seq < 2 * tc; ++seq)
+                        mbar_wait(kv_full + seq % SLOTS, (seq / SLOTS) & 1, p.wait_ns);
+            } else {
+                // Selected keys: 16-byte asynchronous copies, eight lanes a row of 128 bytes, written in the
+                // 128-byte swizzle TMA would use; unseen keys and dims past D become zeros.  (A TMA gather takes
+                // 64 instructions a tile that the lanes issue one after the other: 11.9k cycles a tile.)
+                auto keys = [&](const Ref& r, int (&t)[4]) {
+                    const int k0 = r.tile * kATile + 4 * lane;
+                    const int32_t* src = p.idx + r.row * p.topk + k0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    mv[i].x = good[i] ? a[i] * p.scale_log2 : 0.f;
-                    mv[i].y = good[i] ? log2f(fmaxf(v[i], 0x1p-60f)) : -INFINITY;
-                    all = all && good[i];
-                }
-                float4* m4 = reinterpret_cast<float4*>(sMeta + ms * kATile + 4 * lane);
-                m4[0] = make_float4(mv[0].x, mv[0].y, mv[1].x, mv[1].y);
-                m4[1] = make_float4(mv[2].x, mv[2].y, mv[3].x, mv[3].y);
-                all = __all_sync(0xffffffffu, all);
-                if (lane == 0) {
-                    sFlag[ms] = all ? 0 : 1;
-                    mbar_arrive(meta_full + ms);
-                }
-                r0 = r1;
-                r1 = r2;
+                    for (int i = 0; i < 4; ++i) {
+                        t[i] = r.live && k0 + i < p.topk ? src[i] : -1;
+                        t[i] = t[i] < r.limit ? t[i] : -1;
+                    }
+                };
+                auto pages = [&](const Ref& r, const int (&t)[4], int (&pid)[4]) {
+                    const int32_t* tab = p.table + (int64_t)r.b * p.max_pages;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    t0[i] = t1[i];
-                    t1[i] = t2[i];
-                    pid0[i] = pid1[i];
+                    for (int i = 0; i < 4; ++i) pid[i] = t[i] >= 0 ? tab[t[i] >> p.page_shift] : -1;
+                };
+                int* const sRows = (int*)(smem + C::OFF_GATHER);
+                const int sub = lane & 7, part = lane >> 3;
+                const uint32_t in_row = sub * 16 < p.D ? 16 : 0;
+                const uint32_t off_even = part * 128 + ((sub ^ part) << 4);              // rows 8j .. 8j + 3
+                const uint32_t off_odd = (part + 4) * 128 + ((sub ^ (part + 4)) << 4);  // rows 8j + 4 .. 8j + 7
+                // the tile that was issued `behind` tiles ago has landed: hand it on
+                auto landed = [&](int t) {
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(kv_full + (2 * t) % SLOTS);
+                        mbar_arrive(kv_full + (2 * t + 1) % SLOTS);
+                    }
+                };
+                Ref r0 = next_ref();
+                int t0[4], t1[4], t2[4], pid0[4], pid1[4];
+                keys(r0, t0);
+                Ref r1 = next_ref();
+                keys(r1, t1);
+                pages(r0, t0, pid0);
+                while (ok && r0.live) {
+                    float a[4], v[4];
+                    bool good[4];
+                    int row[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        good[i] = pid0[i] >= 0 && pid0[i] < p.num_pages;
+                        const int cell = (good[i] ? pid0[i] : 0) * p.Hkv + r0.h;  // num_pages * Hkv * page < 2^31
+                        a[i] = p.ks[cell];
+                        v[i] = p.vs[cell];
+                        row[i] = good[i] ? (cell << p.page_shift) + (t0[i] & page_mask) : -1;
+                    }
+                    pages(r1, t1, pid1);
+                    const Ref r2 = next_ref();
+                    keys(r2, t2);
+                    *reinterpret_cast<int4*>(sRows + 4 * lane) = make_int4(row[0], row[1], row[2], row[3]);
+                    claim();
+                    if (!ok) break;
+                    __syncwarp();
+                    const int sk = 2 * tc, ms = tc % kAMeta;
+                    const uint32_t dk = smem_u32(smem) + (sk % SLOTS) * kASlotBytes;
+                    const uint32_t dv = smem_u32(smem) + ((sk + 1) % SLOTS) * kASlotBytes;
+#pragma unroll 4
+                    for (int i = 0; i < 32; ++i) {
+                        const int r = sRows[4 * i + part];
+                        const uint32_t at = (i >> 1) * 1024 + ((i & 1) ? off_odd : off_even);
+                        const int64_t from = r >= 0 ? (int64_t)r * p.D + sub * 16 : 0;
+                        const uint32_t n = r >= 0 ? in_row : 0;
+                        cp_async16(dk + at, p.kc + (n ? from : 0), n);
+                        cp_async16(dv + at, p.vc + (n ? from : 0), n);
+                    }
+                    cp_async_commit();
+                    bool all = true;
+                    float2 mv[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        mv[i].x = good[i] ? a[i] * p.scale_log2 : 0.f;
+                        mv[i].y = good[i] ? __log2f(fmaxf(v[i], 0x1p-60f)) : -INFINITY;
+                        all = all && good[i];
+                    }
+                    float4* m4 = reinterpret_cast<float4*>(sMeta + ms * kATile + 4 * lane);
+                    m4[0] = make_float4(mv[0].x, mv[0].y, mv[1].x, mv[1].y);
+                    m4[1] = make_float4(mv[2].x, mv[2].y, mv[3].x, mv[3].y);
+                    all = __all_sync(0xffffffffu, all);
+                    if (lane == 0) {
+                        sFlag[ms] = all ? 0 : 1;
+                        mbar_arrive(meta_full + ms);
+                    }
+                    if (tc > 0) {  // two tiles in flight
+                        cp_async_wait<1>();
+                        landed(tc - 1);
+                    }
+                    r0 = r1;
+                    r1 = r2;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        t0[i] = t1[i];
+                        t1[i] = t2[i];
+                        pid0[i] = pid1[i];
+                    }
+                    ++tc;
                 }
-                ++tc;
+                cp_async_wait<0>();  // also where a wait ran out: no copy outlives the block
+                if (ok && tc > 0) landed(tc - 1);
             }
-            if (!ok && !p.debug_stall)  // loads in flight end before the memory is given up
-                for (int seq = max(0, 2 * tc - SLOTS); seq < 2 * tc; ++seq)
-                    mbar_wait(kv_full + seq % SLOTS, (seq / SLOTS) & 1, p.wait_ns);
         } else {
             // ------------------------------------- queries: bf16 rows -> e4m3 hi and lo
             // Eight lanes a row, 16 dims each; the two warps take rows 8i .. 8i+3 and 8i+4 .. 8i+7.
@@ -588,20 +642,26 @@ __global__ void __launch_bounds__(kAThreads, 1)
                 const int qb = sc % QB;
                 ok = ok && mbar_wait(q_empty + qb, ((sc / QB) & 1) ^ 1, p.wait_ns);
                 uint8_t* dst = sQ + qb * C::Q_BYTES;
-#pragma unroll 2
-                for (int n = (warp - 2) * 4 + (lane >> 3); n < N; n += 8) {
-                    const int st = n / p.G, s = wk.gr.st * p.TS + st;
-                    const bool in = st < p.TS && s < p.S && sub * 16 < p.D;
-                    uint32_t w[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) w[i] = 0;
-                    if (in) {
+                // the next row's loads are in flight while a row is converted
+                auto load = [&](int n, uint4& u0, uint4& u1) {
+                    const int st = attn_token(p, n), s = wk.gr.st * p.TS + st;
+                    u0 = u1 = make_uint4(0, 0, 0, 0);
+                    if (n < N && st < p.TS && s < p.S && sub * 16 < p.D) {
                         const uint4* src = reinterpret_cast<const uint4*>(
                             p.q + wk.gr.b * p.qs[0] + s * p.qs[1] + (wk.h * p.G + n - st * p.G) * p.qs[2] + sub * 16);
-                        const uint4 u0 = src[0], u1 = src[1];
-                        w[0] = u0.x, w[1] = u0.y, w[2] = u0.z, w[3] = u0.w;
-                        w[4] = u1.x, w[5] = u1.y, w[6] = u1.z, w[7] = u1.w;
+                        u0 = src[0];
+                        u1 = src[1];
                     }
+                };
+                uint4 n0, n1, f0, f1;
+                const int first = (warp - 2) * 4 + (lane >> 3);
+                load(first, n0, n1);
+                load(first + 8, f0, f1);
+#pragma unroll 1
+                for (int n = first; n < N; n += 8) {
+                    const uint32_t w[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
+                    n0 = f0, n1 = f1;
+                    load(n + 16, f0, f1);
                     uint32_t top = 0;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
@@ -644,7 +704,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
         const int c0 = C::SPLIT ? grp * NC : 0;
         const uint32_t bar_id = 1 + grp;
         float* const sW = (float*)(smem + C::OFF_W) + grp * 4 * NC;
-        float2* const sMB = (float2*)(smem + C::OFF_MB) + grp * NC;
+        float* const sSh = (float*)(smem + C::OFF_MB) + grp * 2 * NC;  // 8 - M
+        float* const sBe = sSh + NC;                                    // fade of the tile
         float* const sAl = (float*)(smem + C::OFF_AL) + grp * NC;
         int* const sEnd = (int*)(smem + C::OFF_END) + grp * NC;
         const uint32_t lane_addr = tmem + ((uint32_t)(wg_warp * 32) << 16) + c0;
@@ -657,7 +718,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
             const int st0 = wk.gr.st * p.TS;
             named_bar_sync(bar_id, 128);  // the last segment's are read
             if (wtid < NC) {
-                const int st = (c0 + wtid) / p.G;
+                const int st = attn_token(p, c0 + wtid);
                 sEnd[wtid] = p.idx ? INT_MAX : (st < p.TS && st0 + st < p.S ? attn_end(p, wk.gr.b, st0 + st) : 0);
             }
             const int least = p.idx ? INT_MAX : attn_end(p, wk.gr.b, st0);
@@ -691,13 +752,15 @@ __global__ void __launch_bounds__(kAThreads, 1)
 #pragma unroll
                     for (int cc = 0; cc < NC; cc += CH) {
                         attn_scores<MASK, CH>(s_addr + cc, qs + cc, sEnd + cc, a2, lv2, key, seen, x);
-                        float mine = 0.f;
+                        float top[CH];
 #pragma unroll
-                        for (int i = 0; i < CH; ++i) {
-                            const float r = warp_max(x[i]);
-                            mine = lane == i ? r : mine;
+                        for (int i = 0; i < CH; ++i) top[i] = warp_max(x[i]);
+                        if (lane == 0) {
+#pragma unroll
+                            for (int i = 0; i < CH; i += 4)
+                                *reinterpret_cast<float4*>(sW + wg_warp * NC + cc + i) =
+                                    make_float4(top[i], top[i + 1], top[i + 2], top[i + 3]);
                         }
-                        if (lane < CH) sW[wg_warp * NC + cc + lane] = mine;
                     }
                     named_bar_sync(bar_id, 128);
                     bool fade = false;
@@ -707,7 +770,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
                         const float mn = fmaxf(mw, M);
                         fade = mn > mw && mw != -INFINITY;
                         sAl[wtid] = fade ? exp2_approx(mw - mn) : 1.f;
-                        sMB[wtid] = M == -INFINITY ? make_float2(kATop, 0.f) : make_float2(kATop - M, exp2_approx(M - mn));
+                        sSh[wtid] = M == -INFINITY ? kATop : kATop - M;
+                        sBe[wtid] = M == -INFINITY ? 0.f : exp2_approx(M - mn);
                         sMt[bf * N + c0 + wtid] = M;
                         mw = mn;
                     }
@@ -727,22 +791,24 @@ __global__ void __launch_bounds__(kAThreads, 1)
                             attn_scores<MASK, CH>(s_addr + cc, qs + cc, sEnd + cc, a2, lv2, key, seen, x);
                         uint32_t hi[CH / 4], lo[CH / 4];
 #pragma unroll
-                        for (int i = 0; i < CH; i += 2) {
-                            const float4 mb = *reinterpret_cast<const float4*>(sMB + cc + i);
-                            float e0, e1;
-                            unpack2(add2(pack2(x[i], x[i + 1]), pack2(mb.x, mb.z)), e0, e1);
+                        for (int i = 0; i < CH; i += 4) {
+                            const float4 sh = *reinterpret_cast<const float4*>(sSh + cc + i);
+                            const float4 be = *reinterpret_cast<const float4*>(sBe + cc + i);
+                            float e0, e1, e2, e3;
+                            unpack2(add2(pack2(x[i], x[i + 1]), pack2(sh.x, sh.y)), e0, e1);
+                            unpack2(add2(pack2(x[i + 2], x[i + 3]), pack2(sh.z, sh.w)), e2, e3);
                             const float w0 = exp2_approx(e0), w1 = exp2_approx(e1);
-                            unpack2(fma2(mul2(pack2(w0, w1), iv2), pack2(mb.y, mb.w), pack2(l[cc + i], l[cc + i + 1])),
+                            const float w2 = exp2_approx(e2), w3 = exp2_approx(e3);
+                            unpack2(fma2(mul2(pack2(w0, w1), iv2), pack2(be.x, be.y), pack2(l[cc + i], l[cc + i + 1])),
                                     l[cc + i], l[cc + i + 1]);
-                            uint32_t h2, l2;
-                            split_e4m3(w0, w1, h2, l2);
-                            if (i & 2) {
-                                hi[i / 4] |= h2 << 16;
-                                lo[i / 4] |= l2 << 16;
-                            } else {
-                                hi[i / 4] = h2;
-                                lo[i / 4] = l2;
-                            }
+                            unpack2(fma2(mul2(pack2(w2, w3), iv2), pack2(be.z, be.w),
+                                         pack2(l[cc + i + 2], l[cc + i + 3])),
+                                    l[cc + i + 2], l[cc + i + 3]);
+                            uint32_t h0, l0, h1, l1;
+                            split_e4m3(w0, w1, h0, l0);
+                            split_e4m3(w2, w3, h1, l1);
+                            hi[i / 4] = h0 | (h1 << 16);
+                            lo[i / 4] = l0 | (l1 << 16);
                         }
 #pragma unroll
                         for (int k = 0; k < CH / 16; ++k) {
@@ -797,13 +863,14 @@ __global__ void __launch_bounds__(kAThreads, 1)
         regs_inc<160>();
         const int d = tid - 384, wg_warp = warp & 3;
         const uint32_t lane_addr = tmem + ((uint32_t)(wg_warp * 32) << 16) + 2 * N;
-        float2* const sAB = (float2*)(smem + C::OFF_AB);
+        float* const sA = (float*)(smem + C::OFF_AB);  // [2][N] fade of acc
+        float* const sB = sA + 2 * N;                  // [2][N] of the tile
         float* const sInv = (float*)(smem + C::OFF_INV);
         int* const sRow = (int*)(smem + C::OFF_ROW);
         bool ok = true;
         int tc = 0, sc = 0;
-        AttnHeader hd{0, 0, 0, 0, 0, W};
-        float* const parts = (float*)(p.ws + (size_t)nc * sizeof(AttnHeader));
+        AttnHeader hd{0, 0, 0, 0};
+        float* const parts = (float*)(p.ws + (size_t)gridDim.x * sizeof(AttnHeader));
         while (wk.next(p)) {
             float acc[N];
 #pragma unroll
@@ -815,8 +882,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
                     ok = ok && mbar_wait(p_full + bf, ph, p.wait_ns);
                     if (d < N) {
                         const float M = sMt[bf * N + d], mn = fmaxf(m, M);
-                        sAB[bf * N + d] = make_float2(m == -INFINITY ? 0.f : exp2_approx(m - mn),
-                                                      M == -INFINITY ? 0.f : exp2_approx(M - mn));
+                        sA[bf * N + d] = m == -INFINITY ? 0.f : exp2_approx(m - mn);
+                        sB[bf * N + d] = M == -INFINITY ? 0.f : exp2_approx(M - mn);
                         m = mn;
                     }
                     __syncwarp();
@@ -830,12 +897,17 @@ __global__ void __launch_bounds__(kAThreads, 1)
                         tmem_ld16(lane_addr + bf * N + cc, r);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            const float4 ab = *reinterpret_cast<const float4*>(sAB + bf * N + cc + i);
-                            const uint64_t o = mul2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])),
-                                                    pack2(ab.y, ab.w));
-                            unpack2(fma2(pack2(acc[cc + i], acc[cc + i + 1]), pack2(ab.x, ab.z), o), acc[cc + i],
+                        for (int i = 0; i < 16; i += 4) {
+                            const float4 fa = *reinterpret_cast<const float4*>(sA + bf * N + cc + i);
+                            const float4 fb = *reinterpret_cast<const float4*>(sB + bf * N + cc + i);
+                            const uint64_t o0 = mul2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])),
+                                                     pack2(fb.x, fb.y));
+                            const uint64_t o1 = mul2(pack2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])),
+                                                     pack2(fb.z, fb.w));
+                            unpack2(fma2(pack2(acc[cc + i], acc[cc + i + 1]), pack2(fa.x, fa.y), o0), acc[cc + i],
                                     acc[cc + i + 1]);
+                            unpack2(fma2(pack2(acc[cc + i + 2], acc[cc + i + 3]), pack2(fa.z, fa.w), o1),
+                                    acc[cc + i + 2], acc[cc + i + 3]);
                         }
                     }
                     tc_fence_before();
@@ -860,7 +932,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
             const bool whole = wk.t0 == 0 && wk.t1 == wk.gr.w;
             if (whole) {
                 if (d < N) {
-                    const int st = d / p.G, s = wk.gr.st * p.TS + st;
+                    const int st = attn_token(p, d), s = wk.gr.st * p.TS + st;
                     const int row = st < p.TS && s < p.S
                                         ? (wk.gr.b * p.S + s) * p.Hq + wk.h * p.G + d - st * p.G
                                         : -1;
@@ -887,7 +959,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
                     part[N * 128 + d] = m;
                     part[N * 128 + N + d] = l;
                 }
-                if (wk.t0 == 0) hd = AttnHeader{1, wk.g, wk.h, slot, wk.unit_end, W};
+                if (wk.t0 == 0)  // place unit_end - 1 is in the share of the last CTA that begins at or before it
+                    hd = AttnHeader{(int32_t)((wk.unit_end * nc - 1) / W), wk.g, wk.h, slot};
             }
         }
         if (d == 0) reinterpret_cast<AttnHeader*>(p.ws)[c] = hd;
@@ -902,38 +975,59 @@ __global__ void __launch_bounds__(kAThreads, 1)
     }
 }
 
-// Joins the parts of the units that were cut: block (c, y) takes kJoinRows rows of the unit whose first tiles CTA c had.
-// Parts are added in the line's order.
-constexpr int kJoinRows = 4;
+// Joins the parts of the units that were cut: block (c, y) takes rows y, y + gridDim.y, ... of the unit whose first
+// tiles CTA c had.  The parts follow each other in the workspace (two slots a CTA).  Four groups of 128 threads take
+// every fourth part and are added in order.
+constexpr int kJoinThreads = 512;
+constexpr int kJoinMaxParts = 1024;  // more than SMs of a device
 template <int N>
-__global__ void __launch_bounds__(128) cache_attn_join_kernel(const AttnParams p, int nc) {
+__global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __grid_constant__ AttnParams p, int nc) {
+    __shared__ float s_f[kJoinMaxParts], s_o[3][128], s_red[2][kJoinThreads / 32];
     grid_dependency_wait();
     const AttnHeader hd = reinterpret_cast<const AttnHeader*>(p.ws)[blockIdx.x];
-    if (!hd.owner) return;
+    if (hd.last == 0) return;
     const float* parts = (const float*)(p.ws + (size_t)nc * sizeof(AttnHeader));
-    const int d = threadIdx.x, b = hd.g / p.ST, st0 = hd.g % p.ST * p.TS;
-#pragma unroll 1
-    for (int r = 0; r < kJoinRows; ++r) {
-        const int n = blockIdx.y * kJoinRows + r, st = n / p.G, s = st0 + st;
-        if (st >= p.TS || s >= p.S) break;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, d = tid & 127, quarter = tid >> 7;
+    const int P = hd.last - blockIdx.x + 1, b = hd.g / p.ST, st0 = (hd.g - b * p.ST) * p.TS;
+    auto part_of = [&](int i) {
+        return parts + (size_t)(i == 0 ? hd.slot : 2 * (blockIdx.x + i)) * attn_part_floats(N);
+    };
+    for (int n = blockIdx.y; n < p.TS * p.G; n += gridDim.y) {
+        const int st = attn_token(p, n), s = st0 + st;
+        if (s >= p.S) break;  // uniform
         float m = -INFINITY;
-        for (int c = blockIdx.x; c < nc && attn_share(hd.W, c, nc) < hd.unit_end; ++c) {
-            if (attn_share(hd.W, c, nc) == attn_share(hd.W, c + 1, nc)) continue;
-            const int slot = c == blockIdx.x ? hd.slot : 2 * c;
-            m = fmaxf(m, parts[slot * attn_part_floats(N) + N * 128 + n]);
+        for (int i = tid; i < P; i += kJoinThreads) m = fmaxf(m, part_of(i)[N * 128 + n]);
+        m = warp_max(m);
+        if (lane == 0) s_red[0][warp] = m;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kJoinThreads / 32; ++i) m = fmaxf(m, s_red[0][i]);
+        float l = 0.f;
+        for (int i = tid; i < P; i += kJoinThreads) {
+            const float* part = part_of(i) + N * 128 + n;
+            const float f = m == -INFINITY ? 0.f : exp2_approx(part[0] - m);
+            s_f[i] = f;
+            l += part[N] * f;
         }
-        float l = 0.f, o = 0.f;
-        for (int c = blockIdx.x; m != -INFINITY && c < nc && attn_share(hd.W, c, nc) < hd.unit_end; ++c) {
-            if (attn_share(hd.W, c, nc) == attn_share(hd.W, c + 1, nc)) continue;
-            const float* part = parts + (c == blockIdx.x ? hd.slot : 2 * c) * attn_part_floats(N);
-            const float f = exp2_approx(part[N * 128 + n] - m);
-            l += part[N * 128 + N + n] * f;
-            o += part[n * 128 + d] * f;
-        }
+#pragma unroll
+        for (int i = 16; i; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
+        if (lane == 0) s_red[1][warp] = l;
+        __syncthreads();
+        l = 0.f;
+#pragma unroll
+        for (int i = 0; i < kJoinThreads / 32; ++i) l += s_red[1][i];
+        float o = 0.f;
+#pragma unroll 4
+        for (int i = quarter; i < P; i += 4) o += part_of(i)[n * 128 + d] * s_f[i];
+        if (quarter > 0) s_o[quarter - 1][d] = o;
+        __syncthreads();
         const int64_t row = ((int64_t)b * p.S + s) * p.Hq + hd.h * p.G + n - st * p.G;
-        if (d < p.D)
+        if (tid < p.D) {
+            o = ((o + s_o[0][d]) + s_o[1][d]) + s_o[2][d];
             reinterpret_cast<__nv_bfloat16*>(p.out)[row * p.D + d] = __float2bfloat16_rn(l > 0.f ? o / l : 0.f);
-        if (p.lse && d == 0) p.lse[row] = l > 0.f ? (m + log2f(l) - kATop) * kALn2 : -INFINITY;
+        }
+        if (p.lse && tid == 0) p.lse[row] = l > 0.f ? (m + log2f(l) - kATop) * kALn2 : -INFINITY;
+        __syncthreads();
     }
 }
 
@@ -966,8 +1060,8 @@ static cudaError_t attn_launch(const CUtensorMap& mk, const CUtensorMap& mv, con
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
     const int rows = p.TS * p.G;
-    cfg.gridDim = dim3(grid, (rows + kJoinRows - 1) / kJoinRows);
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(grid, rows < 16 ? rows : 16);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     // the join is set up while the main kernel runs; it waits for its end itself
     cudaLaunchAttribute at;
@@ -1014,7 +1108,7 @@ int lidx_cache_attn(const void* q, const int64_t* qs, const void* k_cache, const
         return LIDX_ERR_ALIGN;
     if ((qs[0] | qs[1] | qs[2]) & 7) return LIDX_ERR_ALIGN;
     const int sms = sm103_sms();
-    if (sms <= 0) return LIDX_ERR_NO_DEVICE;
+    if (sms <= 0 || sms > kJoinMaxParts) return LIDX_ERR_NO_DEVICE;
     AttnParams p;
     memset(&p, 0, sizeof p);
     p.q = (const uint16_t*)q;
@@ -1039,6 +1133,10 @@ int lidx_cache_attn(const void* q, const int64_t* qs, const void* k_cache, const
     const int N = attn_columns(S, p.G, topk_indices != nullptr);
     p.TS = topk_indices ? 1 : (int)(N / p.G < S ? N / p.G : S);
     p.ST = (int)((S + p.TS - 1) / p.TS);
+    p.page_shift = page == 16 ? 4 : (page == 32 ? 5 : (page == 64 ? 6 : 7));
+    p.inv_g = (65536 + p.G - 1) / p.G;
+    p.kc = (const uint8_t*)k_cache;
+    p.vc = (const uint8_t*)v_cache;
     p.scale_log2 = softmax_scale * 1.44269504088896341f;
     p.out = (uint16_t*)out;
     p.lse = lse;
@@ -1052,9 +1150,8 @@ int lidx_cache_attn(const void* q, const int64_t* qs, const void* k_cache, const
     if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u)) return LIDX_ERR_WORKSPACE;
     p.ws = (uint8_t*)workspace;
     CUtensorMap mk, mv;
-    const int box = topk_indices ? 1 : page;
-    if (attn_cache_map(&mk, k_cache, num_pages * Hkv * page, D, box) ||
-        attn_cache_map(&mv, v_cache, num_pages * Hkv * page, D, box))
+    if (attn_cache_map(&mk, k_cache, num_pages * Hkv * page, D, page) ||
+        attn_cache_map(&mv, v_cache, num_pages * Hkv * page, D, page))
         return LIDX_ERR_CUDA;
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
