@@ -299,7 +299,7 @@ typedef enum { LIDX_ROPE_INTERLEAVED = 0, LIDX_ROPE_HALF = 1 } lidx_rope_layout;
  *   pos     int32 [T0,T1], strides ps (host int64[2]; 0 repeats a position)
  *   freqs   device copy of lidx_rope_freqs's array
  *   dtype   of every x and y: 0 fp32, 1 bf16 (computed in fp32, rounded once)
- * Rules: T0, T1, H >= 1; D even, 2 .. 1024; rot_dim even >= 2, 0 <= rot_off,
+ * Rules: T0, T1, H >= 1; T0 * T1 < 2^31; H <= 2^15; D even, 2 .. 1024; rot_dim even >= 2, 0 <= rot_off,
  * rot_off + rot_dim <= D.  Pointers need only be aligned to their element; 16-byte aligned
  * tensors, strides and rotated parts take the faster path.
  */

@@ -29,6 +29,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 import threading
 
 import torch
@@ -420,29 +421,57 @@ def lidx_indexer_bwd(q, k, w, idx, grad, compress_ratio, act="relu", grad_dtype=
     return dq, dk, dw
 
 
-def _need_strided(t, name, dtype, dim):
-    """As _need, with any strides as long as the last dimension is contiguous."""
-    if not isinstance(t, torch.Tensor):
+# The calls below are made once for each layer of each token: their checks read each attribute once, arrays
+# of sizes go to C as packed bytes, and the stream is the raw handle.
+_Tensor, _bf16, _f32, _i32, _i64, _f8 = (torch.Tensor, torch.bfloat16, torch.float32, torch.int32, torch.int64,
+                                          torch.float8_e4m3fn)
+_I2, _I3, _ROPE_TENSOR = struct.Struct("2q").pack, struct.Struct("3q").pack, struct.Struct("PP6qi4x").pack
+
+
+def _strided(t, name, dtype, dev=None):
+    """Checks a 4-dimensional CUDA tensor of any strides that is contiguous in its last dimension; returns its
+    shape, the strides of the leading dimensions (0 where the size is 1: never stepped over) and its device."""
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != dim:
-        raise ValueError(f"{name} must have {dim} dims, got {tuple(t.shape)}")
-    if t.shape[-1] != 1 and t.stride(-1) != 1:
+    shape = t.shape
+    if len(shape) != 4:
+        raise ValueError(f"{name} must have 4 dims, got {tuple(shape)}")
+    a, b, c, d = t.stride()
+    if d != 1 and shape[3] != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
+    at = t.get_device()
+    if dev is not None and at != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+    return shape, (a if shape[0] > 1 else 0, b if shape[1] > 1 else 0, c if shape[2] > 1 else 0), at
 
 
-def _same_device(first, **others):
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, not on {first.device}")
+def _dense(t, name, dtype, shape, dev):
+    """Checks a contiguous CUDA tensor; None in `shape` is any size.  Returns its shape."""
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    s = t.shape
+    if len(s) != len(shape):
+        raise ValueError(f"{name} must have {len(shape)} dims, got {tuple(s)}")
+    for n, m in zip(s, shape):
+        if m is not None and n != m:
+            raise ValueError(f"{name} has shape {tuple(s)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+    return s
 
 
-def _strides(t):
-    """Element strides of the leading dimensions (0 where the size is 1: never stepped over)."""
-    return [st if n > 1 else 0 for st, n in zip(t.stride()[:-1], t.shape[:-1])]
+def _raw_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def lidx_rope_freqs(rot_dim, theta=10000.0, scaling=None, factor=1.0, original_len=4096, beta_fast=32.0,
@@ -459,42 +488,50 @@ def lidx_rope_freqs(rot_dim, theta=10000.0, scaling=None, factor=1.0, original_l
 
 
 def _rope(x, pos, freqs, x2, layout, rot_off, mscale, inverse, stream, out, call):
-    if x.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"x must be float32 or bfloat16, got {x.dtype}")
-    _need_strided(x, "x", x.dtype, 4)
+    dtype = x.dtype if isinstance(x, _Tensor) else _bf16
+    if dtype is not _bf16 and dtype is not _f32:
+        raise TypeError(f"x must be float32 or bfloat16, got {dtype}")
+    shape, xs, dev = _strided(x, "x", dtype)
+    T0, T1, H, D = shape
     if x2 is not None:
-        _need_strided(x2, "x2", x.dtype, 4)
-        if x2.shape[:2] != x.shape[:2] or x2.shape[3] != x.shape[3]:
+        shape2, xs2, _ = _strided(x2, "x2", dtype, dev)
+        if shape2[0] != T0 or shape2[1] != T1 or shape2[3] != D:
             raise ValueError("x and x2 shapes disagree")
-    if not isinstance(pos, torch.Tensor) or pos.dtype != torch.int32 or not pos.is_cuda:
+    if not isinstance(pos, _Tensor) or pos.dtype is not _i32 or not pos.is_cuda:
         raise TypeError("pos must be an int32 CUDA tensor")
-    pos = pos.expand(x.shape[:2])  # repeated positions have stride 0
-    _need(freqs, "freqs", torch.int64, 1)
-    _same_device(x, x2=x2, pos=pos, freqs=freqs)
+    if pos.shape != (T0, T1):
+        pos = pos.expand(T0, T1)  # repeated positions have stride 0
+    if pos.get_device() != dev:
+        raise ValueError(f"pos is on {pos.device}, not on cuda:{dev}")
+    p0, p1 = pos.stride()
+    pairs = _dense(freqs, "freqs", _i64, (None,), dev)[0]
     if layout not in ROPE_LAYOUT:
         raise ValueError(f"layout must be one of {list(ROPE_LAYOUT)}")
-    xs = [x] if x2 is None else [x, x2]
     if out is None:
-        ys = [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in xs]
+        at = x.device
+        y = torch.empty(shape, dtype=dtype, device=at)
+        arr = _ROPE_TENSOR(x.data_ptr(), y.data_ptr(), *xs, T1 * H * D, H * D, D, H)
+        if x2 is not None:
+            H2 = shape2[2]
+            y2 = torch.empty(shape2, dtype=dtype, device=at)
+            arr += _ROPE_TENSOR(x2.data_ptr(), y2.data_ptr(), *xs2, T1 * H2 * D, H2 * D, D, H2)
     else:
-        ys = [out] if x2 is None else list(out)
-        for t, y in zip(xs, ys):
-            _need_strided(y, "out", t.dtype, 4)
-            if y.shape != t.shape:
-                raise ValueError("out has another shape than x")
-            _same_device(x, out=y)
-    T0, T1, _, D = x.shape
-    arr = (_RopeTensor * len(xs))()
-    for a, t, y in zip(arr, xs, ys):
-        a.x, a.y, a.H = t.data_ptr(), y.data_ptr(), t.shape[2]
-        a.xs[:] = _strides(t)
-        a.ys[:] = _strides(y)
-    ps = (C.c_int64 * 2)(*[st if n > 1 else 0 for st, n in zip(pos.stride(), pos.shape)])
-    rc = lib().lidx_rope(arr, len(xs), _ptr(pos), ps, _ptr(freqs), T0, T1, D, 2 * freqs.shape[0], rot_off,
-                         ROPE_LAYOUT[layout], int(inverse), mscale, int(x.dtype == torch.bfloat16),
-                         _stream(stream))
-    _check(rc, call)
-    return ys[0] if x2 is None else tuple(ys)
+        y, y2 = (out, None) if x2 is None else out
+        sy, ys, _ = _strided(y, "out", dtype, dev)
+        if sy != shape:
+            raise ValueError("out has another shape than x")
+        arr = _ROPE_TENSOR(x.data_ptr(), y.data_ptr(), *xs, *ys, H)
+        if x2 is not None:
+            sy, ys, _ = _strided(y2, "out", dtype, dev)
+            if sy != shape2:
+                raise ValueError("out has another shape than x2")
+            arr += _ROPE_TENSOR(x2.data_ptr(), y2.data_ptr(), *xs2, *ys, shape2[2])
+    rc = (_lib or lib()).lidx_rope(arr, 1 if x2 is None else 2, pos.data_ptr(), _I2(p0 if T0 > 1 else 0, p1 if T1 > 1 else 0),
+                                   freqs.data_ptr(), T0, T1, D, 2 * pairs, rot_off, ROPE_LAYOUT[layout], inverse, mscale,
+                                   1 if dtype is _bf16 else 0, _raw_stream(stream, dev))
+    if rc:
+        raise LidxError(rc, call)
+    return y if x2 is None else (y, y2)
 
 
 def lidx_rope(x, pos, freqs, x2=None, layout="interleaved", rot_off=0, mscale=1.0, stream=None, out=None):
@@ -502,33 +539,20 @@ def lidx_rope(x, pos, freqs, x2=None, layout="interleaved", rot_off=0, mscale=1.
     the same launch, of x2 [T0,T1,H2,D].  pos: int32, broadcast to [T0,T1]; freqs: lidx_rope_freqs's,
     the rotated dims are [rot_off, rot_off + 2*len(freqs)).  Returns y, or (y, y2).  ``out`` may be the
     inputs themselves (in place)."""
-    return _rope(x, pos, freqs, x2, layout, rot_off, mscale, False, stream, out, "lidx_rope")
+    return _rope(x, pos, freqs, x2, layout, rot_off, mscale, 0, stream, out, "lidx_rope")
 
 
 def lidx_rope_bwd(g, pos, freqs, x2=None, layout="interleaved", rot_off=0, mscale=1.0, stream=None, out=None):
     """Gradient of lidx_rope's x (and x2) from the gradients g (and x2) of its outputs: the inverse turn."""
-    return _rope(g, pos, freqs, x2, layout, rot_off, mscale, True, stream, out, "lidx_rope_bwd")
+    return _rope(g, pos, freqs, x2, layout, rot_off, mscale, 1, stream, out, "lidx_rope_bwd")
 
 
-def _cache_dims(k_cache, v_cache, k_scale, v_scale, block_table, B):
-    _need(k_cache, "k_cache", torch.float8_e4m3fn, 4)
-    _need(v_cache, "v_cache", torch.float8_e4m3fn, 4)
-    _need(k_scale, "k_scale", torch.float32, 2)
-    _need(v_scale, "v_scale", torch.float32, 2)
-    _need(block_table, "block_table", torch.int32, 2)
-    pages, Hkv, page, D = k_cache.shape
-    if v_cache.shape != k_cache.shape or tuple(k_scale.shape) != (pages, Hkv) or k_scale.shape != v_scale.shape:
-        raise ValueError("cache and scale shapes disagree")
-    if block_table.shape[0] != B:
-        raise ValueError("block_table must have B rows")
-    _same_device(k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, block_table=block_table)
-    return pages, Hkv, page, D, block_table.shape[1]
-
-
-def _per_sequence(t, name, B):
-    _need(t, name, torch.int32, 1)
-    if t.shape[0] != B:
-        raise ValueError(f"{name} must have B entries")
+def _cache(k_cache, v_cache, k_scale, v_scale, block_table, B, Hkv, D, dev):
+    pages, Hkv, page, D = _dense(k_cache, "k_cache", _f8, (None, Hkv, None, D), dev)
+    _dense(v_cache, "v_cache", _f8, (pages, Hkv, page, D), dev)
+    _dense(k_scale, "k_scale", _f32, (pages, Hkv), dev)
+    _dense(v_scale, "v_scale", _f32, (pages, Hkv), dev)
+    return pages, Hkv, page, _dense(block_table, "block_table", _i32, (B, None), dev)[1]
 
 
 def lidx_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, start, count=None, stream=None):
@@ -536,21 +560,21 @@ def lidx_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, sta
     8 bits with a power-of-two scale for each page and head.  k_cache, v_cache [P,Hkv,page,D]
     float8_e4m3fn and k_scale, v_scale [P,Hkv] fp32 are updated in place; block_table int32
     [B,max_pages]; count int32 [B] or None: new tokens of each sequence."""
-    _need_strided(k, "k", torch.bfloat16, 4)
-    _need_strided(v, "v", torch.bfloat16, 4)
-    B, S, Hkv, D = k.shape
-    pages, Hc, page, Dc, MP = _cache_dims(k_cache, v_cache, k_scale, v_scale, block_table, B)
-    if v.shape != k.shape or (Hc, Dc) != (Hkv, D):
-        raise ValueError("k/v/cache shapes disagree")
-    _per_sequence(start, "start", B)
+    shape, ks, dev = _strided(k, "k", _bf16)
+    shape_v, vs, _ = _strided(v, "v", _bf16, dev)
+    if shape_v != shape:
+        raise ValueError("k and v shapes disagree")
+    B, S, Hkv, D = shape
+    pages, _, page, MP = _cache(k_cache, v_cache, k_scale, v_scale, block_table, B, Hkv, D, dev)
+    _dense(start, "start", _i32, (B,), dev)
     if count is not None:
-        _per_sequence(count, "count", B)
-    _same_device(k, v=v, k_cache=k_cache, start=start, count=count)
-    i3 = C.c_int64 * 3
-    rc = lib().lidx_cache_append(_ptr(k), _ptr(v), i3(*_strides(k)), i3(*_strides(v)), _ptr(block_table),
-                                 _ptr(start), _ptr(count), B, S, Hkv, D, page, MP, pages, _ptr(k_cache),
-                                 _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _stream(stream))
-    _check(rc, "lidx_cache_append")
+        _dense(count, "count", _i32, (B,), dev)
+    rc = (_lib or lib()).lidx_cache_append(
+        k.data_ptr(), v.data_ptr(), _I3(*ks), _I3(*vs), block_table.data_ptr(), start.data_ptr(),
+        None if count is None else count.data_ptr(), B, S, Hkv, D, page, MP, pages, k_cache.data_ptr(),
+        v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), _raw_stream(stream, dev))
+    if rc:
+        raise LidxError(rc, "lidx_cache_append")
 
 
 def lidx_cache_attn_workspace_bytes(B, S, Hq, Hkv, D, topk=0) -> int:
@@ -566,44 +590,33 @@ def lidx_cache_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, 
     below (q_pos[b]+s+1)//compress_ratio only.  topk_indices int32 [B,S,topk] or None: the row sees
     only the listed keys (lidx_indexer_fwd's indices).  softmax_scale defaults to D**-0.5.
     Returns (out [B,S,Hq,D] bf16, lse [B,S,Hq] fp32 or None); ``out`` may hold preallocated ones."""
-    _need_strided(q, "q", torch.bfloat16, 4)
-    B, S, Hq, D = q.shape
-    pages, Hkv, page, Dc, MP = _cache_dims(k_cache, v_cache, k_scale, v_scale, block_table, B)
-    if Dc != D:
-        raise ValueError("q/cache shapes disagree")
-    _per_sequence(kv_len, "kv_len", B)
+    shape, qs, dev = _strided(q, "q", _bf16)
+    B, S, Hq, D = shape
+    pages, Hkv, page, MP = _cache(k_cache, v_cache, k_scale, v_scale, block_table, B, None, D, dev)
+    _dense(kv_len, "kv_len", _i32, (B,), dev)
     if q_pos is not None:
-        _per_sequence(q_pos, "q_pos", B)
-    topk = 0
-    if topk_indices is not None:
-        _need(topk_indices, "topk_indices", torch.int32, 3)
-        if tuple(topk_indices.shape[:2]) != (B, S):
-            raise ValueError("topk_indices must be [B,S,topk]")
-        topk = topk_indices.shape[2]
+        _dense(q_pos, "q_pos", _i32, (B,), dev)
+    topk = 0 if topk_indices is None else _dense(topk_indices, "topk_indices", _i32, (B, S, None), dev)[2]
     if out is None:
-        o = torch.empty(B, S, Hq, D, dtype=torch.bfloat16, device=q.device)
-        lse = torch.empty(B, S, Hq, dtype=torch.float32, device=q.device) if want_lse else None
+        o = torch.empty(shape, dtype=_bf16, device=q.device)
+        lse = torch.empty(shape[:3], dtype=_f32, device=q.device) if want_lse else None
     else:
         o, lse = out
-        _need(o, "out", torch.bfloat16, 4)
-        if tuple(o.shape) != (B, S, Hq, D):
-            raise ValueError("out must be [B,S,Hq,D]")
+        _dense(o, "out", _bf16, shape, dev)
         if lse is not None:
-            _need(lse, "lse", torch.float32, 3)
-            if tuple(lse.shape) != (B, S, Hq):
-                raise ValueError("lse must be [B,S,Hq]")
-    _same_device(q, k_cache=k_cache, kv_len=kv_len, q_pos=q_pos, topk_indices=topk_indices, out=o, lse=lse,
-                 workspace=workspace)
-    ws_bytes = lidx_cache_attn_workspace_bytes(B, S, Hq, Hkv, D, topk)
-    if workspace is None and ws_bytes:
+            _dense(lse, "lse", _f32, shape[:3], dev)
+    L = _lib or lib()
+    if workspace is None:
+        ws_bytes = L.lidx_cache_attn_workspace_bytes(B, S, Hq, Hkv, D, topk)
         workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-    elif workspace is not None:
-        _need(workspace, "workspace", torch.uint8, 1)
-        ws_bytes = workspace.numel()
-    rc = lib().lidx_cache_attn(_ptr(q), (C.c_int64 * 3)(*_strides(q)), _ptr(k_cache), _ptr(v_cache),
-                               _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(kv_len), _ptr(q_pos),
-                               _ptr(topk_indices), B, S, Hq, Hkv, D, page, MP, pages, compress_ratio, topk,
-                               D ** -0.5 if softmax_scale is None else softmax_scale, _ptr(o), _ptr(lse),
-                               _ptr(workspace), ws_bytes, _stream(stream))
-    _check(rc, "lidx_cache_attn")
+    else:
+        ws_bytes = _dense(workspace, "workspace", torch.uint8, (None,), dev)[0]
+    rc = L.lidx_cache_attn(
+        q.data_ptr(), _I3(*qs), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        block_table.data_ptr(), kv_len.data_ptr(), None if q_pos is None else q_pos.data_ptr(),
+        None if topk_indices is None else topk_indices.data_ptr(), B, S, Hq, Hkv, D, page, MP, pages, compress_ratio,
+        topk, D ** -0.5 if softmax_scale is None else softmax_scale, o.data_ptr(), None if lse is None else lse.data_ptr(),
+        workspace.data_ptr(), ws_bytes, _raw_stream(stream, dev))
+    if rc:
+        raise LidxError(rc, "lidx_cache_attn")
     return o, lse

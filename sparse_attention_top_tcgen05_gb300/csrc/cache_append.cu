@@ -43,7 +43,7 @@ __device__ __forceinline__ float append_scale(uint32_t amax_bf16) {
     return ldexpf(1.f, e);
 }
 
-__global__ void __launch_bounds__(kAppThreads) cache_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppThreads, 5) cache_append_kernel(const __grid_constant__ AppendParams p) {
     const int b = blockIdx.x / p.J, j = blockIdx.x % p.J, h = blockIdx.y, which = blockIdx.z;
     const int64_t start = p.start[b];
     int64_t count = p.count ? p.count[b] : p.S;
@@ -57,8 +57,6 @@ __global__ void __launch_bounds__(kAppThreads) cache_append_kernel(const AppendP
     hi = hi < p0 + p.page ? hi : p0 + p.page;
     if (hi <= lo || slot >= p.max_pages) return;
     const int64_t pid = p.table[(int64_t)b * p.max_pages + slot];
-    if (pid < 0 || pid >= p.num_pages) return;
-
     const int C = p.D / 8, n = (int)(hi - lo) * C;
     const uint16_t* x = p.x[which] + b * p.xs[which][0] + (lo - start) * p.xs[which][1] + h * p.xs[which][2];
     uint4 v[kAppVecs];
@@ -72,6 +70,7 @@ __global__ void __launch_bounds__(kAppThreads) cache_append_kernel(const AppendP
             top = __vmaxu2(top, v[i].w & 0x7fff7fffu);
         }
     }
+    if (pid < 0 || pid >= p.num_pages) return;  // (the loads did not wait for it)
     __shared__ uint32_t s_top[kAppThreads / 32];
     uint32_t m = max(top & 0xffffu, top >> 16);
     m = __reduce_max_sync(0xffffffffu, m);

@@ -84,8 +84,150 @@ __global__ void rope_any_kernel(const RopeParams p) {
     }
 }
 
+// Aligned tensors.  The items of all (token, head) rows form one line; a block takes PER * 256 of them, a thread PER.  An
+// item is a 16-byte vector, or (half layout, rotated part) the two vectors that hold its pairs.  A thread's loads are all
+// in flight while the block computes the cosines and sines of its few tokens into shared memory.
+constexpr int kRopeThreads = 256;
+constexpr int kRopePer = 4;
+constexpr int kRopeAngles = 4096;  // of a block's tokens: 32 KB
+
+__device__ __forceinline__ void rope_unpack(const uint4& v, float (&f)[4]) {
+    f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+}
+__device__ __forceinline__ void rope_unpack(const uint4& v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ uint4 rope_pack(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+__device__ __forceinline__ uint4 rope_pack(const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <class T, bool HALF, int PER>
+__global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int V = 16 / sizeof(T);
+    extern __shared__ float2 s_cs[];
+    const int R2 = p.R / 2;
+    const int rot = HALF ? R2 / V : p.R / V;      // rotated items of a head
+    const int items = rot + (p.D - p.R) / V;      // then its copied vectors
+    const int row = items * p.heads;              // items of a token
+    const int64_t all = p.T0 * p.T1 * (int64_t)row;
+    const int64_t first = (int64_t)blockIdx.x * (PER * kRopeThreads);
+    const uint32_t tok0 = (uint32_t)(first / row);
+    const int skip = (int)(first - (int64_t)tok0 * row);
+    const int n = (int)min((int64_t)(PER * kRopeThreads), all - first);
+    uint4 a[PER], b[PER];
+    T* dst[PER];
+    int cs[PER];  // first angle of the item, -1: copied
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int e = threadIdx.x + k * kRopeThreads;
+        if (e >= n) break;
+        const uint32_t at = skip + e, t = at / (uint32_t)row, r = at - t * row;
+        const int hh = r / (uint32_t)items, it = r - hh * items;
+        const int which = hh >= p.t[0].H, h = which ? hh - p.t[0].H : hh;
+        const uint32_t tok = tok0 + t, t0 = tok / (uint32_t)p.T1, t1 = tok - t0 * (uint32_t)p.T1;
+        int d;
+        if (it < rot) {
+            d = p.off + it * V;
+            cs[k] = t * R2 + (HALF ? it * V : it * (V / 2));
+        } else {
+            d = (it - rot) * V;
+            if (d >= p.off) d += p.R;
+            cs[k] = -1;
+        }
+        const RopeTensor& x = p.t[which];
+        const T* src = (const T*)x.x + t0 * x.xs[0] + t1 * x.xs[1] + h * x.xs[2] + d;
+        dst[k] = (T*)x.y + t0 * x.ys[0] + t1 * x.ys[1] + h * x.ys[2] + d;
+        a[k] = *reinterpret_cast<const uint4*>(src);
+        if (HALF && it < rot) b[k] = *reinterpret_cast<const uint4*>(src + R2);
+    }
+    const int angles = ((skip + n - 1) / row + 1) * R2;
+    for (int i = threadIdx.x; i < angles; i += kRopeThreads) {
+        const int t = i / R2;
+        const uint32_t tok = tok0 + t, t0 = tok / (uint32_t)p.T1, t1 = tok - t0 * (uint32_t)p.T1;
+        s_cs[i] = rope_cs(p.pos[t0 * p.ps[0] + t1 * p.ps[1]], p.freqs[i - t * R2], p.mscale, p.sign);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        if (threadIdx.x + k * kRopeThreads >= n) break;
+        if (cs[k] >= 0) {
+            const float2* c = s_cs + cs[k];
+            float f[V];
+            rope_unpack(a[k], f);
+            if constexpr (HALF) {
+                float g[V];
+                rope_unpack(b[k], g);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float u = f[i], w = g[i];
+                    f[i] = u * c[i].x - w * c[i].y;
+                    g[i] = w * c[i].x + u * c[i].y;
+                }
+                *reinterpret_cast<uint4*>(dst[k] + R2) = rope_pack(g);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i) {
+                    const float u = f[2 * i], w = f[2 * i + 1];
+                    f[2 * i] = u * c[i].x - w * c[i].y;
+                    f[2 * i + 1] = w * c[i].x + u * c[i].y;
+                }
+            }
+            a[k] = rope_pack(f);
+        }
+        *reinterpret_cast<uint4*>(dst[k]) = a[k];
+    }
+}
+
+// Angles of the tokens that `n` items can touch.
+static int64_t rope_angles(const RopeParams& p, int row, int n) { return (int64_t)((n - 1) / row + 2) * (p.R / 2); }
+
+template <class T, bool HALF>
+static cudaError_t rope_vec_launch(const RopeParams& p, cudaStream_t st) {
+    constexpr int V = 16 / sizeof(T);
+    const int row = ((HALF ? p.R / 2 / V : p.R / V) + (p.D - p.R) / V) * p.heads;
+    const int64_t all = p.T0 * p.T1 * row;
+    // four items a thread, unless that leaves SMs without a block or there are too many angles (a single short head)
+    constexpr int big = kRopePer * kRopeThreads;
+    const int per = all / big >= 2 * current_sms() && rope_angles(p, row, big) <= kRopeAngles ? kRopePer : 1;
+    const int64_t blocks = (all + per * kRopeThreads - 1) / (per * kRopeThreads);
+    if (blocks > INT_MAX) return cudaErrorInvalidValue;
+    const int smem = (int)rope_angles(p, row, per * kRopeThreads) * (int)sizeof(float2);
+    if (per == kRopePer)
+        rope_vec_kernel<T, HALF, kRopePer><<<(unsigned)blocks, kRopeThreads, smem, st>>>(p);
+    else
+        rope_vec_kernel<T, HALF, 1><<<(unsigned)blocks, kRopeThreads, smem, st>>>(p);
+    return cudaGetLastError();
+}
+
+// Every vector of every head starts on 16 bytes and lies in or outside the rotated part as a whole.
+static bool rope_vectors(const RopeParams& p, int V, int es) {
+    if (p.D % V || p.off % V || (p.half ? (p.R / 2) % V : p.R % V)) return false;
+    uintptr_t bits = 0;
+    for (const RopeTensor& t : p.t) {
+        bits |= (uintptr_t)t.x | (uintptr_t)t.y;
+        for (int k = 0; k < 3; ++k) bits |= (uintptr_t)(t.xs[k] * es) | (uintptr_t)(t.ys[k] * es);
+    }
+    return (bits & 15) == 0;
+}
+
 template <class T>
 static cudaError_t rope_launch(const RopeParams& p, cudaStream_t st) {
+    if (rope_vectors(p, 16 / sizeof(T), sizeof(T)))
+        return p.half ? rope_vec_launch<T, true>(p, st) : rope_vec_launch<T, false>(p, st);
     const int64_t n = p.T0 * p.T1 * p.heads * (int64_t)(p.D / 2);
     int64_t blocks = (n + 255) / 256;
     const int64_t cap = (int64_t)current_sms() * 32;
@@ -145,7 +287,7 @@ int lidx_rope(const lidx_rope_tensor* t, int nt, const int32_t* pos, const int64
     p.heads = 0;
     for (int i = 0; i < 2; ++i) {
         const lidx_rope_tensor& s = t[i < nt ? i : 0];
-        if (s.H < 1 || s.H > (1 << 20)) return LIDX_ERR_SHAPE;
+        if (s.H < 1 || s.H > (1 << 15)) return LIDX_ERR_SHAPE;
         if (((uintptr_t)s.x | (uintptr_t)s.y) % es) return LIDX_ERR_ALIGN;
         p.t[i].x = s.x;
         p.t[i].y = s.y;
