@@ -64,7 +64,6 @@ struct AttnParams {
 
 constexpr int kATile = 128;                     // keys of a tile
 constexpr int kASlotBytes = kATile * 128;       // one K or V tile: 128 bytes a key (zero past D)
-constexpr int kAThreads = 512;
 constexpr int kAMeta = 5;                       // stages of per-key scales
 constexpr float kATop = 8.f;                    // weights are scaled to 2^8
 constexpr float kALn2 = 0.693147180559945309f;
@@ -72,37 +71,56 @@ constexpr float kALn2 = 0.693147180559945309f;
 // Shared memory of the configuration with N columns.
 template <int N>
 struct AttnCfg {
-    static constexpr bool SPLIT = N == 128;            // both softmax groups share each tile's columns
-    static constexpr int NC = SPLIT ? 64 : N;          // columns of a softmax group
-    static constexpr int QB = SPLIT ? 1 : 2;           // query buffers
+    // Softmax groups of four warps.  At N = 16 two groups take the tiles in turn; from N = 32 on the groups share each
+    // tile's columns, 16 a group, so that a thread keeps its 16 scores and sums in registers (at N = 64 two groups of
+    // 64 columns took 7.7k cycles a tile, most of it exposed latency and spills).  N = 128 has two groups of 64 columns:
+    // four groups would not leave the registers that joining 128 columns takes.
+    static constexpr int SG = N == 64 ? 4 : 2;
+    static constexpr bool SPLIT = N > 16;
+    static constexpr int NC = SPLIT ? N / SG : N;      // columns of a group
+    static constexpr int QB = N == 128 ? 1 : 2;        // query buffers
     static constexpr int SLOTS = N == 16 ? 9 : (N == 32 ? 8 : 7);
     static constexpr int Q_BYTES = 2 * N * 128;        // hi and lo
     static constexpr int P_BYTES = 2 * kASlotBytes;    // hi and lo
     static constexpr int OFF_P = SLOTS * kASlotBytes;
     static constexpr int OFF_Q = OFF_P + 2 * P_BYTES;
     static constexpr int OFF_META = OFF_Q + QB * Q_BYTES;              // [kAMeta][128] float2
-    static constexpr int OFF_FLAG = OFF_META + kAMeta * kATile * 8;    // [kAMeta] int
-    static constexpr int OFF_QS = OFF_FLAG + 64;                       // [2][N] query scales
-    static constexpr int OFF_W = OFF_QS + 2 * N * 4;                   // [2][4][NC] warp maxima
-    static constexpr int OFF_MB = OFF_W + 2 * 4 * NC * 4;              // [2][2][NC] 8 - M; fade of the tile
-    static constexpr int OFF_AL = OFF_MB + 2 * NC * 8;                 // [2][NC] fade of the sum
-    static constexpr int OFF_END = OFF_AL + 2 * NC * 4;                // [2][NC] keys a column sees
-    static constexpr int OFF_MT = OFF_END + 2 * NC * 4;                // [2][N] tile maxima
+    static constexpr int OFF_FLAG = OFF_META + kAMeta * kATile * 8;    // [kAMeta] four bytes, one a producer
+    static constexpr int OFF_QS = OFF_FLAG + 128;                      // [2][N] query scales
+    static constexpr int OFF_W = OFF_QS + 2 * N * 4;                   // [SG][4][NC] warp maxima
+    static constexpr int OFF_MB = OFF_W + SG * 4 * NC * 4;             // [SG][2][NC] 8 - M; fade of the tile
+    static constexpr int OFF_AL = OFF_MB + SG * NC * 8;                // [SG][NC] fade of the sum
+    static constexpr int OFF_END = OFF_AL + SG * NC * 4;               // [SG][NC] keys a column sees
+    static constexpr int OFF_MT = OFF_END + SG * NC * 4;               // [2][N] tile maxima
     static constexpr int OFF_AB = OFF_MT + 2 * N * 4;                  // [2][2][N] fades of acc and tile
-    static constexpr int OFF_L = OFF_AB + 2 * N * 8;                   // [2][4][NC] sums of the warps
-    static constexpr int OFF_MW = OFF_L + 2 * 4 * NC * 4;              // [2][NC] their reference
-    static constexpr int OFF_INV = OFF_MW + 2 * NC * 4;                // [N] 1 / l
+    static constexpr int OFF_L = OFF_AB + 2 * N * 8;                   // [SG][4][NC] sums of the warps
+    static constexpr int OFF_MW = OFF_L + SG * 4 * NC * 4;             // [SG][NC] their reference
+    static constexpr int OFF_INV = OFF_MW + SG * NC * 4;               // [N] 1 / l
     static constexpr int OFF_ROW = OFF_INV + N * 4;                    // [N] output rows
     static constexpr int OFF_GATHER = OFF_ROW + N * 4;                 // [128] cache rows of a tile's keys
     static constexpr int OFF_BAR = OFF_GATHER + kATile * 4;
     static constexpr int NBAR = 2 * SLOTS + 2 * kAMeta + 2 * 2 + 5 * 2 + 2 + 1;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;                // start of the share, TMEM address
     static constexpr int TOTAL = OFF_MISC + 256 + 1024;                // + alignment of the base
-    static_assert(TOTAL <= 232448 && kAMeta * 4 <= 64, "shared memory");
+    static_assert(TOTAL <= 232448 && kAMeta * 4 <= 128, "shared memory");
     static_assert(OFF_QS % 16 == 0 && OFF_MB % 16 == 0 && OFF_AL % 16 == 0 && OFF_END % 16 == 0 && OFF_AB % 16 == 0 && OFF_W % 16 == 0 &&
                       OFF_GATHER % 16 == 0,
                   "16-byte reads");
     static constexpr int TMEM = 4 * N;                                 // columns: two tiles of S and of O
+    // Warpgroups: MMA and queries; SG of softmax; joining; up to N = 64 four producers (N = 128, whose joining group holds
+    // 128 sums a thread, has no registers for them: one warp of the first group produces).
+    static constexpr bool OWN_PROD = N < 128;
+    static constexpr int THREADS = 128 * (2 + SG + (OWN_PROD ? 1 : 0));
+    static constexpr int W_SOFT = 4, W_JOIN = 4 + 4 * SG;  // first warps
+    static constexpr int PRODUCERS = OWN_PROD ? 4 : 1, W_PROD = OWN_PROD ? W_JOIN + 4 : 1;
+    static constexpr int QWARPS = OWN_PROD ? 3 : 2, W_QUERY = OWN_PROD ? 1 : 2;
+    // registers a thread of each group; their sum is at most what the launch has
+    static constexpr int R_LAUNCH = 65536 / THREADS / 8 * 8;
+    static constexpr int R_MMA = N == 128 ? 80 : 56, R_PROD = 56, R_JOIN = N == 128 ? 160 : 104;
+    static constexpr int R_SOFT = N == 128 ? 136 : (N == 64 ? 72 : 112);
+    static_assert(R_MMA + SG * R_SOFT + R_JOIN + (OWN_PROD ? R_PROD : 0) <= R_LAUNCH * (THREADS / 128), "register split");
+    static_assert(R_MMA < R_LAUNCH && (!OWN_PROD || R_PROD < R_LAUNCH) && R_JOIN > R_LAUNCH && R_SOFT >= R_LAUNCH,
+                  "groups that give registers, groups that take them");
 };
 
 // Row (b, s) sees keys [0, end).
@@ -111,9 +129,9 @@ __device__ __forceinline__ int attn_end(const AttnParams& p, int b, int s) {
     const int cap = p.max_pages * p.page;
     n = n < 0 ? 0 : (n > cap ? cap : n);
     if (p.q_pos) {
-        const int64_t seen = (int64_t)p.q_pos[b] + s + 1;
-        const int64_t e = seen > 0 ? seen / p.ratio : 0;
-        n = e < n ? (int)e : n;
+        const int64_t seen = (int64_t)p.q_pos[b] + s + 1;  // below 2^32
+        const uint32_t e = seen > 0 ? (uint32_t)seen / (uint32_t)p.ratio : 0;
+        n = e < (uint32_t)n ? (int)e : n;
     }
     return n;
 }
@@ -124,14 +142,17 @@ struct AttnGroup {
     int n;             // tiles of a unit (0: nothing to see)
     int w;             // places of a unit on the line: at least one
 };
+__device__ __forceinline__ void attn_group_size(const AttnParams& p, AttnGroup& r) {
+    if (!p.idx) r.limit = attn_end(p, r.b, min(r.st * p.TS + p.TS, p.S) - 1);  // (selected keys: the producers look)
+    r.n = ((p.idx ? p.topk : r.limit) + kATile - 1) / kATile;
+    r.w = max(r.n, 1);
+}
 __device__ __forceinline__ AttnGroup attn_group(const AttnParams& p, int g) {
     AttnGroup r;
     r.b = g / p.ST;
     r.st = g - r.b * p.ST;
-    const int s1 = min(r.st * p.TS + p.TS, p.S) - 1;
-    r.limit = attn_end(p, r.b, s1);
-    r.n = ((p.idx ? p.topk : r.limit) + kATile - 1) / kATile;
-    r.w = max(r.n, 1);
+    r.limit = 0;
+    attn_group_size(p, r);
     return r;
 }
 // Query token of column n within a unit.
@@ -140,34 +161,40 @@ __device__ __forceinline__ int64_t attn_share(int64_t W, int c, int n) { return 
 
 // The segments [t0, t1) of units that make up a CTA's share; every role walks them alike.
 struct AttnWalk {
-    int64_t pos, end, base;  // base: place of the group's first unit
+    int64_t pos, end;   // places not walked yet
+    int64_t unit_end;   // place behind the segment's unit
     int g, h, t0, t1;
-    int64_t unit_end;
     AttnGroup gr;
-    bool first, fresh;
+    bool first, fresh;  // first: the segment is the CTA's first
 
-    __device__ void begin(const AttnParams& p, int64_t pos_, int64_t end_, int g_, int64_t base_) {
+    // pos lies in group g, whose first unit's place is base
+    __device__ void begin(const AttnParams& p, int64_t pos_, int64_t end_, int g_, int64_t base) {
         pos = pos_;
         end = end_;
         g = g_;
-        base = base_;
-        fresh = true;
         t1 = 0;
+        fresh = true;
+        if (pos >= end) return;
+        gr = attn_group(p, g);
+        const int64_t at = pos - base;
+        h = at < INT_MAX ? (int)((uint32_t)at / (uint32_t)gr.w) : (int)(at / gr.w);
+        t0 = (int)(at - (int64_t)h * gr.w);
     }
     __device__ bool next(const AttnParams& p) {
         if (pos >= end) return false;
         first = fresh;
         if (fresh) {
-            gr = attn_group(p, g);
             fresh = false;
-        } else if (pos >= base + (int64_t)gr.w * p.Hkv) {
-            base += (int64_t)gr.w * p.Hkv;
-            gr = attn_group(p, ++g);
+        } else {
+            t0 = 0;
+            if (++h == p.Hkv) {
+                h = 0;
+                ++g;
+                if (++gr.st == p.ST) gr.st = 0, ++gr.b;
+                attn_group_size(p, gr);
+            }
         }
-        const int64_t at = pos - base;
-        h = (int)(at / gr.w);
-        t0 = (int)(at - (int64_t)h * gr.w);
-        unit_end = base + (int64_t)(h + 1) * gr.w;
+        unit_end = pos - t0 + gr.w;
         const int64_t e = unit_end < end ? unit_end : end;
         t1 = t0 + (int)(e - pos);
         pos = e;
@@ -242,7 +269,7 @@ __device__ __forceinline__ void attn_scores(uint32_t s_addr, const float* qs, co
 }
 
 template <int N>
-__global__ void __launch_bounds__(kAThreads, 1)
+__global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                       const __grid_constant__ AttnParams p) {
     using C = AttnCfg<N>;
@@ -253,7 +280,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
     uint8_t* const sP = smem + C::OFF_P;
     uint8_t* const sQ = smem + C::OFF_Q;
     float2* const sMeta = (float2*)(smem + C::OFF_META);
-    int* const sFlag = (int*)(smem + C::OFF_FLAG);
+    uint32_t* const sFlag = (uint32_t*)(smem + C::OFF_FLAG);  // not 0: a key of the tile is not seen
     float* const sQs = (float*)(smem + C::OFF_QS);
     float* const sMt = (float*)(smem + C::OFF_MT);
     float* const sL = (float*)(smem + C::OFF_L);
@@ -273,31 +300,31 @@ __global__ void __launch_bounds__(kAThreads, 1)
     uint64_t* l_full = m_read + 2;          // sums of a segment written
     uint64_t* l_empty = l_full + 1;
     uint64_t* drain = l_empty + 1;
-    int64_t* sScan = (int64_t*)(smem + C::OFF_MISC);  // [16]
-    int64_t* sBase = sScan + 16;
+    int64_t* sScan = (int64_t*)(smem + C::OFF_MISC);  // [28]
+    int64_t* sBase = sScan + 28;
     int* sGroup = (int*)(sBase + 1);
     uint32_t* tmem_slot = (uint32_t*)(sGroup + 1);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < SLOTS; ++i) {
-            mbar_init(kv_full + i, 1);
+            mbar_init(kv_full + i, p.idx ? C::PRODUCERS : 1);
             mbar_init(kv_empty + i, 1);
         }
         for (int i = 0; i < kAMeta; ++i) {
-            mbar_init(meta_full + i, 1);
-            mbar_init(meta_empty + i, C::SPLIT ? 8 : 4);
+            mbar_init(meta_full + i, p.idx ? C::PRODUCERS : 1);
+            mbar_init(meta_empty + i, C::SPLIT ? 4 * C::SG : 4);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(q_full + i, 2);
-            mbar_init(q_empty + i, 1 + 8);
+            mbar_init(q_full + i, C::QWARPS);
+            mbar_init(q_empty + i, 1 + 4 * C::SG);
             mbar_init(s_full + i, 1);
-            mbar_init(p_full + i, C::SPLIT ? 8 : 4);
+            mbar_init(p_full + i, C::SPLIT ? 4 * C::SG : 4);
             mbar_init(o_full + i, 1);
             mbar_init(o_empty + i, 4);
             mbar_init(m_read + i, 4);
         }
-        mbar_init(l_full, 8);
+        mbar_init(l_full, 4 * C::SG);
         mbar_init(l_empty, 4);
         mbar_init(drain, 1);
         fence_mbar_init();
@@ -324,7 +351,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
         g0 = (int)(pos0 / w);
         base0 = g0 * w;
     } else {
-        const int NG = p.B * p.ST, per = (NG + kAThreads - 1) / kAThreads;
+        const int NG = p.B * p.ST, per = (NG + C::THREADS - 1) / C::THREADS;
         const int ga = min(tid * per, NG), gz = min(ga + per, NG);
         int64_t sum = 0;
         for (int g = ga; g < gz; ++g) sum += (int64_t)attn_group(p, g).w * p.Hkv;
@@ -339,7 +366,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
         W = 0;
         int64_t before = 0;
 #pragma unroll
-        for (int i = 0; i < kAThreads / 32; ++i) {
+        for (int i = 0; i < C::THREADS / 32; ++i) {
             if (i == warp) before = W;
             W += sScan[i];
         }
@@ -369,8 +396,196 @@ __global__ void __launch_bounds__(kAThreads, 1)
     AttnWalk wk;
     wk.begin(p, pos0, pos1, g0, base0);
 
+    auto produce = [&]() {
+        // --------------------------------------------------------- producer
+        // Three steps ahead: indices of tile i + 2, page ids of tile i + 1, scales of tile i, so that a
+        // step waits for one memory latency at most.  A lane has four keys.
+        bool ok = !p.debug_stall;
+        struct Ref {
+            bool live;
+            int b, h, tile, limit;
+            int64_t row;  // of topk_indices
+        };
+        int tile = 0;
+        bool more = true;
+        auto next_ref = [&]() {
+            Ref r{false, 0, 0, 0, 0, 0};
+            while (more && (tile >= wk.t1 || wk.gr.n == 0)) {
+                more = wk.next(p);
+                tile = wk.t0;
+                if (more && p.idx) wk.gr.limit = attn_end(p, wk.gr.b, wk.gr.st);
+            }
+            if (more) r = Ref{true, wk.gr.b, wk.h, tile++, wk.gr.limit, (int64_t)wk.gr.b * p.S + wk.gr.st};
+            return r;
+        };
+        int tc = 0;
+        const int page_mask = p.page - 1;
+        // waits for the slots of tile tc's K and V and its stage of scales
+        auto claim = [&]() {
+            const int sk = 2 * tc, ms = tc % kAMeta;
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+                ok = ok && mbar_wait(kv_empty + (sk + w) % SLOTS, (((sk + w) / SLOTS) & 1) ^ 1, p.wait_ns);
+            ok = ok && mbar_wait(meta_empty + ms, ((tc / kAMeta) & 1) ^ 1, p.wait_ns);
+            ok = __all_sync(0xffffffffu, ok);
+        };
+        const int pw = warp - C::W_PROD;  // of the producers
+        if (!p.idx) {
+            if (pw > 0) return;
+            // Pages: the four keys of a lane share one; the lane with a page's first key loads it.
+            auto page_id = [&](const Ref& r) {
+                const int k0 = r.tile * kATile + 4 * lane;
+                return r.live && k0 < r.limit ? p.table[(int64_t)r.b * p.max_pages + (k0 >> p.page_shift)] : -1;
+            };
+            Ref r0 = next_ref();
+            int pid0 = page_id(r0);
+            Ref r1 = next_ref();
+            while (ok && r0.live) {
+                const bool good = pid0 >= 0 && pid0 < p.num_pages;
+                const int64_t cell = (int64_t)(good ? pid0 : 0) * p.Hkv + r0.h;
+                const float a = p.ks[cell], v = p.vs[cell];
+                const int pid1 = page_id(r1);
+                const Ref r2 = next_ref();
+                claim();
+                if (!ok) break;
+                const int sk = 2 * tc, ms = tc % kAMeta, s0 = sk % SLOTS, s1 = (sk + 1) % SLOTS;
+                const bool lead = good && ((4 * lane) & page_mask) == 0;
+                const uint32_t bytes = (128u << p.page_shift) * __popc(__ballot_sync(0xffffffffu, lead));
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(kv_full + s0, bytes);
+                    mbar_arrive_expect_tx(kv_full + s1, bytes);
+                }
+                __syncwarp();
+                if (lead) {
+                    const int row = (int)(cell << p.page_shift);
+                    tma_load_2d(smem + s0 * kASlotBytes + lane * 512, &tmk, kv_full + s0, 0, row);
+                    tma_load_2d(smem + s1 * kASlotBytes + lane * 512, &tmv, kv_full + s1, 0, row);
+                }
+                const int left = good ? r0.limit - (r0.tile * kATile + 4 * lane) : 0;  // keys of the lane that count
+                const float x = a * p.scale_log2, y = __log2f(fmaxf(v, 0x1p-60f));
+                float4* m4 = reinterpret_cast<float4*>(sMeta + ms * kATile + 4 * lane);
+                m4[0] = make_float4(x, left > 0 ? y : -INFINITY, x, left > 1 ? y : -INFINITY);
+                m4[1] = make_float4(x, left > 2 ? y : -INFINITY, x, left > 3 ? y : -INFINITY);
+                const bool all = __all_sync(0xffffffffu, left > 3);
+                if (lane == 0) {
+                    sFlag[ms] = all ? 0 : 1;
+                    mbar_arrive(meta_full + ms);
+                }
+                r0 = r1;
+                r1 = r2;
+                pid0 = pid1;
+                ++tc;
+            }
+            if (!ok && !p.debug_stall)  // loads in flight end before the memory is given up
+                for (int seq = max(0, 2 * tc - SLOTS); seq < 2 * tc; ++seq)
+                    mbar_wait(kv_full + seq % SLOTS, (seq / SLOTS) & 1, p.wait_ns);
+        } else {
+            // Selected keys: 16-byte asynchronous copies, eight lanes a row of 128 bytes, written in the
+            // 128-byte swizzle TMA would use; unseen keys and dims past D become zeros.  A producer has NQ quarters
+            // of 32 keys of each tile, a lane one key of each.  (One warp for the whole tile took 9.9k cycles a
+            // tile, a TMA gather, whose 64 instructions the lanes issue one after the other, 11.9k.)
+            constexpr int NQ = 4 / C::PRODUCERS;
+            auto keys = [&](const Ref& r, int (&t)[NQ]) {
+                const int32_t* src = p.idx + r.row * p.topk;
+#pragma unroll
+                for (int i = 0; i < NQ; ++i) {
+                    const int k = r.tile * kATile + 32 * (pw + i) + lane;
+                    t[i] = r.live && k < p.topk ? src[k] : -1;
+                    t[i] = t[i] < r.limit ? t[i] : -1;
+                }
+            };
+            auto pages = [&](const Ref& r, const int (&t)[NQ], int (&pid)[NQ]) {
+                const int32_t* tab = p.table + (int64_t)r.b * p.max_pages;
+#pragma unroll
+                for (int i = 0; i < NQ; ++i) pid[i] = t[i] >= 0 ? tab[t[i] >> p.page_shift] : -1;
+            };
+            int* const sRows = (int*)(smem + C::OFF_GATHER) + 32 * pw;
+            const int sub = lane & 7, part = lane >> 3;  // chunk of a row; rows 8 part .. 8 part + 7 of a quarter
+            const uint32_t in_row = sub * 16 < p.D ? 16 : 0;
+            const uint8_t* const kc = p.kc + sub * 16;
+            const uint8_t* const vc = p.vc + sub * 16;
+            // this warp's copies of tile t have landed: hand them on
+            auto landed = [&](int t) {
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(kv_full + (2 * t) % SLOTS);
+                    mbar_arrive(kv_full + (2 * t + 1) % SLOTS);
+                }
+            };
+            Ref r0 = next_ref();
+            int t0[NQ], t1[NQ], t2[NQ], pid0[NQ], pid1[NQ];
+            keys(r0, t0);
+            Ref r1 = next_ref();
+            keys(r1, t1);
+            pages(r0, t0, pid0);
+            while (ok && r0.live) {
+                float a[NQ], v[NQ];
+                bool good[NQ];
+#pragma unroll
+                for (int i = 0; i < NQ; ++i) {
+                    good[i] = pid0[i] >= 0 && pid0[i] < p.num_pages;
+                    const int cell = (good[i] ? pid0[i] : 0) * p.Hkv + r0.h;  // num_pages * Hkv * page < 2^31
+                    a[i] = p.ks[cell];
+                    v[i] = p.vs[cell];
+                    sRows[32 * i + lane] = good[i] ? (cell << p.page_shift) + (t0[i] & page_mask) : -1;
+                }
+                pages(r1, t1, pid1);
+                const Ref r2 = next_ref();
+                keys(r2, t2);
+                claim();
+                if (!ok) break;
+                __syncwarp();
+                const int sk = 2 * tc, ms = tc % kAMeta;
+                const uint32_t at = smem_u32(smem) + pw * 4096 + part * 1024;
+                const uint32_t dk = at + (sk % SLOTS) * kASlotBytes, dv = at + ((sk + 1) % SLOTS) * kASlotBytes;
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    const int4 ra = *reinterpret_cast<const int4*>(sRows + 32 * q + 8 * part);
+                    const int4 rb = *reinterpret_cast<const int4*>(sRows + 32 * q + 8 * part + 4);
+                    const int r[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t to = q * 4096 + i * 128 + ((sub ^ i) << 4);
+                        const int64_t from = (int64_t)max(r[i], 0) * p.D;
+                        const uint32_t n = r[i] >= 0 ? in_row : 0;
+                        // (a chunk past D reads nothing; its address stays inside the row before it)
+                        cp_async16(dk + to, n ? kc + from : p.kc, n);
+                        cp_async16(dv + to, n ? vc + from : p.vc, n);
+                    }
+                }
+                cp_async_commit();
+#pragma unroll
+                for (int i = 0; i < NQ; ++i) {
+                    sMeta[ms * kATile + 32 * (pw + i) + lane] =
+                        good[i] ? make_float2(a[i] * p.scale_log2, __log2f(fmaxf(v[i], 0x1p-60f)))
+                                : make_float2(0.f, -INFINITY);
+                    const bool all = __all_sync(0xffffffffu, good[i]);
+                    if (lane == 0) reinterpret_cast<uint8_t*>(sFlag + ms)[pw + i] = all ? 0 : 1;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(meta_full + ms);
+                if (tc > 0) {  // two tiles in flight
+                    cp_async_wait<1>();
+                    landed(tc - 1);
+                }
+                r0 = r1;
+                r1 = r2;
+#pragma unroll
+                for (int i = 0; i < NQ; ++i) {
+                    t0[i] = t1[i];
+                    t1[i] = t2[i];
+                    pid0[i] = pid1[i];
+                }
+                ++tc;
+            }
+            cp_async_wait<0>();  // also where a wait ran out: no copy outlives the block
+            if (ok && tc > 0) landed(tc - 1);
+        }
+    };
+
     if (warp < 4) {
-        regs_dec<80>();
+        regs_dec<C::R_MMA>();
         if (warp == 0) {
             // ------------------------------------------------------- MMA issuer
             // The whole warp walks and waits; one lane issues.
@@ -448,192 +663,9 @@ __global__ void __launch_bounds__(kAThreads, 1)
                 if (issuer) umma_commit(drain);
                 mbar_wait(drain, 0, p.wait_ns);
             }
-        } else if (warp == 1) {
-            // --------------------------------------------------------- producer
-            // Three steps ahead: indices of tile i + 2, page ids of tile i + 1, scales of tile i, so that a
-            // step waits for one memory latency at most.  A lane has four keys.
-            bool ok = !p.debug_stall;
-            struct Ref {
-                bool live;
-                int b, h, tile, limit;
-                int64_t row;  // of topk_indices
-            };
-            int tile = 0;
-            bool more = true;
-            auto next_ref = [&]() {
-                Ref r{false, 0, 0, 0, 0, 0};
-                while (more && (tile >= wk.t1 || wk.gr.n == 0)) {
-                    more = wk.next(p);
-                    tile = wk.t0;
-                }
-                if (more) r = Ref{true, wk.gr.b, wk.h, tile++, wk.gr.limit, (int64_t)wk.gr.b * p.S + wk.gr.st};
-                return r;
-            };
-            int tc = 0;
-            const int page_mask = p.page - 1;
-            // waits for the slots of tile tc's K and V and its stage of scales
-            auto claim = [&]() {
-                const int sk = 2 * tc, ms = tc % kAMeta;
-#pragma unroll
-                for (int w = 0; w < 2; ++w)
-                    ok = ok && mbar_wait(kv_empty + (sk + w) % SLOTS, (((sk + w) / SLOTS) & 1) ^ 1, p.wait_ns);
-                ok = ok && mbar_wait(meta_empty + ms, ((tc / kAMeta) & 1) ^ 1, p.wait_ns);
-                ok = __all_sync(0xffffffffu, ok);
-            };
-            if (!p.idx) {
-                // Pages: the four keys of a lane share one; the lane with a page's first key loads it.
-                auto page_id = [&](const Ref& r) {
-                    const int k0 = r.tile * kATile + 4 * lane;
-                    return r.live && k0 < r.limit ? p.table[(int64_t)r.b * p.max_pages + (k0 >> p.page_shift)] : -1;
-                };
-                Ref r0 = next_ref();
-                int pid0 = page_id(r0);
-                Ref r1 = next_ref();
-                while (ok && r0.live) {
-                    const bool good = pid0 >= 0 && pid0 < p.num_pages;
-                    const int64_t cell = (int64_t)(good ? pid0 : 0) * p.Hkv + r0.h;
-                    const float a = p.ks[cell], v = p.vs[cell];
-                    const int pid1 = page_id(r1);
-                    const Ref r2 = next_ref();
-                    claim();
-                    if (!ok) break;
-                    const int sk = 2 * tc, ms = tc % kAMeta, s0 = sk % SLOTS, s1 = (sk + 1) % SLOTS;
-                    const bool lead = good && ((4 * lane) & page_mask) == 0;
-                    const uint32_t bytes = (128u << p.page_shift) * __popc(__ballot_sync(0xffffffffu, lead));
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(kv_full + s0, bytes);
-                        mbar_arrive_expect_tx(kv_full + s1, bytes);
-                    }
-                    __syncwarp();
-                    if (lead) {
-                        const int row = (int)(cell << p.page_shift);
-                        tma_load_2d(smem + s0 * kASlotBytes + lane * 512, &tmk, kv_full + s0, 0, row);
-                        tma_load_2d(smem + s1 * kASlotBytes + lane * 512, &tmv, kv_full + s1, 0, row);
-                    }
-                    const int left = good ? r0.limit - (r0.tile * kATile + 4 * lane) : 0;  // keys of the lane that count
-                    const float x = a * p.scale_log2, y = __log2f(fmaxf(v, 0x1p-60f));
-                    float4* m4 = reinterpret_cast<float4*>(sMeta + ms * kATile + 4 * lane);
-                    m4[0] = make_float4(x, left > 0 ? y : -INFINITY, x, left > 1 ? y : -INFINITY);
-                    m4[1] = make_float4(x, left > 2 ? y : -INFINITY, x, left > 3 ? y : -INFINITY);
-                    const bool all = __all_sync(0xffffffffu, left > 3);
-                    if (lane == 0) {
-                        sFlag[ms] = all ? 0 : 1;
-                        mbar_arrive(meta_full + ms);
-                    }
-                    r0 = r1;
-                    r1 = r2;
-                    pid0 = pid1;
-                    ++tc;
-                }
-                if (!ok && !p.debug_stall)  // loads in flight end before the memory is given up
-                    for (int seq = max(0, 2 * tc - SLOTS); seq < 2 * tc; ++seq)
-                        mbar_wait(kv_full + seq % SLOTS, (seq / SLOTS) & 1, p.wait_ns);
-            } else {
-                // Selected keys: 16-byte asynchronous copies, eight lanes a row of 128 bytes, written in the
-                // 128-byte swizzle TMA would use; unseen keys and dims past D become zeros.  (A TMA gather takes
-                // 64 instructions a tile that the lanes issue one after the other: 11.9k cycles a tile.)
-                auto keys = [&](const Ref& r, int (&t)[4]) {
-                    const int k0 = r.tile * kATile + 4 * lane;
-                    const int32_t* src = p.idx + r.row * p.topk + k0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        t[i] = r.live && k0 + i < p.topk ? src[i] : -1;
-                        t[i] = t[i] < r.limit ? t[i] : -1;
-                    }
-                };
-                auto pages = [&](const Ref& r, const int (&t)[4], int (&pid)[4]) {
-                    const int32_t* tab = p.table + (int64_t)r.b * p.max_pages;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) pid[i] = t[i] >= 0 ? tab[t[i] >> p.page_shift] : -1;
-                };
-                int* const sRows = (int*)(smem + C::OFF_GATHER);
-                const int sub = lane & 7, part = lane >> 3;
-                const uint32_t in_row = sub * 16 < p.D ? 16 : 0;
-                const uint32_t off_even = part * 128 + ((sub ^ part) << 4);              // rows 8j .. 8j + 3
-                const uint32_t off_odd = (part + 4) * 128 + ((sub ^ (part + 4)) << 4);  // rows 8j + 4 .. 8j + 7
-                // the tile that was issued `behind` tiles ago has landed: hand it on
-                auto landed = [&](int t) {
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(kv_full + (2 * t) % SLOTS);
-                        mbar_arrive(kv_full + (2 * t + 1) % SLOTS);
-                    }
-                };
-                Ref r0 = next_ref();
-                int t0[4], t1[4], t2[4], pid0[4], pid1[4];
-                keys(r0, t0);
-                Ref r1 = next_ref();
-                keys(r1, t1);
-                pages(r0, t0, pid0);
-                while (ok && r0.live) {
-                    float a[4], v[4];
-                    bool good[4];
-                    int row[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        good[i] = pid0[i] >= 0 && pid0[i] < p.num_pages;
-                        const int cell = (good[i] ? pid0[i] : 0) * p.Hkv + r0.h;  // num_pages * Hkv * page < 2^31
-                        a[i] = p.ks[cell];
-                        v[i] = p.vs[cell];
-                        row[i] = good[i] ? (cell << p.page_shift) + (t0[i] & page_mask) : -1;
-                    }
-                    pages(r1, t1, pid1);
-                    const Ref r2 = next_ref();
-                    keys(r2, t2);
-                    *reinterpret_cast<int4*>(sRows + 4 * lane) = make_int4(row[0], row[1], row[2], row[3]);
-                    claim();
-                    if (!ok) break;
-                    __syncwarp();
-                    const int sk = 2 * tc, ms = tc % kAMeta;
-                    const uint32_t dk = smem_u32(smem) + (sk % SLOTS) * kASlotBytes;
-                    const uint32_t dv = smem_u32(smem) + ((sk + 1) % SLOTS) * kASlotBytes;
-#pragma unroll 4
-                    for (int i = 0; i < 32; ++i) {
-                        const int r = sRows[4 * i + part];
-                        const uint32_t at = (i >> 1) * 1024 + ((i & 1) ? off_odd : off_even);
-                        const int64_t from = r >= 0 ? (int64_t)r * p.D + sub * 16 : 0;
-                        const uint32_t n = r >= 0 ? in_row : 0;
-                        cp_async16(dk + at, p.kc + (n ? from : 0), n);
-                        cp_async16(dv + at, p.vc + (n ? from : 0), n);
-                    }
-                    cp_async_commit();
-                    bool all = true;
-                    float2 mv[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        mv[i].x = good[i] ? a[i] * p.scale_log2 : 0.f;
-                        mv[i].y = good[i] ? __log2f(fmaxf(v[i], 0x1p-60f)) : -INFINITY;
-                        all = all && good[i];
-                    }
-                    float4* m4 = reinterpret_cast<float4*>(sMeta + ms * kATile + 4 * lane);
-                    m4[0] = make_float4(mv[0].x, mv[0].y, mv[1].x, mv[1].y);
-                    m4[1] = make_float4(mv[2].x, mv[2].y, mv[3].x, mv[3].y);
-                    all = __all_sync(0xffffffffu, all);
-                    if (lane == 0) {
-                        sFlag[ms] = all ? 0 : 1;
-                        mbar_arrive(meta_full + ms);
-                    }
-                    if (tc > 0) {  // two tiles in flight
-                        cp_async_wait<1>();
-                        landed(tc - 1);
-                    }
-                    r0 = r1;
-                    r1 = r2;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        t0[i] = t1[i];
-                        t1[i] = t2[i];
-                        pid0[i] = pid1[i];
-                    }
-                    ++tc;
-                }
-                cp_async_wait<0>();  // also where a wait ran out: no copy outlives the block
-                if (ok && tc > 0) landed(tc - 1);
-            }
-        } else {
+        } else if (warp >= C::W_QUERY && warp < C::W_QUERY + C::QWARPS) {
             // ------------------------------------- queries: bf16 rows -> e4m3 hi and lo
-            // Eight lanes a row, 16 dims each; the two warps take rows 8i .. 8i+3 and 8i+4 .. 8i+7.
+            // Eight lanes a row, 16 dims each, four rows a warp at a time.
             bool ok = true;
             int sc = 0;
             const int sub = lane & 7;
@@ -654,14 +686,15 @@ __global__ void __launch_bounds__(kAThreads, 1)
                     }
                 };
                 uint4 n0, n1, f0, f1;
-                const int first = (warp - 2) * 4 + (lane >> 3);
+                constexpr int step = 4 * C::QWARPS;
+                const int first = (warp - C::W_QUERY) * 4 + (lane >> 3);
                 load(first, n0, n1);
-                load(first + 8, f0, f1);
+                load(first + step, f0, f1);
 #pragma unroll 1
-                for (int n = first; n < N; n += 8) {
+                for (int n = first; n < N; n += step) {
                     const uint32_t w[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
                     n0 = f0, n1 = f1;
-                    load(n + 16, f0, f1);
+                    load(n + 2 * step, f0, f1);
                     uint32_t top = 0;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
@@ -694,13 +727,14 @@ __global__ void __launch_bounds__(kAThreads, 1)
                 if (lane == 0) mbar_arrive(q_full + qb);
                 ++sc;
             }
+        } else if constexpr (!C::OWN_PROD) {
+            produce();
         }
-    } else if (warp < 12) {
+    } else if (warp < C::W_JOIN) {
         // -------------------------------------------------------------- softmax
-        // A thread has one key of a tile and the columns [c0, c0 + NC).  Up to N = 64 the two groups take
-        // the tiles in turn; at N = 128 each takes half of every tile's columns.
-        regs_inc<136>();
-        const int grp = (warp - 4) >> 2, wtid = tid - 128 - grp * 128, wg_warp = warp & 3;
+        // A thread has one key of a tile and the columns [c0, c0 + NC).
+        if constexpr (C::R_SOFT > C::R_LAUNCH) regs_inc<C::R_SOFT>();
+        const int grp = (warp - C::W_SOFT) >> 2, wtid = tid & 127, wg_warp = warp & 3;
         const int c0 = C::SPLIT ? grp * NC : 0;
         const uint32_t bar_id = 1 + grp;
         float* const sW = (float*)(smem + C::OFF_W) + grp * 4 * NC;
@@ -857,11 +891,13 @@ __global__ void __launch_bounds__(kAThreads, 1)
             }
             ++sc;
         }
-    } else {
+    } else if (warp < C::W_JOIN + 4) {
         // ---------------------------------------------------------------- joining
         // A thread has one output dim (TMEM lane) of every column; thread i < N also keeps column i's maximum.
-        regs_inc<160>();
-        const int d = tid - 384, wg_warp = warp & 3;
+        regs_inc<C::R_JOIN>();
+        const int d = tid & 127, wg_warp = warp & 3;
+        constexpr uint32_t bar_id = 1 + C::SG;
+        constexpr int JC = N == 32 || N == 64 ? 32 : 16;  // columns read at a time
         const uint32_t lane_addr = tmem + ((uint32_t)(wg_warp * 32) << 16) + 2 * N;
         float* const sA = (float*)(smem + C::OFF_AB);  // [2][N] fade of acc
         float* const sB = sA + 2 * N;                  // [2][N] of the tile
@@ -888,16 +924,19 @@ __global__ void __launch_bounds__(kAThreads, 1)
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(m_read + bf);
-                    named_bar_sync(3, 128);
+                    named_bar_sync(bar_id, 128);
                     ok = ok && mbar_wait(o_full + bf, ph, p.wait_ns);
                     tc_fence_after();
 #pragma unroll
-                    for (int cc = 0; cc < N; cc += 16) {
-                        uint32_t r[16];
-                        tmem_ld16(lane_addr + bf * N + cc, r);
+                    for (int cc = 0; cc < N; cc += JC) {
+                        uint32_t r[JC];
+                        if constexpr (JC == 32)
+                            tmem_ld32(lane_addr + bf * N + cc, r);
+                        else
+                            tmem_ld16(lane_addr + bf * N + cc, r);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 16; i += 4) {
+                        for (int i = 0; i < JC; i += 4) {
                             const float4 fa = *reinterpret_cast<const float4*>(sA + bf * N + cc + i);
                             const float4 fb = *reinterpret_cast<const float4*>(sB + bf * N + cc + i);
                             const uint64_t o0 = mul2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])),
@@ -917,7 +956,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
                 ok = ok && mbar_wait(l_full, sc & 1, p.wait_ns);
                 if (d < N) {
 #pragma unroll
-                    for (int gi = 0; gi < 2; ++gi) {
+                    for (int gi = 0; gi < C::SG; ++gi) {
                         if (C::SPLIT && gi != d / NC) continue;
                         const int col = C::SPLIT ? d % NC : d;
                         const float* s = sL + gi * 4 * NC + col;
@@ -940,7 +979,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
                     sInv[d] = l > 0.f ? 1.f / l : 0.f;
                     if (p.lse && row >= 0) p.lse[row] = l > 0.f ? (m + log2f(l) - kATop) * kALn2 : -INFINITY;
                 }
-                named_bar_sync(3, 128);
+                named_bar_sync(bar_id, 128);
                 if (d < p.D) {
                     __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) + d;
 #pragma unroll
@@ -949,7 +988,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
                         if (row >= 0) out[(int64_t)row * p.D] = __float2bfloat16_rn(acc[i] * sInv[i]);
                     }
                 }
-                named_bar_sync(3, 128);
+                named_bar_sync(bar_id, 128);
             } else {
                 const int slot = 2 * c + (wk.first ? 0 : 1);
                 float* part = parts + slot * attn_part_floats(N);
@@ -964,6 +1003,9 @@ __global__ void __launch_bounds__(kAThreads, 1)
             }
         }
         if (d == 0) reinterpret_cast<AttnHeader*>(p.ws)[c] = hd;
+    } else if constexpr (C::OWN_PROD) {
+        regs_dec<C::R_PROD>();
+        produce();
     }
 
     __syncwarp();
@@ -1054,7 +1096,7 @@ static cudaError_t attn_launch(const CUtensorMap& mk, const CUtensorMap& mv, con
                                cudaStream_t st) {
     cudaError_t e = set_smem_attr((const void*)cache_attn_kernel<N>, AttnCfg<N>::TOTAL);
     if (e != cudaSuccess) return e;
-    cache_attn_kernel<N><<<grid, kAThreads, AttnCfg<N>::TOTAL, st>>>(mk, mv, p);
+    cache_attn_kernel<N><<<grid, AttnCfg<N>::THREADS, AttnCfg<N>::TOTAL, st>>>(mk, mv, p);
     e = cudaGetLastError();
     if (e != cudaSuccess || grid == 1) return e;
     cudaLaunchConfig_t cfg;
