@@ -79,7 +79,7 @@ struct AttnCfg {
     static constexpr bool SPLIT = N > 16;
     static constexpr int NC = SPLIT ? N / SG : N;      // columns of a group
     static constexpr int QB = N == 128 ? 1 : 2;        // query buffers
-    static constexpr int SLOTS = N == 16 ? 9 : (N == 32 ? 8 : 7);
+    static constexpr int SLOTS = N == 16 ? 9 : (N == 32 ? 8 : (N == 64 ? 7 : 6));
     static constexpr int Q_BYTES = 2 * N * 128;        // hi and lo
     static constexpr int P_BYTES = 2 * kASlotBytes;    // hi and lo
     static constexpr int OFF_P = SLOTS * kASlotBytes;
@@ -91,15 +91,15 @@ struct AttnCfg {
     static constexpr int OFF_MB = OFF_W + SG * 4 * NC * 4;             // [SG][2][NC] 8 - M; fade of the tile
     static constexpr int OFF_AL = OFF_MB + SG * NC * 8;                // [SG][NC] fade of the sum
     static constexpr int OFF_END = OFF_AL + SG * NC * 4;               // [SG][NC] keys a column sees
-    static constexpr int OFF_MT = OFF_END + SG * NC * 4;               // [2][N] tile maxima
-    static constexpr int OFF_AB = OFF_MT + 2 * N * 4;                  // [2][2][N] fades of acc and tile
+    static constexpr int OFF_MT = OFF_END + SG * NC * 4;               // [4][N] tile maxima
+    static constexpr int OFF_AB = OFF_MT + 4 * N * 4;                  // [2][2][N] fades of acc and tile
     static constexpr int OFF_L = OFF_AB + 2 * N * 8;                   // [SG][4][NC] sums of the warps
     static constexpr int OFF_MW = OFF_L + SG * 4 * NC * 4;             // [SG][NC] their reference
     static constexpr int OFF_INV = OFF_MW + SG * NC * 4;               // [N] 1 / l
     static constexpr int OFF_ROW = OFF_INV + N * 4;                    // [N] output rows
     static constexpr int OFF_GATHER = OFF_ROW + N * 4;                 // [128] cache rows of a tile's keys
     static constexpr int OFF_BAR = OFF_GATHER + kATile * 4;
-    static constexpr int NBAR = 2 * SLOTS + 2 * kAMeta + 2 * 2 + 5 * 2 + 2 + 1;
+    static constexpr int NBAR = 2 * SLOTS + 2 * kAMeta + 2 * 2 + 3 * 2 + 4 + 2 + 1;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;                // start of the share, TMEM address
     static constexpr int TOTAL = OFF_MISC + 256 + 1024;                // + alignment of the base
     static_assert(TOTAL <= 232448 && kAMeta * 4 <= 128, "shared memory");
@@ -116,7 +116,7 @@ struct AttnCfg {
     static constexpr int QWARPS = OWN_PROD ? 3 : 2, W_QUERY = OWN_PROD ? 1 : 2;
     // registers a thread of each group; their sum is at most what the launch has
     static constexpr int R_LAUNCH = 65536 / THREADS / 8 * 8;
-    static constexpr int R_MMA = N == 128 ? 80 : 56, R_PROD = 56, R_JOIN = N == 128 ? 160 : 104;
+    static constexpr int R_MMA = N == 128 ? 80 : (N == 64 ? 56 : 64), R_PROD = N == 64 ? 56 : 88, R_JOIN = N == 128 ? 160 : 104;
     static constexpr int R_SOFT = N == 128 ? 136 : (N == 64 ? 72 : 112);
     static_assert(R_MMA + SG * R_SOFT + R_JOIN + (OWN_PROD ? R_PROD : 0) <= R_LAUNCH * (THREADS / 128), "register split");
     static_assert(R_MMA < R_LAUNCH && (!OWN_PROD || R_PROD < R_LAUNCH) && R_JOIN > R_LAUNCH && R_SOFT >= R_LAUNCH,
@@ -293,11 +293,10 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
     uint64_t* q_full = meta_empty + kAMeta;     // [2]
     uint64_t* q_empty = q_full + 2;             // [2]
     uint64_t* s_full = q_empty + 2;         // [2] S^T of a tile in TMEM
-    uint64_t* p_full = s_full + 2;          // [2] weights and tile maxima written (and S^T read)
-    uint64_t* o_full = p_full + 2;          // [2] O^T of a tile in TMEM (and the weights read)
+    uint64_t* p_full = s_full + 2;          // [4] weights and tile maxima written (and S^T read)
+    uint64_t* o_full = p_full + 4;          // [2] O^T of a tile in TMEM (and the weights read)
     uint64_t* o_empty = o_full + 2;         // [2] O^T read
-    uint64_t* m_read = o_empty + 2;         // [2] tile maxima read
-    uint64_t* l_full = m_read + 2;          // sums of a segment written
+    uint64_t* l_full = o_empty + 2;         // sums of a segment written
     uint64_t* l_empty = l_full + 1;
     uint64_t* drain = l_empty + 1;
     int64_t* sScan = (int64_t*)(smem + C::OFF_MISC);  // [28]
@@ -320,9 +319,9 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
             mbar_init(q_empty + i, 1 + 4 * C::SG);
             mbar_init(s_full + i, 1);
             mbar_init(p_full + i, C::SPLIT ? 4 * C::SG : 4);
+            mbar_init(p_full + 2 + i, C::SPLIT ? 4 * C::SG : 4);
             mbar_init(o_full + i, 1);
             mbar_init(o_empty + i, 4);
-            mbar_init(m_read + i, 4);
         }
         mbar_init(l_full, 4 * C::SG);
         mbar_init(l_empty, 4);
@@ -604,7 +603,7 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                 const int bf = t & 1, ph = (t >> 1) & 1, seq = 2 * t + 1, sl = seq % SLOTS;
                 ok = ok && mbar_wait(kv_full + sl, (seq / SLOTS) & 1, p.wait_ns);
                 ok = ok && mbar_wait(o_empty + bf, ph ^ 1, p.wait_ns);
-                ok = ok && mbar_wait(p_full + bf, ph, p.wait_ns);
+                ok = ok && mbar_wait(p_full + (t & 3), (t >> 2) & 1, p.wait_ns);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) return;
                 tc_fence_after();
@@ -775,6 +774,9 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                 const bool seen = mv.y != -INFINITY;
                 const bool masked = flag || t * kATile + kATile > least;
                 const uint64_t a2 = pack2(mv.x, mv.x), lv2 = pack2(mv.y, mv.y);
+                // S^T of this tile is done, and with it all products issued before: those of O^T of the tile before
+                // last, so its weights' buffer is free, and so are the maxima of four tiles ago (a tile's O^T waits for the
+                // joining of the tile two before it)
                 ok = ok && mbar_wait(s_full + bf, ph, p.wait_ns);
                 tc_fence_after();
                 const uint32_t s_addr = lane_addr + bf * N;
@@ -798,7 +800,6 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                     }
                     named_bar_sync(bar_id, 128);
                     bool fade = false;
-                    ok = ok && mbar_wait(m_read + bf, ph ^ 1, p.wait_ns);
                     if (wtid < NC) {
                         const float M = fmaxf(fmaxf(sW[wtid], sW[NC + wtid]), fmaxf(sW[2 * NC + wtid], sW[3 * NC + wtid]));
                         const float mn = fmaxf(mw, M);
@@ -806,7 +807,7 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                         sAl[wtid] = fade ? exp2_approx(mw - mn) : 1.f;
                         sSh[wtid] = M == -INFINITY ? kATop : kATop - M;
                         sBe[wtid] = M == -INFINITY ? 0.f : exp2_approx(M - mn);
-                        sMt[bf * N + c0 + wtid] = M;
+                        sMt[(tc & 3) * N + c0 + wtid] = M;
                         mw = mn;
                     }
                     if (named_bar_or(bar_id, 128, fade)) {
@@ -816,7 +817,6 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                             l[i] *= f.x, l[i + 1] *= f.y, l[i + 2] *= f.z, l[i + 3] *= f.w;
                         }
                     }
-                    ok = ok && mbar_wait(o_full + bf, ph ^ 1, p.wait_ns);  // the weights before last are read
                     const float ivs = exp2_approx(-mv.y);
                     const uint64_t iv2 = seen ? pack2(ivs, ivs) : pack2(0.f, 0.f);
 #pragma unroll
@@ -871,7 +871,7 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                 fence_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full + bf);
+                if (lane == 0) mbar_arrive(p_full + (tc & 3));
             }
             // the segment's sums: lanes, then (by the joining warps) warps and groups
             ok = ok && mbar_wait(l_empty, (sc & 1) ^ 1, p.wait_ns);
@@ -915,15 +915,14 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
             if (wk.gr.n > 0) {
                 for (int t = wk.t0; t < wk.t1; ++t, ++tc) {
                     const int bf = tc & 1, ph = (tc >> 1) & 1;
-                    ok = ok && mbar_wait(p_full + bf, ph, p.wait_ns);
+                    // (four barriers: the softmax may be three tiles ahead of the joining)
+                    ok = ok && mbar_wait(p_full + (tc & 3), (tc >> 2) & 1, p.wait_ns);
                     if (d < N) {
-                        const float M = sMt[bf * N + d], mn = fmaxf(m, M);
+                        const float M = sMt[(tc & 3) * N + d], mn = fmaxf(m, M);
                         sA[bf * N + d] = m == -INFINITY ? 0.f : exp2_approx(m - mn);
                         sB[bf * N + d] = M == -INFINITY ? 0.f : exp2_approx(M - mn);
                         m = mn;
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(m_read + bf);
                     named_bar_sync(bar_id, 128);
                     ok = ok && mbar_wait(o_full + bf, ph, p.wait_ns);
                     tc_fence_after();

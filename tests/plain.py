@@ -166,3 +166,35 @@ def random_cache(g, pages, Hkv, page, D, lo_exp=-8, hi_exp=-5):
 
 def to_cuda(codes):
     return torch.from_numpy(codes).cuda().view(torch.float8_e4m3fn)
+
+
+def attention_cuda(q, kc, vc, ks, vs, table, kv_len, q_pos=None, ratio=1, idx=None):
+    """attention()'s output in float64 torch operations on the GPU, for sizes the loops above are too slow for."""
+    B, S, Hq, D = q.shape
+    _, Hkv, page, _ = kc.shape
+    G = Hq // Hkv
+    out = torch.zeros(B, S, Hq, D, dtype=torch.float64, device=q.device)
+    s = torch.arange(S, device=q.device)
+    for b in range(B):
+        n = int(kv_len[b])
+        if n == 0:
+            continue
+        ids = table[b, :-(-n // page)].long()
+        k, v = ((c[ids].double() * sc[ids].double()[..., None, None]).transpose(0, 1).reshape(Hkv, -1, D)[:, :n]
+                for c, sc in ((kc, ks), (vc, vs)))
+        end = torch.full_like(s, n) if q_pos is None else ((int(q_pos[b]) + s + 1) // ratio).clamp(0, n)
+        for a in range(0, S, 128):
+            rows = slice(a, min(S, a + 128))
+            qq = q[b, rows].double().view(-1, Hkv, G, D)
+            if idx is None:
+                sc = torch.einsum("rhgd,hkd->rhgk", qq, k)
+                ok = (torch.arange(n, device=q.device) < end[rows, None])[:, None, None]
+            else:
+                t = idx[b, rows].long()
+                ok = ((t >= 0) & (t < end[rows, None]))[:, None, None]
+                t = t.clamp(0, n - 1)
+                sc = torch.einsum("rhgd,hrkd->rhgk", qq, k[:, t])
+            p = torch.nan_to_num(torch.softmax((sc * D ** -0.5).masked_fill(~ok, float("-inf")), -1))
+            o = torch.einsum("rhgk,hkd->rhgd", p, v) if idx is None else torch.einsum("rhgk,hrkd->rhgd", p, v[:, t])
+            out[b, rows] = o.reshape(-1, Hq, D)
+    return out

@@ -269,6 +269,41 @@ def test_many_short_and_one_long_sequence():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,S,Hq,Hkv,page,L,topk,ratio", [
+    (8, 1, 64, 8, 64, 20000, 0, 1),       # several units a CTA, tens of tiles each
+    (3, 1, 24, 1, 16, 30000, 0, 1),
+    (5, 1, 48, 1, 128, 20000, 0, 1),
+    (2, 1, 128, 1, 32, 20000, 0, 1),
+    (2, 700, 32, 4, 64, 3000, 0, 1),      # chunks over many tiles of rows
+    (1, 900, 20, 4, 16, 2000, 0, 2),
+    (1, 1500, 64, 1, 64, 1024, 512, 4),   # selected prompts
+    (1, 300, 128, 1, 32, 900, 300, 1),
+    (2, 500, 16, 2, 16, 700, 200, 1),
+    (24, 1, 40, 1, 64, 9000, 1500, 1),
+])
+def test_large(B, S, Hq, Hkv, page, L, topk, ratio):
+    g = torch.Generator(device=DEV).manual_seed(B + S)
+    D, MP = 128, -(-L // page)
+    NP = B * MP
+    rnd = lambda *n: torch.randn(*n, generator=g, device=DEV)
+    kc, vc = ((rnd(NP, Hkv, page, D) * 100).clamp(-448, 448).to(torch.float8_e4m3fn) for _ in (0, 1))
+    ks, vs = (torch.exp2(torch.randint(-9, -5, (NP, Hkv), generator=g, device=DEV).float()) for _ in (0, 1))
+    table = torch.randperm(NP, generator=g, device=DEV).to(torch.int32).view(B, MP)
+    lens = torch.tensor([L] + [1 + (i * 7919) % L for i in range(1, B)], dtype=torch.int32, device=DEV)
+    q = rnd(B, S, Hq, D).to(torch.bfloat16)
+    q_pos = lens * ratio - S if S > 1 else None
+    idx = torch.randint(-20, L, (B, S, topk), generator=g, device=DEV).to(torch.int32) if topk else None
+    args = (q, kc, vc, ks, vs, table, lens)
+    got, _ = lidx.lidx_cache_attn(*args, q_pos=q_pos, compress_ratio=ratio, topk_indices=idx)
+    for _ in range(5):  # roles that hand work to each other: a race would show as other bits
+        again, _ = lidx.lidx_cache_attn(*args, q_pos=q_pos, compress_ratio=ratio, topk_indices=idx)
+        assert torch.equal(got, again)
+    _status_ok()
+    want = plain.attention_cuda(*args, q_pos=q_pos, ratio=ratio, idx=idx)
+    assert ((got.double() - want).norm() <= 5e-3 * want.norm()).item()
+
+
+@pytest.mark.gpu
 def test_offsets_past_32_bits():
     """A cache of more than 2^32 bytes whose sequence lies at its end."""
     Hkv, page, D, n = 8, 128, 128, 300
