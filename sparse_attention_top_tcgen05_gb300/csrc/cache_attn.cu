@@ -79,7 +79,7 @@ struct AttnCfg {
     static constexpr bool SPLIT = N > 16;
     static constexpr int NC = SPLIT ? N / SG : N;      // columns of a group
     static constexpr int QB = N == 128 ? 1 : 2;        // query buffers
-    static constexpr int SLOTS = N == 16 ? 9 : (N == 32 ? 8 : (N == 64 ? 7 : 6));
+    static constexpr int SLOTS = N <= 32 ? 8 : (N == 64 ? 7 : 6);
     static constexpr int Q_BYTES = 2 * N * 128;        // hi and lo
     static constexpr int P_BYTES = 2 * kASlotBytes;    // hi and lo
     static constexpr int OFF_P = SLOTS * kASlotBytes;
@@ -87,10 +87,9 @@ struct AttnCfg {
     static constexpr int OFF_META = OFF_Q + QB * Q_BYTES;              // [kAMeta][128] float2
     static constexpr int OFF_FLAG = OFF_META + kAMeta * kATile * 8;    // [kAMeta] four bytes, one a producer
     static constexpr int OFF_QS = OFF_FLAG + 128;                      // [2][N] query scales
-    static constexpr int OFF_W = OFF_QS + 2 * N * 4;                   // [SG][4][NC] warp maxima
-    static constexpr int OFF_MB = OFF_W + SG * 4 * NC * 4;             // [SG][2][NC] 8 - M; fade of the tile
-    static constexpr int OFF_AL = OFF_MB + SG * NC * 8;                // [SG][NC] fade of the sum
-    static constexpr int OFF_END = OFF_AL + SG * NC * 4;               // [SG][NC] keys a column sees
+    static constexpr int OFF_W = OFF_QS + 2 * N * 4;                   // [2][SG][4][NC] warp maxima of a tile
+    static constexpr int OFF_MB = OFF_W + 2 * SG * 4 * NC * 4;         // [4 SG][3][NC] of a warp: 8 - M, fades
+    static constexpr int OFF_END = OFF_MB + 4 * SG * 3 * NC * 4;       // [SG][NC] keys a column sees
     static constexpr int OFF_MT = OFF_END + SG * NC * 4;               // [4][N] tile maxima
     static constexpr int OFF_AB = OFF_MT + 4 * N * 4;                  // [2][2][N] fades of acc and tile
     static constexpr int OFF_L = OFF_AB + 2 * N * 8;                   // [SG][4][NC] sums of the warps
@@ -103,7 +102,7 @@ struct AttnCfg {
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;                // start of the share, TMEM address
     static constexpr int TOTAL = OFF_MISC + 256 + 1024;                // + alignment of the base
     static_assert(TOTAL <= 232448 && kAMeta * 4 <= 128, "shared memory");
-    static_assert(OFF_QS % 16 == 0 && OFF_MB % 16 == 0 && OFF_AL % 16 == 0 && OFF_END % 16 == 0 && OFF_AB % 16 == 0 && OFF_W % 16 == 0 &&
+    static_assert(OFF_QS % 16 == 0 && OFF_MB % 16 == 0 && OFF_END % 16 == 0 && OFF_AB % 16 == 0 && OFF_W % 16 == 0 &&
                       OFF_GATHER % 16 == 0,
                   "16-byte reads");
     static constexpr int TMEM = 4 * N;                                 // columns: two tiles of S and of O
@@ -736,32 +735,41 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
         const int grp = (warp - C::W_SOFT) >> 2, wtid = tid & 127, wg_warp = warp & 3;
         const int c0 = C::SPLIT ? grp * NC : 0;
         const uint32_t bar_id = 1 + grp;
-        float* const sW = (float*)(smem + C::OFF_W) + grp * 4 * NC;
-        float* const sSh = (float*)(smem + C::OFF_MB) + grp * 2 * NC;  // 8 - M
-        float* const sBe = sSh + NC;                                    // fade of the tile
-        float* const sAl = (float*)(smem + C::OFF_AL) + grp * NC;
+        float* const sW = (float*)(smem + C::OFF_W) + grp * 4 * NC;  // + parity of the group's tiles * SG * 4 * NC
+        float* const sSh = (float*)(smem + C::OFF_MB) + (grp * 4 + wg_warp) * 3 * NC;  // 8 - M, of this warp alone
+        float* const sBe = sSh + NC;                                                   // fade of the tile
+        float* const sAl = sBe + NC;                                                   // fade of the sum
         int* const sEnd = (int*)(smem + C::OFF_END) + grp * NC;
         const uint32_t lane_addr = tmem + ((uint32_t)(wg_warp * 32) << 16) + c0;
+        constexpr int MC = (NC + 31) / 32;  // columns of a lane where a warp looks at all NC maxima
         bool ok = true;
-        int tc = 0, sc = 0;
+        int tc = 0, sc = 0, odd = 0;
+        if (p.idx) {
+            if (wtid < NC) sEnd[wtid] = INT_MAX;
+            named_bar_sync(bar_id, 128);
+        }
         while (wk.next(p)) {
             if (wk.gr.n == 0) continue;
             const int qb = sc % QB;
-            // keys each column sees
-            const int st0 = wk.gr.st * p.TS;
-            named_bar_sync(bar_id, 128);  // the last segment's are read
-            if (wtid < NC) {
-                const int st = attn_token(p, c0 + wtid);
-                sEnd[wtid] = p.idx ? INT_MAX : (st < p.TS && st0 + st < p.S ? attn_end(p, wk.gr.b, st0 + st) : 0);
+            int least = INT_MAX;  // keys that every column sees
+            if (!p.idx) {
+                const int st0 = wk.gr.st * p.TS;
+                named_bar_sync(bar_id, 128);  // the last segment's ends are read
+                if (wtid < NC) {
+                    const int st = attn_token(p, c0 + wtid);
+                    sEnd[wtid] = st < p.TS && st0 + st < p.S ? attn_end(p, wk.gr.b, st0 + st) : 0;
+                }
+                least = attn_end(p, wk.gr.b, st0);
+                named_bar_sync(bar_id, 128);
             }
-            const int least = p.idx ? INT_MAX : attn_end(p, wk.gr.b, st0);
-            named_bar_sync(bar_id, 128);
             ok = ok && mbar_wait(q_full + qb, (sc / QB) & 1, p.wait_ns);
             const float* const qs = sQs + qb * N + c0;
             float l[NC];
 #pragma unroll
             for (int i = 0; i < NC; ++i) l[i] = 0.f;
-            float mw = -INFINITY;  // of column wtid
+            float mw[MC];  // running maxima of columns lane, lane + 32, the same in the group's four warps
+#pragma unroll
+            for (int i = 0; i < MC; ++i) mw[i] = -INFINITY;
             for (int t = wk.t0; t < wk.t1; ++t, ++tc) {
                 if (!C::SPLIT && (tc & 1) != grp) continue;
                 const int bf = tc & 1, ph = (tc >> 1) & 1, ms = tc % kAMeta;
@@ -782,6 +790,8 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                 const uint32_t s_addr = lane_addr + bf * N;
                 uint8_t* const prow = sP + bf * C::P_BYTES + wtid * 128;
 
+                float* const sWt = sW + odd * C::SG * 4 * NC;
+                odd ^= 1;
                 auto one_tile = [&](auto mask_c) {
                     constexpr bool MASK = decltype(mask_c)::value;
                     float x[CH];
@@ -794,23 +804,30 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                         if (lane == 0) {
 #pragma unroll
                             for (int i = 0; i < CH; i += 4)
-                                *reinterpret_cast<float4*>(sW + wg_warp * NC + cc + i) =
+                                *reinterpret_cast<float4*>(sWt + wg_warp * NC + cc + i) =
                                     make_float4(top[i], top[i + 1], top[i + 2], top[i + 3]);
                         }
                     }
                     named_bar_sync(bar_id, 128);
+                    // every warp takes the tile's maxima by itself: no second barrier.  (The next tile's go to the other
+                    // half of sW, and a warp reads these before it reaches the next tile's barrier.)
                     bool fade = false;
-                    if (wtid < NC) {
-                        const float M = fmaxf(fmaxf(sW[wtid], sW[NC + wtid]), fmaxf(sW[2 * NC + wtid], sW[3 * NC + wtid]));
-                        const float mn = fmaxf(mw, M);
-                        fade = mn > mw && mw != -INFINITY;
-                        sAl[wtid] = fade ? exp2_approx(mw - mn) : 1.f;
-                        sSh[wtid] = M == -INFINITY ? kATop : kATop - M;
-                        sBe[wtid] = M == -INFINITY ? 0.f : exp2_approx(M - mn);
-                        sMt[(tc & 3) * N + c0 + wtid] = M;
-                        mw = mn;
+#pragma unroll
+                    for (int i = 0; i < MC; ++i) {
+                        const int col = lane + 32 * i;
+                        if (col < NC) {
+                            const float M = fmaxf(fmaxf(sWt[col], sWt[NC + col]), fmaxf(sWt[2 * NC + col], sWt[3 * NC + col]));
+                            const float mn = fmaxf(mw[i], M);
+                            const bool f = mn > mw[i] && mw[i] != -INFINITY;
+                            sAl[col] = f ? exp2_approx(mw[i] - mn) : 1.f;
+                            sSh[col] = M == -INFINITY ? kATop : kATop - M;
+                            sBe[col] = M == -INFINITY ? 0.f : exp2_approx(M - mn);
+                            if (wg_warp == 0) sMt[(tc & 3) * N + c0 + col] = M;
+                            mw[i] = mn;
+                            fade = fade || f;
+                        }
                     }
-                    if (named_bar_or(bar_id, 128, fade)) {
+                    if (__any_sync(0xffffffffu, fade)) {  // (orders the writes above for the warp, too)
 #pragma unroll
                         for (int i = 0; i < NC; i += 4) {
                             const float4 f = *reinterpret_cast<const float4*>(sAl + i);
@@ -883,7 +900,11 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                 const float sum = warp_sum_columns(v, lane);
                 if (lane < CH) sL[(grp * 4 + wg_warp) * NC + cc + lane] = sum;
             }
-            if (wtid < NC) sMw[grp * NC + wtid] = mw;
+            if (wg_warp == 0) {
+#pragma unroll
+                for (int i = 0; i < MC; ++i)
+                    if (lane + 32 * i < NC) sMw[grp * NC + lane + 32 * i] = mw[i];
+            }
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(l_full);

@@ -373,20 +373,6 @@ __device__ __forceinline__ float warp_max(float x) {
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
-// The same; returns whether any of the threads passed a true value.
-__device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t nthreads, bool v) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)v), "r"(id), "r"(nthreads)
-        : "memory");
-    return r != 0;
-}
-
 // Registers of this warpgroup (all four warps execute it).
 template <int R>
 __device__ __forceinline__ void regs_inc() {
