@@ -52,8 +52,6 @@ struct AttnParams {
     int TS, ST;            // query tokens of a unit; units of a sequence
     int page_shift;        // page = 1 << page_shift
     uint32_t inv_g;        // ceil(2^16 / G): n / G = n * inv_g >> 16 for n < 128
-    const uint8_t* kc;     // the caches, for gathered keys
-    const uint8_t* vc;
     float scale_log2;      // softmax_scale * log2(e)
     uint16_t* out;
     float* lse;            // nullable
@@ -478,10 +476,8 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                 for (int seq = max(0, 2 * tc - SLOTS); seq < 2 * tc; ++seq)
                     mbar_wait(kv_full + seq % SLOTS, (seq / SLOTS) & 1, p.wait_ns);
         } else {
-            // Selected keys: 16-byte asynchronous copies, eight lanes a row of 128 bytes, written in the
-            // 128-byte swizzle TMA would use; unseen keys and dims past D become zeros.  A producer has NQ quarters
-            // of 32 keys of each tile, a lane one key of each.  (One warp for the whole tile took 9.9k cycles a
-            // tile, a TMA gather, whose 64 instructions the lanes issue one after the other, 11.9k.)
+            // Selected keys: TMA gathers of four rows.  A producer has NQ quarters of 32 keys of each tile, a lane one key of
+            // each.  Unseen keys gather row 0 with the other three (or nothing); the softmax clears their V rows.
             constexpr int NQ = 4 / C::PRODUCERS;
             auto keys = [&](const Ref& r, int (&t)[NQ]) {
                 const int32_t* src = p.idx + r.row * p.topk;
@@ -489,28 +485,14 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                 for (int i = 0; i < NQ; ++i) {
                     const int k = r.tile * kATile + 32 * (pw + i) + lane;
                     t[i] = r.live && k < p.topk ? src[k] : -1;
-                    t[i] = t[i] < r.limit ? t[i] : -1;
                 }
             };
             auto pages = [&](const Ref& r, const int (&t)[NQ], int (&pid)[NQ]) {
                 const int32_t* tab = p.table + (int64_t)r.b * p.max_pages;
 #pragma unroll
-                for (int i = 0; i < NQ; ++i) pid[i] = t[i] >= 0 ? tab[t[i] >> p.page_shift] : -1;
+                for (int i = 0; i < NQ; ++i) pid[i] = t[i] >= 0 && t[i] < r.limit ? tab[t[i] >> p.page_shift] : -1;
             };
             int* const sRows = (int*)(smem + C::OFF_GATHER) + 32 * pw;
-            const int sub = lane & 7, part = lane >> 3;  // chunk of a row; rows 8 part .. 8 part + 7 of a quarter
-            const uint32_t in_row = sub * 16 < p.D ? 16 : 0;
-            const uint8_t* const kc = p.kc + sub * 16;
-            const uint8_t* const vc = p.vc + sub * 16;
-            // this warp's copies of tile t have landed: hand them on
-            auto landed = [&](int t) {
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(kv_full + (2 * t) % SLOTS);
-                    mbar_arrive(kv_full + (2 * t + 1) % SLOTS);
-                }
-            };
             Ref r0 = next_ref();
             int t0[NQ], t1[NQ], t2[NQ], pid0[NQ], pid1[NQ];
             keys(r0, t0);
@@ -534,25 +516,23 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                 claim();
                 if (!ok) break;
                 __syncwarp();
-                const int sk = 2 * tc, ms = tc % kAMeta;
-                const uint32_t at = smem_u32(smem) + pw * 4096 + part * 1024;
-                const uint32_t dk = at + (sk % SLOTS) * kASlotBytes, dv = at + ((sk + 1) % SLOTS) * kASlotBytes;
-#pragma unroll
-                for (int q = 0; q < NQ; ++q) {
-                    const int4 ra = *reinterpret_cast<const int4*>(sRows + 32 * q + 8 * part);
-                    const int4 rb = *reinterpret_cast<const int4*>(sRows + 32 * q + 8 * part + 4);
-                    const int r[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t to = q * 4096 + i * 128 + ((sub ^ i) << 4);
-                        const int64_t from = (int64_t)max(r[i], 0) * p.D;
-                        const uint32_t n = r[i] >= 0 ? in_row : 0;
-                        // (a chunk past D reads nothing; its address stays inside the row before it)
-                        cp_async16(dk + to, n ? kc + from : p.kc, n);
-                        cp_async16(dv + to, n ? vc + from : p.vc, n);
-                    }
+                const int sk = 2 * tc, ms = tc % kAMeta, s0 = sk % SLOTS, s1 = (sk + 1) % SLOTS;
+                // four keys a lane
+                const int4 r = *reinterpret_cast<const int4*>(sRows + 4 * (lane & (8 * NQ - 1)));
+                const bool any = lane < 8 * NQ && (r.x & r.y & r.z & r.w) >= 0;  // one of them is seen
+                const uint32_t bytes = 512u * __popc(__ballot_sync(0xffffffffu, any));
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(kv_full + s0, bytes);
+                    mbar_arrive_expect_tx(kv_full + s1, bytes);
                 }
-                cp_async_commit();
+                __syncwarp();
+                if (any) {
+                    const uint32_t to = pw * 4096 + lane * 512;
+                    tma_gather4(smem + s0 * kASlotBytes + to, &tmk, kv_full + s0, 0, max(r.x, 0), max(r.y, 0),
+                                max(r.z, 0), max(r.w, 0));
+                    tma_gather4(smem + s1 * kASlotBytes + to, &tmv, kv_full + s1, 0, max(r.x, 0), max(r.y, 0),
+                                max(r.z, 0), max(r.w, 0));
+                }
 #pragma unroll
                 for (int i = 0; i < NQ; ++i) {
                     sMeta[ms * kATile + 32 * (pw + i) + lane] =
@@ -563,10 +543,6 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(meta_full + ms);
-                if (tc > 0) {  // two tiles in flight
-                    cp_async_wait<1>();
-                    landed(tc - 1);
-                }
                 r0 = r1;
                 r1 = r2;
 #pragma unroll
@@ -577,8 +553,9 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                 }
                 ++tc;
             }
-            cp_async_wait<0>();  // also where a wait ran out: no copy outlives the block
-            if (ok && tc > 0) landed(tc - 1);
+            if (!ok && !p.debug_stall)  // loads in flight end before the memory is given up
+                for (int seq = max(0, 2 * tc - SLOTS); seq < 2 * tc; ++seq)
+                    mbar_wait(kv_full + seq % SLOTS, (seq / SLOTS) & 1, p.wait_ns);
         }
     };
 
@@ -1197,8 +1174,6 @@ int lidx_cache_attn(const void* q, const int64_t* qs, const void* k_cache, const
     p.ST = (int)((S + p.TS - 1) / p.TS);
     p.page_shift = page == 16 ? 4 : (page == 32 ? 5 : (page == 64 ? 6 : 7));
     p.inv_g = (65536 + p.G - 1) / p.G;
-    p.kc = (const uint8_t*)k_cache;
-    p.vc = (const uint8_t*)v_cache;
     p.scale_log2 = softmax_scale * 1.44269504088896341f;
     p.out = (uint16_t*)out;
     p.lse = lse;
@@ -1212,8 +1187,9 @@ int lidx_cache_attn(const void* q, const int64_t* qs, const void* k_cache, const
     if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u)) return LIDX_ERR_WORKSPACE;
     p.ws = (uint8_t*)workspace;
     CUtensorMap mk, mv;
-    if (attn_cache_map(&mk, k_cache, num_pages * Hkv * page, D, page) ||
-        attn_cache_map(&mv, v_cache, num_pages * Hkv * page, D, page))
+    const int box = topk_indices ? 1 : page;  // rows of a copy
+    if (attn_cache_map(&mk, k_cache, num_pages * Hkv * page, D, box) ||
+        attn_cache_map(&mv, v_cache, num_pages * Hkv * page, D, box))
         return LIDX_ERR_CUDA;
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
