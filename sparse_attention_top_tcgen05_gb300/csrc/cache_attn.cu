@@ -22,70 +22,28 @@
 // sees.  All tiles form one line that is cut into equal shares, one a CTA, found on the device from the
 // lengths.  A CTA that holds only part of a unit writes (m, l, acc) to the workspace, and cache_attn_join_kernel
 // joins the parts in order.  No atomics: two calls give the same bits.
-#include <cuda_bf16.h>
-#include <cuda_runtime.h>
-#include <math.h>
-#include <stdint.h>
 #include <string.h>
 
-#include <climits>
-#include <type_traits>
-
-#include "cache.cuh"
-#include "kernels.h"
-#include "lidx.h"
-#include "ptx.cuh"
+#include "cache_attn.cuh"
 
 namespace lidx {
 
-struct AttnParams {
-    const uint16_t* q;
-    int64_t qs[3];
-    const float* ks;
-    const float* vs;
-    const int32_t* table;
-    const int32_t* kv_len;
-    const int32_t* q_pos;  // nullable
-    const int32_t* idx;    // nullable
-    int64_t num_pages;
-    int B, S, Hq, Hkv, G, D, page, max_pages, ratio, topk;
-    int TS, ST;            // query tokens of a unit; units of a sequence
-    int page_shift;        // page = 1 << page_shift
-    uint32_t inv_g;        // ceil(2^16 / G): n / G = n * inv_g >> 16 for n < 128
-    float scale_log2;      // softmax_scale * log2(e)
-    uint16_t* out;
-    float* lse;            // nullable
-    uint8_t* ws;
-    uint64_t wait_ns;
-    int debug_stall;       // 1: the producer issues nothing (failure-detection tests)
-};
-
-constexpr int kATile = 128;                     // keys of a tile
-constexpr int kASlotBytes = kATile * 128;       // one K or V tile: 128 bytes a key (zero past D)
-constexpr int kAMeta = 5;                       // stages of per-key scales
-constexpr float kATop = 8.f;                    // weights are scaled to 2^8
-constexpr float kALn2 = 0.693147180559945309f;
-
-// Shared memory of the configuration with N columns.
+// Configuration of the kernel with N columns, N = 16 or 32.
 template <int N>
 struct AttnCfg {
-    // Softmax groups of four warps.  At N = 16 two groups take the tiles in turn; from N = 32 on the groups share each
-    // tile's columns, 16 a group, so that a thread keeps its 16 scores and sums in registers (at N = 64 two groups of
-    // 64 columns took 7.7k cycles a tile, most of it exposed latency and spills).  N = 128 has two groups of 64 columns:
-    // four groups would not leave the registers that joining 128 columns takes.
-    static constexpr int SG = N == 64 ? 4 : 2;
-    static constexpr bool SPLIT = N > 16;
-    static constexpr int NC = SPLIT ? N / SG : N;      // columns of a group
-    static constexpr int QB = N == 128 ? 1 : 2;        // query buffers
-    static constexpr int SLOTS = N <= 32 ? 8 : (N == 64 ? 7 : 6);
+    static_assert(N == 16 || N == 32, "columns");
+    // Two softmax groups of four warps, 16 columns each.  At N = 16 they take the tiles in turn, at N = 32 they share each
+    // tile's columns: a thread keeps its 16 scores and sums in registers either way.
+    static constexpr bool SPLIT = N == 32;
+    static constexpr int SG = 2, NC = 16, QB = 2, SLOTS = 8;
     static constexpr int Q_BYTES = 2 * N * 128;        // hi and lo
     static constexpr int P_BYTES = 2 * kASlotBytes;    // hi and lo
     static constexpr int OFF_P = SLOTS * kASlotBytes;
     static constexpr int OFF_Q = OFF_P + 2 * P_BYTES;
-    static constexpr int OFF_META = OFF_Q + QB * Q_BYTES;              // [kAMeta][128] float2
-    static constexpr int OFF_FLAG = OFF_META + kAMeta * kATile * 8;    // [kAMeta] four bytes, one a producer
-    static constexpr int OFF_QS = OFF_FLAG + 128;                      // [2][N] query scales
-    static constexpr int OFF_W = OFF_QS + 2 * N * 4;                   // [2][SG][4][NC] warp maxima of a tile
+    static constexpr int OFF_META = OFF_Q + QB * Q_BYTES;              // [3][kAMeta][128] of the keys
+    static constexpr int OFF_SEEN = OFF_META + 3 * kAMeta * kATile * 4;  // [kAMeta][4], then [kAMeta] flags
+    static constexpr int OFF_QS = OFF_SEEN + 128;                      // [QB][N] query scales
+    static constexpr int OFF_W = OFF_QS + QB * N * 4;                  // [2][SG][4][NC] warp maxima of a tile
     static constexpr int OFF_MB = OFF_W + 2 * SG * 4 * NC * 4;         // [4 SG][3][NC] of a warp: 8 - M, fades
     static constexpr int OFF_END = OFF_MB + 4 * SG * 3 * NC * 4;       // [SG][NC] keys a column sees
     static constexpr int OFF_MT = OFF_END + SG * NC * 4;               // [4][N] tile maxima
@@ -98,129 +56,20 @@ struct AttnCfg {
     static constexpr int OFF_BAR = OFF_GATHER + kATile * 4;
     static constexpr int NBAR = 2 * SLOTS + 2 * kAMeta + 2 * 2 + 3 * 2 + 4 + 2 + 1;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;                // start of the share, TMEM address
-    static constexpr int TOTAL = OFF_MISC + 256 + 1024;                // + alignment of the base
-    static_assert(TOTAL <= 232448 && kAMeta * 4 <= 128, "shared memory");
+    static constexpr int TOTAL = OFF_MISC + 288 + 1024;                // + alignment of the base
+    static_assert(TOTAL <= 232448 && kAMeta * 20 <= 128, "shared memory");
     static_assert(OFF_QS % 16 == 0 && OFF_MB % 16 == 0 && OFF_END % 16 == 0 && OFF_AB % 16 == 0 && OFF_W % 16 == 0 &&
-                      OFF_GATHER % 16 == 0,
+                      OFF_GATHER % 16 == 0 && OFF_MISC % 8 == 0,
                   "16-byte reads");
     static constexpr int TMEM = 4 * N;                                 // columns: two tiles of S and of O
-    // Warpgroups: MMA and queries; SG of softmax; joining; up to N = 64 four producers (N = 128, whose joining group holds
-    // 128 sums a thread, has no registers for them: one warp of the first group produces).
-    static constexpr bool OWN_PROD = N < 128;
-    static constexpr int THREADS = 128 * (2 + SG + (OWN_PROD ? 1 : 0));
-    static constexpr int W_SOFT = 4, W_JOIN = 4 + 4 * SG;  // first warps
-    static constexpr int PRODUCERS = OWN_PROD ? 4 : 1, W_PROD = OWN_PROD ? W_JOIN + 4 : 1;
-    static constexpr int QWARPS = OWN_PROD ? 3 : 2, W_QUERY = OWN_PROD ? 1 : 2;
-    // registers a thread of each group; their sum is at most what the launch has
-    static constexpr int R_LAUNCH = 65536 / THREADS / 8 * 8;
-    static constexpr int R_MMA = N == 128 ? 80 : (N == 64 ? 56 : 64), R_PROD = N == 64 ? 56 : 88, R_JOIN = N == 128 ? 160 : 104;
-    static constexpr int R_SOFT = N == 128 ? 136 : (N == 64 ? 72 : 112);
-    static_assert(R_MMA + SG * R_SOFT + R_JOIN + (OWN_PROD ? R_PROD : 0) <= R_LAUNCH * (THREADS / 128), "register split");
-    static_assert(R_MMA < R_LAUNCH && (!OWN_PROD || R_PROD < R_LAUNCH) && R_JOIN > R_LAUNCH && R_SOFT >= R_LAUNCH,
-                  "groups that give registers, groups that take them");
+    // Warpgroups: MMA and queries; two of softmax; joining; producers.
+    static constexpr int THREADS = 640, PRODUCERS = 4, QWARPS = 3;
+    static constexpr int W_QUERY = 1, W_SOFT = 4, W_JOIN = 12, W_PROD = 16;  // first warps
+    // registers a thread of each group: their sum is at most what the launch has
+    static constexpr int R_LAUNCH = 96, R_MMA = 64, R_SOFT = 112, R_JOIN = 104, R_PROD = 88;
+    static_assert(R_LAUNCH == 65536 / THREADS / 8 * 8 && R_MMA + SG * R_SOFT + R_JOIN + R_PROD <= R_LAUNCH * 5,
+                  "register split");
 };
-
-// Row (b, s) sees keys [0, end).
-__device__ __forceinline__ int attn_end(const AttnParams& p, int b, int s) {
-    int n = p.kv_len[b];
-    const int cap = p.max_pages * p.page;
-    n = n < 0 ? 0 : (n > cap ? cap : n);
-    if (p.q_pos) {
-        const int64_t seen = (int64_t)p.q_pos[b] + s + 1;  // below 2^32
-        const uint32_t e = seen > 0 ? (uint32_t)seen / (uint32_t)p.ratio : 0;
-        n = e < (uint32_t)n ? (int)e : n;
-    }
-    return n;
-}
-
-// ---- the line of tiles.  Group g = (sequence, tile of query tokens); its Hkv units follow each other.
-struct AttnGroup {
-    int b, st, limit;  // limit: keys its last row sees
-    int n;             // tiles of a unit (0: nothing to see)
-    int w;             // places of a unit on the line: at least one
-};
-__device__ __forceinline__ void attn_group_size(const AttnParams& p, AttnGroup& r) {
-    if (!p.idx) r.limit = attn_end(p, r.b, min(r.st * p.TS + p.TS, p.S) - 1);  // (selected keys: the producers look)
-    r.n = ((p.idx ? p.topk : r.limit) + kATile - 1) / kATile;
-    r.w = max(r.n, 1);
-}
-__device__ __forceinline__ AttnGroup attn_group(const AttnParams& p, int g) {
-    AttnGroup r;
-    r.b = g / p.ST;
-    r.st = g - r.b * p.ST;
-    r.limit = 0;
-    attn_group_size(p, r);
-    return r;
-}
-// Query token of column n within a unit.
-__device__ __forceinline__ int attn_token(const AttnParams& p, int n) { return (int)(n * p.inv_g >> 16); }
-__device__ __forceinline__ int64_t attn_share(int64_t W, int c, int n) { return W * c / n; }
-
-// The segments [t0, t1) of units that make up a CTA's share; every role walks them alike.
-struct AttnWalk {
-    int64_t pos, end;   // places not walked yet
-    int64_t unit_end;   // place behind the segment's unit
-    int g, h, t0, t1;
-    AttnGroup gr;
-    bool first, fresh;  // first: the segment is the CTA's first
-
-    // pos lies in group g, whose first unit's place is base
-    __device__ void begin(const AttnParams& p, int64_t pos_, int64_t end_, int g_, int64_t base) {
-        pos = pos_;
-        end = end_;
-        g = g_;
-        t1 = 0;
-        fresh = true;
-        if (pos >= end) return;
-        gr = attn_group(p, g);
-        const int64_t at = pos - base;
-        h = at < INT_MAX ? (int)((uint32_t)at / (uint32_t)gr.w) : (int)(at / gr.w);
-        t0 = (int)(at - (int64_t)h * gr.w);
-    }
-    __device__ bool next(const AttnParams& p) {
-        if (pos >= end) return false;
-        first = fresh;
-        if (fresh) {
-            fresh = false;
-        } else {
-            t0 = 0;
-            if (++h == p.Hkv) {
-                h = 0;
-                ++g;
-                if (++gr.st == p.ST) gr.st = 0, ++gr.b;
-                attn_group_size(p, gr);
-            }
-        }
-        unit_end = pos - t0 + gr.w;
-        const int64_t e = unit_end < end ? unit_end : end;
-        t1 = t0 + (int)(e - pos);
-        pos = e;
-        return true;
-    }
-};
-
-// Workspace: a header for each CTA, then two parts for each (its first segment, its last).
-struct AttnHeader {
-    // last > 0: the CTA holds the first tiles (in part `slot`) of a unit that ends with CTA `last`'s first segment
-    int32_t last, g, h, slot;
-};
-__host__ __device__ inline size_t attn_part_floats(int N) { return (size_t)N * 128 + 2 * N; }
-__host__ __device__ inline size_t attn_ws_bytes(int N, int grid) {
-    return (size_t)grid * sizeof(AttnHeader) + (size_t)grid * 2 * attn_part_floats(N) * 4;
-}
-
-// Two floats (at most 256 in size) -> e4m3 hi and lo pairs in the low halves.
-__device__ __forceinline__ void split_e4m3(float x0, float x1, uint32_t& hi, uint32_t& lo) {
-    uint32_t f, b, r;
-    uint16_t h, l;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(f) : "f"(x1), "f"(x0));
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(f));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"(h));
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(f), "r"(b));  // exact
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(r));
-    hi = h;
-    lo = l;
-}
 
 // Sums over the warp's lanes of 32 columns: lane i returns column i's.
 __device__ __forceinline__ float warp_sum_columns(float (&v)[32], int lane) {
@@ -276,19 +125,26 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t* const sP = smem + C::OFF_P;
     uint8_t* const sQ = smem + C::OFF_Q;
-    float2* const sMeta = (float2*)(smem + C::OFF_META);
-    uint32_t* const sFlag = (uint32_t*)(smem + C::OFF_FLAG);  // not 0: a key of the tile is not seen
-    float* const sQs = (float*)(smem + C::OFF_QS);
     float* const sMt = (float*)(smem + C::OFF_MT);
     float* const sL = (float*)(smem + C::OFF_L);
     float* const sMw = (float*)(smem + C::OFF_MW);
     uint64_t* bars = (uint64_t*)(smem + C::OFF_BAR);
-    uint64_t* kv_full = bars;               // [SLOTS] K or V tile landed
-    uint64_t* kv_empty = kv_full + SLOTS;   // [SLOTS] its product is done
-    uint64_t* meta_full = kv_empty + SLOTS;     // [kAMeta] scales of a tile's keys written
-    uint64_t* meta_empty = meta_full + kAMeta;  // [kAMeta] read by the softmax warps
-    uint64_t* q_full = meta_empty + kAMeta;     // [2]
-    uint64_t* q_empty = q_full + 2;             // [2]
+    AttnPipe x;
+    x.kv = smem;
+    x.q = sQ;
+    x.q_scale = (float*)(smem + C::OFF_QS);
+    x.key_a = (float*)(smem + C::OFF_META);
+    x.key_lv = x.key_a + kAMeta * kATile;
+    x.key_iv = x.key_lv + kAMeta * kATile;
+    x.seen = (uint32_t*)(smem + C::OFF_SEEN);
+    x.flag = x.seen + 4 * kAMeta;
+    x.rows = (int*)(smem + C::OFF_GATHER);
+    uint64_t* const kv_full = x.kv_full = bars;
+    uint64_t* const kv_empty = x.kv_empty = kv_full + SLOTS;
+    uint64_t* const meta_full = x.meta_full = kv_empty + SLOTS;
+    uint64_t* const meta_empty = x.meta_empty = meta_full + kAMeta;
+    uint64_t* const q_full = x.q_full = meta_empty + kAMeta;
+    uint64_t* const q_empty = x.q_empty = q_full + 2;
     uint64_t* s_full = q_empty + 2;         // [2] S^T of a tile in TMEM
     uint64_t* p_full = s_full + 2;          // [4] weights and tile maxima written (and S^T read)
     uint64_t* o_full = p_full + 4;          // [2] O^T of a tile in TMEM (and the weights read)
@@ -296,10 +152,8 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
     uint64_t* l_full = o_empty + 2;         // sums of a segment written
     uint64_t* l_empty = l_full + 1;
     uint64_t* drain = l_empty + 1;
-    int64_t* sScan = (int64_t*)(smem + C::OFF_MISC);  // [28]
-    int64_t* sBase = sScan + 28;
-    int* sGroup = (int*)(sBase + 1);
-    uint32_t* tmem_slot = (uint32_t*)(sGroup + 1);
+    uint32_t* tmem_slot = (uint32_t*)(smem + C::OFF_MISC);
+    int64_t* const scan = (int64_t*)(smem + C::OFF_MISC + 8);  // [34]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
@@ -309,18 +163,18 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
         }
         for (int i = 0; i < kAMeta; ++i) {
             mbar_init(meta_full + i, p.idx ? C::PRODUCERS : 1);
-            mbar_init(meta_empty + i, C::SPLIT ? 4 * C::SG : 4);
+            mbar_init(meta_empty + i, C::SPLIT ? 8 : 4);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + i, C::QWARPS);
-            mbar_init(q_empty + i, 1 + 4 * C::SG);
+            mbar_init(q_empty + i, 1 + 8);
             mbar_init(s_full + i, 1);
-            mbar_init(p_full + i, C::SPLIT ? 4 * C::SG : 4);
-            mbar_init(p_full + 2 + i, C::SPLIT ? 4 * C::SG : 4);
+            mbar_init(p_full + i, C::SPLIT ? 8 : 4);
+            mbar_init(p_full + 2 + i, C::SPLIT ? 8 : 4);
             mbar_init(o_full + i, 1);
             mbar_init(o_empty + i, 4);
         }
-        mbar_init(l_full, 4 * C::SG);
+        mbar_init(l_full, 8);
         mbar_init(l_empty, 4);
         mbar_init(drain, 1);
         fence_mbar_init();
@@ -331,233 +185,12 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
         tmem_alloc(tmem_slot, C::TMEM);
         tmem_relinquish();
     }
-
-    // ---- this CTA's share of the line
-    const int c = blockIdx.x;
-    int nc = gridDim.x;  // CTAs with a share
-    int64_t W, pos0, pos1, base0 = 0;
-    int g0 = 0;
-    if (p.idx) {
-        // every unit has the same places
-        const int64_t w = (int64_t)((p.topk + kATile - 1) / kATile) * p.Hkv;
-        W = w * p.B * p.ST;
-        nc = W < nc ? (int)W : nc;
-        pos0 = attn_share(W, min(c, nc), nc);
-        pos1 = attn_share(W, min(c + 1, nc), nc);
-        g0 = (int)(pos0 / w);
-        base0 = g0 * w;
-    } else {
-        const int NG = p.B * p.ST, per = (NG + C::THREADS - 1) / C::THREADS;
-        const int ga = min(tid * per, NG), gz = min(ga + per, NG);
-        int64_t sum = 0;
-        for (int g = ga; g < gz; ++g) sum += (int64_t)attn_group(p, g).w * p.Hkv;
-        int64_t incl = sum;
-#pragma unroll
-        for (int i = 1; i < 32; i <<= 1) {
-            const int64_t o = __shfl_up_sync(0xffffffffu, incl, i);
-            if (lane >= i) incl += o;
-        }
-        if (lane == 31) sScan[warp] = incl;
-        __syncthreads();
-        W = 0;
-        int64_t before = 0;
-#pragma unroll
-        for (int i = 0; i < C::THREADS / 32; ++i) {
-            if (i == warp) before = W;
-            W += sScan[i];
-        }
-        nc = W < nc ? (int)W : nc;
-        pos0 = attn_share(W, min(c, nc), nc);
-        pos1 = attn_share(W, min(c + 1, nc), nc);
-        int64_t at = before + incl - sum;
-        if (pos0 >= at && pos0 < at + sum) {
-            int g = ga;
-            for (; g < gz; ++g) {
-                const int64_t w = (int64_t)attn_group(p, g).w * p.Hkv;
-                if (pos0 < at + w) break;
-                at += w;
-            }
-            *sGroup = g;
-            *sBase = at;
-        }
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (!p.idx && pos0 < pos1) {
-        g0 = *sGroup;
-        base0 = *sBase;
-    }
-    const uint32_t tmem = *tmem_slot;
     AttnWalk wk;
-    wk.begin(p, pos0, pos1, g0, base0);
-
-    auto produce = [&]() {
-        // --------------------------------------------------------- producer
-        // Three steps ahead: indices of tile i + 2, page ids of tile i + 1, scales of tile i, so that a
-        // step waits for one memory latency at most.  A lane has four keys.
-        bool ok = !p.debug_stall;
-        struct Ref {
-            bool live;
-            int b, h, tile, limit;
-            int64_t row;  // of topk_indices
-        };
-        int tile = 0;
-        bool more = true;
-        auto next_ref = [&]() {
-            Ref r{false, 0, 0, 0, 0, 0};
-            while (more && (tile >= wk.t1 || wk.gr.n == 0)) {
-                more = wk.next(p);
-                tile = wk.t0;
-                if (more && p.idx) wk.gr.limit = attn_end(p, wk.gr.b, wk.gr.st);
-            }
-            if (more) r = Ref{true, wk.gr.b, wk.h, tile++, wk.gr.limit, (int64_t)wk.gr.b * p.S + wk.gr.st};
-            return r;
-        };
-        int tc = 0;
-        const int page_mask = p.page - 1;
-        // waits for the slots of tile tc's K and V and its stage of scales
-        auto claim = [&]() {
-            const int sk = 2 * tc, ms = tc % kAMeta;
-#pragma unroll
-            for (int w = 0; w < 2; ++w)
-                ok = ok && mbar_wait(kv_empty + (sk + w) % SLOTS, (((sk + w) / SLOTS) & 1) ^ 1, p.wait_ns);
-            ok = ok && mbar_wait(meta_empty + ms, ((tc / kAMeta) & 1) ^ 1, p.wait_ns);
-            ok = __all_sync(0xffffffffu, ok);
-        };
-        const int pw = warp - C::W_PROD;  // of the producers
-        if (!p.idx) {
-            if (pw > 0) return;
-            // Pages: the four keys of a lane share one; the lane with a page's first key loads it.
-            auto page_id = [&](const Ref& r) {
-                const int k0 = r.tile * kATile + 4 * lane;
-                return r.live && k0 < r.limit ? p.table[(int64_t)r.b * p.max_pages + (k0 >> p.page_shift)] : -1;
-            };
-            Ref r0 = next_ref();
-            int pid0 = page_id(r0);
-            Ref r1 = next_ref();
-            while (ok && r0.live) {
-                const bool good = pid0 >= 0 && pid0 < p.num_pages;
-                const int64_t cell = (int64_t)(good ? pid0 : 0) * p.Hkv + r0.h;
-                const float a = p.ks[cell], v = p.vs[cell];
-                const int pid1 = page_id(r1);
-                const Ref r2 = next_ref();
-                claim();
-                if (!ok) break;
-                const int sk = 2 * tc, ms = tc % kAMeta, s0 = sk % SLOTS, s1 = (sk + 1) % SLOTS;
-                const bool lead = good && ((4 * lane) & page_mask) == 0;
-                const uint32_t bytes = (128u << p.page_shift) * __popc(__ballot_sync(0xffffffffu, lead));
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(kv_full + s0, bytes);
-                    mbar_arrive_expect_tx(kv_full + s1, bytes);
-                }
-                __syncwarp();
-                if (lead) {
-                    const int row = (int)(cell << p.page_shift);
-                    tma_load_2d(smem + s0 * kASlotBytes + lane * 512, &tmk, kv_full + s0, 0, row);
-                    tma_load_2d(smem + s1 * kASlotBytes + lane * 512, &tmv, kv_full + s1, 0, row);
-                }
-                const int left = good ? r0.limit - (r0.tile * kATile + 4 * lane) : 0;  // keys of the lane that count
-                const float x = a * p.scale_log2, y = __log2f(fmaxf(v, 0x1p-60f));
-                float4* m4 = reinterpret_cast<float4*>(sMeta + ms * kATile + 4 * lane);
-                m4[0] = make_float4(x, left > 0 ? y : -INFINITY, x, left > 1 ? y : -INFINITY);
-                m4[1] = make_float4(x, left > 2 ? y : -INFINITY, x, left > 3 ? y : -INFINITY);
-                const bool all = __all_sync(0xffffffffu, left > 3);
-                if (lane == 0) {
-                    sFlag[ms] = all ? 0 : 1;
-                    mbar_arrive(meta_full + ms);
-                }
-                r0 = r1;
-                r1 = r2;
-                pid0 = pid1;
-                ++tc;
-            }
-            if (!ok && !p.debug_stall)  // loads in flight end before the memory is given up
-                for (int seq = max(0, 2 * tc - SLOTS); seq < 2 * tc; ++seq)
-                    mbar_wait(kv_full + seq % SLOTS, (seq / SLOTS) & 1, p.wait_ns);
-        } else {
-            // Selected keys: TMA gathers of four rows.  A producer has NQ quarters of 32 keys of each tile, a lane one key of
-            // each.  Unseen keys gather row 0 with the other three (or nothing); the softmax clears their V rows.
-            constexpr int NQ = 4 / C::PRODUCERS;
-            auto keys = [&](const Ref& r, int (&t)[NQ]) {
-                const int32_t* src = p.idx + r.row * p.topk;
-#pragma unroll
-                for (int i = 0; i < NQ; ++i) {
-                    const int k = r.tile * kATile + 32 * (pw + i) + lane;
-                    t[i] = r.live && k < p.topk ? src[k] : -1;
-                }
-            };
-            auto pages = [&](const Ref& r, const int (&t)[NQ], int (&pid)[NQ]) {
-                const int32_t* tab = p.table + (int64_t)r.b * p.max_pages;
-#pragma unroll
-                for (int i = 0; i < NQ; ++i) pid[i] = t[i] >= 0 && t[i] < r.limit ? tab[t[i] >> p.page_shift] : -1;
-            };
-            int* const sRows = (int*)(smem + C::OFF_GATHER) + 32 * pw;
-            Ref r0 = next_ref();
-            int t0[NQ], t1[NQ], t2[NQ], pid0[NQ], pid1[NQ];
-            keys(r0, t0);
-            Ref r1 = next_ref();
-            keys(r1, t1);
-            pages(r0, t0, pid0);
-            while (ok && r0.live) {
-                float a[NQ], v[NQ];
-                bool good[NQ];
-#pragma unroll
-                for (int i = 0; i < NQ; ++i) {
-                    good[i] = pid0[i] >= 0 && pid0[i] < p.num_pages;
-                    const int cell = (good[i] ? pid0[i] : 0) * p.Hkv + r0.h;  // num_pages * Hkv * page < 2^31
-                    a[i] = p.ks[cell];
-                    v[i] = p.vs[cell];
-                    sRows[32 * i + lane] = good[i] ? (cell << p.page_shift) + (t0[i] & page_mask) : -1;
-                }
-                pages(r1, t1, pid1);
-                const Ref r2 = next_ref();
-                keys(r2, t2);
-                claim();
-                if (!ok) break;
-                __syncwarp();
-                const int sk = 2 * tc, ms = tc % kAMeta, s0 = sk % SLOTS, s1 = (sk + 1) % SLOTS;
-                // four keys a lane
-                const int4 r = *reinterpret_cast<const int4*>(sRows + 4 * (lane & (8 * NQ - 1)));
-                const bool any = lane < 8 * NQ && (r.x & r.y & r.z & r.w) >= 0;  // one of them is seen
-                const uint32_t bytes = 512u * __popc(__ballot_sync(0xffffffffu, any));
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(kv_full + s0, bytes);
-                    mbar_arrive_expect_tx(kv_full + s1, bytes);
-                }
-                __syncwarp();
-                if (any) {
-                    const uint32_t to = pw * 4096 + lane * 512;
-                    tma_gather4(smem + s0 * kASlotBytes + to, &tmk, kv_full + s0, 0, max(r.x, 0), max(r.y, 0),
-                                max(r.z, 0), max(r.w, 0));
-                    tma_gather4(smem + s1 * kASlotBytes + to, &tmv, kv_full + s1, 0, max(r.x, 0), max(r.y, 0),
-                                max(r.z, 0), max(r.w, 0));
-                }
-#pragma unroll
-                for (int i = 0; i < NQ; ++i) {
-                    sMeta[ms * kATile + 32 * (pw + i) + lane] =
-                        good[i] ? make_float2(a[i] * p.scale_log2, __log2f(fmaxf(v[i], 0x1p-60f)))
-                                : make_float2(0.f, -INFINITY);
-                    const bool all = __all_sync(0xffffffffu, good[i]);
-                    if (lane == 0) reinterpret_cast<uint8_t*>(sFlag + ms)[pw + i] = all ? 0 : 1;
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(meta_full + ms);
-                r0 = r1;
-                r1 = r2;
-#pragma unroll
-                for (int i = 0; i < NQ; ++i) {
-                    t0[i] = t1[i];
-                    t1[i] = t2[i];
-                    pid0[i] = pid1[i];
-                }
-                ++tc;
-            }
-            if (!ok && !p.debug_stall)  // loads in flight end before the memory is given up
-                for (int seq = max(0, 2 * tc - SLOTS); seq < 2 * tc; ++seq)
-                    mbar_wait(kv_full + seq % SLOTS, (seq / SLOTS) & 1, p.wait_ns);
-        }
-    };
+    int64_t W;
+    tc_fence_before();
+    const int nc = attn_begin<C::THREADS>(p, wk, W, scan), c = blockIdx.x;
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
 
     if (warp < 4) {
         regs_dec<C::R_MMA>();
@@ -638,77 +271,13 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                 if (issuer) umma_commit(drain);
                 mbar_wait(drain, 0, p.wait_ns);
             }
-        } else if (warp >= C::W_QUERY && warp < C::W_QUERY + C::QWARPS) {
-            // ------------------------------------- queries: bf16 rows -> e4m3 hi and lo
-            // Eight lanes a row, 16 dims each, four rows a warp at a time.
-            bool ok = true;
-            int sc = 0;
-            const int sub = lane & 7;
-            while (wk.next(p)) {
-                if (wk.gr.n == 0) continue;
-                const int qb = sc % QB;
-                ok = ok && mbar_wait(q_empty + qb, ((sc / QB) & 1) ^ 1, p.wait_ns);
-                uint8_t* dst = sQ + qb * C::Q_BYTES;
-                // the next row's loads are in flight while a row is converted
-                auto load = [&](int n, uint4& u0, uint4& u1) {
-                    const int st = attn_token(p, n), s = wk.gr.st * p.TS + st;
-                    u0 = u1 = make_uint4(0, 0, 0, 0);
-                    if (n < N && st < p.TS && s < p.S && sub * 16 < p.D) {
-                        const uint4* src = reinterpret_cast<const uint4*>(
-                            p.q + wk.gr.b * p.qs[0] + s * p.qs[1] + (wk.h * p.G + n - st * p.G) * p.qs[2] + sub * 16);
-                        u0 = src[0];
-                        u1 = src[1];
-                    }
-                };
-                uint4 n0, n1, f0, f1;
-                constexpr int step = 4 * C::QWARPS;
-                const int first = (warp - C::W_QUERY) * 4 + (lane >> 3);
-                load(first, n0, n1);
-                load(first + step, f0, f1);
-#pragma unroll 1
-                for (int n = first; n < N; n += step) {
-                    const uint32_t w[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
-                    n0 = f0, n1 = f1;
-                    load(n + 2 * step, f0, f1);
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
-                    top = max(top & 0xffffu, top >> 16);
-#pragma unroll
-                    for (int i = 1; i < 8; i <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, i));
-                    // 2^(7 - exponent) brings the largest to [128, 256); exponents are kept where both the
-                    // factor and its inverse are normal numbers
-                    int ex = (int)(top >> 7);
-                    ex = top == 0 ? 127 + 7 : (ex < 16 ? 16 : ex);
-                    const float up = __int_as_float((254 + 7 - ex) << 23);
-                    if (sub == 0) sQs[qb * N + n] = __int_as_float((ex - 7) << 23);
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t h0, l0, h1, l1;
-                        split_e4m3(__uint_as_float(w[2 * i] << 16) * up, __uint_as_float(w[2 * i] & 0xffff0000u) * up, h0,
-                                   l0);
-                        split_e4m3(__uint_as_float(w[2 * i + 1] << 16) * up,
-                                   __uint_as_float(w[2 * i + 1] & 0xffff0000u) * up, h1, l1);
-                        hi[i] = h0 | (h1 << 16);
-                        lo[i] = l0 | (l1 << 16);
-                    }
-                    uint8_t* at = dst + n * 128 + ((sub ^ (n & 7)) << 4);  // 128-byte swizzle
-                    *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(at + N * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(q_full + qb);
-                ++sc;
-            }
-        } else if constexpr (!C::OWN_PROD) {
-            produce();
+        } else {
+            attn_queries<N, QB, C::QWARPS>(p, wk, x, warp - C::W_QUERY, lane);
         }
     } else if (warp < C::W_JOIN) {
         // -------------------------------------------------------------- softmax
         // A thread has one key of a tile and the columns [c0, c0 + NC).
-        if constexpr (C::R_SOFT > C::R_LAUNCH) regs_inc<C::R_SOFT>();
+        regs_inc<C::R_SOFT>();
         const int grp = (warp - C::W_SOFT) >> 2, wtid = tid & 127, wg_warp = warp & 3;
         const int c0 = C::SPLIT ? grp * NC : 0;
         const uint32_t bar_id = 1 + grp;
@@ -740,7 +309,7 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                 named_bar_sync(bar_id, 128);
             }
             ok = ok && mbar_wait(q_full + qb, (sc / QB) & 1, p.wait_ns);
-            const float* const qs = sQs + qb * N + c0;
+            const float* const qs = x.q_scale + qb * N + c0;
             float l[NC];
 #pragma unroll
             for (int i = 0; i < NC; ++i) l[i] = 0.f;
@@ -751,14 +320,15 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                 if (!C::SPLIT && (tc & 1) != grp) continue;
                 const int bf = tc & 1, ph = (tc >> 1) & 1, ms = tc % kAMeta;
                 ok = ok && mbar_wait(meta_full + ms, (tc / kAMeta) & 1, p.wait_ns);
-                const float2 mv = sMeta[ms * kATile + wtid];
-                const bool flag = sFlag[ms] != 0;
+                const float key_a = x.key_a[ms * kATile + wtid], key_lv = x.key_lv[ms * kATile + wtid];
+                const float key_iv = x.key_iv[ms * kATile + wtid];
+                const bool flag = x.flag[ms] != 0;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(meta_empty + ms);
                 const int key = t * kATile + wtid;
-                const bool seen = mv.y != -INFINITY;
+                const bool seen = key_lv != -INFINITY;
                 const bool masked = flag || t * kATile + kATile > least;
-                const uint64_t a2 = pack2(mv.x, mv.x), lv2 = pack2(mv.y, mv.y);
+                const uint64_t a2 = pack2(key_a, key_a), lv2 = pack2(key_lv, key_lv);
                 // S^T of this tile is done, and with it all products issued before: those of O^T of the tile before
                 // last, so its weights' buffer is free, and so are the maxima of four tiles ago (a tile's O^T waits for the
                 // joining of the tile two before it)
@@ -771,13 +341,13 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                 odd ^= 1;
                 auto one_tile = [&](auto mask_c) {
                     constexpr bool MASK = decltype(mask_c)::value;
-                    float x[CH];
+                    float score[CH];
 #pragma unroll
                     for (int cc = 0; cc < NC; cc += CH) {
-                        attn_scores<MASK, CH>(s_addr + cc, qs + cc, sEnd + cc, a2, lv2, key, seen, x);
+                        attn_scores<MASK, CH>(s_addr + cc, qs + cc, sEnd + cc, a2, lv2, key, seen, score);
                         float top[CH];
 #pragma unroll
-                        for (int i = 0; i < CH; ++i) top[i] = warp_max(x[i]);
+                        for (int i = 0; i < CH; ++i) top[i] = warp_max(score[i]);
                         if (lane == 0) {
 #pragma unroll
                             for (int i = 0; i < CH; i += 4)
@@ -811,20 +381,19 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                             l[i] *= f.x, l[i + 1] *= f.y, l[i + 2] *= f.z, l[i + 3] *= f.w;
                         }
                     }
-                    const float ivs = exp2_approx(-mv.y);
-                    const uint64_t iv2 = seen ? pack2(ivs, ivs) : pack2(0.f, 0.f);
+                    const uint64_t iv2 = seen ? pack2(key_iv, key_iv) : pack2(0.f, 0.f);
 #pragma unroll
                     for (int cc = 0; cc < NC; cc += CH) {
                         if constexpr (NC > CH)
-                            attn_scores<MASK, CH>(s_addr + cc, qs + cc, sEnd + cc, a2, lv2, key, seen, x);
+                            attn_scores<MASK, CH>(s_addr + cc, qs + cc, sEnd + cc, a2, lv2, key, seen, score);
                         uint32_t hi[CH / 4], lo[CH / 4];
 #pragma unroll
                         for (int i = 0; i < CH; i += 4) {
                             const float4 sh = *reinterpret_cast<const float4*>(sSh + cc + i);
                             const float4 be = *reinterpret_cast<const float4*>(sBe + cc + i);
                             float e0, e1, e2, e3;
-                            unpack2(add2(pack2(x[i], x[i + 1]), pack2(sh.x, sh.y)), e0, e1);
-                            unpack2(add2(pack2(x[i + 2], x[i + 3]), pack2(sh.z, sh.w)), e2, e3);
+                            unpack2(add2(pack2(score[i], score[i + 1]), pack2(sh.x, sh.y)), e0, e1);
+                            unpack2(add2(pack2(score[i + 2], score[i + 3]), pack2(sh.z, sh.w)), e2, e3);
                             const float w0 = exp2_approx(e0), w1 = exp2_approx(e1);
                             const float w2 = exp2_approx(e2), w3 = exp2_approx(e3);
                             unpack2(fma2(mul2(pack2(w0, w1), iv2), pack2(be.x, be.y), pack2(l[cc + i], l[cc + i + 1])),
@@ -895,7 +464,7 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
         regs_inc<C::R_JOIN>();
         const int d = tid & 127, wg_warp = warp & 3;
         constexpr uint32_t bar_id = 1 + C::SG;
-        constexpr int JC = N == 32 || N == 64 ? 32 : 16;  // columns read at a time
+        constexpr int JC = N;  // columns read at a time
         const uint32_t lane_addr = tmem + ((uint32_t)(wg_warp * 32) << 16) + 2 * N;
         float* const sA = (float*)(smem + C::OFF_AB);  // [2][N] fade of acc
         float* const sB = sA + 2 * N;                  // [2][N] of the tile
@@ -1000,9 +569,9 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
             }
         }
         if (d == 0) reinterpret_cast<AttnHeader*>(p.ws)[c] = hd;
-    } else if constexpr (C::OWN_PROD) {
+    } else {
         regs_dec<C::R_PROD>();
-        produce();
+        attn_produce<SLOTS, C::PRODUCERS>(p, wk, x, &tmk, &tmv, warp - C::W_PROD, lane);
     }
 
     __syncwarp();
@@ -1076,7 +645,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __g
 // indices, as many of the sequence's query tokens as fit.
 static int attn_columns(int64_t S, int G, bool selected) {
     const int64_t want = selected ? G : (S * G < 128 ? S * G : 128);
-    return want <= 16 ? 16 : (want <= 32 ? 32 : (want <= 64 ? 64 : 128));
+    return want <= 16 ? 16 : (want <= 32 ? 32 : 128);
 }
 
 static int attn_cache_map(CUtensorMap* m, const void* cache, int64_t rows, int D, int box_rows) {
@@ -1094,8 +663,11 @@ static cudaError_t attn_launch(const CUtensorMap& mk, const CUtensorMap& mv, con
     cudaError_t e = set_smem_attr((const void*)cache_attn_kernel<N>, AttnCfg<N>::TOTAL);
     if (e != cudaSuccess) return e;
     cache_attn_kernel<N><<<grid, AttnCfg<N>::THREADS, AttnCfg<N>::TOTAL, st>>>(mk, mv, p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || grid == 1) return e;
+    return cudaGetLastError();
+}
+
+template <int N>
+static cudaError_t attn_join(const AttnParams& p, int grid, cudaStream_t st) {
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
     const int rows = p.TS * p.G;
@@ -1196,9 +768,13 @@ int lidx_cache_attn(const void* q, const int64_t* qs, const void* k_cache, const
     switch (N) {
         case 16: e = attn_launch<16>(mk, mv, p, grid, st); break;
         case 32: e = attn_launch<32>(mk, mv, p, grid, st); break;
-        case 64: e = attn_launch<64>(mk, mv, p, grid, st); break;
-        default: e = attn_launch<128>(mk, mv, p, grid, st); break;
+        default: e = attn_launch_wide(mk, mv, p, grid, st); break;
     }
+    if (e == cudaSuccess && grid > 1) switch (N) {
+            case 16: e = attn_join<16>(p, grid, st); break;
+            case 32: e = attn_join<32>(p, grid, st); break;
+            default: e = attn_join<128>(p, grid, st); break;
+        }
     return e == cudaSuccess ? LIDX_OK : LIDX_ERR_CUDA;
 }
 

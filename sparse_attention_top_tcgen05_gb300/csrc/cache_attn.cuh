@@ -1,0 +1,484 @@
+// cache_attn.cuh -- what the two kernels of the attention over the paged 8-bit cache share (see cache_attn.cu):
+// parameters, the line of tiles and its shares, the producer of keys and values and the conversion of queries.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <climits>
+#include <type_traits>
+
+#include "cache.cuh"
+#include "kernels.h"
+#include "lidx.h"
+#include "ptx.cuh"
+
+namespace lidx {
+
+struct AttnParams {
+    const uint16_t* q;
+    int64_t qs[3];
+    const float* ks;
+    const float* vs;
+    const int32_t* table;
+    const int32_t* kv_len;
+    const int32_t* q_pos;  // nullable
+    const int32_t* idx;    // nullable
+    int64_t num_pages;
+    int B, S, Hq, Hkv, G, D, page, max_pages, ratio, topk;
+    int TS, ST;            // query tokens of a unit; units of a sequence
+    int page_shift;        // page = 1 << page_shift
+    uint32_t inv_g;        // ceil(2^16 / G): n / G = n * inv_g >> 16 for n < 128
+    float scale_log2;      // softmax_scale * log2(e)
+    uint16_t* out;
+    float* lse;            // nullable
+    uint8_t* ws;
+    uint64_t wait_ns;
+    int debug_stall;       // 1: the producer issues nothing (failure-detection tests)
+};
+
+constexpr int kATile = 128;                     // keys of a tile
+constexpr int kASlotBytes = kATile * 128;       // one K or V tile: 128 bytes a key (zero past D)
+constexpr int kAMeta = 5;                       // stages of per-key scales
+constexpr float kATop = 8.f;                    // weights are scaled to 2^8
+constexpr float kALn2 = 0.693147180559945309f;
+
+// Row (b, s) sees keys [0, end).
+__device__ __forceinline__ int attn_end(const AttnParams& p, int b, int s) {
+    int n = p.kv_len[b];
+    const int cap = p.max_pages * p.page;
+    n = n < 0 ? 0 : (n > cap ? cap : n);
+    if (p.q_pos) {
+        const int64_t seen = (int64_t)p.q_pos[b] + s + 1;  // below 2^32
+        const uint32_t e = seen > 0 ? (uint32_t)seen / (uint32_t)p.ratio : 0;
+        n = e < (uint32_t)n ? (int)e : n;
+    }
+    return n;
+}
+
+// ---- the line of tiles.  Group g = (sequence, tile of query tokens); its Hkv units follow each other.
+struct AttnGroup {
+    int b, st, limit;  // limit: keys its last row sees
+    int n;             // tiles of a unit (0: nothing to see)
+    int w;             // places of a unit on the line: at least one
+};
+__device__ __forceinline__ void attn_group_size(const AttnParams& p, AttnGroup& r) {
+    if (!p.idx) r.limit = attn_end(p, r.b, min(r.st * p.TS + p.TS, p.S) - 1);  // (selected keys: the producers look)
+    r.n = ((p.idx ? p.topk : r.limit) + kATile - 1) / kATile;
+    r.w = max(r.n, 1);
+}
+__device__ __forceinline__ AttnGroup attn_group(const AttnParams& p, int g) {
+    AttnGroup r;
+    r.b = g / p.ST;
+    r.st = g - r.b * p.ST;
+    r.limit = 0;
+    attn_group_size(p, r);
+    return r;
+}
+// Query token of column n within a unit.
+__device__ __forceinline__ int attn_token(const AttnParams& p, int n) { return (int)(n * p.inv_g >> 16); }
+__device__ __forceinline__ int64_t attn_share(int64_t W, int c, int n) { return W * c / n; }
+
+// The segments [t0, t1) of units that make up a CTA's share; every role walks them alike.
+struct AttnWalk {
+    int64_t pos, end;   // places not walked yet
+    int64_t unit_end;   // place behind the segment's unit
+    int g, h, t0, t1;
+    AttnGroup gr;
+    bool first, fresh;  // first: the segment is the CTA's first
+
+    // pos lies in group g, whose first unit's place is base
+    __device__ void begin(const AttnParams& p, int64_t pos_, int64_t end_, int g_, int64_t base) {
+        pos = pos_;
+        end = end_;
+        g = g_;
+        t1 = 0;
+        fresh = true;
+        if (pos >= end) return;
+        gr = attn_group(p, g);
+        const int64_t at = pos - base;
+        h = at < INT_MAX ? (int)((uint32_t)at / (uint32_t)gr.w) : (int)(at / gr.w);
+        t0 = (int)(at - (int64_t)h * gr.w);
+    }
+    __device__ bool next(const AttnParams& p) {
+        if (pos >= end) return false;
+        first = fresh;
+        if (fresh) {
+            fresh = false;
+        } else {
+            t0 = 0;
+            if (++h == p.Hkv) {
+                h = 0;
+                ++g;
+                if (++gr.st == p.ST) gr.st = 0, ++gr.b;
+                attn_group_size(p, gr);
+            }
+        }
+        unit_end = pos - t0 + gr.w;
+        const int64_t e = unit_end < end ? unit_end : end;
+        t1 = t0 + (int)(e - pos);
+        pos = e;
+        return true;
+    }
+};
+
+// Workspace: a header for each CTA, then two parts for each (its first segment, its last).
+struct AttnHeader {
+    // last > 0: the CTA holds the first tiles (in part `slot`) of a unit that ends with CTA `last`'s first segment
+    int32_t last, g, h, slot;
+};
+__host__ __device__ inline size_t attn_part_floats(int N) { return (size_t)N * 128 + 2 * N; }
+__host__ __device__ inline size_t attn_ws_bytes(int N, int grid) {
+    return (size_t)grid * sizeof(AttnHeader) + (size_t)grid * 2 * attn_part_floats(N) * 4;
+}
+
+// Two floats (at most 256 in size) -> e4m3 hi and lo pairs in the low halves.
+__device__ __forceinline__ void split_e4m3(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+    uint32_t f, b, r;
+    uint16_t h, l;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(f) : "f"(x1), "f"(x0));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(f));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"(h));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(f), "r"(b));  // exact
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(r));
+    hi = h;
+    lo = l;
+}
+
+
+// One pipeline of a CTA in shared memory.
+struct AttnPipe {
+    uint8_t* kv;            // [SLOTS] K or V tiles, in turn
+    uint8_t* q;             // [QB] query rows: hi, lo
+    float* q_scale;         // [QB][N]
+    float* key_a;           // [kAMeta][128] key scale * softmax_scale * log2(e)
+    float* key_lv;          // [kAMeta][128] log2 of the value scale; -inf: the key is not seen
+    float* key_iv;          // [kAMeta][128] its inverse
+    uint32_t* seen;         // [kAMeta][4] bits of the keys that are seen
+    uint32_t* flag;         // [kAMeta] not 0: a key of the tile is not seen
+    int* rows;              // [128] cache rows of gathered keys
+    uint64_t *kv_full;      // [SLOTS] K or V tile landed
+    uint64_t *kv_empty;     // [SLOTS] its product is done
+    uint64_t *meta_full;    // [kAMeta] what belongs to a tile's keys is written
+    uint64_t *meta_empty;   // [kAMeta] and read
+    uint64_t *q_full, *q_empty;  // [QB]
+};
+
+// This CTA's share of the line.  All THREADS threads call it; scan: 34 words of 64 bits.  Returns the number of CTAs
+// that have a share; total: places of the line.
+template <int THREADS>
+__device__ __forceinline__ int attn_begin(const AttnParams& p, AttnWalk& wk, int64_t& total, int64_t* scan) {
+    int64_t* const sScan = scan;
+    int64_t* const sBase = scan + 32;
+    int* const sGroup = (int*)(scan + 33);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    static_assert(THREADS / 32 <= 32, "scan");
+    const int c = blockIdx.x;
+    int nc = gridDim.x;  // CTAs with a share
+    int64_t W, pos0, pos1, base0 = 0;
+    int g0 = 0;
+    if (p.idx) {
+        // every unit has the same places
+        const int64_t w = (int64_t)((p.topk + kATile - 1) / kATile) * p.Hkv;
+        W = w * p.B * p.ST;
+        nc = W < nc ? (int)W : nc;
+        pos0 = attn_share(W, min(c, nc), nc);
+        pos1 = attn_share(W, min(c + 1, nc), nc);
+        g0 = (int)(pos0 / w);
+        base0 = g0 * w;
+    } else {
+        const int NG = p.B * p.ST, per = (NG + THREADS - 1) / THREADS;
+        const int ga = min(tid * per, NG), gz = min(ga + per, NG);
+        int64_t sum = 0;
+        for (int g = ga; g < gz; ++g) sum += (int64_t)attn_group(p, g).w * p.Hkv;
+        int64_t incl = sum;
+#pragma unroll
+        for (int i = 1; i < 32; i <<= 1) {
+            const int64_t o = __shfl_up_sync(0xffffffffu, incl, i);
+            if (lane >= i) incl += o;
+        }
+        if (lane == 31) sScan[warp] = incl;
+        __syncthreads();
+        W = 0;
+        int64_t before = 0;
+#pragma unroll
+        for (int i = 0; i < THREADS / 32; ++i) {
+            if (i == warp) before = W;
+            W += sScan[i];
+        }
+        nc = W < nc ? (int)W : nc;
+        pos0 = attn_share(W, min(c, nc), nc);
+        pos1 = attn_share(W, min(c + 1, nc), nc);
+        int64_t at = before + incl - sum;
+        if (pos0 >= at && pos0 < at + sum) {
+            int g = ga;
+            for (; g < gz; ++g) {
+                const int64_t w = (int64_t)attn_group(p, g).w * p.Hkv;
+                if (pos0 < at + w) break;
+                at += w;
+            }
+            *sGroup = g;
+            *sBase = at;
+        }
+    }
+    __syncthreads();
+    if (!p.idx && pos0 < pos1) {
+        g0 = *sGroup;
+        base0 = *sBase;
+    }
+    wk.begin(p, pos0, pos1, g0, base0);
+    total = W;
+    return nc;
+}
+
+// Loads keys and values: one of PRODUCERS warps.
+template <int SLOTS, int PRODUCERS>
+__device__ __forceinline__ void attn_produce(const AttnParams& p, AttnWalk& wk, const AttnPipe& x, const CUtensorMap* tmk,
+                                             const CUtensorMap* tmv, int pw, int lane) {
+    // Three steps ahead: indices of tile i + 2, page ids of tile i + 1, scales of tile i, so that a
+    // step waits for one memory latency at most.  A lane has four keys.
+    bool ok = !p.debug_stall;
+    struct Ref {
+        bool live;
+        int b, h, tile, limit;
+        int64_t row;  // of topk_indices
+    };
+    int tile = 0;
+    bool more = true;
+    auto next_ref = [&]() {
+        Ref r{false, 0, 0, 0, 0, 0};
+        while (more && (tile >= wk.t1 || wk.gr.n == 0)) {
+            more = wk.next(p);
+            tile = wk.t0;
+            if (more && p.idx) wk.gr.limit = attn_end(p, wk.gr.b, wk.gr.st);
+        }
+        if (more) r = Ref{true, wk.gr.b, wk.h, tile++, wk.gr.limit, (int64_t)wk.gr.b * p.S + wk.gr.st};
+        return r;
+    };
+    int tc = 0;
+    const int page_mask = p.page - 1;
+    // waits for the slots of tile tc's K and V and its stage of scales
+    auto claim = [&]() {
+        const int sk = 2 * tc, ms = tc % kAMeta;
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+            ok = ok && mbar_wait(x.kv_empty + (sk + w) % SLOTS, (((sk + w) / SLOTS) & 1) ^ 1, p.wait_ns);
+        ok = ok && mbar_wait(x.meta_empty + ms, ((tc / kAMeta) & 1) ^ 1, p.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+    };
+    if (!p.idx) {
+        if (pw > 0) return;
+        // Pages: the four keys of a lane share one; the lane with a page's first key loads it.
+        auto page_id = [&](const Ref& r) {
+            const int k0 = r.tile * kATile + 4 * lane;
+            return r.live && k0 < r.limit ? p.table[(int64_t)r.b * p.max_pages + (k0 >> p.page_shift)] : -1;
+        };
+        Ref r0 = next_ref();
+        int pid0 = page_id(r0);
+        Ref r1 = next_ref();
+        while (ok && r0.live) {
+            const bool good = pid0 >= 0 && pid0 < p.num_pages;
+            const int64_t cell = (int64_t)(good ? pid0 : 0) * p.Hkv + r0.h;
+            const float a = p.ks[cell], v = p.vs[cell];
+            const int pid1 = page_id(r1);
+            const Ref r2 = next_ref();
+            claim();
+            if (!ok) break;
+            const int sk = 2 * tc, ms = tc % kAMeta, s0 = sk % SLOTS, s1 = (sk + 1) % SLOTS;
+            const bool lead = good && ((4 * lane) & page_mask) == 0;
+            const uint32_t bytes = (128u << p.page_shift) * __popc(__ballot_sync(0xffffffffu, lead));
+            if (lane == 0) {
+                mbar_arrive_expect_tx(x.kv_full + s0, bytes);
+                mbar_arrive_expect_tx(x.kv_full + s1, bytes);
+            }
+            __syncwarp();
+            if (lead) {
+                const int row = (int)(cell << p.page_shift);
+                tma_load_2d(x.kv + s0 * kASlotBytes + lane * 512, tmk, x.kv_full + s0, 0, row);
+                tma_load_2d(x.kv + s1 * kASlotBytes + lane * 512, tmv, x.kv_full + s1, 0, row);
+            }
+            const int left = good ? r0.limit - (r0.tile * kATile + 4 * lane) : 0;  // keys of the lane that count
+            const float f = a * p.scale_log2, y = __log2f(fmaxf(v, 0x1p-60f)), iv = exp2_approx(-y);
+            const float none = -INFINITY;
+            const int at = ms * kATile + 4 * lane;
+            *reinterpret_cast<float4*>(x.key_a + at) = make_float4(f, f, f, f);
+            *reinterpret_cast<float4*>(x.key_lv + at) = make_float4(left > 0 ? y : none, left > 1 ? y : none,
+                                                                    left > 2 ? y : none, left > 3 ? y : none);
+            *reinterpret_cast<float4*>(x.key_iv + at) = make_float4(iv, iv, iv, iv);
+            uint32_t seen = (left > 3 ? 15u : (left > 0 ? (1u << left) - 1 : 0u)) << (4 * (lane & 7));
+#pragma unroll
+            for (int i = 1; i < 8; i <<= 1) seen |= __shfl_xor_sync(0xffffffffu, seen, i);
+            if ((lane & 7) == 0) x.seen[ms * 4 + (lane >> 3)] = seen;
+            const bool all = __all_sync(0xffffffffu, left > 3);
+            if (lane == 0) x.flag[ms] = all ? 0 : 1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(x.meta_full + ms);
+            r0 = r1;
+            r1 = r2;
+            pid0 = pid1;
+            ++tc;
+        }
+        if (!ok && !p.debug_stall)  // loads in flight end before the memory is given up
+            for (int seq = max(0, 2 * tc - SLOTS); seq < 2 * tc; ++seq)
+                mbar_wait(x.kv_full + seq % SLOTS, (seq / SLOTS) & 1, p.wait_ns);
+    } else {
+        // Selected keys: TMA gathers of four rows.  A producer has NQ quarters of 32 keys of each tile, a lane one key of
+        // each.  Unseen keys gather row 0 with the other three (or nothing); the softmax clears their V rows.
+        constexpr int NQ = 4 / PRODUCERS;
+        auto keys = [&](const Ref& r, int (&t)[NQ]) {
+            const int32_t* src = p.idx + r.row * p.topk;
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                const int k = r.tile * kATile + 32 * (pw + i) + lane;
+                t[i] = r.live && k < p.topk ? src[k] : -1;
+            }
+        };
+        auto pages = [&](const Ref& r, const int (&t)[NQ], int (&pid)[NQ]) {
+            const int32_t* tab = p.table + (int64_t)r.b * p.max_pages;
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) pid[i] = t[i] >= 0 && t[i] < r.limit ? tab[t[i] >> p.page_shift] : -1;
+        };
+        int* const sRows = x.rows + 32 * pw;
+        Ref r0 = next_ref();
+        int t0[NQ], t1[NQ], t2[NQ], pid0[NQ], pid1[NQ];
+        keys(r0, t0);
+        Ref r1 = next_ref();
+        keys(r1, t1);
+        pages(r0, t0, pid0);
+        while (ok && r0.live) {
+            float a[NQ], v[NQ];
+            bool good[NQ];
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                good[i] = pid0[i] >= 0 && pid0[i] < p.num_pages;
+                const int cell = (good[i] ? pid0[i] : 0) * p.Hkv + r0.h;  // num_pages * Hkv * page < 2^31
+                a[i] = p.ks[cell];
+                v[i] = p.vs[cell];
+                sRows[32 * i + lane] = good[i] ? (cell << p.page_shift) + (t0[i] & page_mask) : -1;
+            }
+            pages(r1, t1, pid1);
+            const Ref r2 = next_ref();
+            keys(r2, t2);
+            claim();
+            if (!ok) break;
+            __syncwarp();
+            const int sk = 2 * tc, ms = tc % kAMeta, s0 = sk % SLOTS, s1 = (sk + 1) % SLOTS;
+            // four keys a lane
+            const int4 r = *reinterpret_cast<const int4*>(sRows + 4 * (lane & (8 * NQ - 1)));
+            const bool any = lane < 8 * NQ && (r.x & r.y & r.z & r.w) >= 0;  // one of them is seen
+            const uint32_t bytes = 512u * __popc(__ballot_sync(0xffffffffu, any));
+            if (lane == 0) {
+                mbar_arrive_expect_tx(x.kv_full + s0, bytes);
+                mbar_arrive_expect_tx(x.kv_full + s1, bytes);
+            }
+            __syncwarp();
+            if (any) {
+                const uint32_t to = pw * 4096 + lane * 512;
+                tma_gather4(x.kv + s0 * kASlotBytes + to, tmk, x.kv_full + s0, 0, max(r.x, 0), max(r.y, 0),
+                            max(r.z, 0), max(r.w, 0));
+                tma_gather4(x.kv + s1 * kASlotBytes + to, tmv, x.kv_full + s1, 0, max(r.x, 0), max(r.y, 0),
+                            max(r.z, 0), max(r.w, 0));
+            }
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                const int at = ms * kATile + 32 * (pw + i) + lane;
+                const float y = __log2f(fmaxf(v[i], 0x1p-60f));
+                x.key_a[at] = good[i] ? a[i] * p.scale_log2 : 0.f;
+                x.key_lv[at] = good[i] ? y : -INFINITY;
+                x.key_iv[at] = exp2_approx(-y);
+                const uint32_t seen = __ballot_sync(0xffffffffu, good[i]);
+                if (lane == 0) {
+                    x.seen[ms * 4 + pw + i] = seen;
+                    reinterpret_cast<uint8_t*>(x.flag + ms)[pw + i] = seen == 0xffffffffu ? 0 : 1;
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(x.meta_full + ms);
+            r0 = r1;
+            r1 = r2;
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                t0[i] = t1[i];
+                t1[i] = t2[i];
+                pid0[i] = pid1[i];
+            }
+            ++tc;
+        }
+        if (!ok && !p.debug_stall)  // loads in flight end before the memory is given up
+            for (int seq = max(0, 2 * tc - SLOTS); seq < 2 * tc; ++seq)
+                mbar_wait(x.kv_full + seq % SLOTS, (seq / SLOTS) & 1, p.wait_ns);
+    }
+}
+
+// Query rows of a unit, bf16 -> e4m3 hi and lo: one of QWARPS warps.
+template <int N, int QB, int QWARPS>
+__device__ __forceinline__ void attn_queries(const AttnParams& p, AttnWalk& wk, const AttnPipe& x, int qw, int lane) {
+    // Eight lanes a row, 16 dims each, four rows a warp at a time.
+    bool ok = true;
+    int sc = 0;
+    const int sub = lane & 7;
+    while (wk.next(p)) {
+        if (wk.gr.n == 0) continue;
+        const int qb = sc % QB;
+        ok = ok && mbar_wait(x.q_empty + qb, ((sc / QB) & 1) ^ 1, p.wait_ns);
+        uint8_t* dst = x.q + qb * (2 * N * 128);
+        // the next row's loads are in flight while a row is converted
+        auto load = [&](int n, uint4& u0, uint4& u1) {
+            const int st = attn_token(p, n), s = wk.gr.st * p.TS + st;
+            u0 = u1 = make_uint4(0, 0, 0, 0);
+            if (n < N && st < p.TS && s < p.S && sub * 16 < p.D) {
+                const uint4* src = reinterpret_cast<const uint4*>(
+                    p.q + wk.gr.b * p.qs[0] + s * p.qs[1] + (wk.h * p.G + n - st * p.G) * p.qs[2] + sub * 16);
+                u0 = src[0];
+                u1 = src[1];
+            }
+        };
+        uint4 n0, n1, f0, f1;
+        constexpr int step = 4 * QWARPS;
+        const int first = qw * 4 + (lane >> 3);
+        load(first, n0, n1);
+        load(first + step, f0, f1);
+#pragma unroll 1
+        for (int n = first; n < N; n += step) {
+            const uint32_t w[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
+            n0 = f0, n1 = f1;
+            load(n + 2 * step, f0, f1);
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+            top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+            for (int i = 1; i < 8; i <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, i));
+            // 2^(7 - exponent) brings the largest to [128, 256); exponents are kept where both the
+            // factor and its inverse are normal numbers
+            int ex = (int)(top >> 7);
+            ex = top == 0 ? 127 + 7 : (ex < 16 ? 16 : ex);
+            const float up = __int_as_float((254 + 7 - ex) << 23);
+            if (sub == 0) x.q_scale[qb * N + n] = __int_as_float((ex - 7) << 23);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t h0, l0, h1, l1;
+                split_e4m3(__uint_as_float(w[2 * i] << 16) * up, __uint_as_float(w[2 * i] & 0xffff0000u) * up, h0,
+                           l0);
+                split_e4m3(__uint_as_float(w[2 * i + 1] << 16) * up,
+                           __uint_as_float(w[2 * i + 1] & 0xffff0000u) * up, h1, l1);
+                hi[i] = h0 | (h1 << 16);
+                lo[i] = l0 | (l1 << 16);
+            }
+            uint8_t* at = dst + n * 128 + ((sub ^ (n & 7)) << 4);  // 128-byte swizzle
+            *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(at + N * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(x.q_full + qb);
+        ++sc;
+    }
+}
+
+// Kernels of at most 32 and of at most 128 columns; the parts of either are joined by one kernel.
+cudaError_t attn_launch_wide(const CUtensorMap& mk, const CUtensorMap& mv, const AttnParams& p, int grid, cudaStream_t st);
+
+}  // namespace lidx

@@ -1,0 +1,497 @@
+// cache_attn_wide.cu -- attention over the paged 8-bit cache, units of 33 to 128 rows (see cache_attn.cu).
+//
+// The mathematics is cache_attn.cu's with the operands' roles swapped: the unit's (token, head) rows are the rows of the
+// products, S = Q K^T and O = P V, keys and dims their columns.  A softmax thread owns one row: maximum, sum and fades are
+// its own registers, and nothing crosses lanes or waits at a barrier.  That costs half of the instructions that a thread
+// for each key costs from 64 rows on (10.2k -> 5.3k a tile of 128 x 128), but lanes without a row have no work, so
+// units of up to 32 rows stay with the other kernel.
+#include "cache_attn.cuh"
+
+namespace lidx {
+
+struct WideCfg {
+    static constexpr int N = 128, QB = 2, SLOTS = 5;
+    static constexpr int Q_BYTES = 2 * N * 128, P_BYTES = 2 * N * 128;  // hi and lo
+    static constexpr int OFF_P = SLOTS * kASlotBytes;
+    static constexpr int OFF_Q = OFF_P + 2 * P_BYTES;
+    static constexpr int OFF_META = OFF_Q + QB * Q_BYTES;                // [3][kAMeta][128] of the keys
+    static constexpr int OFF_SEEN = OFF_META + 3 * kAMeta * kATile * 4;  // [kAMeta][4], then [kAMeta] flags
+    static constexpr int OFF_QS = OFF_SEEN + 128;                        // [QB][N] query scales
+    static constexpr int OFF_MT = OFF_QS + QB * N * 4;                   // [4][N] tile maxima
+    static constexpr int OFF_L = OFF_MT + 4 * N * 4;                     // [2][N] float2: a group's sum, its reference
+    static constexpr int OFF_GATHER = OFF_L + 2 * N * 8;                 // [128] cache rows of a tile's keys
+    static constexpr int OFF_BAR = OFF_GATHER + kATile * 4;
+    static constexpr int NBAR = 2 * SLOTS + 2 * kAMeta + 2 * 2 + 3 * 2 + 4 + 2 + 1;
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+    static constexpr int TOTAL = OFF_MISC + 288 + 1024;
+    static_assert(TOTAL <= 232448 && kAMeta * 20 <= 128, "shared memory");
+    static_assert(OFF_QS % 16 == 0 && OFF_GATHER % 16 == 0 && OFF_MISC % 8 == 0, "16-byte reads");
+    static constexpr int TMEM = 512;  // two tiles of S and of O
+    // Warpgroups: MMA and queries; two of softmax that take the tiles in turn; joining; producers.
+    static constexpr int THREADS = 640, PRODUCERS = 4, QWARPS = 3;
+    static constexpr int W_SOFT = 4, W_JOIN = 12, W_PROD = 16;
+    static constexpr int R_LAUNCH = 96, R_MMA = 56, R_SOFT = 104, R_JOIN = 160, R_PROD = 56;
+    static_assert(R_LAUNCH == 65536 / THREADS / 8 * 8 && R_MMA + 2 * R_SOFT + R_JOIN + R_PROD <= R_LAUNCH * 5,
+                  "register split");
+};
+
+// Scores of 32 keys of this thread's row in log2 units: S * (key's factor * row's factor) + log2(v scale).
+// UNI: the keys of a block of 16 share their page's factors.  vis: bits of the keys the row sees (MASK).
+template <bool MASK, bool UNI>
+__device__ __forceinline__ void wide_scores(uint32_t s_addr, const float* a, const float* lv, float qs, uint32_t vis,
+                                            float (&x)[32]) {
+    uint32_t r[32];
+    tmem_ld32(s_addr, r);
+    tmem_ld_wait();
+    if constexpr (UNI) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float f = a[16 * h] * qs, v = lv[16 * h];
+            const uint64_t f2 = pack2(f, f), v2 = pack2(v, v);
+#pragma unroll
+            for (int i = 16 * h; i < 16 * h + 16; i += 2)
+                unpack2(fma2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f2, v2), x[i], x[i + 1]);
+        }
+    } else {
+        const uint64_t q2 = pack2(qs, qs);
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(a + i);
+            const float4 v = *reinterpret_cast<const float4*>(lv + i);
+            unpack2(fma2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), mul2(pack2(f.x, f.y), q2),
+                         pack2(v.x, v.y)),
+                    x[i], x[i + 1]);
+            unpack2(fma2(pack2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), mul2(pack2(f.z, f.w), q2),
+                         pack2(v.z, v.w)),
+                    x[i + 2], x[i + 3]);
+        }
+    }
+    if constexpr (MASK) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = (vis >> i) & 1 ? x[i] : -INFINITY;
+    }
+}
+
+__global__ void __launch_bounds__(WideCfg::THREADS, 1)
+    cache_attn_wide_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                           const __grid_constant__ AttnParams p) {
+    using C = WideCfg;
+    constexpr int N = C::N, SLOTS = C::SLOTS, QB = C::QB;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t* const sP = smem + C::OFF_P;
+    uint8_t* const sQ = smem + C::OFF_Q;
+    float* const sMt = (float*)(smem + C::OFF_MT);
+    float2* const sL = (float2*)(smem + C::OFF_L);
+    uint64_t* bars = (uint64_t*)(smem + C::OFF_BAR);
+    AttnPipe x;
+    x.kv = smem;
+    x.q = sQ;
+    x.q_scale = (float*)(smem + C::OFF_QS);
+    x.key_a = (float*)(smem + C::OFF_META);
+    x.key_lv = x.key_a + kAMeta * kATile;
+    x.key_iv = x.key_lv + kAMeta * kATile;
+    x.seen = (uint32_t*)(smem + C::OFF_SEEN);
+    x.flag = x.seen + 4 * kAMeta;
+    x.rows = (int*)(smem + C::OFF_GATHER);
+    uint64_t* const kv_full = x.kv_full = bars;
+    uint64_t* const kv_empty = x.kv_empty = kv_full + SLOTS;
+    uint64_t* const meta_full = x.meta_full = kv_empty + SLOTS;
+    uint64_t* const meta_empty = x.meta_empty = meta_full + kAMeta;
+    uint64_t* const q_full = x.q_full = meta_empty + kAMeta;
+    uint64_t* const q_empty = x.q_empty = q_full + 2;
+    uint64_t* s_full = q_empty + 2;  // [2] S of a tile in TMEM
+    uint64_t* p_full = s_full + 2;   // [4] weights and tile maxima written (and S read)
+    uint64_t* o_full = p_full + 4;   // [2] O of a tile in TMEM (and the weights read)
+    uint64_t* o_empty = o_full + 2;  // [2] O read
+    uint64_t* l_full = o_empty + 2;  // sums of a segment written
+    uint64_t* l_empty = l_full + 1;
+    uint64_t* drain = l_empty + 1;
+    uint32_t* tmem_slot = (uint32_t*)(smem + C::OFF_MISC);
+    int64_t* const scan = (int64_t*)(smem + C::OFF_MISC + 8);  // [34]
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < SLOTS; ++i) {
+            mbar_init(kv_full + i, p.idx ? C::PRODUCERS : 1);
+            mbar_init(kv_empty + i, 1);
+        }
+        for (int i = 0; i < kAMeta; ++i) {
+            mbar_init(meta_full + i, p.idx ? C::PRODUCERS : 1);
+            mbar_init(meta_empty + i, 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full + i, C::QWARPS);
+            mbar_init(q_empty + i, 1 + 8);
+            mbar_init(s_full + i, 1);
+            mbar_init(p_full + i, 4);
+            mbar_init(p_full + 2 + i, 4);
+            mbar_init(o_full + i, 1);
+            mbar_init(o_empty + i, 4);
+        }
+        mbar_init(l_full, 8);
+        mbar_init(l_empty, 4);
+        mbar_init(drain, 1);
+        fence_mbar_init();
+        tma_prefetch_desc(&tmk);
+        tma_prefetch_desc(&tmv);
+    }
+    if (warp == 0) {
+        tmem_alloc(tmem_slot, C::TMEM);
+        tmem_relinquish();
+    }
+    AttnWalk wk;
+    int64_t W;
+    tc_fence_before();
+    const int nc = attn_begin<C::THREADS>(p, wk, W, scan), c = blockIdx.x;
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int rows = p.TS * p.G;  // of a unit
+
+    if (warp < 4) {
+        regs_dec<C::R_MMA>();
+        if (warp == 0) {
+            // ------------------------------------------------------- MMA issuer
+            // The whole warp walks and waits; one lane issues.
+            const bool issuer = elect_one();
+            const uint32_t id_s = idesc_e4m3_f32(128, kATile);
+            const uint32_t id_o = idesc_e4m3_f32(128, (uint32_t)p.D) | kIdescBMn;
+            const int nk = (p.D + 31) / 32;
+            const uint64_t dk0 = smem_desc_kmajor(smem_u32(smem), 128);
+            const uint64_t dv0 = smem_desc_mn_sw128(smem_u32(smem), kASlotBytes);
+            const uint64_t dq0 = smem_desc_kmajor(smem_u32(sQ), 128);
+            const uint64_t dp0 = smem_desc_kmajor(smem_u32(sP), 128);
+            bool ok = true;
+            int tc = 0, sc = 0;
+            // O of tile t: (hi + lo) V
+            auto second = [&](int t) {
+                const int bf = t & 1, ph = (t >> 1) & 1, seq = 2 * t + 1, sl = seq % SLOTS;
+                ok = ok && mbar_wait(kv_full + sl, (seq / SLOTS) & 1, p.wait_ns);
+                ok = ok && mbar_wait(o_empty + bf, ph ^ 1, p.wait_ns);
+                ok = ok && mbar_wait(p_full + (t & 3), (t >> 2) & 1, p.wait_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) return;
+                tc_fence_after();
+                if (issuer) {
+                    const uint64_t a = dp0 + (uint64_t)(bf * (C::P_BYTES >> 4));
+                    const uint64_t b = dv0 + (uint64_t)(sl * (kASlotBytes >> 4));
+                    const uint32_t d = tmem + 256 + bf * 128;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)  // 32 keys a step
+                        umma_f8(d, a + 2 * k, b + k * (32 * 128 >> 4), id_o, k > 0);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_f8(d, a + (N * 128 >> 4) + 2 * k, b + k * (32 * 128 >> 4), id_o, 1);
+                    umma_commit(o_full + bf);
+                    umma_commit(kv_empty + sl);
+                }
+                __syncwarp();
+            };
+            while (ok && wk.next(p)) {
+                if (wk.gr.n == 0) continue;
+                const int qb = sc % QB;
+                ok = ok && mbar_wait(q_full + qb, (sc / QB) & 1, p.wait_ns);
+                for (int t = wk.t0; ok && t < wk.t1; ++t, ++tc) {
+                    const int seq = 2 * tc, sl = seq % SLOTS;
+                    ok = mbar_wait(kv_full + sl, (seq / SLOTS) & 1, p.wait_ns);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (issuer) {
+                        const uint64_t a = dq0 + (uint64_t)(qb * (C::Q_BYTES >> 4));
+                        const uint64_t b = dk0 + (uint64_t)(sl * (kASlotBytes >> 4));
+                        const uint32_t d = tmem + (tc & 1) * 128;
+                        // 32 dims a step, hi then lo
+                        if (nk == 4) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) umma_f8(d, a + 2 * k, b + 2 * k, id_s, k > 0);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) umma_f8(d, a + (N * 128 >> 4) + 2 * k, b + 2 * k, id_s, 1);
+                        } else {
+                            // (with `if (k < nk)` around unrolled products a build took wrong operands)
+#pragma unroll 1
+                            for (int k = 0; k < nk; ++k) umma_f8(d, a + 2 * k, b + 2 * k, id_s, k > 0);
+#pragma unroll 1
+                            for (int k = 0; k < nk; ++k) umma_f8(d, a + (N * 128 >> 4) + 2 * k, b + 2 * k, id_s, 1);
+                        }
+                        umma_commit(s_full + (tc & 1));
+                        umma_commit(kv_empty + sl);
+                        if (t == wk.t1 - 1) umma_commit(q_empty + qb);
+                    }
+                    __syncwarp();
+                    if (tc > 0) second(tc - 1);
+                }
+                ++sc;
+            }
+            if (ok && tc > 0) second(tc - 1);
+            if (!__all_sync(0xffffffffu, ok)) {  // products in flight end before the memory is given up
+                if (issuer) umma_commit(drain);
+                mbar_wait(drain, 0, p.wait_ns);
+            }
+        } else {
+            attn_queries<N, QB, C::QWARPS>(p, wk, x, warp - 1, lane);
+        }
+    } else if (warp < C::W_JOIN) {
+        // -------------------------------------------------------------- softmax
+        regs_inc<C::R_SOFT>();
+        const int grp = (warp - C::W_SOFT) >> 2, row = tid & 127, wg_warp = warp & 3;
+        const uint32_t lane_addr = tmem + ((uint32_t)(wg_warp * 32) << 16);
+        const bool works = wg_warp * 32 < rows;  // the warp has a row
+        const int st = attn_token(p, row);
+        bool ok = true;
+        int tc = 0, sc = 0;
+        while (wk.next(p)) {
+            if (wk.gr.n == 0) continue;
+            const int qb = sc % QB, s = wk.gr.st * p.TS + st;
+            int end = INT_MAX, least = INT_MAX;  // keys this row sees; keys every row sees
+            if (!p.idx) {
+                end = row < rows && s < p.S ? attn_end(p, wk.gr.b, s) : 0;
+                least = attn_end(p, wk.gr.b, wk.gr.st * p.TS);
+            }
+            ok = ok && mbar_wait(q_full + qb, (sc / QB) & 1, p.wait_ns);
+            const float qs = x.q_scale[qb * N + row];
+            float l = 0.f, m = -INFINITY;
+            for (int t = wk.t0; t < wk.t1; ++t, ++tc) {
+                if ((tc & 1) != grp) continue;
+                const int bf = tc & 1, ph = (tc >> 1) & 1, ms = tc % kAMeta;
+                ok = ok && mbar_wait(x.meta_full + ms, (tc / kAMeta) & 1, p.wait_ns);
+                const float* const ka = x.key_a + ms * kATile;
+                const float* const kl = x.key_lv + ms * kATile;
+                const float* const ki = x.key_iv + ms * kATile;
+                const bool flag = x.flag[ms] != 0;
+                const bool masked = flag || t * kATile + kATile > least;
+                // S of this tile is done, and with it all products issued before: those of O of the tile before last,
+                // so its weights' buffer is free, and so are the maxima of four tiles ago (a tile's O waits for the
+                // joining of the tile two before it)
+                ok = ok && mbar_wait(s_full + bf, ph, p.wait_ns);
+                tc_fence_after();
+                const uint32_t s_addr = lane_addr + bf * 128;
+                uint8_t* const prow = sP + bf * C::P_BYTES + row * 128;
+
+                auto one_tile = [&](auto mask_c, auto uni_c) {
+                    constexpr bool MASK = decltype(mask_c)::value, UNI = decltype(uni_c)::value;
+                    uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
+                    if constexpr (MASK) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int left = end - (t * kATile + 32 * i);  // keys of the word below the row's end
+                            vis[i] = x.seen[ms * 4 + i] & (left >= 32 ? ~0u : (left > 0 ? (1u << left) - 1 : 0u));
+                        }
+                    }
+                    float v[32], top = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        wide_scores<MASK, UNI>(s_addr + 32 * i, ka + 32 * i, kl + 32 * i, qs, vis[i], v);
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) top = fmaxf(top, fmaxf(v[k], v[k + 1]));
+                    }
+                    const float sh = top == -INFINITY ? kATop : kATop - top;
+                    const uint64_t sh2 = pack2(sh, sh);
+                    uint64_t sum0 = pack2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        wide_scores<MASK, UNI>(s_addr + 32 * i, ka + 32 * i, kl + 32 * i, qs, vis[i], v);
+                        uint32_t hi[8], lo[8];
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4) {
+                            float e0, e1, e2, e3;
+                            unpack2(add2(pack2(v[k], v[k + 1]), sh2), e0, e1);
+                            unpack2(add2(pack2(v[k + 2], v[k + 3]), sh2), e2, e3);
+                            const float w0 = exp2_approx(e0), w1 = exp2_approx(e1);
+                            const float w2 = exp2_approx(e2), w3 = exp2_approx(e3);
+                            if constexpr (UNI) {
+                                const float iv = ki[32 * i + (k & 16)];
+                                sum0 = fma2(pack2(w0, w1), pack2(iv, iv), sum0);
+                                sum1 = fma2(pack2(w2, w3), pack2(iv, iv), sum1);
+                            } else {
+                                const float4 iv = *reinterpret_cast<const float4*>(ki + 32 * i + k);
+                                sum0 = fma2(pack2(w0, w1), pack2(iv.x, iv.y), sum0);
+                                sum1 = fma2(pack2(w2, w3), pack2(iv.z, iv.w), sum1);
+                            }
+                            uint32_t h0, l0, h1, l1;
+                            split_e4m3(w0, w1, h0, l0);
+                            split_e4m3(w2, w3, h1, l1);
+                            hi[k / 4] = h0 | (h1 << 16);
+                            lo[k / 4] = l0 | (l1 << 16);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int j = (2 * i + k) ^ (row & 7);  // 128-byte swizzle
+                            *reinterpret_cast<uint4*>(prow + (j << 4)) =
+                                make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
+                            *reinterpret_cast<uint4*>(prow + N * 128 + (j << 4)) =
+                                make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
+                        }
+                    }
+                    float a0, a1, b0, b1;
+                    unpack2(sum0, a0, a1);
+                    unpack2(sum1, b0, b1);
+                    const float mn = fmaxf(m, top);
+                    if (top != -INFINITY) {
+                        l = (m == -INFINITY ? 0.f : l * exp2_approx(m - mn)) + ((a0 + a1) + (b0 + b1)) * exp2_approx(top - mn);
+                        m = mn;
+                    }
+                    sMt[(tc & 3) * N + row] = top;
+                };
+                if (works) {
+                    if (p.idx) {
+                        if (masked)
+                            one_tile(std::true_type{}, std::false_type{});
+                        else
+                            one_tile(std::false_type{}, std::false_type{});
+                    } else {
+                        if (masked)
+                            one_tile(std::true_type{}, std::true_type{});
+                        else
+                            one_tile(std::false_type{}, std::true_type{});
+                    }
+                }
+                if (flag) {
+                    // unseen slots may hold anything (NaN codes): a zero weight alone would not keep them out.
+                    // Thread i clears V's row i.
+                    const int seq = 2 * tc + 1, sl = seq % SLOTS;
+                    ok = ok && mbar_wait(kv_full + sl, (seq / SLOTS) & 1, p.wait_ns);
+                    if (ok && !((x.seen[ms * 4 + wg_warp] >> lane) & 1)) {
+                        uint4* vrow = reinterpret_cast<uint4*>(smem + sl * kASlotBytes + row * 128);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) vrow[i] = make_uint4(0, 0, 0, 0);
+                    }
+                }
+                fence_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(x.meta_empty + ms);
+                    mbar_arrive(p_full + (tc & 3));
+                }
+            }
+            ok = ok && mbar_wait(l_empty, (sc & 1) ^ 1, p.wait_ns);
+            sL[grp * N + row] = make_float2(l, m);
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(l_full);
+                mbar_arrive(q_empty + qb);
+            }
+            ++sc;
+        }
+    } else if (warp < C::W_JOIN + 4) {
+        // ---------------------------------------------------------------- joining
+        // A thread has one row: its D outputs, maximum and sum.
+        regs_inc<C::R_JOIN>();
+        const int row = tid & 127, wg_warp = warp & 3;
+        const uint32_t lane_addr = tmem + ((uint32_t)(wg_warp * 32) << 16) + 256;
+        const bool works = wg_warp * 32 < rows;
+        const int st = attn_token(p, row);
+        bool ok = true;
+        int tc = 0, sc = 0;
+        AttnHeader hd{0, 0, 0, 0};
+        float* const parts = (float*)(p.ws + (size_t)gridDim.x * sizeof(AttnHeader));
+        while (wk.next(p)) {
+            float acc[128];
+#pragma unroll
+            for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+            float m = -INFINITY, l = 0.f;
+            if (wk.gr.n > 0) {
+                for (int t = wk.t0; t < wk.t1; ++t, ++tc) {
+                    const int bf = tc & 1, ph = (tc >> 1) & 1;
+                    // (four barriers: the softmax may be three tiles ahead of the joining)
+                    ok = ok && mbar_wait(p_full + (tc & 3), (tc >> 2) & 1, p.wait_ns);
+                    const float top = works ? sMt[(tc & 3) * N + row] : -INFINITY;
+                    ok = ok && mbar_wait(o_full + bf, ph, p.wait_ns);
+                    tc_fence_after();
+                    if (works) {
+                        const float mn = fmaxf(m, top);
+                        const float fa = m == -INFINITY ? 0.f : exp2_approx(m - mn);
+                        const float fb = top == -INFINITY ? 0.f : exp2_approx(top - mn);
+                        const uint64_t fa2 = pack2(fa, fa), fb2 = pack2(fb, fb);
+                        m = mn;
+#pragma unroll
+                        for (int cc = 0; cc < 128; cc += 16) {
+                            if (cc < p.D) {
+                                uint32_t r[16];
+                                tmem_ld16(lane_addr + bf * 128 + cc, r);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int i = 0; i < 16; i += 2) {
+                                    const uint64_t o = mul2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), fb2);
+                                    unpack2(fma2(pack2(acc[cc + i], acc[cc + i + 1]), fa2, o), acc[cc + i], acc[cc + i + 1]);
+                                }
+                            }
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(o_empty + bf);
+                }
+                ok = ok && mbar_wait(l_full, sc & 1, p.wait_ns);
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const float2 lm = sL[g * N + row];
+                    if (lm.y != -INFINITY) l += lm.x * exp2_approx(lm.y - m);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(l_empty);
+                ++sc;
+            }
+            const bool whole = wk.t0 == 0 && wk.t1 == wk.gr.w;
+            if (whole) {
+                const int s = wk.gr.st * p.TS + st;
+                if (row < rows && s < p.S) {
+                    const int at = (wk.gr.b * p.S + s) * p.Hq + wk.h * p.G + row - st * p.G;
+                    const float inv = l > 0.f ? 1.f / l : 0.f;
+                    uint4* out = reinterpret_cast<uint4*>(p.out + (int64_t)at * p.D);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        if (8 * i < p.D) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const __nv_bfloat162 h =
+                                    __floats2bfloat162_rn(acc[8 * i + 2 * k] * inv, acc[8 * i + 2 * k + 1] * inv);
+                                w[k] = *reinterpret_cast<const uint32_t*>(&h);
+                            }
+                            out[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                    if (p.lse) p.lse[at] = l > 0.f ? (m + log2f(l) - kATop) * kALn2 : -INFINITY;
+                }
+            } else {
+                const int slot = 2 * c + (wk.first ? 0 : 1);
+                float* part = parts + slot * attn_part_floats(N);
+                if (works) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        reinterpret_cast<float4*>(part + row * 128)[i] =
+                            make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+                    part[N * 128 + row] = m;
+                    part[N * 128 + N + row] = l;
+                }
+                if (wk.t0 == 0)  // place unit_end - 1 is in the share of the last CTA that begins at or before it
+                    hd = AttnHeader{(int32_t)((wk.unit_end * nc - 1) / W), wk.g, wk.h, slot};
+            }
+        }
+        if (row == 0) reinterpret_cast<AttnHeader*>(p.ws)[c] = hd;
+    } else {
+        regs_dec<C::R_PROD>();
+        attn_produce<SLOTS, C::PRODUCERS>(p, wk, x, &tmk, &tmv, warp - C::W_PROD, lane);
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM);
+    }
+}
+
+cudaError_t attn_launch_wide(const CUtensorMap& mk, const CUtensorMap& mv, const AttnParams& p, int grid, cudaStream_t st) {
+    cudaError_t e = set_smem_attr((const void*)cache_attn_wide_kernel, WideCfg::TOTAL);
+    if (e != cudaSuccess) return e;
+    cache_attn_wide_kernel<<<grid, WideCfg::THREADS, WideCfg::TOTAL, st>>>(mk, mv, p);
+    return cudaGetLastError();
+}
+
+LIDX_STATUS_READER(status_cache_attn_wide)
+
+}  // namespace lidx

@@ -122,5 +122,6 @@ int status_score_v41(int clear);
 int status_misc(int clear);
 int status_bwd(int clear);
 int status_cache_attn(int clear);
+int status_cache_attn_wide(int clear);
 
 }  // namespace lidx
