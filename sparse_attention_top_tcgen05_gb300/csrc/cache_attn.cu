@@ -155,7 +155,8 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
     uint32_t* tmem_slot = (uint32_t*)(smem + C::OFF_MISC);
     int64_t* const scan = (int64_t*)(smem + C::OFF_MISC + 8);  // [34]
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // the warp's number by a shuffle: known to be uniform, so a role's counters and descriptors live in uniform registers
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < SLOTS; ++i) {
             mbar_init(kv_full + i, p.idx ? C::PRODUCERS : 1);

@@ -411,9 +411,10 @@ __device__ __forceinline__ void attn_produce(const AttnParams& p, AttnWalk& wk, 
     }
 }
 
-// Query rows of a unit, bf16 -> e4m3 hi and lo: one of QWARPS warps.
+// Query rows of a unit, bf16 -> e4m3 hi and lo: one of QWARPS warps.  twice: rows 0 .. 63 are repeated as 64 .. 127.
 template <int N, int QB, int QWARPS>
-__device__ __forceinline__ void attn_queries(const AttnParams& p, AttnWalk& wk, const AttnPipe& x, int qw, int lane) {
+__device__ __forceinline__ void attn_queries(const AttnParams& p, AttnWalk& wk, const AttnPipe& x, int qw, int lane,
+                                             bool twice = false) {
     // Eight lanes a row, 16 dims each, four rows a warp at a time.
     bool ok = true;
     int sc = 0;
@@ -439,8 +440,9 @@ __device__ __forceinline__ void attn_queries(const AttnParams& p, AttnWalk& wk, 
         const int first = qw * 4 + (lane >> 3);
         load(first, n0, n1);
         load(first + step, f0, f1);
+        const int last = twice ? 64 : N;
 #pragma unroll 1
-        for (int n = first; n < N; n += step) {
+        for (int n = first; n < last; n += step) {
             const uint32_t w[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
             n0 = f0, n1 = f1;
             load(n + 2 * step, f0, f1);
@@ -470,6 +472,11 @@ __device__ __forceinline__ void attn_queries(const AttnParams& p, AttnWalk& wk, 
             uint8_t* at = dst + n * 128 + ((sub ^ (n & 7)) << 4);  // 128-byte swizzle
             *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4*>(at + N * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            if (twice) {
+                if (sub == 0) x.q_scale[qb * N + n + 64] = __int_as_float((ex - 7) << 23);
+                *reinterpret_cast<uint4*>(at + 64 * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(at + (N + 64) * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
         }
         fence_async_smem();
         __syncwarp();

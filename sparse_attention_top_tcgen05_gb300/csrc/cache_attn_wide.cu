@@ -5,6 +5,11 @@
 // its own registers, and nothing crosses lanes or waits at a barrier.  That costs half of the instructions that a thread
 // for each key costs from 64 rows on (10.2k -> 5.3k a tile of 128 x 128), but lanes without a row have no work, so
 // units of up to 32 rows stay with the other kernel.
+//
+// Units of at most 64 rows (one selected row of 64 heads, a decode step on a shared key head) are laid out twice: row r
+// again as row r + 64.  Of a tile's keys the first copy's weights hold the first 64, the second copy's the others (zeros
+// elsewhere), so all four warps of a softmax group work, on half of the keys each, with the scores kept in registers;
+// each copy has its own maximum and sum, and the joining warps add the copies when a segment ends.
 #include "cache_attn.cuh"
 
 namespace lidx {
@@ -20,7 +25,8 @@ struct WideCfg {
     static constexpr int OFF_MT = OFF_QS + QB * N * 4;                   // [4][N] tile maxima
     static constexpr int OFF_L = OFF_MT + 4 * N * 4;                     // [2][N] float2: a group's sum, its reference
     static constexpr int OFF_GATHER = OFF_L + 2 * N * 8;                 // [128] cache rows of a tile's keys
-    static constexpr int OFF_BAR = OFF_GATHER + kATile * 4;
+    static constexpr int OFF_X = OFF_GATHER + kATile * 4;                // [16][64] dims of the second copies
+    static constexpr int OFF_BAR = OFF_X + 16 * 64 * 4;
     static constexpr int NBAR = 2 * SLOTS + 2 * kAMeta + 2 * 2 + 3 * 2 + 4 + 2 + 1;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int TOTAL = OFF_MISC + 288 + 1024;
@@ -110,7 +116,8 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
     uint32_t* tmem_slot = (uint32_t*)(smem + C::OFF_MISC);
     int64_t* const scan = (int64_t*)(smem + C::OFF_MISC + 8);  // [34]
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // the warp's number by a shuffle: known to be uniform, so a role's counters and descriptors live in uniform registers
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < SLOTS; ++i) {
             mbar_init(kv_full + i, p.idx ? C::PRODUCERS : 1);
@@ -147,6 +154,7 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int rows = p.TS * p.G;  // of a unit
+    const bool twice = rows <= 64;
 
     if (warp < 4) {
         regs_dec<C::R_MMA>();
@@ -172,10 +180,10 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) return;
                 tc_fence_after();
+                const uint64_t a = dp0 + (uint64_t)(bf * (C::P_BYTES >> 4));
+                const uint64_t b = dv0 + (uint64_t)(sl * (kASlotBytes >> 4));
+                const uint32_t d = tmem + 256 + bf * 128;
                 if (issuer) {
-                    const uint64_t a = dp0 + (uint64_t)(bf * (C::P_BYTES >> 4));
-                    const uint64_t b = dv0 + (uint64_t)(sl * (kASlotBytes >> 4));
-                    const uint32_t d = tmem + 256 + bf * 128;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)  // 32 keys a step
                         umma_f8(d, a + 2 * k, b + k * (32 * 128 >> 4), id_o, k > 0);
@@ -197,10 +205,10 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc_fence_after();
+                    const uint64_t a = dq0 + (uint64_t)(qb * (C::Q_BYTES >> 4));
+                    const uint64_t b = dk0 + (uint64_t)(sl * (kASlotBytes >> 4));
+                    const uint32_t d = tmem + (tc & 1) * 128;
                     if (issuer) {
-                        const uint64_t a = dq0 + (uint64_t)(qb * (C::Q_BYTES >> 4));
-                        const uint64_t b = dk0 + (uint64_t)(sl * (kASlotBytes >> 4));
-                        const uint32_t d = tmem + (tc & 1) * 128;
                         // 32 dims a step, hi then lo
                         if (nk == 4) {
 #pragma unroll
@@ -229,15 +237,25 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                 mbar_wait(drain, 0, p.wait_ns);
             }
         } else {
-            attn_queries<N, QB, C::QWARPS>(p, wk, x, warp - 1, lane);
+            attn_queries<N, QB, C::QWARPS>(p, wk, x, warp - 1, lane, twice);
         }
     } else if (warp < C::W_JOIN) {
         // -------------------------------------------------------------- softmax
         regs_inc<C::R_SOFT>();
         const int grp = (warp - C::W_SOFT) >> 2, row = tid & 127, wg_warp = warp & 3;
         const uint32_t lane_addr = tmem + ((uint32_t)(wg_warp * 32) << 16);
-        const bool works = wg_warp * 32 < rows;  // the warp has a row
-        const int st = attn_token(p, row);
+        const int n = twice ? row & 63 : row;                                 // row of the unit
+        const bool works = (twice ? wg_warp & 1 : wg_warp) * 32 < rows;       // the warp has a row
+        const int st = attn_token(p, n);
+        if (twice) {  // the other half of the keys has no weight in this copy, ever
+            uint8_t* const mine = sP + grp * C::P_BYTES + row * 128;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = ((row < 64 ? 4 : 0) + i) ^ (row & 7);
+                *reinterpret_cast<uint4*>(mine + (j << 4)) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(mine + N * 128 + (j << 4)) = make_uint4(0, 0, 0, 0);
+            }
+        }
         bool ok = true;
         int tc = 0, sc = 0;
         while (wk.next(p)) {
@@ -245,7 +263,7 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
             const int qb = sc % QB, s = wk.gr.st * p.TS + st;
             int end = INT_MAX, least = INT_MAX;  // keys this row sees; keys every row sees
             if (!p.idx) {
-                end = row < rows && s < p.S ? attn_end(p, wk.gr.b, s) : 0;
+                end = n < rows && s < p.S ? attn_end(p, wk.gr.b, s) : 0;
                 least = attn_end(p, wk.gr.b, wk.gr.st * p.TS);
             }
             ok = ok && mbar_wait(q_full + qb, (sc / QB) & 1, p.wait_ns);
@@ -268,43 +286,52 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                 const uint32_t s_addr = lane_addr + bf * 128;
                 uint8_t* const prow = sP + bf * C::P_BYTES + row * 128;
 
-                auto one_tile = [&](auto mask_c, auto uni_c) {
+                // TWICE: chunks of 32 keys [2 half, 2 half + 2), scores kept; else all four, computed twice
+                auto one_tile = [&](auto mask_c, auto uni_c, auto twice_c) {
                     constexpr bool MASK = decltype(mask_c)::value, UNI = decltype(uni_c)::value;
-                    uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
-                    if constexpr (MASK) {
+                    constexpr bool TWICE = decltype(twice_c)::value;
+                    constexpr int NCH = TWICE ? 2 : 4, KEEP = TWICE ? 2 : 1;
+                    const int c0 = TWICE && row >= 64 ? 2 : 0;
+                    uint32_t vis[NCH];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int left = end - (t * kATile + 32 * i);  // keys of the word below the row's end
-                            vis[i] = x.seen[ms * 4 + i] & (left >= 32 ? ~0u : (left > 0 ? (1u << left) - 1 : 0u));
+                    for (int i = 0; i < NCH; ++i) {
+                        vis[i] = ~0u;
+                        if constexpr (MASK) {
+                            const int left = end - (t * kATile + 32 * (c0 + i));  // keys of the word below the row's end
+                            vis[i] = x.seen[ms * 4 + c0 + i] & (left >= 32 ? ~0u : (left > 0 ? (1u << left) - 1 : 0u));
                         }
                     }
-                    float v[32], top = -INFINITY;
+                    float v[KEEP][32], top = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        wide_scores<MASK, UNI>(s_addr + 32 * i, ka + 32 * i, kl + 32 * i, qs, vis[i], v);
+                    for (int i = 0; i < NCH; ++i) {
+                        const int at = 32 * (c0 + i);
+                        float(&u)[32] = v[TWICE ? i : 0];
+                        wide_scores<MASK, UNI>(s_addr + at, ka + at, kl + at, qs, vis[i], u);
 #pragma unroll
-                        for (int k = 0; k < 32; k += 2) top = fmaxf(top, fmaxf(v[k], v[k + 1]));
+                        for (int k = 0; k < 32; k += 2) top = fmaxf(top, fmaxf(u[k], u[k + 1]));
                     }
                     const float sh = top == -INFINITY ? kATop : kATop - top;
                     const uint64_t sh2 = pack2(sh, sh);
                     uint64_t sum0 = pack2(0.f, 0.f), sum1 = sum0;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        wide_scores<MASK, UNI>(s_addr + 32 * i, ka + 32 * i, kl + 32 * i, qs, vis[i], v);
+                    for (int i = 0; i < NCH; ++i) {
+                        const int at = 32 * (c0 + i);
+                        float(&u)[32] = v[TWICE ? i : 0];
+                        if constexpr (!TWICE) wide_scores<MASK, UNI>(s_addr + at, ka + at, kl + at, qs, vis[i], u);
                         uint32_t hi[8], lo[8];
 #pragma unroll
                         for (int k = 0; k < 32; k += 4) {
                             float e0, e1, e2, e3;
-                            unpack2(add2(pack2(v[k], v[k + 1]), sh2), e0, e1);
-                            unpack2(add2(pack2(v[k + 2], v[k + 3]), sh2), e2, e3);
+                            unpack2(add2(pack2(u[k], u[k + 1]), sh2), e0, e1);
+                            unpack2(add2(pack2(u[k + 2], u[k + 3]), sh2), e2, e3);
                             const float w0 = exp2_approx(e0), w1 = exp2_approx(e1);
                             const float w2 = exp2_approx(e2), w3 = exp2_approx(e3);
                             if constexpr (UNI) {
-                                const float iv = ki[32 * i + (k & 16)];
+                                const float iv = ki[at + (k & 16)];
                                 sum0 = fma2(pack2(w0, w1), pack2(iv, iv), sum0);
                                 sum1 = fma2(pack2(w2, w3), pack2(iv, iv), sum1);
                             } else {
-                                const float4 iv = *reinterpret_cast<const float4*>(ki + 32 * i + k);
+                                const float4 iv = *reinterpret_cast<const float4*>(ki + at + k);
                                 sum0 = fma2(pack2(w0, w1), pack2(iv.x, iv.y), sum0);
                                 sum1 = fma2(pack2(w2, w3), pack2(iv.z, iv.w), sum1);
                             }
@@ -316,7 +343,7 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                         }
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const int j = (2 * i + k) ^ (row & 7);  // 128-byte swizzle
+                            const int j = (2 * (c0 + i) + k) ^ (row & 7);  // 128-byte swizzle
                             *reinterpret_cast<uint4*>(prow + (j << 4)) =
                                 make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
                             *reinterpret_cast<uint4*>(prow + N * 128 + (j << 4)) =
@@ -334,16 +361,18 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                     sMt[(tc & 3) * N + row] = top;
                 };
                 if (works) {
-                    if (p.idx) {
-                        if (masked)
-                            one_tile(std::true_type{}, std::false_type{});
+                    const std::true_type yes{};
+                    const std::false_type no{};
+                    if (twice) {
+                        if (p.idx)
+                            masked ? one_tile(yes, no, yes) : one_tile(no, no, yes);
                         else
-                            one_tile(std::false_type{}, std::false_type{});
+                            masked ? one_tile(yes, yes, yes) : one_tile(no, yes, yes);
                     } else {
-                        if (masked)
-                            one_tile(std::true_type{}, std::true_type{});
+                        if (p.idx)
+                            masked ? one_tile(yes, no, no) : one_tile(no, no, no);
                         else
-                            one_tile(std::false_type{}, std::true_type{});
+                            masked ? one_tile(yes, yes, no) : one_tile(no, yes, no);
                     }
                 }
                 if (flag) {
@@ -380,8 +409,11 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
         regs_inc<C::R_JOIN>();
         const int row = tid & 127, wg_warp = warp & 3;
         const uint32_t lane_addr = tmem + ((uint32_t)(wg_warp * 32) << 16) + 256;
-        const bool works = wg_warp * 32 < rows;
-        const int st = attn_token(p, row);
+        const int n = twice ? row & 63 : row;
+        const bool works = (twice ? wg_warp & 1 : wg_warp) * 32 < rows;
+        const bool writes = n < rows && row == n;  // the first copy of a row
+        const int st = attn_token(p, n);
+        float* const sX = (float*)(smem + C::OFF_X);
         bool ok = true;
         int tc = 0, sc = 0;
         AttnHeader hd{0, 0, 0, 0};
@@ -410,12 +442,15 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                             if (cc < p.D) {
                                 uint32_t r[16];
                                 tmem_ld16(lane_addr + bf * 128 + cc, r);
+#pragma unroll
+                                for (int i = 0; i < 16; i += 2)
+                                    unpack2(mul2(pack2(acc[cc + i], acc[cc + i + 1]), fa2), acc[cc + i], acc[cc + i + 1]);
                                 tmem_ld_wait();
 #pragma unroll
-                                for (int i = 0; i < 16; i += 2) {
-                                    const uint64_t o = mul2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), fb2);
-                                    unpack2(fma2(pack2(acc[cc + i], acc[cc + i + 1]), fa2, o), acc[cc + i], acc[cc + i + 1]);
-                                }
+                                for (int i = 0; i < 16; i += 2)
+                                    unpack2(fma2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), fb2,
+                                                 pack2(acc[cc + i], acc[cc + i + 1])),
+                                            acc[cc + i], acc[cc + i + 1]);
                             }
                         }
                     }
@@ -433,11 +468,37 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                 if (lane == 0) mbar_arrive(l_empty);
                 ++sc;
             }
+            if (twice && wk.gr.n > 0) {
+                // the copies' maxima and sums, then 16 dims at a time
+                sX[row] = m;
+                sX[128 + row] = l;
+                named_bar_sync(1, 128);
+                const float mo = sX[row ^ 64], lo = sX[128 + (row ^ 64)], mm = fmaxf(m, mo);
+                const float f = m == -INFINITY ? 0.f : exp2_approx(m - mm), fo = mo == -INFINITY ? 0.f : exp2_approx(mo - mm);
+                l = l * f + lo * fo;
+                m = mm;
+#pragma unroll
+                for (int cc = 0; cc < 128; cc += 16) {
+                    if (cc < p.D) {
+                        named_bar_sync(1, 128);  // what was there is read
+                        if (row >= 64) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) sX[i * 64 + n] = acc[cc + i] * f;
+                        }
+                        named_bar_sync(1, 128);
+                        if (row < 64) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) acc[cc + i] = acc[cc + i] * f + sX[i * 64 + n];
+                        }
+                    }
+                }
+                named_bar_sync(1, 128);
+            }
             const bool whole = wk.t0 == 0 && wk.t1 == wk.gr.w;
             if (whole) {
                 const int s = wk.gr.st * p.TS + st;
-                if (row < rows && s < p.S) {
-                    const int at = (wk.gr.b * p.S + s) * p.Hq + wk.h * p.G + row - st * p.G;
+                if (writes && s < p.S) {
+                    const int at = (wk.gr.b * p.S + s) * p.Hq + wk.h * p.G + n - st * p.G;
                     const float inv = l > 0.f ? 1.f / l : 0.f;
                     uint4* out = reinterpret_cast<uint4*>(p.out + (int64_t)at * p.D);
 #pragma unroll
@@ -458,7 +519,7 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
             } else {
                 const int slot = 2 * c + (wk.first ? 0 : 1);
                 float* part = parts + slot * attn_part_floats(N);
-                if (works) {
+                if (writes) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         reinterpret_cast<float4*>(part + row * 128)[i] =
