@@ -40,7 +40,7 @@ struct AttnParams {
 
 constexpr int kATile = 128;                     // keys of a tile
 constexpr int kASlotBytes = kATile * 128;       // one K or V tile: 128 bytes a key (zero past D)
-constexpr int kAMeta = 5;                       // stages of per-key scales
+constexpr int kAMeta = 6;                       // stages of per-key scales
 constexpr float kATop = 8.f;                    // weights are scaled to 2^8
 constexpr float kALn2 = 0.693147180559945309f;
 

@@ -15,10 +15,9 @@
 namespace lidx {
 
 struct WideCfg {
-    static constexpr int N = 128, QB = 2, SLOTS = 5;
-    static constexpr int Q_BYTES = 2 * N * 128, P_BYTES = 2 * N * 128;  // hi and lo
-    static constexpr int OFF_P = SLOTS * kASlotBytes;
-    static constexpr int OFF_Q = OFF_P + 2 * P_BYTES;
+    static constexpr int N = 128, QB = 2, SLOTS = 9;
+    static constexpr int Q_BYTES = 2 * N * 128;  // hi and lo
+    static constexpr int OFF_Q = SLOTS * kASlotBytes;
     static constexpr int OFF_META = OFF_Q + QB * Q_BYTES;                // [3][kAMeta][128] of the keys
     static constexpr int OFF_SEEN = OFF_META + 3 * kAMeta * kATile * 4;  // [kAMeta][4], then [kAMeta] flags
     static constexpr int OFF_QS = OFF_SEEN + 128;                        // [QB][N] query scales
@@ -85,7 +84,6 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
     constexpr int N = C::N, SLOTS = C::SLOTS, QB = C::QB;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint8_t* const sP = smem + C::OFF_P;
     uint8_t* const sQ = smem + C::OFF_Q;
     float* const sMt = (float*)(smem + C::OFF_MT);
     float2* const sL = (float2*)(smem + C::OFF_L);
@@ -168,7 +166,6 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
             const uint64_t dk0 = smem_desc_kmajor(smem_u32(smem), 128);
             const uint64_t dv0 = smem_desc_mn_sw128(smem_u32(smem), kASlotBytes);
             const uint64_t dq0 = smem_desc_kmajor(smem_u32(sQ), 128);
-            const uint64_t dp0 = smem_desc_kmajor(smem_u32(sP), 128);
             bool ok = true;
             int tc = 0, sc = 0;
             // O of tile t: (hi + lo) V
@@ -180,16 +177,16 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) return;
                 tc_fence_after();
-                const uint64_t a = dp0 + (uint64_t)(bf * (C::P_BYTES >> 4));
+                const uint32_t a = tmem + bf * 128;  // the weights, in the columns of the tile's S
                 const uint64_t b = dv0 + (uint64_t)(sl * (kASlotBytes >> 4));
                 const uint32_t d = tmem + 256 + bf * 128;
                 if (issuer) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)  // 32 keys a step
-                        umma_f8(d, a + 2 * k, b + k * (32 * 128 >> 4), id_o, k > 0);
+                        umma_f8_ts(d, a + 16 * k, b + k * (32 * 128 >> 4), id_o, k > 0);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        umma_f8(d, a + (N * 128 >> 4) + 2 * k, b + k * (32 * 128 >> 4), id_o, 1);
+                        umma_f8_ts(d, a + 16 * k + 8, b + k * (32 * 128 >> 4), id_o, 1);
                     umma_commit(o_full + bf);
                     umma_commit(kv_empty + sl);
                 }
@@ -247,15 +244,6 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
         const int n = twice ? row & 63 : row;                                 // row of the unit
         const bool works = (twice ? wg_warp & 1 : wg_warp) * 32 < rows;       // the warp has a row
         const int st = attn_token(p, n);
-        if (twice) {  // the other half of the keys has no weight in this copy, ever
-            uint8_t* const mine = sP + grp * C::P_BYTES + row * 128;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int j = ((row < 64 ? 4 : 0) + i) ^ (row & 7);
-                *reinterpret_cast<uint4*>(mine + (j << 4)) = make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4*>(mine + N * 128 + (j << 4)) = make_uint4(0, 0, 0, 0);
-            }
-        }
         bool ok = true;
         int tc = 0, sc = 0;
         while (wk.next(p)) {
@@ -284,7 +272,6 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                 ok = ok && mbar_wait(s_full + bf, ph, p.wait_ns);
                 tc_fence_after();
                 const uint32_t s_addr = lane_addr + bf * 128;
-                uint8_t* const prow = sP + bf * C::P_BYTES + row * 128;
 
                 // TWICE: chunks of 32 keys [2 half, 2 half + 2), scores kept; else all four, computed twice
                 auto one_tile = [&](auto mask_c, auto uni_c, auto twice_c) {
@@ -318,7 +305,7 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                         const int at = 32 * (c0 + i);
                         float(&u)[32] = v[TWICE ? i : 0];
                         if constexpr (!TWICE) wide_scores<MASK, UNI>(s_addr + at, ka + at, kl + at, qs, vis[i], u);
-                        uint32_t hi[8], lo[8];
+                        uint32_t w[16];  // hi and lo of 32 keys
 #pragma unroll
                         for (int k = 0; k < 32; k += 4) {
                             float e0, e1, e2, e3;
@@ -338,18 +325,19 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                             uint32_t h0, l0, h1, l1;
                             split_e4m3(w0, w1, h0, l0);
                             split_e4m3(w2, w3, h1, l1);
-                            hi[k / 4] = h0 | (h1 << 16);
-                            lo[k / 4] = l0 | (l1 << 16);
+                            w[k / 4] = h0 | (h1 << 16);
+                            w[8 + k / 4] = l0 | (l1 << 16);
                         }
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int j = (2 * (c0 + i) + k) ^ (row & 7);  // 128-byte swizzle
-                            *reinterpret_cast<uint4*>(prow + (j << 4)) =
-                                make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
-                            *reinterpret_cast<uint4*>(prow + N * 128 + (j << 4)) =
-                                make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
-                        }
+                        tmem_st16(s_addr + at / 2, w);  // columns whose scores have been read
                     }
+                    if constexpr (TWICE) {  // the other half of the keys has no weight in this copy
+                        uint32_t z[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) z[k] = 0;
+                        tmem_st16(s_addr + (c0 ^ 2) * 16, z);
+                        tmem_st16(s_addr + (c0 ^ 2) * 16 + 16, z);
+                    }
+                    tmem_st_wait();
                     float a0, a1, b0, b1;
                     unpack2(sum0, a0, a1);
                     unpack2(sum1, b0, b1);
