@@ -15,7 +15,7 @@
 namespace lidx {
 
 struct WideCfg {
-    static constexpr int N = 128, QB = 2, SLOTS = 9;
+    static constexpr int N = 128, QB = 2, SLOTS = 8;
     static constexpr int Q_BYTES = 2 * N * 128;  // hi and lo
     static constexpr int OFF_Q = SLOTS * kASlotBytes;
     static constexpr int OFF_META = OFF_Q + QB * Q_BYTES;                // [3][kAMeta][128] of the keys
