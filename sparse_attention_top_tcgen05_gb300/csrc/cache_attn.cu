@@ -584,10 +584,12 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
     }
 }
 
-// Joins the parts of the units that were cut: block (c, y) takes rows y, y + gridDim.y, ... of the unit whose first
-// tiles CTA c had.  The parts follow each other in the workspace (two slots a CTA).  Four groups of 128 threads take
-// every fourth part and are added in order.
+// Joins the parts of the units that were cut: block (c, y) takes kJoinRows rows of the unit whose first tiles CTA c had.
+// The parts follow each other in the workspace (two slots a CTA).  Four groups of 128 threads: with few parts each
+// takes a row, with many each takes every fourth part of one row after the other, added in order.
 constexpr int kJoinThreads = 512;
+constexpr int kJoinRows = 4;
+constexpr int kJoinFew = 8;
 constexpr int kJoinMaxParts = 1024;  // more than SMs of a device
 template <int N>
 __global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __grid_constant__ AttnParams p, int nc) {
@@ -601,9 +603,38 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __g
     auto part_of = [&](int i) {
         return parts + (size_t)(i == 0 ? hd.slot : 2 * (blockIdx.x + i)) * attn_part_floats(N);
     };
-    for (int n = blockIdx.y; n < p.TS * p.G; n += gridDim.y) {
-        const int st = attn_token(p, n), s = st0 + st;
-        if (s >= p.S) break;  // uniform
+    auto write = [&](int n, float m, float l, float o) {
+        const int st = attn_token(p, n);
+        const int64_t row = ((int64_t)b * p.S + st0 + st) * p.Hq + hd.h * p.G + n - st * p.G;
+        if (d < p.D) reinterpret_cast<__nv_bfloat16*>(p.out)[row * p.D + d] = __float2bfloat16_rn(l > 0.f ? o / l : 0.f);
+        if (p.lse && d == 0) p.lse[row] = l > 0.f ? (m + log2f(l) - kATop) * kALn2 : -INFINITY;
+    };
+    const int rows = min(p.TS, p.S - st0) * p.G, n0 = blockIdx.y * kJoinRows;
+    if (P <= kJoinFew) {
+        const int n = n0 + quarter;
+        if (n >= rows) return;
+        float pm[kJoinFew], pl[kJoinFew], po[kJoinFew], m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kJoinFew; ++i) {
+            const float* part = part_of(min(i, P - 1));
+            pm[i] = i < P ? part[N * 128 + n] : -INFINITY;
+            pl[i] = part[N * 128 + N + n];
+            po[i] = d < p.D ? part[n * 128 + d] : 0.f;
+            m = fmaxf(m, pm[i]);
+        }
+        float l = 0.f, o = 0.f;
+#pragma unroll
+        for (int i = 0; i < kJoinFew; ++i) {
+            const float f = pm[i] == -INFINITY ? 0.f : exp2_approx(pm[i] - m);
+            if (f > 0.f) {
+                l += pl[i] * f;
+                o += po[i] * f;
+            }
+        }
+        write(n, m, l, o);
+        return;
+    }
+    for (int n = n0; n < min(n0 + kJoinRows, rows); ++n) {
         float m = -INFINITY;
         for (int i = tid; i < P; i += kJoinThreads) m = fmaxf(m, part_of(i)[N * 128 + n]);
         m = warp_max(m);
@@ -626,16 +657,13 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __g
 #pragma unroll
         for (int i = 0; i < kJoinThreads / 32; ++i) l += s_red[1][i];
         float o = 0.f;
+        if (d < p.D) {
 #pragma unroll 4
-        for (int i = quarter; i < P; i += 4) o += part_of(i)[n * 128 + d] * s_f[i];
+            for (int i = quarter; i < P; i += 4) o += part_of(i)[n * 128 + d] * s_f[i];
+        }
         if (quarter > 0) s_o[quarter - 1][d] = o;
         __syncthreads();
-        const int64_t row = ((int64_t)b * p.S + s) * p.Hq + hd.h * p.G + n - st * p.G;
-        if (tid < p.D) {
-            o = ((o + s_o[0][d]) + s_o[1][d]) + s_o[2][d];
-            reinterpret_cast<__nv_bfloat16*>(p.out)[row * p.D + d] = __float2bfloat16_rn(l > 0.f ? o / l : 0.f);
-        }
-        if (p.lse && tid == 0) p.lse[row] = l > 0.f ? (m + log2f(l) - kATop) * kALn2 : -INFINITY;
+        if (quarter == 0) write(n, m, l, ((o + s_o[0][d]) + s_o[1][d]) + s_o[2][d]);
         __syncthreads();
     }
 }
@@ -672,7 +700,7 @@ static cudaError_t attn_join(const AttnParams& p, int grid, cudaStream_t st) {
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
     const int rows = p.TS * p.G;
-    cfg.gridDim = dim3(grid, rows < 16 ? rows : 16);
+    cfg.gridDim = dim3(grid, (rows + kJoinRows - 1) / kJoinRows);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     // the join is set up while the main kernel runs; it waits for its end itself

@@ -24,8 +24,8 @@ struct WideCfg {
     static constexpr int OFF_MT = OFF_QS + QB * N * 4;                   // [4][N] tile maxima
     static constexpr int OFF_L = OFF_MT + 4 * N * 4;                     // [2][N] float2: a group's sum, its reference
     static constexpr int OFF_GATHER = OFF_L + 2 * N * 8;                 // [128] cache rows of a tile's keys
-    static constexpr int OFF_X = OFF_GATHER + kATile * 4;                // [16][64] dims of the second copies
-    static constexpr int OFF_BAR = OFF_X + 16 * 64 * 4;
+    static constexpr int OFF_X = OFF_GATHER + kATile * 4;                // [32][128] dims that the copies exchange
+    static constexpr int OFF_BAR = OFF_X + 32 * 128 * 4;
     static constexpr int NBAR = 2 * SLOTS + 2 * kAMeta + 2 * 2 + 3 * 2 + 4 + 2 + 1;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int TOTAL = OFF_MISC + 288 + 1024;
@@ -35,7 +35,7 @@ struct WideCfg {
     // Warpgroups: MMA and queries; two of softmax that take the tiles in turn; joining; producers.
     static constexpr int THREADS = 640, PRODUCERS = 4, QWARPS = 3;
     static constexpr int W_SOFT = 4, W_JOIN = 12, W_PROD = 16;
-    static constexpr int R_LAUNCH = 96, R_MMA = 56, R_SOFT = 104, R_JOIN = 160, R_PROD = 56;
+    static constexpr int R_LAUNCH = 96, R_MMA = 56, R_SOFT = 96, R_JOIN = 176, R_PROD = 56;
     static_assert(R_LAUNCH == 65536 / THREADS / 8 * 8 && R_MMA + 2 * R_SOFT + R_JOIN + R_PROD <= R_LAUNCH * 5,
                   "register split");
 };
@@ -399,7 +399,8 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
         const uint32_t lane_addr = tmem + ((uint32_t)(wg_warp * 32) << 16) + 256;
         const int n = twice ? row & 63 : row;
         const bool works = (twice ? wg_warp & 1 : wg_warp) * 32 < rows;
-        const bool writes = n < rows && row == n;  // the first copy of a row
+        const int d0 = twice && row >= 64 ? 64 : 0;    // dims this thread writes: [d0, dz)
+        const int dz = twice ? min(p.D, d0 + 64) : p.D;
         const int st = attn_token(p, n);
         float* const sX = (float*)(smem + C::OFF_X);
         bool ok = true;
@@ -457,7 +458,8 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                 ++sc;
             }
             if (twice && wk.gr.n > 0) {
-                // the copies' maxima and sums, then 16 dims at a time
+                // The copies' maxima and sums; then the first copy takes dims 0 .. 63 of both, the second the others, 32
+                // at a time, into acc[0 .. 63].
                 sX[row] = m;
                 sX[128 + row] = l;
                 named_bar_sync(1, 128);
@@ -465,33 +467,29 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                 const float f = m == -INFINITY ? 0.f : exp2_approx(m - mm), fo = mo == -INFINITY ? 0.f : exp2_approx(mo - mm);
                 l = l * f + lo * fo;
                 m = mm;
+                const bool one = row < 64;
 #pragma unroll
-                for (int cc = 0; cc < 128; cc += 16) {
-                    if (cc < p.D) {
-                        named_bar_sync(1, 128);  // what was there is read
-                        if (row >= 64) {
+                for (int r = 0; r < 64; r += 32) {
+                    named_bar_sync(1, 128);  // what was there is read
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) sX[i * 64 + n] = acc[cc + i] * f;
-                        }
-                        named_bar_sync(1, 128);
-                        if (row < 64) {
+                    for (int i = 0; i < 32; ++i) sX[i * 128 + row] = (one ? acc[64 + r + i] : acc[r + i]) * f;
+                    named_bar_sync(1, 128);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) acc[cc + i] = acc[cc + i] * f + sX[i * 64 + n];
-                        }
-                    }
+                    for (int i = 0; i < 32; ++i)
+                        acc[r + i] = (one ? acc[r + i] : acc[64 + r + i]) * f + sX[i * 128 + (row ^ 64)];
                 }
                 named_bar_sync(1, 128);
             }
             const bool whole = wk.t0 == 0 && wk.t1 == wk.gr.w;
             if (whole) {
                 const int s = wk.gr.st * p.TS + st;
-                if (writes && s < p.S) {
+                if (n < rows && s < p.S) {
                     const int at = (wk.gr.b * p.S + s) * p.Hq + wk.h * p.G + n - st * p.G;
                     const float inv = l > 0.f ? 1.f / l : 0.f;
-                    uint4* out = reinterpret_cast<uint4*>(p.out + (int64_t)at * p.D);
+                    uint4* out = reinterpret_cast<uint4*>(p.out + (int64_t)at * p.D + d0);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        if (8 * i < p.D) {
+                        if (d0 + 8 * i < dz) {
                             uint32_t w[4];
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
@@ -502,18 +500,21 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                             out[i] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     }
-                    if (p.lse) p.lse[at] = l > 0.f ? (m + log2f(l) - kATop) * kALn2 : -INFINITY;
+                    if (p.lse && d0 == 0) p.lse[at] = l > 0.f ? (m + log2f(l) - kATop) * kALn2 : -INFINITY;
                 }
             } else {
                 const int slot = 2 * c + (wk.first ? 0 : 1);
                 float* part = parts + slot * attn_part_floats(N);
-                if (writes) {
+                if (n < rows) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        reinterpret_cast<float4*>(part + row * 128)[i] =
-                            make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
-                    part[N * 128 + row] = m;
-                    part[N * 128 + N + row] = l;
+                        if (d0 + 4 * i < dz)
+                            reinterpret_cast<float4*>(part + n * 128 + d0)[i] =
+                                make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+                    if (d0 == 0) {
+                        part[N * 128 + n] = m;
+                        part[N * 128 + N + n] = l;
+                    }
                 }
                 if (wk.t0 == 0)  // place unit_end - 1 is in the share of the last CTA that begins at or before it
                     hd = AttnHeader{(int32_t)((wk.unit_end * nc - 1) / W), wk.g, wk.h, slot};
