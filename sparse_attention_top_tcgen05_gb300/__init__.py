@@ -450,24 +450,22 @@ def _strided(t, name, dtype, dev=None):
 
 
 def _dense(t, name, dtype, shape, dev):
-    """Checks a contiguous CUDA tensor; None in `shape` is any size.  Returns its shape."""
+    """Checks a contiguous CUDA tensor on device dev; None in `shape` is any size.  Returns its shape."""
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        s = t.shape
+        if s == shape or (len(s) == len(shape) and all(m is None or n == m for n, m in zip(s, shape))):
+            return s
     if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    s = t.shape
-    if len(s) != len(shape):
-        raise ValueError(f"{name} must have {len(shape)} dims, got {tuple(s)}")
-    for n, m in zip(s, shape):
-        if m is not None and n != m:
-            raise ValueError(f"{name} has shape {tuple(s)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
-    return s
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape} (None: any)")
 
 
 def _raw_stream(stream, dev):
@@ -548,8 +546,9 @@ def lidx_rope_bwd(g, pos, freqs, x2=None, layout="interleaved", rot_off=0, mscal
 
 
 def _cache(k_cache, v_cache, k_scale, v_scale, block_table, B, Hkv, D, dev):
-    pages, Hkv, page, D = _dense(k_cache, "k_cache", _f8, (None, Hkv, None, D), dev)
-    _dense(v_cache, "v_cache", _f8, (pages, Hkv, page, D), dev)
+    shape = _dense(k_cache, "k_cache", _f8, (None, Hkv, None, D), dev)
+    pages, Hkv, page, _ = shape
+    _dense(v_cache, "v_cache", _f8, shape, dev)
     _dense(k_scale, "k_scale", _f32, (pages, Hkv), dev)
     _dense(v_scale, "v_scale", _f32, (pages, Hkv), dev)
     return pages, Hkv, page, _dense(block_table, "block_table", _i32, (B, None), dev)[1]

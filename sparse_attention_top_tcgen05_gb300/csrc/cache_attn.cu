@@ -584,15 +584,15 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
     }
 }
 
-// Joins the parts of the units that were cut: block (c, y) takes kJoinRows rows of the unit whose first tiles CTA c had.
+// Joins the parts of the units that were cut: block (c, y) takes R rows (at most 4) of the unit whose first tiles CTA c had.
 // The parts follow each other in the workspace (two slots a CTA).  Four groups of 128 threads: with few parts each
 // takes a row, with many each takes every fourth part of one row after the other, added in order.
 constexpr int kJoinThreads = 512;
-constexpr int kJoinRows = 4;
 constexpr int kJoinFew = 8;
 constexpr int kJoinMaxParts = 1024;  // more than SMs of a device
 template <int N>
-__global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __grid_constant__ AttnParams p, int nc) {
+__global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __grid_constant__ AttnParams p, int nc,
+                                                                       int R) {
     __shared__ float s_f[kJoinMaxParts], s_o[3][128], s_red[2][kJoinThreads / 32];
     grid_dependency_wait();
     const AttnHeader hd = reinterpret_cast<const AttnHeader*>(p.ws)[blockIdx.x];
@@ -609,10 +609,10 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __g
         if (d < p.D) reinterpret_cast<__nv_bfloat16*>(p.out)[row * p.D + d] = __float2bfloat16_rn(l > 0.f ? o / l : 0.f);
         if (p.lse && d == 0) p.lse[row] = l > 0.f ? (m + log2f(l) - kATop) * kALn2 : -INFINITY;
     };
-    const int rows = min(p.TS, p.S - st0) * p.G, n0 = blockIdx.y * kJoinRows;
+    const int rows = min(p.TS, p.S - st0) * p.G, n0 = blockIdx.y * R;
     if (P <= kJoinFew) {
         const int n = n0 + quarter;
-        if (n >= rows) return;
+        if (quarter >= R || n >= rows) return;
         float pm[kJoinFew], pl[kJoinFew], po[kJoinFew], m = -INFINITY;
 #pragma unroll
         for (int i = 0; i < kJoinFew; ++i) {
@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __g
         write(n, m, l, o);
         return;
     }
-    for (int n = n0; n < min(n0 + kJoinRows, rows); ++n) {
+    for (int n = n0; n < min(n0 + R, rows); ++n) {
         float m = -INFINITY;
         for (int i = tid; i < P; i += kJoinThreads) m = fmaxf(m, part_of(i)[N * 128 + n]);
         m = warp_max(m);
@@ -700,7 +700,9 @@ static cudaError_t attn_join(const AttnParams& p, int grid, cudaStream_t st) {
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
     const int rows = p.TS * p.G;
-    cfg.gridDim = dim3(grid, (rows + kJoinRows - 1) / kJoinRows);
+    // many rows: four a block, since the blocks of CTAs without a cut unit cost a wave each
+    const int R = rows <= 32 ? 1 : 4;
+    cfg.gridDim = dim3(grid, (rows + R - 1) / R);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     // the join is set up while the main kernel runs; it waits for its end itself
@@ -710,7 +712,7 @@ static cudaError_t attn_join(const AttnParams& p, int grid, cudaStream_t st) {
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<N>, p, grid);
+    return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<N>, p, grid, R);
 }
 
 LIDX_STATUS_READER(status_cache_attn)
