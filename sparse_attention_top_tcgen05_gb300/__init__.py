@@ -507,7 +507,7 @@ def _rope(x, pos, freqs, x2, layout, rot_off, mscale, inverse, stream, out, call
         raise ValueError(f"layout must be one of {list(ROPE_LAYOUT)}")
     if out is None:
         at = x.device
-        y = torch.empty(shape, dtype=dtype, device=at)
+        y = torch.empty_like(x) if x.is_contiguous() else torch.empty(shape, dtype=dtype, device=at)
         arr = _ROPE_TENSOR(x.data_ptr(), y.data_ptr(), *xs, T1 * H * D, H * D, D, H)
         if x2 is not None:
             H2 = shape2[2]
@@ -597,7 +597,7 @@ def lidx_cache_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, 
         _dense(q_pos, "q_pos", _i32, (B,), dev)
     topk = 0 if topk_indices is None else _dense(topk_indices, "topk_indices", _i32, (B, S, None), dev)[2]
     if out is None:
-        o = torch.empty(shape, dtype=_bf16, device=q.device)
+        o = torch.empty_like(q) if q.is_contiguous() else torch.empty(shape, dtype=_bf16, device=q.device)
         lse = torch.empty(shape[:3], dtype=_f32, device=q.device) if want_lse else None
     else:
         o, lse = out

@@ -61,11 +61,22 @@ __global__ void __launch_bounds__(kAppThreads, 5) cache_append_kernel(const __gr
     const uint16_t* x = p.x[which] + b * p.xs[which][0] + (lo - start) * p.xs[which][1] + h * p.xs[which][2];
     uint4 v[kAppVecs];
     uint32_t top = 0;  // packed pairs of |bf16| codes: ordered as integers
+    // vector e is chunk c of a token: both step on without a division
+    const int step = kAppThreads / C, over = kAppThreads - step * C;
+    int c = threadIdx.x % C;
+    const uint16_t* row = x + (int64_t)(threadIdx.x / C) * p.xs[which][1];
+    const int64_t stride = p.xs[which][1], hop = step * stride;
 #pragma unroll
     for (int i = 0; i < kAppVecs; ++i) {
         const int e = threadIdx.x + i * kAppThreads;
         if (e < n) {
-            v[i] = *reinterpret_cast<const uint4*>(x + (int64_t)(e / C) * p.xs[which][1] + (e % C) * 8);
+            v[i] = *reinterpret_cast<const uint4*>(row + c * 8);
+            row += hop;
+            c += over;
+            if (c >= C) {
+                c -= C;
+                row += stride;
+            }
             top = __vmaxu2(__vmaxu2(top, v[i].x & 0x7fff7fffu), __vmaxu2(v[i].y & 0x7fff7fffu, v[i].z & 0x7fff7fffu));
             top = __vmaxu2(top, v[i].w & 0x7fff7fffu);
         }

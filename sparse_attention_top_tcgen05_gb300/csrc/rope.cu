@@ -25,6 +25,23 @@ struct RopeTensor {
     int64_t xs[3], ys[3];
     int H;
 };
+// n / d for n < 2^31: (hi(n * mul) + n) >> shift with shift = ceil(log2 d), mul = floor(2^32 (2^shift - d) / d) + 1
+// (division by an invariant integer through multiplication, Granlund and Montgomery 1994).
+struct RopeDiv {
+    uint32_t d, mul, shift;
+};
+static RopeDiv rope_div(uint32_t d) {
+    RopeDiv r;
+    r.d = d;
+    r.shift = 0;
+    while ((1ull << r.shift) < d) ++r.shift;
+    r.mul = (uint32_t)(((1ull << 32) * ((1ull << r.shift) - d)) / d + 1);
+    return r;
+}
+__device__ __forceinline__ uint32_t rope_quot(uint32_t n, const RopeDiv& v) {
+    return (__umulhi(n, v.mul) + n) >> v.shift;
+}
+
 struct RopeParams {
     RopeTensor t[2];
     const int32_t* pos;
@@ -34,6 +51,7 @@ struct RopeParams {
     int heads;  // of both tensors
     int D, R, off, half;
     float mscale, sign;
+    RopeDiv row, items, tokens1, pairs;  // items of a token and of a head, T1, R / 2 (vector kernel)
 };
 
 // Scaled cosine and sine of position pos of a pair.
@@ -135,10 +153,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(const __grid_con
     for (int k = 0; k < PER; ++k) {
         const int e = threadIdx.x + k * kRopeThreads;
         if (e >= n) break;
-        const uint32_t at = skip + e, t = at / (uint32_t)row, r = at - t * row;
-        const int hh = r / (uint32_t)items, it = r - hh * items;
+        const uint32_t at = skip + e, t = rope_quot(at, p.row), r = at - t * row;
+        const int hh = rope_quot(r, p.items), it = r - hh * items;
         const int which = hh >= p.t[0].H, h = which ? hh - p.t[0].H : hh;
-        const uint32_t tok = tok0 + t, t0 = tok / (uint32_t)p.T1, t1 = tok - t0 * (uint32_t)p.T1;
+        const uint32_t tok = tok0 + t, t0 = rope_quot(tok, p.tokens1), t1 = tok - t0 * (uint32_t)p.T1;
         int d;
         if (it < rot) {
             d = p.off + it * V;
@@ -156,8 +174,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(const __grid_con
     }
     const int angles = ((skip + n - 1) / row + 1) * R2;
     for (int i = threadIdx.x; i < angles; i += kRopeThreads) {
-        const int t = i / R2;
-        const uint32_t tok = tok0 + t, t0 = tok / (uint32_t)p.T1, t1 = tok - t0 * (uint32_t)p.T1;
+        const int t = rope_quot(i, p.pairs);
+        const uint32_t tok = tok0 + t, t0 = rope_quot(tok, p.tokens1), t1 = tok - t0 * (uint32_t)p.T1;
         s_cs[i] = rope_cs(p.pos[t0 * p.ps[0] + t1 * p.ps[1]], p.freqs[i - t * R2], p.mscale, p.sign);
     }
     __syncthreads();
@@ -196,9 +214,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(const __grid_con
 static int64_t rope_angles(const RopeParams& p, int row, int n) { return (int64_t)((n - 1) / row + 2) * (p.R / 2); }
 
 template <class T, bool HALF>
-static cudaError_t rope_vec_launch(const RopeParams& p, cudaStream_t st) {
+static cudaError_t rope_vec_launch(RopeParams p, cudaStream_t st) {
     constexpr int V = 16 / sizeof(T);
-    const int row = ((HALF ? p.R / 2 / V : p.R / V) + (p.D - p.R) / V) * p.heads;
+    const int items = (HALF ? p.R / 2 / V : p.R / V) + (p.D - p.R) / V, row = items * p.heads;
+    p.row = rope_div(row);
+    p.items = rope_div(items);
+    p.tokens1 = rope_div((uint32_t)p.T1);
+    p.pairs = rope_div(p.R / 2);
     const int64_t all = p.T0 * p.T1 * row;
     // four items a thread, unless that leaves SMs without a block or there are too many angles (a single short head)
     constexpr int big = kRopePer * kRopeThreads;
