@@ -469,6 +469,8 @@ def _dense(t, name, dtype, shape, dev):
 
 
 def _raw_stream(stream, dev):
+    if torch._C._cuda_getDevice() != dev:  # launches go to the current device
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 

@@ -347,19 +347,22 @@ def test_workspace_refusals():
 
 
 @pytest.mark.gpu
-def test_stall_times_out_and_the_next_call_is_correct():
+@pytest.mark.parametrize("Hq,selected", [(16, False), (80, False), (80, True), (256, False), (24, True)])
+def test_stall_times_out_and_the_next_call_is_correct(Hq, selected):
     """The producer loads nothing, every wait runs out, the launch ends by itself and says so."""
-    c = Case(17, 3, 1, 16, 2, 64, 32, [500, 0, 90])
+    c = Case(17, 3, 1, Hq, 2, 64, 32, [500, 0, 90])
+    idx = c.g.integers(0, 500, (3, 1, 200)) if selected else None
+    given = None if idx is None else torch.from_numpy(idx.astype(np.int32)).to(DEV)
     assert lidx.lidx_device_status() == 0
     old = lidx.lidx_set_wait_limit_ns(2_000_000)
     lidx.lidx_debug_stall_producer(True)
     try:
-        lidx.lidx_cache_attn(*c.args())
+        lidx.lidx_cache_attn(*c.args(), topk_indices=given)
         assert lidx.lidx_device_status() == 7
     finally:
         lidx.lidx_debug_stall_producer(False)
         lidx.lidx_set_wait_limit_ns(old)
-    c.check()
+    c.check(idx=idx)
 
 
 @pytest.mark.gpu
