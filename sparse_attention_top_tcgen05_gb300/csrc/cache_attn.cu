@@ -16,7 +16,12 @@
 //     m' = max(m, M);  acc = acc 2^(m - m') + O 2^(M - m');  l likewise with w_t / v scale;  o = acc / l.
 //
 // Keys are the rows of both products (S^T = K Q^T, O^T = V^T P^T): 128 keys fill the tensor core's rows however
-// few queries there are.  The N columns are (query token, head of the group), N = 16, 32, 64 or 128.
+// few queries there are.  The N columns are (query token, head of the group), N = 16 or 32; units of more rows go to
+// the kernel in cache_attn_wide.cu.
+//
+// What bounds it: reading the cache once.  8 sequences x 65536 keys, 64 heads on 8: 177 us, 6.1 TB/s (pages of 16
+// tokens, eight copies a tile instead of two: 220-229 us).  One shared head does 8 x 65536 keys in 33 us with 16 query
+// heads and 35 us with 32; one sequence of 1024 keys takes 10 us, which are two launches and one tile's latencies.
 //
 // Work.  The units (sequence, tile of query tokens, kv head) have as many tiles of 128 keys as their last row
 // sees.  All tiles form one line that is cut into equal shares, one a CTA, found on the device from the
@@ -190,6 +195,7 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
     int64_t W;
     tc_fence_before();
     const int nc = attn_begin<C::THREADS>(p, wk, W, scan), c = blockIdx.x;
+    grid_dependency_launch();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
@@ -474,6 +480,7 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
         bool ok = true;
         int tc = 0, sc = 0;
         AttnHeader hd{0, 0, 0, 0};
+        AttnHeader* const heads = reinterpret_cast<AttnHeader*>(p.ws);
         float* const parts = (float*)(p.ws + (size_t)gridDim.x * sizeof(AttnHeader));
         while (wk.next(p)) {
             float acc[N];
@@ -568,8 +575,10 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                 if (wk.t0 == 0)  // place unit_end - 1 is in the share of the last CTA that begins at or before it
                     hd = AttnHeader{(int32_t)((wk.unit_end * nc - 1) / W), wk.g, wk.h, slot};
             }
+            if (p.by_unit && wk.t0 == 0 && d == 0)
+                heads[wk.g * p.Hkv + wk.h] = whole ? AttnHeader{0, 0, 0, 0} : hd;
         }
-        if (d == 0) reinterpret_cast<AttnHeader*>(p.ws)[c] = hd;
+        if (!p.by_unit && d == 0) heads[c] = hd;
     } else {
         regs_dec<C::R_PROD>();
         attn_produce<SLOTS, C::PRODUCERS>(p, wk, x, &tmk, &tmv, warp - C::W_PROD, lane);
@@ -584,94 +593,86 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
     }
 }
 
-// Joins the parts of the units that were cut: block (c, y) takes R rows (at most 4) of the unit whose first tiles CTA c had.
-// The parts follow each other in the workspace (two slots a CTA).  Four groups of 128 threads: with few parts each
-// takes a row, with many each takes every fourth part of one row after the other, added in order.
-constexpr int kJoinThreads = 512;
-constexpr int kJoinFew = 8;
-constexpr int kJoinMaxParts = 1024;  // more than SMs of a device
+// Joins the parts of the units that were cut, block (x, y) rows of the unit of header x.  The parts follow each other in the
+// workspace (two slots a CTA).  W warps share a row, each takes every W-th part with a running maximum, a lane four
+// dims; eight parts are loaded at a time, and the warps' results are added in order.
+// Its bytes are few (two parts a CTA): its time is its launch, two dependent reads and the start of its blocks.
+constexpr int kJoinWarps = 16;
+constexpr int kJoinBatch = 8;
 template <int N>
-__global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __grid_constant__ AttnParams p, int nc,
-                                                                       int R) {
-    __shared__ float s_f[kJoinMaxParts], s_o[3][128], s_red[2][kJoinThreads / 32];
+__global__ void __launch_bounds__(kJoinWarps * 32, 1) cache_attn_join_kernel(const __grid_constant__ AttnParams p, int nc,
+                                                                          int W) {
+    __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
+    __shared__ float4 s_o[kJoinWarps][32];
     grid_dependency_wait();
     const AttnHeader hd = reinterpret_cast<const AttnHeader*>(p.ws)[blockIdx.x];
     if (hd.last == 0) return;
     const float* parts = (const float*)(p.ws + (size_t)nc * sizeof(AttnHeader));
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, d = tid & 127, quarter = tid >> 7;
-    const int P = hd.last - blockIdx.x + 1, b = hd.g / p.ST, st0 = (hd.g - b * p.ST) * p.TS;
-    auto part_of = [&](int i) {
-        return parts + (size_t)(i == 0 ? hd.slot : 2 * (blockIdx.x + i)) * attn_part_floats(N);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp & (W - 1);
+    const int c0 = hd.slot >> 1, P = hd.last - c0 + 1, b = hd.g / p.ST, st0 = (hd.g - b * p.ST) * p.TS;
+    const int rows = min(p.TS, p.S - st0) * p.G, n = (blockIdx.y * kJoinWarps + warp) / W;
+    const bool some = 4 * lane < p.D;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto take = [&](float pm, float pl, const float4& po, float top) {
+        const float f = pm == -INFINITY ? 0.f : exp2_approx(pm - top);
+        l += pl * f;
+        o.x += po.x * f, o.y += po.y * f, o.z += po.z * f, o.w += po.w * f;
     };
-    auto write = [&](int n, float m, float l, float o) {
-        const int st = attn_token(p, n);
-        const int64_t row = ((int64_t)b * p.S + st0 + st) * p.Hq + hd.h * p.G + n - st * p.G;
-        if (d < p.D) reinterpret_cast<__nv_bfloat16*>(p.out)[row * p.D + d] = __float2bfloat16_rn(l > 0.f ? o / l : 0.f);
-        if (p.lse && d == 0) p.lse[row] = l > 0.f ? (m + log2f(l) - kATop) * kALn2 : -INFINITY;
+    auto fade = [&](float top) {
+        const float f = m == -INFINITY ? 0.f : exp2_approx(m - top);
+        l *= f;
+        o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+        m = top;
     };
-    const int rows = min(p.TS, p.S - st0) * p.G, n0 = blockIdx.y * R;
-    if (P <= kJoinFew) {
-        const int n = n0 + quarter;
-        if (quarter >= R || n >= rows) return;
-        float pm[kJoinFew], pl[kJoinFew], po[kJoinFew], m = -INFINITY;
+    if (n < rows)
+        for (int i0 = sub; i0 < P; i0 += kJoinBatch * W) {
+            float pm[kJoinBatch], pl[kJoinBatch], top = m;
+            float4 po[kJoinBatch];
 #pragma unroll
-        for (int i = 0; i < kJoinFew; ++i) {
-            const float* part = part_of(min(i, P - 1));
-            pm[i] = i < P ? part[N * 128 + n] : -INFINITY;
-            pl[i] = part[N * 128 + N + n];
-            po[i] = d < p.D ? part[n * 128 + d] : 0.f;
-            m = fmaxf(m, pm[i]);
-        }
-        float l = 0.f, o = 0.f;
-#pragma unroll
-        for (int i = 0; i < kJoinFew; ++i) {
-            const float f = pm[i] == -INFINITY ? 0.f : exp2_approx(pm[i] - m);
-            if (f > 0.f) {
-                l += pl[i] * f;
-                o += po[i] * f;
+            for (int j = 0; j < kJoinBatch; ++j) {
+                const int i = i0 + j * W, k = i < P ? i : i0;
+                const float* part = parts + (size_t)(k == 0 ? hd.slot : 2 * (c0 + k)) * attn_part_floats(N);
+                pm[j] = i < P ? part[N * 128 + n] : -INFINITY;
+                pl[j] = part[N * 128 + N + n];
+                po[j] = some ? reinterpret_cast<const float4*>(part + n * 128)[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+                top = fmaxf(top, pm[j]);
             }
+            fade(top);
+#pragma unroll
+            for (int j = 0; j < kJoinBatch; ++j) take(pm[j], pl[j], po[j], top);
         }
-        write(n, m, l, o);
-        return;
+    if (W > 1) {
+        if (lane == 0) {
+            s_m[warp] = m;
+            s_l[warp] = l;
+        }
+        s_o[warp][lane] = o;
+        __syncthreads();
+        if (sub > 0) return;
+        for (int i = 1; i < W; ++i) {
+            const float pm = s_m[warp + i], top = fmaxf(m, pm);
+            fade(top);
+            take(pm, s_l[warp + i], s_o[warp + i][lane], top);
+        }
     }
-    for (int n = n0; n < min(n0 + R, rows); ++n) {
-        float m = -INFINITY;
-        for (int i = tid; i < P; i += kJoinThreads) m = fmaxf(m, part_of(i)[N * 128 + n]);
-        m = warp_max(m);
-        if (lane == 0) s_red[0][warp] = m;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kJoinThreads / 32; ++i) m = fmaxf(m, s_red[0][i]);
-        float l = 0.f;
-        for (int i = tid; i < P; i += kJoinThreads) {
-            const float* part = part_of(i) + N * 128 + n;
-            const float f = m == -INFINITY ? 0.f : exp2_approx(part[0] - m);
-            s_f[i] = f;
-            l += part[N] * f;
-        }
-#pragma unroll
-        for (int i = 16; i; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
-        if (lane == 0) s_red[1][warp] = l;
-        __syncthreads();
-        l = 0.f;
-#pragma unroll
-        for (int i = 0; i < kJoinThreads / 32; ++i) l += s_red[1][i];
-        float o = 0.f;
-        if (d < p.D) {
-#pragma unroll 4
-            for (int i = quarter; i < P; i += 4) o += part_of(i)[n * 128 + d] * s_f[i];
-        }
-        if (quarter > 0) s_o[quarter - 1][d] = o;
-        __syncthreads();
-        if (quarter == 0) write(n, m, l, ((o + s_o[0][d]) + s_o[1][d]) + s_o[2][d]);
-        __syncthreads();
+    if (n >= rows) return;
+    const int st = attn_token(p, n);
+    const int64_t row = ((int64_t)b * p.S + st0 + st) * p.Hq + hd.h * p.G + n - st * p.G;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    if (some) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+        reinterpret_cast<uint2*>(p.out + row * p.D)[lane] =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     }
+    if (p.lse && lane == 0) p.lse[row] = l > 0.f ? (m + log2f(l) - kATop) * kALn2 : -INFINITY;
 }
 
 // ------------------------------------------------------------------- host
 
 // Columns of the configuration for a call: the fewest that hold a row's group of heads and, without
-// indices, as many of the sequence's query tokens as fit.
+// indices, as many of the sequence's query tokens as fit.  8 x 65536 keys of one head: 32 rows take 44 us with keys as
+// the products' rows and 50 us in the wide kernel, 64 rows 64 us and 55 us.
 static int attn_columns(int64_t S, int G, bool selected) {
     const int64_t want = selected ? G : (S * G < 128 ? S * G : 128);
     return want <= 16 ? 16 : (want <= 32 ? 32 : 128);
@@ -699,11 +700,13 @@ template <int N>
 static cudaError_t attn_join(const AttnParams& p, int grid, cudaStream_t st) {
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
-    const int rows = p.TS * p.G;
-    // many rows: four a block, since the blocks of CTAs without a cut unit cost a wave each
-    const int R = rows <= 32 ? 1 : 4;
-    cfg.gridDim = dim3(grid, (rows + R - 1) / R);
-    cfg.blockDim = dim3(kJoinThreads);
+    // Warps a row: eight parts each, by the parts that a unit has on average.  A header's blocks that find no cut unit
+    // cost 1.5 ns each, so a block takes as many rows as that leaves it warps for.
+    const int rows = p.TS * p.G, units = p.by_unit ? p.B * p.ST * p.Hkv : grid;
+    int W = 1;
+    while (W < kJoinWarps && W * kJoinBatch < grid / units + 2) W *= 2;
+    cfg.gridDim = dim3(units, (rows * W + kJoinWarps - 1) / kJoinWarps);
+    cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = st;
     // the join is set up while the main kernel runs; it waits for its end itself
     cudaLaunchAttribute at;
@@ -712,7 +715,7 @@ static cudaError_t attn_join(const AttnParams& p, int grid, cudaStream_t st) {
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<N>, p, grid, R);
+    return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<N>, p, grid, W);
 }
 
 LIDX_STATUS_READER(status_cache_attn)
@@ -750,7 +753,7 @@ int lidx_cache_attn(const void* q, const int64_t* qs, const void* k_cache, const
         return LIDX_ERR_ALIGN;
     if ((qs[0] | qs[1] | qs[2]) & 7) return LIDX_ERR_ALIGN;
     const int sms = sm103_sms();
-    if (sms <= 0 || sms > kJoinMaxParts) return LIDX_ERR_NO_DEVICE;
+    if (sms <= 0) return LIDX_ERR_NO_DEVICE;
     AttnParams p;
     memset(&p, 0, sizeof p);
     p.q = (const uint16_t*)q;
@@ -786,6 +789,7 @@ int lidx_cache_attn(const void* q, const int64_t* qs, const void* k_cache, const
     const int64_t tiles = topk_indices ? (topk + kATile - 1) / kATile : (max_pages * page + kATile - 1) / kATile;
     const int64_t most = tiles * B * p.ST * Hkv;
     const int grid = most < sms ? (int)most : sms;
+    p.by_unit = B * p.ST * Hkv <= grid;
     const size_t need = attn_ws_bytes(N, grid);
     if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u)) return LIDX_ERR_WORKSPACE;
     p.ws = (uint8_t*)workspace;

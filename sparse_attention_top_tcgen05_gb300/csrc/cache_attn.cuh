@@ -28,6 +28,7 @@ struct AttnParams {
     int64_t num_pages;
     int B, S, Hq, Hkv, G, D, page, max_pages, ratio, topk;
     int TS, ST;            // query tokens of a unit; units of a sequence
+    int by_unit;           // not more units than CTAs: headers belong to units, not to CTAs
     int page_shift;        // page = 1 << page_shift
     uint32_t inv_g;        // ceil(2^16 / G): n / G = n * inv_g >> 16 for n < 128
     float scale_log2;      // softmax_scale * log2(e)
@@ -123,9 +124,9 @@ struct AttnWalk {
     }
 };
 
-// Workspace: a header for each CTA, then two parts for each (its first segment, its last).
+// Workspace: a header for each unit or CTA, then two parts for each CTA (its first segment, its last).
 struct AttnHeader {
-    // last > 0: the CTA holds the first tiles (in part `slot`) of a unit that ends with CTA `last`'s first segment
+    // last > 0: a unit's first tiles are in part `slot`, of CTA slot / 2, and it ends with CTA `last`'s first segment
     int32_t last, g, h, slot;
 };
 __host__ __device__ inline size_t attn_part_floats(int N) { return (size_t)N * 128 + 2 * N; }

@@ -2,9 +2,14 @@
 //
 // The mathematics is cache_attn.cu's with the operands' roles swapped: the unit's (token, head) rows are the rows of the
 // products, S = Q K^T and O = P V, keys and dims their columns.  A softmax thread owns one row: maximum, sum and fades are
-// its own registers, and nothing crosses lanes or waits at a barrier.  That costs half of the instructions that a thread
-// for each key costs from 64 rows on (10.2k -> 5.3k a tile of 128 x 128), but lanes without a row have no work, so
-// units of up to 32 rows stay with the other kernel.
+// its own registers, and nothing crosses lanes or waits at a barrier.  A tile of 128 x 128 takes 6.3k warp instructions
+// instead of the 10.2k of a thread for each key, but lanes without a row have no work, so units of up to 32 rows stay
+// with the other kernel.  The weights are written over the tile's scores in TMEM and are the A operand of P V: 64 KB of
+// shared memory less than as a shared operand, which holds four more K and V tiles (1.41 -> 1.33 ms on the chunk below).
+//
+// What bounds it: the softmax groups' issue and latencies.  A chunk of 2048 queries over 16384 keys, 64 heads on 8, takes
+// 1.23 ms, 839 TFLOP/s of the products (4 FLOP a pair and dim) or twice that as executed in 8-bit pieces; the tensor pipe
+// is active 31 % of the time, issue slots 47 %.  4096 rows of 512 selected keys, 64 heads on one: 255 us.
 //
 // Units of at most 64 rows (one selected row of 64 heads, a decode step on a shared key head) are laid out twice: row r
 // again as row r + 64.  Of a tile's keys the first copy's weights hold the first 64, the second copy's the others (zeros
@@ -149,6 +154,7 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
     int64_t W;
     tc_fence_before();
     const int nc = attn_begin<C::THREADS>(p, wk, W, scan), c = blockIdx.x;
+    grid_dependency_launch();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int rows = p.TS * p.G;  // of a unit
@@ -406,6 +412,7 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
         bool ok = true;
         int tc = 0, sc = 0;
         AttnHeader hd{0, 0, 0, 0};
+        AttnHeader* const heads = reinterpret_cast<AttnHeader*>(p.ws);
         float* const parts = (float*)(p.ws + (size_t)gridDim.x * sizeof(AttnHeader));
         while (wk.next(p)) {
             float acc[128];
@@ -519,8 +526,10 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                 if (wk.t0 == 0)  // place unit_end - 1 is in the share of the last CTA that begins at or before it
                     hd = AttnHeader{(int32_t)((wk.unit_end * nc - 1) / W), wk.g, wk.h, slot};
             }
+            if (p.by_unit && wk.t0 == 0 && row == 0)
+                heads[wk.g * p.Hkv + wk.h] = whole ? AttnHeader{0, 0, 0, 0} : hd;
         }
-        if (row == 0) reinterpret_cast<AttnHeader*>(p.ws)[c] = hd;
+        if (!p.by_unit && row == 0) heads[c] = hd;
     } else {
         regs_dec<C::R_PROD>();
         attn_produce<SLOTS, C::PRODUCERS>(p, wk, x, &tmk, &tmv, warp - C::W_PROD, lane);

@@ -393,6 +393,11 @@ __device__ __forceinline__ void regs_dec() {
 }
 
 // ------------------------------------------- dependent launch (next kernel of the stream)
+// The next kernel's blocks may start where there is room once every CTA of this one is here or done.
+__device__ __forceinline__ void grid_dependency_launch() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+// The kernels before are done and what they wrote is seen.
 __device__ __forceinline__ void grid_dependency_wait() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }

@@ -7,6 +7,10 @@
 // Frequencies are turns per position in 0.64 fixed point, so pos * freq mod 2^64 is the fraction of
 // a turn exactly, whatever the position: a float angle would lose log2(pos) of its 24 bits.  The upper
 // 32 bits of the product, read as signed, are the angle from half a turn back to half a turn.
+//
+// What bounds it: reading and writing each element once.  2 x 8192 tokens of 65 bf16 heads of 128: 89 us, 6.1 TB/s (with
+// the divisions by sizes as divisions, a third of the instructions, 105 us); 4095 tokens of 40 fp32 heads: 26 us, 6.4
+// TB/s.  16 tokens take 2.2 us, a launch.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -69,7 +73,8 @@ __device__ __forceinline__ float rope_get(const __nv_bfloat16* p) { return __bfl
 __device__ __forceinline__ void rope_put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void rope_put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// Any alignment, any rotated part: one thread per pair or copied pair of elements.
+// Any alignment, any rotated part: one thread per pair or copied pair of elements, which recomputes its angle (the prompt
+// above: 428 us, bound by instructions).
 template <class T>
 __global__ void rope_any_kernel(const RopeParams p) {
     const int units = p.D / 2;  // R/2 rotated pairs, then (D - R)/2 copied pairs
@@ -222,7 +227,8 @@ static cudaError_t rope_vec_launch(RopeParams p, cudaStream_t st) {
     p.tokens1 = rope_div((uint32_t)p.T1);
     p.pairs = rope_div(p.R / 2);
     const int64_t all = p.T0 * p.T1 * row;
-    // four items a thread, unless that leaves SMs without a block or there are too many angles (a single short head)
+    // Four items a thread share a block's angles and overlap their loads (2 x 8192 tokens: 89 us, with one item 129 us),
+    // unless that leaves SMs without a block (16 tokens: 2.2 us with one) or there are too many angles (a single short head).
     constexpr int big = kRopePer * kRopeThreads;
     const int per = all / big >= 2 * current_sms() && rope_angles(p, row, big) <= kRopeAngles ? kRopePer : 1;
     const int64_t blocks = (all + per * kRopeThreads - 1) / (per * kRopeThreads);
