@@ -57,8 +57,8 @@ struct AttnCfg {
     static constexpr int OFF_MW = OFF_L + SG * 4 * NC * 4;             // [SG][NC] their reference
     static constexpr int OFF_INV = OFF_MW + SG * NC * 4;               // [N] 1 / l
     static constexpr int OFF_ROW = OFF_INV + N * 4;                    // [N] output rows
-    static constexpr int OFF_GATHER = OFF_ROW + N * 4;                 // [128] cache rows of a tile's keys
-    static constexpr int OFF_BAR = OFF_GATHER + kATile * 4;
+    static constexpr int OFF_GATHER = OFF_ROW + N * 4;                 // [4][128] cache rows of a tile's keys
+    static constexpr int OFF_BAR = OFF_GATHER + 4 * kATile * 4;
     static constexpr int NBAR = 2 * SLOTS + 2 * kAMeta + 2 * 2 + 3 * 2 + 4 + 2 + 1;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;                // start of the share, TMEM address
     static constexpr int TOTAL = OFF_MISC + 288 + 1024;                // + alignment of the base
@@ -164,11 +164,11 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < SLOTS; ++i) {
-            mbar_init(kv_full + i, p.idx ? C::PRODUCERS : 1);
+            mbar_init(kv_full + i, 1);
             mbar_init(kv_empty + i, 1);
         }
         for (int i = 0; i < kAMeta; ++i) {
-            mbar_init(meta_full + i, p.idx ? C::PRODUCERS : 1);
+            mbar_init(meta_full + i, 1);
             mbar_init(meta_empty + i, C::SPLIT ? 8 : 4);
         }
         for (int i = 0; i < 2; ++i) {

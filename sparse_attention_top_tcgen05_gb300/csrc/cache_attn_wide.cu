@@ -28,15 +28,15 @@ struct WideCfg {
     static constexpr int OFF_QS = OFF_SEEN + 128;                        // [QB][N] query scales
     static constexpr int OFF_MT = OFF_QS + QB * N * 4;                   // [4][N] tile maxima
     static constexpr int OFF_L = OFF_MT + 4 * N * 4;                     // [2][N] float2: a group's sum, its reference
-    static constexpr int OFF_GATHER = OFF_L + 2 * N * 8;                 // [128] cache rows of a tile's keys
-    static constexpr int OFF_X = OFF_GATHER + kATile * 4;                // [32][128] dims that the copies exchange
+    static constexpr int OFF_GATHER = OFF_L + 2 * N * 8;                 // [4][128] cache rows of a tile's keys
+    static constexpr int OFF_X = OFF_GATHER + 4 * kATile * 4;                // [32][128] dims that the copies exchange
     static constexpr int OFF_BAR = OFF_X + 32 * 128 * 4;
-    static constexpr int NBAR = 2 * SLOTS + 2 * kAMeta + 2 * 2 + 3 * 2 + 4 + 2 + 1;
+    static constexpr int NBAR = 2 * SLOTS + 2 * kAMeta + 2 * 2 + 3 + 4 + 2 + 2 + 1;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int TOTAL = OFF_MISC + 288 + 1024;
     static_assert(TOTAL <= 232448 && kAMeta * 20 <= 128, "shared memory");
     static_assert(OFF_QS % 16 == 0 && OFF_GATHER % 16 == 0 && OFF_MISC % 8 == 0, "16-byte reads");
-    static constexpr int TMEM = 512;  // two tiles of S and of O
+    static constexpr int TMEM = 512;  // three tiles of S (and the weights over them), one of O
     // Warpgroups: MMA and queries; two of softmax that take the tiles in turn; joining; producers.
     static constexpr int THREADS = 640, PRODUCERS = 4, QWARPS = 3;
     static constexpr int W_SOFT = 4, W_JOIN = 12, W_PROD = 16;
@@ -109,11 +109,11 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
     uint64_t* const meta_empty = x.meta_empty = meta_full + kAMeta;
     uint64_t* const q_full = x.q_full = meta_empty + kAMeta;
     uint64_t* const q_empty = x.q_empty = q_full + 2;
-    uint64_t* s_full = q_empty + 2;  // [2] S of a tile in TMEM
-    uint64_t* p_full = s_full + 2;   // [4] weights and tile maxima written (and S read)
-    uint64_t* o_full = p_full + 4;   // [2] O of a tile in TMEM (and the weights read)
-    uint64_t* o_empty = o_full + 2;  // [2] O read
-    uint64_t* l_full = o_empty + 2;  // sums of a segment written
+    uint64_t* s_full = q_empty + 2;  // [3] S of a tile in TMEM
+    uint64_t* p_full = s_full + 3;   // [4] weights and tile maxima written (and S read)
+    uint64_t* o_full = p_full + 4;   // O of a tile in TMEM (and the weights read)
+    uint64_t* o_empty = o_full + 1;  // O read
+    uint64_t* l_full = o_empty + 1;  // sums of a segment written
     uint64_t* l_empty = l_full + 1;
     uint64_t* drain = l_empty + 1;
     uint32_t* tmem_slot = (uint32_t*)(smem + C::OFF_MISC);
@@ -123,22 +123,21 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < SLOTS; ++i) {
-            mbar_init(kv_full + i, p.idx ? C::PRODUCERS : 1);
+            mbar_init(kv_full + i, 1);
             mbar_init(kv_empty + i, 1);
         }
         for (int i = 0; i < kAMeta; ++i) {
-            mbar_init(meta_full + i, p.idx ? C::PRODUCERS : 1);
+            mbar_init(meta_full + i, 1);
             mbar_init(meta_empty + i, 4);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + i, C::QWARPS);
             mbar_init(q_empty + i, 1 + 8);
-            mbar_init(s_full + i, 1);
-            mbar_init(p_full + i, 4);
-            mbar_init(p_full + 2 + i, 4);
-            mbar_init(o_full + i, 1);
-            mbar_init(o_empty + i, 4);
         }
+        for (int i = 0; i < 3; ++i) mbar_init(s_full + i, 1);
+        for (int i = 0; i < 4; ++i) mbar_init(p_full + i, 4);
+        mbar_init(o_full, 1);
+        mbar_init(o_empty, 4);
         mbar_init(l_full, 8);
         mbar_init(l_empty, 4);
         mbar_init(drain, 1);
@@ -176,16 +175,16 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
             int tc = 0, sc = 0;
             // O of tile t: (hi + lo) V
             auto second = [&](int t) {
-                const int bf = t & 1, ph = (t >> 1) & 1, seq = 2 * t + 1, sl = seq % SLOTS;
+                const int seq = 2 * t + 1, sl = seq % SLOTS;
                 ok = ok && mbar_wait(kv_full + sl, (seq / SLOTS) & 1, p.wait_ns);
-                ok = ok && mbar_wait(o_empty + bf, ph ^ 1, p.wait_ns);
+                ok = ok && mbar_wait(o_empty, (t & 1) ^ 1, p.wait_ns);
                 ok = ok && mbar_wait(p_full + (t & 3), (t >> 2) & 1, p.wait_ns);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) return;
                 tc_fence_after();
-                const uint32_t a = tmem + bf * 128;  // the weights, in the columns of the tile's S
+                const uint32_t a = tmem + t % 3 * 128;  // the weights, in the columns of the tile's S
                 const uint64_t b = dv0 + (uint64_t)(sl * (kASlotBytes >> 4));
-                const uint32_t d = tmem + 256 + bf * 128;
+                const uint32_t d = tmem + 384;
                 if (issuer) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)  // 32 keys a step
@@ -193,7 +192,7 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         umma_f8_ts(d, a + 16 * k + 8, b + k * (32 * 128 >> 4), id_o, 1);
-                    umma_commit(o_full + bf);
+                    umma_commit(o_full);
                     umma_commit(kv_empty + sl);
                 }
                 __syncwarp();
@@ -210,7 +209,7 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                     tc_fence_after();
                     const uint64_t a = dq0 + (uint64_t)(qb * (C::Q_BYTES >> 4));
                     const uint64_t b = dk0 + (uint64_t)(sl * (kASlotBytes >> 4));
-                    const uint32_t d = tmem + (tc & 1) * 128;
+                    const uint32_t d = tmem + tc % 3 * 128;  // (its last tile's weights are read by a product before)
                     if (issuer) {
                         // 32 dims a step, hi then lo
                         if (nk == 4) {
@@ -225,15 +224,17 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
 #pragma unroll 1
                             for (int k = 0; k < nk; ++k) umma_f8(d, a + (N * 128 >> 4) + 2 * k, b + 2 * k, id_s, 1);
                         }
-                        umma_commit(s_full + (tc & 1));
+                        umma_commit(s_full + tc % 3);
                         umma_commit(kv_empty + sl);
                         if (t == wk.t1 - 1) umma_commit(q_empty + qb);
                     }
                     __syncwarp();
-                    if (tc > 0) second(tc - 1);
+                    // S two tiles ahead of O: a softmax group that ends a tile finds the scores of its next
+                    if (tc > 1) second(tc - 2);
                 }
                 ++sc;
             }
+            if (ok && tc > 1) second(tc - 2);
             if (ok && tc > 0) second(tc - 1);
             if (!__all_sync(0xffffffffu, ok)) {  // products in flight end before the memory is given up
                 if (issuer) umma_commit(drain);
@@ -265,16 +266,15 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
             float l = 0.f, m = -INFINITY;
             for (int t = wk.t0; t < wk.t1; ++t, ++tc) {
                 if ((tc & 1) != grp) continue;
-                const int bf = tc & 1, ph = (tc >> 1) & 1, ms = tc % kAMeta;
+                const int bf = tc % 3, ph = (tc / 3) & 1, ms = tc % kAMeta;
                 ok = ok && mbar_wait(x.meta_full + ms, (tc / kAMeta) & 1, p.wait_ns);
                 const float* const ka = x.key_a + ms * kATile;
                 const float* const kl = x.key_lv + ms * kATile;
                 const float* const ki = x.key_iv + ms * kATile;
                 const bool flag = x.flag[ms] != 0;
                 const bool masked = flag || t * kATile + kATile > least;
-                // S of this tile is done, and with it all products issued before: those of O of the tile before last,
-                // so its weights' buffer is free, and so are the maxima of four tiles ago (a tile's O waits for the
-                // joining of the tile two before it)
+                // S of this tile is done, and with it the O of three tiles ago, which was issued before it when the tile
+                // before that was joined: the maxima of four tiles ago have been read
                 ok = ok && mbar_wait(s_full + bf, ph, p.wait_ns);
                 tc_fence_after();
                 const uint32_t s_addr = lane_addr + bf * 128;
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
         // A thread has one row: its D outputs, maximum and sum.
         regs_inc<C::R_JOIN>();
         const int row = tid & 127, wg_warp = warp & 3;
-        const uint32_t lane_addr = tmem + ((uint32_t)(wg_warp * 32) << 16) + 256;
+        const uint32_t lane_addr = tmem + ((uint32_t)(wg_warp * 32) << 16) + 384;
         const int n = twice ? row & 63 : row;
         const bool works = (twice ? wg_warp & 1 : wg_warp) * 32 < rows;
         const int d0 = twice && row >= 64 ? 64 : 0;    // dims this thread writes: [d0, dz)
@@ -421,29 +421,30 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
             float m = -INFINITY, l = 0.f;
             if (wk.gr.n > 0) {
                 for (int t = wk.t0; t < wk.t1; ++t, ++tc) {
-                    const int bf = tc & 1, ph = (tc >> 1) & 1;
                     // (four barriers: the softmax may be three tiles ahead of the joining)
                     ok = ok && mbar_wait(p_full + (tc & 3), (tc >> 2) & 1, p.wait_ns);
-                    const float top = works ? sMt[(tc & 3) * N + row] : -INFINITY;
-                    ok = ok && mbar_wait(o_full + bf, ph, p.wait_ns);
+                    const float top = works ? sMt[(tc & 3) * N + row] : -INFINITY, mn = fmaxf(m, top);
+                    const float fa = m == -INFINITY ? 1.f : exp2_approx(m - mn);  // (acc is zero before a row's first key)
+                    const float fb = top == -INFINITY ? 0.f : exp2_approx(top - mn);
+                    m = mn;
+                    // what there is fades before O is awaited, and only if a row's maximum grew
+                    if (__any_sync(0xffffffffu, fa != 1.f)) {
+                        const uint64_t fa2 = pack2(fa, fa);
+#pragma unroll
+                        for (int i = 0; i < 128; i += 2) unpack2(mul2(pack2(acc[i], acc[i + 1]), fa2), acc[i], acc[i + 1]);
+                    }
+                    ok = ok && mbar_wait(o_full, tc & 1, p.wait_ns);
                     tc_fence_after();
                     if (works) {
-                        const float mn = fmaxf(m, top);
-                        const float fa = m == -INFINITY ? 0.f : exp2_approx(m - mn);
-                        const float fb = top == -INFINITY ? 0.f : exp2_approx(top - mn);
-                        const uint64_t fa2 = pack2(fa, fa), fb2 = pack2(fb, fb);
-                        m = mn;
+                        const uint64_t fb2 = pack2(fb, fb);
 #pragma unroll
-                        for (int cc = 0; cc < 128; cc += 16) {
-                            if (cc < p.D) {
-                                uint32_t r[16];
-                                tmem_ld16(lane_addr + bf * 128 + cc, r);
-#pragma unroll
-                                for (int i = 0; i < 16; i += 2)
-                                    unpack2(mul2(pack2(acc[cc + i], acc[cc + i + 1]), fa2), acc[cc + i], acc[cc + i + 1]);
+                        for (int cc = 0; cc < 128; cc += 32) {
+                            if (cc < p.D) {  // (columns past D are never used)
+                                uint32_t r[32];
+                                tmem_ld32(lane_addr + cc, r);
                                 tmem_ld_wait();
 #pragma unroll
-                                for (int i = 0; i < 16; i += 2)
+                                for (int i = 0; i < 32; i += 2)
                                     unpack2(fma2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), fb2,
                                                  pack2(acc[cc + i], acc[cc + i + 1])),
                                             acc[cc + i], acc[cc + i + 1]);
@@ -452,7 +453,7 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                     }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(o_empty + bf);
+                    if (lane == 0) mbar_arrive(o_empty);
                 }
                 ok = ok && mbar_wait(l_full, sc & 1, p.wait_ns);
 #pragma unroll
