@@ -581,7 +581,10 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
         if (!p.by_unit && d == 0) heads[c] = hd;
     } else {
         regs_dec<C::R_PROD>();
-        attn_produce<SLOTS, C::PRODUCERS>(p, wk, x, &tmk, &tmv, warp - C::W_PROD, lane);
+        if (p.idx)
+            attn_produce<SLOTS, C::PRODUCERS, true>(p, wk, x, &tmk, &tmv, warp - C::W_PROD, lane);
+        else
+            attn_produce<SLOTS, C::PRODUCERS, false>(p, wk, x, &tmk, &tmv, warp - C::W_PROD, lane);
     }
 
     __syncwarp();

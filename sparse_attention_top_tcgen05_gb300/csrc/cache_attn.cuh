@@ -236,7 +236,7 @@ __device__ __forceinline__ int attn_begin(const AttnParams& p, AttnWalk& wk, int
 // Loads keys and values: warp pw of PRODUCERS.  The warps take the tiles in turn: the lookups of several tiles are then in
 // flight at once, and no tile's keys wait for the slot of an earlier tile's values.  (With a quarter of each tile's
 // gathers a warp, 4096 rows of 512 selected keys took 245 us instead of PROD_T.)
-template <int SLOTS, int PRODUCERS>
+template <int SLOTS, int PRODUCERS, bool SEL>
 __device__ __forceinline__ void attn_produce(const AttnParams& p, AttnWalk& wk, const AttnPipe& x, const CUtensorMap* tmk,
                                              const CUtensorMap* tmv, int pw, int lane) {
     static_assert(SLOTS <= 2 * PRODUCERS, "a warp's tile before has been used when its next one is loaded");
@@ -269,7 +269,7 @@ __device__ __forceinline__ void attn_produce(const AttnParams& p, AttnWalk& wk, 
             }
             count += skip;
             tile += skip;
-            const int limit = p.idx ? attn_end(p, wk.gr.b, wk.gr.st) : wk.gr.limit;
+            const int limit = SEL ? attn_end(p, wk.gr.b, wk.gr.st) : wk.gr.limit;
             r = Ref{true, wk.gr.b, wk.h, tile, limit, count, (int64_t)wk.gr.b * p.S + wk.gr.st};
             ++count;
             ++tile;
@@ -285,7 +285,7 @@ __device__ __forceinline__ void attn_produce(const AttnParams& p, AttnWalk& wk, 
         if (which == 0) ok = ok && mbar_wait(x.meta_empty + tc % kAMeta, ((tc / kAMeta) & 1) ^ 1, p.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
     };
-    if (!p.idx) {
+    if constexpr (!SEL) {
         // Pages: a lane has four keys, which share one; the lane with a page's first key loads it.
         auto page_id = [&](const Ref& r) {
             const int k0 = r.tile * kATile + 4 * lane;

@@ -45,36 +45,41 @@ struct WideCfg {
                   "register split");
 };
 
-// Scores of 32 keys of this thread's row in log2 units: S * (key's factor * row's factor) + log2(v scale).
-// UNI: the keys of a block of 16 share their page's factors.  vis: bits of the keys the row sees (MASK).
-template <bool MASK, bool UNI>
-__device__ __forceinline__ void wide_scores(uint32_t s_addr, const float* a, const float* lv, float qs, uint32_t vis,
-                                            float (&x)[32]) {
+// Products of 32 keys of this thread's row.  vis: bits of the keys the row sees (MASK; others become -inf).
+template <bool MASK>
+__device__ __forceinline__ void wide_products(uint32_t s_addr, uint32_t vis, float (&x)[32]) {
     uint32_t r[32];
     tmem_ld32(s_addr, r);
     tmem_ld_wait();
-    if constexpr (UNI) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float f = a[16 * h] * qs, v = lv[16 * h];
-            const uint64_t f2 = pack2(f, f), v2 = pack2(v, v);
+    for (int i = 0; i < 32; ++i) x[i] = !MASK || ((vis >> i) & 1) ? __uint_as_float(r[i]) : -INFINITY;
+}
+
+// Scores from products, in log2 units: S * (key's factor * row's factor) + log2(v scale) (+ sh with SHIFT).  a, lv: of the 32 keys.
+// UNI: the keys of a block of 16 share their page's factors.
+template <bool MASK, bool UNI, bool SHIFT>
+__device__ __forceinline__ void wide_scores(const float* a, const float* lv, float qs, float sh, uint32_t vis,
+                                            float (&x)[32]) {
+    const uint64_t q2 = pack2(qs, qs), sh2 = pack2(sh, sh);
 #pragma unroll
-            for (int i = 16 * h; i < 16 * h + 16; i += 2)
-                unpack2(fma2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f2, v2), x[i], x[i + 1]);
-        }
-    } else {
-        const uint64_t q2 = pack2(qs, qs);
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
+    for (int i = 0; i < 32; i += 4) {
+        uint64_t f0, f1, v0, v1;
+        if constexpr (UNI) {
+            const float f = a[i & 16] * qs, v = SHIFT ? lv[i & 16] + sh : lv[i & 16];
+            f0 = f1 = pack2(f, f);
+            v0 = v1 = pack2(v, v);
+        } else {
             const float4 f = *reinterpret_cast<const float4*>(a + i);
             const float4 v = *reinterpret_cast<const float4*>(lv + i);
-            unpack2(fma2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), mul2(pack2(f.x, f.y), q2),
-                         pack2(v.x, v.y)),
-                    x[i], x[i + 1]);
-            unpack2(fma2(pack2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), mul2(pack2(f.z, f.w), q2),
-                         pack2(v.z, v.w)),
-                    x[i + 2], x[i + 3]);
+            f0 = mul2(pack2(f.x, f.y), q2);
+            f1 = mul2(pack2(f.z, f.w), q2);
+            v0 = pack2(v.x, v.y);
+            v1 = pack2(v.z, v.w);
         }
+        v0 = fma2(pack2(x[i], x[i + 1]), f0, v0);
+        v1 = fma2(pack2(x[i + 2], x[i + 3]), f1, v1);
+        unpack2(UNI || !SHIFT ? v0 : add2(v0, sh2), x[i], x[i + 1]);
+        unpack2(UNI || !SHIFT ? v1 : add2(v1, sh2), x[i + 2], x[i + 3]);
     }
     if constexpr (MASK) {
 #pragma unroll
@@ -82,6 +87,8 @@ __device__ __forceinline__ void wide_scores(uint32_t s_addr, const float* a, con
     }
 }
 
+// SEL: selected keys.  TWICE: units of at most 64 rows.
+template <bool SEL, bool TWICE>
 __global__ void __launch_bounds__(WideCfg::THREADS, 1)
     cache_attn_wide_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                            const __grid_constant__ AttnParams p) {
@@ -157,7 +164,6 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int rows = p.TS * p.G;  // of a unit
-    const bool twice = rows <= 64;
 
     if (warp < 4) {
         regs_dec<C::R_MMA>();
@@ -241,15 +247,15 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                 mbar_wait(drain, 0, p.wait_ns);
             }
         } else {
-            attn_queries<N, QB, C::QWARPS>(p, wk, x, warp - 1, lane, twice);
+            attn_queries<N, QB, C::QWARPS>(p, wk, x, warp - 1, lane, TWICE);
         }
     } else if (warp < C::W_JOIN) {
         // -------------------------------------------------------------- softmax
         regs_inc<C::R_SOFT>();
         const int grp = (warp - C::W_SOFT) >> 2, row = tid & 127, wg_warp = warp & 3;
         const uint32_t lane_addr = tmem + ((uint32_t)(wg_warp * 32) << 16);
-        const int n = twice ? row & 63 : row;                                 // row of the unit
-        const bool works = (twice ? wg_warp & 1 : wg_warp) * 32 < rows;       // the warp has a row
+        const int n = TWICE ? row & 63 : row;                                 // row of the unit
+        const bool works = (TWICE ? wg_warp & 1 : wg_warp) * 32 < rows;       // the warp has a row
         const int st = attn_token(p, n);
         bool ok = true;
         int tc = 0, sc = 0;
@@ -257,7 +263,7 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
             if (wk.gr.n == 0) continue;
             const int qb = sc % QB, s = wk.gr.st * p.TS + st;
             int end = INT_MAX, least = INT_MAX;  // keys this row sees; keys every row sees
-            if (!p.idx) {
+            if (!SEL) {
                 end = n < rows && s < p.S ? attn_end(p, wk.gr.b, s) : 0;
                 least = attn_end(p, wk.gr.b, wk.gr.st * p.TS);
             }
@@ -279,10 +285,13 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                 tc_fence_after();
                 const uint32_t s_addr = lane_addr + bf * 128;
 
-                // TWICE: chunks of 32 keys [2 half, 2 half + 2), scores kept; else all four, computed twice
-                auto one_tile = [&](auto mask_c, auto uni_c, auto twice_c) {
+                // TWICE: chunks of 32 keys [2 half, 2 half + 2), products kept (scores, where not UNI); else all four, read twice.
+                // UNI (a cache page's keys follow each other, a positive softmax scale): the largest score of a block is
+                // that of its largest product, so the first pass has no scores to compute (chunk: T0 -> T1 ms).  The
+                // second adds the shift to the factor log2(v scale) first, which is only done where scores are below
+                // 2^20, so that no weight comes out above 2^8.3: returns false where they are not.
+                auto one_tile = [&](auto mask_c, auto uni_c) {
                     constexpr bool MASK = decltype(mask_c)::value, UNI = decltype(uni_c)::value;
-                    constexpr bool TWICE = decltype(twice_c)::value;
                     constexpr int NCH = TWICE ? 2 : 4, KEEP = TWICE ? 2 : 1;
                     const int c0 = TWICE && row >= 64 ? 2 : 0;
                     uint32_t vis[NCH];
@@ -299,26 +308,43 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                     for (int i = 0; i < NCH; ++i) {
                         const int at = 32 * (c0 + i);
                         float(&u)[32] = v[TWICE ? i : 0];
-                        wide_scores<MASK, UNI>(s_addr + at, ka + at, kl + at, qs, vis[i], u);
+                        wide_products<MASK && UNI>(s_addr + at, vis[i], u);
+                        if constexpr (UNI) {
 #pragma unroll
-                        for (int k = 0; k < 32; k += 2) top = fmaxf(top, fmaxf(u[k], u[k + 1]));
+                            for (int h = 0; h < 32; h += 16) {
+                                float b = u[h];
+#pragma unroll
+                                for (int k = 1; k < 15; k += 2) b = max3(b, u[h + k], u[h + k + 1]);
+                                b = fmaxf(b, u[h + 15]);
+                                if (b != -INFINITY) top = fmaxf(top, fmaf(b, ka[at + h] * qs, kl[at + h]));
+                            }
+                        } else {
+                            wide_scores<MASK, UNI, false>(ka + at, kl + at, qs, 0.f, vis[i], u);
+#pragma unroll
+                            for (int k = 0; k < 32; k += 2) top = max3(top, u[k], u[k + 1]);
+                        }
                     }
+                    if constexpr (UNI)
+                        if (__any_sync(0xffffffffu, fabsf(top) > 0x1p20f && top != -INFINITY)) return false;
                     const float sh = top == -INFINITY ? kATop : kATop - top;
-                    const uint64_t sh2 = pack2(sh, sh);
                     uint64_t sum0 = pack2(0.f, 0.f), sum1 = sum0;
 #pragma unroll
                     for (int i = 0; i < NCH; ++i) {
                         const int at = 32 * (c0 + i);
                         float(&u)[32] = v[TWICE ? i : 0];
-                        if constexpr (!TWICE) wide_scores<MASK, UNI>(s_addr + at, ka + at, kl + at, qs, vis[i], u);
+                        if constexpr (!TWICE) wide_products<false>(s_addr + at, 0, u);
+                        if constexpr (UNI || !TWICE) {
+                            wide_scores<MASK, UNI, true>(ka + at, kl + at, qs, sh, vis[i], u);
+                        } else {
+                            const uint64_t sh2 = pack2(sh, sh);
+#pragma unroll
+                            for (int k = 0; k < 32; k += 2) unpack2(add2(pack2(u[k], u[k + 1]), sh2), u[k], u[k + 1]);
+                        }
                         uint32_t w[16];  // hi and lo of 32 keys
 #pragma unroll
                         for (int k = 0; k < 32; k += 4) {
-                            float e0, e1, e2, e3;
-                            unpack2(add2(pack2(u[k], u[k + 1]), sh2), e0, e1);
-                            unpack2(add2(pack2(u[k + 2], u[k + 3]), sh2), e2, e3);
-                            const float w0 = exp2_approx(e0), w1 = exp2_approx(e1);
-                            const float w2 = exp2_approx(e2), w3 = exp2_approx(e3);
+                            const float w0 = exp2_approx(u[k]), w1 = exp2_approx(u[k + 1]);
+                            const float w2 = exp2_approx(u[k + 2]), w3 = exp2_approx(u[k + 3]);
                             if constexpr (UNI) {
                                 const float iv = ki[at + (k & 16)];
                                 sum0 = fma2(pack2(w0, w1), pack2(iv, iv), sum0);
@@ -353,20 +379,16 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                         m = mn;
                     }
                     sMt[(tc & 3) * N + row] = top;
+                    return true;
                 };
                 if (works) {
                     const std::true_type yes{};
                     const std::false_type no{};
-                    if (twice) {
-                        if (p.idx)
-                            masked ? one_tile(yes, no, yes) : one_tile(no, no, yes);
-                        else
-                            masked ? one_tile(yes, yes, yes) : one_tile(no, yes, yes);
+                    if constexpr (SEL) {
+                        masked ? one_tile(yes, no) : one_tile(no, no);
                     } else {
-                        if (p.idx)
-                            masked ? one_tile(yes, no, no) : one_tile(no, no, no);
-                        else
-                            masked ? one_tile(yes, yes, no) : one_tile(no, yes, no);
+                        const bool done = p.scale_log2 > 0.f && (masked ? one_tile(yes, yes) : one_tile(no, yes));
+                        if (!done) one_tile(yes, no);
                     }
                 }
                 if (flag) {
@@ -403,10 +425,10 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
         regs_inc<C::R_JOIN>();
         const int row = tid & 127, wg_warp = warp & 3;
         const uint32_t lane_addr = tmem + ((uint32_t)(wg_warp * 32) << 16) + 384;
-        const int n = twice ? row & 63 : row;
-        const bool works = (twice ? wg_warp & 1 : wg_warp) * 32 < rows;
-        const int d0 = twice && row >= 64 ? 64 : 0;    // dims this thread writes: [d0, dz)
-        const int dz = twice ? min(p.D, d0 + 64) : p.D;
+        const int n = TWICE ? row & 63 : row;
+        const bool works = (TWICE ? wg_warp & 1 : wg_warp) * 32 < rows;
+        const int d0 = TWICE && row >= 64 ? 64 : 0;    // dims this thread writes: [d0, dz)
+        const int dz = TWICE ? min(p.D, d0 + 64) : p.D;
         const int st = attn_token(p, n);
         float* const sX = (float*)(smem + C::OFF_X);
         bool ok = true;
@@ -465,7 +487,7 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                 if (lane == 0) mbar_arrive(l_empty);
                 ++sc;
             }
-            if (twice && wk.gr.n > 0) {
+            if (TWICE && wk.gr.n > 0) {
                 // The copies' maxima and sums; then the first copy takes dims 0 .. 63 of both, the second the others, 32
                 // at a time, into acc[0 .. 63].
                 sX[row] = m;
@@ -533,7 +555,7 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
         if (!p.by_unit && row == 0) heads[c] = hd;
     } else {
         regs_dec<C::R_PROD>();
-        attn_produce<SLOTS, C::PRODUCERS>(p, wk, x, &tmk, &tmv, warp - C::W_PROD, lane);
+        attn_produce<SLOTS, C::PRODUCERS, SEL>(p, wk, x, &tmk, &tmv, warp - C::W_PROD, lane);
     }
 
     __syncwarp();
@@ -545,11 +567,19 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
     }
 }
 
-cudaError_t attn_launch_wide(const CUtensorMap& mk, const CUtensorMap& mv, const AttnParams& p, int grid, cudaStream_t st) {
-    cudaError_t e = set_smem_attr((const void*)cache_attn_wide_kernel, WideCfg::TOTAL);
+template <bool SEL, bool TWICE>
+static cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const AttnParams& p, int grid, cudaStream_t st) {
+    auto* kernel = cache_attn_wide_kernel<SEL, TWICE>;
+    cudaError_t e = set_smem_attr((const void*)kernel, WideCfg::TOTAL);
     if (e != cudaSuccess) return e;
-    cache_attn_wide_kernel<<<grid, WideCfg::THREADS, WideCfg::TOTAL, st>>>(mk, mv, p);
+    kernel<<<grid, WideCfg::THREADS, WideCfg::TOTAL, st>>>(mk, mv, p);
     return cudaGetLastError();
+}
+
+cudaError_t attn_launch_wide(const CUtensorMap& mk, const CUtensorMap& mv, const AttnParams& p, int grid, cudaStream_t st) {
+    const bool twice = p.TS * p.G <= 64;
+    if (p.idx) return twice ? launch<true, true>(mk, mv, p, grid, st) : launch<true, false>(mk, mv, p, grid, st);
+    return twice ? launch<false, true>(mk, mv, p, grid, st) : launch<false, false>(mk, mv, p, grid, st);
 }
 
 LIDX_STATUS_READER(status_cache_attn_wide)

@@ -382,6 +382,13 @@ __device__ __forceinline__ float warp_max(float x) {
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
+// The largest of three in one instruction.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // Registers of this warpgroup (all four warps execute it).
 template <int R>
 __device__ __forceinline__ void regs_inc() {

@@ -391,3 +391,44 @@ def test_binding_refusals():
         lidx.lidx_cache_attn(*ok, out=(ok[0][:1], None))
     with pytest.raises(lidx.LidxError):
         lidx.lidx_cache_attn(ok[0][:, :, :3].contiguous(), *ok[1:])  # 3 heads over 2
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,scale", [(16, 1e5), (64, 1e5), (128, 1e5), (16, -0.07), (64, -0.07), (128, -0.07), (64, 0.0),
+                                      (128, 0.0)])
+def test_scores_beyond_fp32_and_other_signs_of_the_scale(Hq, scale):
+    """|score| up to 2^24 and more, the largest ahead by 2^12 or more: the row is that key's value.  Negative and zero scales."""
+    c = Case(Hq, 2, 1, Hq, 1, 128, 64, [300, 129])
+    if scale <= 0:
+        c.check(scale=scale)
+        return
+    # keys are one-hot in a dim each with an own integer code, queries one-hot: the scores are exact products
+    kc = np.zeros((2 * 5 + 2, 1, 64, 128), np.uint8)
+    g = c.g
+    for b, n in enumerate(c.lens):
+        for t in range(int(n)):
+            # 0x40 .. 0x7e are e4m3 codes of 2 .. 448 in order; key t of dim d: one code lies above the others
+            kc[c.table[b, t // 64], 0, t % 64, :] = g.integers(0x38, 0x70, 128)
+    best = g.integers(0, 129, 128)
+    for b in range(2):
+        for d in range(128):
+            t = int(best[d])
+            kc[c.table[b, t // 64], 0, t % 64, d] = 0x7E  # 448
+    c.kc = kc
+    c.ks = np.ones_like(c.ks)
+    q = torch.zeros(2, 1, Hq, 128)
+    for h in range(Hq):
+        q[:, 0, h, h] = 1.0
+    c.q = q.to(torch.bfloat16)
+    o, lse = lidx.lidx_cache_attn(*c.args(), softmax_scale=scale, want_lse=True)
+    _status_ok()
+    o, lse = o.float().cpu(), lse.double().cpu().numpy()
+    e4m3 = torch.from_numpy(c.vc).view(torch.float8_e4m3fn).float()
+    for b in range(2):
+        for h in range(Hq):
+            t = int(best[h])
+            pg = int(c.table[b, t // 64])
+            want = (e4m3[pg, 0, t % 64] * float(c.vs[pg, 0])).to(torch.bfloat16).float()
+            # hi + lo weights: 2^-8 at most, and one bf16 rounding
+            assert ((o[b, 0, h] - want).abs() <= 2.0 ** -7 * want.abs()).all()
+    assert np.allclose(lse, 448 * scale, rtol=2.0 ** -20)
