@@ -19,9 +19,9 @@
 // few queries there are.  The N columns are (query token, head of the group), N = 16 or 32; units of more rows go to
 // the kernel in cache_attn_wide.cu.
 //
-// What bounds it: reading the cache once.  8 sequences x 65536 keys, 64 heads on 8: 177 us, 6.1 TB/s (pages of 16
-// tokens, eight copies a tile instead of two: 220-229 us).  One shared head does 8 x 65536 keys in 33 us with 16 query
-// heads and 35 us with 32; one sequence of 1024 keys takes 10 us, which are two launches and one tile's latencies.
+// What bounds it: reading the cache once.  8 sequences x 65536 keys, 64 heads on 8: 169 us, 6.3 TB/s,
+// with pages of 16 or 64 tokens.  One shared head does 8 x 65536 keys in 33 us with 16 query heads and 36 us with 32; one
+// sequence of 1024 keys takes 10 us, which are two launches and one tile's latencies.
 //
 // Work.  The units (sequence, tile of query tokens, kv head) have as many tiles of 128 keys as their last row
 // sees.  All tiles form one line that is cut into equal shares, one a CTA, found on the device from the
@@ -74,6 +74,7 @@ struct AttnCfg {
     static constexpr int R_LAUNCH = 96, R_MMA = 64, R_SOFT = 112, R_JOIN = 104, R_PROD = 88;
     static_assert(R_LAUNCH == 65536 / THREADS / 8 * 8 && R_MMA + SG * R_SOFT + R_JOIN + R_PROD <= R_LAUNCH * 5,
                   "register split");
+    static_assert(R_MMA <= R_LAUNCH && R_PROD <= R_LAUNCH && R_SOFT >= R_LAUNCH && R_JOIN >= R_LAUNCH, "directions");
 };
 
 // Sums over the warp's lanes of 32 columns: lane i returns column i's.
@@ -674,8 +675,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 1) cache_attn_join_kernel(con
 // ------------------------------------------------------------------- host
 
 // Columns of the configuration for a call: the fewest that hold a row's group of heads and, without
-// indices, as many of the sequence's query tokens as fit.  8 x 65536 keys of one head: 32 rows take 44 us with keys as
-// the products' rows and 50 us in the wide kernel, 64 rows 64 us and 55 us.
+// indices, as many of the sequence's query tokens as fit.  8 x 65536 keys of one head: 32 rows take 36 us with keys as
+// the products' rows and 41 us in the wide kernel; 64 rows took 64 us and 55 us when both had them (43 us now).
 static int attn_columns(int64_t S, int G, bool selected) {
     const int64_t want = selected ? G : (S * G < 128 ? S * G : 128);
     return want <= 16 ? 16 : (want <= 32 ? 32 : 128);

@@ -2,14 +2,18 @@
 //
 // The mathematics is cache_attn.cu's with the operands' roles swapped: the unit's (token, head) rows are the rows of the
 // products, S = Q K^T and O = P V, keys and dims their columns.  A softmax thread owns one row: maximum, sum and fades are
-// its own registers, and nothing crosses lanes or waits at a barrier.  A tile of 128 x 128 takes 6.3k warp instructions
+// its own registers, and nothing crosses lanes or waits at a barrier.  A tile of 128 x 128 takes 5.7k warp instructions
 // instead of the 10.2k of a thread for each key, but lanes without a row have no work, so units of up to 32 rows stay
 // with the other kernel.  The weights are written over the tile's scores in TMEM and are the A operand of P V: 64 KB of
 // shared memory less than as a shared operand, which holds four more K and V tiles (1.41 -> 1.33 ms on the chunk below).
 //
+// Tensor memory holds the scores of three tiles and one O: S runs two tiles ahead of O, so a softmax group that ends a
+// tile finds the scores of its next.
+//
 // What bounds it: the softmax groups' issue and latencies.  A chunk of 2048 queries over 16384 keys, 64 heads on 8, takes
-// 1.23 ms, 839 TFLOP/s of the products (4 FLOP a pair and dim) or twice that as executed in 8-bit pieces; the tensor pipe
-// is active 31 % of the time, issue slots 47 %.  4096 rows of 512 selected keys, 64 heads on one: 255 us.
+// 1.01 ms, 1021 TFLOP/s of the products (4 FLOP a pair and dim) or twice that as executed in 8-bit pieces; the tensor pipe
+// is active 36 % of the time, issue slots 49 %, and without the softmax it takes 0.67 ms.  4096 rows of 512 selected keys,
+// 64 heads on one: 235 us, of which the rows' output and the exchange of their two copies are 45 us.
 //
 // Units of at most 64 rows (one selected row of 64 heads, a decode step on a shared key head) are laid out twice: row r
 // again as row r + 64.  Of a tile's keys the first copy's weights hold the first 64, the second copy's the others (zeros
@@ -43,6 +47,7 @@ struct WideCfg {
     static constexpr int R_LAUNCH = 96, R_MMA = 56, R_SOFT = 96, R_JOIN = 176, R_PROD = 56;
     static_assert(R_LAUNCH == 65536 / THREADS / 8 * 8 && R_MMA + 2 * R_SOFT + R_JOIN + R_PROD <= R_LAUNCH * 5,
                   "register split");
+    static_assert(R_MMA <= R_LAUNCH && R_PROD <= R_LAUNCH && R_SOFT >= R_LAUNCH && R_JOIN >= R_LAUNCH, "directions");
 };
 
 // Products of 32 keys of this thread's row.  vis: bits of the keys the row sees (MASK; others become -inf).
@@ -287,7 +292,7 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
 
                 // TWICE: chunks of 32 keys [2 half, 2 half + 2), products kept (scores, where not UNI); else all four, read twice.
                 // UNI (a cache page's keys follow each other, a positive softmax scale): the largest score of a block is
-                // that of its largest product, so the first pass has no scores to compute (chunk: T0 -> T1 ms).  The
+                // that of its largest product, so the first pass has no scores to compute (chunk: 1.14 -> 1.05 ms).  The
                 // second adds the shift to the factor log2(v scale) first, which is only done where scores are below
                 // 2^20, so that no weight comes out above 2^8.3: returns false where they are not.
                 auto one_tile = [&](auto mask_c, auto uni_c) {

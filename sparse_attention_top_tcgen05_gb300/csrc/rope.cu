@@ -9,7 +9,7 @@
 // 32 bits of the product, read as signed, are the angle from half a turn back to half a turn.
 //
 // What bounds it: reading and writing each element once.  2 x 8192 tokens of 65 bf16 heads of 128: 89 us, 6.1 TB/s (with
-// the divisions by sizes as divisions, a third of the instructions, 105 us); 4095 tokens of 40 fp32 heads: 26 us, 6.4
+// the divisions by sizes as divisions, a third of the instructions, 105 us); 4095 tokens of 40 fp32 heads: 27 us, 6.2
 // TB/s.  16 tokens take 2.2 us, a launch.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
