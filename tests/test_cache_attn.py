@@ -347,7 +347,7 @@ def test_workspace_refusals():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("Hq,selected", [(16, False), (80, False), (80, True), (256, False), (24, True)])
+@pytest.mark.parametrize("Hq,selected", [(16, False), (80, False), (80, True), (256, False), (24, True), (160, True)])
 def test_stall_times_out_and_the_next_call_is_correct(Hq, selected):
     """The producer loads nothing, every wait runs out, the launch ends by itself and says so."""
     c = Case(17, 3, 1, Hq, 2, 64, 32, [500, 0, 90])
