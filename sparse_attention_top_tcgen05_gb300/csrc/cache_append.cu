@@ -9,7 +9,8 @@
 // the maximum and the conversion, so each input byte is read once.
 //
 // What bounds it: a block waits for start, table and tokens one after the other and the maximum at a barrier, so bytes
-// in flight set the rate.  4 x 4097 tokens of 8 heads of 128: 20.8 us, 4.0 TB/s; one token of 64 sequences: 5.7 us.
+// in flight set the rate.  4 x 4097 tokens of 8 heads of 128, call behind call: 17.6 us, 4.8 TB/s with five blocks an SM
+// (18.5 us with four, 18.3 us with six, which spill); one token of 64 sequences: 5.7 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
