@@ -23,6 +23,9 @@ Functions carry the C names:
   lidx_cache_attn           attention over that cache, at every key or at selected ones
   lidx_workspace_bytes, lidx_cache_attn_workspace_bytes, lidx_device_status,
   lidx_status_string, lidx_set_wait_limit_ns, lidx_debug_stall_producer
+
+Calls run on the current stream, or on ``stream``.  There the caller makes the stream wait for the inputs,
+and the reader of the outputs for the stream; what a call allocates itself is the stream's own memory.
 """
 
 from __future__ import annotations
@@ -474,6 +477,32 @@ def _raw_stream(stream, dev):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
+def _on(stream, device):
+    """The context in which `stream`'s own memory is allocated."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    return torch.cuda.stream(stream)
+
+
+def _new(shape, dtype, device, stream):
+    """An output that the call allocates.  It is the stream's on which the kernels run: a block of another stream's pool
+    may still be in use there.  The caller reads it on the current stream, so it is held for that one, too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream, device):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _scratch(nbytes, device, stream):
+    """Scratch that the call drops while its kernels may still run: of their stream's pool, which hands it out behind them."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with _on(stream, device):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def lidx_rope_freqs(rot_dim, theta=10000.0, scaling=None, factor=1.0, original_len=4096, beta_fast=32.0,
                     beta_slow=1.0, device="cuda") -> torch.Tensor:
     """Rotary frequencies int64 [rot_dim/2]: turns per position in 0.64 fixed point (the bits of
@@ -509,11 +538,11 @@ def _rope(x, pos, freqs, x2, layout, rot_off, mscale, inverse, stream, out, call
         raise ValueError(f"layout must be one of {list(ROPE_LAYOUT)}")
     if out is None:
         at = x.device
-        y = torch.empty_like(x) if x.is_contiguous() else torch.empty(shape, dtype=dtype, device=at)
+        y = torch.empty_like(x) if stream is None and x.is_contiguous() else _new(shape, dtype, at, stream)
         arr = _ROPE_TENSOR(x.data_ptr(), y.data_ptr(), *xs, T1 * H * D, H * D, D, H)
         if x2 is not None:
             H2 = shape2[2]
-            y2 = torch.empty(shape2, dtype=dtype, device=at)
+            y2 = _new(shape2, dtype, at, stream)
             arr += _ROPE_TENSOR(x2.data_ptr(), y2.data_ptr(), *xs2, T1 * H2 * D, H2 * D, D, H2)
     else:
         y, y2 = (out, None) if x2 is None else out
@@ -599,8 +628,8 @@ def lidx_cache_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, 
         _dense(q_pos, "q_pos", _i32, (B,), dev)
     topk = 0 if topk_indices is None else _dense(topk_indices, "topk_indices", _i32, (B, S, None), dev)[2]
     if out is None:
-        o = torch.empty_like(q) if q.is_contiguous() else torch.empty(shape, dtype=_bf16, device=q.device)
-        lse = torch.empty(shape[:3], dtype=_f32, device=q.device) if want_lse else None
+        o = torch.empty_like(q) if stream is None and q.is_contiguous() else _new(shape, _bf16, q.device, stream)
+        lse = _new(shape[:3], _f32, q.device, stream) if want_lse else None
     else:
         o, lse = out
         _dense(o, "out", _bf16, shape, dev)
@@ -609,7 +638,7 @@ def lidx_cache_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, 
     L = _lib or lib()
     if workspace is None:
         ws_bytes = L.lidx_cache_attn_workspace_bytes(B, S, Hq, Hkv, D, topk)
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+        workspace = _scratch(ws_bytes, q.device, stream)
     else:
         ws_bytes = _dense(workspace, "workspace", torch.uint8, (None,), dev)[0]
     rc = L.lidx_cache_attn(
