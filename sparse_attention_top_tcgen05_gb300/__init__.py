@@ -144,6 +144,32 @@ def _stream(stream):
     return C.c_void_p(s.cuda_stream)
 
 
+def _on(stream, device):
+    """The context in which `stream`'s own memory is allocated."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    return torch.cuda.stream(stream)
+
+
+def _new(shape, dtype, device, stream):
+    """An output that the call allocates.  It is the stream's on which the kernels run: a block of another stream's pool
+    may still be in use there.  The caller reads it on the current stream, so it is held for that one, too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream, device):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _scratch(nbytes, device, stream):
+    """Scratch that the call drops while its kernels may still run: of their stream's pool, which hands it out behind them."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with _on(stream, device):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _need(t, name, dtype, dim):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -174,7 +200,7 @@ def lidx_device_status(stream=None) -> int:
     return int(lib().lidx_device_status(_stream(stream)))
 
 
-def _fwd_common(q, k, w, topk, topk_indices, materialise_logits, out, workspace):
+def _fwd_common(q, k, w, topk, topk_indices, materialise_logits, out, workspace, stream):
     _need(q, "q", torch.bfloat16, 4)
     _need(k, "k", torch.bfloat16, 3)
     _need(w, "w", torch.float32, 3)
@@ -186,14 +212,14 @@ def _fwd_common(q, k, w, topk, topk_indices, materialise_logits, out, workspace)
         _need(topk_indices, "topk_indices", torch.int32, 3)
     dev = q.device
     if out is None:
-        idx = torch.empty(B, S, topk, dtype=torch.int32, device=dev)
-        sc = torch.empty(B, S, topk, dtype=torch.float32, device=dev)
-        lg = torch.empty(B, S, Skv, dtype=torch.float32, device=dev) if materialise_logits else None
+        idx = _new((B, S, topk), torch.int32, dev, stream)
+        sc = _new((B, S, topk), torch.float32, dev, stream)
+        lg = _new((B, S, Skv), torch.float32, dev, stream) if materialise_logits else None
     else:
         idx, sc, lg = out
     ws_bytes = lidx_workspace_bytes(OP_INDEXER_FWD, B, S, Skv, H, D, topk, lg is not None)
     if workspace is None and ws_bytes:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        workspace = _scratch(ws_bytes, dev, stream)
     return (S, B, H, D, Skv), idx, sc, lg, workspace, ws_bytes
 
 
@@ -205,7 +231,7 @@ def lidx_indexer_fwd(q, k, w, compress_ratio, topk, act="relu", topk_indices=Non
     ``out`` may hold preallocated (indices, scores, logits) tensors.
     """
     (S, B, H, D, Skv), idx, sc, lg, workspace, ws_bytes = _fwd_common(
-        q, k, w, topk, topk_indices, materialise_logits, out, workspace)
+        q, k, w, topk, topk_indices, materialise_logits, out, workspace, stream)
     rc = lib().lidx_indexer_fwd(_ptr(q), _ptr(k), _ptr(w), B, S, Skv, H, D, compress_ratio, topk,
                                 ACT[act], _ptr(topk_indices), _ptr(lg), _ptr(idx), _ptr(sc),
                                 _ptr(workspace), ws_bytes if workspace is not None else 0,
@@ -220,7 +246,7 @@ def lidx_indexer_fwd_ranges(q, k, w, ks, ke, topk, act="relu", topk_indices=None
     _need(ks, "ks", torch.int32, 1)
     _need(ke, "ke", torch.int32, 1)
     (S, B, H, D, Skv), idx, sc, lg, workspace, ws_bytes = _fwd_common(
-        q, k, w, topk, topk_indices, materialise_logits, out, workspace)
+        q, k, w, topk, topk_indices, materialise_logits, out, workspace, stream)
     if ks.shape[0] != S or ke.shape[0] != S:
         raise ValueError("ks/ke must have S entries")
     rc = lib().lidx_indexer_fwd_ranges(_ptr(q), _ptr(k), _ptr(w), B, S, Skv, H, D, _ptr(ks), _ptr(ke),
@@ -241,8 +267,8 @@ def lidx_indexer_fwd_noalloc(q, k, w, compress_ratio, topk, act="relu", stream=N
     S, B, H, D = q.shape
     Skv = k.shape[0]
     if out is None:
-        idx = torch.empty(B, S, topk, dtype=torch.int32, device=q.device)
-        sc = torch.empty(B, S, topk, dtype=torch.float32, device=q.device)
+        idx = _new((B, S, topk), torch.int32, q.device, stream)
+        sc = _new((B, S, topk), torch.float32, q.device, stream)
     else:
         idx, sc = out
     rc = lib().lidx_indexer_fwd_noalloc(_ptr(q), _ptr(k), _ptr(w), B, S, Skv, H, D, compress_ratio,
@@ -262,7 +288,7 @@ def lidx_indexer_logits(q, k, w, compress_ratio=1, ks=None, ke=None, clean=True,
     if ks is not None:
         _need(ks, "ks", torch.int32, 1)
         _need(ke, "ke", torch.int32, 1)
-    lg = torch.empty(B, S, Skv, dtype=torch.float32, device=q.device) if out is None else out
+    lg = _new((B, S, Skv), torch.float32, q.device, stream) if out is None else out
     rc = lib().lidx_indexer_logits(_ptr(q), _ptr(k), _ptr(w), B, S, Skv, H, D, compress_ratio,
                                    _ptr(ks), _ptr(ke), int(bool(clean)), ACT[act], _ptr(lg),
                                    _stream(stream))
@@ -275,7 +301,7 @@ def lidx_extract_topk_scores(logits, idx, stream=None):
     _need(idx, "idx", torch.int32, 3)
     B, S, Skv = logits.shape
     topk = idx.shape[2]
-    out = torch.empty(B, S, topk, dtype=torch.float32, device=logits.device)
+    out = _new((B, S, topk), torch.float32, logits.device, stream)
     rc = lib().lidx_extract_topk_scores(_ptr(logits), _ptr(idx), B, S, Skv, topk, _ptr(out),
                                         _stream(stream))
     _check(rc, "lidx_extract_topk_scores")
@@ -300,8 +326,8 @@ def lidx_topk_rows(logits, topk, compress_ratio=1, ks=None, ke=None, stream=None
         _need(ke, "ke", torch.int32, 1)
     shape = tuple(logits.shape[:-1]) + (topk,)
     if out is None:
-        idx = torch.empty(shape, dtype=torch.int32, device=logits.device)
-        sc = torch.empty(shape, dtype=torch.float32, device=logits.device)
+        idx = _new(shape, torch.int32, logits.device, stream)
+        sc = _new(shape, torch.float32, logits.device, stream)
     else:
         idx, sc = out
     rc = lib().lidx_topk_rows(_ptr(logits), B * S, S, Skv, compress_ratio, _ptr(ks), _ptr(ke), topk,
@@ -322,10 +348,10 @@ def lidx_indexer_scores_v41(q, k, w, allowed, act="relu", stream=None, out=None,
         raise ValueError("allowed must be a contiguous CUDA [B,S,Skv] tensor")
     B, S, H, D = q.shape
     Skv = k.shape[1]
-    res = torch.empty(B, S, Skv, dtype=torch.bfloat16, device=q.device) if out is None else out
+    res = _new((B, S, Skv), torch.bfloat16, q.device, stream) if out is None else out
     ws_bytes = lidx_workspace_bytes(OP_SCORES_V41, B, S, Skv, H, D)
     if workspace is None and ws_bytes:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+        workspace = _scratch(ws_bytes, q.device, stream)
     rc = lib().lidx_indexer_scores_v41(_ptr(q), _ptr(k), _ptr(w), _ptr(allowed), B, S, Skv, H, D,
                                        ACT[act], _ptr(res), _ptr(workspace),
                                        ws_bytes if workspace is not None else 0, _stream(stream))
@@ -348,14 +374,14 @@ def lidx_indexer_topk_v41(q, k, w, allowed, topk, act="relu", keep_scores=True, 
     Skv = k.shape[1]
     dev = q.device
     if out is None:
-        res = torch.empty(B, S, Skv, dtype=torch.bfloat16, device=dev) if keep_scores else None
-        idx = torch.empty(B, S, topk, dtype=torch.int32, device=dev)
-        tsc = torch.empty(B, S, topk, dtype=torch.bfloat16, device=dev)
+        res = _new((B, S, Skv), torch.bfloat16, dev, stream) if keep_scores else None
+        idx = _new((B, S, topk), torch.int32, dev, stream)
+        tsc = _new((B, S, topk), torch.bfloat16, dev, stream)
     else:
         res, idx, tsc = out
     ws_bytes = lidx_workspace_bytes(OP_TOPK_V41, B, S, Skv, H, D, topk, res is not None)
     if workspace is None and ws_bytes:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        workspace = _scratch(ws_bytes, dev, stream)
     rc = lib().lidx_indexer_topk_v41(_ptr(q), _ptr(k), _ptr(w), _ptr(allowed), B, S, Skv, H, D,
                                      ACT[act], topk, _ptr(res), _ptr(idx), _ptr(tsc), _ptr(workspace),
                                      ws_bytes if workspace is not None else 0, _stream(stream))
@@ -373,7 +399,7 @@ def lidx_debug_stall_producer(on: bool) -> int:
     return int(lib().lidx_debug_stall_producer(int(bool(on))))
 
 
-def _bwd_common(q, k, w, idx, grad, grad_dtype, out, workspace):
+def _bwd_common(q, k, w, idx, grad, grad_dtype, out, workspace, stream):
     _need(q, "q", torch.bfloat16, 4)
     _need(k, "k", torch.bfloat16, 3)
     _need(w, "w", torch.float32, 3)
@@ -385,14 +411,14 @@ def _bwd_common(q, k, w, idx, grad, grad_dtype, out, workspace):
     dev = q.device
     gdt = {torch.float32: 0, torch.bfloat16: 1}[grad_dtype]
     if out is None:
-        dq = torch.empty(S, B, H, D, dtype=grad_dtype, device=dev)
-        dk = torch.empty(Skv, B, D, dtype=grad_dtype, device=dev)
-        dw = torch.empty(S, B, H, dtype=torch.float32, device=dev)
+        dq = _new((S, B, H, D), grad_dtype, dev, stream)
+        dk = _new((Skv, B, D), grad_dtype, dev, stream)
+        dw = _new((S, B, H), torch.float32, dev, stream)
     else:
         dq, dk, dw = out
     ws_bytes = lidx_workspace_bytes(OP_INDEXER_BWD, B, S, Skv, H, D, topk)
     if workspace is None and ws_bytes:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        workspace = _scratch(ws_bytes, dev, stream)
     return (S, B, H, D, Skv, topk, gdt), dq, dk, dw, workspace, ws_bytes
 
 
@@ -402,7 +428,7 @@ def lidx_indexer_bwd_ranges(q, k, w, idx, grad, ks, ke, act="relu", grad_dtype=t
     _need(ks, "ks", torch.int32, 1)
     _need(ke, "ke", torch.int32, 1)
     (S, B, H, D, Skv, topk, gdt), dq, dk, dw, workspace, ws_bytes = _bwd_common(
-        q, k, w, idx, grad, grad_dtype, out, workspace)
+        q, k, w, idx, grad, grad_dtype, out, workspace, stream)
     rc = lib().lidx_indexer_bwd_ranges(_ptr(q), _ptr(k), _ptr(w), _ptr(idx), _ptr(grad), B, S, Skv, H,
                                        D, _ptr(ks), _ptr(ke), topk, ACT[act], gdt, _ptr(dq), _ptr(dk),
                                        _ptr(dw), _ptr(workspace),
@@ -415,7 +441,7 @@ def lidx_indexer_bwd(q, k, w, idx, grad, compress_ratio, act="relu", grad_dtype=
                      stream=None, out=None, workspace=None):
     """Gradients (dq [S,B,H,D], dk [Skv,B,D] in grad_dtype (fp32 or bf16), dw [S,B,H] fp32)."""
     (S, B, H, D, Skv, topk, gdt), dq, dk, dw, workspace, ws_bytes = _bwd_common(
-        q, k, w, idx, grad, grad_dtype, out, workspace)
+        q, k, w, idx, grad, grad_dtype, out, workspace, stream)
     rc = lib().lidx_indexer_bwd(_ptr(q), _ptr(k), _ptr(w), _ptr(idx), _ptr(grad), B, S, Skv, H, D,
                                 compress_ratio, topk, ACT[act], gdt, _ptr(dq), _ptr(dk), _ptr(dw),
                                 _ptr(workspace), ws_bytes if workspace is not None else 0,
@@ -475,32 +501,6 @@ def _raw_stream(stream, dev):
     if torch._C._cuda_getDevice() != dev:  # launches go to the current device
         raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _on(stream, device):
-    """The context in which `stream`'s own memory is allocated."""
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
-    return torch.cuda.stream(stream)
-
-
-def _new(shape, dtype, device, stream):
-    """An output that the call allocates.  It is the stream's on which the kernels run: a block of another stream's pool
-    may still be in use there.  The caller reads it on the current stream, so it is held for that one, too."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with _on(stream, device):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(torch.cuda.current_stream(device))
-    return t
-
-
-def _scratch(nbytes, device, stream):
-    """Scratch that the call drops while its kernels may still run: of their stream's pool, which hands it out behind them."""
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    with _on(stream, device):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def lidx_rope_freqs(rot_dim, theta=10000.0, scaling=None, factor=1.0, original_len=4096, beta_fast=32.0,

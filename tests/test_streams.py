@@ -66,6 +66,7 @@ def pools(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: types.SimpleNamespace(cuda_stream=0))
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda self, s: None)
     monkeypatch.setattr(lidx, "_raw_stream", lambda s, dev: 0)
+    monkeypatch.setattr(lidx, "_stream", lambda s: None)
     monkeypatch.setattr(lidx, "_lib", FakeLib())
     monkeypatch.setattr(lidx, "lib", lambda: lidx._lib)
     return log
@@ -83,7 +84,35 @@ def attn_args():
             fake(3, 2, dtype=f32), fake(1, 2, dtype=i32), fake(1, dtype=i32))
 
 
+def v4_args():
+    return fake(4, 2, 8, 32), fake(6, 2, 32), fake(4, 2, 8, dtype=f32)
+
+
+def v41_args():
+    return fake(2, 4, 8, 32), fake(2, 6, 32), fake(2, 4, 8), fake(2, 4, 6, dtype=torch.bool)
+
+
+def ranges():
+    return fake(4, dtype=i32), fake(4, dtype=i32)
+
+
+def bwd_args():
+    return (*v4_args(), fake(2, 4, 3, dtype=i32), fake(2, 4, 3, dtype=f32))
+
+
 CALLS = {
+    "fwd": (lambda **kw: lidx.lidx_indexer_fwd(*v4_args(), 1, 3, **kw), 3),
+    "fwd logits": (lambda **kw: lidx.lidx_indexer_fwd(*v4_args(), 1, 3, materialise_logits=True, **kw), 4),
+    "fwd_ranges": (lambda **kw: lidx.lidx_indexer_fwd_ranges(*v4_args(), *ranges(), 3, **kw), 3),
+    "fwd_noalloc": (lambda **kw: lidx.lidx_indexer_fwd_noalloc(*v4_args(), 1, 3, **kw), 2),
+    "logits": (lambda **kw: lidx.lidx_indexer_logits(*v4_args(), **kw), 1),
+    "extract": (lambda **kw: lidx.lidx_extract_topk_scores(fake(2, 4, 6, dtype=f32), fake(2, 4, 3, dtype=i32), **kw), 1),
+    "topk_rows": (lambda **kw: lidx.lidx_topk_rows(fake(2, 4, 6, dtype=f32), 3, **kw), 2),
+    "scores_v41": (lambda **kw: lidx.lidx_indexer_scores_v41(*v41_args(), **kw), 2),
+    "topk_v41": (lambda **kw: lidx.lidx_indexer_topk_v41(*v41_args(), 3, **kw), 4),
+    "topk_v41 no scores": (lambda **kw: lidx.lidx_indexer_topk_v41(*v41_args(), 3, keep_scores=False, **kw), 3),
+    "bwd": (lambda **kw: lidx.lidx_indexer_bwd(*bwd_args(), 1, **kw), 4),
+    "bwd_ranges": (lambda **kw: lidx.lidx_indexer_bwd_ranges(*bwd_args(), *ranges(), **kw), 4),
     "rope": (lambda **kw: lidx.lidx_rope(*rope_args(), **kw), 1),
     "rope x2": (lambda **kw: lidx.lidx_rope(*rope_args(), x2=fake(2, 3, 1, 16), **kw), 2),
     "rope strided": (lambda **kw: lidx.lidx_rope(fake(3, 2, 4, 16).transpose(0, 1), *rope_args()[1:], **kw), 1),
@@ -136,6 +165,37 @@ def test_scratch_is_not_handed_out_while_the_call_runs(Hq, Hkv):
         st.synchronize()
         assert all(bool((m == 0xA5).all()) for m in mine)
         assert torch.equal(got, want) and torch.equal(gl, wl)
+    assert lidx.lidx_device_status() == 0
+
+
+@pytest.mark.gpu
+def test_scratch_of_the_indexer_calls():
+    """The same for the fused forward and its backward, whose scratch holds logits and partial gradients."""
+    import workloads
+
+    wl = workloads.WORKLOADS["tiny"]
+    q, k, w = (t.to(DEV) for t in workloads.v4_inputs(wl, 5))
+    grad = torch.randn(wl.B, wl.S, wl.topk, generator=torch.Generator(device=DEV).manual_seed(4), device=DEV)
+
+    def both(stream=None):
+        idx, sc, _ = lidx.lidx_indexer_fwd(q, k, w, wl.ratio, wl.topk, stream=stream)
+        return (idx, sc, *lidx.lidx_indexer_bwd(q, k, w, idx, grad, wl.ratio, stream=stream))
+
+    want = both()
+    D = q.shape[3]
+    sizes = [lidx.lidx_workspace_bytes(op, wl.B, wl.S, k.shape[0], wl.H, D, wl.topk)
+             for op in (lidx.OP_INDEXER_FWD, lidx.OP_INDEXER_BWD)]
+    st = torch.cuda.Stream()
+    for _ in range(3):
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            torch.cuda._sleep(20_000_000)
+        got = both(st)
+        mine = [torch.full((n,), 0xA5, dtype=torch.uint8, device=DEV) for n in sizes * 2 if n]
+        torch.cuda.current_stream().synchronize()
+        st.synchronize()
+        assert all(bool((m == 0xA5).all()) for m in mine)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert lidx.lidx_device_status() == 0
 
 
