@@ -382,7 +382,8 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                             fade = fade || f;
                         }
                     }
-                    if (__any_sync(0xffffffffu, fade)) {  // (orders the writes above for the warp, too)
+                    __syncwarp();  // the writes above are seen by all lanes (a vote orders no memory)
+                    if (__any_sync(0xffffffffu, fade)) {
 #pragma unroll
                         for (int i = 0; i < NC; i += 4) {
                             const float4 f = *reinterpret_cast<const float4*>(sAl + i);
