@@ -317,7 +317,8 @@ int lidx_rope(const lidx_rope_tensor* t, int nt, const int32_t* pos, const int64
  *   count        int32 [B], nullable: new tokens of the sequence (at most S; NULL: S)
  * Token i < count[b] goes to position p = start[b] + i: page block_table[b][p / page], slot p % page.
  * Tokens whose position or page id is out of range are dropped.  The scale of a page and head is a
- * power of two: the smallest 2^e, e >= -40, with |x| <= 448 * 2^e for all its new tokens; a
+ * power of two: the smallest 2^e, e >= -40, with |x| <= 448 * 2^e for all finite values of its new tokens
+ * (infinities and NaN are stored as NaN codes, e4m3 having no infinity, and change no scale); a
  * page that holds earlier tokens of the sequence keeps the larger of that and its old scale, and if it
  * grows the earlier tokens are rounded to it.  Other slots and pages are left as they were.
  * A page must belong to one sequence of the call.

@@ -589,7 +589,8 @@ def lidx_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, sta
     """Writes k, v [B,S,Hkv,D] bf16 behind the start[b] tokens that each sequence's pages hold, in
     8 bits with a power-of-two scale for each page and head.  k_cache, v_cache [P,Hkv,page,D]
     float8_e4m3fn and k_scale, v_scale [P,Hkv] fp32 are updated in place; block_table int32
-    [B,max_pages]; count int32 [B] or None: new tokens of each sequence."""
+    [B,max_pages]; count int32 [B] or None: new tokens of each sequence.  Infinities and NaN are stored as
+    NaN and change no scale."""
     shape, ks, dev = _strided(k, "k", _bf16)
     shape_v, vs, _ = _strided(v, "v", _bf16, dev)
     if shape_v != shape:

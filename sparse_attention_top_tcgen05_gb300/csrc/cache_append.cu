@@ -3,7 +3,8 @@
 // A page of one head has one scale, a power of two 2^e: the smallest (e >= -40) for which the page's new
 // tokens fit in +-448 * 2^e, or the page's old scale if that is larger and the page holds earlier
 // tokens.  With powers of two a growing scale only moves the exponents of the earlier codes: they
-// stay exact unless they fall among e4m3's subnormals.
+// stay exact unless they fall among e4m3's subnormals.  Infinities and NaN become NaN codes and do not count for
+// the scale; the pass that sorts them out runs only in blocks that have one.
 //
 // One block per (sequence, page it touches, head, k or v).  It keeps its tokens in registers between
 // the maximum and the conversion, so each input byte is read once.
@@ -37,7 +38,7 @@ struct AppendParams {
     int S, Hkv, D, page, max_pages, J;
 };
 
-// Smallest e >= kCacheMinExp with amax <= 448 * 2^e.  448 = 1.75 * 2^8.
+// Smallest e >= kCacheMinExp with amax <= 448 * 2^e, amax finite.  448 = 1.75 * 2^8.
 __device__ __forceinline__ float append_scale(uint32_t amax_bf16) {
     if (amax_bf16 == 0) return exp2f((float)kCacheMinExp);
     int ex;
@@ -45,6 +46,16 @@ __device__ __forceinline__ float append_scale(uint32_t amax_bf16) {
     int e = ex - 9 + (m > 0.875f ? 1 : 0);
     e = e < kCacheMinExp ? kCacheMinExp : e;
     return ldexpf(1.f, e);
+}
+
+constexpr uint32_t kBf16Inf = 0x7f80;  // |code| of infinity; NaN lies above
+
+// Larger |code| of a pair's finite values; infinities become NaN, which the conversion to e4m3 keeps.
+__device__ __forceinline__ uint32_t append_finite(uint32_t& pair) {
+    uint32_t lo = pair & 0x7fffu, hi = (pair >> 16) & 0x7fffu;
+    if (lo >= kBf16Inf) pair |= 0x7fffu, lo = 0;
+    if (hi >= kBf16Inf) pair |= 0x7fff0000u, hi = 0;
+    return max(lo, hi);
 }
 
 __global__ void __launch_bounds__(kAppThreads, 5) cache_append_kernel(const __grid_constant__ AppendParams p) {
@@ -95,6 +106,26 @@ __global__ void __launch_bounds__(kAppThreads, 5) cache_append_kernel(const __gr
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kAppThreads / 32; ++i) m = max(m, s_top[i]);
+    if (m >= kBf16Inf) {  // (the same in all threads)
+        // Infinities and NaN are stored as NaN (e4m3 has no infinity), and the scale is that of the finite values.
+        uint32_t fin = 0;
+#pragma unroll
+        for (int i = 0; i < kAppVecs; ++i) {
+            if ((int)threadIdx.x + i * kAppThreads < n) {
+                fin = max(fin, append_finite(v[i].x));
+                fin = max(fin, append_finite(v[i].y));
+                fin = max(fin, append_finite(v[i].z));
+                fin = max(fin, append_finite(v[i].w));
+            }
+        }
+        fin = __reduce_max_sync(0xffffffffu, fin);
+        __syncthreads();  // the maxima above are read
+        if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = fin;
+        __syncthreads();
+        m = 0;
+#pragma unroll
+        for (int i = 0; i < kAppThreads / 32; ++i) m = max(m, s_top[i]);
+    }
     const bool kept = p0 < start;
     float now = append_scale(m);
     if (kept) now = fmaxf(now, old);
