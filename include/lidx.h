@@ -334,7 +334,10 @@ int lidx_cache_append(const void* k, const void* v, const int64_t* ks, const int
 /*
  * Attention over a paged 8-bit cache.
  *   q            bf16 [B,S,Hq,D], strides (B, S, Hq) in qs (host int64[3]; multiples of 8)
- *   caches, scales, block_table: as lidx_cache_append; scales positive and finite
+ *   caches, scales, block_table: as lidx_cache_append.  Scales in 2^-80 .. 2^100 (lidx_cache_append gives 2^-40 and
+ *                more, and 2^100 or less where no |x| is above 448 * 2^100), the value scales of the keys that one row
+ *                sees within 2^100 of each other; a value scale below 2^-80 counts as 2^-80.  Scores must be
+ *                finite in fp32
  *   kv_len       int32 [B]: keys of the sequence
  *   q_pos        int32 [B], nullable: position of the sequence's first query.  Row (b,s) sees keys
  *                [0, min(kv_len[b], (q_pos[b]+s+1)/compress_ratio)) (the causal rule of

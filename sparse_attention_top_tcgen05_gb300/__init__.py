@@ -615,7 +615,7 @@ def lidx_cache_attn_workspace_bytes(B, S, Hq, Hkv, D, topk=0) -> int:
 def lidx_cache_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, q_pos=None, compress_ratio=1,
                     topk_indices=None, softmax_scale=None, want_lse=False, stream=None, out=None,
                     workspace=None):
-    """Attention of q [B,S,Hq,D] bf16 over a cache written by lidx_cache_append.
+    """Attention of q [B,S,Hq,D] bf16 over a cache written by lidx_cache_append (scales 2^-80 .. 2^100).
 
     kv_len int32 [B]: keys of each sequence.  q_pos int32 [B] or None: with it, row (b,s) sees keys
     below (q_pos[b]+s+1)//compress_ratio only.  topk_indices int32 [B,S,topk] or None: the row sees

@@ -44,6 +44,9 @@ constexpr int kASlotBytes = kATile * 128;       // one K or V tile: 128 bytes a 
 constexpr int kAMeta = 6;                       // stages of per-key scales
 constexpr float kATop = 8.f;                    // weights are scaled to 2^8
 constexpr float kALn2 = 0.693147180559945309f;
+// Smallest value scale.  A row's sum adds weights of at most 2^8.3 divided by their value scales: 2^30 keys of this one stay
+// below 2^119.  At the other end, 2^100, the largest weight is 2^-92 there, and fp32 has 2^34 normal steps below it.
+constexpr float kAMinScale = 0x1p-80f;
 
 // Row (b, s) sees keys [0, end).
 __device__ __forceinline__ int attn_end(const AttnParams& p, int b, int s) {
@@ -311,7 +314,7 @@ __device__ __forceinline__ void attn_produce(const AttnParams& p, AttnWalk& wk, 
             if (lead) tma_load_2d(x.kv + s0 * kASlotBytes + lane * 512, tmk, x.kv_full + s0, 0, row);
             last_k = tc;
             const int left = good ? r0.limit - (r0.tile * kATile + 4 * lane) : 0;  // keys of the lane that count
-            const float f = a * p.scale_log2, y = __log2f(fmaxf(v, 0x1p-60f)), iv = exp2_approx(-y);
+            const float f = a * p.scale_log2, y = __log2f(fmaxf(v, kAMinScale)), iv = exp2_approx(-y);
             const float none = -INFINITY;
             const int at = ms * kATile + 4 * lane;
             *reinterpret_cast<float4*>(x.key_a + at) = make_float4(f, f, f, f);
@@ -389,7 +392,7 @@ __device__ __forceinline__ void attn_produce(const AttnParams& p, AttnWalk& wk, 
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int at = ms * kATile + 32 * i + lane;
-                const float y = __log2f(fmaxf(v[i], 0x1p-60f));
+                const float y = __log2f(fmaxf(v[i], kAMinScale));
                 x.key_a[at] = good[i] ? a[i] * p.scale_log2 : 0.f;
                 x.key_lv[at] = good[i] ? y : -INFINITY;
                 x.key_iv[at] = exp2_approx(-y);
