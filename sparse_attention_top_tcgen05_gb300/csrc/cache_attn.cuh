@@ -472,7 +472,8 @@ __device__ __forceinline__ void attn_queries(const AttnParams& p, AttnWalk& wk, 
             // factor and its inverse are normal numbers
             int ex = (int)(top >> 7);
             ex = top == 0 ? 127 + 7 : (ex < 16 ? 16 : ex);
-            const float up = __int_as_float((254 + 7 - ex) << 23);
+            // (a row with an infinity or a NaN is NaN as a whole, as its scores are: e4m3 would take infinity for 448)
+            const float up = __int_as_float(ex == 255 ? 0x7fffffff : (254 + 7 - ex) << 23);
             if (sub == 0) x.q_scale[qb * N + n] = __int_as_float((ex - 7) << 23);
             uint32_t hi[4], lo[4];
 #pragma unroll
