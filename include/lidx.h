@@ -350,7 +350,7 @@ int lidx_cache_append(const void* k, const void* v, const int64_t* ks, const int
  *   lse          fp32 [B,S,Hq], nullable: log of the sum of exp(score); -inf where no key is seen
  * Query head h reads key/value head h / (Hq/Hkv).  Keys on pages whose id is out of range are not seen;
  * what unseen slots hold (NaN codes included) does not reach the output.  A row that sees a key and whose
- * query holds an infinity or a NaN is NaN.
+ * query holds an infinity or a NaN is NaN, and so is one that sees a key with a NaN code; its lse is NaN, too.
  *   workspace    lidx_cache_attn_workspace_bytes(...) bytes, 256-byte aligned (NULL when 0)
  * Rules as lidx_cache_append, and: Hq a multiple of Hkv, Hq/Hkv <= 128; topk 1 .. 2^20 with
  * topk_indices; B * S * Hq < 2^31; softmax_scale finite.

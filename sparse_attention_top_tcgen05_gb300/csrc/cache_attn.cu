@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                         attn_scores<MASK, CH>(s_addr + cc, qs + cc, sEnd + cc, a2, lv2, key, seen, score);
                         float top[CH];
 #pragma unroll
-                        for (int i = 0; i < CH; ++i) top[i] = warp_max(score[i]);
+                        for (int i = 0; i < CH; ++i) top[i] = warp_max_nan(score[i]);
                         if (lane == 0) {
 #pragma unroll
                             for (int i = 0; i < CH; i += 4)
@@ -371,8 +371,8 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                     for (int i = 0; i < MC; ++i) {
                         const int col = lane + 32 * i;
                         if (col < NC) {
-                            const float M = fmaxf(fmaxf(sWt[col], sWt[NC + col]), fmaxf(sWt[2 * NC + col], sWt[3 * NC + col]));
-                            const float mn = fmaxf(mw[i], M);
+                            const float M = max_nan(max3_nan(sWt[col], sWt[NC + col], sWt[2 * NC + col]), sWt[3 * NC + col]);
+                            const float mn = max_nan(mw[i], M);
                             const bool f = mn > mw[i] && mw[i] != -INFINITY;
                             sAl[col] = f ? exp2_approx(mw[i] - mn) : 1.f;
                             sSh[col] = M == -INFINITY ? kATop : kATop - M;
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                     // (four barriers: the softmax may be three tiles ahead of the joining)
                     ok = ok && mbar_wait(p_full + (tc & 3), (tc >> 2) & 1, p.wait_ns);
                     if (d < N) {
-                        const float M = sMt[(tc & 3) * N + d], mn = fmaxf(m, M);
+                        const float M = sMt[(tc & 3) * N + d], mn = max_nan(m, M);
                         sA[bf * N + d] = m == -INFINITY ? 0.f : exp2_approx(m - mn);
                         sB[bf * N + d] = M == -INFINITY ? 0.f : exp2_approx(M - mn);
                         m = mn;
@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                                         : -1;
                     sRow[d] = row;
                     sInv[d] = l > 0.f ? 1.f / l : 0.f;
-                    if (p.lse && row >= 0) p.lse[row] = l > 0.f ? (m + log2f(l) - kATop) * kALn2 : -INFINITY;
+                    if (p.lse && row >= 0) p.lse[row] = attn_lse(m, l);
                 }
                 named_bar_sync(bar_id, 128);
                 if (d < p.D) {
@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 1) cache_attn_join_kernel(con
         reinterpret_cast<uint2*>(p.out + row * p.D)[lane] =
             make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     }
-    if (p.lse && lane == 0) p.lse[row] = l > 0.f ? (m + log2f(l) - kATop) * kALn2 : -INFINITY;
+    if (p.lse && lane == 0) p.lse[row] = attn_lse(m, l);
 }
 
 // ------------------------------------------------------------------- host

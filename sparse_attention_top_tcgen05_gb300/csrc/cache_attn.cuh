@@ -137,6 +137,12 @@ __host__ __device__ inline size_t attn_ws_bytes(int N, int grid) {
     return (size_t)grid * sizeof(AttnHeader) + (size_t)grid * 2 * attn_part_floats(N) * 4;
 }
 
+// log of the sum of exp(score) from a row's maximum and sum.  The largest key adds 2^8 / (its value scale), so only a row
+// without keys has a sum of zero.  A NaN score makes its row's maximum and sum NaN.
+__device__ __forceinline__ float attn_lse(float m, float l) {
+    return l == 0.f ? -INFINITY : (m + log2f(l) - kATop) * kALn2;
+}
+
 // Two floats (at most 256 in size) -> e4m3 hi and lo pairs in the low halves.
 __device__ __forceinline__ void split_e4m3(float x0, float x1, uint32_t& hi, uint32_t& lo) {
     uint32_t f, b, r;

@@ -319,14 +319,14 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                             for (int h = 0; h < 32; h += 16) {
                                 float b = u[h];
 #pragma unroll
-                                for (int k = 1; k < 15; k += 2) b = max3(b, u[h + k], u[h + k + 1]);
-                                b = fmaxf(b, u[h + 15]);
-                                if (b != -INFINITY) top = fmaxf(top, fmaf(b, ka[at + h] * qs, kl[at + h]));
+                                for (int k = 1; k < 15; k += 2) b = max3_nan(b, u[h + k], u[h + k + 1]);
+                                b = max_nan(b, u[h + 15]);
+                                if (b != -INFINITY) top = max_nan(top, fmaf(b, ka[at + h] * qs, kl[at + h]));
                             }
                         } else {
                             wide_scores<MASK, UNI, false>(ka + at, kl + at, qs, 0.f, vis[i], u);
 #pragma unroll
-                            for (int k = 0; k < 32; k += 2) top = max3(top, u[k], u[k + 1]);
+                            for (int k = 0; k < 32; k += 2) top = max3_nan(top, u[k], u[k + 1]);
                         }
                     }
                     if constexpr (UNI)
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                     float a0, a1, b0, b1;
                     unpack2(sum0, a0, a1);
                     unpack2(sum1, b0, b1);
-                    const float mn = fmaxf(m, top);
+                    const float mn = max_nan(m, top);
                     if (top != -INFINITY) {
                         l = (m == -INFINITY ? 0.f : l * exp2_approx(m - mn)) + ((a0 + a1) + (b0 + b1)) * exp2_approx(top - mn);
                         m = mn;
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                 for (int t = wk.t0; t < wk.t1; ++t, ++tc) {
                     // (four barriers: the softmax may be three tiles ahead of the joining)
                     ok = ok && mbar_wait(p_full + (tc & 3), (tc >> 2) & 1, p.wait_ns);
-                    const float top = works ? sMt[(tc & 3) * N + row] : -INFINITY, mn = fmaxf(m, top);
+                    const float top = works ? sMt[(tc & 3) * N + row] : -INFINITY, mn = max_nan(m, top);
                     const float fa = m == -INFINITY ? 1.f : exp2_approx(m - mn);  // (acc is zero before a row's first key)
                     const float fb = top == -INFINITY ? 0.f : exp2_approx(top - mn);
                     m = mn;
@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                             out[i] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     }
-                    if (p.lse && d0 == 0) p.lse[at] = l > 0.f ? (m + log2f(l) - kATop) * kALn2 : -INFINITY;
+                    if (p.lse && d0 == 0) p.lse[at] = attn_lse(m, l);
                 }
             } else {
                 const int slot = 2 * c + (wk.first ? 0 : 1);

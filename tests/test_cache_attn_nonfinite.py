@@ -68,3 +68,25 @@ def test_keys(S, Hq, Hkv, D, lens):
     idx = c.g.integers(0, t, (2, S, 60))
     idx[0, :, 30] = t
     _check(c, rows, q_pos=pos, idx=idx)
+
+
+@pytest.mark.parametrize("what", ["q", "q inf", "k"])
+@pytest.mark.parametrize("Hq,n", [(8, 300), (32, 300), (64, 300), (128, 300), (16, 20000), (32, 20000), (48, 20000), (80, 20000)])
+def test_log_sum_exp_of_nan_rows(Hq, n, what):
+    """NaN rows say so: -inf is for rows that see no key.  Short rows and rows joined from parts, early keys and late ones."""
+    c = Case(Hq + n, 4, 1, Hq, 1, 64, 64, [n, n, 0, n])
+    nan = np.zeros((4, 1, Hq), bool)
+    if what == "k":
+        for b, t in ((0, 3), (1, n - 1)):
+            c.kc[c.table[b, t // 64], 0, t % 64, 11] = 0x7F
+        nan[:2] = True
+    else:
+        c.q[0, 0, 2, 7] = c.q[3, 0, Hq - 1, 0] = c.q[2, 0, 1, 0] = NAN if what == "q" else INF
+        nan[0, 0, 2] = nan[3, 0, Hq - 1] = True
+    idx = np.stack([np.concatenate([c.g.permutation(n - 2)[:200], [3, n - 1]]) for _ in range(4)])[:, None]
+    for given in (None, torch.from_numpy(idx.astype(np.int32)).to(DEV)):
+        o, lse = lidx.lidx_cache_attn(*c.args(), topk_indices=given, want_lse=True)
+        _status_ok()
+        o, lse = o.float().cpu().numpy(), lse.cpu().numpy()
+        assert np.array_equal(np.isnan(lse), nan) and np.array_equal(np.isnan(o).all(-1), nan)
+        assert np.isneginf(lse[2]).all() and np.isfinite(lse[~nan & (c.lens > 0)[:, None, None]]).all()
