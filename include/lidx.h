@@ -348,9 +348,14 @@ int lidx_cache_append(const void* k, const void* v, const int64_t* ks, const int
  *   softmax_scale  the scores are softmax_scale * q . k
  *   out          bf16 [B,S,Hq,D]; a row that sees no key is 0
  *   lse          fp32 [B,S,Hq], nullable: log of the sum of exp(score); -inf where no key is seen
- * Query head h reads key/value head h / (Hq/Hkv).  Keys on pages whose id is out of range are not seen;
- * what unseen slots hold (NaN codes included) does not reach the output.  A row that sees a key and whose
- * query holds an infinity or a NaN is NaN, and so is one that sees a key with a NaN code; its lse is NaN, too.
+ * Query head h reads key/value head h / (Hq/Hkv).  Keys on pages whose id is out of range are not seen.
+ * NaN and infinities:
+ *   - What slots hold that no row of the call sees (NaN codes included) does not reach the output.
+ *   - A row that sees a key and whose query holds an infinity or a NaN is NaN, and so is one that sees a key
+ *     with a NaN code; its lse is NaN, too.
+ *   - A NaN code of a value makes its dim NaN in the rows that see the key.  In a causal call over all keys (q_pos,
+ *     no topk_indices) it may do so in the rows of the up to 127 tokens before the first that sees the key, too: they
+ *     share a product with it, and their zero weight times NaN is NaN.  Other dims, the heads of other keys and lse do not change.
  *   workspace    lidx_cache_attn_workspace_bytes(...) bytes, 256-byte aligned (NULL when 0)
  * Rules as lidx_cache_append, and: Hq a multiple of Hkv, Hq/Hkv <= 128; topk 1 .. 2^20 with
  * topk_indices; B * S * Hq < 2^31; softmax_scale finite.
