@@ -33,6 +33,8 @@
 
 namespace lidx {
 
+constexpr int kACols = 16;  // columns of a softmax thread
+
 // Configuration of the kernel with N columns, N = 16 or 32.
 template <int N>
 struct AttnCfg {
@@ -40,7 +42,7 @@ struct AttnCfg {
     // Two softmax groups of four warps, 16 columns each.  At N = 16 they take the tiles in turn, at N = 32 they share each
     // tile's columns: a thread keeps its 16 scores and sums in registers either way.
     static constexpr bool SPLIT = N == 32;
-    static constexpr int SG = 2, NC = 16, QB = 2, SLOTS = 8;
+    static constexpr int SG = 2, NC = kACols, QB = 2, SLOTS = 8;
     static constexpr int Q_BYTES = 2 * N * 128;        // hi and lo
     static constexpr int P_BYTES = 2 * kASlotBytes;    // hi and lo
     static constexpr int OFF_P = SLOTS * kASlotBytes;
@@ -77,10 +79,12 @@ struct AttnCfg {
     static_assert(R_MMA <= R_LAUNCH && R_PROD <= R_LAUNCH && R_SOFT >= R_LAUNCH && R_JOIN >= R_LAUNCH, "directions");
 };
 
-// Sums over the warp's lanes of 32 columns: lane i returns column i's.
-__device__ __forceinline__ float warp_sum_columns(float (&v)[32], int lane) {
+// Sums over the warp's lanes of 16 columns: lanes i and i + 16 return column i's.
+__device__ __forceinline__ float warp_sum_columns(float (&v)[kACols], int lane) {
 #pragma unroll
-    for (int step = 16; step > 0; step >>= 1) {
+    for (int i = 0; i < kACols; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
+#pragma unroll
+    for (int step = 8; step > 0; step >>= 1) {
         const bool up = lane & step;
 #pragma unroll
         for (int i = 0; i < step; ++i) {
@@ -91,18 +95,15 @@ __device__ __forceinline__ float warp_sum_columns(float (&v)[32], int lane) {
     return v[0];
 }
 
-// x of CH columns of this thread's key: (S^T * key's factor) * column's factor + log2(v scale); unseen -inf.
-template <bool MASK, int CH>
+// x of the columns of this thread's key: (S^T * key's factor) * column's factor + log2(v scale); unseen -inf.
+template <bool MASK>
 __device__ __forceinline__ void attn_scores(uint32_t s_addr, const float* qs, const int* ends, uint64_t a2,
-                                            uint64_t lv2, int key, bool seen, float (&x)[CH]) {
-    uint32_t r[CH];
-    if constexpr (CH == 32)
-        tmem_ld32(s_addr, r);
-    else
-        tmem_ld16(s_addr, r);
+                                            uint64_t lv2, int key, bool seen, float (&x)[kACols]) {
+    uint32_t r[kACols];
+    tmem_ld16(s_addr, r);
     tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < CH; i += 4) {
+    for (int i = 0; i < kACols; i += 4) {
         const float4 q4 = *reinterpret_cast<const float4*>(qs + i);
         const uint64_t x0 = fma2(mul2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), a2),
                                  pack2(q4.x, q4.y), lv2);
@@ -126,7 +127,6 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                       const __grid_constant__ AttnParams p) {
     using C = AttnCfg<N>;
     constexpr int NC = C::NC, SLOTS = C::SLOTS, QB = C::QB;
-    constexpr int CH = NC < 32 ? NC : 32;  // columns of a chunk in registers
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t* const sP = smem + C::OFF_P;
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
 #pragma unroll
                             for (int k = 0; k < 4; ++k) umma_f8(d, a + 2 * k, b + (N * 128 >> 4) + 2 * k, id_s, 1);
                         } else {
-                            // (with `if (k < nk)` around unrolled products the N = 128 build took wrong operands)
+                            // narrower heads: whatever lies in the places past D is zero, so fewer steps do
 #pragma unroll 1
                             for (int k = 0; k < nk; ++k) umma_f8(d, a + 2 * k, b + 2 * k, id_s, k > 0);
 #pragma unroll 1
@@ -295,7 +295,6 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
         float* const sAl = sBe + NC;                                                   // fade of the sum
         int* const sEnd = (int*)(smem + C::OFF_END) + grp * NC;
         const uint32_t lane_addr = tmem + ((uint32_t)(wg_warp * 32) << 16) + c0;
-        constexpr int MC = (NC + 31) / 32;  // columns of a lane where a warp looks at all NC maxima
         bool ok = true;
         int tc = 0, sc = 0, odd = 0;
         if (p.idx) {
@@ -321,9 +320,7 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
             float l[NC];
 #pragma unroll
             for (int i = 0; i < NC; ++i) l[i] = 0.f;
-            float mw[MC];  // running maxima of columns lane, lane + 32, the same in the group's four warps
-#pragma unroll
-            for (int i = 0; i < MC; ++i) mw[i] = -INFINITY;
+            float mw = -INFINITY;  // running maximum of column lane (of NC), the same in the group's four warps
             for (int t = wk.t0; t < wk.t1; ++t, ++tc) {
                 if (!C::SPLIT && (tc & 1) != grp) continue;
                 const int bf = tc & 1, ph = (tc >> 1) & 1, ms = tc % kAMeta;
@@ -349,38 +346,29 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                 odd ^= 1;
                 auto one_tile = [&](auto mask_c) {
                     constexpr bool MASK = decltype(mask_c)::value;
-                    float score[CH];
+                    float score[NC], top[NC];
+                    attn_scores<MASK>(s_addr, qs, sEnd, a2, lv2, key, seen, score);
 #pragma unroll
-                    for (int cc = 0; cc < NC; cc += CH) {
-                        attn_scores<MASK, CH>(s_addr + cc, qs + cc, sEnd + cc, a2, lv2, key, seen, score);
-                        float top[CH];
+                    for (int i = 0; i < NC; ++i) top[i] = warp_max_nan(score[i]);
+                    if (lane == 0) {
 #pragma unroll
-                        for (int i = 0; i < CH; ++i) top[i] = warp_max_nan(score[i]);
-                        if (lane == 0) {
-#pragma unroll
-                            for (int i = 0; i < CH; i += 4)
-                                *reinterpret_cast<float4*>(sWt + wg_warp * NC + cc + i) =
-                                    make_float4(top[i], top[i + 1], top[i + 2], top[i + 3]);
-                        }
+                        for (int i = 0; i < NC; i += 4)
+                            *reinterpret_cast<float4*>(sWt + wg_warp * NC + i) =
+                                make_float4(top[i], top[i + 1], top[i + 2], top[i + 3]);
                     }
                     named_bar_sync(bar_id, 128);
                     // every warp takes the tile's maxima by itself: no second barrier.  (The next tile's go to the other
                     // half of sW, and a warp reads these before it reaches the next tile's barrier.)
                     bool fade = false;
-#pragma unroll
-                    for (int i = 0; i < MC; ++i) {
-                        const int col = lane + 32 * i;
-                        if (col < NC) {
-                            const float M = max_nan(max3_nan(sWt[col], sWt[NC + col], sWt[2 * NC + col]), sWt[3 * NC + col]);
-                            const float mn = max_nan(mw[i], M);
-                            const bool f = mn > mw[i] && mw[i] != -INFINITY;
-                            sAl[col] = f ? exp2_approx(mw[i] - mn) : 1.f;
-                            sSh[col] = M == -INFINITY ? kATop : kATop - M;
-                            sBe[col] = M == -INFINITY ? 0.f : exp2_approx(M - mn);
-                            if (wg_warp == 0) sMt[(tc & 3) * N + c0 + col] = M;
-                            mw[i] = mn;
-                            fade = fade || f;
-                        }
+                    if (lane < NC) {
+                        const float M = max_nan(max3_nan(sWt[lane], sWt[NC + lane], sWt[2 * NC + lane]), sWt[3 * NC + lane]);
+                        const float mn = max_nan(mw, M);
+                        fade = mn > mw && mw != -INFINITY;
+                        sAl[lane] = fade ? exp2_approx(mw - mn) : 1.f;
+                        sSh[lane] = M == -INFINITY ? kATop : kATop - M;
+                        sBe[lane] = M == -INFINITY ? 0.f : exp2_approx(M - mn);
+                        if (wg_warp == 0) sMt[(tc & 3) * N + c0 + lane] = M;
+                        mw = mn;
                     }
                     __syncwarp();  // the writes above are seen by all lanes (a vote orders no memory)
                     if (__any_sync(0xffffffffu, fade)) {
@@ -391,40 +379,28 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                         }
                     }
                     const uint64_t iv2 = seen ? pack2(key_iv, key_iv) : pack2(0.f, 0.f);
+                    uint32_t hi[NC / 4], lo[NC / 4];
 #pragma unroll
-                    for (int cc = 0; cc < NC; cc += CH) {
-                        if constexpr (NC > CH)
-                            attn_scores<MASK, CH>(s_addr + cc, qs + cc, sEnd + cc, a2, lv2, key, seen, score);
-                        uint32_t hi[CH / 4], lo[CH / 4];
-#pragma unroll
-                        for (int i = 0; i < CH; i += 4) {
-                            const float4 sh = *reinterpret_cast<const float4*>(sSh + cc + i);
-                            const float4 be = *reinterpret_cast<const float4*>(sBe + cc + i);
-                            float e0, e1, e2, e3;
-                            unpack2(add2(pack2(score[i], score[i + 1]), pack2(sh.x, sh.y)), e0, e1);
-                            unpack2(add2(pack2(score[i + 2], score[i + 3]), pack2(sh.z, sh.w)), e2, e3);
-                            const float w0 = exp2_approx(e0), w1 = exp2_approx(e1);
-                            const float w2 = exp2_approx(e2), w3 = exp2_approx(e3);
-                            unpack2(fma2(mul2(pack2(w0, w1), iv2), pack2(be.x, be.y), pack2(l[cc + i], l[cc + i + 1])),
-                                    l[cc + i], l[cc + i + 1]);
-                            unpack2(fma2(mul2(pack2(w2, w3), iv2), pack2(be.z, be.w),
-                                         pack2(l[cc + i + 2], l[cc + i + 3])),
-                                    l[cc + i + 2], l[cc + i + 3]);
-                            uint32_t h0, l0, h1, l1;
-                            split_e4m3(w0, w1, h0, l0);
-                            split_e4m3(w2, w3, h1, l1);
-                            hi[i / 4] = h0 | (h1 << 16);
-                            lo[i / 4] = l0 | (l1 << 16);
-                        }
-#pragma unroll
-                        for (int k = 0; k < CH / 16; ++k) {
-                            const int j = (((c0 + cc) >> 4) + k) ^ (wtid & 7);  // 128-byte swizzle
-                            *reinterpret_cast<uint4*>(prow + (j << 4)) =
-                                make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
-                            *reinterpret_cast<uint4*>(prow + kASlotBytes + (j << 4)) =
-                                make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
-                        }
+                    for (int i = 0; i < NC; i += 4) {
+                        const float4 sh = *reinterpret_cast<const float4*>(sSh + i);
+                        const float4 be = *reinterpret_cast<const float4*>(sBe + i);
+                        float e0, e1, e2, e3;
+                        unpack2(add2(pack2(score[i], score[i + 1]), pack2(sh.x, sh.y)), e0, e1);
+                        unpack2(add2(pack2(score[i + 2], score[i + 3]), pack2(sh.z, sh.w)), e2, e3);
+                        const float w0 = exp2_approx(e0), w1 = exp2_approx(e1);
+                        const float w2 = exp2_approx(e2), w3 = exp2_approx(e3);
+                        unpack2(fma2(mul2(pack2(w0, w1), iv2), pack2(be.x, be.y), pack2(l[i], l[i + 1])), l[i], l[i + 1]);
+                        unpack2(fma2(mul2(pack2(w2, w3), iv2), pack2(be.z, be.w), pack2(l[i + 2], l[i + 3])), l[i + 2],
+                                l[i + 3]);
+                        uint32_t h0, l0, h1, l1;
+                        split_e4m3(w0, w1, h0, l0);
+                        split_e4m3(w2, w3, h1, l1);
+                        hi[i / 4] = h0 | (h1 << 16);
+                        lo[i / 4] = l0 | (l1 << 16);
                     }
+                    const int j = (c0 >> 4) ^ (wtid & 7);  // 128-byte swizzle
+                    *reinterpret_cast<uint4*>(prow + (j << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(prow + kASlotBytes + (j << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 };
                 if (masked)
                     one_tile(std::true_type{});
@@ -447,18 +423,10 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
             }
             // the segment's sums: lanes, then (by the joining warps) warps and groups
             ok = ok && mbar_wait(l_empty, (sc & 1) ^ 1, p.wait_ns);
-#pragma unroll
-            for (int cc = 0; cc < NC; cc += CH) {
-                float v[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = i < CH ? l[cc + (i < CH ? i : 0)] : 0.f;
-                const float sum = warp_sum_columns(v, lane);
-                if (lane < CH) sL[(grp * 4 + wg_warp) * NC + cc + lane] = sum;
-            }
-            if (wg_warp == 0) {
-#pragma unroll
-                for (int i = 0; i < MC; ++i)
-                    if (lane + 32 * i < NC) sMw[grp * NC + lane + 32 * i] = mw[i];
+            const float sum = warp_sum_columns(l, lane);
+            if (lane < NC) {
+                sL[(grp * 4 + wg_warp) * NC + lane] = sum;
+                if (wg_warp == 0) sMw[grp * NC + lane] = mw;
             }
             __syncwarp();
             if (lane == 0) {
@@ -473,7 +441,6 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
         regs_inc<C::R_JOIN>();
         const int d = tid & 127, wg_warp = warp & 3;
         constexpr uint32_t bar_id = 1 + C::SG;
-        constexpr int JC = N;  // columns read at a time
         const uint32_t lane_addr = tmem + ((uint32_t)(wg_warp * 32) << 16) + 2 * N;
         float* const sA = (float*)(smem + C::OFF_AB);  // [2][N] fade of acc
         float* const sB = sA + 2 * N;                  // [2][N] of the tile
@@ -503,27 +470,21 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
                     named_bar_sync(bar_id, 128);
                     ok = ok && mbar_wait(o_full + bf, ph, p.wait_ns);
                     tc_fence_after();
+                    uint32_t r[N];
+                    if constexpr (N == 32)
+                        tmem_ld32(lane_addr + bf * N, r);
+                    else
+                        tmem_ld16(lane_addr + bf * N, r);
+                    tmem_ld_wait();
 #pragma unroll
-                    for (int cc = 0; cc < N; cc += JC) {
-                        uint32_t r[JC];
-                        if constexpr (JC == 32)
-                            tmem_ld32(lane_addr + bf * N + cc, r);
-                        else
-                            tmem_ld16(lane_addr + bf * N + cc, r);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < JC; i += 4) {
-                            const float4 fa = *reinterpret_cast<const float4*>(sA + bf * N + cc + i);
-                            const float4 fb = *reinterpret_cast<const float4*>(sB + bf * N + cc + i);
-                            const uint64_t o0 = mul2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])),
-                                                     pack2(fb.x, fb.y));
-                            const uint64_t o1 = mul2(pack2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])),
-                                                     pack2(fb.z, fb.w));
-                            unpack2(fma2(pack2(acc[cc + i], acc[cc + i + 1]), pack2(fa.x, fa.y), o0), acc[cc + i],
-                                    acc[cc + i + 1]);
-                            unpack2(fma2(pack2(acc[cc + i + 2], acc[cc + i + 3]), pack2(fa.z, fa.w), o1),
-                                    acc[cc + i + 2], acc[cc + i + 3]);
-                        }
+                    for (int i = 0; i < N; i += 4) {
+                        const float4 fa = *reinterpret_cast<const float4*>(sA + bf * N + i);
+                        const float4 fb = *reinterpret_cast<const float4*>(sB + bf * N + i);
+                        const uint64_t o0 = mul2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), pack2(fb.x, fb.y));
+                        const uint64_t o1 =
+                            mul2(pack2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), pack2(fb.z, fb.w));
+                        unpack2(fma2(pack2(acc[i], acc[i + 1]), pack2(fa.x, fa.y), o0), acc[i], acc[i + 1]);
+                        unpack2(fma2(pack2(acc[i + 2], acc[i + 3]), pack2(fa.z, fa.w), o1), acc[i + 2], acc[i + 3]);
                     }
                     tc_fence_before();
                     __syncwarp();

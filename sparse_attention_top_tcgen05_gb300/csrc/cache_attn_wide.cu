@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
 #pragma unroll
                             for (int k = 0; k < 4; ++k) umma_f8(d, a + (N * 128 >> 4) + 2 * k, b + 2 * k, id_s, 1);
                         } else {
-                            // (with `if (k < nk)` around unrolled products a build took wrong operands)
+                            // narrower heads: whatever lies in the places past D is zero, so fewer steps do
 #pragma unroll 1
                             for (int k = 0; k < nk; ++k) umma_f8(d, a + 2 * k, b + 2 * k, id_s, k > 0);
 #pragma unroll 1
