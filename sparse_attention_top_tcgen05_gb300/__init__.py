@@ -636,6 +636,8 @@ def lidx_cache_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, 
         _dense(o, "out", _bf16, shape, dev)
         if lse is not None:
             _dense(lse, "lse", _f32, shape[:3], dev)
+        elif want_lse:
+            lse = _new(shape[:3], _f32, q.device, stream)
     L = _lib or lib()
     if workspace is None:
         ws_bytes = L.lidx_cache_attn_workspace_bytes(B, S, Hq, Hkv, D, topk)

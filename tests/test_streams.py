@@ -119,6 +119,8 @@ CALLS = {
     "rope_bwd": (lambda **kw: lidx.lidx_rope_bwd(*rope_args(), **kw), 1),
     "cache_attn": (lambda **kw: lidx.lidx_cache_attn(*attn_args(), **kw), 2),
     "cache_attn lse": (lambda **kw: lidx.lidx_cache_attn(*attn_args(), want_lse=True, **kw), 3),
+    "cache_attn out, lse wanted": (
+        lambda **kw: lidx.lidx_cache_attn(*attn_args(), out=(fake(1, 2, 4, 16), None), want_lse=True, **kw), 2),
     "cache_attn out": (lambda **kw: lidx.lidx_cache_attn(*attn_args(), out=(fake(1, 2, 4, 16), None), **kw), 1),
 }
 
@@ -131,6 +133,13 @@ def test_allocations_belong_to_the_stream_of_the_call(pools, call):
     pools.clear()
     fn(stream=types.SimpleNamespace(cuda_stream=7))
     assert pools == ["raw 7"] * n
+
+
+def test_a_wanted_log_sum_exp_is_returned_beside_a_given_output(pools):
+    o = fake(1, 2, 4, 16)
+    got, lse = lidx.lidx_cache_attn(*attn_args(), out=(o, None), want_lse=True)
+    assert got is o and lse is not None and lse.shape == (1, 2, 4)
+    assert lidx.lidx_cache_attn(*attn_args(), out=(o, None))[1] is None
 
 
 # ------------------------------------------------------------------ GPU
