@@ -64,3 +64,13 @@ def test_what_the_writer_gives(Hq):
         c.kc, c.vc = (t.view(torch.uint8).cpu().numpy() for t in (kc, vc))
         c.ks, c.vs = ks.cpu().numpy(), vs.cpu().numpy()
         _check(c)
+
+
+@pytest.mark.parametrize("exps,q", [((-80, -80), 1.0), ((100, 100), 2.0 ** -107), ((60, 100), 2.0 ** -107), ((-80, -10), 2.0 ** 9)])
+@pytest.mark.parametrize("Hq", [8, 32, 64, 128])
+def test_range_of_key_scales(Hq, exps, q):
+    """Key scales of the same range, with queries that bring the scores to ordinary sizes or below."""
+    c = Case(Hq, 2, 1, Hq, 1, 64, 64, [300, 77], q_scale=q, poison=False)
+    c.ks[:] = np.exp2(c.g.integers(exps[0], exps[1] + 1, c.ks.shape)).astype(np.float32)
+    _check(c)
+    _check(c, idx=np.stack([c.g.permutation(300)[:200] for _ in (0, 1)])[:, None])
