@@ -263,7 +263,8 @@ typedef enum {
     LIDX_ROPE_LINEAR = 1,  /* every frequency divided by `factor` */
     LIDX_ROPE_NTK = 2,     /* base theta * factor^(R/(R-2)): the lowest frequency is divided by `factor` */
     LIDX_ROPE_YARN = 3     /* w (1-g)/factor + w g, g = clamp((r - beta_slow)/(beta_fast - beta_slow), 0, 1),
-                              r = original_len * w / (2 pi) turns within the original length */
+                              r = original_len * w / (2 pi) turns within the original length: a ramp that
+                              is linear in turns, not in the pair's index i */
 } lidx_rope_scaling;
 
 /*
@@ -335,9 +336,9 @@ int lidx_cache_append(const void* k, const void* v, const int64_t* ks, const int
  * Attention over a paged 8-bit cache.
  *   q            bf16 [B,S,Hq,D], strides (B, S, Hq) in qs (host int64[3]; multiples of 8)
  *   caches, scales, block_table: as lidx_cache_append.  Scales in 2^-80 .. 2^100 (lidx_cache_append gives 2^-40 and
- *                more, and 2^100 or less where no |x| is above 448 * 2^100), the value scales of the keys that one row
- *                sees within 2^100 of each other; a value scale below 2^-80 counts as 2^-80.  Scores must be
- *                finite in fp32
+ *                more, and 2^100 or less where no |x| is above 448 * 2^100), the value scales of the keys
+ *                that one row sees within 2^100 of each other; a value scale below 2^-80 counts as 2^-80.
+ *                Scores must be finite in fp32
  *   kv_len       int32 [B]: keys of the sequence
  *   q_pos        int32 [B], nullable: position of the sequence's first query.  Row (b,s) sees keys
  *                [0, min(kv_len[b], (q_pos[b]+s+1)/compress_ratio)) (the causal rule of
@@ -351,11 +352,12 @@ int lidx_cache_append(const void* k, const void* v, const int64_t* ks, const int
  * Query head h reads key/value head h / (Hq/Hkv).  Keys on pages whose id is out of range are not seen.
  * NaN and infinities:
  *   - What slots hold that no row of the call sees (NaN codes included) does not reach the output.
- *   - A row that sees a key and whose query holds an infinity or a NaN is NaN, and so is one that sees a key
- *     with a NaN code; its lse is NaN, too.
+ *   - A row that sees a key and whose query holds an infinity or a NaN is NaN, and so is one that sees a
+ *     key with a NaN code; its lse is NaN, too.
  *   - A NaN code of a value makes its dim NaN in the rows that see the key.  In a causal call over all keys (q_pos,
- *     no topk_indices) it may do so in the rows of the up to 127 tokens before the first that sees the key, too: they
- *     share a product with it, and their zero weight times NaN is NaN.  Other dims, the heads of other keys and lse do not change.
+ *     no topk_indices) it may do so in the rows of the up to 127 tokens before the first that sees the key, too:
+ *     they share a product with it, and their zero weight times NaN is NaN.  Other dims, the heads of other
+ *     key/value heads and lse do not change.
  *   workspace    lidx_cache_attn_workspace_bytes(...) bytes, 256-byte aligned (NULL when 0)
  * Rules as lidx_cache_append, and: Hq a multiple of Hkv, Hq/Hkv <= 128; topk 1 .. 2^20 with
  * topk_indices; B * S * Hq < 2^31; softmax_scale finite.

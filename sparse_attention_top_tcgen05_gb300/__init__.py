@@ -506,7 +506,9 @@ def _raw_stream(stream, dev):
 def lidx_rope_freqs(rot_dim, theta=10000.0, scaling=None, factor=1.0, original_len=4096, beta_fast=32.0,
                     beta_slow=1.0, device="cuda") -> torch.Tensor:
     """Rotary frequencies int64 [rot_dim/2]: turns per position in 0.64 fixed point (the bits of
-    unsigned integers).  scaling: None, "linear", "ntk" or "yarn"."""
+    unsigned integers).  scaling: None, "linear", "ntk" or "yarn" (its ramp is linear in the turns that a pair
+    makes within original_len, beta_slow to beta_fast, not in the pair's index).  Any other set of
+    frequencies w, in radians per position, is round(w / (2 pi) * 2**64) as int64."""
     if scaling not in ROPE_SCALING:
         raise ValueError(f"scaling must be one of {list(ROPE_SCALING)}")
     out = torch.empty(max(int(rot_dim) // 2, 1), dtype=torch.int64)
@@ -620,6 +622,7 @@ def lidx_cache_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, 
     kv_len int32 [B]: keys of each sequence.  q_pos int32 [B] or None: with it, row (b,s) sees keys
     below (q_pos[b]+s+1)//compress_ratio only.  topk_indices int32 [B,S,topk] or None: the row sees
     only the listed keys (lidx_indexer_fwd's indices).  softmax_scale defaults to D**-0.5.
+    A row whose query or a key it sees is not finite is NaN, with its log-sum-exp; for NaN values see lidx.h.
     Returns (out [B,S,Hq,D] bf16, lse [B,S,Hq] fp32 or None); ``out`` may hold preallocated ones."""
     shape, qs, dev = _strided(q, "q", _bf16)
     B, S, Hq, D = shape

@@ -10,8 +10,9 @@
 // the maximum and the conversion, so each input byte is read once.
 //
 // What bounds it: a block waits for start, table and tokens one after the other and the maximum at a barrier, so bytes
-// in flight set the rate.  4 x 4097 tokens of 8 heads of 128, call behind call: 17.6 us, 4.8 TB/s with five blocks an SM
-// (18.5 us with four, 18.3 us with six, which spill); one token of 64 sequences: 5.7 us.
+// in flight set the rate.  4 x 4097 tokens of 8 heads of 128 (84 MB): 24.5 us, 3.4 TB/s, with inputs that come from memory;
+// 17.3 us with the same inputs again, most of which L2 holds.  Five blocks an SM (with L2's help 17.6 us, four 18.5 us, six,
+// which spill, 18.3 us).  One token of 64 sequences: 5.4 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

@@ -19,8 +19,8 @@
 // few queries there are.  The N columns are (query token, head of the group), N = 16 or 32; units of more rows go to
 // the kernel in cache_attn_wide.cu.
 //
-// What bounds it: reading the cache once.  8 sequences x 65536 keys, 64 heads on 8: 169 us, 6.3 TB/s,
-// with pages of 16 or 64 tokens.  One shared head does 8 x 65536 keys in 33 us with 16 query heads and 36 us with 32; one
+// What bounds it: reading the cache once.  8 sequences x 65536 keys, 64 heads on 8: 165 us, 6.5 TB/s.
+// One shared head does 8 x 65536 keys in 33 us with 16 query heads and 35 us with 32; one
 // sequence of 1024 keys takes 10 us, which are two launches and one tile's latencies.
 //
 // Work.  The units (sequence, tile of query tokens, kv head) have as many tiles of 128 keys as their last row
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(AttnCfg<N>::THREADS, 1)
 #pragma unroll
                             for (int k = 0; k < 4; ++k) umma_f8(d, a + 2 * k, b + (N * 128 >> 4) + 2 * k, id_s, 1);
                         } else {
-                            // narrower heads: whatever lies in the places past D is zero, so fewer steps do
+                            // (the places past D are zero: a narrower head takes fewer steps)
 #pragma unroll 1
                             for (int k = 0; k < nk; ++k) umma_f8(d, a + 2 * k, b + 2 * k, id_s, k > 0);
 #pragma unroll 1

@@ -10,10 +10,14 @@
 // Tensor memory holds the scores of three tiles and one O: S runs two tiles ahead of O, so a softmax group that ends a
 // tile finds the scores of its next.
 //
-// What bounds it: the softmax groups' issue and latencies.  A chunk of 2048 queries over 16384 keys, 64 heads on 8, takes
-// 1.01 ms, 1021 TFLOP/s of the products (4 FLOP a pair and dim) or twice that as executed in 8-bit pieces; the tensor pipe
-// is active 36 % of the time, issue slots 49 %, and without the softmax it takes 0.67 ms.  4096 rows of 512 selected keys,
-// 64 heads on one: 235 us, of which the rows' output and the exchange of their two copies are 45 us.
+// What bounds it.  Chunks: the softmax groups' issue and latencies.  2048 queries over 16384 keys, 64 heads on 8, take
+// 1.00 ms, 1027 TFLOP/s of the products (4 FLOP a pair and dim) or twice that as executed in 8-bit pieces; the tensor pipe
+// is active 36 % of the time, issue slots 49 %, and without the softmax it takes 0.68 ms.  Selected keys: loading them.  4096
+// rows of 512 keys, 64 heads on one, take 238 us where all of them are seen and 285 us in the causal prompt of 1024
+// compressed keys, whose first rows see few (unseen tiles are walked like others).  Of the 238 us, 151 us are left without softmax,
+// joining, output and conversion of queries.
+//
+// The register split leaves the four kernels 260 to 412 bytes of spills (-Xptxas -v).
 //
 // Units of at most 64 rows (one selected row of 64 heads, a decode step on a shared key head) are laid out twice: row r
 // again as row r + 64.  Of a tile's keys the first copy's weights hold the first 64, the second copy's the others (zeros
@@ -229,7 +233,7 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
 #pragma unroll
                             for (int k = 0; k < 4; ++k) umma_f8(d, a + (N * 128 >> 4) + 2 * k, b + 2 * k, id_s, 1);
                         } else {
-                            // narrower heads: whatever lies in the places past D is zero, so fewer steps do
+                            // (the places past D are zero: a narrower head takes fewer steps)
 #pragma unroll 1
                             for (int k = 0; k < nk; ++k) umma_f8(d, a + 2 * k, b + 2 * k, id_s, k > 0);
 #pragma unroll 1
