@@ -170,6 +170,11 @@ def _scratch(nbytes, device, stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
+def _nbytes(workspace):
+    """Size of a workspace, a caller's own as it is: the library refuses one that is too small."""
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
 def _need(t, name, dtype, dim):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -220,7 +225,7 @@ def _fwd_common(q, k, w, topk, topk_indices, materialise_logits, out, workspace,
     ws_bytes = lidx_workspace_bytes(OP_INDEXER_FWD, B, S, Skv, H, D, topk, lg is not None)
     if workspace is None and ws_bytes:
         workspace = _scratch(ws_bytes, dev, stream)
-    return (S, B, H, D, Skv), idx, sc, lg, workspace, ws_bytes
+    return (S, B, H, D, Skv), idx, sc, lg, workspace
 
 
 def lidx_indexer_fwd(q, k, w, compress_ratio, topk, act="relu", topk_indices=None,
@@ -230,11 +235,11 @@ def lidx_indexer_fwd(q, k, w, compress_ratio, topk, act="relu", topk_indices=Non
     Returns (indices [B,S,topk] int32, scores [B,S,topk] fp32, logits or None).
     ``out`` may hold preallocated (indices, scores, logits) tensors.
     """
-    (S, B, H, D, Skv), idx, sc, lg, workspace, ws_bytes = _fwd_common(
+    (S, B, H, D, Skv), idx, sc, lg, workspace = _fwd_common(
         q, k, w, topk, topk_indices, materialise_logits, out, workspace, stream)
     rc = lib().lidx_indexer_fwd(_ptr(q), _ptr(k), _ptr(w), B, S, Skv, H, D, compress_ratio, topk,
                                 ACT[act], _ptr(topk_indices), _ptr(lg), _ptr(idx), _ptr(sc),
-                                _ptr(workspace), ws_bytes if workspace is not None else 0,
+                                _ptr(workspace), _nbytes(workspace),
                                 _stream(stream))
     _check(rc, "lidx_indexer_fwd")
     return idx, sc, lg
@@ -245,14 +250,14 @@ def lidx_indexer_fwd_ranges(q, k, w, ks, ke, topk, act="relu", topk_indices=None
     """V4 forward where row (b,s) sees keys [ks[s], ke[s]) (int32 [S] CUDA tensors)."""
     _need(ks, "ks", torch.int32, 1)
     _need(ke, "ke", torch.int32, 1)
-    (S, B, H, D, Skv), idx, sc, lg, workspace, ws_bytes = _fwd_common(
+    (S, B, H, D, Skv), idx, sc, lg, workspace = _fwd_common(
         q, k, w, topk, topk_indices, materialise_logits, out, workspace, stream)
     if ks.shape[0] != S or ke.shape[0] != S:
         raise ValueError("ks/ke must have S entries")
     rc = lib().lidx_indexer_fwd_ranges(_ptr(q), _ptr(k), _ptr(w), B, S, Skv, H, D, _ptr(ks), _ptr(ke),
                                        topk, ACT[act], _ptr(topk_indices), _ptr(lg), _ptr(idx),
                                        _ptr(sc), _ptr(workspace),
-                                       ws_bytes if workspace is not None else 0, _stream(stream))
+                                       _nbytes(workspace), _stream(stream))
     _check(rc, "lidx_indexer_fwd_ranges")
     return idx, sc, lg
 
@@ -354,7 +359,7 @@ def lidx_indexer_scores_v41(q, k, w, allowed, act="relu", stream=None, out=None,
         workspace = _scratch(ws_bytes, q.device, stream)
     rc = lib().lidx_indexer_scores_v41(_ptr(q), _ptr(k), _ptr(w), _ptr(allowed), B, S, Skv, H, D,
                                        ACT[act], _ptr(res), _ptr(workspace),
-                                       ws_bytes if workspace is not None else 0, _stream(stream))
+                                       _nbytes(workspace), _stream(stream))
     _check(rc, "lidx_indexer_scores_v41")
     return res
 
@@ -384,7 +389,7 @@ def lidx_indexer_topk_v41(q, k, w, allowed, topk, act="relu", keep_scores=True, 
         workspace = _scratch(ws_bytes, dev, stream)
     rc = lib().lidx_indexer_topk_v41(_ptr(q), _ptr(k), _ptr(w), _ptr(allowed), B, S, Skv, H, D,
                                      ACT[act], topk, _ptr(res), _ptr(idx), _ptr(tsc), _ptr(workspace),
-                                     ws_bytes if workspace is not None else 0, _stream(stream))
+                                     _nbytes(workspace), _stream(stream))
     _check(rc, "lidx_indexer_topk_v41")
     return res, idx, tsc
 
@@ -419,7 +424,7 @@ def _bwd_common(q, k, w, idx, grad, grad_dtype, out, workspace, stream):
     ws_bytes = lidx_workspace_bytes(OP_INDEXER_BWD, B, S, Skv, H, D, topk)
     if workspace is None and ws_bytes:
         workspace = _scratch(ws_bytes, dev, stream)
-    return (S, B, H, D, Skv, topk, gdt), dq, dk, dw, workspace, ws_bytes
+    return (S, B, H, D, Skv, topk, gdt), dq, dk, dw, workspace
 
 
 def lidx_indexer_bwd_ranges(q, k, w, idx, grad, ks, ke, act="relu", grad_dtype=torch.float32,
@@ -427,12 +432,12 @@ def lidx_indexer_bwd_ranges(q, k, w, idx, grad, ks, ke, act="relu", grad_dtype=t
     """Backward where row (b,s) sees keys [ks[s], ke[s]); dk is this call's partial sum."""
     _need(ks, "ks", torch.int32, 1)
     _need(ke, "ke", torch.int32, 1)
-    (S, B, H, D, Skv, topk, gdt), dq, dk, dw, workspace, ws_bytes = _bwd_common(
+    (S, B, H, D, Skv, topk, gdt), dq, dk, dw, workspace = _bwd_common(
         q, k, w, idx, grad, grad_dtype, out, workspace, stream)
     rc = lib().lidx_indexer_bwd_ranges(_ptr(q), _ptr(k), _ptr(w), _ptr(idx), _ptr(grad), B, S, Skv, H,
                                        D, _ptr(ks), _ptr(ke), topk, ACT[act], gdt, _ptr(dq), _ptr(dk),
                                        _ptr(dw), _ptr(workspace),
-                                       ws_bytes if workspace is not None else 0, _stream(stream))
+                                       _nbytes(workspace), _stream(stream))
     _check(rc, "lidx_indexer_bwd_ranges")
     return dq, dk, dw
 
@@ -440,11 +445,11 @@ def lidx_indexer_bwd_ranges(q, k, w, idx, grad, ks, ke, act="relu", grad_dtype=t
 def lidx_indexer_bwd(q, k, w, idx, grad, compress_ratio, act="relu", grad_dtype=torch.float32,
                      stream=None, out=None, workspace=None):
     """Gradients (dq [S,B,H,D], dk [Skv,B,D] in grad_dtype (fp32 or bf16), dw [S,B,H] fp32)."""
-    (S, B, H, D, Skv, topk, gdt), dq, dk, dw, workspace, ws_bytes = _bwd_common(
+    (S, B, H, D, Skv, topk, gdt), dq, dk, dw, workspace = _bwd_common(
         q, k, w, idx, grad, grad_dtype, out, workspace, stream)
     rc = lib().lidx_indexer_bwd(_ptr(q), _ptr(k), _ptr(w), _ptr(idx), _ptr(grad), B, S, Skv, H, D,
                                 compress_ratio, topk, ACT[act], gdt, _ptr(dq), _ptr(dk), _ptr(dw),
-                                _ptr(workspace), ws_bytes if workspace is not None else 0,
+                                _ptr(workspace), _nbytes(workspace),
                                 _stream(stream))
     _check(rc, "lidx_indexer_bwd")
     return dq, dk, dw
