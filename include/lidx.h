@@ -309,6 +309,62 @@ int lidx_rope(const lidx_rope_tensor* t, int nt, const int32_t* pos, const int64
               int layout, int inverse, float mscale, int dtype, void* stream);
 
 /*
+ * A rotation with positions on several axes (text: one; images and video: time, height, width).  Pair i of a
+ * token turns by pos[axis[i]][token] * freqs[i].
+ *   pos     int32 [axes][T0][T1], strides ps (axis, T0, T1) in elements; 0 repeats a position
+ *   freqs   device copy of lidx_rope_freqs's array (or any other in its format)
+ *   axis    uint8 [rot_dim/2] on the device: the axis of each pair; ids of `axes` and more count as axes - 1.  May be
+ *           NULL where axes is 1
+ * Rules: axes 1 .. 255; rot_dim, rot_off, layout and mscale as in lidx_rope.
+ */
+typedef struct {
+    const int32_t* pos;
+    int64_t ps[3];
+    const uint64_t* freqs;
+    const uint8_t* axis;
+    int axes, rot_dim, rot_off, layout;
+    float mscale;
+} lidx_rope_turn;
+
+/* lidx_rope with a rotation of several axes; inverse = 1: its gradient. */
+int lidx_rope_axes(const lidx_rope_tensor* t, int nt, const lidx_rope_turn* r, int64_t T0, int64_t T1, int D, int inverse,
+                   int dtype, void* stream);
+
+/* One tensor of a norm with rotation: x, g and y [T0,T1,H,D] with strides (T0, T1, H) in elements. */
+typedef struct {
+    const void* x;
+    const void* g;   /* backward: gradient of the output */
+    void* y;         /* output; backward: gradient of x.  May be x (or g) with equal strides; other overlaps are
+                        not supported */
+    int64_t xs[3];
+    int64_t gs[3];
+    int64_t ys[3];
+    const void* w;   /* [D], nullable: the norm's weight */
+    float* dw;       /* backward, fp32 [D], nullable: gradient of w (of a weight of ones where w is NULL) */
+    int H;
+} lidx_norm_tensor;
+
+/*
+ * Norm of each head and its rotary positions in one pass: n = x (mean_d x^2 + eps)^-1/2 w over the whole head (D), then
+ * its pairs turn as in lidx_rope; dims outside the rotated part are n.  Computed in fp32, rounded once.
+ *   t        host array of nt = 1 or 2 tensors that share positions (queries and keys), each with its own weight
+ *   dtype    of every x, g and y: 0 fp32, 1 bf16;  w_dtype of every w: 0 fp32, 1 bf16
+ * lidx_norm_rope_bwd: y is the gradient of x, dw that of w summed over all rows (fp32; overwritten).  No atomics: two
+ * calls give the same bits.
+ *   workspace  lidx_norm_rope_bwd_workspace_bytes(D) bytes, 256-byte aligned
+ * A row with an infinity or a NaN is NaN, and its gradients are.  Rules as lidx_rope, and eps >= 0 and finite.  16-byte
+ * aligned tensors, strides and rotated parts (half layout: halves) of heads of up to 512 dims in bf16 and 256 in fp32 take
+ * the faster path.
+ */
+int lidx_norm_rope(const lidx_norm_tensor* t, int nt, const lidx_rope_turn* r, float eps, int64_t T0, int64_t T1, int D,
+                   int dtype, int w_dtype, void* stream);
+int lidx_norm_rope_bwd(const lidx_norm_tensor* t, int nt, const lidx_rope_turn* r, float eps, int64_t T0, int64_t T1, int D,
+                       int dtype, int w_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Device scratch of lidx_norm_rope_bwd on the current device, in bytes. */
+size_t lidx_norm_rope_bwd_workspace_bytes(int D);
+
+/*
  * Writing new keys and values into a paged 8-bit cache.
  *   k, v         bf16 [B,S,Hkv,D], strides (B, S, Hkv) in ks, vs (host int64[3]; multiples of 8)
  *   k/v_cache    e4m3 [num_pages,Hkv,page,D] (1 + 4 + 3 bits, +-448, contiguous)

@@ -19,6 +19,8 @@ Functions carry the C names:
   lidx_indexer_fwd_noalloc  fused forward with the library's own scratch
   lidx_rope_freqs           rotary frequencies in fixed point, scaled for long contexts
   lidx_rope, lidx_rope_bwd  rotary positions of queries and keys, and their gradient
+  lidx_rope_axis_map        the axis of each pair where positions have several (time, height, width)
+  lidx_norm_rope, lidx_norm_rope_bwd  norms of each head with the rotary positions in one pass, and their gradients
   lidx_cache_append         new keys and values into a paged 8-bit cache
   lidx_cache_attn           attention over that cache, at every key or at selected ones
   lidx_workspace_bytes, lidx_cache_attn_workspace_bytes, lidx_device_status,
@@ -56,12 +58,23 @@ EXPORTS = ("lidx_indexer_fwd", "lidx_indexer_fwd_ranges", "lidx_indexer_logits",
            "lidx_workspace_bytes", "lidx_device_status", "lidx_status_string", "lidx_version",
            "lidx_indexer_fwd_noalloc", "lidx_noalloc_scratch_bytes", "lidx_set_wait_limit_ns",
            "lidx_debug_stall_producer", "lidx_rope_freqs", "lidx_rope", "lidx_cache_append",
-           "lidx_cache_attn", "lidx_cache_attn_workspace_bytes")
+           "lidx_cache_attn", "lidx_cache_attn_workspace_bytes", "lidx_rope_axes", "lidx_norm_rope",
+           "lidx_norm_rope_bwd", "lidx_norm_rope_bwd_workspace_bytes")
 
 
 class _RopeTensor(C.Structure):
     _fields_ = [("x", C.c_void_p), ("y", C.c_void_p), ("xs", C.c_int64 * 3), ("ys", C.c_int64 * 3),
                 ("H", C.c_int)]
+
+
+class _RopeTurn(C.Structure):
+    _fields_ = [("pos", C.c_void_p), ("ps", C.c_int64 * 3), ("freqs", C.c_void_p), ("axis", C.c_void_p),
+                ("axes", C.c_int), ("rot_dim", C.c_int), ("rot_off", C.c_int), ("layout", C.c_int), ("mscale", C.c_float)]
+
+
+class _NormTensor(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("g", C.c_void_p), ("y", C.c_void_p), ("xs", C.c_int64 * 3), ("gs", C.c_int64 * 3),
+                ("ys", C.c_int64 * 3), ("w", C.c_void_p), ("dw", C.c_void_p), ("H", C.c_int)]
 
 
 class LidxError(RuntimeError):
@@ -125,7 +138,13 @@ def lib() -> C.CDLL:
                                           i64, i64, i32, i32, f32, P, P, P, sz, P]
             L.lidx_cache_attn_workspace_bytes.argtypes = [i64, i64, i32, i32, i32, i32]
             L.lidx_cache_attn_workspace_bytes.restype = sz
+            L.lidx_rope_axes.argtypes = [P, i32, P, i64, i64, i32, i32, i32, P]
+            L.lidx_norm_rope.argtypes = [P, i32, P, f32, i64, i64, i32, i32, i32, P]
+            L.lidx_norm_rope_bwd.argtypes = [P, i32, P, f32, i64, i64, i32, i32, i32, P, sz, P]
+            L.lidx_norm_rope_bwd_workspace_bytes.argtypes = [i32]
+            L.lidx_norm_rope_bwd_workspace_bytes.restype = sz
             for name in ("lidx_rope_freqs", "lidx_rope", "lidx_cache_append", "lidx_cache_attn",
+                         "lidx_rope_axes", "lidx_norm_rope", "lidx_norm_rope_bwd",
                          "lidx_indexer_fwd", "lidx_indexer_fwd_ranges", "lidx_indexer_logits",
                          "lidx_extract_topk_scores", "lidx_topk_rows", "lidx_indexer_scores_v41",
                          "lidx_indexer_topk_v41", "lidx_indexer_bwd", "lidx_indexer_bwd_ranges",
@@ -460,6 +479,7 @@ def lidx_indexer_bwd(q, k, w, idx, grad, compress_ratio, act="relu", grad_dtype=
 _Tensor, _bf16, _f32, _i32, _i64, _f8 = (torch.Tensor, torch.bfloat16, torch.float32, torch.int32, torch.int64,
                                           torch.float8_e4m3fn)
 _I2, _I3, _ROPE_TENSOR = struct.Struct("2q").pack, struct.Struct("3q").pack, struct.Struct("PP6qi4x").pack
+_ROPE_TURN, _NORM_TENSOR, _u8 = struct.Struct("P3qPP4if4x").pack, struct.Struct("PPP9qPPi4x").pack, torch.uint8
 
 
 def _strided(t, name, dtype, dev=None):
@@ -523,7 +543,49 @@ def lidx_rope_freqs(rot_dim, theta=10000.0, scaling=None, factor=1.0, original_l
     return out.to(device)
 
 
-def _rope(x, pos, freqs, x2, layout, rot_off, mscale, inverse, stream, out, call):
+def lidx_rope_axis_map(sections, interleaved=False, device="cuda") -> torch.Tensor:
+    """Axis of each rotated pair, uint8 [sum(sections)]: sections[a] pairs of axis a, one section after the other or, with
+    interleaved, in turns for as long as each axis has pairs left."""
+    left = [int(n) for n in sections]
+    if not left or min(left) < 0 or sum(left) < 1 or len(left) > 255:
+        raise ValueError("sections must be 1 to 255 numbers of pairs")
+    if interleaved:
+        ids = [a for i in range(max(left)) for a, n in enumerate(left) if i < n]
+    else:
+        ids = [a for a, n in enumerate(left) for _ in range(n)]
+    return torch.tensor(ids, dtype=_u8).to(device)
+
+
+def _turn(pos, freqs, layout, rot_off, mscale, axes, T0, T1, dev):
+    """The packed lidx_rope_turn of a rotation."""
+    if not isinstance(pos, _Tensor) or pos.dtype is not _i32 or not pos.is_cuda:
+        raise TypeError("pos must be an int32 CUDA tensor")
+    if pos.get_device() != dev:
+        raise ValueError(f"pos is on {pos.device}, not on cuda:{dev}")
+    pairs = _dense(freqs, "freqs", _i64, (None,), dev)[0]
+    if layout not in ROPE_LAYOUT:
+        raise ValueError(f"layout must be one of {list(ROPE_LAYOUT)}")
+    if axes is None:
+        A, axis = 1, None
+        if pos.shape != (T0, T1):
+            pos = pos.expand(T0, T1)  # repeated positions have stride 0
+        p0, p1 = pos.stride()
+        pa = 0
+    else:
+        _dense(axes, "axes", _u8, (pairs,), dev)
+        if pos.dim() < 1:
+            raise ValueError("pos must have the axes as its first dim")
+        A, axis = pos.shape[0], axes.data_ptr()
+        if not 1 <= A <= 255:
+            raise ValueError(f"pos has {A} axes: 1 to 255 are supported")
+        if pos.shape != (A, T0, T1):
+            pos = pos.view(A, *(1,) * (3 - pos.dim()), *pos.shape[1:]).expand(A, T0, T1)
+        pa, p0, p1 = pos.stride()
+    return _ROPE_TURN(pos.data_ptr(), pa, p0 if T0 > 1 else 0, p1 if T1 > 1 else 0, freqs.data_ptr(), axis or 0, A, 2 * pairs,
+                      rot_off, ROPE_LAYOUT[layout], mscale)
+
+
+def _rope(x, pos, freqs, x2, layout, rot_off, mscale, inverse, stream, out, axes, call):
     dtype = x.dtype if isinstance(x, _Tensor) else _bf16
     if dtype is not _bf16 and dtype is not _f32:
         raise TypeError(f"x must be float32 or bfloat16, got {dtype}")
@@ -533,16 +595,7 @@ def _rope(x, pos, freqs, x2, layout, rot_off, mscale, inverse, stream, out, call
         shape2, xs2, _ = _strided(x2, "x2", dtype, dev)
         if shape2[0] != T0 or shape2[1] != T1 or shape2[3] != D:
             raise ValueError("x and x2 shapes disagree")
-    if not isinstance(pos, _Tensor) or pos.dtype is not _i32 or not pos.is_cuda:
-        raise TypeError("pos must be an int32 CUDA tensor")
-    if pos.shape != (T0, T1):
-        pos = pos.expand(T0, T1)  # repeated positions have stride 0
-    if pos.get_device() != dev:
-        raise ValueError(f"pos is on {pos.device}, not on cuda:{dev}")
-    p0, p1 = pos.stride()
-    pairs = _dense(freqs, "freqs", _i64, (None,), dev)[0]
-    if layout not in ROPE_LAYOUT:
-        raise ValueError(f"layout must be one of {list(ROPE_LAYOUT)}")
+    turn = _turn(pos, freqs, layout, rot_off, mscale, axes, T0, T1, dev)
     if out is None:
         at = x.device
         y = torch.empty_like(x) if stream is None and x.is_contiguous() else _new(shape, dtype, at, stream)
@@ -562,25 +615,111 @@ def _rope(x, pos, freqs, x2, layout, rot_off, mscale, inverse, stream, out, call
             if sy != shape2:
                 raise ValueError("out has another shape than x2")
             arr += _ROPE_TENSOR(x2.data_ptr(), y2.data_ptr(), *xs2, *ys, shape2[2])
-    rc = (_lib or lib()).lidx_rope(arr, 1 if x2 is None else 2, pos.data_ptr(), _I2(p0 if T0 > 1 else 0, p1 if T1 > 1 else 0),
-                                   freqs.data_ptr(), T0, T1, D, 2 * pairs, rot_off, ROPE_LAYOUT[layout], inverse, mscale,
-                                   1 if dtype is _bf16 else 0, _raw_stream(stream, dev))
+    rc = (_lib or lib()).lidx_rope_axes(arr, 1 if x2 is None else 2, turn, T0, T1, D, inverse, 1 if dtype is _bf16 else 0,
+                                        _raw_stream(stream, dev))
     if rc:
         raise LidxError(rc, call)
     return y if x2 is None else (y, y2)
 
 
-def lidx_rope(x, pos, freqs, x2=None, layout="interleaved", rot_off=0, mscale=1.0, stream=None, out=None):
+def lidx_rope(x, pos, freqs, x2=None, layout="interleaved", rot_off=0, mscale=1.0, stream=None, out=None, axes=None):
     """Rotary positions of x [T0,T1,H,D] (fp32 or bf16, any strides of the leading dimensions) and, in
     the same launch, of x2 [T0,T1,H2,D].  pos: int32, broadcast to [T0,T1]; freqs: lidx_rope_freqs's,
     the rotated dims are [rot_off, rot_off + 2*len(freqs)).  Returns y, or (y, y2).  ``out`` may be the
-    inputs themselves (in place)."""
-    return _rope(x, pos, freqs, x2, layout, rot_off, mscale, 0, stream, out, "lidx_rope")
+    inputs themselves (in place).
+    axes (lidx_rope_axis_map's, uint8 [len(freqs)]): positions on several axes, pos int32 [A, ...] with [...] broadcast to
+    [T0,T1]; pair i turns by pos[axes[i]] (ids of A and more count as A - 1)."""
+    return _rope(x, pos, freqs, x2, layout, rot_off, mscale, 0, stream, out, axes, "lidx_rope")
 
 
-def lidx_rope_bwd(g, pos, freqs, x2=None, layout="interleaved", rot_off=0, mscale=1.0, stream=None, out=None):
+def lidx_rope_bwd(g, pos, freqs, x2=None, layout="interleaved", rot_off=0, mscale=1.0, stream=None, out=None, axes=None):
     """Gradient of lidx_rope's x (and x2) from the gradients g (and x2) of its outputs: the inverse turn."""
-    return _rope(g, pos, freqs, x2, layout, rot_off, mscale, 1, stream, out, "lidx_rope_bwd")
+    return _rope(g, pos, freqs, x2, layout, rot_off, mscale, 1, stream, out, axes, "lidx_rope_bwd")
+
+
+def _norm_side(x, w, g, y, name, dtype, w_dtype, lead, D, dev):
+    """Checks of one tensor of a norm and its weight; returns its shape and strides (x, g)."""
+    shape, xs, dev = _strided(x, "x" + name, dtype, dev)
+    if lead is not None and (shape[0], shape[1], shape[3]) != (*lead, D):
+        raise ValueError("x and x2 shapes disagree")
+    gs = (0, 0, 0)
+    if g is not None:
+        sg, gs, _ = _strided(g, "g" + name, dtype, dev)
+        if sg != shape:
+            raise ValueError(f"g{name} has another shape than x{name}")
+    if w is not None:
+        _dense(w, "weight" + name, w_dtype, (shape[3],), dev)
+    return shape, xs, gs, dev
+
+
+def _norm_rope(x, weight, pos, freqs, g, x2, weight2, g2, eps, layout, rot_off, mscale, axes, stream, out, workspace, bwd):
+    dtype = x.dtype if isinstance(x, _Tensor) else _bf16
+    if dtype is not _bf16 and dtype is not _f32:
+        raise TypeError(f"x must be float32 or bfloat16, got {dtype}")
+    w_dtype = next((w.dtype for w in (weight, weight2) if isinstance(w, _Tensor)), _f32)
+    if w_dtype is not _bf16 and w_dtype is not _f32:
+        raise TypeError(f"weight must be float32 or bfloat16, got {w_dtype}")
+    if bwd and (g is None or (x2 is None) != (g2 is None)):
+        raise TypeError("each of x and x2 needs the gradient of its output")
+    shape, xs, gs, dev = _norm_side(x, weight, g, None, "", dtype, w_dtype, None, None, None)
+    T0, T1, H, D = shape
+    turn = _turn(pos, freqs, layout, rot_off, mscale, axes, T0, T1, dev)
+    sides = [(x, weight, g, shape, xs, gs)]
+    if x2 is not None:
+        shape2, xs2, gs2, _ = _norm_side(x2, weight2, g2, None, "2", dtype, w_dtype, (T0, T1), D, dev)
+        sides.append((x2, weight2, g2, shape2, xs2, gs2))
+    at, arr, res = x.device, b"", ()
+    given = None if out is None else (out if bwd or x2 is not None else (out,))
+    for i, (xi, wi, gi, si, xsi, gsi) in enumerate(sides):
+        Hi = si[2]
+        dwi = None
+        if given is None:
+            y, ys = _new(si, dtype, at, stream), (T1 * Hi * D, Hi * D, D)
+            if bwd:
+                dwi = None if wi is None else _new((D,), _f32, at, stream)
+        else:
+            y = given[2 * i if bwd else i]
+            sy, ys, _ = _strided(y, "out", dtype, dev)
+            if sy != si:
+                raise ValueError("out has another shape than " + ("x2" if i else "x"))
+            if bwd:
+                dwi = given[2 * i + 1]
+                if dwi is not None:
+                    _dense(dwi, "out", _f32, (D,), dev)
+        arr += _NORM_TENSOR(xi.data_ptr(), 0 if gi is None else gi.data_ptr(), y.data_ptr(), *xsi, *gsi, *ys,
+                            0 if wi is None else wi.data_ptr(), 0 if dwi is None else dwi.data_ptr(), Hi)
+        res += (y, dwi) if bwd else (y,)
+    L, dt, wdt = _lib or lib(), 1 if dtype is _bf16 else 0, 1 if w_dtype is _bf16 else 0
+    if bwd:
+        if workspace is None:
+            ws_bytes = L.lidx_norm_rope_bwd_workspace_bytes(D)
+            workspace = _scratch(ws_bytes, at, stream)
+        else:
+            ws_bytes = _dense(workspace, "workspace", _u8, (None,), dev)[0]
+        rc = L.lidx_norm_rope_bwd(arr, len(sides), turn, eps, T0, T1, D, dt, wdt, workspace.data_ptr(), ws_bytes,
+                                  _raw_stream(stream, dev))
+    else:
+        rc = L.lidx_norm_rope(arr, len(sides), turn, eps, T0, T1, D, dt, wdt, _raw_stream(stream, dev))
+    if rc:
+        raise LidxError(rc, "lidx_norm_rope_bwd" if bwd else "lidx_norm_rope")
+    return res if bwd or len(res) > 1 else res[0]
+
+
+def lidx_norm_rope(x, weight, pos, freqs, x2=None, weight2=None, eps=1e-6, layout="interleaved", rot_off=0, mscale=1.0,
+                   axes=None, stream=None, out=None):
+    """Root-mean-square norm of each head of x [T0,T1,H,D] over its D dims, times weight [D] (fp32 or bf16; None: ones), and
+    its rotary positions as lidx_rope's, in one pass; in the same launch those of x2 with weight2 (queries and keys).
+    Computed in fp32 and rounded once.  Returns y, or (y, y2).  ``out`` may be the inputs themselves."""
+    return _norm_rope(x, weight, pos, freqs, None, x2, weight2, None, eps, layout, rot_off, mscale, axes, stream, out, None,
+                      False)
+
+
+def lidx_norm_rope_bwd(g, x, weight, pos, freqs, g2=None, x2=None, weight2=None, eps=1e-6, layout="interleaved", rot_off=0,
+                       mscale=1.0, axes=None, stream=None, out=None, workspace=None):
+    """Gradients of lidx_norm_rope from its inputs and the gradients g (and g2) of its outputs: (dx, dw) or (dx, dw, dx2,
+    dw2).  dw, the sum over all rows, is fp32 [D] (None where the weight is); dx may be g or x itself (``out``)."""
+    return _norm_rope(x, weight, pos, freqs, g, x2, weight2, g2, eps, layout, rot_off, mscale, axes, stream, out, workspace,
+                      True)
 
 
 def _cache(k_cache, v_cache, k_scale, v_scale, block_table, B, Hkv, D, dev):

@@ -1,0 +1,593 @@
+// norm_rope.cu -- root-mean-square norms of queries and keys for each head, with the rotary positions in the same pass,
+// forward and backward.
+//
+// Forward: with r = (mean_d x^2 + eps)^-1/2 a head's n = x r w turns as in rope.cu; y = turn(n).
+// Backward, from g = dL/dy: u = turn^T(g) (the inverse turn), t = u w, and with h = x r
+//     dx = r (t - h mean_d(t h)),    dw_d = sum over rows of u_d h_d.
+// The backward takes r from x again: reading a saved r would cost what it saves.  All of it is computed in fp32 from the
+// inputs as they are, and rounded once; weights' gradients are fp32.  dw: a thread adds its rows in order, a block its
+// threads, a second launch the blocks, all in fixed orders: two calls give the same bits.
+//
+// What bounds it: reading and writing each element once.
+#include <string.h>
+
+#include "ptx.cuh"
+#include "rope.cuh"
+
+namespace lidx {
+
+struct NormTensor {
+    const void* x;
+    const void* g;  // backward
+    void* y;        // output, or gradient of x
+    int64_t xs[3], gs[3], ys[3];
+    const void* w;  // nullable
+    float* dw;      // nullable
+    int H, blocks;  // blocks of this tensor
+    RopeDiv heads;
+};
+struct NormParams {
+    NormTensor t[2];
+    RopeTurn r;
+    int64_t T0, T1;
+    int D, w32;  // w32: weights are fp32, else bf16
+    float eps, inv_d;
+    RopeDiv tokens1, pairs;
+    float* part;  // backward: [blocks][D] sums of u h
+};
+
+constexpr int kNormThreads = 256;
+constexpr int kNormPer = 4;         // rows a thread, forward
+constexpr int kNormPerBwd = 2;
+constexpr int kNormAngles = 4096;   // of a block's tokens: 32 KB
+constexpr int kNormBlocks = 4;      // blocks an SM of the backward, at most
+
+__device__ __forceinline__ float norm_weight(const NormParams& p, const void* w, int d) {
+    if (!w) return 1.f;
+    return p.w32 ? ((const float*)w)[d] : __bfloat162float(((const __nv_bfloat16*)w)[d]);
+}
+
+// ------------------------------------------------------------------ aligned tensors
+// A row (token, head) belongs to LANES neighbouring lanes, each with two 16-byte vectors: in the half layout the two that
+// hold its pairs, so that no element crosses lanes; sums over the row are a few shuffles.
+struct NormLane {
+    int n;       // vectors of the lane: 0 .. 2
+    int d0, d1;  // their first dims
+    int c0, c1;  // their first angles, -1: not rotated
+};
+template <bool HALF, int V>
+__device__ __forceinline__ NormLane norm_lane(const RopeTurn& r, int D, int l) {
+    NormLane o{0, 0, 0, -1, -1};
+    if constexpr (HALF) {
+        const int np = r.R / 2 / V;
+        if (l < np) {
+            o = NormLane{2, r.off + l * V, r.off + l * V + r.R / 2, l * V, l * V};
+        } else {
+            const int q = 2 * (l - np), nc = (D - r.R) / V;
+            o.n = max(0, min(2, nc - q));
+            o.d0 = q * V < r.off ? q * V : q * V + r.R;
+            o.d1 = (q + 1) * V < r.off ? (q + 1) * V : (q + 1) * V + r.R;
+        }
+    } else {
+        const int nv = D / V, half = (nv + 1) / 2;
+        o.n = l >= half ? 0 : (l + half < nv ? 2 : 1);
+        o.d0 = l * V;
+        o.d1 = (l + half) * V;
+        if (o.d0 >= r.off && o.d0 < r.off + r.R) o.c0 = (o.d0 - r.off) / 2;
+        if (o.d1 >= r.off && o.d1 < r.off + r.R) o.c1 = (o.d1 - r.off) / 2;
+    }
+    return o;
+}
+static int norm_lanes(const RopeTurn& r, int D, int V) {
+    return r.half ? r.R / 2 / V + ((D - r.R) / V + 1) / 2 : (D / V + 1) / 2;
+}
+
+// The two vectors of a lane turn.  cs: angles of the row's token.
+template <bool HALF, int V>
+__device__ __forceinline__ void norm_turn(const NormLane& o, const float2* cs, float (&a)[V], float (&b)[V]) {
+    if constexpr (HALF) {
+        if (o.c0 >= 0) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float2 c = cs[o.c0 + i];
+                const float u = a[i], w = b[i];
+                a[i] = u * c.x - w * c.y;
+                b[i] = w * c.x + u * c.y;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            if (o.c0 >= 0) {
+                const float2 c = cs[o.c0 + i / 2];
+                const float u = a[i], w = a[i + 1];
+                a[i] = u * c.x - w * c.y;
+                a[i + 1] = w * c.x + u * c.y;
+            }
+            if (o.c1 >= 0) {
+                const float2 c = cs[o.c1 + i / 2];
+                const float u = b[i], w = b[i + 1];
+                b[i] = u * c.x - w * c.y;
+                b[i + 1] = w * c.x + u * c.y;
+            }
+        }
+    }
+}
+
+template <int LANES>
+__device__ __forceinline__ float norm_sum(float v) {
+#pragma unroll
+    for (int i = 1; i < LANES; i <<= 1) v += __shfl_xor_sync(0xffffffffu, v, i);
+    return v;
+}
+
+// Rows [first, first + n) of a tensor: where row e of a block is.
+struct NormRows {
+    int64_t tok0;
+    int skip, n;
+    __device__ NormRows(const NormParams& p, const NormTensor& t, int64_t first, int rows) {
+        const int64_t all = p.T0 * p.T1 * t.H;
+        tok0 = first / t.H;
+        skip = (int)(first - tok0 * t.H);
+        n = (int)min((int64_t)rows, all - first);
+    }
+    // token of the block, and place of row e with strides s
+    __device__ int token(const NormTensor& t, int e) const { return (int)rope_quot(skip + e, t.heads); }
+    __device__ int64_t at(const NormParams& p, const NormTensor& t, const int64_t (&s)[3], int e, int tok) const {
+        const uint32_t k = (uint32_t)tok0 + tok, t0 = rope_quot(k, p.tokens1), t1 = k - t0 * (uint32_t)p.T1;
+        return t0 * s[0] + t1 * s[1] + (int64_t)(skip + e - tok * t.H) * s[2];
+    }
+    // angles of the block's tokens
+    __device__ void angles(const NormParams& p, const NormTensor& t, float2* s_cs) const {
+        const int R2 = p.r.R / 2, all = (token(t, n - 1) + 1) * R2;
+        for (int i = threadIdx.x; i < all; i += kNormThreads) {
+            const int k = rope_quot(i, p.pairs);
+            const uint32_t tok = (uint32_t)tok0 + k, t0 = rope_quot(tok, p.tokens1), t1 = tok - t0 * (uint32_t)p.T1;
+            s_cs[i] = rope_cs(p.r, t0, t1, i - k * R2);
+        }
+    }
+};
+
+template <class T, bool HALF, int LANES, int PER>
+__global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_constant__ NormParams p) {
+    constexpr int V = 16 / sizeof(T), G = kNormThreads / LANES;
+    extern __shared__ __align__(16) float s_norm[];
+    float* const s_w = s_norm;                       // [D]
+    float2* const s_cs = (float2*)(s_norm + p.D);    // (D a multiple of V)
+    const int which = (int)blockIdx.x >= p.t[0].blocks;
+    const NormTensor& t = p.t[which];
+    const int64_t first = (int64_t)(blockIdx.x - (which ? p.t[0].blocks : 0)) * (G * PER);
+    const NormRows rows(p, t, first, G * PER);
+    const NormLane o = norm_lane<HALF, V>(p.r, p.D, threadIdx.x % LANES);
+    const int grp = threadIdx.x / LANES;
+    uint4 a[PER], b[PER];
+    int tok[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int e = grp + k * G;
+        a[k] = b[k] = make_uint4(0, 0, 0, 0);
+        tok[k] = 0;
+        if (e < rows.n) {
+            tok[k] = rows.token(t, e);
+            const T* x = (const T*)t.x + rows.at(p, t, t.xs, e, tok[k]);
+            if (o.n > 0) a[k] = *reinterpret_cast<const uint4*>(x + o.d0);
+            if (o.n > 1) b[k] = *reinterpret_cast<const uint4*>(x + o.d1);
+        }
+    }
+    for (int d = threadIdx.x; d < p.D; d += kNormThreads) s_w[d] = norm_weight(p, t.w, d);
+    rows.angles(p, t, s_cs);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int e = grp + k * G;
+        float f[V], g[V];
+        rope_unpack(a[k], f);
+        rope_unpack(b[k], g);
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) ss += f[i] * f[i] + g[i] * g[i];
+        const float r = __frsqrt_rn(norm_sum<LANES>(ss) * p.inv_d + p.eps);
+        if (e >= rows.n || o.n == 0) continue;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            f[i] *= r * s_w[o.d0 + i];
+            if (o.n > 1) g[i] *= r * s_w[o.d1 + i];
+        }
+        norm_turn<HALF, V>(o, s_cs + tok[k] * (p.r.R / 2), f, g);
+        T* y = (T*)t.y + rows.at(p, t, t.ys, e, tok[k]);
+        *reinterpret_cast<uint4*>(y + o.d0) = rope_pack(f);
+        if (o.n > 1) *reinterpret_cast<uint4*>(y + o.d1) = rope_pack(g);
+    }
+}
+
+template <class T, bool HALF, int LANES>
+__global__ void __launch_bounds__(kNormThreads) norm_rope_bwd_kernel(const __grid_constant__ NormParams p) {
+    constexpr int V = 16 / sizeof(T), G = kNormThreads / LANES, PER = kNormPerBwd;
+    extern __shared__ __align__(16) float s_norm[];
+    float* const s_w = s_norm;
+    float2* const s_cs = (float2*)(s_norm + p.D);
+    const int which = (int)blockIdx.x >= p.t[0].blocks;
+    const NormTensor& t = p.t[which];
+    const NormLane o = norm_lane<HALF, V>(p.r, p.D, threadIdx.x % LANES);
+    const int grp = threadIdx.x / LANES;
+    grid_dependency_launch();
+    for (int d = threadIdx.x; d < p.D; d += kNormThreads) s_w[d] = norm_weight(p, t.w, d);
+    float wa[V], wb[V];  // sums of u h
+#pragma unroll
+    for (int i = 0; i < V; ++i) wa[i] = wb[i] = 0.f;
+    const int64_t all = p.T0 * p.T1 * t.H;
+    for (int64_t first = (int64_t)(blockIdx.x - (which ? p.t[0].blocks : 0)) * (G * PER); first < all;
+         first += (int64_t)t.blocks * (G * PER)) {
+        const NormRows rows(p, t, first, G * PER);
+        uint4 xa[PER], xb[PER], ga[PER], gb[PER];
+        int tok[PER];
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int e = grp + k * G;
+            xa[k] = xb[k] = ga[k] = gb[k] = make_uint4(0, 0, 0, 0);
+            tok[k] = 0;
+            if (e < rows.n) {
+                tok[k] = rows.token(t, e);
+                const T* x = (const T*)t.x + rows.at(p, t, t.xs, e, tok[k]);
+                const T* g = (const T*)t.g + rows.at(p, t, t.gs, e, tok[k]);
+                if (o.n > 0) {
+                    xa[k] = *reinterpret_cast<const uint4*>(x + o.d0);
+                    ga[k] = *reinterpret_cast<const uint4*>(g + o.d0);
+                }
+                if (o.n > 1) {
+                    xb[k] = *reinterpret_cast<const uint4*>(x + o.d1);
+                    gb[k] = *reinterpret_cast<const uint4*>(g + o.d1);
+                }
+            }
+        }
+        __syncthreads();  // the angles before are read
+        rows.angles(p, t, s_cs);
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int e = grp + k * G;
+            float x0[V], x1[V], u0[V], u1[V];
+            rope_unpack(xa[k], x0);
+            rope_unpack(xb[k], x1);
+            rope_unpack(ga[k], u0);
+            rope_unpack(gb[k], u1);
+            if (e < rows.n) norm_turn<HALF, V>(o, s_cs + tok[k] * (p.r.R / 2), u0, u1);
+            float s2 = 0.f, s3 = 0.f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                s2 += x0[i] * x0[i] + x1[i] * x1[i];
+                if (o.n > 0) s3 += u0[i] * s_w[o.d0 + i] * x0[i];
+                if (o.n > 1) s3 += u1[i] * s_w[o.d1 + i] * x1[i];
+            }
+            const float r = __frsqrt_rn(norm_sum<LANES>(s2) * p.inv_d + p.eps);
+            const float c = r * r * (norm_sum<LANES>(s3) * p.inv_d);
+            if (e >= rows.n || o.n == 0) continue;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                wa[i] += u0[i] * (x0[i] * r);
+                u0[i] = r * (u0[i] * s_w[o.d0 + i] - x0[i] * c);
+                if (o.n > 1) {
+                    wb[i] += u1[i] * (x1[i] * r);
+                    u1[i] = r * (u1[i] * s_w[o.d1 + i] - x1[i] * c);
+                }
+            }
+            T* y = (T*)t.y + rows.at(p, t, t.ys, e, tok[k]);
+            *reinterpret_cast<uint4*>(y + o.d0) = rope_pack(u0);
+            if (o.n > 1) *reinterpret_cast<uint4*>(y + o.d1) = rope_pack(u1);
+        }
+    }
+    // the block's sums: one row of smem a group, added in order
+    __syncthreads();
+    float* const s_sum = (float*)s_cs;  // [G][D]
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        if (o.n > 0) s_sum[grp * p.D + o.d0 + i] = wa[i];
+        if (o.n > 1) s_sum[grp * p.D + o.d1 + i] = wb[i];
+    }
+    __syncthreads();
+    for (int d = threadIdx.x; d < p.D; d += kNormThreads) {
+        float s = 0.f;
+        for (int i = 0; i < G; ++i) s += s_sum[i * p.D + d];
+        p.part[(int64_t)blockIdx.x * p.D + d] = s;
+    }
+}
+
+// ------------------------------------------------------------------ any alignment, any rotated part
+// A warp a row; a lane has pairs (or two copied dims) and recomputes their angles.
+__device__ __forceinline__ void norm_unit(const RopeTurn& r, int u, int& ia, int& ib) {
+    if (u < r.R / 2) {
+        ia = r.half ? r.off + u : r.off + 2 * u;
+        ib = r.half ? ia + r.R / 2 : ia + 1;
+    } else {  // the dims that are not rotated, those before the rotated part first
+        const int d = 2 * (u - r.R / 2);
+        ia = d < r.off ? d : d + r.R;
+        ib = d + 1 < r.off ? d + 1 : d + 1 + r.R;
+    }
+}
+template <class T, bool BWD>
+__global__ void __launch_bounds__(kNormThreads) norm_rope_any_kernel(const __grid_constant__ NormParams p) {
+    extern __shared__ __align__(16) float s_norm[];  // backward: [warps][D] sums of u h
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, units = p.D / 2;
+    const int which = (int)blockIdx.x >= p.t[0].blocks;
+    const NormTensor& t = p.t[which];
+    float* const sum = s_norm + warp * p.D;
+    if constexpr (BWD) {
+        grid_dependency_launch();
+        for (int d = lane; d < p.D; d += 32) sum[d] = 0.f;
+        __syncwarp();
+    }
+    const int64_t all = p.T0 * p.T1 * t.H;
+    for (int64_t row = (int64_t)(blockIdx.x - (which ? p.t[0].blocks : 0)) * (kNormThreads / 32) + warp; row < all;
+         row += (int64_t)t.blocks * (kNormThreads / 32)) {
+        const int64_t tok = row / t.H, t0 = tok / p.T1, t1 = tok - t0 * p.T1;
+        const int h = (int)(row - tok * t.H);
+        const T* x = (const T*)t.x + t0 * t.xs[0] + t1 * t.xs[1] + h * t.xs[2];
+        const T* g = BWD ? (const T*)t.g + t0 * t.gs[0] + t1 * t.gs[1] + h * t.gs[2] : nullptr;
+        T* y = (T*)t.y + t0 * t.ys[0] + t1 * t.ys[1] + h * t.ys[2];
+        // gradients of the pair before the turn
+        auto grad = [&](int u, int ia, int ib, float& a, float& b) {
+            a = rope_get(g + ia), b = rope_get(g + ib);
+            if (u < p.r.R / 2) {
+                const float2 c = rope_cs(p.r, t0, t1, u);
+                const float s = a;
+                a = s * c.x - b * c.y;
+                b = b * c.x + s * c.y;
+            }
+        };
+        float s2 = 0.f, s3 = 0.f;
+        for (int u = lane; u < units; u += 32) {
+            int ia, ib;
+            norm_unit(p.r, u, ia, ib);
+            const float a = rope_get(x + ia), b = rope_get(x + ib);
+            s2 += a * a + b * b;
+            if constexpr (BWD) {
+                float ga, gb;
+                grad(u, ia, ib, ga, gb);
+                s3 += ga * norm_weight(p, t.w, ia) * a + gb * norm_weight(p, t.w, ib) * b;
+            }
+        }
+        const float r = __frsqrt_rn(norm_sum<32>(s2) * p.inv_d + p.eps);
+        const float c = BWD ? r * r * (norm_sum<32>(s3) * p.inv_d) : 0.f;
+        for (int u = lane; u < units; u += 32) {
+            int ia, ib;
+            norm_unit(p.r, u, ia, ib);
+            const float a = rope_get(x + ia), b = rope_get(x + ib);
+            const float wa = norm_weight(p, t.w, ia), wb = norm_weight(p, t.w, ib);
+            if constexpr (BWD) {
+                float ga, gb;
+                grad(u, ia, ib, ga, gb);
+                sum[ia] += ga * (a * r);
+                sum[ib] += gb * (b * r);
+                rope_put(y + ia, r * (ga * wa - a * c));
+                rope_put(y + ib, r * (gb * wb - b * c));
+            } else {
+                const float na = a * (r * wa), nb = b * (r * wb);
+                if (u < p.r.R / 2) {
+                    const float2 cs = rope_cs(p.r, t0, t1, u);
+                    rope_put(y + ia, na * cs.x - nb * cs.y);
+                    rope_put(y + ib, nb * cs.x + na * cs.y);
+                } else {
+                    rope_put(y + ia, na);
+                    rope_put(y + ib, nb);
+                }
+            }
+        }
+    }
+    if constexpr (BWD) {
+        __syncthreads();
+        for (int d = threadIdx.x; d < p.D; d += kNormThreads) {
+            float s = 0.f;
+            for (int i = 0; i < kNormThreads / 32; ++i) s += s_norm[i * p.D + d];
+            p.part[(int64_t)blockIdx.x * p.D + d] = s;
+        }
+    }
+}
+
+// dw of a tensor: block x has 32 dims, block y the tensor; 32 runs of blocks, then those, in order.
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const __grid_constant__ NormParams p) {
+    __shared__ float s[32][33];
+    const NormTensor& t = p.t[blockIdx.y];
+    grid_dependency_wait();
+    if (!t.dw) return;
+    const int c = threadIdx.x & 31, run = threadIdx.x >> 5, d = blockIdx.x * 32 + c;
+    const float* part = p.part + (blockIdx.y ? (int64_t)p.t[0].blocks * p.D : 0);
+    float v = 0.f;
+    if (d < p.D)
+        for (int b = run; b < t.blocks; b += 32) v += part[(int64_t)b * p.D + d];
+    s[run][c] = v;
+    __syncthreads();
+    if (run == 0 && d < p.D) {
+        v = 0.f;
+        for (int i = 0; i < 32; ++i) v += s[i][c];
+        t.dw[d] = v;
+    }
+}
+
+// ------------------------------------------------------------------- host
+
+static bool norm_vectors(const NormParams& p, int nt, int V, int es, bool bwd) {
+    const RopeTurn& r = p.r;
+    if (p.D % V || r.off % V || (r.half ? (r.R / 2) % V : r.R % V) || norm_lanes(r, p.D, V) > 32) return false;
+    uintptr_t bits = 0;
+    for (int i = 0; i < nt; ++i) {
+        const NormTensor& t = p.t[i];
+        bits |= (uintptr_t)t.x | (uintptr_t)t.y | (bwd ? (uintptr_t)t.g : 0);
+        for (int k = 0; k < 3; ++k)
+            bits |= (uintptr_t)(t.xs[k] * es) | (uintptr_t)(t.ys[k] * es) | (bwd ? (uintptr_t)(t.gs[k] * es) : 0);
+    }
+    return (bits & 15) == 0;
+}
+
+// Blocks of the backward, shared out by the tensors' rows.
+static void norm_share(NormParams& p, int nt, int rows) {
+    int64_t chunks[2] = {0, 0}, all = 0;
+    for (int i = 0; i < nt; ++i) all += chunks[i] = (p.T0 * p.T1 * p.t[i].H + rows - 1) / rows;
+    const int64_t most = (int64_t)kNormBlocks * current_sms();
+    for (int i = 0; i < nt; ++i) {
+        int64_t n = all <= most ? chunks[i] : chunks[i] * (most - 1) / all;
+        p.t[i].blocks = (int)(n < 1 ? 1 : n);
+    }
+}
+
+template <class T, bool HALF, int LANES>
+static cudaError_t norm_launch_lanes(NormParams& p, int nt, bool bwd, cudaStream_t st) {
+    constexpr int G = kNormThreads / LANES;
+    auto smem = [&](int rows) {  // weights, angles of the tokens of `rows` rows (or the sums of the groups)
+        int64_t angles = 0;
+        for (int i = 0; i < nt; ++i) {
+            const int64_t n = (int64_t)((rows - 1) / p.t[i].H + 2) * (p.r.R / 2);
+            angles = n > angles ? n : angles;
+        }
+        return angles;
+    };
+    if (bwd) {
+        norm_share(p, nt, G * kNormPerBwd);
+        const int64_t a = smem(G * kNormPerBwd) * 8, s = (int64_t)G * p.D * 4;
+        norm_rope_bwd_kernel<T, HALF, LANES>
+            <<<p.t[0].blocks + p.t[1].blocks, kNormThreads, (int)((a > s ? a : s) + p.D * 4), st>>>(p);
+        return cudaGetLastError();
+    }
+    constexpr int big = G * kNormPer;
+    int64_t rows = 0, n[2] = {0, 0};
+    for (int i = 0; i < nt; ++i) rows += p.T0 * p.T1 * p.t[i].H;
+    const int per = rows / big >= 2 * current_sms() && smem(big) <= kNormAngles ? kNormPer : 1;
+    for (int i = 0; i < nt; ++i) {
+        n[i] = (p.T0 * p.T1 * p.t[i].H + G * per - 1) / (G * per);
+        p.t[i].blocks = (int)n[i];
+    }
+    if (n[0] + n[1] > INT_MAX) return cudaErrorInvalidValue;
+    const int bytes = (int)smem(G * per) * 8 + p.D * 4;
+    if (per == kNormPer)
+        norm_rope_kernel<T, HALF, LANES, kNormPer><<<(unsigned)(n[0] + n[1]), kNormThreads, bytes, st>>>(p);
+    else
+        norm_rope_kernel<T, HALF, LANES, 1><<<(unsigned)(n[0] + n[1]), kNormThreads, bytes, st>>>(p);
+    return cudaGetLastError();
+}
+
+template <class T, bool HALF>
+static cudaError_t norm_launch_vec(NormParams& p, int nt, bool bwd, cudaStream_t st) {
+    const int lanes = norm_lanes(p.r, p.D, 16 / sizeof(T));
+    if (lanes <= 4) return norm_launch_lanes<T, HALF, 4>(p, nt, bwd, st);
+    if (lanes <= 8) return norm_launch_lanes<T, HALF, 8>(p, nt, bwd, st);
+    if (lanes <= 16) return norm_launch_lanes<T, HALF, 16>(p, nt, bwd, st);
+    return norm_launch_lanes<T, HALF, 32>(p, nt, bwd, st);
+}
+
+template <class T>
+static cudaError_t norm_launch(NormParams& p, int nt, bool bwd, cudaStream_t st) {
+    if (norm_vectors(p, nt, 16 / sizeof(T), sizeof(T), bwd))
+        return p.r.half ? norm_launch_vec<T, true>(p, nt, bwd, st) : norm_launch_vec<T, false>(p, nt, bwd, st);
+    constexpr int rows = kNormThreads / 32;
+    if (bwd) {
+        norm_share(p, nt, rows);
+        norm_rope_any_kernel<T, true>
+            <<<p.t[0].blocks + p.t[1].blocks, kNormThreads, rows * p.D * 4, st>>>(p);
+        return cudaGetLastError();
+    }
+    const int64_t cap = (int64_t)current_sms() * 32;
+    for (int i = 0; i < nt; ++i) {
+        const int64_t n = (p.T0 * p.T1 * p.t[i].H + rows - 1) / rows;
+        p.t[i].blocks = (int)(n < cap ? n : cap);
+    }
+    norm_rope_any_kernel<T, false><<<p.t[0].blocks + p.t[1].blocks, kNormThreads, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+static size_t norm_ws_bytes(int nt, int D, int sms) { return (size_t)(kNormBlocks * sms + nt) * D * sizeof(float); }
+
+// Checks of both directions; fills p.
+static int norm_params(const lidx_norm_tensor* t, int nt, const lidx_rope_turn* r, float eps, int64_t T0, int64_t T1, int D,
+                       int dtype, int w_dtype, bool bwd, NormParams& p) {
+    if (!t) return LIDX_ERR_NULL;
+    memset(&p, 0, sizeof p);
+    int rc = rope_turn(r, D, bwd, p.r);
+    if (rc) return rc;
+    if (nt < 1 || nt > 2 || (dtype != 0 && dtype != 1) || (w_dtype != 0 && w_dtype != 1)) return LIDX_ERR_SHAPE;
+    for (int i = 0; i < nt; ++i)
+        if (!t[i].x || !t[i].y || (bwd && !t[i].g)) return LIDX_ERR_NULL;
+    if (!(eps >= 0.f) || !isfinite(eps)) return LIDX_ERR_SHAPE;
+    if (T0 < 1 || T1 < 1 || T0 > (1 << 30) || T1 > (1 << 30) || T0 * T1 > INT_MAX) return LIDX_ERR_SHAPE;
+    const uintptr_t es = dtype == 0 ? 4 : 2, ws = w_dtype == 0 ? 4 : 2;
+    for (int i = 0; i < nt; ++i) {
+        NormTensor& o = p.t[i];
+        if (t[i].H < 1 || t[i].H > (1 << 15)) return LIDX_ERR_SHAPE;
+        if (((uintptr_t)t[i].x | (uintptr_t)t[i].y | (bwd ? (uintptr_t)t[i].g : 0)) % es || (uintptr_t)t[i].w % ws ||
+            (bwd && (uintptr_t)t[i].dw % 4))
+            return LIDX_ERR_ALIGN;
+        o.x = t[i].x;
+        o.g = t[i].g;
+        o.y = t[i].y;
+        for (int k = 0; k < 3; ++k) {
+            o.xs[k] = t[i].xs[k];
+            o.gs[k] = t[i].gs[k];
+            o.ys[k] = t[i].ys[k];
+        }
+        o.w = t[i].w;
+        o.dw = bwd ? t[i].dw : nullptr;
+        o.H = t[i].H;
+        o.heads = rope_div(o.H);
+    }
+    rc = rope_turn_aligned(*r);
+    if (rc) return rc;
+    p.T0 = T0;
+    p.T1 = T1;
+    p.D = D;
+    p.w32 = w_dtype == 0;
+    p.eps = eps;
+    p.inv_d = 1.f / D;
+    p.tokens1 = rope_div((uint32_t)T1);
+    p.pairs = rope_div(p.r.R / 2);
+    return sm103_sms() <= 0 ? LIDX_ERR_NO_DEVICE : LIDX_OK;
+}
+
+}  // namespace lidx
+
+using namespace lidx;
+
+extern "C" {
+
+int lidx_norm_rope(const lidx_norm_tensor* t, int nt, const lidx_rope_turn* r, float eps, int64_t T0, int64_t T1, int D,
+                   int dtype, int w_dtype, void* stream) {
+    NormParams p;
+    const int rc = norm_params(t, nt, r, eps, T0, T1, D, dtype, w_dtype, false, p);
+    if (rc) return rc;
+    cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = dtype == 0 ? norm_launch<float>(p, nt, false, st) : norm_launch<__nv_bfloat16>(p, nt, false, st);
+    return e == cudaSuccess ? LIDX_OK : LIDX_ERR_CUDA;
+}
+
+size_t lidx_norm_rope_bwd_workspace_bytes(int D) {
+    if (D < 2 || D > 1024) return 0;
+    const int sms = sm103_sms();
+    return norm_ws_bytes(2, D, sms > 0 ? sms : 256);  // no device: an upper bound
+}
+
+int lidx_norm_rope_bwd(const lidx_norm_tensor* t, int nt, const lidx_rope_turn* r, float eps, int64_t T0, int64_t T1, int D,
+                       int dtype, int w_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    NormParams p;
+    const int rc = norm_params(t, nt, r, eps, T0, T1, D, dtype, w_dtype, true, p);
+    if (rc) return rc;
+    if (!workspace || workspace_bytes < norm_ws_bytes(2, D, current_sms()) || ((uintptr_t)workspace & 255u))
+        return LIDX_ERR_WORKSPACE;
+    p.part = (float*)workspace;
+    cudaStream_t st = (cudaStream_t)stream;
+    cudaError_t e = dtype == 0 ? norm_launch<float>(p, nt, true, st) : norm_launch<__nv_bfloat16>(p, nt, true, st);
+    if (e == cudaSuccess && (p.t[0].dw || p.t[1].dw)) {
+        cudaLaunchConfig_t cfg;
+        memset(&cfg, 0, sizeof cfg);
+        cfg.gridDim = dim3((D + 31) / 32, nt);
+        cfg.blockDim = dim3(1024);
+        cfg.stream = st;
+        // set up while the main kernel runs; it waits for its end itself
+        cudaLaunchAttribute at;
+        memset(&at, 0, sizeof at);
+        at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, norm_dw_kernel, p);
+    }
+    return e == cudaSuccess ? LIDX_OK : LIDX_ERR_CUDA;
+}
+
+}  // extern "C"

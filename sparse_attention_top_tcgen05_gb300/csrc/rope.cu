@@ -3,23 +3,13 @@
 // Pair (a, b) of a head turns by the angle of its position:
 //     (a, b) -> (a c - b s, b c + a s),   c = m cos(2 pi t), s = m sin(2 pi t),
 // with t the position times the pair's frequency in turns.  The backward is the same turn with -s.
-//
-// Frequencies are turns per position in 0.64 fixed point, so pos * freq mod 2^64 is the fraction of
-// a turn exactly, whatever the position: a float angle would lose log2(pos) of its 24 bits.  The upper
-// 32 bits of the product, read as signed, are the angle from half a turn back to half a turn.
+// With several axes (time, height, width) a token has a position on each, and a pair turns by its axis's: only the lookup of
+// the angle changes.
 //
 // What bounds it: reading and writing each element once.  2 x 8192 tokens of 65 bf16 heads of 128: 89 us, 6.1 TB/s (with
 // the divisions by sizes as divisions, a third of the instructions, 105 us); 4095 tokens of 40 fp32 heads: 27 us, 6.2
 // TB/s.  16 tokens take 2.2 us, a launch.
-#include <cuda_bf16.h>
-#include <cuda_runtime.h>
-#include <math.h>
-#include <stdint.h>
-
-#include <climits>
-
-#include "kernels.h"
-#include "lidx.h"
+#include "rope.cuh"
 
 namespace lidx {
 
@@ -29,49 +19,14 @@ struct RopeTensor {
     int64_t xs[3], ys[3];
     int H;
 };
-// n / d for n < 2^31: (hi(n * mul) + n) >> shift with shift = ceil(log2 d), mul = floor(2^32 (2^shift - d) / d) + 1
-// (division by an invariant integer through multiplication, Granlund and Montgomery 1994).
-struct RopeDiv {
-    uint32_t d, mul, shift;
-};
-static RopeDiv rope_div(uint32_t d) {
-    RopeDiv r;
-    r.d = d;
-    r.shift = 0;
-    while ((1ull << r.shift) < d) ++r.shift;
-    r.mul = (uint32_t)(((1ull << 32) * ((1ull << r.shift) - d)) / d + 1);
-    return r;
-}
-__device__ __forceinline__ uint32_t rope_quot(uint32_t n, const RopeDiv& v) {
-    return (__umulhi(n, v.mul) + n) >> v.shift;
-}
-
 struct RopeParams {
     RopeTensor t[2];
-    const int32_t* pos;
-    int64_t ps[2];
-    const uint64_t* freqs;
+    RopeTurn r;
     int64_t T0, T1;
     int heads;  // of both tensors
-    int D, R, off, half;
-    float mscale, sign;
+    int D;
     RopeDiv row, items, tokens1, pairs;  // items of a token and of a head, T1, R / 2 (vector kernel)
 };
-
-// Scaled cosine and sine of position pos of a pair.
-__device__ __forceinline__ float2 rope_cs(int pos, uint64_t freq, float mscale, float sign) {
-    const uint64_t t = (uint64_t)(int64_t)pos * freq;
-    // half turns in [-1, 1): 32 bits of the fraction, rounded once
-    const float h = (float)(int32_t)(t >> 32) * 0x1p-31f;
-    float s, c;
-    sincospif(h, &s, &c);
-    return make_float2(c * mscale, s * mscale * sign);
-}
-
-__device__ __forceinline__ float rope_get(const float* p) { return *p; }
-__device__ __forceinline__ float rope_get(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void rope_put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void rope_put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
 // Any alignment, any rotated part: one thread per pair or copied pair of elements, which recomputes its angle (the prompt
 // above: 428 us, bound by instructions).
@@ -90,17 +45,17 @@ __global__ void rope_any_kernel(const RopeParams p) {
         const int h = which ? hh - p.t[0].H : hh;
         const T* x = (const T*)t.x + t0 * t.xs[0] + t1 * t.xs[1] + h * t.xs[2];
         T* y = (T*)t.y + t0 * t.ys[0] + t1 * t.ys[1] + h * t.ys[2];
-        if (u < p.R / 2) {
-            const int ia = p.half ? p.off + u : p.off + 2 * u;
-            const int ib = p.half ? ia + p.R / 2 : ia + 1;
-            const float2 cs = rope_cs(p.pos[t0 * p.ps[0] + t1 * p.ps[1]], p.freqs[u], p.mscale, p.sign);
+        if (u < p.r.R / 2) {
+            const int ia = p.r.half ? p.r.off + u : p.r.off + 2 * u;
+            const int ib = p.r.half ? ia + p.r.R / 2 : ia + 1;
+            const float2 cs = rope_cs(p.r, t0, t1, u);
             const float a = rope_get(x + ia), b = rope_get(x + ib);
             rope_put(y + ia, a * cs.x - b * cs.y);
             rope_put(y + ib, b * cs.x + a * cs.y);
         } else {
-            int d = 2 * (u - p.R / 2);  // the copied dims, those before the rotated part first
+            int d = 2 * (u - p.r.R / 2);  // the copied dims, those before the rotated part first
             for (int k = 0; k < 2; ++k, ++d) {
-                const int at = d < p.off ? d : d + p.R;
+                const int at = d < p.r.off ? d : d + p.r.R;
                 y[at] = x[at];
             }
         }
@@ -114,37 +69,13 @@ constexpr int kRopeThreads = 256;
 constexpr int kRopePer = 4;
 constexpr int kRopeAngles = 4096;  // of a block's tokens: 32 KB
 
-__device__ __forceinline__ void rope_unpack(const uint4& v, float (&f)[4]) {
-    f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
-}
-__device__ __forceinline__ void rope_unpack(const uint4& v, float (&f)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ uint4 rope_pack(const float (&f)[4]) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-}
-__device__ __forceinline__ uint4 rope_pack(const float (&f)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 template <class T, bool HALF, int PER>
 __global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(const __grid_constant__ RopeParams p) {
     constexpr int V = 16 / sizeof(T);
     extern __shared__ float2 s_cs[];
-    const int R2 = p.R / 2;
-    const int rot = HALF ? R2 / V : p.R / V;      // rotated items of a head
-    const int items = rot + (p.D - p.R) / V;      // then its copied vectors
+    const int R2 = p.r.R / 2;
+    const int rot = HALF ? R2 / V : p.r.R / V;      // rotated items of a head
+    const int items = rot + (p.D - p.r.R) / V;      // then its copied vectors
     const int row = items * p.heads;              // items of a token
     const int64_t all = p.T0 * p.T1 * (int64_t)row;
     const int64_t first = (int64_t)blockIdx.x * (PER * kRopeThreads);
@@ -164,11 +95,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(const __grid_con
         const uint32_t tok = tok0 + t, t0 = rope_quot(tok, p.tokens1), t1 = tok - t0 * (uint32_t)p.T1;
         int d;
         if (it < rot) {
-            d = p.off + it * V;
+            d = p.r.off + it * V;
             cs[k] = t * R2 + (HALF ? it * V : it * (V / 2));
         } else {
             d = (it - rot) * V;
-            if (d >= p.off) d += p.R;
+            if (d >= p.r.off) d += p.r.R;
             cs[k] = -1;
         }
         const RopeTensor& x = p.t[which];
@@ -181,7 +112,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(const __grid_con
     for (int i = threadIdx.x; i < angles; i += kRopeThreads) {
         const int t = rope_quot(i, p.pairs);
         const uint32_t tok = tok0 + t, t0 = rope_quot(tok, p.tokens1), t1 = tok - t0 * (uint32_t)p.T1;
-        s_cs[i] = rope_cs(p.pos[t0 * p.ps[0] + t1 * p.ps[1]], p.freqs[i - t * R2], p.mscale, p.sign);
+        s_cs[i] = rope_cs(p.r, t0, t1, i - t * R2);
     }
     __syncthreads();
 #pragma unroll
@@ -216,16 +147,16 @@ __global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(const __grid_con
 }
 
 // Angles of the tokens that `n` items can touch.
-static int64_t rope_angles(const RopeParams& p, int row, int n) { return (int64_t)((n - 1) / row + 2) * (p.R / 2); }
+static int64_t rope_angles(const RopeParams& p, int row, int n) { return (int64_t)((n - 1) / row + 2) * (p.r.R / 2); }
 
 template <class T, bool HALF>
 static cudaError_t rope_vec_launch(RopeParams p, cudaStream_t st) {
     constexpr int V = 16 / sizeof(T);
-    const int items = (HALF ? p.R / 2 / V : p.R / V) + (p.D - p.R) / V, row = items * p.heads;
+    const int items = (HALF ? p.r.R / 2 / V : p.r.R / V) + (p.D - p.r.R) / V, row = items * p.heads;
     p.row = rope_div(row);
     p.items = rope_div(items);
     p.tokens1 = rope_div((uint32_t)p.T1);
-    p.pairs = rope_div(p.R / 2);
+    p.pairs = rope_div(p.r.R / 2);
     const int64_t all = p.T0 * p.T1 * row;
     // Four items a thread share a block's angles and overlap their loads (2 x 8192 tokens: 89 us, with one item 129 us),
     // unless that leaves SMs without a block (16 tokens: 2.2 us with one) or there are too many angles (a single short head).
@@ -243,7 +174,7 @@ static cudaError_t rope_vec_launch(RopeParams p, cudaStream_t st) {
 
 // Every vector of every head starts on 16 bytes and lies in or outside the rotated part as a whole.
 static bool rope_vectors(const RopeParams& p, int V, int es) {
-    if (p.D % V || p.off % V || (p.half ? (p.R / 2) % V : p.R % V)) return false;
+    if (p.D % V || p.r.off % V || (p.r.half ? (p.r.R / 2) % V : p.r.R % V)) return false;
     uintptr_t bits = 0;
     for (const RopeTensor& t : p.t) {
         bits |= (uintptr_t)t.x | (uintptr_t)t.y;
@@ -252,10 +183,34 @@ static bool rope_vectors(const RopeParams& p, int V, int es) {
     return (bits & 15) == 0;
 }
 
+// Rules of a rotation (see lidx.h), and its device form.
+int rope_turn(const lidx_rope_turn* r, int D, int inverse, RopeTurn& out, bool own_pos) {
+    if (!r || !r->freqs || (!r->pos && !own_pos)) return LIDX_ERR_NULL;
+    if (D < 2 || D > 1024 || D % 2 || r->rot_dim < 2 || r->rot_dim % 2 || r->rot_off < 0 ||
+        r->rot_off + (int64_t)r->rot_dim > D)
+        return LIDX_ERR_SHAPE;
+    if ((r->layout != 0 && r->layout != 1) || (inverse != 0 && inverse != 1) || !isfinite(r->mscale)) return LIDX_ERR_SHAPE;
+    if (r->axes < 1 || r->axes > 255 || (r->axes > 1 && !r->axis)) return LIDX_ERR_SHAPE;
+    out.pos = r->pos;
+    for (int i = 0; i < 3; ++i) out.ps[i] = r->ps[i];
+    out.freqs = r->freqs;
+    out.axis = r->axes > 1 ? r->axis : nullptr;
+    out.axes = r->axes;
+    out.R = r->rot_dim;
+    out.off = r->rot_off;
+    out.half = r->layout == LIDX_ROPE_HALF;
+    out.mscale = r->mscale;
+    out.sign = inverse ? -1.f : 1.f;
+    return LIDX_OK;
+}
+int rope_turn_aligned(const lidx_rope_turn& r) {
+    return (uintptr_t)r.pos % 4 || (uintptr_t)r.freqs % 8 ? LIDX_ERR_ALIGN : LIDX_OK;
+}
+
 template <class T>
 static cudaError_t rope_launch(const RopeParams& p, cudaStream_t st) {
     if (rope_vectors(p, 16 / sizeof(T), sizeof(T)))
-        return p.half ? rope_vec_launch<T, true>(p, st) : rope_vec_launch<T, false>(p, st);
+        return p.r.half ? rope_vec_launch<T, true>(p, st) : rope_vec_launch<T, false>(p, st);
     const int64_t n = p.T0 * p.T1 * p.heads * (int64_t)(p.D / 2);
     int64_t blocks = (n + 255) / 256;
     const int64_t cap = (int64_t)current_sms() * 32;
@@ -297,21 +252,17 @@ int lidx_rope_freqs(int rot_dim, double theta, int scaling, double factor, doubl
     return LIDX_OK;
 }
 
-int lidx_rope(const lidx_rope_tensor* t, int nt, const int32_t* pos, const int64_t* ps,
-              const uint64_t* freqs, int64_t T0, int64_t T1, int D, int rot_dim, int rot_off,
-              int layout, int inverse, float mscale, int dtype, void* stream) {
-    if (!t || !pos || !ps || !freqs) return LIDX_ERR_NULL;
-    if (nt < 1 || nt > 2) return LIDX_ERR_SHAPE;
+int lidx_rope_axes(const lidx_rope_tensor* t, int nt, const lidx_rope_turn* r, int64_t T0, int64_t T1, int D, int inverse,
+                   int dtype, void* stream) {
+    if (!t) return LIDX_ERR_NULL;
+    RopeParams p;
+    int rc = rope_turn(r, D, inverse, p.r);
+    if (rc) return rc;
+    if (nt < 1 || nt > 2 || (dtype != 0 && dtype != 1)) return LIDX_ERR_SHAPE;
     for (int i = 0; i < nt; ++i)
         if (!t[i].x || !t[i].y) return LIDX_ERR_NULL;
     if (T0 < 1 || T1 < 1 || T0 > (1 << 30) || T1 > (1 << 30) || T0 * T1 > INT_MAX) return LIDX_ERR_SHAPE;
-    if (D < 2 || D > 1024 || D % 2 || rot_dim < 2 || rot_dim % 2 || rot_off < 0 || rot_off + (int64_t)rot_dim > D)
-        return LIDX_ERR_SHAPE;
-    if ((layout != 0 && layout != 1) || (inverse != 0 && inverse != 1) || (dtype != 0 && dtype != 1) ||
-        !isfinite(mscale))
-        return LIDX_ERR_SHAPE;
     const uintptr_t es = dtype == 0 ? 4 : 2;
-    RopeParams p;
     p.heads = 0;
     for (int i = 0; i < 2; ++i) {
         const lidx_rope_tensor& s = t[i < nt ? i : 0];
@@ -326,23 +277,23 @@ int lidx_rope(const lidx_rope_tensor* t, int nt, const int32_t* pos, const int64
         p.t[i].H = s.H;
         if (i < nt) p.heads += s.H;
     }
-    if ((uintptr_t)pos % 4 || (uintptr_t)freqs % 8) return LIDX_ERR_ALIGN;
-    p.pos = pos;
-    p.ps[0] = ps[0];
-    p.ps[1] = ps[1];
-    p.freqs = freqs;
+    rc = rope_turn_aligned(*r);
+    if (rc) return rc;
     p.T0 = T0;
     p.T1 = T1;
     p.D = D;
-    p.R = rot_dim;
-    p.off = rot_off;
-    p.half = layout == LIDX_ROPE_HALF;
-    p.mscale = mscale;
-    p.sign = inverse ? -1.f : 1.f;
     if (sm103_sms() <= 0) return LIDX_ERR_NO_DEVICE;
     cudaStream_t st = (cudaStream_t)stream;
     const cudaError_t e = dtype == 0 ? rope_launch<float>(p, st) : rope_launch<__nv_bfloat16>(p, st);
     return e == cudaSuccess ? LIDX_OK : LIDX_ERR_CUDA;
+}
+
+int lidx_rope(const lidx_rope_tensor* t, int nt, const int32_t* pos, const int64_t* ps,
+              const uint64_t* freqs, int64_t T0, int64_t T1, int D, int rot_dim, int rot_off,
+              int layout, int inverse, float mscale, int dtype, void* stream) {
+    if (!ps) return LIDX_ERR_NULL;
+    const lidx_rope_turn r = {pos, {0, ps[0], ps[1]}, freqs, nullptr, 1, rot_dim, rot_off, layout, mscale};
+    return lidx_rope_axes(t, nt, &r, T0, T1, D, inverse, dtype, stream);
 }
 
 }  // extern "C"
