@@ -389,6 +389,47 @@ int lidx_cache_append(const void* k, const void* v, const int64_t* ks, const int
                       float* v_scale, void* stream);
 
 /*
+ * lidx_cache_append with the norm and the rotary positions of the keys on the way, in fp32; keys and values are rounded
+ * once, to the cache's numbers.
+ *   r        the rotation.  Its positions are int32 [axes][B][S]; pos NULL: token i of sequence b is at start[b] + i on
+ *            every axis
+ *   w, eps   the norm of lidx_norm_rope (w fp32 or bf16 [D]: w_dtype 0 or 1); w NULL: no norm
+ * Everything else is as in lidx_cache_append; r's rules are lidx_rope_turn's.  An infinity or a NaN in a key is NaN in
+ * both dims of its pair, with w in the whole key.
+ */
+int lidx_rope_cache_append(const void* k, const void* v, const int64_t* ks, const int64_t* vs, const lidx_rope_turn* r,
+                           const void* w, int w_dtype, float eps, const int32_t* block_table, const int32_t* start,
+                           const int32_t* count, int64_t B, int64_t S, int Hkv, int D, int page, int64_t max_pages,
+                           int64_t num_pages, void* k_cache, void* v_cache, float* k_scale, float* v_scale, void* stream);
+
+/*
+ * A paged cache of 4-bit numbers.
+ *   k/v_cache    uint8 [num_pages,Hkv,page,D/2]: codes of two dims a byte, the even dim in the low half.  A code is a sign
+ *                bit, two exponent bits and a fraction bit: 0 .5 1 1.5 2 3 4 6 and their negatives
+ *   k/v_exps     int32 [num_pages,Hkv,page]: an exponent x of four bits for each 16 dims of a slot, the first dims' in the
+ *                lowest bits
+ *   k/v_scale    fp32 [num_pages,Hkv]: a slot holds the numbers code * 2^x * scale, x = 0 .. 11; x of 12 and more: NaN
+ * That is D/2 + 4 bytes a key and head.
+ *
+ * lidx_cache4_append writes new tokens as lidx_rope_cache_append does (r NULL: no rotation, w NULL: no norm).  The scale
+ * of a page and head is the smallest 2^e, e >= -40, with |x| <= 6 * 2^11 * 2^e for all finite values of its new tokens, or
+ * its old scale if that is larger and the page holds earlier tokens of the sequence; the exponent of a group is the
+ * smallest with |x| <= 6 * 2^x * scale, its codes are rounded to nearest, ties to even.  Where a scale grows, the
+ * earlier tokens' exponents fall with it and their codes are rounded again only if the exponent would fall below 0.
+ * A group with an infinity or a NaN has exponent 15 and codes of 0 and changes no scale.
+ */
+int lidx_cache4_append(const void* k, const void* v, const int64_t* ks, const int64_t* vs, const lidx_rope_turn* r,
+                       const void* w, int w_dtype, float eps, const int32_t* block_table, const int32_t* start,
+                       const int32_t* count, int64_t B, int64_t S, int Hkv, int D, int page, int64_t max_pages,
+                       int64_t num_pages, void* k_cache, void* v_cache, int32_t* k_exps, int32_t* v_exps, float* k_scale,
+                       float* v_scale, void* stream);
+
+/* A 4-bit cache as an 8-bit one: k8, v8 e4m3 [num_pages,Hkv,page,D] hold code * 2^x / 32, exactly (NaN codes where x is not
+ * an exponent), so that with scales of 32 times the 4-bit cache's they are the same cache. */
+int lidx_cache4_to_8(const void* k_cache, const void* v_cache, const int32_t* k_exps, const int32_t* v_exps, int Hkv, int D,
+                     int page, int64_t num_pages, void* k8, void* v8, void* stream);
+
+/*
  * Attention over a paged 8-bit cache.
  *   q            bf16 [B,S,Hq,D], strides (B, S, Hq) in qs (host int64[3]; multiples of 8)
  *   caches, scales, block_table: as lidx_cache_append.  Scales in 2^-80 .. 2^100 (lidx_cache_append gives 2^-40 and
@@ -425,7 +466,21 @@ int lidx_cache_attn(const void* q, const int64_t* qs, const void* k_cache, const
                     int64_t num_pages, int compress_ratio, int topk, float softmax_scale, void* out,
                     float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Device scratch of lidx_cache_attn on the current device, in bytes. */
+/*
+ * Attention over a paged cache of 4-bit numbers (lidx_cache4_append's): lidx_cache_attn with codes, exponents and scales in
+ * place of an 8-bit cache.  Everything is as there, with these differences:
+ *   - scales of keys and values are 1/32 of those that lidx_cache_attn allows: value scales in 2^-85 .. 2^95
+ *   - a group of 16 dims whose exponent is 12 or more counts as NaN codes
+ *   workspace    lidx_cache_attn_workspace_bytes(...) bytes, 256-byte aligned
+ * Exponents need 4-byte alignment, codes 16-byte alignment.
+ */
+int lidx_cache4_attn(const void* q, const int64_t* qs, const void* k_cache, const void* v_cache, const int32_t* k_exps,
+                     const int32_t* v_exps, const float* k_scale, const float* v_scale, const int32_t* block_table,
+                     const int32_t* kv_len, const int32_t* q_pos, const int32_t* topk_indices, int64_t B, int64_t S, int Hq,
+                     int Hkv, int D, int page, int64_t max_pages, int64_t num_pages, int compress_ratio, int topk,
+                     float softmax_scale, void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Device scratch of lidx_cache_attn and lidx_cache4_attn on the current device, in bytes. */
 size_t lidx_cache_attn_workspace_bytes(int64_t B, int64_t S, int Hq, int Hkv, int D, int topk);
 
 /* Device scratch the call needs for these sizes, in bytes (0 = none).

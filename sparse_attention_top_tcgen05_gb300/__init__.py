@@ -22,7 +22,10 @@ Functions carry the C names:
   lidx_rope_axis_map        the axis of each pair where positions have several (time, height, width)
   lidx_norm_rope, lidx_norm_rope_bwd  norms of each head with the rotary positions in one pass, and their gradients
   lidx_cache_append         new keys and values into a paged 8-bit cache
+  lidx_rope_cache_append    the same with the norm and the rotary positions of the keys on the way
   lidx_cache_attn           attention over that cache, at every key or at selected ones
+  lidx_cache4_append, lidx_cache4_to_8  a paged cache of 4-bit numbers, and the same as an 8-bit one
+  lidx_cache4_attn          attention over the 4-bit cache
   lidx_workspace_bytes, lidx_cache_attn_workspace_bytes, lidx_device_status,
   lidx_status_string, lidx_set_wait_limit_ns, lidx_debug_stall_producer
 
@@ -59,7 +62,8 @@ EXPORTS = ("lidx_indexer_fwd", "lidx_indexer_fwd_ranges", "lidx_indexer_logits",
            "lidx_indexer_fwd_noalloc", "lidx_noalloc_scratch_bytes", "lidx_set_wait_limit_ns",
            "lidx_debug_stall_producer", "lidx_rope_freqs", "lidx_rope", "lidx_cache_append",
            "lidx_cache_attn", "lidx_cache_attn_workspace_bytes", "lidx_rope_axes", "lidx_norm_rope",
-           "lidx_norm_rope_bwd", "lidx_norm_rope_bwd_workspace_bytes")
+           "lidx_norm_rope_bwd", "lidx_norm_rope_bwd_workspace_bytes", "lidx_rope_cache_append",
+           "lidx_cache4_append", "lidx_cache4_to_8", "lidx_cache4_attn")
 
 
 class _RopeTensor(C.Structure):
@@ -141,10 +145,18 @@ def lib() -> C.CDLL:
             L.lidx_rope_axes.argtypes = [P, i32, P, i64, i64, i32, i32, i32, P]
             L.lidx_norm_rope.argtypes = [P, i32, P, f32, i64, i64, i32, i32, i32, P]
             L.lidx_norm_rope_bwd.argtypes = [P, i32, P, f32, i64, i64, i32, i32, i32, P, sz, P]
+            L.lidx_rope_cache_append.argtypes = [P, P, P, P, P, P, i32, f32, P, P, P, i64, i64, i32, i32, i32, i64, i64,
+                                                 P, P, P, P, P]
+            L.lidx_cache4_append.argtypes = [P, P, P, P, P, P, i32, f32, P, P, P, i64, i64, i32, i32, i32, i64, i64,
+                                             P, P, P, P, P, P, P]
+            L.lidx_cache4_attn.argtypes = [P, P, P, P, P, P, P, P, P, P, P, P, i64, i64, i32, i32, i32, i32,
+                                           i64, i64, i32, i32, f32, P, P, P, sz, P]
+            L.lidx_cache4_to_8.argtypes = [P, P, P, P, i32, i32, i32, i64, P, P, P]
             L.lidx_norm_rope_bwd_workspace_bytes.argtypes = [i32]
             L.lidx_norm_rope_bwd_workspace_bytes.restype = sz
             for name in ("lidx_rope_freqs", "lidx_rope", "lidx_cache_append", "lidx_cache_attn",
-                         "lidx_rope_axes", "lidx_norm_rope", "lidx_norm_rope_bwd",
+                         "lidx_rope_axes", "lidx_norm_rope", "lidx_norm_rope_bwd", "lidx_rope_cache_append",
+                         "lidx_cache4_append", "lidx_cache4_to_8", "lidx_cache4_attn",
                          "lidx_indexer_fwd", "lidx_indexer_fwd_ranges", "lidx_indexer_logits",
                          "lidx_extract_topk_scores", "lidx_topk_rows", "lidx_indexer_scores_v41",
                          "lidx_indexer_topk_v41", "lidx_indexer_bwd", "lidx_indexer_bwd_ranges",
@@ -556,8 +568,15 @@ def lidx_rope_axis_map(sections, interleaved=False, device="cuda") -> torch.Tens
     return torch.tensor(ids, dtype=_u8).to(device)
 
 
-def _turn(pos, freqs, layout, rot_off, mscale, axes, T0, T1, dev):
-    """The packed lidx_rope_turn of a rotation."""
+def _turn(pos, freqs, layout, rot_off, mscale, axes, T0, T1, dev, own_pos=False):
+    """The packed lidx_rope_turn of a rotation.  own_pos: pos may be None, for the call's own positions."""
+    if pos is None and own_pos:
+        pairs = _dense(freqs, "freqs", _i64, (None,), dev)[0]
+        if axes is not None:
+            raise ValueError("axes needs pos, with the positions on each axis")
+        if layout not in ROPE_LAYOUT:
+            raise ValueError(f"layout must be one of {list(ROPE_LAYOUT)}")
+        return _ROPE_TURN(0, 0, 0, 0, freqs.data_ptr(), 0, 1, 2 * pairs, rot_off, ROPE_LAYOUT[layout], mscale)
     if not isinstance(pos, _Tensor) or pos.dtype is not _i32 or not pos.is_cuda:
         raise TypeError("pos must be an int32 CUDA tensor")
     if pos.get_device() != dev:
@@ -754,6 +773,96 @@ def lidx_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, sta
         raise LidxError(rc, "lidx_cache_append")
 
 
+def _append_args(k, v, freqs, pos, weight, layout, rot_off, mscale, axes, start, count):
+    """Checks of the new tokens, of their norm and rotation, and what goes to C of them before the table."""
+    shape, ks, dev = _strided(k, "k", _bf16)
+    shape_v, vs, _ = _strided(v, "v", _bf16, dev)
+    if shape_v != shape:
+        raise ValueError("k and v shapes disagree")
+    B, S, Hkv, D = shape
+    turn = None
+    if freqs is not None:
+        turn = _turn(pos, freqs, layout, rot_off, mscale, axes, B, S, dev, True)
+    elif pos is not None or axes is not None:
+        raise ValueError("pos and axes need freqs")
+    wdt = 0
+    if weight is not None:
+        if not isinstance(weight, _Tensor) or (weight.dtype is not _f32 and weight.dtype is not _bf16):
+            raise TypeError("weight must be a float32 or bfloat16 tensor")
+        _dense(weight, "weight", weight.dtype, (D,), dev)
+        wdt = 1 if weight.dtype is _bf16 else 0
+    _dense(start, "start", _i32, (B,), dev)
+    if count is not None:
+        _dense(count, "count", _i32, (B,), dev)
+    return shape, dev, (k.data_ptr(), v.data_ptr(), _I3(*ks), _I3(*vs), turn,
+                        None if weight is None else weight.data_ptr(), wdt)
+
+
+def lidx_rope_cache_append(k, v, freqs, k_cache, v_cache, k_scale, v_scale, block_table, start, count=None, pos=None,
+                           weight=None, eps=1e-6, layout="interleaved", rot_off=0, mscale=1.0, axes=None, stream=None):
+    """lidx_cache_append with the norm (weight [D] fp32 or bf16; None: no norm) and the rotary positions of the keys on the
+    way, as lidx_norm_rope's and lidx_rope's, in fp32: keys are rounded once, to the cache's numbers.  pos: int32, broadcast
+    to [B,S] (with axes [A, ...]); None: token i of sequence b is at start[b] + i."""
+    (B, S, Hkv, D), dev, args = _append_args(k, v, freqs, pos, weight, layout, rot_off, mscale, axes, start, count)
+    if freqs is None:
+        raise TypeError("freqs must be lidx_rope_freqs's tensor")
+    pages, _, page, MP = _cache(k_cache, v_cache, k_scale, v_scale, block_table, B, Hkv, D, dev)
+    rc = (_lib or lib()).lidx_rope_cache_append(
+        *args, eps, block_table.data_ptr(), start.data_ptr(), None if count is None else count.data_ptr(), B, S, Hkv, D,
+        page, MP, pages, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        _raw_stream(stream, dev))
+    if rc:
+        raise LidxError(rc, "lidx_rope_cache_append")
+
+
+def _cache4(k_cache, v_cache, k_exps, v_exps, Hkv, D, dev):
+    shape = _dense(k_cache, "k_cache", _u8, (None, Hkv, None, None if D is None else D // 2), dev)
+    _dense(v_cache, "v_cache", _u8, shape, dev)
+    _dense(k_exps, "k_exps", _i32, shape[:3], dev)
+    _dense(v_exps, "v_exps", _i32, shape[:3], dev)
+    return shape
+
+
+def lidx_cache4_append(k, v, k_cache, v_cache, k_exps, v_exps, k_scale, v_scale, block_table, start, count=None, freqs=None,
+                       pos=None, weight=None, eps=1e-6, layout="interleaved", rot_off=0, mscale=1.0, axes=None, stream=None):
+    """Writes k, v [B,S,Hkv,D] bf16 behind the start[b] tokens that each sequence's pages hold, in 4 bits, with the norm
+    (weight) and the rotary positions (freqs) of the keys on the way as in lidx_rope_cache_append; both may be left out.
+
+    k_cache, v_cache uint8 [P,Hkv,page,D/2] (two codes a byte), k_exps, v_exps int32 [P,Hkv,page] (an exponent of four bits
+    for each 16 dims) and k_scale, v_scale fp32 [P,Hkv] are updated in place: a slot holds code * 2^exponent * scale, the
+    codes being 0 .5 1 1.5 2 3 4 6 and their negatives.  A group of 16 dims with an infinity or a NaN reads as NaN."""
+    (B, S, Hkv, D), dev, args = _append_args(k, v, freqs, pos, weight, layout, rot_off, mscale, axes, start, count)
+    pages, _, page, _ = _cache4(k_cache, v_cache, k_exps, v_exps, Hkv, D, dev)
+    _dense(k_scale, "k_scale", _f32, (pages, Hkv), dev)
+    _dense(v_scale, "v_scale", _f32, (pages, Hkv), dev)
+    MP = _dense(block_table, "block_table", _i32, (B, None), dev)[1]
+    rc = (_lib or lib()).lidx_cache4_append(
+        *args, eps, block_table.data_ptr(), start.data_ptr(), None if count is None else count.data_ptr(), B, S, Hkv, D,
+        page, MP, pages, k_cache.data_ptr(), v_cache.data_ptr(), k_exps.data_ptr(), v_exps.data_ptr(), k_scale.data_ptr(),
+        v_scale.data_ptr(), _raw_stream(stream, dev))
+    if rc:
+        raise LidxError(rc, "lidx_cache4_append")
+
+
+def lidx_cache4_to_8(k_cache, v_cache, k_exps, v_exps, stream=None, out=None):
+    """A 4-bit cache as an 8-bit one: (k8, v8) float8_e4m3fn [P,Hkv,page,D] that hold code * 2^exponent / 32 exactly, NaN
+    where a group reads as NaN.  With scales of 32 times the 4-bit cache's they are the same cache for lidx_cache_attn."""
+    dev = k_cache.get_device() if isinstance(k_cache, _Tensor) else 0
+    pages, Hkv, page, half = _cache4(k_cache, v_cache, k_exps, v_exps, None, None, dev)
+    shape = (pages, Hkv, page, 2 * half)
+    if out is None:
+        k8, v8 = _new(shape, _f8, k_cache.device, stream), _new(shape, _f8, k_cache.device, stream)
+    else:
+        k8, v8 = out
+        _dense(k8, "out", _f8, shape, dev)
+        _dense(v8, "out", _f8, shape, dev)
+    rc = (_lib or lib()).lidx_cache4_to_8(k_cache.data_ptr(), v_cache.data_ptr(), k_exps.data_ptr(), v_exps.data_ptr(), Hkv,
+                                          2 * half, page, pages, k8.data_ptr(), v8.data_ptr(), _raw_stream(stream, dev))
+    if rc:
+        raise LidxError(rc, "lidx_cache4_to_8")
+    return k8, v8
+
+
 def lidx_cache_attn_workspace_bytes(B, S, Hq, Hkv, D, topk=0) -> int:
     return int(lib().lidx_cache_attn_workspace_bytes(B, S, Hq, Hkv, D, topk))
 
@@ -769,8 +878,29 @@ def lidx_cache_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, 
     A row whose query or a key it sees is not finite is NaN, with its log-sum-exp; for NaN values see lidx.h.
     Returns (out [B,S,Hq,D] bf16, lse [B,S,Hq] fp32 or None); ``out`` may hold preallocated ones."""
     shape, qs, dev = _strided(q, "q", _bf16)
+    pages, Hkv, page, MP = _cache(k_cache, v_cache, k_scale, v_scale, block_table, shape[0], None, shape[3], dev)
+    return _cache_attn((_lib or lib()).lidx_cache_attn, q, shape, qs, dev, (k_cache, v_cache, k_scale, v_scale, block_table),
+                       Hkv, page, MP, pages, kv_len, q_pos, compress_ratio, topk_indices, softmax_scale, want_lse, stream, out,
+                       workspace, "lidx_cache_attn")
+
+
+def lidx_cache4_attn(q, k_cache, v_cache, k_exps, v_exps, k_scale, v_scale, block_table, kv_len, q_pos=None,
+                     compress_ratio=1, topk_indices=None, softmax_scale=None, want_lse=False, stream=None, out=None,
+                     workspace=None):
+    """lidx_cache_attn over a cache written by lidx_cache4_append (codes, exponents and scales; value scales 2^-85 .. 2^95)."""
+    shape, qs, dev = _strided(q, "q", _bf16)
+    pages, Hkv, page, _ = _cache4(k_cache, v_cache, k_exps, v_exps, None, shape[3], dev)
+    _dense(k_scale, "k_scale", _f32, (pages, Hkv), dev)
+    _dense(v_scale, "v_scale", _f32, (pages, Hkv), dev)
+    MP = _dense(block_table, "block_table", _i32, (shape[0], None), dev)[1]
+    return _cache_attn((_lib or lib()).lidx_cache4_attn, q, shape, qs, dev,
+                       (k_cache, v_cache, k_exps, v_exps, k_scale, v_scale, block_table), Hkv, page, MP, pages, kv_len, q_pos,
+                       compress_ratio, topk_indices, softmax_scale, want_lse, stream, out, workspace, "lidx_cache4_attn")
+
+
+def _cache_attn(call, q, shape, qs, dev, cache, Hkv, page, MP, pages, kv_len, q_pos, compress_ratio, topk_indices,
+                softmax_scale, want_lse, stream, out, workspace, name):
     B, S, Hq, D = shape
-    pages, Hkv, page, MP = _cache(k_cache, v_cache, k_scale, v_scale, block_table, B, None, D, dev)
     _dense(kv_len, "kv_len", _i32, (B,), dev)
     if q_pos is not None:
         _dense(q_pos, "q_pos", _i32, (B,), dev)
@@ -791,12 +921,11 @@ def lidx_cache_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, 
         workspace = _scratch(ws_bytes, q.device, stream)
     else:
         ws_bytes = _dense(workspace, "workspace", torch.uint8, (None,), dev)[0]
-    rc = L.lidx_cache_attn(
-        q.data_ptr(), _I3(*qs), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-        block_table.data_ptr(), kv_len.data_ptr(), None if q_pos is None else q_pos.data_ptr(),
+    rc = call(
+        q.data_ptr(), _I3(*qs), *[t.data_ptr() for t in cache], kv_len.data_ptr(), None if q_pos is None else q_pos.data_ptr(),
         None if topk_indices is None else topk_indices.data_ptr(), B, S, Hq, Hkv, D, page, MP, pages, compress_ratio,
         topk, D ** -0.5 if softmax_scale is None else softmax_scale, o.data_ptr(), None if lse is None else lse.data_ptr(),
         workspace.data_ptr(), ws_bytes, _raw_stream(stream, dev))
     if rc:
-        raise LidxError(rc, "lidx_cache_attn")
+        raise LidxError(rc, name)
     return o, lse

@@ -323,7 +323,7 @@ int lidx_device_status(void* stream) {
     // one status word per translation unit with kernels; every one is read (and cleared)
     const int st[] = {status_score_v4(1), status_score_v4_short(1), status_score_v4_fused(1),
                       status_score_v41(1), status_misc(1), status_bwd(1),
-                      status_cache_attn(1), status_cache_attn_wide(1)};
+                      status_cache_attn(1), status_cache_attn_wide(1), status_cache4_attn(1), status_cache4_attn_wide(1)};
     int first = 0;
     for (int v : st) {
         if (v < 0) return LIDX_ERR_CUDA;

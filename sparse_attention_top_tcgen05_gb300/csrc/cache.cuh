@@ -1,5 +1,5 @@
-// cache.cuh -- what the paged 8-bit cache's writer (cache_append.cu) and its
-// reader (cache_attn.cu) share: the layout's rules and the e4m3 conversions.
+// cache.cuh -- what the paged caches' writers (cache_append.cu, rope_append.cu) and readers (cache_attn.cu,
+// cache4_attn.cu) share: the layout's rules and the conversions of e4m3 and of 4-bit numbers.
 #pragma once
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -40,6 +40,37 @@ __device__ __forceinline__ float f16_to_f32(uint16_t v) {
 __device__ __forceinline__ float2 e4m3x2_to(uint32_t v) {
     const uint32_t h = f16x2_from_e4m3x2(v & 0xffffu);
     return make_float2(f16_to_f32((uint16_t)(h & 0xffffu)), f16_to_f32((uint16_t)(h >> 16)));
+}
+
+// ---- 4-bit numbers.  A slot's codes are e2m1 (sign, two exponent bits, one fraction bit: 0 .5 1 1.5 2 3 4 6), dim i in bits
+// 4 (i % 8) of word i / 8; each 16 dims have an exponent x of 4 bits, 0 .. 11, and 12 .. 15 where they are not numbers.
+// code * 2^x is e4m3 times 2^5 exactly: codes of 1 and more add x to e4m3's exponent field, and so does .5, which is a
+// power of two.  (e4m3's largest finite is 448; 6 * 2^11 / 2^5 = 384.)
+constexpr int kCache4Exps = 12;
+constexpr float kCache4Unit = 32.f;
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+    return r;
+}
+// e4m3 codes of the eight sizes with exponent x: bytes of lo and hi.
+__device__ __forceinline__ void cache4_table(uint32_t x, uint32_t& lo, uint32_t& hi) {
+    lo = x * 0x08080800u + 0x14100800u;
+    hi = x * 0x08080808u + 0x24201c18u;
+    if (x >= kCache4Exps) lo = hi = 0x7f7f7f7fu;
+}
+// Eight 4-bit codes -> eight e4m3 codes: sizes by a byte lookup, signs by a byte's replicated top bit.
+__device__ __forceinline__ uint2 cache4_widen(uint32_t w, uint32_t lo, uint32_t hi) {
+    const uint32_t m = w & 0x77777777u, u = w << 4;
+    const uint32_t a = prmt(lo, hi, m), b = prmt(lo, hi, m >> 16);
+    return make_uint2(a | (prmt(u, w, 0xd9c8u) & 0x80808080u), b | (prmt(u, w, 0xfbeau) & 0x80808080u));
+}
+// Two floats -> two codes (lo in the low bits); rounds to nearest even, saturates at +-6.
+__device__ __forceinline__ uint32_t e2m1x2_from(float lo, float hi) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 
 }  // namespace lidx

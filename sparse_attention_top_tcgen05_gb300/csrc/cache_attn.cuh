@@ -37,11 +37,15 @@ struct AttnParams {
     uint8_t* ws;
     uint64_t wait_ns;
     int debug_stall;       // 1: the producer issues nothing (failure-detection tests)
+    const uint8_t* codes[2];  // 4 bits: keys, values
+    const int32_t* exps[2];
 };
 
 constexpr int kATile = 128;                     // keys of a tile
 constexpr int kASlotBytes = kATile * 128;       // one K or V tile: 128 bytes a key (zero past D)
 constexpr int kAMeta = 6;                       // stages of per-key scales
+constexpr int kAKeys4 = 64;                     // 4 bits: keys of a producer warp, half a tile
+constexpr int kAStage4 = kAKeys4 * 2 * (64 + 4);  // its packed keys and values and their exponents
 constexpr float kATop = 8.f;                    // weights are scaled to 2^8
 constexpr float kALn2 = 0.693147180559945309f;
 // Smallest value scale.  A row's sum adds weights of at most 2^8.3 divided by their value scales: 2^30 keys of this one stay
@@ -167,7 +171,8 @@ struct AttnPipe {
     float* key_iv;          // [kAMeta][128] its inverse
     uint32_t* seen;         // [kAMeta][4] bits of the keys that are seen
     uint32_t* flag;         // [kAMeta] not 0: a key of the tile is not seen
-    int* rows;              // [PRODUCERS][128] cache rows of gathered keys
+    int* rows;              // [PRODUCERS][128] cache rows of gathered keys (4 bits: [PRODUCERS][kAKeys4])
+    uint8_t* stage;         // 4 bits: [PRODUCERS][kAStage4]
     uint64_t *kv_full;      // [SLOTS] K or V tile landed
     uint64_t *kv_empty;     // [SLOTS] its product is done
     uint64_t *meta_full;    // [kAMeta] what belongs to a tile's keys is written
@@ -433,6 +438,201 @@ __device__ __forceinline__ void attn_produce(const AttnParams& p, AttnWalk& wk, 
     }
 }
 
+// The same over a cache of 4-bit numbers: warp pw, two warps a tile, TL tiles in turn.  A warp copies the packed rows of its 64
+// keys into a stage of its own, asynchronously and a tile ahead, and widens them to the e4m3 codes of code * 2^x / 32 in
+// the layout that the 8-bit cache's tiles have, so that all that follows is the same.  Keys that no row of the unit sees (and
+// dims past the head) are written as zeros.
+template <int SLOTS, int TL, bool SEL>
+__device__ __forceinline__ void attn_produce4(const AttnParams& p, AttnWalk& wk, const AttnPipe& x, int pw, int lane) {
+    const int turn = pw >> 1, half = pw & 1;
+    uint8_t* const stage = x.stage + pw * kAStage4;
+    int* const rows = x.rows + pw * kAKeys4;
+    bool ok = !p.debug_stall;
+    struct Ref {
+        bool live;
+        int b, h, tile, limit;
+        int tc;       // tiles of the CTA before it
+        int64_t row;  // of topk_indices
+    };
+    int tile = 0, count = 0;
+    bool more = true;
+    auto next_ref = [&]() {
+        Ref r{false, 0, 0, 0, 0, 0, 0};
+        while (more) {
+            if (tile >= wk.t1 || wk.gr.n == 0) {
+                more = wk.next(p);
+                tile = wk.t0;
+                continue;
+            }
+            // on to the first tile of this segment that is the warp's
+            const int skip = (turn - count % TL + TL) % TL, left = wk.t1 - tile;
+            if (skip >= left) {
+                count += left;
+                tile = wk.t1;
+                continue;
+            }
+            count += skip;
+            tile += skip;
+            const int limit = SEL ? attn_end(p, wk.gr.b, wk.gr.st) : wk.gr.limit;
+            r = Ref{true, wk.gr.b, wk.h, tile, limit, count, (int64_t)wk.gr.b * p.S + wk.gr.st};
+            ++count;
+            ++tile;
+            break;
+        }
+        return r;
+    };
+    const int page_mask = p.page - 1;
+    // a lane has keys lane and lane + 32 of the warp's 64
+    auto keys = [&](const Ref& r, int (&t)[2]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int k = r.tile * kATile + kAKeys4 * half + 32 * i + lane;
+            if constexpr (SEL)
+                t[i] = r.live && k < p.topk ? p.idx[r.row * p.topk + k] : -1;
+            else
+                t[i] = r.live ? k : -1;
+        }
+    };
+    auto pages = [&](const Ref& r, const int (&t)[2], int (&pid)[2]) {
+        const int32_t* tab = p.table + (int64_t)r.b * p.max_pages;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) pid[i] = t[i] >= 0 && t[i] < r.limit ? tab[t[i] >> p.page_shift] : -1;
+    };
+    float a[2], v[2];
+    uint32_t seen[2];
+    // scales and rows of a tile's keys; bits of the keys that are seen
+    auto lookup = [&](const Ref& r, const int (&t)[2], const int (&pid)[2], float (&a)[2], float (&v)[2], uint32_t (&seen)[2]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const bool good = pid[i] >= 0 && pid[i] < p.num_pages;
+            const int cell = (good ? pid[i] : 0) * p.Hkv + r.h;  // num_pages * Hkv * page < 2^31
+            a[i] = p.ks[cell];
+            v[i] = p.vs[cell];
+            rows[32 * i + lane] = good ? (cell << p.page_shift) + (t[i] & page_mask) : -1;
+            seen[i] = __ballot_sync(0xffffffffu, good);
+        }
+        __syncwarp();
+    };
+    // A row is copied in units of 16 bytes, or of 8 where D / 2 is no multiple of 16; lanes of a row: 2^us
+    const bool wide = p.D % 32 == 0;
+    const int units = wide ? p.D / 32 : p.D / 16, us = units <= 1 ? 0 : (units <= 2 ? 1 : (units <= 4 ? 2 : 3));
+    const int cs = p.D <= 32 ? 0 : (p.D <= 64 ? 1 : 2);  // lanes of a row, 32 dims each: 2^cs
+    const int pitch = 16 << cs;
+    const uint32_t stage_u = smem_u32(stage);
+    auto copy = [&](int which) {
+        const uint8_t* const src = p.codes[which];
+        const uint32_t to = stage_u + which * (kAKeys4 * 64);
+        const int u = lane & ((1 << us) - 1);
+#pragma unroll 4
+        for (int r0 = 0; r0 < kAKeys4; r0 += 32 >> us) {
+            const int r = r0 + (lane >> us), row = rows[r];
+            if (row >= 0 && u < units) {
+                if (wide)
+                    cp_async16(to + r * pitch + u * 16, src + (int64_t)row * (p.D / 2) + u * 16);
+                else
+                    cp_async8(to + r * pitch + u * 8, src + (int64_t)row * (p.D / 2) + u * 8);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = rows[32 * i + lane];
+            if (row >= 0)
+                cp_async4(stage_u + 2 * (kAKeys4 * 64) + which * (kAKeys4 * 4) + (32 * i + lane) * 4, p.exps[which] + row);
+        }
+        cp_async_commit();
+    };
+    auto widen = [&](int which, uint8_t* tile_at, const uint32_t (&seen)[2]) {
+        cp_async_wait<1>();
+        __syncwarp();
+        const uint8_t* const from = stage + which * (kAKeys4 * 64);
+        const uint32_t* const ex = reinterpret_cast<const uint32_t*>(stage + 2 * (kAKeys4 * 64) + which * (kAKeys4 * 4));
+        const int c = lane & ((1 << cs) - 1);
+        const bool some = 32 * c < p.D, both = 32 * c + 16 < p.D;
+        if (some) {
+#pragma unroll 4
+            for (int r0 = 0; r0 < kAKeys4; r0 += 32 >> cs) {
+                const int r = r0 + (lane >> cs);
+                uint4 w = *reinterpret_cast<const uint4*>(from + r * pitch + c * 16);
+                uint32_t e = ex[r] >> (8 * c);
+                if (!((seen[r >> 5] >> (r & 31)) & 1)) w = make_uint4(0, 0, 0, 0), e = 0;
+                if (!both) w.z = w.w = 0, e &= 15u;
+                uint32_t lo, hi;
+                cache4_table(e & 15u, lo, hi);
+                const uint2 w0 = cache4_widen(w.x, lo, hi), w1 = cache4_widen(w.y, lo, hi);
+                cache4_table((e >> 4) & 15u, lo, hi);
+                const uint2 w2 = cache4_widen(w.z, lo, hi), w3 = cache4_widen(w.w, lo, hi);
+                uint8_t* const at = tile_at + (kAKeys4 * half + r) * 128;
+                const int j = 2 * c;
+                *reinterpret_cast<uint4*>(at + ((j ^ (r & 7)) << 4)) = make_uint4(w0.x, w0.y, w1.x, w1.y);
+                *reinterpret_cast<uint4*>(at + (((j + 1) ^ (r & 7)) << 4)) = make_uint4(w2.x, w2.y, w3.x, w3.y);
+            }
+        }
+        fence_async_smem();
+        __syncwarp();
+    };
+    // waits for the slot of tile tc's K (which = 0) or V
+    auto claim = [&](int tc, int which) {
+        const int seq = 2 * tc + which;
+        ok = ok && mbar_wait(x.kv_empty + seq % SLOTS, ((seq / SLOTS) & 1) ^ 1, p.wait_ns);
+        if (which == 0) ok = ok && mbar_wait(x.meta_empty + tc % kAMeta, ((tc / kAMeta) & 1) ^ 1, p.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+    };
+    // Steps ahead: indices of the warp's tile after next, page ids and then rows of its next, so that a step waits for one
+    // memory latency at most.
+    Ref r0 = next_ref();
+    int t1[2], t2[2], pid1[2];
+    keys(r0, t1);
+    pages(r0, t1, pid1);
+    lookup(r0, t1, pid1, a, v, seen);
+    if (ok) {
+        copy(0);
+        copy(1);
+    }
+    Ref r1 = next_ref();
+    keys(r1, t1);
+    Ref r2 = next_ref();
+    keys(r2, t2);
+    pages(r1, t1, pid1);
+    while (ok && r0.live) {
+        const int tc = r0.tc, sk = 2 * tc, ms = tc % kAMeta, s0 = sk % SLOTS, s1 = (sk + 1) % SLOTS;
+        claim(tc, 0);
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const bool good = (seen[i] >> lane) & 1;
+            const int at = ms * kATile + kAKeys4 * half + 32 * i + lane;
+            const float y = __log2f(fmaxf(v[i] * kCache4Unit, kAMinScale));
+            x.key_a[at] = good || !SEL ? a[i] * (kCache4Unit * p.scale_log2) : 0.f;
+            x.key_lv[at] = good ? y : -INFINITY;
+            x.key_iv[at] = exp2_approx(-y);
+            if (lane == 0) {
+                x.seen[ms * 4 + 2 * half + i] = seen[i];
+                reinterpret_cast<uint8_t*>(x.flag + ms)[2 * half + i] = seen[i] == 0xffffffffu ? 0 : 1;
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(x.meta_full + ms);
+        widen(0, x.kv + s0 * kASlotBytes, seen);
+        if (lane == 0) mbar_arrive(x.kv_full + s0);
+        const uint32_t now[2] = {seen[0], seen[1]};
+        lookup(r1, t1, pid1, a, v, seen);
+        copy(0);
+        pages(r2, t2, pid1);
+        const Ref r3 = next_ref();
+        t1[0] = t2[0], t1[1] = t2[1];
+        keys(r3, t2);
+        claim(tc, 1);
+        if (!ok) break;
+        widen(1, x.kv + s1 * kASlotBytes, now);
+        if (lane == 0) mbar_arrive(x.kv_full + s1);
+        copy(1);
+        r0 = r1;
+        r1 = r2;
+        r2 = r3;
+    }
+    cp_async_wait<0>();  // copies in flight end before the memory is given up
+}
+
 // Query rows of a unit, bf16 -> e4m3 hi and lo: one of QWARPS warps.  twice: rows 0 .. 63 are repeated as 64 .. 127.
 template <int N, int QB, int QWARPS>
 __device__ __forceinline__ void attn_queries(const AttnParams& p, AttnWalk& wk, const AttnPipe& x, int qw, int lane,
@@ -508,7 +708,10 @@ __device__ __forceinline__ void attn_queries(const AttnParams& p, AttnWalk& wk, 
     }
 }
 
-// Kernels of at most 32 and of at most 128 columns; the parts of either are joined by one kernel.
+// Kernels of at most 32 (attn_launch of cache_attn_narrow.cuh) and of at most 128 columns, of the 8-bit and the 4-bit cache;
+// the parts of any are joined by one kernel.
+cudaError_t attn4_launch(int N, const AttnParams& p, int grid, cudaStream_t st);
+cudaError_t attn4_launch_wide(const AttnParams& p, int grid, cudaStream_t st);
 cudaError_t attn_launch_wide(const CUtensorMap& mk, const CUtensorMap& mv, const AttnParams& p, int grid, cudaStream_t st);
 
 }  // namespace lidx

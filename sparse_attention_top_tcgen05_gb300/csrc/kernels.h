@@ -123,5 +123,7 @@ int status_misc(int clear);
 int status_bwd(int clear);
 int status_cache_attn(int clear);
 int status_cache_attn_wide(int clear);
+int status_cache4_attn(int clear);
+int status_cache4_attn_wide(int clear);
 
 }  // namespace lidx
