@@ -471,8 +471,8 @@ int lidx_cache_attn(const void* q, const int64_t* qs, const void* k_cache, const
  * place of an 8-bit cache.  Everything is as there, with these differences:
  *   - scales of keys and values are 1/32 of those that lidx_cache_attn allows: value scales in 2^-85 .. 2^95
  *   - a group of 16 dims whose exponent is 12 or more counts as NaN codes
- *   workspace    lidx_cache_attn_workspace_bytes(...) bytes, 256-byte aligned
- * Exponents need 4-byte alignment, codes 16-byte alignment.
+ *   workspace    lidx_cache4_attn_workspace_bytes(...) bytes, 256-byte aligned
+ * Codes and exponents need 16-byte alignment.
  */
 int lidx_cache4_attn(const void* q, const int64_t* qs, const void* k_cache, const void* v_cache, const int32_t* k_exps,
                      const int32_t* v_exps, const float* k_scale, const float* v_scale, const int32_t* block_table,
@@ -480,7 +480,12 @@ int lidx_cache4_attn(const void* q, const int64_t* qs, const void* k_cache, cons
                      int Hkv, int D, int page, int64_t max_pages, int64_t num_pages, int compress_ratio, int topk,
                      float softmax_scale, void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Device scratch of lidx_cache_attn and lidx_cache4_attn on the current device, in bytes. */
+/* Device scratch of lidx_cache4_attn on the current device, in bytes (topk 0: all keys).  Where a key is read by several units
+ * of 128 rows (S * Hq/Hkv > 128), or S * topk is at least twice max_pages * page, it holds the sequences' pages in 8 bits,
+ * 2 * B * max_pages * page * Hkv * D bytes and little more, if those are not more than 2 GiB. */
+size_t lidx_cache4_attn_workspace_bytes(int64_t B, int64_t S, int Hq, int Hkv, int D, int page, int64_t max_pages, int topk);
+
+/* Device scratch of lidx_cache_attn on the current device, in bytes. */
 size_t lidx_cache_attn_workspace_bytes(int64_t B, int64_t S, int Hq, int Hkv, int D, int topk);
 
 /* Device scratch the call needs for these sizes, in bytes (0 = none).

@@ -26,7 +26,7 @@ Functions carry the C names:
   lidx_cache_attn           attention over that cache, at every key or at selected ones
   lidx_cache4_append, lidx_cache4_to_8  a paged cache of 4-bit numbers, and the same as an 8-bit one
   lidx_cache4_attn          attention over the 4-bit cache
-  lidx_workspace_bytes, lidx_cache_attn_workspace_bytes, lidx_device_status,
+  lidx_workspace_bytes, lidx_cache_attn_workspace_bytes, lidx_cache4_attn_workspace_bytes, lidx_device_status,
   lidx_status_string, lidx_set_wait_limit_ns, lidx_debug_stall_producer
 
 Calls run on the current stream, or on ``stream``.  There the caller makes the stream wait for the inputs,
@@ -63,7 +63,8 @@ EXPORTS = ("lidx_indexer_fwd", "lidx_indexer_fwd_ranges", "lidx_indexer_logits",
            "lidx_debug_stall_producer", "lidx_rope_freqs", "lidx_rope", "lidx_cache_append",
            "lidx_cache_attn", "lidx_cache_attn_workspace_bytes", "lidx_rope_axes", "lidx_norm_rope",
            "lidx_norm_rope_bwd", "lidx_norm_rope_bwd_workspace_bytes", "lidx_rope_cache_append",
-           "lidx_cache4_append", "lidx_cache4_to_8", "lidx_cache4_attn")
+           "lidx_cache4_append", "lidx_cache4_to_8", "lidx_cache4_attn",
+           "lidx_cache4_attn_workspace_bytes")
 
 
 class _RopeTensor(C.Structure):
@@ -151,6 +152,8 @@ def lib() -> C.CDLL:
                                              P, P, P, P, P, P, P]
             L.lidx_cache4_attn.argtypes = [P, P, P, P, P, P, P, P, P, P, P, P, i64, i64, i32, i32, i32, i32,
                                            i64, i64, i32, i32, f32, P, P, P, sz, P]
+            L.lidx_cache4_attn_workspace_bytes.argtypes = [i64, i64, i32, i32, i32, i32, i64, i32]
+            L.lidx_cache4_attn_workspace_bytes.restype = sz
             L.lidx_cache4_to_8.argtypes = [P, P, P, P, i32, i32, i32, i64, P, P, P]
             L.lidx_norm_rope_bwd_workspace_bytes.argtypes = [i32]
             L.lidx_norm_rope_bwd_workspace_bytes.restype = sz
@@ -867,6 +870,10 @@ def lidx_cache_attn_workspace_bytes(B, S, Hq, Hkv, D, topk=0) -> int:
     return int(lib().lidx_cache_attn_workspace_bytes(B, S, Hq, Hkv, D, topk))
 
 
+def lidx_cache4_attn_workspace_bytes(B, S, Hq, Hkv, D, page, max_pages, topk=0) -> int:
+    return int(lib().lidx_cache4_attn_workspace_bytes(B, S, Hq, Hkv, D, page, max_pages, topk))
+
+
 def lidx_cache_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, q_pos=None, compress_ratio=1,
                     topk_indices=None, softmax_scale=None, want_lse=False, stream=None, out=None,
                     workspace=None):
@@ -917,7 +924,10 @@ def _cache_attn(call, q, shape, qs, dev, cache, Hkv, page, MP, pages, kv_len, q_
             lse = _new(shape[:3], _f32, q.device, stream)
     L = _lib or lib()
     if workspace is None:
-        ws_bytes = L.lidx_cache_attn_workspace_bytes(B, S, Hq, Hkv, D, topk)
+        if len(cache) == 5:
+            ws_bytes = L.lidx_cache_attn_workspace_bytes(B, S, Hq, Hkv, D, topk)
+        else:
+            ws_bytes = L.lidx_cache4_attn_workspace_bytes(B, S, Hq, Hkv, D, page, MP, topk)
         workspace = _scratch(ws_bytes, q.device, stream)
     else:
         ws_bytes = _dense(workspace, "workspace", torch.uint8, (None,), dev)[0]

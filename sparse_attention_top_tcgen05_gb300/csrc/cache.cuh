@@ -66,6 +66,13 @@ __device__ __forceinline__ uint2 cache4_widen(uint32_t w, uint32_t lo, uint32_t 
     const uint32_t a = prmt(lo, hi, m), b = prmt(lo, hi, m >> 16);
     return make_uint2(a | (prmt(u, w, 0xd9c8u) & 0x80808080u), b | (prmt(u, w, 0xfbeau) & 0x80808080u));
 }
+// The same with shifts that are products (by 16 and, the upper half, 2^16), for loops that the integer pipe bounds: products
+// go to another.  The factors are registers that the compiler knows nothing of.
+__device__ __forceinline__ uint2 cache4_widen_mul(uint32_t w, uint32_t lo, uint32_t hi, uint32_t f16, uint32_t f65536) {
+    const uint32_t m = w & 0x77777777u, u = w * f16;
+    const uint32_t a = prmt(lo, hi, m), b = prmt(lo, hi, __umulhi(m, f65536));
+    return make_uint2(a | (prmt(u, w, 0xd9c8u) & 0x80808080u), b | (prmt(u, w, 0xfbeau) & 0x80808080u));
+}
 // Two floats -> two codes (lo in the low bits); rounds to nearest even, saturates at +-6.
 __device__ __forceinline__ uint32_t e2m1x2_from(float lo, float hi) {
     uint32_t r;

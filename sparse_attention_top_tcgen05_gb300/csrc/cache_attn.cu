@@ -149,6 +149,22 @@ static cudaError_t attn_join(const AttnParams& p, int grid, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<N>, p, grid, W);
 }
 
+static size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+// 4 bits: whether a call widens the sequences' pages first (see cache4_attn.cu), and into how many bytes.  A tile costs an SM
+// about 2.6 us where a kernel of 128 rows widens it and 1.25 us where it is widened already; to write and read the copy costs
+// it 1.1 us once (chunk of 2048 queries over 16384 keys, 128 units a key: 2.1 ms and 1.0 ms).  So two units a key, or two
+// selections of it on average, are enough.  kCopyMost: a copy beyond that is taken for too much memory.
+constexpr size_t kCopyMost = (size_t)2 << 30;
+static size_t attn4_copy_bytes(int64_t B, int64_t S, int G, int Hkv, int D, int page, int64_t max_pages, int topk) {
+    const int64_t keys = max_pages * page;
+    if (topk > 0 ? S * topk < 2 * keys : S * G <= 128) return 0;
+    if (B * max_pages > INT_MAX / page / Hkv) return 0;  // as num_pages
+    const size_t pages = (size_t)(B * max_pages), bytes = 2 * pages * Hkv * page * D;
+    if (bytes > kCopyMost) return 0;
+    return round256(bytes) + round256(2 * pages * Hkv * sizeof(float)) + round256(pages * sizeof(int32_t));
+}
+
 // Both entries; bits 8: exps NULL.
 static int attn_call(int bits, const void* q, const int64_t* qs, const void* k_cache, const void* v_cache,
                     const int32_t* k_exps, const int32_t* v_exps,
@@ -165,9 +181,10 @@ static int attn_call(int bits, const void* q, const int64_t* qs, const void* k_c
     if (Hq < 1 || Hq % Hkv || Hq / Hkv > 128 || B * S > INT_MAX || B * S * Hq > INT_MAX) return LIDX_ERR_SHAPE;
     if (compress_ratio < 1 || !isfinite(softmax_scale) || (topk_indices && (topk < 1 || topk > (1 << 20))))
         return LIDX_ERR_SHAPE;
-    if (((uintptr_t)q | (uintptr_t)k_cache | (uintptr_t)v_cache | (uintptr_t)out) & 15u) return LIDX_ERR_ALIGN;
+    if (((uintptr_t)q | (uintptr_t)k_cache | (uintptr_t)v_cache | (uintptr_t)out | (uintptr_t)k_exps | (uintptr_t)v_exps) & 15u)
+        return LIDX_ERR_ALIGN;
     if (((uintptr_t)k_scale | (uintptr_t)v_scale | (uintptr_t)block_table | (uintptr_t)kv_len |
-         (uintptr_t)q_pos | (uintptr_t)topk_indices | (uintptr_t)lse | (uintptr_t)k_exps | (uintptr_t)v_exps) & 3u)
+         (uintptr_t)q_pos | (uintptr_t)topk_indices | (uintptr_t)lse) & 3u)
         return LIDX_ERR_ALIGN;
     if ((qs[0] | qs[1] | qs[2]) & 7) return LIDX_ERR_ALIGN;
     const int sms = sm103_sms();
@@ -208,20 +225,44 @@ static int attn_call(int bits, const void* q, const int64_t* qs, const void* k_c
     const int64_t most = tiles * B * p.ST * Hkv;
     const int grid = most < sms ? (int)most : sms;
     p.by_unit = B * p.ST * Hkv <= grid;
-    const size_t need = attn_ws_bytes(N, grid);
+    const size_t copy = bits == 4 ? attn4_copy_bytes(B, S, p.G, Hkv, D, page, max_pages, topk_indices ? topk : 0) : 0;
+    const size_t need = copy + attn_ws_bytes(N, grid);
     if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u)) return LIDX_ERR_WORKSPACE;
-    p.ws = (uint8_t*)workspace;
+    p.ws = (uint8_t*)workspace + copy;
     p.codes[0] = (const uint8_t*)k_cache;
     p.codes[1] = (const uint8_t*)v_cache;
     p.exps[0] = k_exps;
     p.exps[1] = v_exps;
     CUtensorMap mk, mv;
     const int box = topk_indices ? 1 : page;  // rows of a copy
-    if (bits == 8 && (attn_cache_map(&mk, k_cache, num_pages * Hkv * page, D, box) ||
-                      attn_cache_map(&mv, v_cache, num_pages * Hkv * page, D, box)))
+    Attn4Copy to;
+    if (copy) {
+        const int64_t pages = B * max_pages;
+        uint8_t* at = (uint8_t*)workspace;
+        to.cache[0] = at;
+        to.cache[1] = at + pages * Hkv * page * D;
+        at += round256((size_t)2 * pages * Hkv * page * D);
+        to.scale[0] = (float*)at;
+        to.scale[1] = to.scale[0] + pages * Hkv;
+        to.table = (int32_t*)(at + round256((size_t)2 * pages * Hkv * sizeof(float)));
+        k_cache = to.cache[0];
+        v_cache = to.cache[1];
+        num_pages = pages;
+    }
+    if ((bits == 8 || copy) && (attn_cache_map(&mk, k_cache, num_pages * Hkv * page, D, box) ||
+                                attn_cache_map(&mv, v_cache, num_pages * Hkv * page, D, box)))
         return LIDX_ERR_CUDA;
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
+    if (copy) {
+        e = attn4_widen_pages(p, to, st);
+        if (e != cudaSuccess) return LIDX_ERR_CUDA;
+        p.ks = to.scale[0];
+        p.vs = to.scale[1];
+        p.table = to.table;
+        p.num_pages = num_pages;
+        bits = 8;
+    }
     if (bits == 4)
         e = N <= 32 ? attn4_launch(N, p, grid, st) : attn4_launch_wide(p, grid, st);
     else if (N == 16)
@@ -250,6 +291,12 @@ size_t lidx_cache_attn_workspace_bytes(int64_t B, int64_t S, int Hq, int Hkv, in
     int sms = sm103_sms();
     if (sms <= 0) sms = 256;  // no device: an upper bound
     return attn_ws_bytes(attn_columns(S, Hq / Hkv, topk > 0), sms);
+}
+
+size_t lidx_cache4_attn_workspace_bytes(int64_t B, int64_t S, int Hq, int Hkv, int D, int page, int64_t max_pages, int topk) {
+    if (check_cache(B, S, Hkv, D, page, max_pages, 1) || topk < 0) return 0;
+    const size_t parts = lidx_cache_attn_workspace_bytes(B, S, Hq, Hkv, D, topk);
+    return parts ? parts + attn4_copy_bytes(B, S, Hq / Hkv, Hkv, D, page, max_pages, topk) : 0;
 }
 
 int lidx_cache_attn(const void* q, const int64_t* qs, const void* k_cache, const void* v_cache,

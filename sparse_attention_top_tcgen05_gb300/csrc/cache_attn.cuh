@@ -44,8 +44,8 @@ struct AttnParams {
 constexpr int kATile = 128;                     // keys of a tile
 constexpr int kASlotBytes = kATile * 128;       // one K or V tile: 128 bytes a key (zero past D)
 constexpr int kAMeta = 6;                       // stages of per-key scales
-constexpr int kAKeys4 = 64;                     // 4 bits: keys of a producer warp, half a tile
-constexpr int kAStage4 = kAKeys4 * 2 * (64 + 4);  // its packed keys and values and their exponents
+// 4 bits: a packed K or V tile is its rows' codes, D / 2 bytes each, then their exponents, then bits of the rows that are seen
+constexpr int kAPackedExps = kATile * 64, kAPackedSeen = kAPackedExps + kATile * 4, kAPackedBytes = kAPackedSeen + 16;
 constexpr float kATop = 8.f;                    // weights are scaled to 2^8
 constexpr float kALn2 = 0.693147180559945309f;
 // Smallest value scale.  A row's sum adds weights of at most 2^8.3 divided by their value scales: 2^30 keys of this one stay
@@ -161,6 +161,18 @@ __device__ __forceinline__ void split_e4m3(float x0, float x1, uint32_t& hi, uin
 }
 
 
+// Slots of the tiles that the products read.  8 bits: K and V tiles share SLOTS slots in turn, as they are loaded.  4 bits: K
+// tiles have KS slots, V tiles VS behind them: a V tile is held until its O is done, two tiles after its S.
+template <int BITS, int KS, int VS>
+struct AttnSlots {
+    static constexpr int ALL = KS + VS;
+    static_assert(BITS == 4 || KS == VS, "in turn");
+    static __device__ __forceinline__ int at(int t, int which) {
+        return BITS == 8 ? (2 * t + which) % ALL : (which ? KS + t % VS : t % KS);
+    }
+    static __device__ __forceinline__ int phase(int t, int which) { return (which ? t / VS : t / KS) & 1; }
+};
+
 // One pipeline of a CTA in shared memory.
 struct AttnPipe {
     uint8_t* kv;            // [SLOTS] K or V tiles, in turn
@@ -171,8 +183,10 @@ struct AttnPipe {
     float* key_iv;          // [kAMeta][128] its inverse
     uint32_t* seen;         // [kAMeta][4] bits of the keys that are seen
     uint32_t* flag;         // [kAMeta] not 0: a key of the tile is not seen
-    int* rows;              // [PRODUCERS][128] cache rows of gathered keys (4 bits: [PRODUCERS][kAKeys4])
-    uint8_t* stage;         // 4 bits: [PRODUCERS][kAStage4]
+    int* rows;              // [PRODUCERS][128] cache rows of gathered keys
+    uint8_t* packed;        // 4 bits: [PACKED][kAPackedBytes] K or V tiles, in turn
+    uint64_t *pk_full;      // [PACKED] packed K or V tile landed
+    uint64_t *pk_empty;     // [PACKED] it is widened
     uint64_t *kv_full;      // [SLOTS] K or V tile landed
     uint64_t *kv_empty;     // [SLOTS] its product is done
     uint64_t *meta_full;    // [kAMeta] what belongs to a tile's keys is written
@@ -438,16 +452,12 @@ __device__ __forceinline__ void attn_produce(const AttnParams& p, AttnWalk& wk, 
     }
 }
 
-// The same over a cache of 4-bit numbers: warp pw, two warps a tile, TL tiles in turn.  A warp copies the packed rows of its 64
-// keys into a stage of its own, asynchronously and a tile ahead, and widens them to the e4m3 codes of code * 2^x / 32 in
-// the layout that the 8-bit cache's tiles have, so that all that follows is the same.  Keys that no row of the unit sees (and
-// dims past the head) are written as zeros.
-template <int SLOTS, int TL, bool SEL>
+// 4 bits: loads packed keys and values, warp pw of PRODUCERS, which take the tiles in turn.  Pages come as bulk copies, selected
+// keys as copies of the lanes.
+template <int PACKED, int PRODUCERS, bool SEL>
 __device__ __forceinline__ void attn_produce4(const AttnParams& p, AttnWalk& wk, const AttnPipe& x, int pw, int lane) {
-    const int turn = pw >> 1, half = pw & 1;
-    uint8_t* const stage = x.stage + pw * kAStage4;
-    int* const rows = x.rows + pw * kAKeys4;
     bool ok = !p.debug_stall;
+    int last = -1;  // the last packed tile that was asked for
     struct Ref {
         bool live;
         int b, h, tile, limit;
@@ -465,7 +475,7 @@ __device__ __forceinline__ void attn_produce4(const AttnParams& p, AttnWalk& wk,
                 continue;
             }
             // on to the first tile of this segment that is the warp's
-            const int skip = (turn - count % TL + TL) % TL, left = wk.t1 - tile;
+            const int skip = (pw - count % PRODUCERS + PRODUCERS) % PRODUCERS, left = wk.t1 - tile;
             if (skip >= left) {
                 count += left;
                 tile = wk.t1;
@@ -481,156 +491,263 @@ __device__ __forceinline__ void attn_produce4(const AttnParams& p, AttnWalk& wk,
         }
         return r;
     };
-    const int page_mask = p.page - 1;
-    // a lane has keys lane and lane + 32 of the warp's 64
-    auto keys = [&](const Ref& r, int (&t)[2]) {
+    const int page_mask = p.page - 1, pitch = p.D / 2;
+    const float unit = kCache4Unit * p.scale_log2;
+    auto claim = [&](int seq) {
+        ok = ok && mbar_wait(x.pk_empty + seq % PACKED, ((seq / PACKED) & 1) ^ 1, p.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+    };
+    auto claim_meta = [&](int tc) {
+        ok = ok && mbar_wait(x.meta_empty + tc % kAMeta, ((tc / kAMeta) & 1) ^ 1, p.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+    };
+    if constexpr (!SEL) {
+        // A lane has four keys, which share a page; the lane with a page's first key loads it.
+        auto page_id = [&](const Ref& r) {
+            const int k0 = r.tile * kATile + 4 * lane;
+            return r.live && k0 < r.limit ? p.table[(int64_t)r.b * p.max_pages + (k0 >> p.page_shift)] : -1;
+        };
+        Ref r0 = next_ref();
+        int pid0 = page_id(r0);
+        Ref r1 = next_ref();
+        while (ok && r0.live) {
+            const bool good = pid0 >= 0 && pid0 < p.num_pages;
+            const int cell = (good ? pid0 : 0) * p.Hkv + r0.h;  // num_pages * Hkv * page < 2^31
+            const float a = p.ks[cell], v = p.vs[cell];
+            const int pid1 = page_id(r1);
+            const Ref r2 = next_ref();
+            const int tc = r0.tc, ms = tc % kAMeta;
+            const bool lead = good && ((4 * lane) & page_mask) == 0;
+            const uint32_t pages = __popc(__ballot_sync(0xffffffffu, lead)), codes = (uint32_t)pitch << p.page_shift;
+            const int row = cell << p.page_shift;
+            const int left = good ? r0.limit - (r0.tile * kATile + 4 * lane) : 0;  // keys of the lane that count
+            uint32_t seen = (left > 3 ? 15u : (left > 0 ? (1u << left) - 1 : 0u)) << (4 * (lane & 7));
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int k = r.tile * kATile + kAKeys4 * half + 32 * i + lane;
-            if constexpr (SEL)
-                t[i] = r.live && k < p.topk ? p.idx[r.row * p.topk + k] : -1;
-            else
-                t[i] = r.live ? k : -1;
+            for (int i = 1; i < 8; i <<= 1) seen |= __shfl_xor_sync(0xffffffffu, seen, i);
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
+                const int seq = 2 * tc + which;
+                claim(seq);
+                if (!ok) break;
+                uint8_t* const to = x.packed + seq % PACKED * kAPackedBytes;
+                uint64_t* const bar = x.pk_full + seq % PACKED;
+                if ((lane & 7) == 0) reinterpret_cast<uint32_t*>(to + kAPackedSeen)[lane >> 3] = seen;
+                __syncwarp();
+                if (lane == 0) mbar_arrive_expect_tx(bar, pages * (codes + (4u << p.page_shift)));
+                __syncwarp();
+                if (lead) {
+                    bulk_load(to + 4 * lane * pitch, p.codes[which] + (int64_t)row * pitch, codes, bar);
+                    bulk_load(to + kAPackedExps + 16 * lane, p.exps[which] + row, 4u << p.page_shift, bar);
+                }
+                last = seq;
+            }
+            if (!ok) break;
+            claim_meta(tc);
+            if (!ok) break;
+            const float f = a * unit, y = __log2f(fmaxf(v * kCache4Unit, kAMinScale)), iv = exp2_approx(-y);
+            const float none = -INFINITY;
+            const int at = ms * kATile + 4 * lane;
+            *reinterpret_cast<float4*>(x.key_a + at) = make_float4(f, f, f, f);
+            *reinterpret_cast<float4*>(x.key_lv + at) = make_float4(left > 0 ? y : none, left > 1 ? y : none,
+                                                                    left > 2 ? y : none, left > 3 ? y : none);
+            *reinterpret_cast<float4*>(x.key_iv + at) = make_float4(iv, iv, iv, iv);
+            if ((lane & 7) == 0) x.seen[ms * 4 + (lane >> 3)] = seen;
+            const bool all = __all_sync(0xffffffffu, left > 3);
+            if (lane == 0) x.flag[ms] = all ? 0 : 1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(x.meta_full + ms);
+            r0 = r1;
+            r1 = r2;
+            pid0 = pid1;
         }
-    };
-    auto pages = [&](const Ref& r, const int (&t)[2], int (&pid)[2]) {
-        const int32_t* tab = p.table + (int64_t)r.b * p.max_pages;
+        // loads in flight end before the memory is given up
+        if (!ok)
+            for (int seq = max(0, last - PACKED + 1); seq <= last; ++seq)
+                if ((seq >> 1) % PRODUCERS == pw) mbar_wait(x.pk_full + seq % PACKED, (seq / PACKED) & 1, p.wait_ns);
+    } else {
+        // A lane has a key of each quarter of the tile.  Keys that are not seen are not loaded.
+        auto keys = [&](const Ref& r, int (&t)[4]) {
+            const int32_t* src = p.idx + r.row * p.topk;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) pid[i] = t[i] >= 0 && t[i] < r.limit ? tab[t[i] >> p.page_shift] : -1;
-    };
-    float a[2], v[2];
-    uint32_t seen[2];
-    // scales and rows of a tile's keys; bits of the keys that are seen
-    auto lookup = [&](const Ref& r, const int (&t)[2], const int (&pid)[2], float (&a)[2], float (&v)[2], uint32_t (&seen)[2]) {
+            for (int i = 0; i < 4; ++i) {
+                const int k = r.tile * kATile + 32 * i + lane;
+                t[i] = r.live && k < p.topk ? src[k] : -1;
+            }
+        };
+        auto pages = [&](const Ref& r, const int (&t)[4], int (&pid)[4]) {
+            const int32_t* tab = p.table + (int64_t)r.b * p.max_pages;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const bool good = pid[i] >= 0 && pid[i] < p.num_pages;
-            const int cell = (good ? pid[i] : 0) * p.Hkv + r.h;  // num_pages * Hkv * page < 2^31
-            a[i] = p.ks[cell];
-            v[i] = p.vs[cell];
-            rows[32 * i + lane] = good ? (cell << p.page_shift) + (t[i] & page_mask) : -1;
-            seen[i] = __ballot_sync(0xffffffffu, good);
-        }
-        __syncwarp();
-    };
-    // A row is copied in units of 16 bytes, or of 8 where D / 2 is no multiple of 16; lanes of a row: 2^us
-    const bool wide = p.D % 32 == 0;
-    const int units = wide ? p.D / 32 : p.D / 16, us = units <= 1 ? 0 : (units <= 2 ? 1 : (units <= 4 ? 2 : 3));
-    const int cs = p.D <= 32 ? 0 : (p.D <= 64 ? 1 : 2);  // lanes of a row, 32 dims each: 2^cs
-    const int pitch = 16 << cs;
-    const uint32_t stage_u = smem_u32(stage);
-    auto copy = [&](int which) {
-        const uint8_t* const src = p.codes[which];
-        const uint32_t to = stage_u + which * (kAKeys4 * 64);
+            for (int i = 0; i < 4; ++i) pid[i] = t[i] >= 0 && t[i] < r.limit ? tab[t[i] >> p.page_shift] : -1;
+        };
+        int* const rows = x.rows + kATile * pw;
+        // a row is copied in units of 16 bytes, or of 8 where its size is no multiple of 16; 2^us lanes a row
+        const bool by16 = pitch % 16 == 0;
+        const int units = by16 ? pitch / 16 : pitch / 8, us = units <= 1 ? 0 : (units <= 2 ? 1 : (units <= 4 ? 2 : 3));
         const int u = lane & ((1 << us) - 1);
+        Ref r0 = next_ref();
+        int t0[4], t1[4], t2[4], pid0[4], pid1[4];
+        keys(r0, t0);
+        Ref r1 = next_ref();
+        keys(r1, t1);
+        pages(r0, t0, pid0);
+        while (ok && r0.live) {
+            float a[4], v[4];
+            uint32_t seen[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool good = pid0[i] >= 0 && pid0[i] < p.num_pages;
+                const int cell = (good ? pid0[i] : 0) * p.Hkv + r0.h;
+                a[i] = p.ks[cell];
+                v[i] = p.vs[cell];
+                rows[32 * i + lane] = good ? (cell << p.page_shift) + (t0[i] & page_mask) : -1;
+                seen[i] = __ballot_sync(0xffffffffu, good);
+            }
+            pages(r1, t1, pid1);
+            const Ref r2 = next_ref();
+            keys(r2, t2);
+            __syncwarp();
+            const int tc = r0.tc, ms = tc % kAMeta;
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
+                const int seq = 2 * tc + which;
+                claim(seq);
+                if (!ok) break;
+                uint8_t* const to = x.packed + seq % PACKED * kAPackedBytes;
+                uint64_t* const bar = x.pk_full + seq % PACKED;
+                const uint32_t to_u = smem_u32(to);
+                if (lane == 0) *reinterpret_cast<uint4*>(to + kAPackedSeen) = make_uint4(seen[0], seen[1], seen[2], seen[3]);
 #pragma unroll 4
-        for (int r0 = 0; r0 < kAKeys4; r0 += 32 >> us) {
-            const int r = r0 + (lane >> us), row = rows[r];
-            if (row >= 0 && u < units) {
-                if (wide)
-                    cp_async16(to + r * pitch + u * 16, src + (int64_t)row * (p.D / 2) + u * 16);
-                else
-                    cp_async8(to + r * pitch + u * 8, src + (int64_t)row * (p.D / 2) + u * 8);
+                for (int k0 = 0; k0 < kATile; k0 += 32 >> us) {
+                    const int k = k0 + (lane >> us), row = rows[k];
+                    if (row >= 0 && u < units) {
+                        if (by16)
+                            cp_async16(to_u + k * pitch + u * 16, p.codes[which] + (int64_t)row * pitch + u * 16);
+                        else
+                            cp_async8(to_u + k * pitch + u * 8, p.codes[which] + (int64_t)row * pitch + u * 8);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = rows[32 * i + lane];
+                    if (row >= 0) cp_async4(to_u + kAPackedExps + (32 * i + lane) * 4, p.exps[which] + row);
+                }
+                cp_async_arrive(bar);
+                if (lane == 0) mbar_arrive(bar);  // the bits are written
+            }
+            if (!ok) break;
+            claim_meta(tc);
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool good = (seen[i] >> lane) & 1;
+                const int at = ms * kATile + 32 * i + lane;
+                const float y = __log2f(fmaxf(v[i] * kCache4Unit, kAMinScale));
+                x.key_a[at] = good ? a[i] * unit : 0.f;
+                x.key_lv[at] = good ? y : -INFINITY;
+                x.key_iv[at] = exp2_approx(-y);
+                if (lane == 0) {
+                    x.seen[ms * 4 + i] = seen[i];
+                    reinterpret_cast<uint8_t*>(x.flag + ms)[i] = seen[i] == 0xffffffffu ? 0 : 1;
+                }
+            }
+            __syncwarp();  // (and the rows are read)
+            if (lane == 0) mbar_arrive(x.meta_full + ms);
+            r0 = r1;
+            r1 = r2;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                t0[i] = t1[i];
+                t1[i] = t2[i];
+                pid0[i] = pid1[i];
             }
         }
+        cp_async_wait_all();  // copies in flight end before the memory is given up
+    }
+}
+
+// 4 bits: widens packed tiles to the e4m3 codes of code * 2^x / 32, in the layout that the 8-bit cache's tiles have, so that
+// all that follows is the same.  Four warps share a tile, warp q its rows [32 q, 32 q + 32); first, STEP: which of the K
+// and V tiles in turn they take.  Rows that are not seen, and dims past the head that a product reads, are written as zeros.
+template <class RING, int PACKED, int STEP>
+__device__ __forceinline__ void attn_widen(const AttnParams& p, AttnWalk& wk, const AttnPipe& x, int first, int q, int lane) {
+    bool ok = true;
+    int tiles = 0;
+    while (wk.next(p))
+        if (wk.gr.n > 0) tiles += wk.t1 - wk.t0;
+    const int pitch = p.D / 2, cs = p.D <= 32 ? 0 : (p.D <= 64 ? 1 : 2);  // 32 dims a lane, 2^cs lanes a row
+    const int c = lane & ((1 << cs) - 1), k0 = lane >> cs;
+    uint32_t f16 = 16, f65536 = 65536;
+    asm volatile("" : "+r"(f16), "+r"(f65536));
+    for (int seq = first; seq < 2 * tiles; seq += STEP) {
+        const int pk = seq % PACKED, sl = RING::at(seq >> 1, seq & 1);
+        ok = ok && mbar_wait(x.pk_full + pk, (seq / PACKED) & 1, p.wait_ns);
+        const uint32_t from = smem_u32(x.packed) + pk * kAPackedBytes, to = smem_u32(x.kv) + sl * kASlotBytes;
+        const uint32_t seen = lds32(from + kAPackedSeen + 4 * q);
+        const uint32_t src = from + (32 * q + k0) * pitch + c * 16, ex = from + kAPackedExps + (32 * q + k0) * 4;
+        bool whole = p.D == 128 && seen == 0xffffffffu;
+        uint32_t e[4];
+        uint4 w[4];
+        if (whole) {  // (read before the slot is awaited)
+            uint32_t bad = 0;  // exponents of 12 and more
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row = rows[32 * i + lane];
-            if (row >= 0)
-                cp_async4(stage_u + 2 * (kAKeys4 * 64) + which * (kAKeys4 * 4) + (32 * i + lane) * 4, p.exps[which] + row);
+            for (int i = 0; i < 4; ++i) e[i] = lds32(ex + i * 32);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = lds128(src + i * 512);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) bad |= e[i] & (e[i] << 1);
+            whole = !__any_sync(0xffffffffu, bad & 0x88888888u);
         }
-        cp_async_commit();
-    };
-    auto widen = [&](int which, uint8_t* tile_at, const uint32_t (&seen)[2]) {
-        cp_async_wait<1>();
-        __syncwarp();
-        const uint8_t* const from = stage + which * (kAKeys4 * 64);
-        const uint32_t* const ex = reinterpret_cast<const uint32_t*>(stage + 2 * (kAKeys4 * 64) + which * (kAKeys4 * 4));
-        const int c = lane & ((1 << cs) - 1);
-        const bool some = 32 * c < p.D, both = 32 * c + 16 < p.D;
-        if (some) {
-#pragma unroll 4
-            for (int r0 = 0; r0 < kAKeys4; r0 += 32 >> cs) {
-                const int r = r0 + (lane >> cs);
-                uint4 w = *reinterpret_cast<const uint4*>(from + r * pitch + c * 16);
-                uint32_t e = ex[r] >> (8 * c);
-                if (!((seen[r >> 5] >> (r & 31)) & 1)) w = make_uint4(0, 0, 0, 0), e = 0;
-                if (!both) w.z = w.w = 0, e &= 15u;
-                uint32_t lo, hi;
-                cache4_table(e & 15u, lo, hi);
-                const uint2 w0 = cache4_widen(w.x, lo, hi), w1 = cache4_widen(w.y, lo, hi);
-                cache4_table((e >> 4) & 15u, lo, hi);
-                const uint2 w2 = cache4_widen(w.z, lo, hi), w3 = cache4_widen(w.w, lo, hi);
-                uint8_t* const at = tile_at + (kAKeys4 * half + r) * 128;
-                const int j = 2 * c;
-                *reinterpret_cast<uint4*>(at + ((j ^ (r & 7)) << 4)) = make_uint4(w0.x, w0.y, w1.x, w1.y);
-                *reinterpret_cast<uint4*>(at + (((j + 1) ^ (r & 7)) << 4)) = make_uint4(w2.x, w2.y, w3.x, w3.y);
+        ok = ok && mbar_wait(x.kv_empty + sl, RING::phase(seq >> 1, seq & 1) ^ 1, p.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (whole) {
+            // whole rows of numbers that are all seen: four lanes a row; a lane's place in the swizzle does not change
+            const uint32_t dst = to + (32 * q + k0) * 128;
+            const uint32_t dst0 = dst + (((2 * c) ^ k0) << 4), dst1 = dst + (((2 * c + 1) ^ k0) << 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t x01 = prmt(e[i], 0, 0x4440u + c), x0 = x01 & 15u, x1 = x01 >> 4;  // byte c
+                uint32_t lo = x0 * 0x08080800u + 0x14100800u, hi = x0 * 0x08080808u + 0x24201c18u;
+                const uint2 w0 = cache4_widen_mul(w[i].x, lo, hi, f16, f65536);
+                const uint2 w1 = cache4_widen_mul(w[i].y, lo, hi, f16, f65536);
+                lo = x1 * 0x08080800u + 0x14100800u, hi = x1 * 0x08080808u + 0x24201c18u;
+                const uint2 w2 = cache4_widen_mul(w[i].z, lo, hi, f16, f65536);
+                const uint2 w3 = cache4_widen_mul(w[i].w, lo, hi, f16, f65536);
+                sts128(dst0 + i * 1024, make_uint4(w0.x, w0.y, w1.x, w1.y));
+                sts128(dst1 + i * 1024, make_uint4(w2.x, w2.y, w3.x, w3.y));
+            }
+        } else if (32 * c < p.D) {
+            const bool both = 32 * c + 16 < p.D;
+#pragma unroll 1
+            for (int i = 0; i < 32; i += 32 >> cs) {
+                const int k = i + k0, r = 32 * q + k;
+                uint2 a = make_uint2(0, 0), b = a;
+                uint32_t x0 = 0, x1 = 0, lo, hi;
+                if ((seen >> k) & 1) {
+                    const uint32_t x = lds32(ex + i * 4) >> (8 * c);
+                    a = lds64(src + i * pitch);
+                    x0 = x & 15u;
+                    if (both) {
+                        b = lds64(src + i * pitch + 8);
+                        x1 = (x >> 4) & 15u;
+                    }
+                }
+                cache4_table(x0, lo, hi);
+                const uint2 w0 = cache4_widen(a.x, lo, hi), w1 = cache4_widen(a.y, lo, hi);
+                cache4_table(x1, lo, hi);
+                const uint2 w2 = cache4_widen(b.x, lo, hi), w3 = cache4_widen(b.y, lo, hi);
+                const uint32_t dst = to + r * 128;
+                sts128(dst + (((2 * c) ^ (r & 7)) << 4), make_uint4(w0.x, w0.y, w1.x, w1.y));
+                sts128(dst + (((2 * c + 1) ^ (r & 7)) << 4), make_uint4(w2.x, w2.y, w3.x, w3.y));
             }
         }
         fence_async_smem();
         __syncwarp();
-    };
-    // waits for the slot of tile tc's K (which = 0) or V
-    auto claim = [&](int tc, int which) {
-        const int seq = 2 * tc + which;
-        ok = ok && mbar_wait(x.kv_empty + seq % SLOTS, ((seq / SLOTS) & 1) ^ 1, p.wait_ns);
-        if (which == 0) ok = ok && mbar_wait(x.meta_empty + tc % kAMeta, ((tc / kAMeta) & 1) ^ 1, p.wait_ns);
-        ok = __all_sync(0xffffffffu, ok);
-    };
-    // Steps ahead: indices of the warp's tile after next, page ids and then rows of its next, so that a step waits for one
-    // memory latency at most.
-    Ref r0 = next_ref();
-    int t1[2], t2[2], pid1[2];
-    keys(r0, t1);
-    pages(r0, t1, pid1);
-    lookup(r0, t1, pid1, a, v, seen);
-    if (ok) {
-        copy(0);
-        copy(1);
-    }
-    Ref r1 = next_ref();
-    keys(r1, t1);
-    Ref r2 = next_ref();
-    keys(r2, t2);
-    pages(r1, t1, pid1);
-    while (ok && r0.live) {
-        const int tc = r0.tc, sk = 2 * tc, ms = tc % kAMeta, s0 = sk % SLOTS, s1 = (sk + 1) % SLOTS;
-        claim(tc, 0);
-        if (!ok) break;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const bool good = (seen[i] >> lane) & 1;
-            const int at = ms * kATile + kAKeys4 * half + 32 * i + lane;
-            const float y = __log2f(fmaxf(v[i] * kCache4Unit, kAMinScale));
-            x.key_a[at] = good || !SEL ? a[i] * (kCache4Unit * p.scale_log2) : 0.f;
-            x.key_lv[at] = good ? y : -INFINITY;
-            x.key_iv[at] = exp2_approx(-y);
-            if (lane == 0) {
-                x.seen[ms * 4 + 2 * half + i] = seen[i];
-                reinterpret_cast<uint8_t*>(x.flag + ms)[2 * half + i] = seen[i] == 0xffffffffu ? 0 : 1;
-            }
+        if (lane == 0) {
+            mbar_arrive(x.pk_empty + pk);
+            mbar_arrive(x.kv_full + sl);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(x.meta_full + ms);
-        widen(0, x.kv + s0 * kASlotBytes, seen);
-        if (lane == 0) mbar_arrive(x.kv_full + s0);
-        const uint32_t now[2] = {seen[0], seen[1]};
-        lookup(r1, t1, pid1, a, v, seen);
-        copy(0);
-        pages(r2, t2, pid1);
-        const Ref r3 = next_ref();
-        t1[0] = t2[0], t1[1] = t2[1];
-        keys(r3, t2);
-        claim(tc, 1);
-        if (!ok) break;
-        widen(1, x.kv + s1 * kASlotBytes, now);
-        if (lane == 0) mbar_arrive(x.kv_full + s1);
-        copy(1);
-        r0 = r1;
-        r1 = r2;
-        r2 = r3;
     }
-    cp_async_wait<0>();  // copies in flight end before the memory is given up
 }
 
 // Query rows of a unit, bf16 -> e4m3 hi and lo: one of QWARPS warps.  twice: rows 0 .. 63 are repeated as 64 .. 127.
@@ -712,6 +829,14 @@ __device__ __forceinline__ void attn_queries(const AttnParams& p, AttnWalk& wk, 
 // the parts of any are joined by one kernel.
 cudaError_t attn4_launch(int N, const AttnParams& p, int grid, cudaStream_t st);
 cudaError_t attn4_launch_wide(const AttnParams& p, int grid, cudaStream_t st);
+
+// 4 bits, many rows for each key: the sequences' pages are widened once into an 8-bit cache in the workspace.
+struct Attn4Copy {
+    uint8_t* cache[2];  // e4m3 [B max_pages, Hkv, page, D]
+    float* scale[2];    // [B max_pages, Hkv]
+    int32_t* table;     // [B, max_pages]: pages of the copy, -1 where the cache's page id is out of range
+};
+cudaError_t attn4_widen_pages(const AttnParams& p, const Attn4Copy& to, cudaStream_t st);
 cudaError_t attn_launch_wide(const CUtensorMap& mk, const CUtensorMap& mv, const AttnParams& p, int grid, cudaStream_t st);
 
 }  // namespace lidx

@@ -5,7 +5,11 @@
 
 namespace lidx {
 
-// Configuration of the kernel with N columns, N = 16 or 32, of which a softmax thread has NC, over a cache of BITS bits.
+// Configuration of the kernel with room for N rows, N = 16 or 32, of which a softmax thread has NC, over a cache of BITS bits.
+//
+// The products' columns are the rows' hi and lo parts.  8 bits: a product for the hi part and one for the lo part into the
+// same columns.  4 bits, where reading K and V out of shared memory is what bounds the kernel: one product of twice the
+// columns, which reads them once; whoever reads its columns adds the two.
 template <int N, int NC_, int BITS>
 struct AttnCfg {
     static_assert((N == 16 && (NC_ == 8 || NC_ == 16)) || (N == 32 && NC_ == 16), "columns");
@@ -13,16 +17,19 @@ struct AttnCfg {
     // tile's columns: a thread keeps its scores and sums in registers either way.
     static constexpr bool SPLIT = N == 32;
     static constexpr int COLS = SPLIT ? N : NC_;       // columns that hold rows
-    static constexpr int SG = 2, NC = NC_, QB = 2, SLOTS = BITS == 8 ? 8 : 6;
-    static constexpr int Q_BYTES = 2 * N * 128;        // hi and lo
-    // Weights, a key 128 bytes, two buffers of hi and lo: each in a tile of its own, or (4 bits, whose packed tiles need the
-    // room) side by side in the 16-byte chunks of one
-    static constexpr int P_HALF = BITS == 8 ? kASlotBytes : N, P_BYTES = 2 * P_HALF;
+    static constexpr int SG = 2, NC = NC_, QB = 2;
+    using RING = AttnSlots<BITS, BITS == 8 ? 4 : 2, BITS == 8 ? 4 : 3>;
+    static constexpr int SLOTS = RING::ALL, PACKED = BITS == 8 ? 0 : 11;
+    static constexpr int MN = BITS == 8 ? N : 2 * COLS;  // columns of a product
+    static constexpr int Q_BYTES = 2 * COLS * 128;     // hi and lo
+    // Weights, a key 128 bytes, two buffers: 8 bits, hi and lo in a tile each; 4 bits, whose packed tiles need the room, hi
+    // and lo columns of both buffers beside each other in one tile
+    static constexpr int P_BYTES = BITS == 8 ? 2 * kASlotBytes : MN;
     static constexpr int OFF_P = SLOTS * kASlotBytes;
     static constexpr int OFF_Q = OFF_P + (BITS == 8 ? 2 * P_BYTES : kASlotBytes);
     static constexpr int OFF_META = OFF_Q + QB * Q_BYTES;              // [3][kAMeta][128] of the keys
     static constexpr int OFF_SEEN = OFF_META + 3 * kAMeta * kATile * 4;  // [kAMeta][4], then [kAMeta] flags
-    static constexpr int OFF_QS = OFF_SEEN + 128;                      // [QB][N] query scales
+    static constexpr int OFF_QS = OFF_SEEN + 128;                      // [QB][COLS] query scales
     static constexpr int OFF_W = OFF_QS + QB * N * 4;                  // [2][SG][4][NC] warp maxima of a tile
     static constexpr int OFF_MB = OFF_W + 2 * SG * 4 * NC * 4;         // [4 SG][3][NC] of a warp: 8 - M, fades
     static constexpr int OFF_END = OFF_MB + 4 * SG * 3 * NC * 4;       // [SG][NC] keys a column sees
@@ -33,24 +40,25 @@ struct AttnCfg {
     static constexpr int OFF_INV = OFF_MW + SG * NC * 4;               // [N] 1 / l
     static constexpr int OFF_ROW = OFF_INV + N * 4;                    // [N] output rows
     static constexpr int OFF_GATHER = OFF_ROW + N * 4;                 // [4][128] cache rows of a tile's keys
-    static constexpr int OFF_STAGE = OFF_GATHER + 4 * kATile * 4;      // 4 bits: packed keys of the producers
-    static constexpr int OFF_BAR = OFF_STAGE + (BITS == 4 ? 8 * kAStage4 : 0);
-    static constexpr int NBAR = 2 * SLOTS + 2 * kAMeta + 2 * 2 + 3 * 2 + 4 + 2 + 1;
+    static constexpr int OFF_PACKED = OFF_GATHER + 4 * kATile * 4;     // 4 bits: packed tiles
+    static constexpr int OFF_BAR = OFF_PACKED + PACKED * kAPackedBytes;
+    static constexpr int NBAR = 2 * SLOTS + 2 * kAMeta + 2 * 2 + 3 * 2 + 4 + 2 + 1 + 2 * PACKED;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;                // start of the share, TMEM address
     static constexpr int TOTAL = OFF_MISC + 288 + 1024;                // + alignment of the base
     static_assert(TOTAL <= 232448 && kAMeta * 20 <= 128, "shared memory");
     static_assert(OFF_QS % 16 == 0 && OFF_MB % 16 == 0 && OFF_END % 16 == 0 && OFF_AB % 16 == 0 && OFF_W % 16 == 0 &&
                       OFF_GATHER % 16 == 0 && OFF_MISC % 8 == 0,
                   "16-byte reads");
-    static constexpr int TMEM = 4 * N;                                 // columns: two tiles of S and of O
-    // Warpgroups: MMA and queries; two of softmax; joining; producers (4 bits: two, which widen the tiles).
-    static constexpr int THREADS = BITS == 8 ? 640 : 768, PRODUCERS = BITS == 8 ? 4 : 8, QWARPS = 3;
+    static constexpr int TMEM = 4 * MN;                                // columns: two tiles of S and of O
+    // Warpgroups: MMA and queries (4 bits: and the producers); two of softmax; joining; producers (4 bits: two that widen).
+    static constexpr int THREADS = BITS == 8 ? 640 : 768, PRODUCERS = BITS == 8 ? 4 : 2, QWARPS = BITS == 8 ? 3 : 1;
     static constexpr int W_QUERY = 1, W_SOFT = 4, W_JOIN = 12, W_PROD = 16;  // first warps
     // registers a thread of each group: their sum is at most what the launch has
-    static constexpr int R_LAUNCH = BITS == 8 ? 96 : 80, R_MMA = BITS == 8 ? 64 : 56, R_SOFT = BITS == 8 ? 112 : 104;
-    static constexpr int R_JOIN = BITS == 8 || SPLIT ? 104 : 80, R_PROD = BITS == 8 ? 88 : (SPLIT ? 56 : 64);
+    static constexpr int R_LAUNCH = BITS == 8 ? 96 : 80, R_MMA = BITS == 8 ? 64 : (SPLIT ? 72 : 80);
+    static constexpr int R_SOFT = BITS == 8 ? 112 : (NC == 8 ? 88 : 96), R_JOIN = BITS == 8 ? 104 : (SPLIT ? 104 : 80);
+    static constexpr int R_PROD = BITS == 8 ? 88 : (SPLIT ? 56 : 64);
     static_assert(R_LAUNCH == 65536 / THREADS / 8 * 8 &&
-                      R_MMA + SG * R_SOFT + R_JOIN + R_PROD * (PRODUCERS / 4) <= R_LAUNCH * (THREADS / 128),
+                      R_MMA + SG * R_SOFT + R_JOIN + R_PROD * (THREADS / 32 - W_PROD) / 4 <= R_LAUNCH * (THREADS / 128),
                   "register split");
     static_assert(R_MMA <= R_LAUNCH && R_PROD <= R_LAUNCH && R_SOFT >= R_LAUNCH && R_JOIN >= R_LAUNCH, "directions");
 };
@@ -75,16 +83,30 @@ __device__ __forceinline__ float warp_sum_columns(float (&v)[NC], int lane) {
     return v[0];
 }
 
-// x of the columns of this thread's key: (S^T * key's factor) * column's factor + log2(v scale); unseen -inf.
-template <bool MASK, int NC>
+// x of the columns of this thread's key: (S^T * key's factor) * column's factor + log2(v scale); unseen -inf.  LO > 0: the lo
+// parts' products are LO columns on.
+template <bool MASK, int NC, int LO>
 __device__ __forceinline__ void attn_scores(uint32_t s_addr, const float* qs, const int* ends, uint64_t a2,
                                             uint64_t lv2, int key, bool seen, float (&x)[NC]) {
     uint32_t r[NC];
-    if constexpr (NC == 16)
+    if constexpr (NC == 8) {
+        uint32_t both[16];
+        tmem_ld16(s_addr, both);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(__uint_as_float(both[i]) + __uint_as_float(both[8 + i]));
+    } else {
         tmem_ld16(s_addr, r);
-    else
-        tmem_ld8(s_addr, r);
-    tmem_ld_wait();
+        if constexpr (LO > 0) {
+            uint32_t lo[16];
+            tmem_ld16(s_addr + LO, lo);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(lo[i]));
+        } else {
+            tmem_ld_wait();
+        }
+    }
 #pragma unroll
     for (int i = 0; i < NC; i += 4) {
         const float4 q4 = *reinterpret_cast<const float4*>(qs + i);
@@ -109,6 +131,7 @@ __global__ void __launch_bounds__(AttnCfg<N, NC_, BITS>::THREADS, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                       const __grid_constant__ AttnParams p) {
     using C = AttnCfg<N, NC_, BITS>;
+    using RING = typename C::RING;
     constexpr int NC = C::NC, SLOTS = C::SLOTS, QB = C::QB, COLS = C::COLS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -128,7 +151,7 @@ __global__ void __launch_bounds__(AttnCfg<N, NC_, BITS>::THREADS, 1)
     x.seen = (uint32_t*)(smem + C::OFF_SEEN);
     x.flag = x.seen + 4 * kAMeta;
     x.rows = (int*)(smem + C::OFF_GATHER);
-    x.stage = smem + C::OFF_STAGE;
+    x.packed = smem + C::OFF_PACKED;
     uint64_t* const kv_full = x.kv_full = bars;
     uint64_t* const kv_empty = x.kv_empty = kv_full + SLOTS;
     uint64_t* const meta_full = x.meta_full = kv_empty + SLOTS;
@@ -142,6 +165,8 @@ __global__ void __launch_bounds__(AttnCfg<N, NC_, BITS>::THREADS, 1)
     uint64_t* l_full = o_empty + 2;         // sums of a segment written
     uint64_t* l_empty = l_full + 1;
     uint64_t* drain = l_empty + 1;
+    uint64_t* const pk_full = x.pk_full = drain + 1;
+    uint64_t* const pk_empty = x.pk_empty = pk_full + C::PACKED;
     uint32_t* tmem_slot = (uint32_t*)(smem + C::OFF_MISC);
     int64_t* const scan = (int64_t*)(smem + C::OFF_MISC + 8);  // [34]
 
@@ -149,11 +174,11 @@ __global__ void __launch_bounds__(AttnCfg<N, NC_, BITS>::THREADS, 1)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < SLOTS; ++i) {
-            mbar_init(kv_full + i, BITS == 8 ? 1 : 2);
+            mbar_init(kv_full + i, BITS == 8 ? 1 : 4);
             mbar_init(kv_empty + i, 1);
         }
         for (int i = 0; i < kAMeta; ++i) {
-            mbar_init(meta_full + i, BITS == 8 ? 1 : 2);
+            mbar_init(meta_full + i, 1);
             mbar_init(meta_empty + i, C::SPLIT ? 8 : 4);
         }
         for (int i = 0; i < 2; ++i) {
@@ -168,6 +193,10 @@ __global__ void __launch_bounds__(AttnCfg<N, NC_, BITS>::THREADS, 1)
         mbar_init(l_full, 8);
         mbar_init(l_empty, 4);
         mbar_init(drain, 1);
+        for (int i = 0; i < C::PACKED; ++i) {
+            mbar_init(pk_full + i, p.idx ? 33 : 1);  // copies of the lanes arrive by themselves
+            mbar_init(pk_empty + i, 4);
+        }
         fence_mbar_init();
         if constexpr (BITS == 8) {
             tma_prefetch_desc(&tmk);
@@ -192,8 +221,8 @@ __global__ void __launch_bounds__(AttnCfg<N, NC_, BITS>::THREADS, 1)
             // ------------------------------------------------------- MMA issuer
             // The whole warp walks and waits; one lane issues.
             const bool issuer = elect_one();
-            const uint32_t id_s = idesc_e4m3_f32(128, N);
-            const uint32_t id_o = idesc_e4m3_f32(128, N) | kIdescAMn | kIdescBMn;
+            const uint32_t id_s = idesc_e4m3_f32(128, C::MN);
+            const uint32_t id_o = idesc_e4m3_f32(128, C::MN) | kIdescAMn | kIdescBMn;
             const int nk = (p.D + 31) / 32;
             const uint64_t dk0 = smem_desc_kmajor(smem_u32(smem), 128);
             const uint64_t dv0 = smem_desc_mn_sw128(smem_u32(smem), kASlotBytes);
@@ -203,8 +232,8 @@ __global__ void __launch_bounds__(AttnCfg<N, NC_, BITS>::THREADS, 1)
             int tc = 0, sc = 0;
             // O^T of tile t: V^T (hi + lo)
             auto second = [&](int t) {
-                const int bf = t & 1, ph = (t >> 1) & 1, seq = 2 * t + 1, sl = seq % SLOTS;
-                ok = ok && mbar_wait(kv_full + sl, (seq / SLOTS) & 1, p.wait_ns);
+                const int bf = t & 1, ph = (t >> 1) & 1, sl = RING::at(t, 1);
+                ok = ok && mbar_wait(kv_full + sl, RING::phase(t, 1), p.wait_ns);
                 ok = ok && mbar_wait(o_empty + bf, ph ^ 1, p.wait_ns);
                 ok = ok && mbar_wait(p_full + (t & 3), (t >> 2) & 1, p.wait_ns);
                 ok = __all_sync(0xffffffffu, ok);
@@ -213,11 +242,12 @@ __global__ void __launch_bounds__(AttnCfg<N, NC_, BITS>::THREADS, 1)
                 if (issuer) {
                     const uint64_t a = dv0 + (uint64_t)(sl * (kASlotBytes >> 4));
                     const uint64_t b = dp0 + (uint64_t)(bf * (C::P_BYTES >> 4));
-                    const uint32_t d = tmem + 2 * N + bf * N;
+                    const uint32_t d = tmem + 2 * C::MN + bf * C::MN;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {  // 32 keys a step
                         umma_f8(d, a + k * (32 * 128 >> 4), b + k * (32 * 128 >> 4), id_o, k > 0);
-                        umma_f8(d, a + k * (32 * 128 >> 4), b + (C::P_HALF >> 4) + k * (32 * 128 >> 4), id_o, 1);
+                        if (BITS == 8)
+                            umma_f8(d, a + k * (32 * 128 >> 4), b + (kASlotBytes >> 4) + k * (32 * 128 >> 4), id_o, 1);
                     }
                     umma_commit(o_full + bf);
                     umma_commit(kv_empty + sl);
@@ -229,27 +259,29 @@ __global__ void __launch_bounds__(AttnCfg<N, NC_, BITS>::THREADS, 1)
                 const int qb = sc % QB;
                 ok = ok && mbar_wait(q_full + qb, (sc / QB) & 1, p.wait_ns);
                 for (int t = wk.t0; ok && t < wk.t1; ++t, ++tc) {
-                    const int seq = 2 * tc, sl = seq % SLOTS;
-                    ok = mbar_wait(kv_full + sl, (seq / SLOTS) & 1, p.wait_ns);
+                    const int sl = RING::at(tc, 0);
+                    ok = mbar_wait(kv_full + sl, RING::phase(tc, 0), p.wait_ns);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc_fence_after();
                     if (issuer) {
                         const uint64_t a = dk0 + (uint64_t)(sl * (kASlotBytes >> 4));
                         const uint64_t b = dq0 + (uint64_t)(qb * (C::Q_BYTES >> 4));
-                        const uint32_t d = tmem + (tc & 1) * N;
+                        const uint32_t d = tmem + (tc & 1) * C::MN;
                         // 32 dims a step, hi then lo
                         if (nk == 4) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k) umma_f8(d, a + 2 * k, b + 2 * k, id_s, k > 0);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) umma_f8(d, a + 2 * k, b + (N * 128 >> 4) + 2 * k, id_s, 1);
+                            for (int k = 0; k < 4; ++k)
+                                if (BITS == 8) umma_f8(d, a + 2 * k, b + (N * 128 >> 4) + 2 * k, id_s, 1);
                         } else {
                             // (the places past D are zero: a narrower head takes fewer steps)
 #pragma unroll 1
                             for (int k = 0; k < nk; ++k) umma_f8(d, a + 2 * k, b + 2 * k, id_s, k > 0);
 #pragma unroll 1
-                            for (int k = 0; k < nk; ++k) umma_f8(d, a + 2 * k, b + (N * 128 >> 4) + 2 * k, id_s, 1);
+                            for (int k = 0; k < nk; ++k)
+                                if (BITS == 8) umma_f8(d, a + 2 * k, b + (N * 128 >> 4) + 2 * k, id_s, 1);
                         }
                         umma_commit(s_full + (tc & 1));
                         umma_commit(kv_empty + sl);
@@ -265,8 +297,13 @@ __global__ void __launch_bounds__(AttnCfg<N, NC_, BITS>::THREADS, 1)
                 if (issuer) umma_commit(drain);
                 mbar_wait(drain, 0, p.wait_ns);
             }
-        } else {
-            attn_queries<N, QB, C::QWARPS>(p, wk, x, warp - C::W_QUERY, lane);
+        } else if (warp <= C::QWARPS) {
+            attn_queries<COLS, QB, C::QWARPS>(p, wk, x, warp - C::W_QUERY, lane);
+        } else if constexpr (BITS == 4) {
+            if (p.idx)
+                attn_produce4<C::PACKED, C::PRODUCERS, true>(p, wk, x, warp - 1 - C::QWARPS, lane);
+            else
+                attn_produce4<C::PACKED, C::PRODUCERS, false>(p, wk, x, warp - 1 - C::QWARPS, lane);
         }
     } else if (warp < C::W_JOIN) {
         // -------------------------------------------------------------- softmax
@@ -302,7 +339,7 @@ __global__ void __launch_bounds__(AttnCfg<N, NC_, BITS>::THREADS, 1)
                 named_bar_sync(bar_id, 128);
             }
             ok = ok && mbar_wait(q_full + qb, (sc / QB) & 1, p.wait_ns);
-            const float* const qs = x.q_scale + qb * N + c0;
+            const float* const qs = x.q_scale + qb * COLS + c0;
             float l[NC];
 #pragma unroll
             for (int i = 0; i < NC; ++i) l[i] = 0.f;
@@ -325,7 +362,7 @@ __global__ void __launch_bounds__(AttnCfg<N, NC_, BITS>::THREADS, 1)
                 // joining of the tile two before it)
                 ok = ok && mbar_wait(s_full + bf, ph, p.wait_ns);
                 tc_fence_after();
-                const uint32_t s_addr = lane_addr + bf * N;
+                const uint32_t s_addr = lane_addr + bf * C::MN;
                 uint8_t* const prow = sP + (BITS == 8 ? bf * C::P_BYTES : 0) + wtid * 128;
 
                 float* const sWt = sW + odd * C::SG * 4 * NC;
@@ -333,7 +370,7 @@ __global__ void __launch_bounds__(AttnCfg<N, NC_, BITS>::THREADS, 1)
                 auto one_tile = [&](auto mask_c) {
                     constexpr bool MASK = decltype(mask_c)::value;
                     float score[NC], top[NC];
-                    attn_scores<MASK, NC>(s_addr, qs, sEnd, a2, lv2, key, seen, score);
+                    attn_scores<MASK, NC, BITS == 8 ? 0 : COLS>(s_addr, qs, sEnd, a2, lv2, key, seen, score);
 #pragma unroll
                     for (int i = 0; i < NC; ++i) top[i] = warp_max_nan(score[i]);
                     if (lane == 0) {
@@ -385,15 +422,14 @@ __global__ void __launch_bounds__(AttnCfg<N, NC_, BITS>::THREADS, 1)
                         lo[i / 4] = l0 | (l1 << 16);
                     }
                     // 128-byte swizzle
-                    const int j = (c0 >> 4) + (BITS == 8 ? 0 : bf * (C::P_BYTES >> 4)), jl = j + (BITS == 8 ? 0 : C::P_HALF >> 4);
+                    const int j = (c0 >> 4) + (BITS == 8 ? 0 : bf * (C::MN >> 4));
                     uint8_t* const ph = prow + ((j ^ (wtid & 7)) << 4);
-                    uint8_t* const pl = prow + (BITS == 8 ? kASlotBytes : 0) + ((jl ^ (wtid & 7)) << 4);
                     if constexpr (NC == 16) {
+                        uint8_t* const pl = prow + (BITS == 8 ? kASlotBytes : 0) + (((j + (BITS == 8 ? 0 : COLS >> 4)) ^ (wtid & 7)) << 4);
                         *reinterpret_cast<uint4*>(ph) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                         *reinterpret_cast<uint4*>(pl) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                    } else {  // (the columns past the rows are never read)
-                        *reinterpret_cast<uint2*>(ph) = make_uint2(hi[0], hi[1]);
-                        *reinterpret_cast<uint2*>(pl) = make_uint2(lo[0], lo[1]);
+                    } else {
+                        *reinterpret_cast<uint4*>(ph) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
                     }
                 };
                 if (masked)
@@ -402,8 +438,8 @@ __global__ void __launch_bounds__(AttnCfg<N, NC_, BITS>::THREADS, 1)
                     one_tile(std::false_type{});
                 if (BITS == 8 && flag && c0 == 0) {  // (4 bits: the producers write zeros there)
                     // unseen slots may hold anything (NaN codes): a zero weight alone would not keep them out
-                    const int seq = 2 * tc + 1, sl = seq % SLOTS;
-                    ok = ok && mbar_wait(kv_full + sl, (seq / SLOTS) & 1, p.wait_ns);
+                    const int sl = RING::at(tc, 1);
+                    ok = ok && mbar_wait(kv_full + sl, RING::phase(tc, 1), p.wait_ns);
                     if (!seen && ok) {
                         uint4* vrow = reinterpret_cast<uint4*>(smem + sl * kASlotBytes + wtid * 128);
 #pragma unroll
@@ -435,7 +471,7 @@ __global__ void __launch_bounds__(AttnCfg<N, NC_, BITS>::THREADS, 1)
         regs_inc<C::R_JOIN>();
         const int d = tid & 127, wg_warp = warp & 3;
         constexpr uint32_t bar_id = 1 + C::SG;
-        const uint32_t lane_addr = tmem + ((uint32_t)(wg_warp * 32) << 16) + 2 * N;
+        const uint32_t lane_addr = tmem + ((uint32_t)(wg_warp * 32) << 16) + 2 * C::MN;
         float* const sA = (float*)(smem + C::OFF_AB);  // [2][N] fade of acc
         float* const sB = sA + 2 * N;                  // [2][N] of the tile
         float* const sInv = (float*)(smem + C::OFF_INV);
@@ -465,13 +501,29 @@ __global__ void __launch_bounds__(AttnCfg<N, NC_, BITS>::THREADS, 1)
                     ok = ok && mbar_wait(o_full + bf, ph, p.wait_ns);
                     tc_fence_after();
                     uint32_t r[COLS];
-                    if constexpr (COLS == 32)
-                        tmem_ld32(lane_addr + bf * N, r);
-                    else if constexpr (COLS == 16)
-                        tmem_ld16(lane_addr + bf * N, r);
-                    else
-                        tmem_ld8(lane_addr + bf * N, r);
-                    tmem_ld_wait();
+                    if constexpr (BITS == 8) {
+                        if constexpr (COLS == 32)
+                            tmem_ld32(lane_addr + bf * C::MN, r);
+                        else
+                            tmem_ld16(lane_addr + bf * C::MN, r);
+                        tmem_ld_wait();
+                    } else if constexpr (COLS == 8) {
+                        uint32_t both[16];
+                        tmem_ld16(lane_addr + bf * C::MN, both);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(__uint_as_float(both[i]) + __uint_as_float(both[8 + i]));
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < COLS; c += 16) {
+                            uint32_t h[16], l[16];
+                            tmem_ld16(lane_addr + bf * C::MN + c, h);
+                            tmem_ld16(lane_addr + bf * C::MN + COLS + c, l);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) r[c + i] = __float_as_uint(__uint_as_float(h[i]) + __uint_as_float(l[i]));
+                        }
+                    }
 #pragma unroll
                     for (int i = 0; i < COLS; i += 4) {
                         const float4 fa = *reinterpret_cast<const float4*>(sA + bf * N + i);
@@ -546,10 +598,8 @@ __global__ void __launch_bounds__(AttnCfg<N, NC_, BITS>::THREADS, 1)
             else
                 attn_produce<SLOTS, C::PRODUCERS, false>(p, wk, x, &tmk, &tmv, warp - C::W_PROD, lane);
         } else {
-            if (p.idx)
-                attn_produce4<SLOTS, C::PRODUCERS / 2, true>(p, wk, x, warp - C::W_PROD, lane);
-            else
-                attn_produce4<SLOTS, C::PRODUCERS / 2, false>(p, wk, x, warp - C::W_PROD, lane);
+            // one group widens the K tiles, the other the V tiles
+            attn_widen<RING, C::PACKED, 2>(p, wk, x, (warp - C::W_PROD) >> 2, warp & 3, lane);
         }
     }
 

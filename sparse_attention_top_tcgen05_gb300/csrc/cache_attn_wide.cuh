@@ -29,9 +29,12 @@
 
 namespace lidx {
 
-template <int BITS>
+// TWICE: units of at most 64 rows.
+template <int BITS, bool TWICE>
 struct WideCfg {
-    static constexpr int N = 128, QB = 2, SLOTS = BITS == 8 ? 8 : 4;
+    static constexpr int N = 128, QB = 2;
+    using RING = AttnSlots<BITS, BITS == 8 ? 4 : 2, BITS == 8 ? 4 : 3>;
+    static constexpr int SLOTS = RING::ALL, PACKED = BITS == 8 ? 0 : (TWICE ? 5 : 7);
     static constexpr int Q_BYTES = 2 * N * 128;  // hi and lo
     static constexpr int OFF_Q = SLOTS * kASlotBytes;
     static constexpr int OFF_META = OFF_Q + QB * Q_BYTES;                // [3][kAMeta][128] of the keys
@@ -41,18 +44,19 @@ struct WideCfg {
     static constexpr int OFF_L = OFF_MT + 4 * N * 4;                     // [2][N] float2: a group's sum, its reference
     static constexpr int OFF_GATHER = OFF_L + 2 * N * 8;                 // [4][128] cache rows of a tile's keys
     static constexpr int OFF_X = OFF_GATHER + 4 * kATile * 4;                // [32][128] dims that the copies exchange
-    static constexpr int OFF_STAGE = OFF_X + 32 * 128 * 4;  // 4 bits: packed keys of the producers
-    static constexpr int OFF_BAR = OFF_STAGE + (BITS == 4 ? 4 * kAStage4 : 0);
-    static constexpr int NBAR = 2 * SLOTS + 2 * kAMeta + 2 * 2 + 3 + 4 + 2 + 2 + 1;
+    static constexpr int OFF_PACKED = OFF_X + (TWICE ? 32 * 128 * 4 : 0);  // 4 bits: packed tiles
+    static constexpr int OFF_BAR = OFF_PACKED + PACKED * kAPackedBytes;
+    static constexpr int NBAR = 2 * SLOTS + 2 * kAMeta + 2 * 2 + 3 + 4 + 2 + 2 + 1 + 2 * PACKED;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int TOTAL = OFF_MISC + 288 + 1024;
     static_assert(TOTAL <= 232448 && kAMeta * 20 <= 128, "shared memory");
     static_assert(OFF_QS % 16 == 0 && OFF_GATHER % 16 == 0 && OFF_MISC % 8 == 0, "16-byte reads");
     static constexpr int TMEM = 512;  // three tiles of S (and the weights over them), one of O
-    // Warpgroups: MMA and queries; two of softmax that take the tiles in turn; joining; producers.
-    static constexpr int THREADS = 640, PRODUCERS = 4, QWARPS = 3;
+    // Warpgroups: MMA and queries (4 bits: and the producers); two of softmax that take the tiles in turn; joining; producers
+    // (4 bits: four warps that widen).
+    static constexpr int THREADS = 640, PRODUCERS = BITS == 8 ? 4 : 2, QWARPS = BITS == 8 ? 3 : 1;
     static constexpr int W_SOFT = 4, W_JOIN = 12, W_PROD = 16;
-    static constexpr int R_LAUNCH = 96, R_MMA = 56, R_SOFT = 96, R_JOIN = 176, R_PROD = 56;
+    static constexpr int R_LAUNCH = 96, R_MMA = BITS == 8 ? 56 : 64, R_SOFT = 96, R_JOIN = 176, R_PROD = BITS == 8 ? 56 : 48;
     static_assert(R_LAUNCH == 65536 / THREADS / 8 * 8 && R_MMA + 2 * R_SOFT + R_JOIN + R_PROD <= R_LAUNCH * 5,
                   "register split");
     static_assert(R_MMA <= R_LAUNCH && R_PROD <= R_LAUNCH && R_SOFT >= R_LAUNCH && R_JOIN >= R_LAUNCH, "directions");
@@ -102,10 +106,11 @@ __device__ __forceinline__ void wide_scores(const float* a, const float* lv, flo
 
 // SEL: selected keys.  TWICE: units of at most 64 rows.
 template <bool SEL, bool TWICE, int BITS>
-__global__ void __launch_bounds__(WideCfg<BITS>::THREADS, 1)
+__global__ void __launch_bounds__(WideCfg<BITS, TWICE>::THREADS, 1)
     cache_attn_wide_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                            const __grid_constant__ AttnParams p) {
-    using C = WideCfg<BITS>;
+    using C = WideCfg<BITS, TWICE>;
+    using RING = typename C::RING;
     constexpr int N = C::N, SLOTS = C::SLOTS, QB = C::QB;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -123,7 +128,7 @@ __global__ void __launch_bounds__(WideCfg<BITS>::THREADS, 1)
     x.seen = (uint32_t*)(smem + C::OFF_SEEN);
     x.flag = x.seen + 4 * kAMeta;
     x.rows = (int*)(smem + C::OFF_GATHER);
-    x.stage = smem + C::OFF_STAGE;
+    x.packed = smem + C::OFF_PACKED;
     uint64_t* const kv_full = x.kv_full = bars;
     uint64_t* const kv_empty = x.kv_empty = kv_full + SLOTS;
     uint64_t* const meta_full = x.meta_full = kv_empty + SLOTS;
@@ -137,6 +142,8 @@ __global__ void __launch_bounds__(WideCfg<BITS>::THREADS, 1)
     uint64_t* l_full = o_empty + 1;  // sums of a segment written
     uint64_t* l_empty = l_full + 1;
     uint64_t* drain = l_empty + 1;
+    uint64_t* const pk_full = x.pk_full = drain + 1;
+    uint64_t* const pk_empty = x.pk_empty = pk_full + C::PACKED;
     uint32_t* tmem_slot = (uint32_t*)(smem + C::OFF_MISC);
     int64_t* const scan = (int64_t*)(smem + C::OFF_MISC + 8);  // [34]
 
@@ -144,11 +151,11 @@ __global__ void __launch_bounds__(WideCfg<BITS>::THREADS, 1)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < SLOTS; ++i) {
-            mbar_init(kv_full + i, BITS == 8 ? 1 : 2);
+            mbar_init(kv_full + i, BITS == 8 ? 1 : 4);
             mbar_init(kv_empty + i, 1);
         }
         for (int i = 0; i < kAMeta; ++i) {
-            mbar_init(meta_full + i, BITS == 8 ? 1 : 2);
+            mbar_init(meta_full + i, 1);
             mbar_init(meta_empty + i, 4);
         }
         for (int i = 0; i < 2; ++i) {
@@ -162,6 +169,10 @@ __global__ void __launch_bounds__(WideCfg<BITS>::THREADS, 1)
         mbar_init(l_full, 8);
         mbar_init(l_empty, 4);
         mbar_init(drain, 1);
+        for (int i = 0; i < C::PACKED; ++i) {
+            mbar_init(pk_full + i, SEL ? 33 : 1);  // copies of the lanes arrive by themselves
+            mbar_init(pk_empty + i, 4);
+        }
         fence_mbar_init();
         if constexpr (BITS == 8) {
             tma_prefetch_desc(&tmk);
@@ -197,8 +208,8 @@ __global__ void __launch_bounds__(WideCfg<BITS>::THREADS, 1)
             int tc = 0, sc = 0;
             // O of tile t: (hi + lo) V
             auto second = [&](int t) {
-                const int seq = 2 * t + 1, sl = seq % SLOTS;
-                ok = ok && mbar_wait(kv_full + sl, (seq / SLOTS) & 1, p.wait_ns);
+                const int sl = RING::at(t, 1);
+                ok = ok && mbar_wait(kv_full + sl, RING::phase(t, 1), p.wait_ns);
                 ok = ok && mbar_wait(o_empty, (t & 1) ^ 1, p.wait_ns);
                 ok = ok && mbar_wait(p_full + (t & 3), (t >> 2) & 1, p.wait_ns);
                 ok = __all_sync(0xffffffffu, ok);
@@ -224,8 +235,8 @@ __global__ void __launch_bounds__(WideCfg<BITS>::THREADS, 1)
                 const int qb = sc % QB;
                 ok = ok && mbar_wait(q_full + qb, (sc / QB) & 1, p.wait_ns);
                 for (int t = wk.t0; ok && t < wk.t1; ++t, ++tc) {
-                    const int seq = 2 * tc, sl = seq % SLOTS;
-                    ok = mbar_wait(kv_full + sl, (seq / SLOTS) & 1, p.wait_ns);
+                    const int sl = RING::at(tc, 0);
+                    ok = mbar_wait(kv_full + sl, RING::phase(tc, 0), p.wait_ns);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc_fence_after();
@@ -262,8 +273,10 @@ __global__ void __launch_bounds__(WideCfg<BITS>::THREADS, 1)
                 if (issuer) umma_commit(drain);
                 mbar_wait(drain, 0, p.wait_ns);
             }
-        } else {
+        } else if (warp <= C::QWARPS) {
             attn_queries<N, QB, C::QWARPS>(p, wk, x, warp - 1, lane, TWICE);
+        } else if constexpr (BITS == 4) {
+            attn_produce4<C::PACKED, C::PRODUCERS, SEL>(p, wk, x, warp - 1 - C::QWARPS, lane);
         }
     } else if (warp < C::W_JOIN) {
         // -------------------------------------------------------------- softmax
@@ -410,8 +423,8 @@ __global__ void __launch_bounds__(WideCfg<BITS>::THREADS, 1)
                 if (BITS == 8 && flag) {  // (4 bits: the producers write zeros there)
                     // unseen slots may hold anything (NaN codes): a zero weight alone would not keep them out.
                     // Thread i clears V's row i.
-                    const int seq = 2 * tc + 1, sl = seq % SLOTS;
-                    ok = ok && mbar_wait(kv_full + sl, (seq / SLOTS) & 1, p.wait_ns);
+                    const int sl = RING::at(tc, 1);
+                    ok = ok && mbar_wait(kv_full + sl, RING::phase(tc, 1), p.wait_ns);
                     if (ok && !((x.seen[ms * 4 + wg_warp] >> lane) & 1)) {
                         uint4* vrow = reinterpret_cast<uint4*>(smem + sl * kASlotBytes + row * 128);
 #pragma unroll
@@ -574,7 +587,7 @@ __global__ void __launch_bounds__(WideCfg<BITS>::THREADS, 1)
         if constexpr (BITS == 8)
             attn_produce<SLOTS, C::PRODUCERS, SEL>(p, wk, x, &tmk, &tmv, warp - C::W_PROD, lane);
         else
-            attn_produce4<SLOTS, C::PRODUCERS / 2, SEL>(p, wk, x, warp - C::W_PROD, lane);
+            attn_widen<RING, C::PACKED, 1>(p, wk, x, 0, warp & 3, lane);
     }
 
     __syncwarp();
@@ -589,9 +602,9 @@ __global__ void __launch_bounds__(WideCfg<BITS>::THREADS, 1)
 template <bool SEL, bool TWICE, int BITS>
 static cudaError_t wide_launch(const CUtensorMap& mk, const CUtensorMap& mv, const AttnParams& p, int grid, cudaStream_t st) {
     auto* kernel = cache_attn_wide_kernel<SEL, TWICE, BITS>;
-    cudaError_t e = set_smem_attr((const void*)kernel, WideCfg<BITS>::TOTAL);
+    cudaError_t e = set_smem_attr((const void*)kernel, WideCfg<BITS, TWICE>::TOTAL);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, WideCfg<BITS>::THREADS, WideCfg<BITS>::TOTAL, st>>>(mk, mv, p);
+    kernel<<<grid, WideCfg<BITS, TWICE>::THREADS, WideCfg<BITS, TWICE>::TOTAL, st>>>(mk, mv, p);
     return cudaGetLastError();
 }
 template <int BITS>

@@ -120,6 +120,7 @@ __global__ void __launch_bounds__(kRaThreads) rope_append_kernel(const __grid_co
         uint32_t top = 0;
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
+            if (k * G >= n) break;
             const int e = grp + k * G;
             float(&y)[16] = f[k];
             rope_unpack(va[k], reinterpret_cast<float(&)[8]>(y[0]));
@@ -275,6 +276,7 @@ __global__ void __launch_bounds__(kRaThreads) rope_append_kernel(const __grid_co
             }
 #pragma unroll
             for (int k = 0; k < PER; ++k) {
+                if (k * G >= n) break;
                 const int t = (int)(lo - p0) + grp + k * G;
                 const bool live = grp + k * G < n;
                 uint32_t g = 0;

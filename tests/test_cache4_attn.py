@@ -4,9 +4,10 @@ code * 2^x * scale is e4m3 code * (32 scale) exactly, so the definition and the 
 8-bit cache (plain.attention), on the cache's 8-bit form.  One term is added, since the groups of these caches differ by up
 to 2^11: a weight below 2^-14 of its tile's largest, 2^8, lies among the lower half's subnormals, whose step is 2^-9; it is off
 by 2^-10, 2^-18 of the largest weight, and the sum of all weights is at least that weight.  plain.attention counts that once, for
-the largest value; every key may be off by as much, so a dim by 2^-18 sum_t |v_t|.  The kernels widen the codes to that form and go on as the 8-bit
-ones with the same shares and orders of additions: the outputs are the 8-bit call's bit for bit.  On random inputs the
-error of a whole output stays below 5e-3 of its norm as there."""
+the largest value; every key may be off by as much, so a dim by 2^-18 sum_t |v_t|.  The kernels
+widen the codes to that form and go on as the 8-bit ones; units of up to 32 rows add the products of a row's two parts
+after them, not in them.  Either call is within the tolerance of the definition, so they are within twice that of each other.
+On random inputs the error of a whole output stays below 5e-3 of its norm as there."""
 
 import ctypes as C
 import math
@@ -50,8 +51,8 @@ def test_refusals_without_gpu():
                 dict(D=256), dict(page=24), dict(MP=0), dict(NP=0), dict(NP=1 << 29), dict(ratio=0),
                 dict(idx=16, topk=0), dict(idx=16, topk=(1 << 20) + 1), dict(scale=math.nan), dict(B=1 << 16, S=1 << 16)):
         assert call(**bad) == 2, bad
-    for bad in (dict(q=24), dict(qs=odd), dict(kc=8), dict(vc=8), dict(out=8), dict(lens=18), dict(table=18), dict(ke=18),
-                dict(ve=18), dict(pos=18), dict(idx=18, topk=1), dict(lse=18), dict(ksc=18), dict(vsc=18)):
+    for bad in (dict(q=24), dict(qs=odd), dict(kc=8), dict(vc=8), dict(out=8), dict(lens=18), dict(table=18), dict(ke=24), dict(ke=24),
+                dict(ve=24), dict(pos=18), dict(idx=18, topk=1), dict(lse=18), dict(ksc=18), dict(vsc=18)):
         assert call(**bad) == 3, bad
 
 
@@ -125,7 +126,8 @@ class Case:
         if whole and seen.any():
             assert np.linalg.norm(od - ro) <= 5e-3 * np.linalg.norm(ro)
         o8, l8 = lidx.lidx_cache_attn(*self.args8(), want_lse=True, **kw)
-        assert torch.equal(o, o8) and torch.equal(lse, l8)
+        assert (np.abs(od - o8.double().cpu().numpy()) <= 2 * so).all()
+        assert (np.abs(lse_d[seen] - l8.double().cpu().numpy()[seen]) <= 2 * sl[seen]).all()
         return od, lse_d
 
 
@@ -272,11 +274,37 @@ def test_strided_queries_streams_and_preallocated_outputs():
     q.copy_(args[0])
     st = torch.cuda.Stream()
     out = (torch.full_like(want, 7.0), torch.full_like(wl, 7.0))
-    ws = torch.empty(lidx.lidx_cache_attn_workspace_bytes(3, 5, 8, 2, 64) + 256, dtype=torch.uint8, device=DEV)
+    ws = torch.empty(lidx.lidx_cache4_attn_workspace_bytes(3, 5, 8, 2, 64, 16, 7) + 256, dtype=torch.uint8, device=DEV)
     st.wait_stream(torch.cuda.current_stream())
     got, gl = lidx.lidx_cache4_attn(q, *args[1:], q_pos=pos, stream=st, out=out, workspace=ws)
     torch.cuda.current_stream().wait_stream(st)
     assert got is out[0] and torch.equal(got, want) and torch.equal(gl, wl)
+    _status_ok()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("selected", [False, True])
+def test_many_rows_with_pages_out_of_range_nan_and_an_own_workspace(selected):
+    """Calls of many rows a key widen pages into the workspace: pages that are not seen, NaN groups, an empty sequence and
+    slots behind the last stay what they are, and a workspace that another call has left is as good as a new one."""
+    B, S, Hq, Hkv, D, page = 3, 90, 8, 2, 80, 16
+    c = Case(21, B, S, Hq, Hkv, D, page, [200, 0, 70])
+    c.table[0, 3], c.table[2, 1] = -7, 10 ** 6
+    idx = c.g.integers(-3, 230, (B, S, 40)) if selected else None
+    pos = [200 - S, 5, 0]
+    c.check(q_pos=pos, idx=idx)
+    need = lidx.lidx_cache4_attn_workspace_bytes(B, S, Hq, Hkv, D, page, c.table.shape[1], 40 if selected else 0)
+    assert need > 2 * B * c.table.shape[1] * page * Hkv * D  # the copy is in it
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV)
+    t = lambda a: None if a is None else torch.from_numpy(np.asarray(a, np.int32)).to(DEV)
+    kw = dict(q_pos=t(pos), topk_indices=t(idx))
+    want, _ = lidx.lidx_cache4_attn(*c.args(), **kw)
+    for _ in range(2):
+        got, _ = lidx.lidx_cache4_attn(*c.args(), workspace=ws, **kw)
+        assert torch.equal(got, want)
+    with pytest.raises(lidx.LidxError) as e:
+        lidx.lidx_cache4_attn(*c.args(), workspace=ws[:lidx.lidx_cache_attn_workspace_bytes(B, S, Hq, Hkv, D, 40)], **kw)
+    assert e.value.status == 5
     _status_ok()
 
 
@@ -321,7 +349,7 @@ def test_large(B, S, Hq, Hkv, D, page, L, topk, ratio):
     _status_ok()
     k8, v8 = lidx.lidx_cache4_to_8(kc, vc, ke, ve)
     as8, _ = lidx.lidx_cache_attn(q, k8, v8, ks * 32, vs * 32, table, lens, **kw)
-    assert torch.equal(got, as8)
+    assert ((got.double() - as8.double()).norm() <= 1e-2 * as8.double().norm()).item()
     want = plain.attention_cuda(q, k8, v8, ks * 32, vs * 32, table, lens, q_pos=kw["q_pos"], ratio=ratio,
                                 idx=kw["topk_indices"])
     assert ((got.double() - want).norm() <= 5e-3 * want.norm()).item()
