@@ -40,7 +40,10 @@ constexpr int kNormThreads = 256;
 constexpr int kNormPer = 4;         // rows a thread, forward
 constexpr int kNormPerBwd = 2;
 constexpr int kNormAngles = 4096;   // of a block's tokens: 32 KB
-constexpr int kNormBlocks = 4;      // blocks an SM of the backward, at most
+// Blocks an SM of the backward, which go over all rows: as many as its registers allow without spills.
+constexpr int kNormBlocks = 3;
+template <class T>
+constexpr int norm_bwd_blocks() { return sizeof(T) == 4 ? kNormBlocks : 2; }
 
 __device__ __forceinline__ float norm_weight(const NormParams& p, const void* w, int d) {
     if (!w) return 1.f;
@@ -53,7 +56,7 @@ __device__ __forceinline__ float norm_weight(const NormParams& p, const void* w,
 struct NormLane {
     int n;       // vectors of the lane: 0 .. 2
     int d0, d1;  // their first dims
-    int c0, c1;  // their first angles, -1: not rotated
+    int c0, c1;  // their items among the rotated ones, -1: not rotated
 };
 template <bool HALF, int V>
 __device__ __forceinline__ NormLane norm_lane(const RopeTurn& r, int D, int l) {
@@ -61,7 +64,7 @@ __device__ __forceinline__ NormLane norm_lane(const RopeTurn& r, int D, int l) {
     if constexpr (HALF) {
         const int np = r.R / 2 / V;
         if (l < np) {
-            o = NormLane{2, r.off + l * V, r.off + l * V + r.R / 2, l * V, l * V};
+            o = NormLane{2, r.off + l * V, r.off + l * V + r.R / 2, l, l};
         } else {
             const int q = 2 * (l - np), nc = (D - r.R) / V;
             o.n = max(0, min(2, nc - q));
@@ -73,8 +76,8 @@ __device__ __forceinline__ NormLane norm_lane(const RopeTurn& r, int D, int l) {
         o.n = l >= half ? 0 : (l + half < nv ? 2 : 1);
         o.d0 = l * V;
         o.d1 = (l + half) * V;
-        if (o.d0 >= r.off && o.d0 < r.off + r.R) o.c0 = (o.d0 - r.off) / 2;
-        if (o.d1 >= r.off && o.d1 < r.off + r.R) o.c1 = (o.d1 - r.off) / 2;
+        if (o.d0 >= r.off && o.d0 < r.off + r.R) o.c0 = (o.d0 - r.off) / V;
+        if (o.d1 >= r.off && o.d1 < r.off + r.R) o.c1 = (o.d1 - r.off) / V;
     }
     return o;
 }
@@ -82,35 +85,62 @@ static int norm_lanes(const RopeTurn& r, int D, int V) {
     return r.half ? r.R / 2 / V + ((D - r.R) / V + 1) / 2 : (D / V + 1) / 2;
 }
 
-// The two vectors of a lane turn.  cs: angles of the row's token.
+// The two vectors of a lane turn.  cs: angles of the row's token; items: rotated items of a head.
 template <bool HALF, int V>
-__device__ __forceinline__ void norm_turn(const NormLane& o, const float2* cs, float (&a)[V], float (&b)[V]) {
+__device__ __forceinline__ void norm_turn(const NormLane& o, const float2* cs, int items, float (&a)[V], float (&b)[V]) {
+    constexpr int A = HALF ? V : V / 2;
+    float2 c[A];
     if constexpr (HALF) {
         if (o.c0 >= 0) {
+            rope_angles_of<A>(cs, o.c0, items, c);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float2 c = cs[o.c0 + i];
                 const float u = a[i], w = b[i];
-                a[i] = u * c.x - w * c.y;
-                b[i] = w * c.x + u * c.y;
+                a[i] = u * c[i].x - w * c[i].y;
+                b[i] = w * c[i].x + u * c[i].y;
             }
         }
     } else {
+        if (o.c0 >= 0) {
+            rope_angles_of<A>(cs, o.c0, items, c);
 #pragma unroll
-        for (int i = 0; i < V; i += 2) {
-            if (o.c0 >= 0) {
-                const float2 c = cs[o.c0 + i / 2];
-                const float u = a[i], w = a[i + 1];
-                a[i] = u * c.x - w * c.y;
-                a[i + 1] = w * c.x + u * c.y;
-            }
-            if (o.c1 >= 0) {
-                const float2 c = cs[o.c1 + i / 2];
-                const float u = b[i], w = b[i + 1];
-                b[i] = u * c.x - w * c.y;
-                b[i + 1] = w * c.x + u * c.y;
+            for (int i = 0; i < A; ++i) {
+                const float u = a[2 * i], w = a[2 * i + 1];
+                a[2 * i] = u * c[i].x - w * c[i].y;
+                a[2 * i + 1] = w * c[i].x + u * c[i].y;
             }
         }
+        if (o.c1 >= 0) {
+            rope_angles_of<A>(cs, o.c1, items, c);
+#pragma unroll
+            for (int i = 0; i < A; ++i) {
+                const float u = b[2 * i], w = b[2 * i + 1];
+                b[2 * i] = u * c[i].x - w * c[i].y;
+                b[2 * i + 1] = w * c[i].x + u * c[i].y;
+            }
+        }
+    }
+}
+
+// Weights in shared memory, words of 16 bytes: the lanes' k-th words follow each other.
+template <int LANES, int V>
+__device__ __forceinline__ void norm_load_weights(const NormParams& p, const void* w, const NormLane& o, float* s_w) {
+    if (threadIdx.x < LANES) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            s_w[(i / 4 * LANES + threadIdx.x) * 4 + i % 4] = o.n > 0 ? norm_weight(p, w, o.d0 + i) : 0.f;
+            s_w[((V + i) / 4 * LANES + threadIdx.x) * 4 + i % 4] = o.n > 1 ? norm_weight(p, w, o.d1 + i) : 0.f;
+        }
+    }
+}
+template <int LANES, int V>
+__device__ __forceinline__ void norm_weights(const float* s_w, int l, float (&wa)[V], float (&wb)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+        const float4 a = reinterpret_cast<const float4*>(s_w)[i / 4 * LANES + l];
+        const float4 b = reinterpret_cast<const float4*>(s_w)[(V + i) / 4 * LANES + l];
+        wa[i] = a.x, wa[i + 1] = a.y, wa[i + 2] = a.z, wa[i + 3] = a.w;
+        wb[i] = b.x, wb[i + 1] = b.y, wb[i + 2] = b.z, wb[i + 3] = b.w;
     }
 }
 
@@ -137,29 +167,30 @@ struct NormRows {
         const uint32_t k = (uint32_t)tok0 + tok, t0 = rope_quot(k, p.tokens1), t1 = k - t0 * (uint32_t)p.T1;
         return t0 * s[0] + t1 * s[1] + (int64_t)(skip + e - tok * t.H) * s[2];
     }
-    // angles of the block's tokens
+    // angles of the block's tokens; A of an item
+    template <int A>
     __device__ void angles(const NormParams& p, const NormTensor& t, float2* s_cs) const {
         const int R2 = p.r.R / 2, all = (token(t, n - 1) + 1) * R2;
         for (int i = threadIdx.x; i < all; i += kNormThreads) {
             const int k = rope_quot(i, p.pairs);
             const uint32_t tok = (uint32_t)tok0 + k, t0 = rope_quot(tok, p.tokens1), t1 = tok - t0 * (uint32_t)p.T1;
-            s_cs[i] = rope_cs(p.r, t0, t1, i - k * R2);
+            s_cs[k * R2 + rope_angle_at<A>(i - k * R2, R2 / A)] = rope_cs(p.r, t0, t1, i - k * R2);
         }
     }
 };
 
 template <class T, bool HALF, int LANES, int PER>
 __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_constant__ NormParams p) {
-    constexpr int V = 16 / sizeof(T), G = kNormThreads / LANES;
+    constexpr int V = 16 / sizeof(T), G = kNormThreads / LANES, A = HALF ? V : V / 2;
     extern __shared__ __align__(16) float s_norm[];
-    float* const s_w = s_norm;                       // [D]
-    float2* const s_cs = (float2*)(s_norm + p.D);    // (D a multiple of V)
+    float* const s_w = s_norm;                               // [2 V / 4][LANES] words
+    float2* const s_cs = (float2*)(s_norm + 2 * V * LANES);
     const int which = (int)blockIdx.x >= p.t[0].blocks;
     const NormTensor& t = p.t[which];
     const int64_t first = (int64_t)(blockIdx.x - (which ? p.t[0].blocks : 0)) * (G * PER);
     const NormRows rows(p, t, first, G * PER);
-    const NormLane o = norm_lane<HALF, V>(p.r, p.D, threadIdx.x % LANES);
-    const int grp = threadIdx.x / LANES;
+    const int l = threadIdx.x % LANES, grp = threadIdx.x / LANES;
+    const NormLane o = norm_lane<HALF, V>(p.r, p.D, l);
     uint4 a[PER], b[PER];
     int tok[PER];
 #pragma unroll
@@ -174,13 +205,14 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_co
             if (o.n > 1) b[k] = *reinterpret_cast<const uint4*>(x + o.d1);
         }
     }
-    for (int d = threadIdx.x; d < p.D; d += kNormThreads) s_w[d] = norm_weight(p, t.w, d);
-    rows.angles(p, t, s_cs);
+    norm_load_weights<LANES, V>(p, t.w, o, s_w);
+    rows.angles<A>(p, t, s_cs);
     __syncthreads();
+    const int R2 = p.r.R / 2;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
         const int e = grp + k * G;
-        float f[V], g[V];
+        float f[V], g[V], wa[V], wb[V];
         rope_unpack(a[k], f);
         rope_unpack(b[k], g);
         float ss = 0.f;
@@ -188,101 +220,105 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_co
         for (int i = 0; i < V; ++i) ss += f[i] * f[i] + g[i] * g[i];
         const float r = __frsqrt_rn(norm_sum<LANES>(ss) * p.inv_d + p.eps);
         if (e >= rows.n || o.n == 0) continue;
+        norm_weights<LANES, V>(s_w, l, wa, wb);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            f[i] *= r * s_w[o.d0 + i];
-            if (o.n > 1) g[i] *= r * s_w[o.d1 + i];
+            f[i] *= r * wa[i];
+            g[i] *= r * wb[i];
         }
-        norm_turn<HALF, V>(o, s_cs + tok[k] * (p.r.R / 2), f, g);
+        norm_turn<HALF, V>(o, s_cs + tok[k] * R2, R2 / A, f, g);
         T* y = (T*)t.y + rows.at(p, t, t.ys, e, tok[k]);
         *reinterpret_cast<uint4*>(y + o.d0) = rope_pack(f);
         if (o.n > 1) *reinterpret_cast<uint4*>(y + o.d1) = rope_pack(g);
     }
 }
 
+// A block goes over its rows in chunks.  A chunk's loads are issued as the chunk before is computed, and its angles go to the
+// other half of their buffer, so that a chunk has one barrier.
 template <class T, bool HALF, int LANES>
-__global__ void __launch_bounds__(kNormThreads) norm_rope_bwd_kernel(const __grid_constant__ NormParams p) {
-    constexpr int V = 16 / sizeof(T), G = kNormThreads / LANES, PER = kNormPerBwd;
+__global__ void __launch_bounds__(kNormThreads, norm_bwd_blocks<T>()) norm_rope_bwd_kernel(const __grid_constant__ NormParams p,
+                                                                                int half_angles) {
+    constexpr int V = 16 / sizeof(T), G = kNormThreads / LANES, PER = kNormPerBwd, A = HALF ? V : V / 2;
     extern __shared__ __align__(16) float s_norm[];
     float* const s_w = s_norm;
-    float2* const s_cs = (float2*)(s_norm + p.D);
+    float2* const s_cs = (float2*)(s_norm + 2 * V * LANES);  // two halves of half_angles
     const int which = (int)blockIdx.x >= p.t[0].blocks;
     const NormTensor& t = p.t[which];
-    const NormLane o = norm_lane<HALF, V>(p.r, p.D, threadIdx.x % LANES);
-    const int grp = threadIdx.x / LANES;
+    const int l = threadIdx.x % LANES, grp = threadIdx.x / LANES, R2 = p.r.R / 2;
+    const NormLane o = norm_lane<HALF, V>(p.r, p.D, l);
     grid_dependency_launch();
-    for (int d = threadIdx.x; d < p.D; d += kNormThreads) s_w[d] = norm_weight(p, t.w, d);
-    float wa[V], wb[V];  // sums of u h
+    norm_load_weights<LANES, V>(p, t.w, o, s_w);
+    float sa[V], sb[V];  // sums of u h
 #pragma unroll
-    for (int i = 0; i < V; ++i) wa[i] = wb[i] = 0.f;
-    const int64_t all = p.T0 * p.T1 * t.H;
-    for (int64_t first = (int64_t)(blockIdx.x - (which ? p.t[0].blocks : 0)) * (G * PER); first < all;
-         first += (int64_t)t.blocks * (G * PER)) {
-        const NormRows rows(p, t, first, G * PER);
-        uint4 xa[PER], xb[PER], ga[PER], gb[PER];
-        int tok[PER];
-#pragma unroll
-        for (int k = 0; k < PER; ++k) {
-            const int e = grp + k * G;
-            xa[k] = xb[k] = ga[k] = gb[k] = make_uint4(0, 0, 0, 0);
-            tok[k] = 0;
-            if (e < rows.n) {
-                tok[k] = rows.token(t, e);
-                const T* x = (const T*)t.x + rows.at(p, t, t.xs, e, tok[k]);
-                const T* g = (const T*)t.g + rows.at(p, t, t.gs, e, tok[k]);
-                if (o.n > 0) {
-                    xa[k] = *reinterpret_cast<const uint4*>(x + o.d0);
-                    ga[k] = *reinterpret_cast<const uint4*>(g + o.d0);
-                }
-                if (o.n > 1) {
-                    xb[k] = *reinterpret_cast<const uint4*>(x + o.d1);
-                    gb[k] = *reinterpret_cast<const uint4*>(g + o.d1);
-                }
+    for (int i = 0; i < V; ++i) sa[i] = sb[i] = 0.f;
+    const int64_t all = p.T0 * p.T1 * t.H, step = (int64_t)t.blocks * (G * PER);
+    uint4 xa[PER], xb[PER], ga[PER], gb[PER];
+    auto load = [&](const NormRows& rows, int k) {
+        const int e = grp + k * G;
+        xa[k] = xb[k] = ga[k] = gb[k] = make_uint4(0, 0, 0, 0);
+        if (e < rows.n) {
+            const int tok = rows.token(t, e);
+            const T* x = (const T*)t.x + rows.at(p, t, t.xs, e, tok);
+            const T* g = (const T*)t.g + rows.at(p, t, t.gs, e, tok);
+            if (o.n > 0) {
+                xa[k] = *reinterpret_cast<const uint4*>(x + o.d0);
+                ga[k] = *reinterpret_cast<const uint4*>(g + o.d0);
+            }
+            if (o.n > 1) {
+                xb[k] = *reinterpret_cast<const uint4*>(x + o.d1);
+                gb[k] = *reinterpret_cast<const uint4*>(g + o.d1);
             }
         }
-        __syncthreads();  // the angles before are read
-        rows.angles(p, t, s_cs);
+    };
+    int64_t first = (int64_t)(blockIdx.x - (which ? p.t[0].blocks : 0)) * (G * PER);
+    NormRows rows(p, t, first, G * PER);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) load(rows, k);
+    for (int odd = 0; first < all; first += step, odd ^= 1) {
+        float2* const cs = s_cs + odd * half_angles;
+        rows.angles<A>(p, t, cs);
         __syncthreads();
+        const NormRows next(p, t, first + step < all ? first + step : 0, first + step < all ? G * PER : 0);
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
-            const int e = grp + k * G;
-            float x0[V], x1[V], u0[V], u1[V];
+            const int e = grp + k * G, tok = e < rows.n ? rows.token(t, e) : 0;
+            float x0[V], x1[V], u0[V], u1[V], wa[V], wb[V];
             rope_unpack(xa[k], x0);
             rope_unpack(xb[k], x1);
             rope_unpack(ga[k], u0);
             rope_unpack(gb[k], u1);
-            if (e < rows.n) norm_turn<HALF, V>(o, s_cs + tok[k] * (p.r.R / 2), u0, u1);
+            load(next, k);
+            norm_turn<HALF, V>(o, cs + tok * R2, R2 / A, u0, u1);
+            norm_weights<LANES, V>(s_w, l, wa, wb);
             float s2 = 0.f, s3 = 0.f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 s2 += x0[i] * x0[i] + x1[i] * x1[i];
-                if (o.n > 0) s3 += u0[i] * s_w[o.d0 + i] * x0[i];
-                if (o.n > 1) s3 += u1[i] * s_w[o.d1 + i] * x1[i];
+                s3 += u0[i] * wa[i] * x0[i] + u1[i] * wb[i] * x1[i];
             }
             const float r = __frsqrt_rn(norm_sum<LANES>(s2) * p.inv_d + p.eps);
             const float c = r * r * (norm_sum<LANES>(s3) * p.inv_d);
             if (e >= rows.n || o.n == 0) continue;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                wa[i] += u0[i] * (x0[i] * r);
-                u0[i] = r * (u0[i] * s_w[o.d0 + i] - x0[i] * c);
-                if (o.n > 1) {
-                    wb[i] += u1[i] * (x1[i] * r);
-                    u1[i] = r * (u1[i] * s_w[o.d1 + i] - x1[i] * c);
-                }
+                sa[i] += u0[i] * (x0[i] * r);
+                u0[i] = r * (u0[i] * wa[i] - x0[i] * c);
+                sb[i] += u1[i] * (x1[i] * r);
+                u1[i] = r * (u1[i] * wb[i] - x1[i] * c);
             }
-            T* y = (T*)t.y + rows.at(p, t, t.ys, e, tok[k]);
+            T* y = (T*)t.y + rows.at(p, t, t.ys, e, tok);
             *reinterpret_cast<uint4*>(y + o.d0) = rope_pack(u0);
             if (o.n > 1) *reinterpret_cast<uint4*>(y + o.d1) = rope_pack(u1);
         }
+        rows = next;
     }
     // the block's sums: one row of smem a group, added in order
     __syncthreads();
     float* const s_sum = (float*)s_cs;  // [G][D]
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        if (o.n > 0) s_sum[grp * p.D + o.d0 + i] = wa[i];
-        if (o.n > 1) s_sum[grp * p.D + o.d1 + i] = wb[i];
+        if (o.n > 0) s_sum[grp * p.D + o.d0 + i] = sa[i];
+        if (o.n > 1) s_sum[grp * p.D + o.d1 + i] = sb[i];
     }
     __syncthreads();
     for (int d = threadIdx.x; d < p.D; d += kNormThreads) {
@@ -419,10 +455,10 @@ static bool norm_vectors(const NormParams& p, int nt, int V, int es, bool bwd) {
 }
 
 // Blocks of the backward, shared out by the tensors' rows.
-static void norm_share(NormParams& p, int nt, int rows) {
+static void norm_share(NormParams& p, int nt, int rows, int per_sm) {
     int64_t chunks[2] = {0, 0}, all = 0;
     for (int i = 0; i < nt; ++i) all += chunks[i] = (p.T0 * p.T1 * p.t[i].H + rows - 1) / rows;
-    const int64_t most = (int64_t)kNormBlocks * current_sms();
+    const int64_t most = (int64_t)per_sm * current_sms();
     for (int i = 0; i < nt; ++i) {
         int64_t n = all <= most ? chunks[i] : chunks[i] * (most - 1) / all;
         p.t[i].blocks = (int)(n < 1 ? 1 : n);
@@ -432,7 +468,8 @@ static void norm_share(NormParams& p, int nt, int rows) {
 template <class T, bool HALF, int LANES>
 static cudaError_t norm_launch_lanes(NormParams& p, int nt, bool bwd, cudaStream_t st) {
     constexpr int G = kNormThreads / LANES;
-    auto smem = [&](int rows) {  // weights, angles of the tokens of `rows` rows (or the sums of the groups)
+    constexpr int weights = 2 * (16 / (int)sizeof(T)) * LANES * 4;
+    auto smem = [&](int rows) {  // angles of the tokens of `rows` rows
         int64_t angles = 0;
         for (int i = 0; i < nt; ++i) {
             const int64_t n = (int64_t)((rows - 1) / p.t[i].H + 2) * (p.r.R / 2);
@@ -441,10 +478,15 @@ static cudaError_t norm_launch_lanes(NormParams& p, int nt, bool bwd, cudaStream
         return angles;
     };
     if (bwd) {
-        norm_share(p, nt, G * kNormPerBwd);
-        const int64_t a = smem(G * kNormPerBwd) * 8, s = (int64_t)G * p.D * 4;
-        norm_rope_bwd_kernel<T, HALF, LANES>
-            <<<p.t[0].blocks + p.t[1].blocks, kNormThreads, (int)((a > s ? a : s) + p.D * 4), st>>>(p);
+        norm_share(p, nt, G * kNormPerBwd, norm_bwd_blocks<T>());
+        const int64_t angles = smem(G * kNormPerBwd) + (smem(G * kNormPerBwd) & 1), a = 2 * angles * 8, s = (int64_t)G * p.D * 4;
+        const int bytes = (int)(a > s ? a : s) + weights;
+        auto* kernel = norm_rope_bwd_kernel<T, HALF, LANES>;
+        if (bytes > 48 * 1024) {
+            const cudaError_t e = set_smem_attr((const void*)kernel, bytes);
+            if (e != cudaSuccess) return e;
+        }
+        kernel<<<p.t[0].blocks + p.t[1].blocks, kNormThreads, bytes, st>>>(p, (int)angles);
         return cudaGetLastError();
     }
     constexpr int big = G * kNormPer;
@@ -456,7 +498,7 @@ static cudaError_t norm_launch_lanes(NormParams& p, int nt, bool bwd, cudaStream
         p.t[i].blocks = (int)n[i];
     }
     if (n[0] + n[1] > INT_MAX) return cudaErrorInvalidValue;
-    const int bytes = (int)smem(G * per) * 8 + p.D * 4;
+    const int bytes = (int)smem(G * per) * 8 + weights;
     if (per == kNormPer)
         norm_rope_kernel<T, HALF, LANES, kNormPer><<<(unsigned)(n[0] + n[1]), kNormThreads, bytes, st>>>(p);
     else
@@ -479,7 +521,7 @@ static cudaError_t norm_launch(NormParams& p, int nt, bool bwd, cudaStream_t st)
         return p.r.half ? norm_launch_vec<T, true>(p, nt, bwd, st) : norm_launch_vec<T, false>(p, nt, bwd, st);
     constexpr int rows = kNormThreads / 32;
     if (bwd) {
-        norm_share(p, nt, rows);
+        norm_share(p, nt, rows, kNormBlocks);
         norm_rope_any_kernel<T, true>
             <<<p.t[0].blocks + p.t[1].blocks, kNormThreads, rows * p.D * 4, st>>>(p);
         return cudaGetLastError();

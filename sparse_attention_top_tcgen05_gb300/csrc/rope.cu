@@ -72,7 +72,8 @@ constexpr int kRopeAngles = 4096;  // of a block's tokens: 32 KB
 template <class T, bool HALF, int PER>
 __global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(const __grid_constant__ RopeParams p) {
     constexpr int V = 16 / sizeof(T);
-    extern __shared__ float2 s_cs[];
+    constexpr int A = HALF ? V : V / 2;  // angles of an item
+    extern __shared__ __align__(16) float2 s_cs[];
     const int R2 = p.r.R / 2;
     const int rot = HALF ? R2 / V : p.r.R / V;      // rotated items of a head
     const int items = rot + (p.D - p.r.R) / V;      // then its copied vectors
@@ -84,7 +85,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(const __grid_con
     const int n = (int)min((int64_t)(PER * kRopeThreads), all - first);
     uint4 a[PER], b[PER];
     T* dst[PER];
-    int cs[PER];  // first angle of the item, -1: copied
+    int cs[PER];  // place of the item's first angles (16-byte words), -1: copied
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
         const int e = threadIdx.x + k * kRopeThreads;
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(const __grid_con
         int d;
         if (it < rot) {
             d = p.r.off + it * V;
-            cs[k] = t * R2 + (HALF ? it * V : it * (V / 2));
+            cs[k] = t * (R2 / 2) + it;
         } else {
             d = (it - rot) * V;
             if (d >= p.r.off) d += p.r.R;
@@ -112,14 +113,15 @@ __global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(const __grid_con
     for (int i = threadIdx.x; i < angles; i += kRopeThreads) {
         const int t = rope_quot(i, p.pairs);
         const uint32_t tok = tok0 + t, t0 = rope_quot(tok, p.tokens1), t1 = tok - t0 * (uint32_t)p.T1;
-        s_cs[i] = rope_cs(p.r, t0, t1, i - t * R2);
+        s_cs[t * R2 + rope_angle_at<A>(i - t * R2, rot)] = rope_cs(p.r, t0, t1, i - t * R2);
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
         if (threadIdx.x + k * kRopeThreads >= n) break;
         if (cs[k] >= 0) {
-            const float2* c = s_cs + cs[k];
+            float2 c[A];
+            rope_angles_of<A>(s_cs, cs[k], rot, c);
             float f[V];
             rope_unpack(a[k], f);
             if constexpr (HALF) {

@@ -89,6 +89,24 @@ __device__ __forceinline__ uint4 rope_pack(const float (&f)[8]) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Angles in shared memory.  An item (a vector of the interleaved layout, a pair of vectors of the half layout) has A
+// consecutive angles; two of them are a 16-byte word, and the items' k-th words follow each other, so that lanes with
+// neighbouring items read neighbouring words: with an item's angles side by side their reads met in the same banks.
+template <int A>
+__device__ __forceinline__ int rope_angle_at(int u, int items) {  // place of angle u of a token
+    const int item = u / A, j = u % A;
+    return ((j >> 1) * items + item) * 2 + (j & 1);
+}
+template <int A>
+__device__ __forceinline__ void rope_angles_of(const float2* token, int item, int items, float2 (&c)[A]) {
+#pragma unroll
+    for (int k = 0; k < A / 2; ++k) {
+        const float4 v = reinterpret_cast<const float4*>(token)[k * items + item];
+        c[2 * k] = make_float2(v.x, v.y);
+        c[2 * k + 1] = make_float2(v.z, v.w);
+    }
+}
+
 // Rules of a rotation's host arguments (see lidx.h), and its device form.  own_pos: pos may be NULL.
 int rope_turn(const lidx_rope_turn* r, int D, int inverse, RopeTurn& out, bool own_pos = false);
 int rope_turn_aligned(const lidx_rope_turn& r);
