@@ -50,14 +50,14 @@ struct AttnCfg {
                       OFF_GATHER % 16 == 0 && OFF_MISC % 8 == 0,
                   "16-byte reads");
     static constexpr int TMEM = 4 * MN;                                // columns: two tiles of S and of O
-    // Warpgroups: MMA and queries (4 bits: and the producers); two of softmax; joining; producers (4 bits: WIDE that widen).
-    static constexpr int WIDE = BITS == 8 ? 0 : (NC == 8 ? 4 : 2);
-    static constexpr int THREADS = BITS == 8 ? 640 : 512 + 128 * WIDE, PRODUCERS = BITS == 8 ? 4 : 2, QWARPS = BITS == 8 ? 3 : 1;
+    // Warpgroups: MMA and queries (4 bits: and the producers); two of softmax; joining; producers (4 bits: two that widen, K
+    // tiles and V tiles).
+    static constexpr int THREADS = BITS == 8 ? 640 : 768, PRODUCERS = BITS == 8 ? 4 : 2, QWARPS = BITS == 8 ? 3 : 1;
     static constexpr int W_QUERY = 1, W_SOFT = 4, W_JOIN = 12, W_PROD = 16;  // first warps
     // registers a thread of each group: their sum is at most what the launch has
-    static constexpr int R_LAUNCH = BITS == 8 ? 96 : (NC == 8 ? 64 : 80), R_MMA = BITS == 8 ? 64 : (SPLIT ? 72 : (NC == 8 ? 64 : 80));
-    static constexpr int R_SOFT = BITS == 8 ? 112 : (NC == 8 ? 80 : 96), R_JOIN = BITS == 8 || SPLIT ? 104 : (NC == 8 ? 64 : 80);
-    static constexpr int R_PROD = BITS == 8 ? 88 : (NC == 8 || SPLIT ? 56 : 64);
+    static constexpr int R_LAUNCH = BITS == 8 ? 96 : 80, R_MMA = BITS == 8 ? 64 : (SPLIT ? 72 : 80);
+    static constexpr int R_SOFT = BITS == 8 ? 112 : (NC == 8 ? 88 : 96), R_JOIN = BITS == 8 || SPLIT ? 104 : 80;
+    static constexpr int R_PROD = BITS == 8 ? 88 : (SPLIT ? 56 : 64);
     static_assert(R_LAUNCH == 65536 / THREADS / 8 * 8 &&
                       R_MMA + SG * R_SOFT + R_JOIN + R_PROD * (THREADS / 32 - W_PROD) / 4 <= R_LAUNCH * (THREADS / 128),
                   "register split");
@@ -599,8 +599,7 @@ __global__ void __launch_bounds__(AttnCfg<N, NC_, BITS>::THREADS, 1)
             else
                 attn_produce<SLOTS, C::PRODUCERS, false>(p, wk, x, &tmk, &tmv, warp - C::W_PROD, lane);
         } else {
-            // the groups take the K and V tiles in turn: even ones the K tiles, odd ones the V tiles
-            attn_widen<RING, C::PACKED, C::WIDE>(p, wk, x, (warp - C::W_PROD) >> 2, warp & 3, lane);
+            attn_widen<RING, C::PACKED, 2>(p, wk, x, (warp - C::W_PROD) >> 2, warp & 3, lane);
         }
     }
 
