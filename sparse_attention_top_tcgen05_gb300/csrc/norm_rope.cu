@@ -37,13 +37,14 @@ struct NormParams {
 };
 
 constexpr int kNormThreads = 256;
-constexpr int kNormPer = 4;         // rows a thread, forward
-constexpr int kNormPerBwd = 2;
+// Rows a thread, blocks an SM.  Forward (2 x 8192 tokens of 72 bf16 heads): two rows and five blocks 104.7 us, two and as many as
+// fit 110.5 us, four 107.4 us.  Backward, whose blocks go over all rows (4095 tokens of 40 fp32 heads): one row and four blocks
+// 46.6 us, two and three 51.2 us.
+constexpr int kNormPer = 2;
 constexpr int kNormAngles = 4096;   // of a block's tokens: 32 KB
-// Blocks an SM of the backward, which go over all rows: as many as its registers allow without spills.
-constexpr int kNormBlocks = 3;
+constexpr int kNormBlocks = 4;
 template <class T>
-constexpr int norm_bwd_blocks() { return sizeof(T) == 4 ? kNormBlocks : 2; }
+constexpr int norm_bwd_blocks() { return sizeof(T) == 4 ? kNormBlocks : 2; }  // (without spills)
 
 __device__ __forceinline__ float norm_weight(const NormParams& p, const void* w, int d) {
     if (!w) return 1.f;
@@ -85,63 +86,95 @@ static int norm_lanes(const RopeTurn& r, int D, int V) {
     return r.half ? r.R / 2 / V + ((D - r.R) / V + 1) / 2 : (D / V + 1) / 2;
 }
 
-// The two vectors of a lane turn.  cs: angles of the row's token; items: rotated items of a head.
+// A lane's elements as P and Q: element i of P and element i of Q are a pair (half layout: of the two vectors; interleaved:
+// neighbours, the first vector's and then the second's).  Two neighbouring elements of either are an operand of packed
+// arithmetic.
+template <bool HALF, class T, int V>
+__device__ __forceinline__ void norm_unpack(const uint4& a, const uint4& b, float (&P)[V], float (&Q)[V]) {
+    float f[V], g[V];
+    rope_unpack(a, f);
+    rope_unpack(b, g);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        P[i] = HALF ? f[i] : (i < V / 2 ? f[2 * i] : g[2 * i - V]);
+        Q[i] = HALF ? g[i] : (i < V / 2 ? f[2 * i + 1] : g[2 * i + 1 - V]);
+    }
+}
 template <bool HALF, int V>
-__device__ __forceinline__ void norm_turn(const NormLane& o, const float2* cs, int items, float (&a)[V], float (&b)[V]) {
-    constexpr int A = HALF ? V : V / 2;
-    float2 c[A];
+__device__ __forceinline__ void norm_pack(const float (&P)[V], const float (&Q)[V], uint4& a, uint4& b) {
+    float f[V], g[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        f[i] = HALF ? P[i] : (i % 2 ? Q[i / 2] : P[i / 2]);
+        g[i] = HALF ? Q[i] : (i % 2 ? Q[V / 2 + i / 2] : P[V / 2 + i / 2]);
+    }
+    a = rope_pack(f);
+    b = rope_pack(g);
+}
+// Place of element i of P (q: of Q) among the lane's dims.
+template <bool HALF, int V>
+__device__ __forceinline__ int norm_dim(const NormLane& o, int i, bool q) {
+    if (HALF) return (q ? o.d1 : o.d0) + i;
+    return (i < V / 2 ? o.d0 + 2 * i : o.d1 + 2 * i - V) + q;
+}
+template <bool HALF, int V>
+__device__ __forceinline__ bool norm_has(const NormLane& o, int i, bool q) {
+    return o.n > (HALF ? q : i >= V / 2);
+}
+
+// Pairs turn.  cs: angles of the row's token; items: rotated items of a head.
+template <bool HALF, int V>
+__device__ __forceinline__ void norm_turn(const NormLane& o, const float2* cs, int items, float (&P)[V], float (&Q)[V]) {
+    auto turn = [&](int i0, int n, int item) {
+#pragma unroll
+        for (int k = 0; k < n / 2; ++k) {
+            const int i = i0 + 2 * k;
+            const float4 v = reinterpret_cast<const float4*>(cs)[k * items + item];
+            const uint64_t c = pack2(v.x, v.y), s = pack2(v.z, v.w), m = pack2(-v.z, -v.w);
+            const uint64_t a = pack2(P[i], P[i + 1]), b = pack2(Q[i], Q[i + 1]);
+            unpack2(fma2(b, m, mul2(a, c)), P[i], P[i + 1]);
+            unpack2(fma2(a, s, mul2(b, c)), Q[i], Q[i + 1]);
+        }
+    };
     if constexpr (HALF) {
-        if (o.c0 >= 0) {
-            rope_angles_of<A>(cs, o.c0, items, c);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float u = a[i], w = b[i];
-                a[i] = u * c[i].x - w * c[i].y;
-                b[i] = w * c[i].x + u * c[i].y;
-            }
-        }
+        if (o.c0 >= 0) turn(0, V, o.c0);
     } else {
-        if (o.c0 >= 0) {
-            rope_angles_of<A>(cs, o.c0, items, c);
-#pragma unroll
-            for (int i = 0; i < A; ++i) {
-                const float u = a[2 * i], w = a[2 * i + 1];
-                a[2 * i] = u * c[i].x - w * c[i].y;
-                a[2 * i + 1] = w * c[i].x + u * c[i].y;
-            }
-        }
-        if (o.c1 >= 0) {
-            rope_angles_of<A>(cs, o.c1, items, c);
-#pragma unroll
-            for (int i = 0; i < A; ++i) {
-                const float u = b[2 * i], w = b[2 * i + 1];
-                b[2 * i] = u * c[i].x - w * c[i].y;
-                b[2 * i + 1] = w * c[i].x + u * c[i].y;
-            }
-        }
+        if (o.c0 >= 0) turn(0, V / 2, o.c0);
+        if (o.c1 >= 0) turn(V / 2, V / 2, o.c1);
     }
 }
 
-// Weights in shared memory, words of 16 bytes: the lanes' k-th words follow each other.
-template <int LANES, int V>
+// Weights in shared memory as the lanes' P and Q, words of 16 bytes: the lanes' k-th words follow each other.
+template <bool HALF, int LANES, int V>
 __device__ __forceinline__ void norm_load_weights(const NormParams& p, const void* w, const NormLane& o, float* s_w) {
-    if (threadIdx.x < LANES) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            s_w[(i / 4 * LANES + threadIdx.x) * 4 + i % 4] = o.n > 0 ? norm_weight(p, w, o.d0 + i) : 0.f;
-            s_w[((V + i) / 4 * LANES + threadIdx.x) * 4 + i % 4] = o.n > 1 ? norm_weight(p, w, o.d1 + i) : 0.f;
-        }
+    for (int e = threadIdx.x / LANES; e < 2 * V; e += kNormThreads / LANES) {
+        const int i = e % V;
+        const bool q = e >= V;
+        s_w[(e / 4 * LANES + threadIdx.x % LANES) * 4 + e % 4] =
+            norm_has<HALF, V>(o, i, q) ? norm_weight(p, w, norm_dim<HALF, V>(o, i, q)) : 0.f;
     }
 }
+// P (or Q) times weights and r; returns the pairs.
 template <int LANES, int V>
-__device__ __forceinline__ void norm_weights(const float* s_w, int l, float (&wa)[V], float (&wb)[V]) {
+__device__ __forceinline__ void norm_weights(const float* s_w, int l, int part, uint64_t (&w)[V / 2]) {
 #pragma unroll
     for (int i = 0; i < V; i += 4) {
-        const float4 a = reinterpret_cast<const float4*>(s_w)[i / 4 * LANES + l];
-        const float4 b = reinterpret_cast<const float4*>(s_w)[(V + i) / 4 * LANES + l];
-        wa[i] = a.x, wa[i + 1] = a.y, wa[i + 2] = a.z, wa[i + 3] = a.w;
-        wb[i] = b.x, wb[i + 1] = b.y, wb[i + 2] = b.z, wb[i + 3] = b.w;
+        const float4 a = reinterpret_cast<const float4*>(s_w)[(part * V + i) / 4 * LANES + l];
+        w[i / 2] = pack2(a.x, a.y);
+        w[i / 2 + 1] = pack2(a.z, a.w);
     }
+}
+template <int V>
+__device__ __forceinline__ float norm_dot(const float (&a)[V], const float (&b)[V], const float (&c)[V], const float (&d)[V]) {
+    uint64_t s = pack2(0.f, 0.f), t = s;  // a . b + c . d
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+        s = fma2(pack2(a[i], a[i + 1]), pack2(b[i], b[i + 1]), s);
+        t = fma2(pack2(c[i], c[i + 1]), pack2(d[i], d[i + 1]), t);
+    }
+    float x, y;
+    unpack2(add2(s, t), x, y);
+    return x + y;
 }
 
 template <int LANES>
@@ -161,11 +194,14 @@ struct NormRows {
         skip = (int)(first - tok0 * t.H);
         n = (int)min((int64_t)rows, all - first);
     }
-    // token of the block, and place of row e with strides s
+    // token of the block, and places of row e with strides s and z
     __device__ int token(const NormTensor& t, int e) const { return (int)rope_quot(skip + e, t.heads); }
-    __device__ int64_t at(const NormParams& p, const NormTensor& t, const int64_t (&s)[3], int e, int tok) const {
+    __device__ void at(const NormParams& p, const NormTensor& t, const int64_t (&s)[3], const int64_t (&z)[3], int e, int tok,
+                       int64_t (&out)[2]) const {
         const uint32_t k = (uint32_t)tok0 + tok, t0 = rope_quot(k, p.tokens1), t1 = k - t0 * (uint32_t)p.T1;
-        return t0 * s[0] + t1 * s[1] + (int64_t)(skip + e - tok * t.H) * s[2];
+        const int h = skip + e - tok * t.H;
+        out[0] = t0 * s[0] + t1 * s[1] + h * s[2];
+        out[1] = t0 * z[0] + t1 * z[1] + h * z[2];
     }
     // angles of the block's tokens; A of an item
     template <int A>
@@ -174,13 +210,13 @@ struct NormRows {
         for (int i = threadIdx.x; i < all; i += kNormThreads) {
             const int k = rope_quot(i, p.pairs);
             const uint32_t tok = (uint32_t)tok0 + k, t0 = rope_quot(tok, p.tokens1), t1 = tok - t0 * (uint32_t)p.T1;
-            s_cs[k * R2 + rope_angle_at<A>(i - k * R2, R2 / A)] = rope_cs(p.r, t0, t1, i - k * R2);
+            rope_put_angle<A>(s_cs + k * R2, i - k * R2, R2 / A, rope_cs(p.r, t0, t1, i - k * R2));
         }
     }
 };
 
 template <class T, bool HALF, int LANES, int PER>
-__global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kNormThreads, 5) norm_rope_kernel(const __grid_constant__ NormParams p) {
     constexpr int V = 16 / sizeof(T), G = kNormThreads / LANES, A = HALF ? V : V / 2;
     extern __shared__ __align__(16) float s_norm[];
     float* const s_w = s_norm;                               // [2 V / 4][LANES] words
@@ -193,43 +229,45 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_co
     const NormLane o = norm_lane<HALF, V>(p.r, p.D, l);
     uint4 a[PER], b[PER];
     int tok[PER];
+    T* y[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
         const int e = grp + k * G;
         a[k] = b[k] = make_uint4(0, 0, 0, 0);
         tok[k] = 0;
+        y[k] = nullptr;
         if (e < rows.n) {
+            int64_t at[2];
             tok[k] = rows.token(t, e);
-            const T* x = (const T*)t.x + rows.at(p, t, t.xs, e, tok[k]);
+            rows.at(p, t, t.xs, t.ys, e, tok[k], at);
+            const T* x = (const T*)t.x + at[0];
+            y[k] = (T*)t.y + at[1];
             if (o.n > 0) a[k] = *reinterpret_cast<const uint4*>(x + o.d0);
             if (o.n > 1) b[k] = *reinterpret_cast<const uint4*>(x + o.d1);
         }
     }
-    norm_load_weights<LANES, V>(p, t.w, o, s_w);
+    norm_load_weights<HALF, LANES, V>(p, t.w, o, s_w);
     rows.angles<A>(p, t, s_cs);
     __syncthreads();
     const int R2 = p.r.R / 2;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-        const int e = grp + k * G;
-        float f[V], g[V], wa[V], wb[V];
-        rope_unpack(a[k], f);
-        rope_unpack(b[k], g);
-        float ss = 0.f;
+        float P[V], Q[V];
+        norm_unpack<HALF, T, V>(a[k], b[k], P, Q);
+        const float r = __frsqrt_rn(norm_sum<LANES>(norm_dot(P, P, Q, Q)) * p.inv_d + p.eps);
+        if (!y[k] || o.n == 0) continue;
+        const uint64_t r2 = pack2(r, r);
+        uint64_t w[V / 2];
+        norm_weights<LANES, V>(s_w, l, 0, w);
 #pragma unroll
-        for (int i = 0; i < V; ++i) ss += f[i] * f[i] + g[i] * g[i];
-        const float r = __frsqrt_rn(norm_sum<LANES>(ss) * p.inv_d + p.eps);
-        if (e >= rows.n || o.n == 0) continue;
-        norm_weights<LANES, V>(s_w, l, wa, wb);
+        for (int i = 0; i < V; i += 2) unpack2(mul2(pack2(P[i], P[i + 1]), mul2(r2, w[i / 2])), P[i], P[i + 1]);
+        norm_weights<LANES, V>(s_w, l, 1, w);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            f[i] *= r * wa[i];
-            g[i] *= r * wb[i];
-        }
-        norm_turn<HALF, V>(o, s_cs + tok[k] * R2, R2 / A, f, g);
-        T* y = (T*)t.y + rows.at(p, t, t.ys, e, tok[k]);
-        *reinterpret_cast<uint4*>(y + o.d0) = rope_pack(f);
-        if (o.n > 1) *reinterpret_cast<uint4*>(y + o.d1) = rope_pack(g);
+        for (int i = 0; i < V; i += 2) unpack2(mul2(pack2(Q[i], Q[i + 1]), mul2(r2, w[i / 2])), Q[i], Q[i + 1]);
+        norm_turn<HALF, V>(o, s_cs + tok[k] * R2, R2 / A, P, Q);
+        norm_pack<HALF, V>(P, Q, a[k], b[k]);
+        *reinterpret_cast<uint4*>(y[k] + o.d0) = a[k];
+        if (o.n > 1) *reinterpret_cast<uint4*>(y[k] + o.d1) = b[k];
     }
 }
 
@@ -238,7 +276,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_co
 template <class T, bool HALF, int LANES>
 __global__ void __launch_bounds__(kNormThreads, norm_bwd_blocks<T>()) norm_rope_bwd_kernel(const __grid_constant__ NormParams p,
                                                                                 int half_angles) {
-    constexpr int V = 16 / sizeof(T), G = kNormThreads / LANES, PER = kNormPerBwd, A = HALF ? V : V / 2;
+    constexpr int V = 16 / sizeof(T), G = kNormThreads / LANES, A = HALF ? V : V / 2;
     extern __shared__ __align__(16) float s_norm[];
     float* const s_w = s_norm;
     float2* const s_cs = (float2*)(s_norm + 2 * V * LANES);  // two halves of half_angles
@@ -247,68 +285,71 @@ __global__ void __launch_bounds__(kNormThreads, norm_bwd_blocks<T>()) norm_rope_
     const int l = threadIdx.x % LANES, grp = threadIdx.x / LANES, R2 = p.r.R / 2;
     const NormLane o = norm_lane<HALF, V>(p.r, p.D, l);
     grid_dependency_launch();
-    norm_load_weights<LANES, V>(p, t.w, o, s_w);
-    float sa[V], sb[V];  // sums of u h
+    norm_load_weights<HALF, LANES, V>(p, t.w, o, s_w);
+    float sp[V], sq[V];  // sums of u h
 #pragma unroll
-    for (int i = 0; i < V; ++i) sa[i] = sb[i] = 0.f;
-    const int64_t all = p.T0 * p.T1 * t.H, step = (int64_t)t.blocks * (G * PER);
-    uint4 xa[PER], xb[PER], ga[PER], gb[PER];
-    auto load = [&](const NormRows& rows, int k) {
-        const int e = grp + k * G;
-        xa[k] = xb[k] = ga[k] = gb[k] = make_uint4(0, 0, 0, 0);
-        if (e < rows.n) {
-            const int tok = rows.token(t, e);
-            const T* x = (const T*)t.x + rows.at(p, t, t.xs, e, tok);
-            const T* g = (const T*)t.g + rows.at(p, t, t.gs, e, tok);
+    for (int i = 0; i < V; ++i) sp[i] = sq[i] = 0.f;
+    const int64_t all = p.T0 * p.T1 * t.H, step = (int64_t)t.blocks * G;
+    uint4 xa, xb, ga, gb;
+    auto load = [&](const NormRows& rows) {
+        xa = xb = ga = gb = make_uint4(0, 0, 0, 0);
+        if (grp < rows.n) {
+            int64_t at[2];
+            rows.at(p, t, t.xs, t.gs, grp, rows.token(t, grp), at);
+            const T* x = (const T*)t.x + at[0];
+            const T* g = (const T*)t.g + at[1];
             if (o.n > 0) {
-                xa[k] = *reinterpret_cast<const uint4*>(x + o.d0);
-                ga[k] = *reinterpret_cast<const uint4*>(g + o.d0);
+                xa = *reinterpret_cast<const uint4*>(x + o.d0);
+                ga = *reinterpret_cast<const uint4*>(g + o.d0);
             }
             if (o.n > 1) {
-                xb[k] = *reinterpret_cast<const uint4*>(x + o.d1);
-                gb[k] = *reinterpret_cast<const uint4*>(g + o.d1);
+                xb = *reinterpret_cast<const uint4*>(x + o.d1);
+                gb = *reinterpret_cast<const uint4*>(g + o.d1);
             }
         }
     };
-    int64_t first = (int64_t)(blockIdx.x - (which ? p.t[0].blocks : 0)) * (G * PER);
-    NormRows rows(p, t, first, G * PER);
-#pragma unroll
-    for (int k = 0; k < PER; ++k) load(rows, k);
+    int64_t first = (int64_t)(blockIdx.x - (which ? p.t[0].blocks : 0)) * G;
+    NormRows rows(p, t, first, G);
+    load(rows);
     for (int odd = 0; first < all; first += step, odd ^= 1) {
         float2* const cs = s_cs + odd * half_angles;
         rows.angles<A>(p, t, cs);
         __syncthreads();
-        const NormRows next(p, t, first + step < all ? first + step : 0, first + step < all ? G * PER : 0);
+        const NormRows next(p, t, first + step < all ? first + step : 0, first + step < all ? G : 0);
+        const int tok = grp < rows.n ? rows.token(t, grp) : 0;
+        float xp[V], xq[V], up[V], uq[V], tp[V], tq[V];
+        norm_unpack<HALF, T, V>(xa, xb, xp, xq);
+        norm_unpack<HALF, T, V>(ga, gb, up, uq);
+        load(next);
+        norm_turn<HALF, V>(o, cs + tok * R2, R2 / A, up, uq);
+        uint64_t w[V / 2];
+        norm_weights<LANES, V>(s_w, l, 0, w);
 #pragma unroll
-        for (int k = 0; k < PER; ++k) {
-            const int e = grp + k * G, tok = e < rows.n ? rows.token(t, e) : 0;
-            float x0[V], x1[V], u0[V], u1[V], wa[V], wb[V];
-            rope_unpack(xa[k], x0);
-            rope_unpack(xb[k], x1);
-            rope_unpack(ga[k], u0);
-            rope_unpack(gb[k], u1);
-            load(next, k);
-            norm_turn<HALF, V>(o, cs + tok * R2, R2 / A, u0, u1);
-            norm_weights<LANES, V>(s_w, l, wa, wb);
-            float s2 = 0.f, s3 = 0.f;
+        for (int i = 0; i < V; i += 2) unpack2(mul2(pack2(up[i], up[i + 1]), w[i / 2]), tp[i], tp[i + 1]);
+        norm_weights<LANES, V>(s_w, l, 1, w);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                s2 += x0[i] * x0[i] + x1[i] * x1[i];
-                s3 += u0[i] * wa[i] * x0[i] + u1[i] * wb[i] * x1[i];
-            }
-            const float r = __frsqrt_rn(norm_sum<LANES>(s2) * p.inv_d + p.eps);
-            const float c = r * r * (norm_sum<LANES>(s3) * p.inv_d);
-            if (e >= rows.n || o.n == 0) continue;
+        for (int i = 0; i < V; i += 2) unpack2(mul2(pack2(uq[i], uq[i + 1]), w[i / 2]), tq[i], tq[i + 1]);
+        const float r = __frsqrt_rn(norm_sum<LANES>(norm_dot(xp, xp, xq, xq)) * p.inv_d + p.eps);
+        const float c = -r * r * (norm_sum<LANES>(norm_dot(tp, xp, tq, xq)) * p.inv_d);
+        if (grp < rows.n && o.n > 0) {
+            const uint64_t r2 = pack2(r, r), c2 = pack2(c, c);
+            auto grad = [&](const float (&x)[V], const float (&u)[V], float (&t)[V], float (&sum)[V]) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                sa[i] += u0[i] * (x0[i] * r);
-                u0[i] = r * (u0[i] * wa[i] - x0[i] * c);
-                sb[i] += u1[i] * (x1[i] * r);
-                u1[i] = r * (u1[i] * wb[i] - x1[i] * c);
-            }
-            T* y = (T*)t.y + rows.at(p, t, t.ys, e, tok);
-            *reinterpret_cast<uint4*>(y + o.d0) = rope_pack(u0);
-            if (o.n > 1) *reinterpret_cast<uint4*>(y + o.d1) = rope_pack(u1);
+                for (int i = 0; i < V; i += 2) {
+                    const uint64_t x2 = pack2(x[i], x[i + 1]);
+                    unpack2(fma2(pack2(u[i], u[i + 1]), mul2(x2, r2), pack2(sum[i], sum[i + 1])), sum[i], sum[i + 1]);
+                    unpack2(mul2(r2, fma2(x2, c2, pack2(t[i], t[i + 1]))), t[i], t[i + 1]);
+                }
+            };
+            grad(xp, up, tp, sp);
+            grad(xq, uq, tq, sq);
+            int64_t at[2];
+            rows.at(p, t, t.ys, t.ys, grp, tok, at);
+            T* y = (T*)t.y + at[0];
+            uint4 a, b;
+            norm_pack<HALF, V>(tp, tq, a, b);
+            *reinterpret_cast<uint4*>(y + o.d0) = a;
+            if (o.n > 1) *reinterpret_cast<uint4*>(y + o.d1) = b;
         }
         rows = next;
     }
@@ -317,8 +358,8 @@ __global__ void __launch_bounds__(kNormThreads, norm_bwd_blocks<T>()) norm_rope_
     float* const s_sum = (float*)s_cs;  // [G][D]
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        if (o.n > 0) s_sum[grp * p.D + o.d0 + i] = sa[i];
-        if (o.n > 1) s_sum[grp * p.D + o.d1 + i] = sb[i];
+        if (norm_has<HALF, V>(o, i, false)) s_sum[grp * p.D + norm_dim<HALF, V>(o, i, false)] = sp[i];
+        if (norm_has<HALF, V>(o, i, true)) s_sum[grp * p.D + norm_dim<HALF, V>(o, i, true)] = sq[i];
     }
     __syncthreads();
     for (int d = threadIdx.x; d < p.D; d += kNormThreads) {
@@ -478,8 +519,8 @@ static cudaError_t norm_launch_lanes(NormParams& p, int nt, bool bwd, cudaStream
         return angles;
     };
     if (bwd) {
-        norm_share(p, nt, G * kNormPerBwd, norm_bwd_blocks<T>());
-        const int64_t angles = smem(G * kNormPerBwd) + (smem(G * kNormPerBwd) & 1), a = 2 * angles * 8, s = (int64_t)G * p.D * 4;
+        norm_share(p, nt, G, norm_bwd_blocks<T>());
+        const int64_t angles = smem(G) + (smem(G) & 1), a = 2 * angles * 8, s = (int64_t)G * p.D * 4;
         const int bytes = (int)(a > s ? a : s) + weights;
         auto* kernel = norm_rope_bwd_kernel<T, HALF, LANES>;
         if (bytes > 48 * 1024) {

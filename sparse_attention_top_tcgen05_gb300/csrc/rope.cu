@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(const __grid_con
     for (int i = threadIdx.x; i < angles; i += kRopeThreads) {
         const int t = rope_quot(i, p.pairs);
         const uint32_t tok = tok0 + t, t0 = rope_quot(tok, p.tokens1), t1 = tok - t0 * (uint32_t)p.T1;
-        s_cs[t * R2 + rope_angle_at<A>(i - t * R2, rot)] = rope_cs(p.r, t0, t1, i - t * R2);
+        rope_put_angle<A>(s_cs + t * R2, i - t * R2, rot, rope_cs(p.r, t0, t1, i - t * R2));
     }
     __syncthreads();
 #pragma unroll

@@ -90,20 +90,23 @@ __device__ __forceinline__ uint4 rope_pack(const float (&f)[8]) {
 }
 
 // Angles in shared memory.  An item (a vector of the interleaved layout, a pair of vectors of the half layout) has A
-// consecutive angles; two of them are a 16-byte word, and the items' k-th words follow each other, so that lanes with
-// neighbouring items read neighbouring words: with an item's angles side by side their reads met in the same banks.
+// consecutive angles; two of them are a 16-byte word (two cosines, two sines: operands of packed arithmetic), and the items'
+// k-th words follow each other, so that lanes with neighbouring items read neighbouring words: with an item's angles side by
+// side their reads met in the same banks.
 template <int A>
-__device__ __forceinline__ int rope_angle_at(int u, int items) {  // place of angle u of a token
+__device__ __forceinline__ void rope_put_angle(float2* token, int u, int items, const float2& c) {  // angle u of a token
     const int item = u / A, j = u % A;
-    return ((j >> 1) * items + item) * 2 + (j & 1);
+    float* at = reinterpret_cast<float*>(token) + ((j >> 1) * items + item) * 4 + (j & 1);
+    at[0] = c.x;
+    at[2] = c.y;
 }
 template <int A>
 __device__ __forceinline__ void rope_angles_of(const float2* token, int item, int items, float2 (&c)[A]) {
 #pragma unroll
     for (int k = 0; k < A / 2; ++k) {
         const float4 v = reinterpret_cast<const float4*>(token)[k * items + item];
-        c[2 * k] = make_float2(v.x, v.y);
-        c[2 * k + 1] = make_float2(v.z, v.w);
+        c[2 * k] = make_float2(v.x, v.z);
+        c[2 * k + 1] = make_float2(v.y, v.w);
     }
 }
 

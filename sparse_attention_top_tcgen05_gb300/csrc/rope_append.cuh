@@ -13,6 +13,7 @@
 // page's tokens are computed once a block into shared memory and serve its heads.
 #pragma once
 #include "cache.cuh"
+#include "ptx.cuh"
 #include "rope.cuh"
 
 namespace lidx {
@@ -67,6 +68,16 @@ __device__ __forceinline__ uint32_t ra_block_max(uint32_t m, uint32_t* s) {
     return m;
 }
 
+// Largest size of a lane's 16 dims; NaN where one is.
+__device__ __forceinline__ float ra_size(const float (&y)[16]) {
+    float g = fabsf(y[0]);
+#pragma unroll
+    for (int i = 1; i < 15; i += 2) g = max3_nan(g, fabsf(y[i]), fabsf(y[i + 1]));
+    return max_nan(g, fabsf(y[15]));
+}
+// Two neighbouring dims times f.
+__device__ __forceinline__ void ra_times(float& a, float& b, uint64_t f) { unpack2(mul2(pack2(a, b), f), a, b); }
+
 template <int BITS, int LANES, int MODE, int PER>
 __global__ void __launch_bounds__(kRaThreads, PER == 4 ? 2 : 3) rope_append_kernel(const __grid_constant__ RopeAppendParams p) {
     constexpr int G = kRaThreads / LANES;                                // tokens a pass, PER passes
@@ -115,7 +126,10 @@ __global__ void __launch_bounds__(kRaThreads, PER == 4 ? 2 : 3) rope_append_kern
             const int e = rope_quot(i, p.pairs), u = i - e * R2;
             const int64_t at = lo - start + e;
             const float2 c = p.r.pos ? rope_cs(p.r, b, at, u) : rope_cs((int)(lo + e), p.r.freqs[u], p.r.mscale, 1.f);
-            s_cs[e * R2 + (MODE == kRaAny ? u : rope_angle_at<A>(u, R2 / A))] = c;
+            if constexpr (MODE == kRaAny)
+                s_cs[e * R2 + u] = c;
+            else
+                rope_put_angle<A>(s_cs + e * R2, u, R2 / A, c);
         }
     }
     if (norms && threadIdx.x < LANES && on) {
@@ -136,15 +150,20 @@ __global__ void __launch_bounds__(kRaThreads, PER == 4 ? 2 : 3) rope_append_kern
         }
         if (h + 1 < hz) load(h + 1);
         uint32_t top = 0;
+        float size[PER];  // of the lane's dims
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
-            if (k * G >= n) break;
+            size[k] = 0.f;
+            if (k * G >= n) continue;
             const int e = grp + k * G;
             float(&y)[16] = f[k];
             if (norms) {
-                float ss = 0.f;
+                uint64_t s2 = pack2(0.f, 0.f);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) ss += y[i] * y[i];
+                for (int i = 0; i < 16; i += 2) s2 = fma2(pack2(y[i], y[i + 1]), pack2(y[i], y[i + 1]), s2);
+                float ss, odd;
+                unpack2(s2, ss, odd);
+                ss += odd;
 #pragma unroll
                 for (int i = 1; i < LANES; i <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, i);
                 const float r = __frsqrt_rn(ss * p.inv_d + p.eps);
@@ -152,7 +171,8 @@ __global__ void __launch_bounds__(kRaThreads, PER == 4 ? 2 : 3) rope_append_kern
 #pragma unroll
                     for (int i = 0; i < 16; i += 4) {
                         const float4 w = reinterpret_cast<const float4*>(s_w)[i / 4 * LANES + l];
-                        y[i] *= r * w.x, y[i + 1] *= r * w.y, y[i + 2] *= r * w.z, y[i + 3] *= r * w.w;
+                        ra_times(y[i], y[i + 1], mul2(pack2(r, r), pack2(w.x, w.y)));
+                        ra_times(y[i + 2], y[i + 3], mul2(pack2(r, r), pack2(w.z, w.w)));
                     }
                 }
             }
@@ -175,12 +195,14 @@ __global__ void __launch_bounds__(kRaThreads, PER == 4 ? 2 : 3) rope_append_kern
                     const int hop = R2 / 16;
                     const bool first = at >= 0 && at < R2, second = at >= R2 && at < p.r.R;
                     const int lane = threadIdx.x & 31, peer = first ? lane + hop : (second ? lane - hop : lane);
-                    float2 c[A];
-                    rope_angles_of<A>(cs, first ? at / 16 : (second ? (at - R2) / 16 : 0), R2 / A, c);
+                    const int item = first ? at / 16 : (second ? (at - R2) / 16 : 0);
+                    const float sign = first ? -1.f : 1.f;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float t = __shfl_sync(0xffffffffu, y[i], peer);
-                        if (first || second) y[i] = y[i] * c[i].x + (first ? -t : t) * c[i].y;
+                    for (int i = 0; i < 16; i += 2) {
+                        const float4 v = reinterpret_cast<const float4*>(cs)[i / 2 * (R2 / A) + item];  // two cosines, two sines
+                        const float t0 = __shfl_sync(0xffffffffu, y[i], peer), t1 = __shfl_sync(0xffffffffu, y[i + 1], peer);
+                        const uint64_t t = mul2(pack2(t0 * sign, t1 * sign), pack2(v.z, v.w));
+                        if (first || second) unpack2(fma2(pack2(y[i], y[i + 1]), pack2(v.x, v.y), t), y[i], y[i + 1]);
                     }
                 } else {
                     float* row = (float*)(s_cs + min(p.page, p.S) * R2) + grp * p.D;
@@ -203,10 +225,8 @@ __global__ void __launch_bounds__(kRaThreads, PER == 4 ? 2 : 3) rope_append_kern
                     }
                 }
             }
-            if (e < n) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(y[i]) & 0x7fffffffu);
-            }
+            size[k] = ra_size(y);
+            if (e < n) top = max(top, __float_as_uint(size[k]));
         }
         top = ra_block_max(top, s_top);
         if (top >= 0x7f800000u) {  // (the same in all threads) what is not finite does not count
@@ -248,9 +268,10 @@ __global__ void __launch_bounds__(kRaThreads, PER == 4 ? 2 : 3) rope_append_kern
                 if (grp + k * G < n && on) {
                     uint32_t q[4];
 #pragma unroll
+                    for (int i = 0; i < 16; i += 2) ra_times(f[k][i], f[k][i + 1], pack2(inv, inv));
+#pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        q[i] = e4m3x2_from(f[k][4 * i] * inv, f[k][4 * i + 1] * inv) |
-                               (e4m3x2_from(f[k][4 * i + 2] * inv, f[k][4 * i + 3] * inv) << 16);
+                        q[i] = e4m3x2_from(f[k][4 * i], f[k][4 * i + 1]) | (e4m3x2_from(f[k][4 * i + 2], f[k][4 * i + 3]) << 16);
                     *reinterpret_cast<uint4*>(out + (grp + k * G) * p.D) = make_uint4(q[0], q[1], q[2], q[3]);
                 }
             }
@@ -299,21 +320,19 @@ __global__ void __launch_bounds__(kRaThreads, PER == 4 ? 2 : 3) rope_append_kern
                 if (k * G >= n) break;
                 const int t = (int)(lo - p0) + grp + k * G;
                 const bool live = grp + k * G < n;
-                uint32_t g = 0;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) g = max(g, __float_as_uint(f[k][i]) & 0x7fffffffu);
-                const bool number = g < 0x7f800000u;
-                int x = g > 0 ? ra_exp(__uint_as_float(g) * inv, 0.75f, 3) : 0;
+                const bool number = size[k] <= 3.4028235e38f;
+                int x = size[k] > 0.f ? ra_exp(size[k] * inv, 0.75f, 3) : 0;
                 x = !number ? 15 : max(0, min(x, kCache4Exps - 1));
                 const float m = number ? ldexpf(inv, -x) : 0.f;
                 if (live && on) {
                     uint32_t q[2];
 #pragma unroll
+                    for (int i = 0; i < 16; i += 2) ra_times(f[k][i], f[k][i + 1], pack2(m, m));
+#pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         q[i] = 0;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            q[i] |= e2m1x2_from(f[k][8 * i + 2 * c] * m, f[k][8 * i + 2 * c + 1] * m) << (8 * c);
+                        for (int c = 0; c < 4; ++c) q[i] |= e2m1x2_from(f[k][8 * i + 2 * c], f[k][8 * i + 2 * c + 1]) << (8 * c);
                         if (!number) q[i] = 0;
                     }
                     *reinterpret_cast<uint2*>(out + t * (p.D / 2)) = make_uint2(q[0], q[1]);
