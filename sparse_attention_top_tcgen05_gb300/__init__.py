@@ -659,72 +659,73 @@ def lidx_rope_bwd(g, pos, freqs, x2=None, layout="interleaved", rot_off=0, mscal
     return _rope(g, pos, freqs, x2, layout, rot_off, mscale, 1, stream, out, axes, "lidx_rope_bwd")
 
 
-def _norm_side(x, w, g, y, name, dtype, w_dtype, lead, D, dev):
-    """Checks of one tensor of a norm and its weight; returns its shape and strides (x, g)."""
-    shape, xs, dev = _strided(x, "x" + name, dtype, dev)
-    if lead is not None and (shape[0], shape[1], shape[3]) != (*lead, D):
-        raise ValueError("x and x2 shapes disagree")
-    gs = (0, 0, 0)
-    if g is not None:
-        sg, gs, _ = _strided(g, "g" + name, dtype, dev)
+def _fresh(x, shape, dtype, stream):
+    """An output of x's shape and type, contiguous."""
+    return torch.empty_like(x) if stream is None and x.is_contiguous() else _new(shape, dtype, x.device, stream)
+
+
+def _norm_side(x, weight, g, y, dw, name, dtype, w_dtype, dev, bwd, stream):
+    """Checks of one tensor of a norm, its weight, gradient and outputs, which it makes where they are None; returns its
+    shape, device, what goes to C and the outputs."""
+    shape, (a, b, c), dev = _strided(x, "x" + name, dtype, dev)
+    H, D = shape[2], shape[3]
+    if weight is not None:
+        _dense(weight, "weight" + name, w_dtype, (D,), dev)
+    if y is None:
+        y = _fresh(x, shape, dtype, stream)
+        ya, yb, yc = shape[1] * H * D, H * D, D
+        if bwd and weight is not None:
+            dw = _new((D,), _f32, x.device, stream)
+    else:
+        sy, (ya, yb, yc), _ = _strided(y, "out", dtype, dev)
+        if sy != shape:
+            raise ValueError(f"out has another shape than x{name}")
+        if dw is not None:
+            _dense(dw, "out", _f32, (D,), dev)
+    ga = gb = gc = gp = 0
+    if bwd:
+        sg, (ga, gb, gc), _ = _strided(g, "g" + name, dtype, dev)
         if sg != shape:
             raise ValueError(f"g{name} has another shape than x{name}")
-    if w is not None:
-        _dense(w, "weight" + name, w_dtype, (shape[3],), dev)
-    return shape, xs, gs, dev
+        gp = g.data_ptr()
+    return shape, dev, _NORM_TENSOR(x.data_ptr(), gp, y.data_ptr(), a, b, c, ga, gb, gc, ya, yb, yc,
+                                    0 if weight is None else weight.data_ptr(), 0 if dw is None else dw.data_ptr(), H), y, dw
 
 
 def _norm_rope(x, weight, pos, freqs, g, x2, weight2, g2, eps, layout, rot_off, mscale, axes, stream, out, workspace, bwd):
     dtype = x.dtype if isinstance(x, _Tensor) else _bf16
     if dtype is not _bf16 and dtype is not _f32:
         raise TypeError(f"x must be float32 or bfloat16, got {dtype}")
-    w_dtype = next((w.dtype for w in (weight, weight2) if isinstance(w, _Tensor)), _f32)
+    w_dtype = weight.dtype if isinstance(weight, _Tensor) else weight2.dtype if isinstance(weight2, _Tensor) else _f32
     if w_dtype is not _bf16 and w_dtype is not _f32:
         raise TypeError(f"weight must be float32 or bfloat16, got {w_dtype}")
     if bwd and (g is None or (x2 is None) != (g2 is None)):
         raise TypeError("each of x and x2 needs the gradient of its output")
-    shape, xs, gs, dev = _norm_side(x, weight, g, None, "", dtype, w_dtype, None, None, None)
-    T0, T1, H, D = shape
-    turn = _turn(pos, freqs, layout, rot_off, mscale, axes, T0, T1, dev)
-    sides = [(x, weight, g, shape, xs, gs)]
+    o = (None,) * 4 if out is None else out if bwd else (out, None) if x2 is None else (out[0], None, out[1], None)
+    shape, dev, arr, y, dw = _norm_side(x, weight, g, o[0], o[1], "", dtype, w_dtype, None, bwd, stream)
+    T0, T1, _, D = shape
     if x2 is not None:
-        shape2, xs2, gs2, _ = _norm_side(x2, weight2, g2, None, "2", dtype, w_dtype, (T0, T1), D, dev)
-        sides.append((x2, weight2, g2, shape2, xs2, gs2))
-    at, arr, res = x.device, b"", ()
-    given = None if out is None else (out if bwd or x2 is not None else (out,))
-    for i, (xi, wi, gi, si, xsi, gsi) in enumerate(sides):
-        Hi = si[2]
-        dwi = None
-        if given is None:
-            y, ys = _new(si, dtype, at, stream), (T1 * Hi * D, Hi * D, D)
-            if bwd:
-                dwi = None if wi is None else _new((D,), _f32, at, stream)
-        else:
-            y = given[2 * i if bwd else i]
-            sy, ys, _ = _strided(y, "out", dtype, dev)
-            if sy != si:
-                raise ValueError("out has another shape than " + ("x2" if i else "x"))
-            if bwd:
-                dwi = given[2 * i + 1]
-                if dwi is not None:
-                    _dense(dwi, "out", _f32, (D,), dev)
-        arr += _NORM_TENSOR(xi.data_ptr(), 0 if gi is None else gi.data_ptr(), y.data_ptr(), *xsi, *gsi, *ys,
-                            0 if wi is None else wi.data_ptr(), 0 if dwi is None else dwi.data_ptr(), Hi)
-        res += (y, dwi) if bwd else (y,)
-    L, dt, wdt = _lib or lib(), 1 if dtype is _bf16 else 0, 1 if w_dtype is _bf16 else 0
+        s2, _, arr2, y2, dw2 = _norm_side(x2, weight2, g2, o[2], o[3], "2", dtype, w_dtype, dev, bwd, stream)
+        if s2[0] != T0 or s2[1] != T1 or s2[3] != D:
+            raise ValueError("x and x2 shapes disagree")
+        arr += arr2
+    turn = _turn(pos, freqs, layout, rot_off, mscale, axes, T0, T1, dev)
+    L, nt, dt, wdt = _lib or lib(), 1 if x2 is None else 2, 1 if dtype is _bf16 else 0, 1 if w_dtype is _bf16 else 0
     if bwd:
         if workspace is None:
             ws_bytes = L.lidx_norm_rope_bwd_workspace_bytes(D)
-            workspace = _scratch(ws_bytes, at, stream)
+            workspace = _scratch(ws_bytes, x.device, stream)
         else:
             ws_bytes = _dense(workspace, "workspace", _u8, (None,), dev)[0]
-        rc = L.lidx_norm_rope_bwd(arr, len(sides), turn, eps, T0, T1, D, dt, wdt, workspace.data_ptr(), ws_bytes,
+        rc = L.lidx_norm_rope_bwd(arr, nt, turn, eps, T0, T1, D, dt, wdt, workspace.data_ptr(), ws_bytes,
                                   _raw_stream(stream, dev))
-    else:
-        rc = L.lidx_norm_rope(arr, len(sides), turn, eps, T0, T1, D, dt, wdt, _raw_stream(stream, dev))
+        if rc:
+            raise LidxError(rc, "lidx_norm_rope_bwd")
+        return (y, dw) if x2 is None else (y, dw, y2, dw2)
+    rc = L.lidx_norm_rope(arr, nt, turn, eps, T0, T1, D, dt, wdt, _raw_stream(stream, dev))
     if rc:
-        raise LidxError(rc, "lidx_norm_rope_bwd" if bwd else "lidx_norm_rope")
-    return res if bwd or len(res) > 1 else res[0]
+        raise LidxError(rc, "lidx_norm_rope")
+    return y if x2 is None else (y, y2)
 
 
 def lidx_norm_rope(x, weight, pos, freqs, x2=None, weight2=None, eps=1e-6, layout="interleaved", rot_off=0, mscale=1.0,
