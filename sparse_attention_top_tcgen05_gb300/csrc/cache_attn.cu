@@ -159,7 +159,7 @@ constexpr size_t kCopyMost = (size_t)2 << 30;
 static size_t attn4_copy_bytes(int64_t B, int64_t S, int G, int Hkv, int D, int page, int64_t max_pages, int topk) {
     const int64_t keys = max_pages * page;
     if (topk > 0 ? S * topk < 2 * keys : S * G <= 128) return 0;
-    if (B * max_pages > INT_MAX / page / Hkv) return 0;  // as num_pages
+    if (B * max_pages > INT_MAX / page / Hkv || Hkv > 65535) return 0;  // as num_pages; blocks of the widening launch
     const size_t pages = (size_t)(B * max_pages), bytes = 2 * pages * Hkv * page * D;
     if (bytes > kCopyMost) return 0;
     return round256(bytes) + round256(2 * pages * Hkv * sizeof(float)) + round256(pages * sizeof(int32_t));
