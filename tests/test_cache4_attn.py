@@ -476,6 +476,10 @@ def test_binding_refusals():
             lidx.lidx_cache4_attn(*ok, **kw)
     with pytest.raises(lidx.LidxError):
         lidx.lidx_cache4_attn(ok[0][:, :, :3].contiguous(), *ok[1:])  # 3 heads over 2
+    shifted = torch.zeros(ok[3].numel() + 1, dtype=torch.int32, device=DEV)[1:].view(ok[3].shape)  # 4 bytes off
+    with pytest.raises(lidx.LidxError) as e:
+        lidx.lidx_cache4_attn(*but(3, shifted))
+    assert e.value.status == 3
     with pytest.raises(lidx.LidxError) as e:
         lidx.lidx_cache4_attn(*ok, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
     assert e.value.status == 5

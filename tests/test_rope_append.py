@@ -235,6 +235,32 @@ def test_turned_keys_against_the_definition(case, bits, normed, A, given, layout
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D,page,Hkv,S", [(128, 128, 8, 300), (80, 64, 5, 200), (64, 16, 3, 40), (16, 16, 1, 3)])
+def test_norm_alone_and_blocks_of_several_heads(D, page, Hkv, S):
+    """A norm without a rotation is that with frequencies of zero (cosines of 1, sines of 0: exact), and a call of many heads
+    and tokens, whose blocks take several heads, holds what calls of one head each hold."""
+    starts, cnt = [5, 0, 2 * page], [S, S - 2, S]
+    g, table, k, v, sides, _ = _setup(3, S, Hkv, D, page, starts, cnt, 4, True, D)
+    table = g.permutation(table.size).reshape(table.shape).astype(np.int32)
+    w = torch.from_numpy(1 + 0.3 * g.standard_normal(D)).float().to(DEV)
+    a, b, c = ([_cuda(s, 4) for s in sides] for _ in range(3))
+    zero = torch.zeros(D // 2, dtype=torch.int64, device=DEV)
+    k, v = k.to(DEV), v.to(DEV)
+    _call(4, k, v, *a, table, starts, cnt, weight=w)
+    _call(4, k, v, *b, table, starts, cnt, weight=w, freqs=zero)
+    for x, y in zip(a[0] + a[1], b[0] + b[1]):
+        assert torch.equal(x, y)
+    freqs = lidx.lidx_rope_freqs(D)
+    _call(4, k, v, *b, table, starts, cnt, weight=w, freqs=freqs, layout="half")
+    for h in range(Hkv):
+        one = [[t[:, h:h + 1].contiguous() for t in side] for side in c]
+        _call(4, k[:, :, h:h + 1], v[:, :, h:h + 1], *one, table, starts, cnt, weight=w)
+        _call(4, k[:, :, h:h + 1], v[:, :, h:h + 1], *one, table, starts, cnt, weight=w, freqs=freqs, layout="half")
+        for x, y in zip(b[0] + b[1], one[0] + one[1]):
+            assert torch.equal(x[:, h:h + 1], y)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("bits", [4, 8])
 def test_infinities_and_nan(bits):
     """They read as NaN (in 4 bits their group does), change no scale and nothing else; a key's partner in the turn is NaN,
