@@ -23,8 +23,10 @@ struct NormTensor {
     int64_t xs[3], gs[3], ys[3];
     const void* w;  // nullable
     float* dw;      // nullable
+    int64_t all;    // rows
     int H, blocks;  // blocks of this tensor
     RopeDiv heads;
+    uint32_t step_tok, step_row;  // backward: rows from a block's chunk to its next, as tokens and rows
 };
 struct NormParams {
     NormTensor t[2];
@@ -186,19 +188,27 @@ __device__ __forceinline__ float norm_sum(float v) {
 
 // Rows [first, first + n) of a tensor: where row e of a block is.
 struct NormRows {
-    int64_t tok0;
+    uint32_t tok0;
     int skip, n;
-    __device__ NormRows(const NormParams& p, const NormTensor& t, int64_t first, int rows) {
-        const int64_t all = p.T0 * p.T1 * t.H;
-        tok0 = first / t.H;
-        skip = (int)(first - tok0 * t.H);
-        n = (int)min((int64_t)rows, all - first);
+    __device__ NormRows(const NormTensor& t, int64_t first, int rows) {
+        tok0 = t.all < INT_MAX ? rope_quot((uint32_t)first, t.heads) : (uint32_t)(first / t.H);
+        skip = (int)(first - (int64_t)tok0 * t.H);
+        n = (int)max((int64_t)0, min((int64_t)rows, t.all - first));
+    }
+    // on by a step of t.step_tok tokens and t.step_row rows; n rows there
+    __device__ NormRows after(const NormTensor& t, int rows) const {
+        NormRows r = *this;
+        r.tok0 += t.step_tok;
+        r.skip += t.step_row;
+        if (r.skip >= t.H) r.skip -= t.H, ++r.tok0;
+        r.n = rows;
+        return r;
     }
     // token of the block, and places of row e with strides s and z
     __device__ int token(const NormTensor& t, int e) const { return (int)rope_quot(skip + e, t.heads); }
     __device__ void at(const NormParams& p, const NormTensor& t, const int64_t (&s)[3], const int64_t (&z)[3], int e, int tok,
                        int64_t (&out)[2]) const {
-        const uint32_t k = (uint32_t)tok0 + tok, t0 = rope_quot(k, p.tokens1), t1 = k - t0 * (uint32_t)p.T1;
+        const uint32_t k = tok0 + tok, t0 = rope_quot(k, p.tokens1), t1 = k - t0 * (uint32_t)p.T1;
         const int h = skip + e - tok * t.H;
         out[0] = t0 * s[0] + t1 * s[1] + h * s[2];
         out[1] = t0 * z[0] + t1 * z[1] + h * z[2];
@@ -209,7 +219,7 @@ struct NormRows {
         const int R2 = p.r.R / 2, all = (token(t, n - 1) + 1) * R2;
         for (int i = threadIdx.x; i < all; i += kNormThreads) {
             const int k = rope_quot(i, p.pairs);
-            const uint32_t tok = (uint32_t)tok0 + k, t0 = rope_quot(tok, p.tokens1), t1 = tok - t0 * (uint32_t)p.T1;
+            const uint32_t tok = tok0 + k, t0 = rope_quot(tok, p.tokens1), t1 = tok - t0 * (uint32_t)p.T1;
             rope_put_angle<A>(s_cs + k * R2, i - k * R2, R2 / A, rope_cs(p.r, t0, t1, i - k * R2));
         }
     }
@@ -224,7 +234,7 @@ __global__ void __launch_bounds__(kNormThreads, 5) norm_rope_kernel(const __grid
     const int which = (int)blockIdx.x >= p.t[0].blocks;
     const NormTensor& t = p.t[which];
     const int64_t first = (int64_t)(blockIdx.x - (which ? p.t[0].blocks : 0)) * (G * PER);
-    const NormRows rows(p, t, first, G * PER);
+    const NormRows rows(t, first, G * PER);
     const int l = threadIdx.x % LANES, grp = threadIdx.x / LANES;
     const NormLane o = norm_lane<HALF, V>(p.r, p.D, l);
     uint4 a[PER], b[PER];
@@ -289,7 +299,7 @@ __global__ void __launch_bounds__(kNormThreads, norm_bwd_blocks<T>()) norm_rope_
     float sp[V], sq[V];  // sums of u h
 #pragma unroll
     for (int i = 0; i < V; ++i) sp[i] = sq[i] = 0.f;
-    const int64_t all = p.T0 * p.T1 * t.H, step = (int64_t)t.blocks * G;
+    const int64_t step = (int64_t)t.blocks * G;
     uint4 xa, xb, ga, gb;
     auto load = [&](const NormRows& rows) {
         xa = xb = ga = gb = make_uint4(0, 0, 0, 0);
@@ -309,13 +319,13 @@ __global__ void __launch_bounds__(kNormThreads, norm_bwd_blocks<T>()) norm_rope_
         }
     };
     int64_t first = (int64_t)(blockIdx.x - (which ? p.t[0].blocks : 0)) * G;
-    NormRows rows(p, t, first, G);
+    NormRows rows(t, first, G);
     load(rows);
-    for (int odd = 0; first < all; first += step, odd ^= 1) {
+    for (int odd = 0; first < t.all; first += step, odd ^= 1) {
         float2* const cs = s_cs + odd * half_angles;
         rows.angles<A>(p, t, cs);
         __syncthreads();
-        const NormRows next(p, t, first + step < all ? first + step : 0, first + step < all ? G : 0);
+        const NormRows next = rows.after(t, (int)max((int64_t)0, min((int64_t)G, t.all - (first + step))));
         const int tok = grp < rows.n ? rows.token(t, grp) : 0;
         float xp[V], xq[V], up[V], uq[V], tp[V], tq[V];
         norm_unpack<HALF, T, V>(xa, xb, xp, xq);
@@ -393,8 +403,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_any_kernel(const __gri
         for (int d = lane; d < p.D; d += 32) sum[d] = 0.f;
         __syncwarp();
     }
-    const int64_t all = p.T0 * p.T1 * t.H;
-    for (int64_t row = (int64_t)(blockIdx.x - (which ? p.t[0].blocks : 0)) * (kNormThreads / 32) + warp; row < all;
+    for (int64_t row = (int64_t)(blockIdx.x - (which ? p.t[0].blocks : 0)) * (kNormThreads / 32) + warp; row < t.all;
          row += (int64_t)t.blocks * (kNormThreads / 32)) {
         const int64_t tok = row / t.H, t0 = tok / p.T1, t1 = tok - t0 * p.T1;
         const int h = (int)(row - tok * t.H);
@@ -503,6 +512,9 @@ static void norm_share(NormParams& p, int nt, int rows, int per_sm) {
     for (int i = 0; i < nt; ++i) {
         int64_t n = all <= most ? chunks[i] : chunks[i] * (most - 1) / all;
         p.t[i].blocks = (int)(n < 1 ? 1 : n);
+        const int64_t step = (int64_t)p.t[i].blocks * rows;
+        p.t[i].step_tok = (uint32_t)(step / p.t[i].H);
+        p.t[i].step_row = (uint32_t)(step % p.t[i].H);
     }
 }
 
@@ -609,6 +621,7 @@ static int norm_params(const lidx_norm_tensor* t, int nt, const lidx_rope_turn* 
         o.dw = bwd ? t[i].dw : nullptr;
         o.H = t[i].H;
         o.heads = rope_div(o.H);
+        o.all = T0 * T1 * o.H;
     }
     rc = rope_turn_aligned(*r);
     if (rc) return rc;

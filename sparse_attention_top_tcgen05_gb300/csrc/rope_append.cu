@@ -63,6 +63,7 @@ static int ra_append(int bits, const void* k, const void* v, const int64_t* ks, 
     p.page = page;
     p.max_pages = (int)max_pages;
     p.J = (int)J;
+    p.page_shift = page == 16 ? 4 : (page == 32 ? 5 : (page == 64 ? 6 : 7));
     // A block of several heads computes its tokens' angles once and loads a head while it converts the one before, so it takes
     // as many as leave four blocks an SM; a few tokens are a chain of latencies, and their blocks take one.
     p.heads = 1;

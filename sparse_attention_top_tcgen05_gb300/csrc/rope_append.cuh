@@ -36,6 +36,7 @@ struct RopeAppendParams {
     const int32_t* count;
     int64_t num_pages;
     int S, Hkv, D, page, max_pages, J;
+    int page_shift;        // page = 1 << page_shift
     int heads;             // of a block
     RopeDiv pairs;
 };
@@ -90,7 +91,7 @@ __global__ void __launch_bounds__(kRaThreads, PER == 4 ? 2 : 3) rope_append_kern
     count = count < 0 ? 0 : (count > p.S ? p.S : count);
     // page slots are counted from the page of the first position that is not negative
     const int64_t from = start < 0 ? 0 : start;
-    const int64_t slot = from / p.page + j;
+    const int64_t slot = (from >> p.page_shift) + j;
     const int64_t p0 = slot * p.page;
     const int64_t lo = from > p0 ? from : p0;  // new tokens: positions [lo, hi)
     int64_t hi = start + count;
