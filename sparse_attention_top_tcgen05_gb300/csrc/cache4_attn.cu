@@ -6,6 +6,10 @@
 //   - few rows (decode steps): packed tiles come to shared memory, and warps of the kernel widen them there
 //   - a key is read by several units of 128 rows, or by several selections: its page is widened once, into the workspace,
 //     and the 8-bit kernels read that
+//
+// What bounds it.  64 ragged sequences to 32768 keys, 64 heads on 8: 339 us (8 bits 337 us), half of the copy rate.  A tile of 128
+// keys takes 1650 cycles, of which the widening warps work 1200: 1490 of a tile's 3830 warp instructions widen.  ALU pipes are 52 %
+// busy, issue slots 60 %.  Without widening 252 us.  One sequence of 1024 keys: 10.3 us.
 #include "cache_attn_narrow.cuh"
 
 namespace lidx {

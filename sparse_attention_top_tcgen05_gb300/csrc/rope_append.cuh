@@ -11,6 +11,10 @@
 // One block per (sequence, page it touches, some heads, k or v); LANES lanes a token, 16 dims each, so that a group's
 // maximum is a lane's own.  A page's tokens stay in registers between the page's maximum and the conversion.  Angles of the
 // page's tokens are computed once a block into shared memory and serve its heads.
+//
+// What bounds it.  8 bits, 4 x 4097 tokens of 8 heads of 128, half of each key turned: 27 us (25.5 us for cache_append.cu, which
+// turns nothing), a block's dependent reads and barriers.  4 bits, the same with a norm and all of each key turned by three axes:
+// 32.4 us, 67 % of issue slots busy.  One token of 64 sequences: 8.8 us.
 #pragma once
 #include "cache.cuh"
 #include "ptx.cuh"
