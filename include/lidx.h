@@ -352,8 +352,9 @@ typedef struct {
  * lidx_norm_rope_bwd: y is the gradient of x, dw that of w summed over all rows (fp32; overwritten).  No atomics: two
  * calls give the same bits.
  *   workspace  lidx_norm_rope_bwd_workspace_bytes(D) bytes, 256-byte aligned
- * A row with an infinity or a NaN is NaN, and its gradients are.  Rules as lidx_rope, and eps >= 0 and finite.  16-byte
- * aligned tensors, strides and rotated parts (half layout: halves) of heads of up to 512 dims in bf16 and 256 in fp32 take
+ * A row with a NaN is NaN.  Where a row's sum of squares is infinite in fp32 (an infinity, sizes of 2^64), its r is 0:
+ * infinities and their pairs are NaN, everything else is 0.  Gradients of rows with a NaN or an infinity are not numbers.
+ * A row of zeros with eps 0 is NaN.  Rules as lidx_rope, and eps >= 0 and finite.  16-byte aligned tensors, strides and rotated parts (half layout: halves) of heads of up to 512 dims in bf16 and 256 in fp32 take
  * the faster path.
  */
 int lidx_norm_rope(const lidx_norm_tensor* t, int nt, const lidx_rope_turn* r, float eps, int64_t T0, int64_t T1, int D,
@@ -395,7 +396,7 @@ int lidx_cache_append(const void* k, const void* v, const int64_t* ks, const int
  *            every axis
  *   w, eps   the norm of lidx_norm_rope (w fp32 or bf16 [D]: w_dtype 0 or 1); w NULL: no norm
  * Everything else is as in lidx_cache_append; r's rules are lidx_rope_turn's.  An infinity or a NaN in a key is NaN in
- * both dims of its pair, with w in the whole key.
+ * both dims of its pair; with w a NaN is NaN in the whole key, and the rest of a key with an infinity is 0.
  */
 int lidx_rope_cache_append(const void* k, const void* v, const int64_t* ks, const int64_t* vs, const lidx_rope_turn* r,
                            const void* w, int w_dtype, float eps, const int32_t* block_table, const int32_t* start,

@@ -348,6 +348,32 @@ def test_no_weight_and_rows_that_are_not_finite():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 66])
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+def test_rows_whose_squares_are_infinite(layout, D):
+    """r is 0: the infinity and its pair are NaN, everything else and rows of finite, huge elements are 0; no other row
+    differs, forward or backward.  (66 dims take the kernel without vectors.)"""
+    g = torch.Generator(device=DEV).manual_seed(9)
+    x, gr = (torch.randn(1, 5, 3, D, generator=g, device=DEV) for _ in (0, 1))
+    pos = torch.arange(5, dtype=torch.int32, device=DEV)
+    w, freqs = torch.rand(D, generator=g, device=DEV) + 0.5, lidx.lidx_rope_freqs(64)
+    want = lidx.lidx_norm_rope(x, w, pos, freqs, layout=layout)
+    dwant, _ = lidx.lidx_norm_rope_bwd(gr, x, w, pos, freqs, layout=layout)
+    bad = x.clone()
+    bad[0, 2, 1, 5], bad[0, 4, 2] = float("inf"), 2.0 ** 64
+    y = lidx.lidx_norm_rope(bad, w, pos, freqs, layout=layout)
+    dx, dw = lidx.lidx_norm_rope_bwd(gr, bad, w, pos, freqs, layout=layout)
+    rest = torch.ones(1, 5, 3, dtype=torch.bool, device=DEV)
+    rest[0, 2, 1] = rest[0, 4, 2] = False
+    assert torch.equal(y[rest], want[rest]) and torch.equal(dx[rest], dwant[rest])
+    pair = [4, 5] if layout == "interleaved" else [5, 37]
+    row = y[0, 2, 1]
+    assert row[pair].isnan().all() and row.isnan().sum() == 2 and (row[~row.isnan()] == 0).all()
+    assert (y[0, 4, 2] == 0).all()
+    assert dx[0, 2, 1].isnan().any() and dw[5].isnan()
+
+
+@pytest.mark.gpu
 def test_captured_and_replayed_with_two_graphs():
     """Two captured backward passes, each with its workspace, replayed with new inputs while eager calls go on."""
     g = torch.Generator(device=DEV).manual_seed(5)

@@ -301,6 +301,22 @@ def test_norm_of_a_row_that_is_not_finite():
 
 
 @pytest.mark.gpu
+def test_norm_of_a_row_with_an_infinity():
+    """Its pair is NaN, the rest of the key 0; nothing else differs."""
+    g, table, k, v, sides, cnt = _setup(1, 3, 2, 64, 16, [0], None, 8, False, 4)
+    a, b = ([_cuda(s, 8) for s in sides] for _ in (0, 1))
+    kw = dict(freqs=lidx.lidx_rope_freqs(64), weight=torch.ones(64, device=DEV))
+    k[0, 1, 1] = 0.0
+    _call(8, k.to(DEV), v.to(DEV), *a, table, [0], cnt, **kw)
+    k[0, 1, 1] = 1.0
+    k[0, 1, 1, 7] = float("inf")
+    _call(8, k.to(DEV), v.to(DEV), *b, table, [0], cnt, **kw)
+    x, y = (plain.E4M3[_numpy(t[0][0])[table[0, 0]]] for t in (a, b))
+    assert np.isnan(y[1, 1, 6:8]).all() and np.isnan(y).sum() == 2
+    assert np.array_equal(np.nan_to_num(y), x)
+
+
+@pytest.mark.gpu
 def test_token_by_token_equals_at_once_in_four_bits():
     """Powers of two move exponents only, so a page filled token by token holds what it holds when filled at once, where no
     group falls below the lowest exponent: sizes here lie within 2^6 of each other.  The single calls read slices of a fused,
