@@ -18,7 +18,9 @@
 // compressed keys, whose first rows see few (unseen tiles are walked like others).  Of the 238 us, 151 us are left without softmax,
 // joining, output and conversion of queries.
 //
-// The register split leaves the four kernels 260 to 412 bytes of spills (-Xptxas -v).
+// The register split leaves the four kernels of the 8-bit cache 260 to 412 bytes of spills, those of the 4-bit cache 360 to 468
+// (-Xptxas -v).  A second group of widening warps there takes registers from the others: 32 decode rows of 2048 selected keys 32.0
+// us instead of 30.0, 4 sequences of 131072 keys with 64 heads on one 64.0 us instead of 61.7.
 //
 // Units of at most 64 rows (one selected row of 64 heads, a decode step on a shared key head) are laid out twice: row r
 // again as row r + 64.  Of a tile's keys the first copy's weights hold the first 64, the second copy's the others (zeros
