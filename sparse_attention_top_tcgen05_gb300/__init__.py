@@ -701,6 +701,8 @@ def _norm_rope(x, weight, pos, freqs, g, x2, weight2, g2, eps, layout, rot_off, 
         raise TypeError(f"weight must be float32 or bfloat16, got {w_dtype}")
     if bwd and (g is None or (x2 is None) != (g2 is None)):
         raise TypeError("each of x and x2 needs the gradient of its output")
+    if x2 is None and weight2 is not None:
+        raise TypeError("weight2 needs x2")
     o = (None,) * 4 if out is None else out if bwd else (out, None) if x2 is None else (out[0], None, out[1], None)
     shape, dev, arr, y, dw = _norm_side(x, weight, g, o[0], o[1], "", dtype, w_dtype, None, bwd, stream)
     T0, T1, _, D = shape

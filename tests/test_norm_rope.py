@@ -424,3 +424,11 @@ def test_binding_refusals():
                 lambda: bwd(x, x, w, pos, freqs, workspace=torch.empty(256, dtype=torch.uint8, device=DEV))):
         with pytest.raises(lidx.LidxError):
             bad()
+
+
+def test_a_second_weight_needs_a_second_tensor():
+    x = torch.zeros(1, 1, 1, 64)
+    with pytest.raises(TypeError, match="weight2"):
+        lidx.lidx_norm_rope(x, None, None, None, weight2=torch.ones(64))
+    with pytest.raises(TypeError, match="weight2"):
+        lidx.lidx_norm_rope_bwd(x, x, None, None, None, weight2=torch.ones(64))
