@@ -12,6 +12,7 @@
 
 #include "lidx.h"
 #include "kernels.h"
+#include "smem_attr.h"
 #include "topk.cuh"
 
 namespace lidx {
@@ -134,28 +135,16 @@ int current_sms() {
     return d && d->sms > 0 ? d->sms : 148;
 }
 
-// cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per (device, kernel, size).
-struct AttrEntry {
-    int dev;
-    const void* fn;
-    int smem;
-};
-static AttrEntry g_attr[256];
-static int g_nattr = 0;
-static std::mutex g_attr_mu;
+constexpr int kMaxKernels = 512;  // that ask for more shared memory than any kernel may have (the library has about 200)
+static SmemLimits<kMaxKernels, kMaxDevices> g_smem;
 
 cudaError_t set_smem_attr(const void* fn, int smem) {
     const int dev = current_device();
-    {
-        std::lock_guard<std::mutex> lock(g_attr_mu);
-        for (int i = 0; i < g_nattr; ++i)
-            if (g_attr[i].dev == dev && g_attr[i].fn == fn && g_attr[i].smem >= smem) return cudaSuccess;
-    }
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    std::lock_guard<std::mutex> lock(g_attr_mu);
-    if (g_nattr < 256) g_attr[g_nattr++] = AttrEntry{dev, fn, smem};
-    return cudaSuccess;
+    if (dev < 0) return cudaErrorInvalidDevice;
+    const int e = g_smem.ensure(dev, fn, smem, [&](int bytes) {
+        return (int)cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    });
+    return e < 0 ? cudaErrorMemoryAllocation : (cudaError_t)e;
 }
 
 // SM count of the current device, 0 if it is not an sm_103 part.

@@ -110,7 +110,7 @@ int check_fwd(const void* q, const void* k, const float* w, int64_t B, int64_t S
 // host-side state shared by the launchers (api.cu)
 int current_sms();                                   // SM count of the current device
 int sm103_sms();                                     // the same, 0 if it is not an sm_103 part
-cudaError_t set_smem_attr(const void* fn, int smem);  // once per (device, kernel, size)
+cudaError_t set_smem_attr(const void* fn, int smem);  // allows a kernel smem bytes or more on the current device
 uint64_t wait_limit_ns();                             // limit of every pipeline wait
 int debug_stall();                                    // failure-detection test switch
 
