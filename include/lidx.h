@@ -353,7 +353,8 @@ typedef struct {
  * calls give the same bits.
  *   workspace  lidx_norm_rope_bwd_workspace_bytes(D) bytes, 256-byte aligned
  * A row with a NaN is NaN.  Where a row's sum of squares is infinite in fp32 (an infinity, sizes of 2^64), its r is 0:
- * infinities and their pairs are NaN, everything else is 0.  Gradients of rows with a NaN or an infinity are not numbers.
+ * infinities and their pairs are NaN, everything else is 0.  Gradients of rows with a NaN or an infinity are not numbers;
+ * of finite rows whose sum of squares is infinite they are 0, and such rows add nothing to dw.
  * A row of zeros with eps 0 is NaN.  Rules as lidx_rope, and eps >= 0 and finite.  16-byte aligned tensors, strides and rotated parts (half layout: halves) of heads of up to 512 dims in bf16 and 256 in fp32 take
  * the faster path.
  */

@@ -342,15 +342,22 @@ __global__ void __launch_bounds__(kNormThreads, norm_bwd_blocks<T>()) norm_rope_
 #pragma unroll
         for (int i = 0; i < V; i += 2) unpack2(mul2(pack2(uq[i], uq[i + 1]), w[i / 2]), tq[i], tq[i + 1]);
         const float r = __frsqrt_rn(norm_sum<LANES>(norm_dot(xp, xp, xq, xq)) * p.inv_d + p.eps);
-        const float c = -r * r * (norm_sum<LANES>(norm_dot(tp, xp, tq, xq)) * p.inv_d);
+        const uint64_t r2 = pack2(r, r);
+        // x becomes h, which is at most D^1/2 whatever the row's size: the mean of t x overflows with large x, and r r with small
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            unpack2(mul2(pack2(xp[i], xp[i + 1]), r2), xp[i], xp[i + 1]);
+            unpack2(mul2(pack2(xq[i], xq[i + 1]), r2), xq[i], xq[i + 1]);
+        }
+        const float c = -(norm_sum<LANES>(norm_dot(tp, xp, tq, xq)) * p.inv_d);
         if (grp < rows.n && o.n > 0) {
-            const uint64_t r2 = pack2(r, r), c2 = pack2(c, c);
-            auto grad = [&](const float (&x)[V], const float (&u)[V], float (&t)[V], float (&sum)[V]) {
+            const uint64_t c2 = pack2(c, c);
+            auto grad = [&](const float (&h)[V], const float (&u)[V], float (&t)[V], float (&sum)[V]) {
 #pragma unroll
                 for (int i = 0; i < V; i += 2) {
-                    const uint64_t x2 = pack2(x[i], x[i + 1]);
-                    unpack2(fma2(pack2(u[i], u[i + 1]), mul2(x2, r2), pack2(sum[i], sum[i + 1])), sum[i], sum[i + 1]);
-                    unpack2(mul2(r2, fma2(x2, c2, pack2(t[i], t[i + 1]))), t[i], t[i + 1]);
+                    const uint64_t h2 = pack2(h[i], h[i + 1]);
+                    unpack2(fma2(pack2(u[i], u[i + 1]), h2, pack2(sum[i], sum[i + 1])), sum[i], sum[i + 1]);
+                    unpack2(mul2(r2, fma2(h2, c2, pack2(t[i], t[i + 1]))), t[i], t[i + 1]);
                 }
             };
             grad(xp, up, tp, sp);
@@ -435,7 +442,24 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_any_kernel(const __gri
             }
         }
         const float r = __frsqrt_rn(norm_sum<32>(s2) * p.inv_d + p.eps);
-        const float c = BWD ? r * r * (norm_sum<32>(s3) * p.inv_d) : 0.f;
+        float c = 0.f;  // mean of t h
+        if constexpr (BWD) {
+            s3 = norm_sum<32>(s3);
+            c = r * (s3 * p.inv_d);
+            if (!(fabsf(s3) > 0x1p-100f && fabsf(s3) < INFINITY)) {
+                // products t x beyond fp32's range, or behind it: those of h, which is at most D^1/2, are not (a pass more in every
+                // row costs an eighth of the time)
+                s3 = 0.f;
+                for (int u = lane; u < units; u += 32) {
+                    int ia, ib;
+                    norm_unit(p.r, u, ia, ib);
+                    float ga, gb;
+                    grad(u, ia, ib, ga, gb);
+                    s3 += ga * norm_weight(p, t.w, ia) * (rope_get(x + ia) * r) + gb * norm_weight(p, t.w, ib) * (rope_get(x + ib) * r);
+                }
+                c = norm_sum<32>(s3) * p.inv_d;
+            }
+        }
         for (int u = lane; u < units; u += 32) {
             int ia, ib;
             norm_unit(p.r, u, ia, ib);
@@ -444,10 +468,11 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_any_kernel(const __gri
             if constexpr (BWD) {
                 float ga, gb;
                 grad(u, ia, ib, ga, gb);
-                sum[ia] += ga * (a * r);
-                sum[ib] += gb * (b * r);
-                rope_put(y + ia, r * (ga * wa - a * c));
-                rope_put(y + ib, r * (gb * wb - b * c));
+                const float ha = a * r, hb = b * r;
+                sum[ia] += ga * ha;
+                sum[ib] += gb * hb;
+                rope_put(y + ia, r * (ga * wa - ha * c));
+                rope_put(y + ib, r * (gb * wb - hb * c));
             } else {
                 const float na = a * (r * wa), nb = b * (r * wb);
                 if (u < p.r.R / 2) {
