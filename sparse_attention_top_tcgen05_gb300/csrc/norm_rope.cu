@@ -548,7 +548,12 @@ static void norm_share(NormParams& p, int nt, int rows, int per_sm) {
 template <class T, bool HALF, int LANES>
 static cudaError_t norm_launch_lanes(NormParams& p, int nt, bool bwd, cudaStream_t st) {
     constexpr int G = kNormThreads / LANES;
-    constexpr int weights = 2 * (16 / (int)sizeof(T)) * LANES * 4;
+    constexpr int V = 16 / (int)sizeof(T), weights = 2 * V * LANES * 4;
+    // A head has at most 2 V LANES dims, all of them turned, and a row may be a token: every launch stays within what any kernel may
+    // have (two halves of angles of G + 1 tokens backward; forward one of G + 1, or kNormAngles).
+    static_assert(2 * 8 * (G + 1) * V * LANES + weights <= 48 * 1024 && G * 2 * V * LANES * 4 + weights <= 48 * 1024 &&
+                      8 * kNormAngles + weights <= 48 * 1024,
+                  "shared memory");
     auto smem = [&](int rows) {  // angles of the tokens of `rows` rows
         int64_t angles = 0;
         for (int i = 0; i < nt; ++i) {
@@ -561,12 +566,7 @@ static cudaError_t norm_launch_lanes(NormParams& p, int nt, bool bwd, cudaStream
         norm_share(p, nt, G, norm_bwd_blocks<T>());
         const int64_t angles = smem(G) + (smem(G) & 1), a = 2 * angles * 8, s = (int64_t)G * p.D * 4;
         const int bytes = (int)(a > s ? a : s) + weights;
-        auto* kernel = norm_rope_bwd_kernel<T, HALF, LANES>;
-        if (bytes > 48 * 1024) {
-            const cudaError_t e = set_smem_attr((const void*)kernel, bytes);
-            if (e != cudaSuccess) return e;
-        }
-        kernel<<<p.t[0].blocks + p.t[1].blocks, kNormThreads, bytes, st>>>(p, (int)angles);
+        norm_rope_bwd_kernel<T, HALF, LANES><<<p.t[0].blocks + p.t[1].blocks, kNormThreads, bytes, st>>>(p, (int)angles);
         return cudaGetLastError();
     }
     constexpr int big = G * kNormPer;
