@@ -571,6 +571,13 @@ def lidx_rope_axis_map(sections, interleaved=False, device="cuda") -> torch.Tens
     return torch.tensor(ids, dtype=_u8).to(device)
 
 
+def _pack_turn(head, rot_off, layout, mscale):
+    try:
+        return _ROPE_TURN(*head, rot_off, layout, mscale)
+    except struct.error:
+        raise ValueError(f"rot_off must be a 32-bit integer and mscale a number, got {rot_off} and {mscale}") from None
+
+
 def _turn(pos, freqs, layout, rot_off, mscale, axes, T0, T1, dev, own_pos=False):
     """The packed lidx_rope_turn of a rotation.  own_pos: pos may be None, for the call's own positions."""
     if pos is None and own_pos:
@@ -579,7 +586,7 @@ def _turn(pos, freqs, layout, rot_off, mscale, axes, T0, T1, dev, own_pos=False)
             raise ValueError("axes needs pos, with the positions on each axis")
         if layout not in ROPE_LAYOUT:
             raise ValueError(f"layout must be one of {list(ROPE_LAYOUT)}")
-        return _ROPE_TURN(0, 0, 0, 0, freqs.data_ptr(), 0, 1, 2 * pairs, rot_off, ROPE_LAYOUT[layout], mscale)
+        return _pack_turn((0, 0, 0, 0, freqs.data_ptr(), 0, 1, 2 * pairs), rot_off, ROPE_LAYOUT[layout], mscale)
     if not isinstance(pos, _Tensor) or pos.dtype is not _i32 or not pos.is_cuda:
         raise TypeError("pos must be an int32 CUDA tensor")
     if pos.get_device() != dev:
@@ -603,7 +610,7 @@ def _turn(pos, freqs, layout, rot_off, mscale, axes, T0, T1, dev, own_pos=False)
         if pos.shape != (A, T0, T1):
             pos = pos.view(A, *(1,) * (3 - pos.dim()), *pos.shape[1:]).expand(A, T0, T1)
         pa, p0, p1 = pos.stride()
-    return _ROPE_TURN(pos.data_ptr(), pa, p0 if T0 > 1 else 0, p1 if T1 > 1 else 0, freqs.data_ptr(), axis or 0, A, 2 * pairs,
+    return _pack_turn((pos.data_ptr(), pa, p0 if T0 > 1 else 0, p1 if T1 > 1 else 0, freqs.data_ptr(), axis or 0, A, 2 * pairs),
                       rot_off, ROPE_LAYOUT[layout], mscale)
 
 
@@ -674,14 +681,15 @@ def _norm_side(x, weight, g, y, dw, name, dtype, w_dtype, dev, bwd, stream):
     if y is None:
         y = _fresh(x, shape, dtype, stream)
         ya, yb, yc = shape[1] * H * D, H * D, D
-        if bwd and weight is not None:
-            dw = _new((D,), _f32, x.device, stream)
     else:
         sy, (ya, yb, yc), _ = _strided(y, "out", dtype, dev)
         if sy != shape:
             raise ValueError(f"out has another shape than x{name}")
+    if bwd:
         if dw is not None:
             _dense(dw, "out", _f32, (D,), dev)
+        elif weight is not None:
+            dw = _new((D,), _f32, x.device, stream)
     ga = gb = gc = gp = 0
     if bwd:
         sg, (ga, gb, gc), _ = _strided(g, "g" + name, dtype, dev)
@@ -703,7 +711,15 @@ def _norm_rope(x, weight, pos, freqs, g, x2, weight2, g2, eps, layout, rot_off, 
         raise TypeError("each of x and x2 needs the gradient of its output")
     if x2 is None and weight2 is not None:
         raise TypeError("weight2 needs x2")
-    o = (None,) * 4 if out is None else out if bwd else (out, None) if x2 is None else (out[0], None, out[1], None)
+    if out is None:
+        o = (None,) * 4
+    elif not bwd and x2 is None:
+        o = (out, None)
+    else:
+        o, n = tuple(out), (1 if x2 is None else 2) * (2 if bwd else 1)
+        if len(o) != n:
+            raise ValueError(f"out has {len(o)} tensors, not {n}")
+        o = o if bwd else (o[0], None, o[1], None)
     shape, dev, arr, y, dw = _norm_side(x, weight, g, o[0], o[1], "", dtype, w_dtype, None, bwd, stream)
     T0, T1, _, D = shape
     if x2 is not None:
@@ -742,7 +758,8 @@ def lidx_norm_rope(x, weight, pos, freqs, x2=None, weight2=None, eps=1e-6, layou
 def lidx_norm_rope_bwd(g, x, weight, pos, freqs, g2=None, x2=None, weight2=None, eps=1e-6, layout="interleaved", rot_off=0,
                        mscale=1.0, axes=None, stream=None, out=None, workspace=None):
     """Gradients of lidx_norm_rope from its inputs and the gradients g (and g2) of its outputs: (dx, dw) or (dx, dw, dx2,
-    dw2).  dw, the sum over all rows, is fp32 [D] (None where the weight is); dx may be g or x itself (``out``)."""
+    dw2).  dw, the sum over all rows, is fp32 [D] (None where the weight is).  ``out`` has a tensor, or None, for each of
+    them; dx may be g or x itself."""
     return _norm_rope(x, weight, pos, freqs, g, x2, weight2, g2, eps, layout, rot_off, mscale, axes, stream, out, workspace,
                       True)
 
