@@ -522,8 +522,14 @@ def _dense(t, name, dtype, shape, dev):
     """Checks a contiguous CUDA tensor on device dev; None in `shape` is any size.  Returns its shape."""
     if isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
         s = t.shape
-        if s == shape or (len(s) == len(shape) and all(m is None or n == m for n, m in zip(s, shape))):
+        if s == shape:
             return s
+        if len(s) == len(shape):
+            for n, m in zip(s, shape):
+                if m is not None and n != m:
+                    break
+            else:
+                return s
     if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -571,47 +577,44 @@ def lidx_rope_axis_map(sections, interleaved=False, device="cuda") -> torch.Tens
     return torch.tensor(ids, dtype=_u8).to(device)
 
 
-def _pack_turn(head, rot_off, layout, mscale):
-    try:
-        return _ROPE_TURN(*head, rot_off, layout, mscale)
-    except struct.error:
-        raise ValueError(f"rot_off must be a 32-bit integer and mscale a number, got {rot_off} and {mscale}") from None
-
-
 def _turn(pos, freqs, layout, rot_off, mscale, axes, T0, T1, dev, own_pos=False):
     """The packed lidx_rope_turn of a rotation.  own_pos: pos may be None, for the call's own positions."""
     if pos is None and own_pos:
         pairs = _dense(freqs, "freqs", _i64, (None,), dev)[0]
         if axes is not None:
             raise ValueError("axes needs pos, with the positions on each axis")
-        if layout not in ROPE_LAYOUT:
-            raise ValueError(f"layout must be one of {list(ROPE_LAYOUT)}")
-        return _pack_turn((0, 0, 0, 0, freqs.data_ptr(), 0, 1, 2 * pairs), rot_off, ROPE_LAYOUT[layout], mscale)
-    if not isinstance(pos, _Tensor) or pos.dtype is not _i32 or not pos.is_cuda:
-        raise TypeError("pos must be an int32 CUDA tensor")
-    if pos.get_device() != dev:
-        raise ValueError(f"pos is on {pos.device}, not on cuda:{dev}")
-    pairs = _dense(freqs, "freqs", _i64, (None,), dev)[0]
+        at = pa = p0 = p1 = axis = 0
+        A = 1
+    else:
+        if not isinstance(pos, _Tensor) or pos.dtype is not _i32 or not pos.is_cuda:
+            raise TypeError("pos must be an int32 CUDA tensor")
+        if pos.get_device() != dev:
+            raise ValueError(f"pos is on {pos.device}, not on cuda:{dev}")
+        pairs = _dense(freqs, "freqs", _i64, (None,), dev)[0]
+        if axes is None:
+            A, axis = 1, 0
+            if pos.shape != (T0, T1):
+                pos = pos.expand(T0, T1)  # repeated positions have stride 0
+            p0, p1 = pos.stride()
+            pa = 0
+        else:
+            _dense(axes, "axes", _u8, (pairs,), dev)
+            if pos.dim() < 1:
+                raise ValueError("pos must have the axes as its first dim")
+            A, axis = pos.shape[0], axes.data_ptr()
+            if not 1 <= A <= 255:
+                raise ValueError(f"pos has {A} axes: 1 to 255 are supported")
+            if pos.shape != (A, T0, T1):
+                pos = pos.view(A, *(1,) * (3 - pos.dim()), *pos.shape[1:]).expand(A, T0, T1)
+            pa, p0, p1 = pos.stride()
+        at = pos.data_ptr()
     if layout not in ROPE_LAYOUT:
         raise ValueError(f"layout must be one of {list(ROPE_LAYOUT)}")
-    if axes is None:
-        A, axis = 1, None
-        if pos.shape != (T0, T1):
-            pos = pos.expand(T0, T1)  # repeated positions have stride 0
-        p0, p1 = pos.stride()
-        pa = 0
-    else:
-        _dense(axes, "axes", _u8, (pairs,), dev)
-        if pos.dim() < 1:
-            raise ValueError("pos must have the axes as its first dim")
-        A, axis = pos.shape[0], axes.data_ptr()
-        if not 1 <= A <= 255:
-            raise ValueError(f"pos has {A} axes: 1 to 255 are supported")
-        if pos.shape != (A, T0, T1):
-            pos = pos.view(A, *(1,) * (3 - pos.dim()), *pos.shape[1:]).expand(A, T0, T1)
-        pa, p0, p1 = pos.stride()
-    return _pack_turn((pos.data_ptr(), pa, p0 if T0 > 1 else 0, p1 if T1 > 1 else 0, freqs.data_ptr(), axis or 0, A, 2 * pairs),
-                      rot_off, ROPE_LAYOUT[layout], mscale)
+    try:
+        return _ROPE_TURN(at, pa, p0 if T0 > 1 else 0, p1 if T1 > 1 else 0, freqs.data_ptr(), axis, A, 2 * pairs, rot_off,
+                          ROPE_LAYOUT[layout], mscale)
+    except struct.error:
+        raise ValueError(f"rot_off must be a 32-bit integer and mscale a number, got {rot_off} and {mscale}") from None
 
 
 def _rope(x, pos, freqs, x2, layout, rot_off, mscale, inverse, stream, out, axes, call):
@@ -906,9 +909,10 @@ def lidx_cache_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, 
     Returns (out [B,S,Hq,D] bf16, lse [B,S,Hq] fp32 or None); ``out`` may hold preallocated ones."""
     shape, qs, dev = _strided(q, "q", _bf16)
     pages, Hkv, page, MP = _cache(k_cache, v_cache, k_scale, v_scale, block_table, shape[0], None, shape[3], dev)
-    return _cache_attn((_lib or lib()).lidx_cache_attn, q, shape, qs, dev, (k_cache, v_cache, k_scale, v_scale, block_table),
+    return _cache_attn(False, q, shape, qs, dev, (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                                                  v_scale.data_ptr(), block_table.data_ptr()),
                        Hkv, page, MP, pages, kv_len, q_pos, compress_ratio, topk_indices, softmax_scale, want_lse, stream, out,
-                       workspace, "lidx_cache_attn")
+                       workspace)
 
 
 def lidx_cache4_attn(q, k_cache, v_cache, k_exps, v_exps, k_scale, v_scale, block_table, kv_len, q_pos=None,
@@ -920,13 +924,15 @@ def lidx_cache4_attn(q, k_cache, v_cache, k_exps, v_exps, k_scale, v_scale, bloc
     _dense(k_scale, "k_scale", _f32, (pages, Hkv), dev)
     _dense(v_scale, "v_scale", _f32, (pages, Hkv), dev)
     MP = _dense(block_table, "block_table", _i32, (shape[0], None), dev)[1]
-    return _cache_attn((_lib or lib()).lidx_cache4_attn, q, shape, qs, dev,
-                       (k_cache, v_cache, k_exps, v_exps, k_scale, v_scale, block_table), Hkv, page, MP, pages, kv_len, q_pos,
-                       compress_ratio, topk_indices, softmax_scale, want_lse, stream, out, workspace, "lidx_cache4_attn")
+    return _cache_attn(True, q, shape, qs, dev, (k_cache.data_ptr(), v_cache.data_ptr(), k_exps.data_ptr(), v_exps.data_ptr(),
+                                                 k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr()),
+                       Hkv, page, MP, pages, kv_len, q_pos, compress_ratio, topk_indices, softmax_scale, want_lse, stream, out,
+                       workspace)
 
 
-def _cache_attn(call, q, shape, qs, dev, cache, Hkv, page, MP, pages, kv_len, q_pos, compress_ratio, topk_indices,
-                softmax_scale, want_lse, stream, out, workspace, name):
+def _cache_attn(four, q, shape, qs, dev, cache, Hkv, page, MP, pages, kv_len, q_pos, compress_ratio, topk_indices,
+                softmax_scale, want_lse, stream, out, workspace):
+    """The calls of both caches from their checked queries; cache: the addresses of the cache's parts and of its table."""
     B, S, Hq, D = shape
     _dense(kv_len, "kv_len", _i32, (B,), dev)
     if q_pos is not None:
@@ -944,18 +950,18 @@ def _cache_attn(call, q, shape, qs, dev, cache, Hkv, page, MP, pages, kv_len, q_
             lse = _new(shape[:3], _f32, q.device, stream)
     L = _lib or lib()
     if workspace is None:
-        if len(cache) == 5:
-            ws_bytes = L.lidx_cache_attn_workspace_bytes(B, S, Hq, Hkv, D, topk)
-        else:
+        if four:
             ws_bytes = L.lidx_cache4_attn_workspace_bytes(B, S, Hq, Hkv, D, page, MP, topk)
+        else:
+            ws_bytes = L.lidx_cache_attn_workspace_bytes(B, S, Hq, Hkv, D, topk)
         workspace = _scratch(ws_bytes, q.device, stream)
     else:
         ws_bytes = _dense(workspace, "workspace", torch.uint8, (None,), dev)[0]
-    rc = call(
-        q.data_ptr(), _I3(*qs), *[t.data_ptr() for t in cache], kv_len.data_ptr(), None if q_pos is None else q_pos.data_ptr(),
+    rc = (L.lidx_cache4_attn if four else L.lidx_cache_attn)(
+        q.data_ptr(), _I3(*qs), *cache, kv_len.data_ptr(), None if q_pos is None else q_pos.data_ptr(),
         None if topk_indices is None else topk_indices.data_ptr(), B, S, Hq, Hkv, D, page, MP, pages, compress_ratio,
         topk, D ** -0.5 if softmax_scale is None else softmax_scale, o.data_ptr(), None if lse is None else lse.data_ptr(),
         workspace.data_ptr(), ws_bytes, _raw_stream(stream, dev))
     if rc:
-        raise LidxError(rc, name)
+        raise LidxError(rc, "lidx_cache4_attn" if four else "lidx_cache_attn")
     return o, lse
