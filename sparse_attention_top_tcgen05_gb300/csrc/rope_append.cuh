@@ -23,6 +23,7 @@
 namespace lidx {
 
 constexpr int kRaThreads = 256;
+constexpr int kRaStatic = kRaThreads / 32 * (int)sizeof(uint32_t);  // bytes of s_top
 
 struct RopeAppendParams {
     const uint16_t* x[2];  // k, v
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(kRaThreads, PER == 4 ? 2 : 3) rope_append_kern
 template <int BITS, int LANES, int MODE, int PER>
 static cudaError_t ra_launch_passes(const RopeAppendParams& p, int64_t B, int smem, cudaStream_t st) {
     auto* kernel = rope_append_kernel<BITS, LANES, MODE, PER>;
-    if (smem > 48 * 1024) {
+    if (smem + kRaStatic > 48 * 1024) {  // what every kernel may have is counted with s_top
         const cudaError_t e = set_smem_attr((const void*)kernel, smem);
         if (e != cudaSuccess) return e;
     }
