@@ -484,7 +484,10 @@ int lidx_cache4_attn(const void* q, const int64_t* qs, const void* k_cache, cons
 
 /* Device scratch of lidx_cache4_attn on the current device, in bytes (topk 0: all keys).  Where a key is read by several units
  * of 128 rows (S * Hq/Hkv > 128), or S * topk is at least twice max_pages * page, it holds the sequences' pages in 8 bits,
- * 2 * B * max_pages * page * Hkv * D bytes and little more, if those are not more than 2 GiB. */
+ * 2 * B * max_pages * page * Hkv * D bytes and little more, if those are not more than 2 GiB.  Lengths are on the device, so
+ * the copy's size goes by the table's width, and each page and head of the table that no sequence has reached costs 0.5 ns: a
+ * table of such a call is best not much wider than the longest sequence.  Beyond 2 GiB there is no copy, every unit widens its
+ * own keys, and a call may take twice the time: such a batch is best split. */
 size_t lidx_cache4_attn_workspace_bytes(int64_t B, int64_t S, int Hq, int Hkv, int D, int page, int64_t max_pages, int topk);
 
 /* Device scratch of lidx_cache_attn on the current device, in bytes. */

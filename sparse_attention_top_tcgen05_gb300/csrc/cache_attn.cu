@@ -154,7 +154,10 @@ static size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 // 4 bits: whether a call widens the sequences' pages first (see cache4_attn.cu), and into how many bytes.  A tile costs an SM
 // about 2.6 us where a kernel of 128 rows widens it and 1.25 us where it is widened already; to write and read the copy costs
 // it 1.1 us once (chunk of 2048 queries over 16384 keys, 128 units a key: 2.1 ms and 1.0 ms).  So two units a key, or two
-// selections of it on average, are enough.  kCopyMost: a copy beyond that is taken for too much memory.
+// selections of it on average, are enough.  kCopyMost: a copy beyond that is taken for too much memory.  Both go by the table's
+// places, since lengths are on the device: a chunk of 2048 over 2048 keys (8 heads of 128, pages of 16) takes 518 us with a
+// table of as many, 582 us with 2^18 places and 797 us with 2^20, the most, and 767 us without a copy; over 16384 keys 1045,
+// 1108 and 1309 us, and 2305 us without.
 constexpr size_t kCopyMost = (size_t)2 << 30;
 static size_t attn4_copy_bytes(int64_t B, int64_t S, int G, int Hkv, int D, int page, int64_t max_pages, int topk) {
     const int64_t keys = max_pages * page;

@@ -9,7 +9,8 @@
 // threads, a second launch the blocks, all in fixed orders: two calls give the same bits.
 //
 // What bounds it: reading and writing each element once.  2 x 8192 tokens of 72 bf16 heads of 128: 107 us, 5.6 TB/s;
-// backward of 4095 tokens of 40 fp32 heads: 45 us, 5.6 TB/s with the second launch; 16 tokens: 2.5 us, a launch.
+// backward of 4095 tokens of 40 fp32 heads: 44 us, 5.7 TB/s with the second launch; 16 tokens: 2.5 us, a launch.  In bf16 the
+// same backward takes 34 us, 3.7 TB/s: two blocks an SM have half the bytes in flight.  (2 x 4096 tokens of 72 heads: 103 us.)
 #include <string.h>
 
 #include "ptx.cuh"
@@ -42,7 +43,8 @@ struct NormParams {
 constexpr int kNormThreads = 256;
 // Rows a thread, blocks an SM.  Forward (2 x 8192 tokens of 72 bf16 heads): two rows and five blocks 107 us, two and four 110 us,
 // two and six 109 us, one and six 117 us; four and three 105 us, but 9.3 us for 1024 tokens (8.8 us) and 50.3 us for 4096 of fp32
-// (48.8 us).  A call with fewer than two such blocks an SM takes one row.
+// (48.8 us).  Five blocks leave 48 registers, and kernels of two rows spill 16 to 32 bytes (-Xptxas -v), but for interleaved fp32; with
+// four nothing spills, and that is the 110 us.  A call with fewer than two such blocks an SM takes one row.
 // Backward, whose blocks go over all rows (4095 tokens of 40 fp32 heads): one row and four blocks 45 us, two and three 51 us.
 constexpr int kNormPer = 2;
 constexpr int kNormAngles = 4096;   // of a block's tokens: 32 KB
@@ -389,7 +391,8 @@ __global__ void __launch_bounds__(kNormThreads, norm_bwd_blocks<T>()) norm_rope_
 }
 
 // ------------------------------------------------------------------ any alignment, any rotated part
-// A warp a row; a lane has pairs (or two copied dims) and recomputes their angles.
+// A warp a row; a lane has pairs (or two copied dims) and recomputes their angles, in the backward twice: what bounds it.  4095
+// tokens of 24 bf16 heads of 80 dims, of which half layouts turn 40: 46 us, backward 85 us (their bytes 4.6 and 7 us).
 __device__ __forceinline__ void norm_unit(const RopeTurn& r, int u, int& ia, int& ib) {
     if (u < r.R / 2) {
         ia = r.half ? r.off + u : r.off + 2 * u;
