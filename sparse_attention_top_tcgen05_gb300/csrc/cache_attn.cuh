@@ -261,27 +261,20 @@ __device__ __forceinline__ int attn_begin(const AttnParams& p, AttnWalk& wk, int
     return nc;
 }
 
-// Loads keys and values: warp pw of PRODUCERS.  The warps take the tiles in turn: the lookups of several tiles are then in
-// flight at once, and no tile's keys wait for the slot of an earlier tile's values.  (With one warp for all pages, 8
-// sequences x 65536 keys took 178 us instead of 169, in pages of 16 tokens 228 us instead of 169.)
-template <int SLOTS, int PRODUCERS, bool SEL>
-__device__ __forceinline__ void attn_produce(const AttnParams& p, AttnWalk& wk, const AttnPipe& x, const CUtensorMap* tmk,
-                                             const CUtensorMap* tmv, int pw, int lane) {
-    static_assert(SLOTS <= 2 * PRODUCERS, "a warp's tile before has been used when its next one is loaded");
-    // Three steps ahead: indices of the warp's tile after next, page ids of its next tile, scales of this one, so that a
-    // step waits for one memory latency at most.
-    bool ok = !p.debug_stall;
-    int last_k = -1, last_v = -1;  // tiles of the last loads
-    struct Ref {
-        bool live;
-        int b, h, tile, limit;
-        int tc;       // tiles of the CTA before it
-        int64_t row;  // of topk_indices
-    };
+// A tile that a producer loads.
+struct AttnRef {
+    bool live;
+    int b, h, tile, limit;
+    int tc;       // tiles of the CTA before it
+    int64_t row;  // of topk_indices
+};
+// The tiles of producer warp pw of PRODUCERS, which take the CTA's in turn.
+template <int PRODUCERS, bool SEL>
+struct AttnRefs {
     int tile = 0, count = 0;
     bool more = true;
-    auto next_ref = [&]() {
-        Ref r{false, 0, 0, 0, 0, 0, 0};
+    __device__ __forceinline__ AttnRef next(const AttnParams& p, AttnWalk& wk, int pw) {
+        AttnRef r{false, 0, 0, 0, 0, 0, 0};
         while (more) {
             if (tile >= wk.t1 || wk.gr.n == 0) {
                 more = wk.next(p);
@@ -298,13 +291,48 @@ __device__ __forceinline__ void attn_produce(const AttnParams& p, AttnWalk& wk, 
             count += skip;
             tile += skip;
             const int limit = SEL ? attn_end(p, wk.gr.b, wk.gr.st) : wk.gr.limit;
-            r = Ref{true, wk.gr.b, wk.h, tile, limit, count, (int64_t)wk.gr.b * p.S + wk.gr.st};
+            r = AttnRef{true, wk.gr.b, wk.h, tile, limit, count, (int64_t)wk.gr.b * p.S + wk.gr.st};
             ++count;
             ++tile;
             break;
         }
         return r;
-    };
+    }
+};
+// All keys: page of the lane's four keys.
+__device__ __forceinline__ int attn_page_id(const AttnParams& p, const AttnRef& r, int lane) {
+    const int k0 = r.tile * kATile + 4 * lane;
+    return r.live && k0 < r.limit ? p.table[(int64_t)r.b * p.max_pages + (k0 >> p.page_shift)] : -1;
+}
+// Selected keys: the lane's key of each quarter of the tile, and their pages.
+__device__ __forceinline__ void attn_keys(const AttnParams& p, const AttnRef& r, int lane, int (&t)[4]) {
+    const int32_t* src = p.idx + r.row * p.topk;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int k = r.tile * kATile + 32 * i + lane;
+        t[i] = r.live && k < p.topk ? src[k] : -1;
+    }
+}
+__device__ __forceinline__ void attn_pages(const AttnParams& p, const AttnRef& r, const int (&t)[4], int (&pid)[4]) {
+    const int32_t* tab = p.table + (int64_t)r.b * p.max_pages;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pid[i] = t[i] >= 0 && t[i] < r.limit ? tab[t[i] >> p.page_shift] : -1;
+}
+
+// Loads keys and values: warp pw of PRODUCERS.  The warps take the tiles in turn: the lookups of several tiles are then in
+// flight at once, and no tile's keys wait for the slot of an earlier tile's values.  (With one warp for all pages, 8
+// sequences x 65536 keys took 178 us instead of 169, in pages of 16 tokens 228 us instead of 169.)
+template <int SLOTS, int PRODUCERS, bool SEL>
+__device__ __forceinline__ void attn_produce(const AttnParams& p, AttnWalk& wk, const AttnPipe& x, const CUtensorMap* tmk,
+                                             const CUtensorMap* tmv, int pw, int lane) {
+    static_assert(SLOTS <= 2 * PRODUCERS, "a warp's tile before has been used when its next one is loaded");
+    // Three steps ahead: indices of the warp's tile after next, page ids of its next tile, scales of this one, so that a
+    // step waits for one memory latency at most.
+    bool ok = !p.debug_stall;
+    int last_k = -1, last_v = -1;  // tiles of the last loads
+    using Ref = AttnRef;
+    AttnRefs<PRODUCERS, SEL> refs;
+    auto next_ref = [&]() { return refs.next(p, wk, pw); };
     const int page_mask = p.page - 1;
     // waits for the slot of tile tc's K (which = 0) or V
     auto claim = [&](int tc, int which) {
@@ -315,10 +343,7 @@ __device__ __forceinline__ void attn_produce(const AttnParams& p, AttnWalk& wk, 
     };
     if constexpr (!SEL) {
         // Pages: a lane has four keys, which share one; the lane with a page's first key loads it.
-        auto page_id = [&](const Ref& r) {
-            const int k0 = r.tile * kATile + 4 * lane;
-            return r.live && k0 < r.limit ? p.table[(int64_t)r.b * p.max_pages + (k0 >> p.page_shift)] : -1;
-        };
+        auto page_id = [&](const Ref& r) { return attn_page_id(p, r, lane); };
         Ref r0 = next_ref();
         int pid0 = page_id(r0);
         Ref r1 = next_ref();
@@ -367,19 +392,8 @@ __device__ __forceinline__ void attn_produce(const AttnParams& p, AttnWalk& wk, 
     } else {
         // Selected keys: TMA gathers of four rows.  A lane has a key of each quarter of the tile.  Unseen keys gather row 0
         // with the other three (or nothing); the softmax clears their V rows.
-        auto keys = [&](const Ref& r, int (&t)[4]) {
-            const int32_t* src = p.idx + r.row * p.topk;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int k = r.tile * kATile + 32 * i + lane;
-                t[i] = r.live && k < p.topk ? src[k] : -1;
-            }
-        };
-        auto pages = [&](const Ref& r, const int (&t)[4], int (&pid)[4]) {
-            const int32_t* tab = p.table + (int64_t)r.b * p.max_pages;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) pid[i] = t[i] >= 0 && t[i] < r.limit ? tab[t[i] >> p.page_shift] : -1;
-        };
+        auto keys = [&](const Ref& r, int (&t)[4]) { attn_keys(p, r, lane, t); };
+        auto pages = [&](const Ref& r, const int (&t)[4], int (&pid)[4]) { attn_pages(p, r, t, pid); };
         int* const sRows = x.rows + kATile * pw;
         Ref r0 = next_ref();
         int t0[4], t1[4], t2[4], pid0[4], pid1[4];
@@ -458,39 +472,9 @@ template <int PACKED, int PRODUCERS, bool SEL>
 __device__ __forceinline__ void attn_produce4(const AttnParams& p, AttnWalk& wk, const AttnPipe& x, int pw, int lane) {
     bool ok = !p.debug_stall;
     int last = -1;  // the last packed tile that was asked for
-    struct Ref {
-        bool live;
-        int b, h, tile, limit;
-        int tc;       // tiles of the CTA before it
-        int64_t row;  // of topk_indices
-    };
-    int tile = 0, count = 0;
-    bool more = true;
-    auto next_ref = [&]() {
-        Ref r{false, 0, 0, 0, 0, 0, 0};
-        while (more) {
-            if (tile >= wk.t1 || wk.gr.n == 0) {
-                more = wk.next(p);
-                tile = wk.t0;
-                continue;
-            }
-            // on to the first tile of this segment that is the warp's
-            const int skip = (pw - count % PRODUCERS + PRODUCERS) % PRODUCERS, left = wk.t1 - tile;
-            if (skip >= left) {
-                count += left;
-                tile = wk.t1;
-                continue;
-            }
-            count += skip;
-            tile += skip;
-            const int limit = SEL ? attn_end(p, wk.gr.b, wk.gr.st) : wk.gr.limit;
-            r = Ref{true, wk.gr.b, wk.h, tile, limit, count, (int64_t)wk.gr.b * p.S + wk.gr.st};
-            ++count;
-            ++tile;
-            break;
-        }
-        return r;
-    };
+    using Ref = AttnRef;
+    AttnRefs<PRODUCERS, SEL> refs;
+    auto next_ref = [&]() { return refs.next(p, wk, pw); };
     const int page_mask = p.page - 1, pitch = p.D / 2;
     const float unit = kCache4Unit * p.scale_log2;
     auto claim = [&](int seq) {
@@ -503,10 +487,7 @@ __device__ __forceinline__ void attn_produce4(const AttnParams& p, AttnWalk& wk,
     };
     if constexpr (!SEL) {
         // A lane has four keys, which share a page; the lane with a page's first key loads it.
-        auto page_id = [&](const Ref& r) {
-            const int k0 = r.tile * kATile + 4 * lane;
-            return r.live && k0 < r.limit ? p.table[(int64_t)r.b * p.max_pages + (k0 >> p.page_shift)] : -1;
-        };
+        auto page_id = [&](const Ref& r) { return attn_page_id(p, r, lane); };
         Ref r0 = next_ref();
         int pid0 = page_id(r0);
         Ref r1 = next_ref();
@@ -566,19 +547,8 @@ __device__ __forceinline__ void attn_produce4(const AttnParams& p, AttnWalk& wk,
                 if ((seq >> 1) % PRODUCERS == pw) mbar_wait(x.pk_full + seq % PACKED, (seq / PACKED) & 1, p.wait_ns);
     } else {
         // A lane has a key of each quarter of the tile.  Keys that are not seen are not loaded.
-        auto keys = [&](const Ref& r, int (&t)[4]) {
-            const int32_t* src = p.idx + r.row * p.topk;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int k = r.tile * kATile + 32 * i + lane;
-                t[i] = r.live && k < p.topk ? src[k] : -1;
-            }
-        };
-        auto pages = [&](const Ref& r, const int (&t)[4], int (&pid)[4]) {
-            const int32_t* tab = p.table + (int64_t)r.b * p.max_pages;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) pid[i] = t[i] >= 0 && t[i] < r.limit ? tab[t[i] >> p.page_shift] : -1;
-        };
+        auto keys = [&](const Ref& r, int (&t)[4]) { attn_keys(p, r, lane, t); };
+        auto pages = [&](const Ref& r, const int (&t)[4], int (&pid)[4]) { attn_pages(p, r, t, pid); };
         int* const rows = x.rows + kATile * pw;
         // a row is copied in units of 16 bytes, or of 8 where its size is no multiple of 16; 2^us lanes a row
         const bool by16 = pitch % 16 == 0;

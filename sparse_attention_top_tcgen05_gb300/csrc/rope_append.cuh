@@ -15,7 +15,7 @@
 // What bounds it.  8 bits, 4 x 4097 tokens of 8 heads of 128, half of each key turned: 26.5 us (25.5 us for cache_append.cu, which
 // turns nothing), a block's dependent reads and barriers.  4 bits, the same with a norm and all of each key turned by three axes:
 // 32.5 us, 67 % of issue slots busy.  One token of 64 sequences, normed and turned: 8.7 us, in 4 bits 9.5 us; passes go by the page,
-// so its 1024 blocks of 256 threads run three rounds.
+// so its 1024 blocks of 256 threads run in three waves.
 //
 // Blocks an SM: two of four passes (128 registers), three of fewer (80).  With that the kernels of half layouts spill 44 to 128
 // bytes and those of pairs side by side up to 48 (-Xptxas -v).  One and two blocks spill nothing and take longer: the prompts above 29.3
